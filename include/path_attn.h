@@ -360,6 +360,127 @@ int path_cp_attend_block(const path_attn_desc_t* desc, int block_len, const void
 int path_cp_pass_block(const path_attn_desc_t* desc, int block_len, float* k_block, float* b_k,
                        const float* t_shard, const float* f_tot, void* stream);
 
+/*
+ * Paged serving
+ * -------------
+ * A cache of many sequences of different lengths, in pages: keys in one pool, values in another, and
+ * for every sequence slot one table of page numbers into each.  Row j of slot b lies in page
+ * k_table[b][j / page_size] (v_table for its value) at row j % page_size.  As in the dense decode
+ * cache, keys are held transported to the newest position, so every step rewrites every key of its
+ * sequence: a key page belongs to exactly one sequence.  Values (and the forget gate's running sums,
+ * which lie beside the values) never change once written: a value page may be shared.
+ *
+ * All pointers are device memory of the caller; the lists and tables are read on the device, so that
+ * a captured step replays with new contents.  A slot with seq_len < 0 is empty.
+ */
+typedef struct {
+  int slots;        /* sequence slots: rows of the tables, 1..65535 */
+  int heads;        /* key/value heads */
+  int head_dim;     /* 64 or 128 */
+  int page_size;    /* rows of a page: 16, 32, 64, 128 or 256 */
+  int table_width;  /* columns of the tables: a slot holds at most table_width * page_size tokens */
+  int k_pages;      /* pages of the key pool */
+  int v_pages;      /* pages of the value pool */
+  int cache_dtype;  /* path_dtype_t of the pools and of q, k, v, w, o */
+  void* k_pool;     /* [k_pages][heads][page_size][head_dim] */
+  void* v_pool;     /* [v_pages][heads][page_size][head_dim] */
+  float* a_pool;    /* [v_pages][heads][page_size]: running sums of log f (PaTH-FoX), or NULL */
+  int* k_table;     /* [slots][table_width]; -1: no page */
+  int* v_table;     /* [slots][table_width] */
+  int* seq_len;     /* [slots]: tokens in the cache; < 0: empty slot */
+  int* k_ref;       /* [k_pages]: 1 in use, 0 free */
+  int* v_ref;       /* [v_pages]: sequences that hold the page, 0 free */
+  int* status;      /* one int: the first PATH_PAGED_* code since it was last cleared (start it at 0) */
+} path_paged_cache_t;
+
+/* Codes of the status word: what a call found on the device.  None of them makes a kernel leave its
+ * buffers; see each call for what it then leaves undone. */
+enum {
+  PATH_PAGED_BAD_PAGE = 1,    /* a needed table entry is not a page of the pool */
+  PATH_PAGED_CAPACITY = 2,    /* a sequence would outgrow table_width * page_size */
+  PATH_PAGED_BAD_SLOT = 3,    /* slot out of range, listed twice, empty where it must not be, or in use */
+  PATH_PAGED_NO_PAGES = 4,    /* not enough free pages */
+  PATH_PAGED_BAD_START = 5,   /* q_start falls, leaves [0, total_tokens] or exceeds max_new */
+  PATH_PAGED_WAIT = 64        /* and above: a bounded wait of a tensor-core kernel gave up */
+};
+
+typedef struct {
+  int heads_q;       /* query heads, a multiple of cache.heads (at most 16 times): head hq reads key head
+                        hq / (heads_q / heads) */
+  int total_tokens;  /* new tokens of the call */
+  int max_new;       /* at least the most new tokens of one slot */
+  float scale;       /* multiplies the logit; the forget bias is added unscaled */
+  int window;        /* 0: every earlier token is seen; W > 0: the token at position p sees j > p - W ... */
+  int sinks;         /* ... and the first `sinks` tokens of its sequence */
+} path_paged_desc_t;
+
+/* Bytes of workspace path_paged_extend needs; 0 if cache or desc is invalid.  Host only. */
+size_t path_paged_workspace_size(const path_paged_cache_t* cache, const path_paged_desc_t* desc);
+
+/*
+ * Attention of new tokens over the paged cache: a prompt chunk, a few draft tokens or one token per
+ * sequence, in any mixture.  Tokens are packed: q, o [total_tokens][heads_q][head_dim], k, v, w
+ * [total_tokens][heads][head_dim] in cache_dtype, beta (clamped to [0, 2]) and log_f (NULL exactly when
+ * a_pool is) [total_tokens][heads] float32.  Slot b's new tokens are q_start[b] .. q_start[b + 1] - 1 (int32
+ * [slots + 1]); they take positions seq_len[b] and up.  q_start NULL: one token per slot, token b for
+ * slot b (total_tokens = slots), empty slots skipped (their rows of o are not written).
+ * With H_t = I - beta_t w_t w_t^T, for every token at position p of a slot,
+ *   o_p = sum_j softmax_j(scale k_j^T H_{j+1} ... H_p q_p  (+ a_p - a_j)) v_j   over the j <= p it sees;
+ * afterwards the new rows are appended (keys transported to the last new token) and every cached key
+ * that a later token sees is k_j <- H_last ... H_first k_j, rounded once per call.  Keys that the window
+ * hides from every later token are left as they are; their table entries may be -1.
+ * seq_len is read, not changed (path_paged_advance does that).  The pages must be there
+ * (path_pages_reserve).  A slot whose row of q_start or length is bad is left out whole; rows whose
+ * page is missing are treated as hidden and are not written; status gets the code.
+ * Pool rows behind seq_len and pages that no table names may hold anything.  An infinity or NaN in a
+ * slot's own tokens or cached rows may reach any output of that slot, never another slot's.
+ * ws: at least path_paged_workspace_size(cache, desc) bytes, 256-byte aligned.  Two calls that may
+ * run at the same time need two workspaces (and must not share a slot).
+ */
+int path_paged_extend(const path_paged_cache_t* cache, const path_paged_desc_t* desc, const int* q_start,
+                      const void* q, const void* k, const void* v, const void* w, const float* beta,
+                      const float* log_f, void* o, void* ws, size_t ws_bytes, void* stream);
+
+/* seq_len[b] += q_start[b + 1] - q_start[b] for the slots in use (q_start NULL: += 1). */
+int path_paged_advance(const path_paged_cache_t* cache, const int* q_start, void* stream);
+
+/*
+ * Reads the status word (synchronises the stream) and clears it.  PATH_OK with *code 0; or *code is
+ * the first code recorded: PATH_ERR_INVALID_ARG for BAD_PAGE, BAD_SLOT and BAD_START, PATH_ERR_CAPACITY
+ * for CAPACITY and NO_PAGES, PATH_ERR_INTERNAL from PATH_PAGED_WAIT on.
+ */
+int path_paged_status(const path_paged_cache_t* cache, int* code, void* stream);
+
+/* Bytes of workspace the path_pages_* calls need; 0 if cache is invalid.  Host only. */
+size_t path_pages_workspace_size(const path_paged_cache_t* cache);
+
+/*
+ * Page management.  Lists are int32 device arrays.  Pages are given out lowest free number first, in
+ * the order of the list (of the slots) and then of the columns.  A call that records a code changes
+ * nothing (path_paged_advance: nothing of that slot).  ws: at least path_pages_workspace_size(cache)
+ * bytes, 256-byte aligned.
+ *
+ * reserve: pages for n_new[b] more tokens ([slots], NULL: 1 for every slot in use) behind seq_len[b]; an
+ *   empty slot with n_new[b] > 0 is opened with length 0.
+ * fork: children[i] (an empty slot, listed once) becomes a copy of parents[i] (a slot in use; it may have
+ *   several children).  Its keys are copied to new pages, because the next step rewrites them; full
+ *   value pages are shared, a partly filled last one is copied with its running sums.  Reserved pages
+ *   behind the parent's last row are not taken over.
+ * free: the slots become empty and their pages return (a shared value page with its last holder).
+ * trim: returns the pages of every slot in use that hold only rows which a window of `window` tokens
+ *   and `sinks` first tokens hides from every later token; their table entries become -1.  The page
+ *   of the last row stays.
+ * compact: moves the pages in use to the front of each pool: with n pages in use, those numbered n and
+ *   above go, in rising order, to the free numbers below n.  Tables and counts follow.
+ */
+int path_pages_reserve(const path_paged_cache_t* cache, const int* n_new, void* ws, size_t ws_bytes, void* stream);
+int path_pages_fork(const path_paged_cache_t* cache, const int* parents, const int* children, int count, void* ws,
+                    size_t ws_bytes, void* stream);
+int path_pages_free(const path_paged_cache_t* cache, const int* slots, int count, void* ws, size_t ws_bytes,
+                    void* stream);
+int path_pages_trim(const path_paged_cache_t* cache, int window, int sinks, void* ws, size_t ws_bytes, void* stream);
+int path_pages_compact(const path_paged_cache_t* cache, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,120 @@
+// Paged serving: declarations shared by its translation units (not part of the ABI).
+#pragma once
+
+#include "../../include/path_attn.h"
+#include "internal.h"
+
+namespace pathattn {
+
+constexpr int kPagedMaxGroup = 16;   // query heads per key head
+constexpr int kPagedChunk = 32;      // new tokens per UT chunk of the CUDA-core kernels
+
+// What a kernel of path_paged_extend needs of the call, by value.
+struct PagedArgs {
+  path_paged_cache_t c;
+  int hq, G;            // query heads; query heads per key head
+  int total, max_new;
+  int window, sinks;
+  float scl;            // scale * log2(e)
+  const int* q_start;   // or null: one token per slot
+  const void *q, *k, *v, *w;
+  const float *beta, *log_f;
+  void* o;
+};
+
+#ifdef __CUDACC__
+#define PATH_HD __host__ __device__ inline
+#else
+#define PATH_HD inline
+#endif
+
+// The new tokens of slot b: first packed token and count, and the cached length.  A bad row of q_start, a
+// negative or overlong length gives count 0 and its code.
+struct SlotSpan {
+  int q0, n, t0, code;
+};
+PATH_HD SlotSpan slot_span_of(int b, const int* q_start, int seq_len, int total, int max_new, int table_width,
+                              int page_size) {
+  SlotSpan s{0, 0, seq_len, 0};
+  int n = 1, q0 = b;
+  if (q_start) {
+    q0 = q_start[b];
+    const long long dn = (long long)q_start[b + 1] - q0;
+    if (q0 < 0 || dn < 0 || (long long)q0 + dn > total || dn > max_new) {
+      s.code = PATH_PAGED_BAD_START;
+      return s;
+    }
+    n = (int)dn;
+    if (n == 0) return s;
+    if (seq_len < 0) {
+      s.code = PATH_PAGED_BAD_SLOT;
+      return s;
+    }
+  } else if (seq_len < 0) {
+    return s;
+  }
+  if ((long long)seq_len + n > (long long)table_width * page_size) {
+    s.code = PATH_PAGED_CAPACITY;
+    return s;
+  }
+  s.q0 = q0;
+  s.n = n;
+  return s;
+}
+// Row j of slot b in a pool: its row number for head h, or -1 where the table holds no page of the pool.
+PATH_HD long long pool_row(const path_paged_cache_t& c, const int* table, int pages, int b, int h, int j) {
+  const int pg = table[(size_t)b * c.table_width + j / c.page_size];
+  if ((unsigned)pg >= (unsigned)pages) return -1;
+  return ((long long)pg * c.heads + h) * c.page_size + j % c.page_size;
+}
+// Whether the token at position pq sees row j <= pq (window 0: all).
+PATH_HD bool sees(int window, int sinks, int pq, int j) { return window <= 0 || j > pq - window || j < sinks; }
+
+// The cached rows of a sequence that a call works on: rows [0, sinks) (first tokens that stay visible) and
+// those its first new token sees, up to t0, cut into tiles of `rows` rows that start at multiples of
+// `rows`.  Tile i of the list is tile i < nh ? i : i + skip of the sequence.
+struct LiveTiles {
+  int nh, skip, count;
+};
+PATH_HD LiveTiles live_tiles(int t0, int window, int sinks, int rows) {
+  LiveTiles l{0, 0, 0};
+  const int all = t0 <= 0 ? 0 : (t0 + rows - 1) / rows;
+  l.nh = l.count = all;
+  if (window <= 0 || all == 0) return l;
+  const int head = sinks < t0 ? sinks : t0;
+  const int from = t0 - window + 1 > 0 ? t0 - window + 1 : 0;
+  const int nh = (head + rows - 1) / rows;
+  const int first = from >= t0 ? all : from / rows;
+  if (first <= nh) return l;
+  l.nh = nh;
+  l.skip = first - nh;
+  l.count = all - l.skip;
+  return l;
+}
+PATH_HD int live_tile(const LiveTiles& l, int i) { return i < l.nh ? i : i + l.skip; }
+
+#ifdef __CUDACC__
+__device__ __forceinline__ SlotSpan slot_span(const PagedArgs& p, int b) {
+  return slot_span_of(b, p.q_start, p.c.seq_len[b], p.total, p.max_new, p.c.table_width, p.c.page_size);
+}
+__device__ __forceinline__ void paged_error(int* status, int code) { atomicCAS(status, 0, code); }
+#endif
+
+// ---- launchers ----
+// path_paged_extend: chooses the kernels of a call.
+size_t paged_ws_bytes(const PagedArgs& p);
+cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st);
+
+size_t paged_chunk_ws_bytes(const PagedArgs& p);
+cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st);
+
+size_t pages_ws_bytes(const path_paged_cache_t& c);
+cudaError_t launch_pages_reserve(const path_paged_cache_t& c, const int* n_new, char* ws, cudaStream_t st);
+cudaError_t launch_pages_fork(const path_paged_cache_t& c, const int* parents, const int* children, int count, char* ws,
+                              cudaStream_t st);
+cudaError_t launch_pages_free(const path_paged_cache_t& c, const int* slots, int count, char* ws, cudaStream_t st);
+cudaError_t launch_pages_trim(const path_paged_cache_t& c, int window, int sinks, char* ws, cudaStream_t st);
+cudaError_t launch_pages_compact(const path_paged_cache_t& c, char* ws, cudaStream_t st);
+cudaError_t launch_paged_advance(const path_paged_cache_t& c, const int* q_start, cudaStream_t st);
+
+}  // namespace pathattn

@@ -1,0 +1,626 @@
+// Paged serving: attention of a chunk of new tokens over a paged cache, CUDA-core kernels (fp32 caches;
+// products of bf16 caches on TF32 warp MMAs).
+//
+// Mathematics (one sequence, one key head; t0 cached rows, n new tokens with rows of W and beta; the UT
+// representation of the PaTH reading notes, cc.laoqi.cc/papers/2505.16381, §2.6-§2.8).  The new
+// tokens are cut into chunks of B rows.  Per chunk
+//   U = (I + strictLower(D W W^T))^-1 D,   X = U strictLower(W K^T),   Y = U^T W,
+//   Q<- = Q - lower(Q W^T) U W   (queries at the chunk's start),   K-> = K - X^T W   (keys at its end),
+//   F = I - W^T Y = H_first ... H_last,   S_diag = lower(Q K^T) - lower(Q W^T) X.
+// A query meets the earlier new chunks right to left, Z <- Z F_c^T, and arrives at the start of the new
+// tokens as z; the logit of a cached row is then z . k~ (k~ as the cache holds it).  The new keys walk to
+// the end of the call, K->_c F_{c+1} ... F_last, and the cached rows become k~ M, M = F_0 ... F_last.
+//
+// Six launches: plan (lengths, chunk list), chunk preparation, then one of {query scan, key walk} per
+// block, cached attention split over key ranges, cached rewrite, and the merge of the splits.
+#include "paged.h"
+#include "dev_common.cuh"
+#include "smem_mm.cuh"
+
+#include <type_traits>
+
+namespace pathattn {
+namespace {
+
+constexpr int NT = 256;
+constexpr int B = kPagedChunk;
+constexpr int KT = 64;  // cached rows per tile
+
+// Workspace (element offsets are computed on the host and the device from the same sizes).
+struct ChunkWs {
+  int nch;             // chunk slots: at least the chunks of any legal q_start
+  int nsplit;          // key ranges of the cached attention (range 0 also carries the new tokens' state)
+  size_t plan;         // int: [slots + 1] first chunk of each slot, [slots + 1] first live cached tile
+  size_t kr, f;        // K-> [nch][H][B][D], F [nch][H][D][D]
+  size_t fa, ft;       // forget gate: inclusive sums inside the chunk [nch][H][B], chunk totals [nch][H]
+  size_t z, qb;        // Q<-, then z [nch][hq][B][D]; row biases sum of log f since t0 [nch][hq][B]
+  size_t m, l, acc;    // softmax states [nsplit][nch][hq][B](, [D])
+  size_t mm;           // M [slots][H][D][D]
+  size_t total;
+};
+ChunkWs chunk_ws(const PagedArgs& p) {
+  ChunkWs w{};
+  const size_t D = p.c.head_dim, H = p.c.heads, hq = p.hq;
+  // every slot may end in a partly filled chunk
+  const long long most = (p.total + (long long)(B - 1) * (p.c.slots < p.total ? p.c.slots : p.total)) / B;
+  w.nch = (int)(most < 1 ? 1 : most);
+  const long long ctas = (long long)w.nch * p.hq;
+  w.nsplit = ctas >= 1216 ? 1 : (int)((1216 + ctas - 1) / ctas);
+  if (w.nsplit > 64) w.nsplit = 64;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, 256); return o; };
+  w.plan = take((size_t)2 * (p.c.slots + 1) * 4);
+  w.kr = take((size_t)w.nch * H * B * D * 4);
+  w.f = take((size_t)w.nch * H * D * D * 4);
+  w.fa = take((size_t)w.nch * H * B * 4);
+  w.ft = take((size_t)w.nch * H * 4);
+  w.z = take((size_t)w.nch * hq * B * D * 4);
+  w.qb = take((size_t)w.nch * hq * B * 4);
+  w.m = take((size_t)w.nsplit * w.nch * hq * B * 4);
+  w.l = take((size_t)w.nsplit * w.nch * hq * B * 4);
+  w.acc = take((size_t)w.nsplit * w.nch * hq * B * D * 4);
+  w.mm = take((size_t)p.c.slots * H * D * D * 4);
+  w.total = off;
+  return w;
+}
+
+// First chunk and first live tile of every slot (exclusive prefix sums; entry `slots` holds the totals).
+__global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict__ plan) {
+  __shared__ int wsum[2][32];
+  __shared__ int carry[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int* cstart = plan;
+  int* tstart = plan + p.c.slots + 1;
+  if (tid < 2) carry[tid] = 0;
+  __syncthreads();
+  for (int base = 0; base < p.c.slots; base += 1024) {
+    const int b = base + tid;
+    int nc = 0, nt = 0;
+    if (b < p.c.slots) {
+      const SlotSpan s = slot_span(p, b);
+      if (s.code) paged_error(p.c.status, s.code);
+      nc = (s.n + B - 1) / B;
+      nt = s.n ? live_tiles(s.t0, p.window, p.sinks, KT).count : 0;
+    }
+    int ic = nc, it = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, ic, o), e = __shfl_up_sync(0xffffffffu, it, o);
+      if (lane >= o) { ic += a; it += e; }
+    }
+    if (lane == 31) { wsum[0][warp] = ic; wsum[1][warp] = it; }
+    __syncthreads();
+    int oc = carry[0], ot = carry[1];
+    for (int w = 0; w < warp; ++w) { oc += wsum[0][w]; ot += wsum[1][w]; }
+    if (b < p.c.slots) { cstart[b] = oc + ic - nc; tstart[b] = ot + it - nt; }
+    __syncthreads();
+    if (tid == 1023) { carry[0] = oc + ic; carry[1] = ot + it; }
+    __syncthreads();
+  }
+  if (tid == 0) { cstart[p.c.slots] = carry[0]; tstart[p.c.slots] = carry[1]; }
+}
+
+// The slot that owns entry x of a prefix array with x < start[slots].
+__device__ __forceinline__ int owner(const int* start, int slots, int x) {
+  int lo = 0, hi = slots;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <int D>
+struct PrepSmem {
+  static constexpr int DS = D + 4, BS = B + 4;
+  static constexpr int kW = 0, kK = kW + B * DS, kQ = kK + B * DS, kV = kQ + B * DS, kY = kV + B * DS;
+  static constexpr int kU = kY + B * DS, kX = kU + B * BS, kG = kX + B * BS, kN = kG + B * BS;
+  static constexpr int kM1 = kN + B * BS, kA = kM1 + B * BS, kS = kA + B * BS;
+  static constexpr int kBeta = kS + B * BS, kLf = kBeta + B, total = kLf + B;
+};
+
+// One block per (chunk, key head).
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+  extern __shared__ float sm[];
+  using S = PrepSmem<D>;
+  constexpr int DS = S::DS, BS = S::BS;
+  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
+  float *sW = sm + S::kW, *sK = sm + S::kK, *sQ = sm + S::kQ, *sV = sm + S::kV, *sY = sm + S::kY;
+  float *sU = sm + S::kU, *sX = sm + S::kX, *sG = sm + S::kG, *sN = sm + S::kN, *sM1 = sm + S::kM1;
+  float *sA = sm + S::kA, *sS = sm + S::kS, *sBeta = sm + S::kBeta, *sLf = sm + S::kLf;
+  const int* cstart = (const int*)(ws + w.plan);
+  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, H = p.c.heads;
+  if (c >= cstart[p.c.slots]) return;
+  const int b = owner(cstart, p.c.slots, c);
+  const SlotSpan sp = slot_span(p, b);
+  const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
+  const T *k = (const T*)p.k, *v = (const T*)p.v, *wv = (const T*)p.w, *q = (const T*)p.q;
+  const size_t tok0 = (size_t)sp.q0 + r0;
+  for (int e = tid; e < B * D; e += NT) {
+    const int r = e / D, x = e % D;
+    const bool ok = r < rows;
+    const size_t at = ((tok0 + r) * H + h) * D + x;
+    sW[r * DS + x] = ok ? to_f(wv[at]) : 0.f;
+    sK[r * DS + x] = ok ? to_f(k[at]) : 0.f;
+    sV[r * DS + x] = ok ? to_f(v[at]) : 0.f;
+  }
+  if (tid < B) {
+    const bool ok = tid < rows;
+    sBeta[tid] = ok ? clamp_beta(p.beta[(tok0 + tid) * H + h]) : 0.f;
+    float a = ok && p.log_f ? p.log_f[(tok0 + tid) * H + h] : 0.f;  // inclusive sums by a warp scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, a, o);
+      if (tid >= o) a += y;
+    }
+    sLf[tid] = a;
+  }
+  __syncthreads();
+  smem_mm<B, B, D, false, true, TC>(sW, DS, sW, DS, [&](int i, int j, float x) { sG[i * BS + j] = j < i ? x : 0.f; });
+  smem_mm<B, B, D, false, true, TC>(sW, DS, sK, DS, [&](int i, int j, float x) { sN[i * BS + j] = j < i ? x : 0.f; });
+  __syncthreads();
+  // U by forward substitution, one column per lane: u_i = beta_i (e_i - sum_{m<i} G_im u_m)
+  if (tid < 32) {
+    float u[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float a0 = (tid == i) ? 1.f : 0.f, a1 = 0.f;
+#pragma unroll
+      for (int m = 0; m + 1 < i; m += 2) {
+        a0 -= sG[i * BS + m] * u[m];
+        a1 -= sG[i * BS + m + 1] * u[m + 1];
+      }
+      if (i & 1) a0 -= sG[i * BS + i - 1] * u[i - 1];
+      u[i] = sBeta[i] * (a0 + a1);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sU[i * BS + tid] = u[i];
+  }
+  __syncthreads();
+  smem_mm<B, B, B, false, false, TC>(sU, BS, sN, BS, [&](int i, int j, float x) { sX[i * BS + j] = x; });
+  smem_mm<B, D, B, true, false, TC>(sU, BS, sW, DS, [&](int m, int n, float x) { sY[m * DS + n] = x; });
+  __syncthreads();
+  {
+    float* kr = (float*)(ws + w.kr) + ((size_t)c * H + h) * B * D;
+    float* f = (float*)(ws + w.f) + ((size_t)c * H + h) * D * D;
+    smem_mm<B, D, B, true, false, TC>(sX, BS, sW, DS, [&](int j, int n, float x) { kr[j * D + n] = sK[j * DS + n] - x; });
+    smem_mm<D, D, B, true, false, TC>(sW, DS, sY, DS, [&](int n, int x, float y) { f[n * D + x] = (n == x ? 1.f : 0.f) - y; });
+    if (p.log_f && tid < B) ((float*)(ws + w.fa))[((size_t)c * H + h) * B + tid] = sLf[tid];
+    if (p.log_f && tid == 0) ((float*)(ws + w.ft))[(size_t)c * H + h] = sLf[B - 1];
+  }
+  for (int g = 0; g < p.G; ++g) {
+    const int qh = h * p.G + g;
+    __syncthreads();
+    for (int e = tid; e < B * D; e += NT) {
+      const int r = e / D, x = e % D;
+      sQ[r * DS + x] = r < rows ? to_f(q[((tok0 + r) * p.hq + qh) * D + x]) : 0.f;
+    }
+    __syncthreads();
+    smem_mm<B, B, D, false, true, TC>(sQ, DS, sW, DS, [&](int i, int j, float x) { sM1[i * BS + j] = j <= i ? x : 0.f; });
+    smem_mm<B, B, D, false, true, TC>(sQ, DS, sK, DS, [&](int i, int j, float x) { sS[i * BS + j] = x; });
+    __syncthreads();
+    smem_mm<B, B, B, false, false, TC>(sM1, BS, sU, BS, [&](int i, int j, float x) { sA[i * BS + j] = x; });
+    smem_mm<B, B, B, false, false, TC>(sM1, BS, sX, BS, [&](int i, int j, float x) { sS[i * BS + j] -= x; });
+    __syncthreads();
+    const size_t row = ((size_t)c * p.hq + qh) * B;
+    float* z = (float*)(ws + w.z) + row * D;
+    smem_mm<B, D, B, false, false, TC>(sA, BS, sW, DS, [&](int i, int n, float x) { z[i * D + n] = sQ[i * DS + n] - x; });
+    // softmax of the diagonal chunk: 8 threads per row (log2 domain)
+    const int r = tid >> 3, sub = tid & 7;
+    float mx = -INFINITY;
+    for (int j = sub; j < B; j += 8) {
+      float s = -INFINITY;
+      if (j <= r && r < rows && sees(p.window, p.sinks, sp.t0 + r0 + r, sp.t0 + r0 + j))
+        s = sS[r * BS + j] * p.scl + (sLf[r] - sLf[j]) * kLog2e;
+      sS[r * BS + j] = s;
+      mx = fmaxf(mx, s);
+    }
+    mx = group_max<8>(mx);
+    float l = 0.f;
+    for (int j = sub; j < B; j += 8) {
+      const float s = sS[r * BS + j];
+      const float e = s == -INFINITY ? 0.f : fast_exp2(s - mx);
+      sS[r * BS + j] = e;
+      l += e;
+    }
+    l = group_sum<8>(l);
+    if (sub == 0) {
+      ((float*)(ws + w.m))[row + r] = mx;
+      ((float*)(ws + w.l))[row + r] = l;
+    }
+    __syncthreads();
+    float* acc = (float*)(ws + w.acc) + row * D;
+    smem_mm<B, D, B, false, false, TC>(sS, BS, sV, DS, [&](int i, int n, float x) { acc[i * D + n] = x; });
+  }
+}
+
+template <int D>
+struct ScanSmem {
+  static constexpr int DS = D + 4, KS = KT + 4;
+  static constexpr int kZ = 0, kZn = kZ + B * DS, kK = kZn + B * DS, kV = kK + KT * DS, kAcc = kV + KT * DS;
+  static constexpr int kP = kAcc + B * DS;
+  static constexpr int kM = kP + B * KS, kBias = kM + B * 3, attend = kBias + KT;  // kM: maximum, sum, row bias
+};
+
+// Online softmax of the score tile sP [B][nk] (already masked, log2 domain): probabilities replace the
+// scores, the row's maximum and sum are updated and acc rescaled.  All threads; ends with a barrier.
+template <int D>
+__device__ __forceinline__ void softmax_step(float* sP, int ps, int nk, float* sM, float* sAcc, int ds) {
+  const int r = threadIdx.x >> 3, sub = threadIdx.x & 7;
+  float mx = -INFINITY;
+  for (int j = sub; j < nk; j += 8) mx = fmaxf(mx, sP[r * ps + j]);
+  mx = group_max<8>(mx);
+  const float mo = sM[r], mn = fmaxf(mo, mx);
+  const float corr = mn == -INFINITY ? 1.f : fast_exp2(mo - mn);
+  float l = 0.f;
+  for (int j = sub; j < nk; j += 8) {
+    const float s = sP[r * ps + j];
+    const float e = s == -INFINITY ? 0.f : fast_exp2(s - mn);
+    sP[r * ps + j] = e;
+    l += e;
+  }
+  l = group_sum<8>(l);
+  for (int x = sub; x < D; x += 8) sAcc[r * ds + x] *= corr;
+  __syncwarp();
+  if (sub == 0) {
+    sM[r] = mn;
+    sM[B + r] = sM[B + r] * corr + l;
+  }
+  __syncthreads();
+}
+
+// Query scan over the earlier new chunks of the slot: one block per (chunk, query head).
+template <typename T, int D>
+__device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float* sm, int c, int qh) {
+  using S = ScanSmem<D>;
+  constexpr int DS = S::DS, KS = S::KS;
+  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
+  float *sZ = sm + S::kZ, *sZn = sm + S::kZn, *sK = sm + S::kK, *sV = sm + S::kV, *sAcc = sm + S::kAcc;
+  float *sP = sm + S::kP, *sM = sm + S::kM, *sF = sm + S::attend;
+  const int* cstart = (const int*)(ws + w.plan);
+  const int tid = threadIdx.x, H = p.c.heads, h = qh / p.G;
+  const int b = owner(cstart, p.c.slots, c);
+  const SlotSpan sp = slot_span(p, b);
+  const int lc = c - cstart[b], rows = min(B, sp.n - lc * B);
+  const size_t row = ((size_t)c * p.hq + qh) * B;
+  float* z = (float*)(ws + w.z) + row * D;
+  float* acc = (float*)(ws + w.acc) + row * D;
+  float *gm = (float*)(ws + w.m) + row, *gl = (float*)(ws + w.l) + row;
+  const float* fa = (const float*)(ws + w.fa);
+  const float* ft = (const float*)(ws + w.ft);
+  if (lc == 0) {  // already at the start of the new tokens
+    if (p.log_f && tid < B) ((float*)(ws + w.qb))[row + tid] = fa[((size_t)c * H + h) * B + tid];
+    return;
+  }
+  for (int e = tid; e < B * D; e += NT) {
+    sZ[(e / D) * DS + e % D] = z[e];
+    sAcc[(e / D) * DS + e % D] = acc[e];
+  }
+  if (tid < B) {
+    sM[tid] = gm[tid];
+    sM[B + tid] = gl[tid];
+    sM[2 * B + tid] = p.log_f ? fa[((size_t)c * H + h) * B + tid] : 0.f;  // row bias so far
+  }
+  const T* v = (const T*)p.v;
+  for (int c2 = lc - 1; c2 >= 0; --c2) {
+    const size_t cc = (size_t)(c - lc + c2) * H + h;
+    const float* kr = (const float*)(ws + w.kr) + cc * B * D;
+    const float* f = (const float*)(ws + w.f) + cc * D * D;
+    const size_t tok = (size_t)sp.q0 + (size_t)c2 * B;
+    __syncthreads();
+    for (int e = tid; e < B * D; e += NT) {
+      const int r = e / D, x = e % D;
+      sK[r * DS + x] = kr[e];
+      sV[r * DS + x] = to_f(v[((tok + r) * H + h) * D + x]);  // an earlier chunk is full
+    }
+    for (int e = tid; e < D * D; e += NT) sF[(e / D) * DS + e % D] = f[e];
+    __syncthreads();
+    smem_mm<B, B, D, false, true, TC>(sZ, DS, sK, DS, [&](int i, int j, float x) {
+      float s = -INFINITY;
+      const int jn = c2 * B + j, in = lc * B + i;
+      if (i < rows && sees(p.window, p.sinks, sp.t0 + in, sp.t0 + jn)) {
+        s = x * p.scl;
+        if (p.log_f) s += (sM[2 * B + i] + (ft[cc] - fa[cc * B + j])) * kLog2e;
+      }
+      sP[i * KS + j] = s;
+    });
+    smem_mm<B, D, D, false, true, TC>(sZ, DS, sF, DS, [&](int i, int n, float x) { sZn[i * DS + n] = x; });
+    __syncthreads();
+    softmax_step<D>(sP, KS, B, sM, sAcc, DS);
+    smem_mm<B, D, B, false, false, TC>(sP, KS, sV, DS, [&](int i, int n, float x) { sAcc[i * DS + n] += x; });
+    if (p.log_f && tid < B) sM[2 * B + tid] += ft[cc];
+    float* t = sZ; sZ = sZn; sZn = t;
+  }
+  __syncthreads();
+  for (int e = tid; e < B * D; e += NT) {
+    z[e] = sZ[(e / D) * DS + e % D];
+    acc[e] = sAcc[(e / D) * DS + e % D];
+  }
+  if (tid < B) {
+    gm[tid] = sM[tid];
+    gl[tid] = sM[B + tid];
+    if (p.log_f) ((float*)(ws + w.qb))[row + tid] = sM[2 * B + tid];
+  }
+}
+
+// Key walk of one (slot, key head): the new rows to the end of the call and into the pages, M.
+template <typename T, int D>
+__device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float* sm, int b, int h) {
+  constexpr int DS = D + 4;
+  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
+  float *sR = sm, *sF = sR + D * DS, *sK = sF + D * DS;
+  const int* cstart = (const int*)(ws + w.plan);
+  const int tid = threadIdx.x, H = p.c.heads;
+  const SlotSpan sp = slot_span(p, b);
+  if (sp.n == 0) return;
+  const int nc = cstart[b + 1] - cstart[b];
+  T* kp = (T*)p.c.k_pool;
+  T* vp = (T*)p.c.v_pool;
+  const T* v = (const T*)p.v;
+  // values and running sums
+  for (int r = tid >> 4; r < sp.n; r += NT / 16) {
+    const long long at = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r);
+    if (at < 0) {
+      paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+      continue;
+    }
+    for (int x = tid & 15; x < D; x += 16) vp[at * D + x] = v[(((size_t)sp.q0 + r) * H + h) * D + x];
+  }
+  if (p.log_f && tid == 0) {
+    const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
+    double a = last >= 0 ? p.c.a_pool[last] : 0.0;
+    for (int r = 0; r < sp.n; ++r) {
+      a += p.log_f[((size_t)sp.q0 + r) * H + h];
+      const long long at = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r);
+      if (at >= 0) p.c.a_pool[at] = (float)a;
+    }
+  }
+  for (int e = tid; e < D * D; e += NT) sR[(e / D) * DS + e % D] = (e / D == e % D) ? 1.f : 0.f;
+  float* mm = (float*)(ws + w.mm) + ((size_t)b * H + h) * D * D;
+  for (int lc = nc - 1; lc >= 0; --lc) {
+    const size_t cc = (size_t)(cstart[b] + lc) * H + h;
+    const float* kr = (const float*)(ws + w.kr) + cc * B * D;
+    const float* f = (const float*)(ws + w.f) + cc * D * D;
+    const int rows = min(B, sp.n - lc * B);
+    __syncthreads();
+    for (int e = tid; e < B * D; e += NT) sK[(e / D) * DS + e % D] = kr[e];
+    for (int e = tid; e < D * D; e += NT) sF[(e / D) * DS + e % D] = f[e];
+    __syncthreads();
+    smem_mm<B, D, D, false, false, TC>(sK, DS, sR, DS, [&](int i, int n, float x) {
+      if (i < rows) {
+        const long long at = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0 + lc * B + i);
+        if (at >= 0) kp[at * D + n] = from_f<T>(lc == nc - 1 ? sK[i * DS + n] : x);
+        else paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+      }
+    });
+    // R <- F_c R, by way of M's place in global memory until every thread has read R
+    smem_mm<D, D, D, false, false, TC>(sF, DS, sR, DS, [&](int i, int n, float x) { mm[i * D + n] = x; });
+    __syncthreads();
+    for (int e = tid; e < D * D; e += NT) sR[(e / D) * DS + e % D] = mm[e];
+  }
+}
+
+template <int D>
+constexpr size_t scan_walk_smem() {
+  constexpr size_t scan = (size_t)(ScanSmem<D>::attend + D * (D + 4)) * 4;
+  constexpr size_t walk = (size_t)(2 * D + B) * (D + 4) * 4;
+  return scan > walk ? scan : walk;
+}
+
+// Blocks [0, slots * H) walk keys, the others scan queries.
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+  extern __shared__ float sm[];
+  const int nw = p.c.slots * p.c.heads;
+  if ((int)blockIdx.x < nw) {
+    walk_block<T, D>(p, w, ws, sm, blockIdx.x / p.c.heads, blockIdx.x % p.c.heads);
+    return;
+  }
+  const int x = blockIdx.x - nw, c = x / p.hq;
+  if (c >= ((const int*)(ws + w.plan))[p.c.slots]) return;
+  scan_block<T, D>(p, w, ws, sm, c, x % p.hq);
+}
+
+// Cached attention: one block per (chunk, query head, key range).
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+  extern __shared__ float sm[];
+  using S = ScanSmem<D>;
+  constexpr int DS = S::DS, KS = S::KS;
+  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
+  float *sZ = sm + S::kZ, *sK = sm + S::kK, *sV = sm + S::kV, *sAcc = sm + S::kAcc, *sP = sm + S::kP, *sM = sm + S::kM;
+  float* sB = sm + S::kBias;  // key biases a_last - a_j; hidden rows -inf
+  const int* cstart = (const int*)(ws + w.plan);
+  const int c = blockIdx.x, qh = blockIdx.y, split = blockIdx.z, tid = threadIdx.x;
+  if (c >= cstart[p.c.slots]) return;
+  const int h = qh / p.G, b = owner(cstart, p.c.slots, c);
+  const SlotSpan sp = slot_span(p, b);
+  const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
+  const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, KT);
+  const int per = (lt.count + w.nsplit - 1) / w.nsplit;
+  const int i0 = min(split * per, lt.count), i1 = min(i0 + per, lt.count);
+  const size_t row0 = ((size_t)c * p.hq + qh) * B;
+  const size_t row = (size_t)split * w.nch * p.hq * B + row0;
+  if (split == 0 && i0 >= i1) return;  // the new tokens' state stands
+  float* acc = (float*)(ws + w.acc) + row * D;
+  float *gm = (float*)(ws + w.m) + row, *gl = (float*)(ws + w.l) + row;
+  if (i0 >= i1) {
+    if (tid < B) {
+      gm[tid] = -INFINITY;
+      gl[tid] = 0.f;
+    }
+    return;
+  }
+  const float* z = (const float*)(ws + w.z) + row0 * D;
+  for (int e = tid; e < B * D; e += NT) {
+    sZ[(e / D) * DS + e % D] = z[e];
+    sAcc[(e / D) * DS + e % D] = split == 0 ? acc[e] : 0.f;
+  }
+  if (tid < B) {
+    sM[tid] = split == 0 ? gm[tid] : -INFINITY;
+    sM[B + tid] = split == 0 ? gl[tid] : 0.f;
+    sM[2 * B + tid] = p.log_f ? ((const float*)(ws + w.qb))[row0 + tid] : 0.f;
+  }
+  float a_last = 0.f;
+  if (p.log_f) {
+    const long long last = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1);
+    if (last >= 0) a_last = p.c.a_pool[last];
+  }
+  const T* kp = (const T*)p.c.k_pool;
+  const T* vp = (const T*)p.c.v_pool;
+  for (int i = i0; i < i1; ++i) {
+    const int j0 = live_tile(lt, i) * KT;
+    __syncthreads();
+    for (int r = tid >> 3; r < KT; r += NT / 8) {
+      const int j = j0 + r;
+      // a row that no query of the chunk sees is not looked up (its page may be gone)
+      bool any = j < sp.t0 && sees(p.window, p.sinks, sp.t0 + r0, j);
+      long long ka = -1, va = -1;
+      if (any) {
+        ka = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j);
+        va = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, j);
+        if (ka < 0 || va < 0) {
+          any = false;
+          paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+        }
+      }
+      for (int x = tid & 7; x < D; x += 8) {
+        sK[r * DS + x] = any ? to_f(kp[ka * D + x]) : 0.f;
+        sV[r * DS + x] = any ? to_f(vp[va * D + x]) : 0.f;
+      }
+      if ((tid & 7) == 0) sB[r] = any ? (p.log_f ? a_last - p.c.a_pool[va] : 0.f) : -INFINITY;
+    }
+    __syncthreads();
+    smem_mm<B, KT, D, false, true, TC>(sZ, DS, sK, DS, [&](int r, int j, float x) {
+      float s = -INFINITY;
+      if (r < rows && sB[j] != -INFINITY && sees(p.window, p.sinks, sp.t0 + r0 + r, j0 + j))
+        s = x * p.scl + (sB[j] + sM[2 * B + r]) * kLog2e;
+      sP[r * KS + j] = s;
+    });
+    __syncthreads();
+    softmax_step<D>(sP, KS, KT, sM, sAcc, DS);
+    smem_mm<B, D, KT, false, false, TC>(sP, KS, sV, DS, [&](int r, int n, float x) { sAcc[r * DS + n] += x; });
+  }
+  __syncthreads();
+  for (int e = tid; e < B * D; e += NT) acc[e] = sAcc[(e / D) * DS + e % D];
+  if (tid < B) {
+    gm[tid] = sM[tid];
+    gl[tid] = sM[B + tid];
+  }
+}
+
+// k <- k M for the cached rows that a later token sees: blocks take runs of (live tile, head).
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, const char* __restrict__ ws) {
+  extern __shared__ float sm[];
+  constexpr int DS = D + 4;
+  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
+  float *sMm = sm, *sK = sMm + D * DS;
+  const int* tstart = (const int*)(ws + w.plan) + p.c.slots + 1;
+  const int tid = threadIdx.x, H = p.c.heads;
+  const long long units = (long long)tstart[p.c.slots] * H;
+  const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  T* kp = (T*)p.c.k_pool;
+  int have = -1;  // (slot, head) whose M is in shared memory
+  for (long long u = u0; u < u1; ++u) {
+    // units of a slot: head-major, so that a block keeps its M
+    const int b = owner(tstart, p.c.slots, (int)(u / H));
+    const int nt = tstart[b + 1] - tstart[b];
+    const long long in = u - (long long)tstart[b] * H;
+    const int h = (int)(in / nt), i = (int)(in % nt);
+    const SlotSpan sp = slot_span(p, b);
+    const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, KT);
+    const int j0 = live_tile(lt, i) * KT;
+    __syncthreads();
+    if (have != b * H + h) {
+      const float* mm = (const float*)(ws + w.mm) + ((size_t)b * H + h) * D * D;
+      for (int e = tid; e < D * D; e += NT) sMm[(e / D) * DS + e % D] = mm[e];
+      have = b * H + h;
+    }
+    auto keep = [&](int j) { return j < sp.t0 && sees(p.window, p.sinks, sp.t0 + sp.n, j); };
+    for (int r = tid >> 3; r < KT; r += NT / 8) {
+      const long long at = keep(j0 + r) ? pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j0 + r) : -1;
+      for (int x = tid & 7; x < D; x += 8) sK[r * DS + x] = at >= 0 ? to_f(kp[at * D + x]) : 0.f;
+    }
+    __syncthreads();
+    smem_mm<KT, D, D, false, false, TC>(sK, DS, sMm, DS, [&](int r, int n, float x) {
+      if (keep(j0 + r)) {
+        const long long at = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j0 + r);
+        if (at >= 0) kp[at * D + n] = from_f<T>(x);
+      }
+    });
+  }
+}
+
+// Merge of the key ranges: one warp per (row, query head).
+template <typename T, int D>
+__global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const char* __restrict__ ws) {
+  const int* cstart = (const int*)(ws + w.plan);
+  const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (c >= cstart[p.c.slots]) return;
+  const int b = owner(cstart, p.c.slots, c);
+  const SlotSpan sp = slot_span(p, b);
+  const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
+  const float *gm = (const float*)(ws + w.m), *gl = (const float*)(ws + w.l), *ga = (const float*)(ws + w.acc);
+  const size_t stride = (size_t)w.nch * p.hq * B;
+  for (int r = warp; r < rows; r += NT / 32) {
+    const size_t row = ((size_t)c * p.hq + qh) * B + r;
+    float M = -INFINITY;
+    for (int s = 0; s < w.nsplit; ++s) M = fmaxf(M, gm[s * stride + row]);
+    float l = 0.f, a[D / 32];
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) a[x] = 0.f;
+    for (int s = 0; s < w.nsplit; ++s) {
+      const float ms = gm[s * stride + row];
+      if (ms == -INFINITY) continue;
+      const float f = fast_exp2(ms - M);
+      l += gl[s * stride + row] * f;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) a[x] += ga[(s * stride + row) * D + x * 32 + lane] * f;
+    }
+    T* o = (T*)p.o + (((size_t)sp.q0 + r0 + r) * p.hq + qh) * D;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) o[x * 32 + lane] = from_f<T>(a[x] * inv);
+  }
+}
+
+template <typename T, int D>
+cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
+  const ChunkWs w = chunk_ws(p);
+  cudaError_t e;
+  auto prep = prep_kernel<T, D>;
+  auto scan = scan_walk_kernel<T, D>;
+  auto att = attend_kernel<T, D>;
+  auto rew = rewrite_kernel<T, D>;
+  const size_t s1 = (size_t)PrepSmem<D>::total * 4, s2 = scan_walk_smem<D>();
+  const size_t s3 = (size_t)ScanSmem<D>::attend * 4, s4 = (size_t)(D + KT) * (D + 4) * 4;
+  if ((e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(att, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s3)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(rew, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s4)) != cudaSuccess) return e;
+  plan_kernel<<<1, 1024, 0, st>>>(p, (int*)(ws + w.plan));
+  prep<<<dim3(w.nch, p.c.heads), NT, s1, st>>>(p, w, ws);
+  scan<<<(unsigned)(p.c.slots * p.c.heads + w.nch * p.hq), NT, s2, st>>>(p, w, ws);
+  att<<<dim3(w.nch, p.hq, w.nsplit), NT, s3, st>>>(p, w, ws);
+  rew<<<608, NT, s4, st>>>(p, w, ws);
+  merge_kernel<T, D><<<dim3(w.nch, p.hq), NT, 0, st>>>(p, w, ws);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t paged_chunk_ws_bytes(const PagedArgs& p) { return chunk_ws(p).total; }
+
+cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st) {
+  if (p.c.head_dim == kHeadDim)
+    return p.c.cache_dtype == PATH_BF16 ? chunk_t<__nv_bfloat16, kHeadDim>(p, ws, st) : chunk_t<float, kHeadDim>(p, ws, st);
+  return p.c.cache_dtype == PATH_BF16 ? chunk_t<__nv_bfloat16, kHeadDimWide>(p, ws, st)
+                                      : chunk_t<float, kHeadDimWide>(p, ws, st);
+}
+
+size_t paged_ws_bytes(const PagedArgs& p) { return paged_chunk_ws_bytes(p); }
+cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st) { return launch_paged_chunk(p, ws, st); }
+
+}  // namespace pathattn

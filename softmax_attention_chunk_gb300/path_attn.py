@@ -38,6 +38,18 @@ class path_decode_desc_t(ctypes.Structure):
                 ("capacity", ctypes.c_int), ("cache_dtype", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
+class path_paged_cache_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("slots", "heads", "head_dim", "page_size", "table_width", "k_pages",
+                                            "v_pages", "cache_dtype")] + \
+               [(n, ctypes.c_void_p) for n in ("k_pool", "v_pool", "a_pool", "k_table", "v_table", "seq_len", "k_ref",
+                                               "v_ref", "status")]
+
+
+class path_paged_desc_t(ctypes.Structure):
+    _fields_ = [("heads_q", ctypes.c_int), ("total_tokens", ctypes.c_int), ("max_new", ctypes.c_int),
+                ("scale", ctypes.c_float), ("window", ctypes.c_int), ("sinks", ctypes.c_int)]
+
+
 _vp, _sz, _i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _DP = ctypes.POINTER(path_attn_desc_t)
 _DDP = ctypes.POINTER(path_decode_desc_t)
@@ -81,6 +93,27 @@ _lib.path_cp_attend_block.restype = _i
 _lib.path_cp_attend_block.argtypes = [_DP, _i] + [_vp] * 5 + [_vp, _sz, _vp, _sz, _vp]
 _lib.path_cp_pass_block.restype = _i
 _lib.path_cp_pass_block.argtypes = [_DP, _i] + [_vp] * 4 + [_vp]
+_CP, _PP = ctypes.POINTER(path_paged_cache_t), ctypes.POINTER(path_paged_desc_t)
+_lib.path_paged_workspace_size.restype = _sz
+_lib.path_paged_workspace_size.argtypes = [_CP, _PP]
+_lib.path_paged_extend.restype = _i
+_lib.path_paged_extend.argtypes = [_CP, _PP] + [_vp] * 9 + [_sz, _vp]
+_lib.path_paged_advance.restype = _i
+_lib.path_paged_advance.argtypes = [_CP, _vp, _vp]
+_lib.path_paged_status.restype = _i
+_lib.path_paged_status.argtypes = [_CP, ctypes.POINTER(_i), _vp]
+_lib.path_pages_workspace_size.restype = _sz
+_lib.path_pages_workspace_size.argtypes = [_CP]
+_lib.path_pages_reserve.restype = _i
+_lib.path_pages_reserve.argtypes = [_CP, _vp, _vp, _sz, _vp]
+_lib.path_pages_fork.restype = _i
+_lib.path_pages_fork.argtypes = [_CP, _vp, _vp, _i, _vp, _sz, _vp]
+_lib.path_pages_free.restype = _i
+_lib.path_pages_free.argtypes = [_CP, _vp, _i, _vp, _sz, _vp]
+_lib.path_pages_trim.restype = _i
+_lib.path_pages_trim.argtypes = [_CP, _i, _i, _vp, _sz, _vp]
+_lib.path_pages_compact.restype = _i
+_lib.path_pages_compact.argtypes = [_CP, _vp, _sz, _vp]
 PATH_DECODE_NOALLOC_MAX_HEADS = 496
 PATH_ERR_INTERNAL = 6
 
@@ -95,7 +128,10 @@ EXPORTED = ("path_status_string", "path_attn_chunk", "path_attn_workspace_size",
             "path_decode_step", "path_decode_step_noalloc", "path_decode_prefill_workspace_size",
             "path_decode_prefill", "path_decode_step_fox", "path_attn_workspace_status",
             "path_decode_prefill_status", "path_cp_prepare_workspace_size", "path_cp_shard_prepare",
-            "path_cp_block_workspace_size", "path_cp_attend_block", "path_cp_pass_block")
+            "path_cp_block_workspace_size", "path_cp_attend_block", "path_cp_pass_block",
+            "path_paged_workspace_size", "path_paged_extend", "path_paged_advance", "path_paged_status",
+            "path_pages_workspace_size", "path_pages_reserve", "path_pages_fork", "path_pages_free",
+            "path_pages_trim", "path_pages_compact")
 
 
 # ---------------- raw entry points (same names as the C ABI) ----------------
@@ -202,6 +238,50 @@ def path_cp_attend_block(desc, block_len, q_start, k_block, v_block, a_q, b_k, f
 
 def path_cp_pass_block(desc, block_len, k_block, b_k, t_shard, f_tot, stream) -> int:
     return _lib.path_cp_pass_block(ctypes.byref(desc), int(block_len), k_block, b_k, t_shard, f_tot, stream)
+
+
+def path_paged_workspace_size(cache, desc) -> int:
+    return _lib.path_paged_workspace_size(ctypes.byref(cache), ctypes.byref(desc))
+
+
+def path_paged_extend(cache, desc, q_start, q, k, v, w, beta, log_f, o, ws, ws_bytes, stream) -> int:
+    return _lib.path_paged_extend(ctypes.byref(cache), ctypes.byref(desc), q_start, q, k, v, w, beta, log_f, o, ws,
+                                  ws_bytes, stream)
+
+
+def path_paged_advance(cache, q_start, stream) -> int:
+    return _lib.path_paged_advance(ctypes.byref(cache), q_start, stream)
+
+
+def path_paged_status(cache, stream):
+    """(status, code): reads and clears the cache's status word; synchronises the stream."""
+    code = _i(0)
+    rc = _lib.path_paged_status(ctypes.byref(cache), ctypes.byref(code), stream)
+    return rc, code.value
+
+
+def path_pages_workspace_size(cache) -> int:
+    return _lib.path_pages_workspace_size(ctypes.byref(cache))
+
+
+def path_pages_reserve(cache, n_new, ws, ws_bytes, stream) -> int:
+    return _lib.path_pages_reserve(ctypes.byref(cache), n_new, ws, ws_bytes, stream)
+
+
+def path_pages_fork(cache, parents, children, count, ws, ws_bytes, stream) -> int:
+    return _lib.path_pages_fork(ctypes.byref(cache), parents, children, int(count), ws, ws_bytes, stream)
+
+
+def path_pages_free(cache, slots, count, ws, ws_bytes, stream) -> int:
+    return _lib.path_pages_free(ctypes.byref(cache), slots, int(count), ws, ws_bytes, stream)
+
+
+def path_pages_trim(cache, window, sinks, ws, ws_bytes, stream) -> int:
+    return _lib.path_pages_trim(ctypes.byref(cache), int(window), int(sinks), ws, ws_bytes, stream)
+
+
+def path_pages_compact(cache, ws, ws_bytes, stream) -> int:
+    return _lib.path_pages_compact(ctypes.byref(cache), ws, ws_bytes, stream)
 
 
 # ---------------- torch-tensor wrappers ----------------
