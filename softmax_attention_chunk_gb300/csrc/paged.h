@@ -20,6 +20,7 @@ struct PagedArgs {
   const void *q, *k, *v, *w;
   const float *beta, *log_f;
   void* o;
+  int min_new;          // the chunk kernels leave out slots with fewer new tokens
 };
 
 #ifdef __CUDACC__
@@ -107,6 +108,10 @@ cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st);
 
 size_t paged_chunk_ws_bytes(const PagedArgs& p);
 cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st);
+
+// Slots with one new token, bf16.
+size_t paged_token_ws_bytes(const PagedArgs& p);
+cudaError_t launch_paged_token(const PagedArgs& p, char* ws, cudaStream_t st);
 
 size_t pages_ws_bytes(const path_paged_cache_t& c);
 cudaError_t launch_pages_reserve(const path_paged_cache_t& c, const int* n_new, char* ws, cudaStream_t st);

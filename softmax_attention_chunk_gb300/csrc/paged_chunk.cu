@@ -64,6 +64,12 @@ ChunkWs chunk_ws(const PagedArgs& p) {
   return w;
 }
 
+__device__ __forceinline__ SlotSpan chunk_span(const PagedArgs& p, int b) {
+  SlotSpan s = slot_span(p, b);
+  if (s.n < p.min_new) s.n = 0;
+  return s;
+}
+
 // First chunk and first live tile of every slot (exclusive prefix sums; entry `slots` holds the totals).
 __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict__ plan) {
   __shared__ int wsum[2][32];
@@ -77,7 +83,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict
     const int b = base + tid;
     int nc = 0, nt = 0;
     if (b < p.c.slots) {
-      const SlotSpan s = slot_span(p, b);
+      const SlotSpan s = chunk_span(p, b);
       if (s.code) paged_error(p.c.status, s.code);
       nc = (s.n + B - 1) / B;
       nt = s.n ? live_tiles(s.t0, p.window, p.sinks, KT).count : 0;
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
   const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, H = p.c.heads;
   if (c >= cstart[p.c.slots]) return;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
   const T *k = (const T*)p.k, *v = (const T*)p.v, *wv = (const T*)p.w, *q = (const T*)p.q;
   const size_t tok0 = (size_t)sp.q0 + r0;
@@ -281,7 +287,7 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads, h = qh / p.G;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   const int lc = c - cstart[b], rows = min(B, sp.n - lc * B);
   const size_t row = ((size_t)c * p.hq + qh) * B;
   float* z = (float*)(ws + w.z) + row * D;
@@ -352,7 +358,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   float *sR = sm, *sF = sR + D * DS, *sK = sF + D * DS;
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads;
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   if (sp.n == 0) return;
   const int nc = cstart[b + 1] - cstart[b];
   T* kp = (T*)p.c.k_pool;
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
   const int c = blockIdx.x, qh = blockIdx.y, split = blockIdx.z, tid = threadIdx.x;
   if (c >= cstart[p.c.slots]) return;
   const int h = qh / p.G, b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
   const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, KT);
   const int per = (lt.count + w.nsplit - 1) / w.nsplit;
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
     const int nt = tstart[b + 1] - tstart[b];
     const long long in = u - (long long)tstart[b] * H;
     const int h = (int)(in / nt), i = (int)(in % nt);
-    const SlotSpan sp = slot_span(p, b);
+    const SlotSpan sp = chunk_span(p, b);
     const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, KT);
     const int j0 = live_tile(lt, i) * KT;
     __syncthreads();
@@ -560,7 +566,7 @@ __global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const
   const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (c >= cstart[p.c.slots]) return;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
   const float *gm = (const float*)(ws + w.m), *gl = (const float*)(ws + w.l), *ga = (const float*)(ws + w.acc);
   const size_t stride = (size_t)w.nch * p.hq * B;
@@ -620,7 +626,17 @@ cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st) {
                                       : chunk_t<float, kHeadDimWide>(p, ws, st);
 }
 
-size_t paged_ws_bytes(const PagedArgs& p) { return paged_chunk_ws_bytes(p); }
-cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st) { return launch_paged_chunk(p, ws, st); }
+size_t paged_ws_bytes(const PagedArgs& p) {
+  if (p.c.cache_dtype != PATH_BF16) return paged_chunk_ws_bytes(p);
+  return paged_token_ws_bytes(p) + (p.max_new > 1 ? paged_chunk_ws_bytes(p) : 0);
+}
+cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st) {
+  if (p.c.cache_dtype != PATH_BF16) return launch_paged_chunk(p, ws, st);
+  const cudaError_t e = launch_paged_token(p, ws, st);
+  if (e != cudaSuccess || p.max_new <= 1) return e;
+  PagedArgs more = p;
+  more.min_new = 2;
+  return launch_paged_chunk(more, ws + paged_token_ws_bytes(p), st);
+}
 
 }  // namespace pathattn

@@ -1,0 +1,668 @@
+// Paged serving of bf16 caches, few new tokens per slot (one token, or draft tokens): one pass over the
+// cache that reads every key and value once and writes every key once.
+//
+// Mathematics: as in paged_chunk.cu, with the slot's n <= 16 new tokens as a single chunk.  Per key head
+// the n * G transported queries z (G query heads per key head) and the n rows of W meet a cached key k as
+//   s = k . z,   c = k W^T,   k <- k - c Y   (Y = U^T W;  n = 1: Y = beta w, z = q - beta (w . q) w).
+//
+// Bound: HBM (key read, key write, value read: 6 D bytes per cached row and head).  So:
+//  * every warp works alone, without barriers, on its share of the call: the (slot, head, 16-row tile) units
+//    of all sequences in one list, cut into equal runs, so that ragged lengths load all SMs alike; a run that
+//    ends inside a (slot, head) leaves a partial softmax state, merged by a second kernel in a fixed order;
+//  * a tile's rows go from global memory straight into the operand registers of 16x8x16 warp MMAs: the
+//    operands' summation index may be permuted at will as long as both sides agree, so a lane's 16-byte
+//    piece of a key row is two A fragments of K Z^T and of K W^T (keys are the 16 rows, queries and tokens the
+//    columns), and its pieces of four value rows, paired by byte permutes, are A fragments of V^T P^T.  The
+//    rewritten key leaves in the registers it came in.  tcgen05 would take 64 or 128 rows of queries where there are
+//    1 to 32 and a trip through shared memory; here the tensor work stays far below the memory time;
+//  * z, P and c are held as bf16 pairs (high + rest, about 16 bits), so that the only rounding to 8 bits is the
+//    one that the cache and the output need: the extra MMAs are free under the memory bound.
+#include "paged.h"
+#include "dev_common.cuh"
+#include "mma_common.cuh"
+
+namespace pathattn {
+namespace {
+
+constexpr int NT = 128, WARPS = NT / 32;
+constexpr int RT = 16;             // rows per tile
+constexpr int kSmemSlots = 1024;   // slots whose unit list each block builds for itself
+constexpr float kTau = 8.f;        // lazy rescale: the reference moves when a score exceeds it by 2^8
+
+struct TokenWs {
+  int blocks;              // of the streaming kernel
+  int nq;                  // query columns of a (slot, head): 8 NQ8
+  size_t ustart;           // int [slots + 1]: first unit of each slot (more than kSmemSlots slots)
+  size_t m, l, acc;        // partial states [2 * warps][nq](, [D])
+  size_t frag;             // draft tokens: per (slot, head) z and W, Y fragments
+  size_t sm, sl, sacc;     // draft tokens: the new tokens' own state [slots][H][nq](, [D])
+  size_t total;
+};
+
+// Blocks per SM: what the registers of the operands in flight (32 at head dim 64, 64 at 128) and of the
+// accumulators (D NQ8 / 4) leave without spills.
+constexpr int blocks_per_sm(int D, int nq8) { return D == 64 ? (nq8 == 1 ? 4 : nq8 == 2 ? 3 : 2) : (nq8 == 1 ? 3 : 2); }
+
+// Which slots the kernels here take: by the tokens of a slot.
+enum { kOnlyOne = 0, kDrafts = 1 };
+
+template <int D, int NQ8>
+constexpr int frag_words() {  // uint32 per lane of one (slot, head): z high and rest, W, Y high and rest
+  return NQ8 * (D / 8) * 2 + 2 * (D / 8) + 2 * (D / 8) * 2;
+}
+int token_nq(const PagedArgs& p, int n) {  // query columns for slots of at most n tokens
+  const int c = n * p.G;
+  return c <= 8 ? 8 : c <= 16 ? 16 : 32;
+}
+TokenWs token_ws(const PagedArgs& p, int n) {
+  TokenWs w{};
+  const size_t D = p.c.head_dim;
+  w.nq = token_nq(p, n);
+  const long long most = (long long)p.c.slots * p.c.heads * (((long long)p.c.table_width * p.c.page_size + RT - 1) / RT);
+  const int full = 152 * blocks_per_sm((int)D, w.nq / 8);
+  w.blocks = (int)(most < (long long)full * WARPS ? (most + WARPS - 1) / WARPS : full);
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, 256); return o; };
+  w.ustart = take((size_t)(p.c.slots + 1) * 4);
+  const size_t parts = (size_t)2 * w.blocks * WARPS * w.nq;
+  w.m = take(parts * 4);
+  w.l = take(parts * 4);
+  w.acc = take(parts * D * 4);
+  if (n > 1) {
+    const size_t items = (size_t)p.c.slots * p.c.heads;
+    w.frag = take(items * 32 * 4 * (size_t)((w.nq / 8) * (D / 8) * 2 + 2 * (D / 8) + 2 * (D / 8) * 2));
+    w.sm = take(items * w.nq * 4);
+    w.sl = take(items * w.nq * 4);
+    w.sacc = take(items * w.nq * D * 4);
+  }
+  w.total = off;
+  return w;
+}
+
+// Units of a slot: its live tiles for every head, at least one per head (the new tokens themselves).
+__device__ __forceinline__ int slot_units(const PagedArgs& p, int b, int mode, bool report) {
+  const SlotSpan s = slot_span(p, b);
+  if (report && s.code) paged_error(p.c.status, s.code);
+  if (s.n == 0 || (mode == kOnlyOne && s.n != 1)) return 0;
+  const int nt = live_tiles(s.t0, p.window, p.sinks, RT).count;
+  return (nt > 0 ? nt : 1) * p.c.heads;
+}
+// First unit of each slot, by the whole block; out may be shared memory.
+template <int THREADS>
+__device__ void unit_starts(const PagedArgs& p, int mode, bool report, int* out) {
+  __shared__ int wsum[THREADS / 32], carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) carry = 0;
+  __syncthreads();
+  for (int base = 0; base < p.c.slots; base += THREADS) {
+    const int b = base + tid;
+    const int n = b < p.c.slots ? slot_units(p, b, mode, report) : 0;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += a;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (b < p.c.slots) out[b] = before + x - n;
+    __syncthreads();
+    if (tid == THREADS - 1) carry = before + x;
+    __syncthreads();
+  }
+  if (tid == 0) out[p.c.slots] = carry;
+  __syncthreads();
+}
+__global__ void __launch_bounds__(1024) unit_starts_kernel(PagedArgs p, int mode, int* out) {
+  unit_starts<1024>(p, mode, true, out);
+}
+__device__ __forceinline__ int find_slot(const int* start, int slots, int u) {
+  int lo = 0, hi = slots;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+__device__ __forceinline__ int first_unit(int w, int units, int warps) { return (int)((long long)units * w / warps); }
+
+__device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// One warp: the softmax state of the query columns over the rows it has met.
+template <int D, int NQ8>
+struct State {
+  float acc[NQ8][D / 16][4];  // O^T: tile j of column tile q; lane (g, t): d = 64 (j / 4) + 8 g + 2 (j % 4) (+ 1: c2, c3),
+                              // columns 2t (c0, c2) and 2t + 1 (c1, c3)
+  float m[NQ8][2], l[NQ8][2];  // reference (the same in all lanes of a column), this lane's share of the sum
+};
+
+// ONE: every slot of the list has one token.  Otherwise the fragments come from draft_prep_kernel.
+template <int D, int NQ8, bool ONE, bool FOX>
+__global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
+  __shared__ int s_start[kSmemSlots + 1];
+  // z in B fragment order: registers where they are few, else one copy per warp in shared memory
+  constexpr bool ZS = ONE && (D == 128 || NQ8 > 1);
+  __shared__ uint4 s_z[ZS ? WARPS : 1][ZS ? NQ8 * 2 * (D / 32) : 1][32];
+  constexpr int KB = D / 32;  // 32-column blocks of a row: a lane holds one 16-byte piece of each
+  constexpr int CS = D / 64;  // 64-column blocks: value pieces per row and lane
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = blockIdx.x * WARPS + (threadIdx.x >> 5), warps = gridDim.x * WARPS;
+  const int H = p.c.heads, G = p.G, P = p.c.page_size;
+  const int* start;
+  if (p.c.slots <= kSmemSlots) {
+    unit_starts<NT>(p, ONE ? kOnlyOne : kDrafts, blockIdx.x == 0, s_start);
+    start = s_start;
+  } else {
+    start = (const int*)(ws + w.ustart);
+  }
+  const int units = start[p.c.slots];
+  const int u0 = first_unit(warp, units, warps), u1 = first_unit(warp + 1, units, warps);
+  if (u0 >= u1) return;
+
+  const __nv_bfloat16* kpool = (const __nv_bfloat16*)p.c.k_pool;
+  const __nv_bfloat16* vpool = (const __nv_bfloat16*)p.c.v_pool;
+  int b = find_slot(start, p.c.slots, u0);
+  int u = u0;
+  while (u < u1) {
+    while (start[b + 1] <= u) ++b;  // slots without units are passed over
+    const SlotSpan sp = slot_span(p, b);
+    const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, RT);
+    const int per = lt.count > 0 ? lt.count : 1;
+    const int h = (u - start[b]) / per;
+    const int s0 = start[b] + h * per;           // the item's first unit
+    const int e0 = s0 + per;                     // and the one behind it
+    const int ue = e0 < u1 ? e0 : u1;
+    const int n = ONE ? 1 : sp.n;
+    const int cols = n * G;
+    State<D, NQ8> st;
+    uint32_t zh[ZS ? 1 : NQ8][KB][4], zl[ZS ? 1 : NQ8][KB][4];  // ONE: z in B fragment order
+    uint32_t wf[KB][4];                          // ONE: the lane's pieces of w
+    float beta = 0.f;
+    const uint32_t* frag = nullptr;              // drafts: this item's fragments, lane-major words
+    // bias of a column's token since t0 (FOX) and its position
+    float cb[NQ8][2];
+    int cp[NQ8][2];
+#pragma unroll
+    for (int q = 0; q < NQ8; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 8 * q + 2 * t + e, i = col < cols ? col / G : 0;
+        cp[q][e] = sp.t0 + i;
+        cb[q][e] = 0.f;
+        if (FOX)
+          for (int x = 0; x <= i; ++x) cb[q][e] += p.log_f[((size_t)sp.q0 + x) * H + h];
+      }
+    float a_last = 0.f;
+    if (FOX && sp.t0 > 0) {
+      const long long r = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1);
+      if (r >= 0) a_last = p.c.a_pool[r];
+    }
+    const size_t tok = (size_t)sp.q0 * H + h;    // the first new token's row of k, v, w
+    if constexpr (ONE) {
+      beta = clamp_beta(p.beta[tok]);
+      float wd[KB][8];
+#pragma unroll
+      for (int x = 0; x < KB; ++x) {
+        const uint4 r = ld16((const __nv_bfloat16*)p.w + tok * D + 32 * x + 8 * t);
+        wf[x][0] = r.x; wf[x][1] = r.y; wf[x][2] = r.z; wf[x][3] = r.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { wd[x][2 * i] = lo_f(wf[x][i]); wd[x][2 * i + 1] = hi_f(wf[x][i]); }
+      }
+#pragma unroll
+      for (int q = 0; q < NQ8; ++q) {
+        const int col = 8 * q + g;
+        float qd[KB][8], dot = 0.f, self = 0.f;
+#pragma unroll
+        for (int x = 0; x < KB; ++x) {
+          uint4 r = make_uint4(0, 0, 0, 0);
+          if (col < cols) r = ld16((const __nv_bfloat16*)p.q + ((size_t)sp.q0 * p.hq + h * G + col) * D + 32 * x + 8 * t);
+          const uint4 kr = ld16((const __nv_bfloat16*)p.k + tok * D + 32 * x + 8 * t);
+          const uint32_t rr[4] = {r.x, r.y, r.z, r.w}, kk[4] = {kr.x, kr.y, kr.z, kr.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            qd[x][2 * i] = lo_f(rr[i]);
+            qd[x][2 * i + 1] = hi_f(rr[i]);
+            dot += qd[x][2 * i] * wd[x][2 * i] + qd[x][2 * i + 1] * wd[x][2 * i + 1];
+            self += qd[x][2 * i] * lo_f(kk[i]) + qd[x][2 * i + 1] * hi_f(kk[i]);
+          }
+        }
+        dot = group_sum<4>(dot) * beta;
+        self = group_sum<4>(self) * p.scl;
+#pragma unroll
+        for (int x = 0; x < KB; ++x) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            split2(qd[x][2 * i] - dot * wd[x][2 * i], qd[x][2 * i + 1] - dot * wd[x][2 * i + 1], hi[i], lo[i]);
+          if constexpr (ZS) {  // (read back by the same lane only)
+            s_z[threadIdx.x >> 5][(2 * q) * KB + x][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            s_z[threadIdx.x >> 5][(2 * q + 1) * KB + x][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { zh[q][x][i] = hi[i]; zl[q][x][i] = lo[i]; }
+          }
+        }
+        // the new token's own score, at the lanes of its column
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float s = __shfl_sync(0xffffffffu, self, (2 * t + e) * 4);
+          st.m[q][e] = u == s0 ? s : -INFINITY;
+          st.l[q][e] = u == s0 && g == 0 ? 1.f : 0.f;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < CS; ++x) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (u == s0) r = ld16((const __nv_bfloat16*)p.v + tok * D + 64 * x + 8 * g);
+        const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = 0; q < NQ8; ++q) {
+            st.acc[q][4 * x + i][0] = st.acc[q][4 * x + i][1] = lo_f(rr[i]);
+            st.acc[q][4 * x + i][2] = st.acc[q][4 * x + i][3] = hi_f(rr[i]);
+          }
+      }
+      if (u == s0) {  // the new row joins the cache
+        const long long kr = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0);
+        const long long vr = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0);
+        if (kr < 0 || vr < 0) {
+          if (lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+        } else {
+          if (lane < D / 8) {
+            *reinterpret_cast<uint4*>((__nv_bfloat16*)p.c.k_pool + kr * D + lane * 8) = ld16((const __nv_bfloat16*)p.k + tok * D + lane * 8);
+            *reinterpret_cast<uint4*>((__nv_bfloat16*)p.c.v_pool + vr * D + lane * 8) = ld16((const __nv_bfloat16*)p.v + tok * D + lane * 8);
+          }
+          if (FOX && lane == 0) p.c.a_pool[vr] = a_last + p.log_f[tok];
+        }
+      }
+    } else {
+      const size_t item = (size_t)b * H + h;
+      frag = (const uint32_t*)(ws + w.frag) + item * 32 * frag_words<D, NQ8>();
+      // the item's first run starts from the new tokens' own state
+#pragma unroll
+      for (int q = 0; q < NQ8; ++q) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const size_t at = item * w.nq + 8 * q + 2 * t + e;
+          st.m[q][e] = u == s0 ? __ldg((const float*)(ws + w.sm) + at) : -INFINITY;
+          st.l[q][e] = u == s0 && g == 0 ? __ldg((const float*)(ws + w.sl) + at) : 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            float2 v = make_float2(0.f, 0.f);
+            if (u == s0)
+              v = __ldg(reinterpret_cast<const float2*>((const float*)(ws + w.sacc) + at * D + 64 * (j / 4) + 8 * g + 2 * (j % 4)));
+            st.acc[q][j][e] = v.x;
+            st.acc[q][j][2 + e] = v.y;
+          }
+        }
+      }
+    }
+
+    // ---- the cached tiles ----
+    const int i0 = u - s0, i1 = lt.count > 0 ? ue - s0 : i0;  // (no cached rows: nothing to stream)
+    uint4 kr[2][KB], vr[4][CS];
+    float aj[2] = {0.f, 0.f};
+    auto page = [&](const int* table, int i) { return __ldg(table + (size_t)b * p.c.table_width + live_tile(lt, i) * RT / P); };
+    int kp = -1, vp = -1, kpn = -1, vpn = -1;  // pages of the current and the next tile
+    long long krow = 0, vrow = 0;
+    auto rows_of = [&](int i, int pk, int pv, long long& rk, long long& rv) {
+      const int in = live_tile(lt, i) * RT % P;
+      rk = ((long long)pk * H + h) * P + in;
+      rv = ((long long)pv * H + h) * P + in;
+    };
+    auto good = [&](int pk, int pv) { return (unsigned)pk < (unsigned)p.c.k_pages && (unsigned)pv < (unsigned)p.c.v_pages; };
+    auto load_k = [&](long long r) {
+      const __nv_bfloat16* at = kpool + r * D + 8 * t;
+#pragma unroll
+      for (int x = 0; x < KB; ++x) {
+        kr[0][x] = ld16(at + (size_t)g * D + 32 * x);
+        kr[1][x] = ld16(at + (size_t)(g + 8) * D + 32 * x);
+      }
+    };
+    auto load_v = [&](long long r) {
+      const __nv_bfloat16* at = vpool + r * D + 8 * g;
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int x = 0; x < CS; ++x) vr[y][x] = ld16(at + (size_t)(2 * t + (y & 1) + 8 * (y >> 1)) * D + 64 * x);
+      if (FOX) {
+        aj[0] = p.c.a_pool[r + g];
+        aj[1] = p.c.a_pool[r + g + 8];
+      }
+    };
+    bool ok = false;
+    if (i0 < i1) {
+      kp = page(p.c.k_table, i0);
+      vp = page(p.c.v_table, i0);
+      ok = good(kp, vp);
+      if (ok) {
+        rows_of(i0, kp, vp, krow, vrow);
+        load_k(krow);
+        load_v(vrow);
+      }
+      if (i0 + 1 < i1) {
+        kpn = page(p.c.k_table, i0 + 1);
+        vpn = page(p.c.v_table, i0 + 1);
+      }
+    }
+    for (int i = i0; i < i1; ++i) {
+      const int j0 = live_tile(lt, i) * RT;
+      const bool cur = ok;
+      if (!cur && lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+      float s[NQ8][4], c[ONE ? 1 : 2][4];
+      // whole: every row of the tile is there, seen by every token and kept
+      const bool whole = j0 + RT <= sp.t0 && (p.window <= 0 || j0 > sp.t0 + n - p.window || j0 + RT <= p.sinks);
+      const long long kat = krow;
+      if (cur) {
+        // scores and rewriting coefficients; the A fragments are the loaded pieces
+#pragma unroll
+        for (int q = 0; q < NQ8; ++q) s[q][0] = s[q][1] = s[q][2] = s[q][3] = 0.f;
+#pragma unroll
+        for (int q = 0; q < (ONE ? 1 : 2); ++q) c[q][0] = c[q][1] = c[q][2] = c[q][3] = 0.f;
+#pragma unroll
+        for (int x = 0; x < KB; ++x) {
+          const uint32_t r0[4] = {kr[0][x].x, kr[0][x].y, kr[0][x].z, kr[0][x].w};
+          const uint32_t r1[4] = {kr[1][x].x, kr[1][x].y, kr[1][x].z, kr[1][x].w};
+          uint4 zq[ZS ? NQ8 : 1][2];
+          if constexpr (ZS) {
+#pragma unroll
+            for (int q = 0; q < NQ8; ++q) {
+              zq[q][0] = s_z[threadIdx.x >> 5][(2 * q) * KB + x][lane];
+              zq[q][1] = s_z[threadIdx.x >> 5][(2 * q + 1) * KB + x][lane];
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t a0 = r0[2 * y], a1 = r1[2 * y], a2 = r0[2 * y + 1], a3 = r1[2 * y + 1];
+            if constexpr (ONE) {
+#pragma unroll
+              for (int q = 0; q < NQ8; ++q) {
+                if constexpr (ZS) {
+                  mma_bf16(s[q], a0, a1, a2, a3, y ? zq[q][0].z : zq[q][0].x, y ? zq[q][0].w : zq[q][0].y);
+                  mma_bf16(s[q], a0, a1, a2, a3, y ? zq[q][1].z : zq[q][1].x, y ? zq[q][1].w : zq[q][1].y);
+                } else {
+                  mma_bf16(s[q], a0, a1, a2, a3, zh[q][x][2 * y], zh[q][x][2 * y + 1]);
+                  mma_bf16(s[q], a0, a1, a2, a3, zl[q][x][2 * y], zl[q][x][2 * y + 1]);
+                }
+              }
+              const uint32_t b0 = g == 0 ? wf[x][2 * y] : 0u, b1 = g == 0 ? wf[x][2 * y + 1] : 0u;
+              mma_bf16(c[0], a0, a1, a2, a3, b0, b1);
+            } else {
+              // words of a fragment: [z: column tile][high, rest][W: token tile], pairs (b0, b1) per (x, y)
+              const uint2* f = reinterpret_cast<const uint2*>(frag) + lane;
+              const int k = 2 * x + y;
+#pragma unroll
+              for (int q = 0; q < NQ8; ++q) {
+                const uint2 zhv = __ldg(f + ((2 * q) * (D / 16) + k) * 32), zlv = __ldg(f + ((2 * q + 1) * (D / 16) + k) * 32);
+                mma_bf16(s[q], a0, a1, a2, a3, zhv.x, zhv.y);
+                mma_bf16(s[q], a0, a1, a2, a3, zlv.x, zlv.y);
+              }
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint2 wv = __ldg(f + ((2 * NQ8 + q) * (D / 16) + k) * 32);
+                mma_bf16(c[q], a0, a1, a2, a3, wv.x, wv.y);
+              }
+            }
+          }
+        }
+        // k <- k - c Y, stored where it came from
+        bool keep0 = true, keep1 = true;
+        if (!whole) {
+          keep0 = j0 + g < sp.t0 && sees(p.window, p.sinks, sp.t0 + n, j0 + g);
+          keep1 = j0 + g + 8 < sp.t0 && sees(p.window, p.sinks, sp.t0 + n, j0 + g + 8);
+        }
+        __nv_bfloat16* dst = (__nv_bfloat16*)p.c.k_pool + kat * D + 8 * t;
+        if constexpr (ONE) {
+          const float c0 = -beta * __shfl_sync(0xffffffffu, c[0][0], lane & 28), c1 = -beta * __shfl_sync(0xffffffffu, c[0][2], lane & 28);
+#pragma unroll
+          for (int x = 0; x < KB; ++x) {
+            uint32_t r0[4] = {kr[0][x].x, kr[0][x].y, kr[0][x].z, kr[0][x].w};
+            uint32_t r1[4] = {kr[1][x].x, kr[1][x].y, kr[1][x].z, kr[1][x].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float wl = lo_f(wf[x][y]), wh = hi_f(wf[x][y]);
+              r0[y] = pack2(fmaf(c0, wl, lo_f(r0[y])), fmaf(c0, wh, hi_f(r0[y])));
+              r1[y] = pack2(fmaf(c1, wl, lo_f(r1[y])), fmaf(c1, wh, hi_f(r1[y])));
+            }
+            if (keep0) *reinterpret_cast<uint4*>(dst + (size_t)g * D + 32 * x) = make_uint4(r0[0], r0[1], r0[2], r0[3]);
+            if (keep1) *reinterpret_cast<uint4*>(dst + (size_t)(g + 8) * D + 32 * x) = make_uint4(r1[0], r1[1], r1[2], r1[3]);
+          }
+        } else {
+          uint32_t ah[4], al[4];  // c as an A fragment over 16 tokens
+          split2(c[0][0], c[0][1], ah[0], al[0]);
+          split2(c[0][2], c[0][3], ah[1], al[1]);
+          split2(c[1][0], c[1][1], ah[2], al[2]);
+          split2(c[1][2], c[1][3], ah[3], al[3]);
+          const uint2* f = reinterpret_cast<const uint2*>(frag) + (2 * NQ8 + 2) * (D / 16) * 32 + lane;
+#pragma unroll
+          for (int x = 0; x < KB; ++x) {
+            uint32_t r0[4] = {kr[0][x].x, kr[0][x].y, kr[0][x].z, kr[0][x].w};
+            uint32_t r1[4] = {kr[1][x].x, kr[1][x].y, kr[1][x].z, kr[1][x].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              float k4[4] = {lo_f(r0[y]), hi_f(r0[y]), lo_f(r1[y]), hi_f(r1[y])};
+              const uint2 yh = __ldg(f + (4 * x + y) * 32), yl = __ldg(f + (D / 8 + 4 * x + y) * 32);  // -Y
+              mma_bf16(k4, ah[0], ah[1], ah[2], ah[3], yh.x, yh.y);
+              mma_bf16(k4, al[0], al[1], al[2], al[3], yh.x, yh.y);
+              mma_bf16(k4, ah[0], ah[1], ah[2], ah[3], yl.x, yl.y);
+              r0[y] = pack2(k4[0], k4[1]);
+              r1[y] = pack2(k4[2], k4[3]);
+            }
+            if (keep0) *reinterpret_cast<uint4*>(dst + (size_t)g * D + 32 * x) = make_uint4(r0[0], r0[1], r0[2], r0[3]);
+            if (keep1) *reinterpret_cast<uint4*>(dst + (size_t)(g + 8) * D + 32 * x) = make_uint4(r1[0], r1[1], r1[2], r1[3]);
+          }
+        }
+      }
+      // the next tile's keys set out as soon as this one's registers are free
+      long long kn = 0, vn = 0;
+      ok = i + 1 < i1 && good(kpn, vpn);
+      if (ok) {
+        rows_of(i + 1, kpn, vpn, kn, vn);
+        load_k(kn);
+      }
+      krow = kn;
+      const long long vnext = vn;
+      if (i + 2 < i1) {
+        kpn = page(p.c.k_table, i + 2);
+        vpn = page(p.c.v_table, i + 2);
+      }
+      if (cur) {
+        const float bias0 = FOX ? a_last - aj[0] : 0.f, bias1 = FOX ? a_last - aj[1] : 0.f;
+        bool up = false;
+#pragma unroll
+        for (int q = 0; q < NQ8; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = s[q][e] * p.scl;
+            if (FOX) x += ((e < 2 ? bias0 : bias1) + cb[q][e & 1]) * kLog2e;
+            if (!whole) {
+              const int j = j0 + g + (e < 2 ? 0 : 8);
+              if (j >= sp.t0 || !sees(p.window, p.sinks, cp[q][e & 1], j)) x = -INFINITY;
+            }
+            s[q][e] = x;
+            up |= x > st.m[q][e & 1] + kTau;
+          }
+        if (!whole) {  // rows behind the sequence may hold anything: 0 times that has to be 0
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (j0 + 2 * t + (y & 1) + 8 * (y >> 1) >= sp.t0) {
+#pragma unroll
+              for (int x = 0; x < CS; ++x) vr[y][x] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int q = 0; q < NQ8; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(s[q][e], s[q][e + 2]);
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              const float mo = st.m[q][e], mn = fmaxf(mo, x);
+              const float f = mn == -INFINITY ? 1.f : fast_exp2(mo - mn);
+              st.m[q][e] = mn;
+              st.l[q][e] *= f;
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) {
+                st.acc[q][j][e] *= f;
+                st.acc[q][j][e + 2] *= f;
+              }
+            }
+        }
+        // probabilities as B fragments of V^T P^T: keys become the rows
+        uint32_t ph[NQ8][2], pl[NQ8][2];
+#pragma unroll
+        for (int q = 0; q < NQ8; ++q) {
+          const float m0 = st.m[q][0] == -INFINITY ? 0.f : st.m[q][0], m1 = st.m[q][1] == -INFINITY ? 0.f : st.m[q][1];
+          const float p0 = fast_exp2(s[q][0] - m0), p1 = fast_exp2(s[q][1] - m1);
+          const float p2 = fast_exp2(s[q][2] - m0), p3 = fast_exp2(s[q][3] - m1);
+          st.l[q][0] += p0 + p2;
+          st.l[q][1] += p1 + p3;
+          uint32_t h0, h1, l0, l1;
+          split2(p0, p1, h0, l0);
+          split2(p2, p3, h1, l1);
+          ph[q][0] = transpose8(h0);
+          ph[q][1] = transpose8(h1);
+          pl[q][0] = transpose8(l0);
+          pl[q][1] = transpose8(l1);
+        }
+#pragma unroll
+        for (int x = 0; x < CS; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            auto word = [&](int k) { return y == 0 ? vr[k][x].x : y == 1 ? vr[k][x].y : y == 2 ? vr[k][x].z : vr[k][x].w; };
+            const uint32_t a0 = __byte_perm(word(0), word(1), 0x5410), a1 = __byte_perm(word(0), word(1), 0x7632);
+            const uint32_t a2 = __byte_perm(word(2), word(3), 0x5410), a3 = __byte_perm(word(2), word(3), 0x7632);
+#pragma unroll
+            for (int q = 0; q < NQ8; ++q) {
+              mma_bf16(st.acc[q][4 * x + y], a0, a1, a2, a3, ph[q][0], ph[q][1]);
+              mma_bf16(st.acc[q][4 * x + y], a0, a1, a2, a3, pl[q][0], pl[q][1]);
+            }
+          }
+      }
+      if (ok) load_v(vnext);
+    }
+
+    // ---- the item's end or the run's: output, or a partial state ----
+    const bool complete = u == s0 && ue == e0;
+    const size_t slot = ((size_t)2 * warp + (u == u0 ? 0 : 1)) * w.nq;
+#pragma unroll
+    for (int q = 0; q < NQ8; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = st.l[q][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int col = 8 * q + 2 * t + e;
+        if (col >= cols) continue;
+        if (complete) {
+          const float inv = 1.f / l;
+          __nv_bfloat16* o = (__nv_bfloat16*)p.o + (((size_t)sp.q0 + col / G) * p.hq + h * G + col % G) * D + 8 * g;
+#pragma unroll
+          for (int x = 0; x < CS; ++x) {
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = pack2(st.acc[q][4 * x + i][e] * inv, st.acc[q][4 * x + i][2 + e] * inv);
+            *reinterpret_cast<uint4*>(o + 64 * x) = make_uint4(r[0], r[1], r[2], r[3]);
+          }
+        } else {
+          if (g == 0) {
+            ((float*)(ws + w.m))[slot + col] = st.m[q][e];
+            ((float*)(ws + w.l))[slot + col] = l;
+          }
+          float* a = (float*)(ws + w.acc) + (slot + col) * D + 8 * g;
+#pragma unroll
+          for (int x = 0; x < CS; ++x) {
+            *reinterpret_cast<float4*>(a + 64 * x) = make_float4(st.acc[q][4 * x][e], st.acc[q][4 * x][2 + e],
+                                                                 st.acc[q][4 * x + 1][e], st.acc[q][4 * x + 1][2 + e]);
+            *reinterpret_cast<float4*>(a + 64 * x + 4) = make_float4(st.acc[q][4 * x + 2][e], st.acc[q][4 * x + 2][2 + e],
+                                                                     st.acc[q][4 * x + 3][e], st.acc[q][4 * x + 3][2 + e]);
+          }
+        }
+      }
+    u = ue;
+  }
+}
+
+// Merge of the partial states: one block per (slot, head), one warp per query column, runs in list order.
+template <int D>
+__global__ void __launch_bounds__(NT) token_merge_kernel(PagedArgs p, TokenWs w, const char* __restrict__ ws, int mode, int warps) {
+  __shared__ int s_start[kSmemSlots + 1];
+  const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const SlotSpan sp = slot_span(p, b);
+  if (sp.n == 0 || (mode == kOnlyOne && sp.n != 1)) return;
+  const int* start;
+  if (p.c.slots <= kSmemSlots) {
+    unit_starts<NT>(p, mode, false, s_start);
+    start = s_start;
+  } else {
+    start = (const int*)(ws + w.ustart);
+  }
+  const int units = start[p.c.slots];
+  const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, RT);
+  const int per = lt.count > 0 ? lt.count : 1;
+  const int s0 = start[b] + h * per, e0 = s0 + per;
+  // the runs that hold units s0 and e0 - 1
+  auto run_of = [&](int u) {
+    int r = (int)(((long long)u * warps) / units);
+    while (first_unit(r + 1, units, warps) <= u) ++r;
+    while (first_unit(r, units, warps) > u) --r;
+    return r;
+  };
+  const int ra = run_of(s0), rb = run_of(e0 - 1);
+  if (ra == rb) return;  // written by its run
+  const float *gm = (const float*)(ws + w.m), *gl = (const float*)(ws + w.l), *ga = (const float*)(ws + w.acc);
+  const int lead = first_unit(ra, units, warps) == s0 ? 0 : 1;  // the place of run ra's part
+  for (int col = wid; col < sp.n * p.G; col += WARPS) {
+    auto at = [&](int r) { return ((size_t)2 * r + (r == ra ? lead : 0)) * w.nq + col; };
+    float M = -INFINITY;
+    for (int r = ra + lane; r <= rb; r += 32)
+      if (first_unit(r, units, warps) < first_unit(r + 1, units, warps)) M = fmaxf(M, gm[at(r)]);
+    M = group_max<32>(M);
+    float l = 0.f, a[D / 32];
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) a[x] = 0.f;
+    for (int r = ra; r <= rb; ++r) {
+      if (first_unit(r, units, warps) >= first_unit(r + 1, units, warps)) continue;  // an empty run
+      const float ms = gm[at(r)];
+      const float f = ms == -INFINITY ? 0.f : fast_exp2(ms - M);
+      l += gl[at(r)] * f;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) a[x] += ga[at(r) * D + x * 32 + lane] * f;
+    }
+    __nv_bfloat16* o = (__nv_bfloat16*)p.o + (((size_t)sp.q0 + col / p.G) * p.hq + h * p.G + col % p.G) * D;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) o[x * 32 + lane] = __float2bfloat16_rn(a[x] * inv);
+  }
+}
+
+template <int D, int NQ8, bool ONE, bool FOX>
+cudaError_t token_t(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
+  const int mode = ONE ? kOnlyOne : kDrafts;
+  if (p.c.slots > kSmemSlots) unit_starts_kernel<<<1, 1024, 0, st>>>(p, mode, (int*)(ws + w.ustart));
+  token_kernel<D, NQ8, ONE, FOX><<<w.blocks, NT, 0, st>>>(p, w, ws);
+  token_merge_kernel<D><<<dim3(p.c.slots, p.c.heads), NT, 0, st>>>(p, w, ws, mode, w.blocks * WARPS);
+  return cudaGetLastError();
+}
+template <int D, bool FOX>
+cudaError_t token_d(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
+  return w.nq == 8 ? token_t<D, 1, true, FOX>(p, w, ws, st) : token_t<D, 2, true, FOX>(p, w, ws, st);
+}
+
+}  // namespace
+
+size_t paged_token_ws_bytes(const PagedArgs& p) { return token_ws(p, 1).total; }
+cudaError_t launch_paged_token(const PagedArgs& p, char* ws, cudaStream_t st) {
+  const TokenWs w = token_ws(p, 1);
+  const bool fox = p.log_f != nullptr;
+  if (p.c.head_dim == kHeadDim) return fox ? token_d<kHeadDim, true>(p, w, ws, st) : token_d<kHeadDim, false>(p, w, ws, st);
+  return fox ? token_d<kHeadDimWide, true>(p, w, ws, st) : token_d<kHeadDimWide, false>(p, w, ws, st);
+}
+
+}  // namespace pathattn
