@@ -13,7 +13,7 @@
 //
 // Six launches: plan (lengths, chunk list), chunk preparation, then one of {query scan, key walk} per
 // block, cached attention split over key ranges, cached rewrite, and the merge of the splits.
-#include "paged.h"
+#include "paged_tc.h"
 #include "dev_common.cuh"
 #include "smem_mm.cuh"
 
@@ -36,6 +36,11 @@ struct ChunkWs {
   size_t z, qb;        // Q<-, then z [nch][hq][B][D]; row biases sum of log f since t0 [nch][hq][B]
   size_t m, l, acc;    // softmax states [nsplit][nch][hq][B](, [D])
   size_t mm;           // M [slots][H][D][D]
+  // bf16: the cached attention runs on the tensor cores
+  int pairs;           // query pairs of a head
+  size_t zq;           // z [H][pairs][256][D] bf16, row i G + g of a slot
+  size_t ps, us;       // first query pair (int) and first unit (long long) of each slot
+  size_t pm, pl, pacc, err;
   size_t total;
 };
 ChunkWs chunk_ws(const PagedArgs& p) {
@@ -47,6 +52,8 @@ ChunkWs chunk_ws(const PagedArgs& p) {
   const long long ctas = (long long)w.nch * p.hq;
   w.nsplit = ctas >= 1216 ? 1 : (int)((1216 + ctas - 1) / ctas);
   if (w.nsplit > 64) w.nsplit = 64;
+  const bool tc = p.c.cache_dtype == PATH_BF16;
+  if (tc) w.nsplit = 1;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, 256); return o; };
   w.plan = take((size_t)2 * (p.c.slots + 1) * 4);
@@ -60,6 +67,19 @@ ChunkWs chunk_ws(const PagedArgs& p) {
   w.l = take((size_t)w.nsplit * w.nch * hq * B * 4);
   w.acc = take((size_t)w.nsplit * w.nch * hq * B * D * 4);
   w.mm = take((size_t)p.c.slots * H * D * D * 4);
+  if (tc) {
+    const long long live = p.c.slots < p.total ? p.c.slots : p.total;
+    w.pairs = (int)(((long long)p.total * p.G + (kTcPair - 1) * live) / kTcPair);
+    if (w.pairs < 1) w.pairs = 1;
+    w.zq = take((size_t)H * w.pairs * kTcPair * D * 2);
+    w.ps = take((size_t)(p.c.slots + 1) * 4);
+    w.us = take((size_t)(p.c.slots + 1) * 8);
+    const size_t parts = (size_t)H * w.pairs + kTcBlocks;
+    w.pm = take(parts * kTcPair * 4);
+    w.pl = take(parts * kTcPair * 4);
+    w.pacc = take(parts * kTcPair * D * 4);
+    w.err = take(4);
+  }
   w.total = off;
   return w;
 }
@@ -104,6 +124,39 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict
     __syncthreads();
   }
   if (tid == 0) { cstart[p.c.slots] = carry[0]; tstart[p.c.slots] = carry[1]; }
+}
+
+// Query pairs and (head, pair, key tile) units of every slot (tensor-core attention); clears the wait code.
+__global__ void __launch_bounds__(1024) plan_tc_kernel(PagedArgs p, TcPlan pl) {
+  __shared__ long long wsum[2][32], carry[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 2) carry[tid] = 0;
+  if (tid == 0) *pl.err = 0;
+  __syncthreads();
+  for (int base = 0; base < p.c.slots; base += 1024) {
+    const int b = base + tid;
+    long long np = 0, nu = 0;
+    if (b < p.c.slots) {
+      const SlotSpan s = chunk_span(p, b);
+      np = ((long long)s.n * p.G + kTcPair - 1) / kTcPair;
+      nu = s.n ? np * p.c.heads * live_tiles(s.t0, p.window, p.sinks, kTcKeys).count : 0;
+    }
+    long long ip = np, iu = nu;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long a = __shfl_up_sync(0xffffffffu, ip, o), e = __shfl_up_sync(0xffffffffu, iu, o);
+      if (lane >= o) { ip += a; iu += e; }
+    }
+    if (lane == 31) { wsum[0][warp] = ip; wsum[1][warp] = iu; }
+    __syncthreads();
+    long long op = carry[0], ou = carry[1];
+    for (int w = 0; w < warp; ++w) { op += wsum[0][w]; ou += wsum[1][w]; }
+    if (b < p.c.slots) { pl.pstart[b] = (int)(op + ip - np); pl.ustart[b] = ou + iu - nu; }
+    __syncthreads();
+    if (tid == 1023) { carry[0] = op + ip; carry[1] = ou + iu; }
+    __syncthreads();
+  }
+  if (tid == 0) { pl.pstart[p.c.slots] = (int)carry[0]; pl.ustart[p.c.slots] = carry[1]; }
 }
 
 // The slot that owns entry x of a prefix array with x < start[slots].
@@ -295,8 +348,14 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   float *gm = (float*)(ws + w.m) + row, *gl = (float*)(ws + w.l) + row;
   const float* fa = (const float*)(ws + w.fa);
   const float* ft = (const float*)(ws + w.ft);
+  __nv_bfloat16* zq = nullptr;  // row 0 of the chunk, bf16: head g of token i in row i G + g
+  if (TC)
+    zq = (__nv_bfloat16*)(ws + w.zq) +
+         (((size_t)h * w.pairs + ((const int*)(ws + w.ps))[b]) * kTcPair + (size_t)lc * B * p.G + qh % p.G) * D;
   if (lc == 0) {  // already at the start of the new tokens
     if (p.log_f && tid < B) ((float*)(ws + w.qb))[row + tid] = fa[((size_t)c * H + h) * B + tid];
+    if (TC)
+      for (int e = tid; e < rows * D; e += NT) zq[(size_t)(e / D) * p.G * D + e % D] = __float2bfloat16_rn(z[e]);
     return;
   }
   for (int e = tid; e < B * D; e += NT) {
@@ -340,7 +399,8 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   }
   __syncthreads();
   for (int e = tid; e < B * D; e += NT) {
-    z[e] = sZ[(e / D) * DS + e % D];
+    if (!TC) z[e] = sZ[(e / D) * DS + e % D];
+    else if (e / D < rows) zq[(size_t)(e / D) * p.G * D + e % D] = __float2bfloat16_rn(sZ[(e / D) * DS + e % D]);
     acc[e] = sAcc[(e / D) * DS + e % D];
   }
   if (tid < B) {
@@ -592,6 +652,53 @@ __global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const
   }
 }
 
+// Merge of the tensor-core parts with the new tokens' own state: one warp per (row, query head), parts in list
+// order.  Cached scores lack the row's own bias (sum of log f since t0): it moves their maximum.
+template <int D>
+__global__ void __launch_bounds__(NT) merge_tc_kernel(PagedArgs p, ChunkWs w, TcPlan pl, const char* __restrict__ ws) {
+  const int* cstart = (const int*)(ws + w.plan);
+  const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (c == 0 && qh == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
+  if (c >= cstart[p.c.slots]) return;
+  const int b = owner(cstart, p.c.slots, c);
+  const SlotSpan sp = chunk_span(p, b);
+  const int lc = c - cstart[b], rows = min(B, sp.n - lc * B), h = qh / p.G, g = qh % p.G;
+  const int kt = live_tiles(sp.t0, p.window, p.sinks, kTcKeys).count;
+  const int np = pl.pstart[b + 1] - pl.pstart[b];
+  const long long units = pl.ustart[p.c.slots], per = (units + kTcBlocks - 1) / kTcBlocks;
+  for (int r = warp; r < rows; r += NT / 32) {
+    const size_t row = ((size_t)c * p.hq + qh) * B + r;
+    const int R = (lc * B + r) * p.G + g, pair = R / kTcPair;
+    const float m0 = ((const float*)(ws + w.m))[row], bias = p.log_f ? ((const float*)(ws + w.qb))[row] * kLog2e : 0.f;
+    float M = m0;
+    long long first = 0, last = -1;
+    const long long which = (long long)h * np + pair, item = (long long)pl.pstart[b] * p.c.heads + which;
+    if (kt > 0) {
+      const long long us = pl.ustart[b] + which * kt;
+      first = us / per;
+      last = (us + kt - 1) / per;
+    }
+    auto at = [&](long long x) { return (size_t)(item + x) * kTcPair + R % kTcPair; };
+    for (long long x = first; x <= last; ++x) M = fmaxf(M, pl.m[at(x)] + bias);
+    float f = fast_exp2(m0 - M);
+    float l = ((const float*)(ws + w.l))[row] * f, a[D / 32];
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) a[x] = ((const float*)(ws + w.acc))[row * D + x * 32 + lane] * f;
+    for (long long x = first; x <= last; ++x) {
+      const float ms = pl.m[at(x)];
+      if (ms == -INFINITY) continue;
+      f = fast_exp2(ms + bias - M);
+      l += pl.l[at(x)] * f;
+#pragma unroll
+      for (int y = 0; y < D / 32; ++y) a[y] += pl.acc[at(x) * D + y * 32 + lane] * f;
+    }
+    __nv_bfloat16* o = (__nv_bfloat16*)p.o + (((size_t)sp.q0 + lc * B + r) * p.hq + qh) * D;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) o[x * 32 + lane] = __float2bfloat16_rn(a[x] * inv);
+  }
+}
+
 template <typename T, int D>
 cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
   const ChunkWs w = chunk_ws(p);
@@ -606,12 +713,24 @@ cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
   if ((e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(att, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s3)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(rew, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s4)) != cudaSuccess) return e;
+  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
+  TcPlan pl{};
   plan_kernel<<<1, 1024, 0, st>>>(p, (int*)(ws + w.plan));
+  if (TC) {
+    pl = {w.pairs, (int*)(ws + w.ps), (long long*)(ws + w.us), (float*)(ws + w.pm), (float*)(ws + w.pl),
+          (float*)(ws + w.pacc), (int*)(ws + w.err)};
+    plan_tc_kernel<<<1, 1024, 0, st>>>(p, pl);
+  }
   prep<<<dim3(w.nch, p.c.heads), NT, s1, st>>>(p, w, ws);
   scan<<<(unsigned)(p.c.slots * p.c.heads + w.nch * p.hq), NT, s2, st>>>(p, w, ws);
-  att<<<dim3(w.nch, p.hq, w.nsplit), NT, s3, st>>>(p, w, ws);
+  if (TC) {
+    if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attend_tc(p, pl, ws + w.zq, st)) != cudaSuccess) return e;
+  } else {
+    att<<<dim3(w.nch, p.hq, w.nsplit), NT, s3, st>>>(p, w, ws);
+  }
   rew<<<608, NT, s4, st>>>(p, w, ws);
-  merge_kernel<T, D><<<dim3(w.nch, p.hq), NT, 0, st>>>(p, w, ws);
+  if (TC) merge_tc_kernel<D><<<dim3(w.nch, p.hq), NT, 0, st>>>(p, w, pl, ws);
+  else merge_kernel<T, D><<<dim3(w.nch, p.hq), NT, 0, st>>>(p, w, ws);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,476 @@
+// Paged serving of bf16 caches: attention of many queries over cached rows on the tensor cores (tcgen05).
+//
+// Mathematics: the queries come transported to the start of the call's new tokens (z, paged_chunk.cu), so the
+// cached rows need no transport: s = z k~^T, softmax, o = P V, with the running maximum and sum of one pass.
+// Row i G + g of a (slot, key head) is head g of new token i: the G query heads that share keys share tiles.
+//
+// Bound: the tensor cores and the exponentials (4 D flops and one exponential per query-key pair; the keys and
+// values of a tile are read once per 256 query rows, from L2 after the first).  So one persistent block per SM with
+// two 128-row query tiles: while the softmax threads of one tile work on its scores, the tensor core forms the
+// other's.  Per step of 128 keys and tile:
+//   S = Z K^T (both operands in shared memory), softmax by one thread per row, P (bf16) over the first half of S in
+//   TMEM, O += P V with P as the TMEM operand.
+// Warp 8 brings key and value tiles by TMA, one box per page piece (pages of 16 to 256 rows; the 128-byte swizzle
+// repeats every 8 rows), into a ring; warp 9 issues the MMAs and clears value rows that hold no cached token (their
+// probabilities are 0, but 0 times what lies there has to be 0).  The (slot, head, query pair, key tile) units of a
+// call are one list cut into equal runs, one per block; a run's share of a query pair leaves its softmax state in
+// a part of the workspace, merged in list order by merge kernel with the new tokens' own state.
+#include "paged_tc.h"
+#include "dev_common.cuh"
+#include "tc_common.cuh"
+#include "scan_common.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+namespace pathattn {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+using namespace tc;
+
+constexpr int KT = kTcKeys;
+constexpr int NSOFT = 256, NTHREADS = NSOFT + 64;
+constexpr int NINFO = 8;      // key tiles whose masks and biases are kept: more than the ring runs ahead
+constexpr float kTau = 8.f;   // lazy rescale threshold (log2 units)
+constexpr uint32_t COL_S = 0, COL_O = 256;  // two tiles each: S 128 columns, O D columns
+constexpr uint32_t TILE = 128 * 128;        // bytes of a 128 x 64 bf16 tile
+
+template <int D, bool FOX>
+struct __align__(1024) TcSmem {
+  static constexpr int X = D / 64;
+  static constexpr int NBUF = D == 64 ? 10 : FOX ? 4 : 5;  // what 227 KB hold
+  uint8_t z[2][X][TILE];
+  uint8_t buf[NBUF][X][TILE];
+  float aj[FOX ? NINFO : 1][FOX ? KT : 1];  // forget gate: running sums of the tile's rows
+  uint32_t okmask[NINFO];       // 16-row groups of the tile that are there
+  uint64_t info[NINFO];
+  uint64_t full[NBUF], empty[NBUF];
+  uint64_t z_full, z_empty, s_full[2], p_ready[2], o_full[2], o_read[2];
+  uint32_t tmem_base;
+};
+
+// A run's share of one query pair.
+struct Segment {
+  int b, h, pair, rows;     // rows of the pair (1..256)
+  int i0, i1;               // live key tiles
+  long long item;           // number of the (slot, head, pair)
+  SlotSpan sp;
+  LiveTiles lt;
+};
+// The segment that starts at unit u, and the first unit behind it.
+__device__ __forceinline__ Segment segment_at(const PagedArgs& p, const TcPlan& pl, long long u, long long u1, long long* next) {
+  Segment s;
+  int lo = 0, hi = p.c.slots;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.ustart[mid] <= u) lo = mid; else hi = mid;
+  }
+  s.b = lo;
+  s.sp = slot_span(p, s.b);  // (a slot with units has tokens)
+  s.lt = live_tiles(s.sp.t0, p.window, p.sinks, KT);
+  const int np = pl.pstart[s.b + 1] - pl.pstart[s.b];
+  const long long in = u - pl.ustart[s.b];
+  const int which = (int)(in / s.lt.count);  // (head, pair), head-major
+  s.h = which / np;
+  s.pair = which % np;
+  s.i0 = (int)(in % s.lt.count);
+  const long long left = u1 - u;
+  s.i1 = left < s.lt.count - s.i0 ? s.i0 + (int)left : s.lt.count;
+  s.rows = min(256, s.sp.n * p.G - s.pair * 256);
+  s.item = (long long)pl.pstart[s.b] * p.c.heads + which;
+  *next = u + (s.i1 - s.i0);
+  return s;
+}
+
+template <int D, bool FOX>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const PagedArgs p, const TcPlan pl) {
+  extern __shared__ uint8_t smem_raw[];
+  using Smem = TcSmem<D, FOX>;
+  constexpr int X = Smem::X, NBUF = Smem::NBUF;
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long units = pl.ustart[p.c.slots];
+  const long long per = (units + gridDim.x - 1) / gridDim.x;
+  const long long u0 = per * blockIdx.x, u1 = u0 + per < units ? u0 + per : units;
+  if (u0 >= u1) return;
+  if (tid == 0) {
+    for (int i = 0; i < NBUF; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < NINFO; ++i) mbar_init(&s.info[i], 1);
+    mbar_init(&s.z_full, 1);
+    mbar_init(&s.z_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s.s_full[t], 1);
+      mbar_init(&s.p_ready[t], 128);
+      mbar_init(&s.o_full[t], 1);
+      mbar_init(&s.o_read[t], 128);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(&s.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = s.tmem_base;
+  int* err = pl.err;
+
+  if (warp == 8) {
+    // ---------------- producer: Z once per segment, key and value tiles ----------------
+    const int P = p.c.page_size, RB = P < KT ? P : KT, nl = KT / RB, sub = RB / 16;
+    int n = 0, kk = 0, seg = 0;  // buffers, key tiles and segments so far
+    bool ok = true;
+    for (long long u = u0; ok && u < u1;) {
+      const Segment g = segment_at(p, pl, u, u1, &u);
+      if (seg > 0) ok = mbar_wait_lean(&s.z_empty, (seg - 1) & 1, err, 1);
+      if (!ok) break;
+      const int tiles = g.rows > 128 ? 2 : 1;
+      if (lane == 0) {
+        const int zr = (g.h * pl.pairs + pl.pstart[g.b] + g.pair) * 256;
+        mbar_arrive_expect_tx(&s.z_full, (uint32_t)tiles * X * TILE);
+        for (int t = 0; t < tiles; ++t)
+          for (int x = 0; x < X; ++x) tma_load_2d(s.z[t][x], &tm_z, 64 * x, zr + 128 * t, &s.z_full);
+      }
+      ++seg;
+      // the pair's first token sees the farthest back
+      const int p_min = g.sp.t0 + g.pair * 256 / p.G;
+      for (int i = g.i0; i < g.i1; ++i, ++kk) {
+        const int j0 = live_tile(g.lt, i) * KT;
+        const int j = j0 + 16 * lane;
+        int kp = -1, vp = -1;
+        bool here = lane < 8 && j < g.sp.t0 && (p.window <= 0 || j < p.sinks || j + 15 > p_min - p.window);
+        if (here) {
+          kp = p.c.k_table[(size_t)g.b * p.c.table_width + j / P];
+          vp = p.c.v_table[(size_t)g.b * p.c.table_width + j / P];
+          if ((unsigned)kp >= (unsigned)p.c.k_pages || (unsigned)vp >= (unsigned)p.c.v_pages) {
+            here = false;
+            paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+          }
+        }
+        const uint32_t groups = __ballot_sync(0xffffffffu, here);
+        // lane l brings piece l: the first group of it that is there names the page
+        const uint32_t mine = lane < nl ? (groups >> (lane * sub)) & ((1u << sub) - 1) : 0u;
+        const int from = lane < nl && mine ? lane * sub + __ffs(mine) - 1 : lane;
+        kp = __shfl_sync(0xffffffffu, kp, from);
+        vp = __shfl_sync(0xffffffffu, vp, from);
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, mine != 0));
+        const int in = (j0 + lane * RB) % P;
+        const int kb = n % NBUF, vb = (n + 1) % NBUF, ib = kk % NINFO;
+        if (n >= NBUF) ok = ok && mbar_wait_lean(&s.empty[kb], (n / NBUF - 1) & 1, err, 2);
+        if (!ok) break;
+        if (lane == 0) {
+          s.okmask[ib] = groups;
+          if (FOX) mbar_arrive_expect_tx(&s.info[ib], loads * RB * 4);
+          else mbar_arrive(&s.info[ib]);
+          mbar_arrive_expect_tx(&s.full[kb], loads * RB * 128 * X);
+        }
+        __syncwarp();
+        if (mine) {
+#pragma unroll
+          for (int x = 0; x < X; ++x)
+            tma_load_2d(s.buf[kb][x] + lane * RB * 128, &tm_k, 64 * x, (kp * p.c.heads + g.h) * P + in, &s.full[kb]);
+          if (FOX)
+            bulk_load(s.aj[ib] + lane * RB, p.c.a_pool + ((size_t)vp * p.c.heads + g.h) * P + in, RB * 4, &s.info[ib]);
+        }
+        if (n + 1 >= NBUF) ok = mbar_wait_lean(&s.empty[vb], ((n + 1) / NBUF - 1) & 1, err, 3);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&s.full[vb], loads * RB * 128 * X);
+        __syncwarp();
+        if (mine) {
+#pragma unroll
+          for (int x = 0; x < X; ++x)
+            tma_load_2d(s.buf[vb][x] + lane * RB * 128, &tm_v, 64 * x, (vp * p.c.heads + g.h) * P + in, &s.full[vb]);
+        }
+        n += 2;
+      }
+    }
+    // after a failure: no copy may land in shared memory once the block has gone (bounded waits)
+    if (!ok) {
+      if (seg > 0) mbar_wait_ns(&s.z_full, (seg - 1) & 1, nullptr, 0, 1000000ull);
+      for (int i = n > NBUF ? n - NBUF : 0; i < n + 2; ++i) mbar_wait_ns(&s.full[i % NBUF], (i / NBUF) & 1, nullptr, 0, 1000000ull);
+      for (int i = kk > NINFO ? kk - NINFO : 0; i <= kk; ++i) mbar_wait_ns(&s.info[i % NINFO], (i / NINFO) & 1, nullptr, 0, 1000000ull);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issuer (the whole warp walks; lane 0 issues) ----------------
+    const uint32_t idesc_s = idesc_bf16(128, KT, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
+    const uint64_t dz = sdesc_sw128(smem_u32(s.z[0][0]), 1024, 16);
+    const uint64_t dk = sdesc_sw128(smem_u32(s.buf[0][0]), 1024, 16);
+    const uint64_t dv = sdesc_sw128(smem_u32(s.buf[0][0]), 1024, TILE);
+    int n = 0, kk = 0, seg = 0;
+    bool ok = true;
+    auto issue_s = [&](int t, int buf) {
+      if (lane == 0) {
+        const uint64_t a = dz + (uint64_t)(t * X * (TILE / 16)), b = dk + (uint64_t)(buf * X * (TILE / 16));
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tb + COL_S + 128 * t, a + (uint64_t)(x * (TILE / 16) + 2 * k), b + (uint64_t)(x * (TILE / 16) + 2 * k), idesc_s,
+                   (x | k) ? 1u : 0u);
+        mma_commit(&s.s_full[t]);
+      }
+    };
+    auto issue_o = [&](int t, int buf, bool first) {
+      if (lane == 0) {
+        const uint64_t b = dv + (uint64_t)(buf * X * (TILE / 16));
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k)
+          mma_ts(tb + COL_O + D * t, tb + COL_S + 128 * t + 8 * k, b + (uint64_t)(128 * k), idesc_o, (first && k == 0) ? 0u : 1u);
+      }
+    };
+    int pr[2] = {0, 0};   // p_ready phases consumed
+    int os[2] = {0, 0};   // segments of each tile so far
+    for (long long u = u0; ok && u < u1;) {
+      const Segment g = segment_at(p, pl, u, u1, &u);
+      const int tiles = g.rows > 128 ? 2 : 1, nk = g.i1 - g.i0;
+      ok = mbar_wait_lean(&s.z_full, seg & 1, err, 4) && mbar_wait_lean(&s.full[n % NBUF], (n / NBUF) & 1, err, 5);
+      if (!ok) break;
+      tc_fence_after();
+      for (int t = 0; t < tiles; ++t) issue_s(t, n % NBUF);
+      if (lane == 0) {
+        mma_commit(&s.empty[n % NBUF]);
+        if (nk == 1) mma_commit(&s.z_empty);
+      }
+      for (int k = 0; ok && k < nk; ++k, ++kk, n += 2) {
+        const int vb = (n + 1) % NBUF, nb = (n + 2) % NBUF;
+        ok = mbar_wait_lean(&s.full[vb], ((n + 1) / NBUF) & 1, err, 6);
+        if (!ok) break;
+        const int j0 = live_tile(g.lt, g.i0 + k) * KT;
+        // (the tile's mask: written by the producer before it arrived for the key buffer, which this warp has
+        // waited for)
+        const uint32_t groups = *reinterpret_cast<volatile uint32_t*>(&s.okmask[kk % NINFO]);
+        if (groups != 0xffu || j0 + KT > g.sp.t0) {
+          for (int r = lane >> 3; r < KT; r += 4)
+            if (!(groups >> (r >> 4) & 1) || j0 + r >= g.sp.t0)
+#pragma unroll
+              for (int x = 0; x < X; ++x) *reinterpret_cast<uint4*>(s.buf[vb][x] + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        for (int t = 0; ok && t < tiles; ++t) {
+          ok = mbar_wait_lean(&s.p_ready[t], pr[t] & 1, err, 7);
+          if (ok && k == 0 && os[t] > 0) ok = mbar_wait_lean(&s.o_read[t], (os[t] - 1) & 1, err, 8);
+          if (!ok) break;
+          ++pr[t];
+          tc_fence_after();
+          issue_o(t, vb, k == 0);
+          if (t == tiles - 1 && lane == 0) mma_commit(&s.empty[vb]);
+          if (k + 1 < nk) {
+            if (t == 0) ok = mbar_wait_lean(&s.full[nb], ((n + 2) / NBUF) & 1, err, 9);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(t, nb);
+            if (t == tiles - 1 && lane == 0) {
+              mma_commit(&s.empty[nb]);
+              if (k + 2 == nk) mma_commit(&s.z_empty);
+            }
+          } else {
+            if (lane == 0) mma_commit(&s.o_full[t]);
+            ++os[t];
+          }
+        }
+      }
+      ++seg;
+    }
+  } else {
+    // ---------------- softmax: thread = row of tile warp / 4 ----------------
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t c_s = tb + lane_off + COL_S + 128 * t, c_o = tb + lane_off + COL_O + D * t;
+    int kk = 0, ns = 0, os = 0;
+    bool ok = true;
+    for (long long u = u0; ok && u < u1;) {
+      const Segment g = segment_at(p, pl, u, u1, &u);
+      const int nk = g.i1 - g.i0;
+      if (t == 1 && g.rows <= 128) {  // no second tile
+        kk += nk;
+        continue;
+      }
+      const int R = g.pair * 256 + 128 * t + r;
+      const int pos = g.sp.t0 + R / p.G;
+      // positions of this warp's tile: a tile of keys that all of them see needs no mask
+      const int p_max = g.sp.t0 + (g.pair * 256 + 128 * t + 127) / p.G;
+      float a_last = 0.f;
+      if (FOX && g.sp.t0 > 0) {
+        const long long row = pool_row(p.c, p.c.v_table, p.c.v_pages, g.b, g.h, g.sp.t0 - 1);
+        if (row >= 0) a_last = p.c.a_pool[row];
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; ok && k < nk; ++k, ++kk, ++ns) {
+        // (the scores first: with them the producer is known to be at most one phase of `info` ahead)
+        ok = mbar_wait_lean(&s.s_full[t], ns & 1, err, 10) && mbar_wait_lean(&s.info[kk % NINFO], (kk / NINFO) & 1, err, 11);
+        if (!ok) break;
+        tc_fence_after();
+        const int j0 = live_tile(g.lt, g.i0 + k) * KT;
+        const uint32_t groups = s.okmask[kk % NINFO];
+        const bool mask = groups != 0xffu || j0 + KT > g.sp.t0 ||
+                          (p.window > 0 && j0 + KT > p.sinks && j0 <= p_max - p.window);
+        const bool logd = FOX || mask;  // scores in the log2 domain with biases and hidden ones -inf; else raw
+        const float f = logd ? 1.f : p.scl;
+        // 32 scores of the row; read twice (maximum, probabilities): TMEM has the room, the registers have not
+        auto scores = [&](int q, uint32_t (&x)[32]) {
+          if (FOX) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              x[j] = __float_as_uint(fmaf(a_last - s.aj[kk % NINFO][32 * q + j], kLog2e, __uint_as_float(x[j]) * p.scl));
+          } else if (mask) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * p.scl);
+          }
+          if (mask) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int jj = 32 * q + j;
+              if (!(groups >> (jj >> 4) & 1) || j0 + jj >= g.sp.t0 || !sees(p.window, p.sinks, pos, j0 + jj))
+                x[j] = 0xff800000u;
+            }
+          }
+        };
+        float e0, e1;
+        const bool low = !logd && p.scl < 0.f;
+        e0 = e1 = low ? INFINITY : -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          uint32_t x[32], y[32];
+          tmem_ld32(c_s + 32 * q, x);
+          tmem_ld32(c_s + 32 * q + 32, y);
+          tmem_ld_wait();
+          scores(q, x);
+          scores(q + 1, y);
+          if (low) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              e0 = min3(e0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+              e1 = min3(e1, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              e0 = max3(e0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+              e1 = max3(e1, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+            }
+          }
+        }
+        const float mx = (low ? fminf(e0, e1) : fmaxf(e0, e1)) * f;
+        const bool up = mx > m + kTau;
+        if (__any_sync(0xffffffffu, up)) {
+          const float mn = up ? fmaxf(m, mx) : m;
+          const float corr = up ? fast_exp2(m - mn) : 1.f;  // (m = -inf at first: 0)
+          m = mn;
+          l *= corr;
+          if (k > 0) {  // (S of this step was issued behind the last P V, which has completed with it)
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t ob[32];
+              tmem_ld32(c_o + 32 * q, ob);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) ob[j] = __float_as_uint(__uint_as_float(ob[j]) * corr);
+              tmem_st32(c_o + 32 * q, ob);
+            }
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        uint64_t acc[2] = {0ull, 0ull};
+        const uint64_t nm = f2(-mu, -mu), sc = f2(f, f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t x[32], pk[16];
+          tmem_ld32(c_s + 32 * q, x);
+          tmem_ld_wait();
+          scores(q, x);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float a0, a1;
+            f2_split(f2_fma(f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc, nm), a0, a1);
+            const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+            acc[j & 1] = f2_add(acc[j & 1], f2(p0, p1));
+            pk[j] = pack_bf16(p0, p1);
+          }
+          tmem_st16(c_s + 16 * q, pk);  // (over scores that this row has read)
+        }
+        float s0, s1, s2, s3;
+        f2_split(acc[0], s0, s1);
+        f2_split(acc[1], s2, s3);
+        l += (s0 + s1) + (s2 + s3);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&s.p_ready[t]);
+      }
+      if (!ok) break;
+      ok = mbar_wait_lean(&s.o_full[t], os & 1, err, 12);
+      ++os;
+      if (!ok) break;
+      tc_fence_after();
+      const size_t row = (size_t)(g.item + blockIdx.x) * 256 + 128 * t + r;
+      float* dst = pl.acc + row * D;
+      const bool real = 128 * t + r < g.rows;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t ob[32];
+        tmem_ld32(c_o + 32 * q, ob);
+        tmem_ld_wait();
+        if (real)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<uint4*>(dst + 32 * q + j) = make_uint4(ob[j], ob[j + 1], ob[j + 2], ob[j + 3]);
+      }
+      if (real) {
+        pl.m[row] = m;
+        pl.l[row] = l;
+      }
+      tc_fence_before();
+      mbar_arrive(&s.o_read[t]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
+}
+
+// 2-D map over [rows][D] bf16 with 128-byte swizzled boxes of box_rows x 64.
+bool make_map(CUtensorMap* m, const void* base, int D, uint64_t rows, uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D, rows};
+  cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool FOX>
+cudaError_t attend_t(const PagedArgs& p, const TcPlan& pl, const void* z, cudaStream_t st) {
+  CUtensorMap mz, mk, mv;
+  const int P = p.c.page_size, RB = P < KT ? P : KT;
+  if (!make_map(&mz, z, D, (uint64_t)p.c.heads * pl.pairs * 256, 128) ||
+      !make_map(&mk, p.c.k_pool, D, (uint64_t)p.c.k_pages * p.c.heads * P, RB) ||
+      !make_map(&mv, p.c.v_pool, D, (uint64_t)p.c.v_pages * p.c.heads * P, RB))
+    return cudaErrorInvalidValue;
+  auto kern = attend_tc_kernel<D, FOX>;
+  const size_t smem = sizeof(TcSmem<D, FOX>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<kTcBlocks, NTHREADS, smem, st>>>(mz, mk, mv, p, pl);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tc(const PagedArgs& p, const TcPlan& pl, const void* z, cudaStream_t st) {
+  const bool fox = p.log_f != nullptr;
+  if (p.c.head_dim == kHeadDim) return fox ? attend_t<kHeadDim, true>(p, pl, z, st) : attend_t<kHeadDim, false>(p, pl, z, st);
+  return fox ? attend_t<kHeadDimWide, true>(p, pl, z, st) : attend_t<kHeadDimWide, false>(p, pl, z, st);
+}
+
+}  // namespace pathattn
