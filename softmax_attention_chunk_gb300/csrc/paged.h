@@ -20,7 +20,8 @@ struct PagedArgs {
   const void *q, *k, *v, *w;
   const float *beta, *log_f;
   void* o;
-  int min_new;          // the chunk kernels leave out slots with fewer new tokens
+  int min_new;          // prompt chunks: slots with fewer new tokens are left to the streaming kernels
+  int skip;             // prompt chunks: new tokens of each slot that earlier passes have done
 };
 
 #ifdef __CUDACC__
@@ -112,6 +113,10 @@ cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st);
 // Slots with one new token, bf16.
 size_t paged_token_ws_bytes(const PagedArgs& p);
 cudaError_t launch_paged_token(const PagedArgs& p, char* ws, cudaStream_t st);
+
+// Prompt chunks, bf16.
+size_t paged_new_ws_bytes(const PagedArgs& p);
+cudaError_t launch_paged_new(const PagedArgs& p, char* ws, cudaStream_t st);
 
 size_t pages_ws_bytes(const path_paged_cache_t& c);
 cudaError_t launch_pages_reserve(const path_paged_cache_t& c, const int* n_new, char* ws, cudaStream_t st);

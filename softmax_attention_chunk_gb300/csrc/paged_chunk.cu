@@ -1,5 +1,4 @@
-// Paged serving: attention of a chunk of new tokens over a paged cache, CUDA-core kernels (fp32 caches;
-// products of bf16 caches on TF32 warp MMAs).
+// Paged serving: attention of new tokens over a paged cache, CUDA-core kernels in fp32 arithmetic (fp32 caches).
 //
 // Mathematics (one sequence, one key head; t0 cached rows, n new tokens with rows of W and beta; the UT
 // representation of the PaTH reading notes, cc.laoqi.cc/papers/2505.16381, §2.6-§2.8).  The new
@@ -13,11 +12,9 @@
 //
 // Six launches: plan (lengths, chunk list), chunk preparation, then one of {query scan, key walk} per
 // block, cached attention split over key ranges, cached rewrite, and the merge of the splits.
-#include "paged_tc.h"
+#include "paged.h"
 #include "dev_common.cuh"
 #include "smem_mm.cuh"
-
-#include <type_traits>
 
 namespace pathattn {
 namespace {
@@ -36,11 +33,6 @@ struct ChunkWs {
   size_t z, qb;        // Q<-, then z [nch][hq][B][D]; row biases sum of log f since t0 [nch][hq][B]
   size_t m, l, acc;    // softmax states [nsplit][nch][hq][B](, [D])
   size_t mm;           // M [slots][H][D][D]
-  // bf16: the cached attention runs on the tensor cores
-  int pairs;           // query pairs of a head
-  size_t zq;           // z [H][pairs][256][D] bf16, row i G + g of a slot
-  size_t ps, us;       // first query pair (int) and first unit (long long) of each slot
-  size_t pm, pl, pacc, err;
   size_t total;
 };
 ChunkWs chunk_ws(const PagedArgs& p) {
@@ -52,8 +44,6 @@ ChunkWs chunk_ws(const PagedArgs& p) {
   const long long ctas = (long long)w.nch * p.hq;
   w.nsplit = ctas >= 1216 ? 1 : (int)((1216 + ctas - 1) / ctas);
   if (w.nsplit > 64) w.nsplit = 64;
-  const bool tc = p.c.cache_dtype == PATH_BF16;
-  if (tc) w.nsplit = 1;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, 256); return o; };
   w.plan = take((size_t)2 * (p.c.slots + 1) * 4);
@@ -67,27 +57,8 @@ ChunkWs chunk_ws(const PagedArgs& p) {
   w.l = take((size_t)w.nsplit * w.nch * hq * B * 4);
   w.acc = take((size_t)w.nsplit * w.nch * hq * B * D * 4);
   w.mm = take((size_t)p.c.slots * H * D * D * 4);
-  if (tc) {
-    const long long live = p.c.slots < p.total ? p.c.slots : p.total;
-    w.pairs = (int)(((long long)p.total * p.G + (kTcPair - 1) * live) / kTcPair);
-    if (w.pairs < 1) w.pairs = 1;
-    w.zq = take((size_t)H * w.pairs * kTcPair * D * 2);
-    w.ps = take((size_t)(p.c.slots + 1) * 4);
-    w.us = take((size_t)(p.c.slots + 1) * 8);
-    const size_t parts = (size_t)H * w.pairs + kTcBlocks;
-    w.pm = take(parts * kTcPair * 4);
-    w.pl = take(parts * kTcPair * 4);
-    w.pacc = take(parts * kTcPair * D * 4);
-    w.err = take(4);
-  }
   w.total = off;
   return w;
-}
-
-__device__ __forceinline__ SlotSpan chunk_span(const PagedArgs& p, int b) {
-  SlotSpan s = slot_span(p, b);
-  if (s.n < p.min_new) s.n = 0;
-  return s;
 }
 
 // First chunk and first live tile of every slot (exclusive prefix sums; entry `slots` holds the totals).
@@ -103,7 +74,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict
     const int b = base + tid;
     int nc = 0, nt = 0;
     if (b < p.c.slots) {
-      const SlotSpan s = chunk_span(p, b);
+      const SlotSpan s = slot_span(p, b);
       if (s.code) paged_error(p.c.status, s.code);
       nc = (s.n + B - 1) / B;
       nt = s.n ? live_tiles(s.t0, p.window, p.sinks, KT).count : 0;
@@ -126,39 +97,6 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict
   if (tid == 0) { cstart[p.c.slots] = carry[0]; tstart[p.c.slots] = carry[1]; }
 }
 
-// Query pairs and (head, pair, key tile) units of every slot (tensor-core attention); clears the wait code.
-__global__ void __launch_bounds__(1024) plan_tc_kernel(PagedArgs p, TcPlan pl) {
-  __shared__ long long wsum[2][32], carry[2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < 2) carry[tid] = 0;
-  if (tid == 0) *pl.err = 0;
-  __syncthreads();
-  for (int base = 0; base < p.c.slots; base += 1024) {
-    const int b = base + tid;
-    long long np = 0, nu = 0;
-    if (b < p.c.slots) {
-      const SlotSpan s = chunk_span(p, b);
-      np = ((long long)s.n * p.G + kTcPair - 1) / kTcPair;
-      nu = s.n ? np * p.c.heads * live_tiles(s.t0, p.window, p.sinks, kTcKeys).count : 0;
-    }
-    long long ip = np, iu = nu;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long a = __shfl_up_sync(0xffffffffu, ip, o), e = __shfl_up_sync(0xffffffffu, iu, o);
-      if (lane >= o) { ip += a; iu += e; }
-    }
-    if (lane == 31) { wsum[0][warp] = ip; wsum[1][warp] = iu; }
-    __syncthreads();
-    long long op = carry[0], ou = carry[1];
-    for (int w = 0; w < warp; ++w) { op += wsum[0][w]; ou += wsum[1][w]; }
-    if (b < p.c.slots) { pl.pstart[b] = (int)(op + ip - np); pl.ustart[b] = ou + iu - nu; }
-    __syncthreads();
-    if (tid == 1023) { carry[0] = op + ip; carry[1] = ou + iu; }
-    __syncthreads();
-  }
-  if (tid == 0) { pl.pstart[p.c.slots] = (int)carry[0]; pl.ustart[p.c.slots] = carry[1]; }
-}
-
 // The slot that owns entry x of a prefix array with x < start[slots].
 __device__ __forceinline__ int owner(const int* start, int slots, int x) {
   int lo = 0, hi = slots;
@@ -179,12 +117,11 @@ struct PrepSmem {
 };
 
 // One block per (chunk, key head).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
   extern __shared__ float sm[];
   using S = PrepSmem<D>;
   constexpr int DS = S::DS, BS = S::BS;
-  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
   float *sW = sm + S::kW, *sK = sm + S::kK, *sQ = sm + S::kQ, *sV = sm + S::kV, *sY = sm + S::kY;
   float *sU = sm + S::kU, *sX = sm + S::kX, *sG = sm + S::kG, *sN = sm + S::kN, *sM1 = sm + S::kM1;
   float *sA = sm + S::kA, *sS = sm + S::kS, *sBeta = sm + S::kBeta, *sLf = sm + S::kLf;
@@ -192,17 +129,17 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
   const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, H = p.c.heads;
   if (c >= cstart[p.c.slots]) return;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = chunk_span(p, b);
+  const SlotSpan sp = slot_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
-  const T *k = (const T*)p.k, *v = (const T*)p.v, *wv = (const T*)p.w, *q = (const T*)p.q;
+  const float *k = (const float*)p.k, *v = (const float*)p.v, *wv = (const float*)p.w, *q = (const float*)p.q;
   const size_t tok0 = (size_t)sp.q0 + r0;
   for (int e = tid; e < B * D; e += NT) {
     const int r = e / D, x = e % D;
     const bool ok = r < rows;
     const size_t at = ((tok0 + r) * H + h) * D + x;
-    sW[r * DS + x] = ok ? to_f(wv[at]) : 0.f;
-    sK[r * DS + x] = ok ? to_f(k[at]) : 0.f;
-    sV[r * DS + x] = ok ? to_f(v[at]) : 0.f;
+    sW[r * DS + x] = ok ? (wv[at]) : 0.f;
+    sK[r * DS + x] = ok ? (k[at]) : 0.f;
+    sV[r * DS + x] = ok ? (v[at]) : 0.f;
   }
   if (tid < B) {
     const bool ok = tid < rows;
@@ -216,8 +153,8 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
     sLf[tid] = a;
   }
   __syncthreads();
-  smem_mm<B, B, D, false, true, TC>(sW, DS, sW, DS, [&](int i, int j, float x) { sG[i * BS + j] = j < i ? x : 0.f; });
-  smem_mm<B, B, D, false, true, TC>(sW, DS, sK, DS, [&](int i, int j, float x) { sN[i * BS + j] = j < i ? x : 0.f; });
+  smem_mm<B, B, D, false, true, false>(sW, DS, sW, DS, [&](int i, int j, float x) { sG[i * BS + j] = j < i ? x : 0.f; });
+  smem_mm<B, B, D, false, true, false>(sW, DS, sK, DS, [&](int i, int j, float x) { sN[i * BS + j] = j < i ? x : 0.f; });
   __syncthreads();
   // U by forward substitution, one column per lane: u_i = beta_i (e_i - sum_{m<i} G_im u_m)
   if (tid < 32) {
@@ -237,14 +174,14 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
     for (int i = 0; i < 32; ++i) sU[i * BS + tid] = u[i];
   }
   __syncthreads();
-  smem_mm<B, B, B, false, false, TC>(sU, BS, sN, BS, [&](int i, int j, float x) { sX[i * BS + j] = x; });
-  smem_mm<B, D, B, true, false, TC>(sU, BS, sW, DS, [&](int m, int n, float x) { sY[m * DS + n] = x; });
+  smem_mm<B, B, B, false, false, false>(sU, BS, sN, BS, [&](int i, int j, float x) { sX[i * BS + j] = x; });
+  smem_mm<B, D, B, true, false, false>(sU, BS, sW, DS, [&](int m, int n, float x) { sY[m * DS + n] = x; });
   __syncthreads();
   {
     float* kr = (float*)(ws + w.kr) + ((size_t)c * H + h) * B * D;
     float* f = (float*)(ws + w.f) + ((size_t)c * H + h) * D * D;
-    smem_mm<B, D, B, true, false, TC>(sX, BS, sW, DS, [&](int j, int n, float x) { kr[j * D + n] = sK[j * DS + n] - x; });
-    smem_mm<D, D, B, true, false, TC>(sW, DS, sY, DS, [&](int n, int x, float y) { f[n * D + x] = (n == x ? 1.f : 0.f) - y; });
+    smem_mm<B, D, B, true, false, false>(sX, BS, sW, DS, [&](int j, int n, float x) { kr[j * D + n] = sK[j * DS + n] - x; });
+    smem_mm<D, D, B, true, false, false>(sW, DS, sY, DS, [&](int n, int x, float y) { f[n * D + x] = (n == x ? 1.f : 0.f) - y; });
     if (p.log_f && tid < B) ((float*)(ws + w.fa))[((size_t)c * H + h) * B + tid] = sLf[tid];
     if (p.log_f && tid == 0) ((float*)(ws + w.ft))[(size_t)c * H + h] = sLf[B - 1];
   }
@@ -253,18 +190,18 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
     __syncthreads();
     for (int e = tid; e < B * D; e += NT) {
       const int r = e / D, x = e % D;
-      sQ[r * DS + x] = r < rows ? to_f(q[((tok0 + r) * p.hq + qh) * D + x]) : 0.f;
+      sQ[r * DS + x] = r < rows ? (q[((tok0 + r) * p.hq + qh) * D + x]) : 0.f;
     }
     __syncthreads();
-    smem_mm<B, B, D, false, true, TC>(sQ, DS, sW, DS, [&](int i, int j, float x) { sM1[i * BS + j] = j <= i ? x : 0.f; });
-    smem_mm<B, B, D, false, true, TC>(sQ, DS, sK, DS, [&](int i, int j, float x) { sS[i * BS + j] = x; });
+    smem_mm<B, B, D, false, true, false>(sQ, DS, sW, DS, [&](int i, int j, float x) { sM1[i * BS + j] = j <= i ? x : 0.f; });
+    smem_mm<B, B, D, false, true, false>(sQ, DS, sK, DS, [&](int i, int j, float x) { sS[i * BS + j] = x; });
     __syncthreads();
-    smem_mm<B, B, B, false, false, TC>(sM1, BS, sU, BS, [&](int i, int j, float x) { sA[i * BS + j] = x; });
-    smem_mm<B, B, B, false, false, TC>(sM1, BS, sX, BS, [&](int i, int j, float x) { sS[i * BS + j] -= x; });
+    smem_mm<B, B, B, false, false, false>(sM1, BS, sU, BS, [&](int i, int j, float x) { sA[i * BS + j] = x; });
+    smem_mm<B, B, B, false, false, false>(sM1, BS, sX, BS, [&](int i, int j, float x) { sS[i * BS + j] -= x; });
     __syncthreads();
     const size_t row = ((size_t)c * p.hq + qh) * B;
     float* z = (float*)(ws + w.z) + row * D;
-    smem_mm<B, D, B, false, false, TC>(sA, BS, sW, DS, [&](int i, int n, float x) { z[i * D + n] = sQ[i * DS + n] - x; });
+    smem_mm<B, D, B, false, false, false>(sA, BS, sW, DS, [&](int i, int n, float x) { z[i * D + n] = sQ[i * DS + n] - x; });
     // softmax of the diagonal chunk: 8 threads per row (log2 domain)
     const int r = tid >> 3, sub = tid & 7;
     float mx = -INFINITY;
@@ -290,7 +227,7 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
     }
     __syncthreads();
     float* acc = (float*)(ws + w.acc) + row * D;
-    smem_mm<B, D, B, false, false, TC>(sS, BS, sV, DS, [&](int i, int n, float x) { acc[i * D + n] = x; });
+    smem_mm<B, D, B, false, false, false>(sS, BS, sV, DS, [&](int i, int n, float x) { acc[i * D + n] = x; });
   }
 }
 
@@ -330,17 +267,16 @@ __device__ __forceinline__ void softmax_step(float* sP, int ps, int nk, float* s
 }
 
 // Query scan over the earlier new chunks of the slot: one block per (chunk, query head).
-template <typename T, int D>
+template <int D>
 __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float* sm, int c, int qh) {
   using S = ScanSmem<D>;
   constexpr int DS = S::DS, KS = S::KS;
-  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
   float *sZ = sm + S::kZ, *sZn = sm + S::kZn, *sK = sm + S::kK, *sV = sm + S::kV, *sAcc = sm + S::kAcc;
   float *sP = sm + S::kP, *sM = sm + S::kM, *sF = sm + S::attend;
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads, h = qh / p.G;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = chunk_span(p, b);
+  const SlotSpan sp = slot_span(p, b);
   const int lc = c - cstart[b], rows = min(B, sp.n - lc * B);
   const size_t row = ((size_t)c * p.hq + qh) * B;
   float* z = (float*)(ws + w.z) + row * D;
@@ -348,14 +284,8 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   float *gm = (float*)(ws + w.m) + row, *gl = (float*)(ws + w.l) + row;
   const float* fa = (const float*)(ws + w.fa);
   const float* ft = (const float*)(ws + w.ft);
-  __nv_bfloat16* zq = nullptr;  // row 0 of the chunk, bf16: head g of token i in row i G + g
-  if (TC)
-    zq = (__nv_bfloat16*)(ws + w.zq) +
-         (((size_t)h * w.pairs + ((const int*)(ws + w.ps))[b]) * kTcPair + (size_t)lc * B * p.G + qh % p.G) * D;
   if (lc == 0) {  // already at the start of the new tokens
     if (p.log_f && tid < B) ((float*)(ws + w.qb))[row + tid] = fa[((size_t)c * H + h) * B + tid];
-    if (TC)
-      for (int e = tid; e < rows * D; e += NT) zq[(size_t)(e / D) * p.G * D + e % D] = __float2bfloat16_rn(z[e]);
     return;
   }
   for (int e = tid; e < B * D; e += NT) {
@@ -367,7 +297,7 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     sM[B + tid] = gl[tid];
     sM[2 * B + tid] = p.log_f ? fa[((size_t)c * H + h) * B + tid] : 0.f;  // row bias so far
   }
-  const T* v = (const T*)p.v;
+  const float* v = (const float*)p.v;
   for (int c2 = lc - 1; c2 >= 0; --c2) {
     const size_t cc = (size_t)(c - lc + c2) * H + h;
     const float* kr = (const float*)(ws + w.kr) + cc * B * D;
@@ -377,11 +307,11 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     for (int e = tid; e < B * D; e += NT) {
       const int r = e / D, x = e % D;
       sK[r * DS + x] = kr[e];
-      sV[r * DS + x] = to_f(v[((tok + r) * H + h) * D + x]);  // an earlier chunk is full
+      sV[r * DS + x] = (v[((tok + r) * H + h) * D + x]);  // an earlier chunk is full
     }
     for (int e = tid; e < D * D; e += NT) sF[(e / D) * DS + e % D] = f[e];
     __syncthreads();
-    smem_mm<B, B, D, false, true, TC>(sZ, DS, sK, DS, [&](int i, int j, float x) {
+    smem_mm<B, B, D, false, true, false>(sZ, DS, sK, DS, [&](int i, int j, float x) {
       float s = -INFINITY;
       const int jn = c2 * B + j, in = lc * B + i;
       if (i < rows && sees(p.window, p.sinks, sp.t0 + in, sp.t0 + jn)) {
@@ -390,17 +320,16 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
       }
       sP[i * KS + j] = s;
     });
-    smem_mm<B, D, D, false, true, TC>(sZ, DS, sF, DS, [&](int i, int n, float x) { sZn[i * DS + n] = x; });
+    smem_mm<B, D, D, false, true, false>(sZ, DS, sF, DS, [&](int i, int n, float x) { sZn[i * DS + n] = x; });
     __syncthreads();
     softmax_step<D>(sP, KS, B, sM, sAcc, DS);
-    smem_mm<B, D, B, false, false, TC>(sP, KS, sV, DS, [&](int i, int n, float x) { sAcc[i * DS + n] += x; });
+    smem_mm<B, D, B, false, false, false>(sP, KS, sV, DS, [&](int i, int n, float x) { sAcc[i * DS + n] += x; });
     if (p.log_f && tid < B) sM[2 * B + tid] += ft[cc];
     float* t = sZ; sZ = sZn; sZn = t;
   }
   __syncthreads();
   for (int e = tid; e < B * D; e += NT) {
-    if (!TC) z[e] = sZ[(e / D) * DS + e % D];
-    else if (e / D < rows) zq[(size_t)(e / D) * p.G * D + e % D] = __float2bfloat16_rn(sZ[(e / D) * DS + e % D]);
+    z[e] = sZ[(e / D) * DS + e % D];
     acc[e] = sAcc[(e / D) * DS + e % D];
   }
   if (tid < B) {
@@ -411,19 +340,18 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
 }
 
 // Key walk of one (slot, key head): the new rows to the end of the call and into the pages, M.
-template <typename T, int D>
+template <int D>
 __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float* sm, int b, int h) {
   constexpr int DS = D + 4;
-  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
   float *sR = sm, *sF = sR + D * DS, *sK = sF + D * DS;
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads;
-  const SlotSpan sp = chunk_span(p, b);
+  const SlotSpan sp = slot_span(p, b);
   if (sp.n == 0) return;
   const int nc = cstart[b + 1] - cstart[b];
-  T* kp = (T*)p.c.k_pool;
-  T* vp = (T*)p.c.v_pool;
-  const T* v = (const T*)p.v;
+  float* kp = (float*)p.c.k_pool;
+  float* vp = (float*)p.c.v_pool;
+  const float* v = (const float*)p.v;
   // values and running sums
   for (int r = tid >> 4; r < sp.n; r += NT / 16) {
     const long long at = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r);
@@ -453,15 +381,15 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     for (int e = tid; e < B * D; e += NT) sK[(e / D) * DS + e % D] = kr[e];
     for (int e = tid; e < D * D; e += NT) sF[(e / D) * DS + e % D] = f[e];
     __syncthreads();
-    smem_mm<B, D, D, false, false, TC>(sK, DS, sR, DS, [&](int i, int n, float x) {
+    smem_mm<B, D, D, false, false, false>(sK, DS, sR, DS, [&](int i, int n, float x) {
       if (i < rows) {
         const long long at = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0 + lc * B + i);
-        if (at >= 0) kp[at * D + n] = from_f<T>(lc == nc - 1 ? sK[i * DS + n] : x);
+        if (at >= 0) kp[at * D + n] = (lc == nc - 1 ? sK[i * DS + n] : x);
         else paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
       }
     });
     // R <- F_c R, by way of M's place in global memory until every thread has read R
-    smem_mm<D, D, D, false, false, TC>(sF, DS, sR, DS, [&](int i, int n, float x) { mm[i * D + n] = x; });
+    smem_mm<D, D, D, false, false, false>(sF, DS, sR, DS, [&](int i, int n, float x) { mm[i * D + n] = x; });
     __syncthreads();
     for (int e = tid; e < D * D; e += NT) sR[(e / D) * DS + e % D] = mm[e];
   }
@@ -475,33 +403,32 @@ constexpr size_t scan_walk_smem() {
 }
 
 // Blocks [0, slots * H) walk keys, the others scan queries.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
   extern __shared__ float sm[];
   const int nw = p.c.slots * p.c.heads;
   if ((int)blockIdx.x < nw) {
-    walk_block<T, D>(p, w, ws, sm, blockIdx.x / p.c.heads, blockIdx.x % p.c.heads);
+    walk_block<D>(p, w, ws, sm, blockIdx.x / p.c.heads, blockIdx.x % p.c.heads);
     return;
   }
   const int x = blockIdx.x - nw, c = x / p.hq;
   if (c >= ((const int*)(ws + w.plan))[p.c.slots]) return;
-  scan_block<T, D>(p, w, ws, sm, c, x % p.hq);
+  scan_block<D>(p, w, ws, sm, c, x % p.hq);
 }
 
 // Cached attention: one block per (chunk, query head, key range).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
   extern __shared__ float sm[];
   using S = ScanSmem<D>;
   constexpr int DS = S::DS, KS = S::KS;
-  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
   float *sZ = sm + S::kZ, *sK = sm + S::kK, *sV = sm + S::kV, *sAcc = sm + S::kAcc, *sP = sm + S::kP, *sM = sm + S::kM;
   float* sB = sm + S::kBias;  // key biases a_last - a_j; hidden rows -inf
   const int* cstart = (const int*)(ws + w.plan);
   const int c = blockIdx.x, qh = blockIdx.y, split = blockIdx.z, tid = threadIdx.x;
   if (c >= cstart[p.c.slots]) return;
   const int h = qh / p.G, b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = chunk_span(p, b);
+  const SlotSpan sp = slot_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
   const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, KT);
   const int per = (lt.count + w.nsplit - 1) / w.nsplit;
@@ -533,8 +460,8 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
     const long long last = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1);
     if (last >= 0) a_last = p.c.a_pool[last];
   }
-  const T* kp = (const T*)p.c.k_pool;
-  const T* vp = (const T*)p.c.v_pool;
+  const float* kp = (const float*)p.c.k_pool;
+  const float* vp = (const float*)p.c.v_pool;
   for (int i = i0; i < i1; ++i) {
     const int j0 = live_tile(lt, i) * KT;
     __syncthreads();
@@ -552,13 +479,13 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
         }
       }
       for (int x = tid & 7; x < D; x += 8) {
-        sK[r * DS + x] = any ? to_f(kp[ka * D + x]) : 0.f;
-        sV[r * DS + x] = any ? to_f(vp[va * D + x]) : 0.f;
+        sK[r * DS + x] = any ? (kp[ka * D + x]) : 0.f;
+        sV[r * DS + x] = any ? (vp[va * D + x]) : 0.f;
       }
       if ((tid & 7) == 0) sB[r] = any ? (p.log_f ? a_last - p.c.a_pool[va] : 0.f) : -INFINITY;
     }
     __syncthreads();
-    smem_mm<B, KT, D, false, true, TC>(sZ, DS, sK, DS, [&](int r, int j, float x) {
+    smem_mm<B, KT, D, false, true, false>(sZ, DS, sK, DS, [&](int r, int j, float x) {
       float s = -INFINITY;
       if (r < rows && sB[j] != -INFINITY && sees(p.window, p.sinks, sp.t0 + r0 + r, j0 + j))
         s = x * p.scl + (sB[j] + sM[2 * B + r]) * kLog2e;
@@ -566,7 +493,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
     });
     __syncthreads();
     softmax_step<D>(sP, KS, KT, sM, sAcc, DS);
-    smem_mm<B, D, KT, false, false, TC>(sP, KS, sV, DS, [&](int r, int n, float x) { sAcc[r * DS + n] += x; });
+    smem_mm<B, D, KT, false, false, false>(sP, KS, sV, DS, [&](int r, int n, float x) { sAcc[r * DS + n] += x; });
   }
   __syncthreads();
   for (int e = tid; e < B * D; e += NT) acc[e] = sAcc[(e / D) * DS + e % D];
@@ -577,17 +504,16 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
 }
 
 // k <- k M for the cached rows that a later token sees: blocks take runs of (live tile, head).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, const char* __restrict__ ws) {
   extern __shared__ float sm[];
   constexpr int DS = D + 4;
-  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
   float *sMm = sm, *sK = sMm + D * DS;
   const int* tstart = (const int*)(ws + w.plan) + p.c.slots + 1;
   const int tid = threadIdx.x, H = p.c.heads;
   const long long units = (long long)tstart[p.c.slots] * H;
   const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-  T* kp = (T*)p.c.k_pool;
+  float* kp = (float*)p.c.k_pool;
   int have = -1;  // (slot, head) whose M is in shared memory
   for (long long u = u0; u < u1; ++u) {
     // units of a slot: head-major, so that a block keeps its M
@@ -595,7 +521,7 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
     const int nt = tstart[b + 1] - tstart[b];
     const long long in = u - (long long)tstart[b] * H;
     const int h = (int)(in / nt), i = (int)(in % nt);
-    const SlotSpan sp = chunk_span(p, b);
+    const SlotSpan sp = slot_span(p, b);
     const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, KT);
     const int j0 = live_tile(lt, i) * KT;
     __syncthreads();
@@ -607,26 +533,26 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
     auto keep = [&](int j) { return j < sp.t0 && sees(p.window, p.sinks, sp.t0 + sp.n, j); };
     for (int r = tid >> 3; r < KT; r += NT / 8) {
       const long long at = keep(j0 + r) ? pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j0 + r) : -1;
-      for (int x = tid & 7; x < D; x += 8) sK[r * DS + x] = at >= 0 ? to_f(kp[at * D + x]) : 0.f;
+      for (int x = tid & 7; x < D; x += 8) sK[r * DS + x] = at >= 0 ? (kp[at * D + x]) : 0.f;
     }
     __syncthreads();
-    smem_mm<KT, D, D, false, false, TC>(sK, DS, sMm, DS, [&](int r, int n, float x) {
+    smem_mm<KT, D, D, false, false, false>(sK, DS, sMm, DS, [&](int r, int n, float x) {
       if (keep(j0 + r)) {
         const long long at = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j0 + r);
-        if (at >= 0) kp[at * D + n] = from_f<T>(x);
+        if (at >= 0) kp[at * D + n] = (x);
       }
     });
   }
 }
 
 // Merge of the key ranges: one warp per (row, query head).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const char* __restrict__ ws) {
   const int* cstart = (const int*)(ws + w.plan);
   const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (c >= cstart[p.c.slots]) return;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = chunk_span(p, b);
+  const SlotSpan sp = slot_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
   const float *gm = (const float*)(ws + w.m), *gl = (const float*)(ws + w.l), *ga = (const float*)(ws + w.acc);
   const size_t stride = (size_t)w.nch * p.hq * B;
@@ -645,92 +571,33 @@ __global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) a[x] += ga[(s * stride + row) * D + x * 32 + lane] * f;
     }
-    T* o = (T*)p.o + (((size_t)sp.q0 + r0 + r) * p.hq + qh) * D;
+    float* o = (float*)p.o + (((size_t)sp.q0 + r0 + r) * p.hq + qh) * D;
     const float inv = 1.f / l;
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) o[x * 32 + lane] = from_f<T>(a[x] * inv);
+    for (int x = 0; x < D / 32; ++x) o[x * 32 + lane] = (a[x] * inv);
   }
 }
 
-// Merge of the tensor-core parts with the new tokens' own state: one warp per (row, query head), parts in list
-// order.  Cached scores lack the row's own bias (sum of log f since t0): it moves their maximum.
 template <int D>
-__global__ void __launch_bounds__(NT) merge_tc_kernel(PagedArgs p, ChunkWs w, TcPlan pl, const char* __restrict__ ws) {
-  const int* cstart = (const int*)(ws + w.plan);
-  const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (c == 0 && qh == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
-  if (c >= cstart[p.c.slots]) return;
-  const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = chunk_span(p, b);
-  const int lc = c - cstart[b], rows = min(B, sp.n - lc * B), h = qh / p.G, g = qh % p.G;
-  const int kt = live_tiles(sp.t0, p.window, p.sinks, kTcKeys).count;
-  const int np = pl.pstart[b + 1] - pl.pstart[b];
-  const long long units = pl.ustart[p.c.slots], per = (units + kTcBlocks - 1) / kTcBlocks;
-  for (int r = warp; r < rows; r += NT / 32) {
-    const size_t row = ((size_t)c * p.hq + qh) * B + r;
-    const int R = (lc * B + r) * p.G + g, pair = R / kTcPair;
-    const float m0 = ((const float*)(ws + w.m))[row], bias = p.log_f ? ((const float*)(ws + w.qb))[row] * kLog2e : 0.f;
-    float M = m0;
-    long long first = 0, last = -1;
-    const long long which = (long long)h * np + pair, item = (long long)pl.pstart[b] * p.c.heads + which;
-    if (kt > 0) {
-      const long long us = pl.ustart[b] + which * kt;
-      first = us / per;
-      last = (us + kt - 1) / per;
-    }
-    auto at = [&](long long x) { return (size_t)(item + x) * kTcPair + R % kTcPair; };
-    for (long long x = first; x <= last; ++x) M = fmaxf(M, pl.m[at(x)] + bias);
-    float f = fast_exp2(m0 - M);
-    float l = ((const float*)(ws + w.l))[row] * f, a[D / 32];
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x) a[x] = ((const float*)(ws + w.acc))[row * D + x * 32 + lane] * f;
-    for (long long x = first; x <= last; ++x) {
-      const float ms = pl.m[at(x)];
-      if (ms == -INFINITY) continue;
-      f = fast_exp2(ms + bias - M);
-      l += pl.l[at(x)] * f;
-#pragma unroll
-      for (int y = 0; y < D / 32; ++y) a[y] += pl.acc[at(x) * D + y * 32 + lane] * f;
-    }
-    __nv_bfloat16* o = (__nv_bfloat16*)p.o + (((size_t)sp.q0 + lc * B + r) * p.hq + qh) * D;
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x) o[x * 32 + lane] = __float2bfloat16_rn(a[x] * inv);
-  }
-}
-
-template <typename T, int D>
 cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
   const ChunkWs w = chunk_ws(p);
   cudaError_t e;
-  auto prep = prep_kernel<T, D>;
-  auto scan = scan_walk_kernel<T, D>;
-  auto att = attend_kernel<T, D>;
-  auto rew = rewrite_kernel<T, D>;
+  auto prep = prep_kernel<D>;
+  auto scan = scan_walk_kernel<D>;
+  auto att = attend_kernel<D>;
+  auto rew = rewrite_kernel<D>;
   const size_t s1 = (size_t)PrepSmem<D>::total * 4, s2 = scan_walk_smem<D>();
   const size_t s3 = (size_t)ScanSmem<D>::attend * 4, s4 = (size_t)(D + KT) * (D + 4) * 4;
   if ((e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(att, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s3)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(rew, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s4)) != cudaSuccess) return e;
-  constexpr bool TC = std::is_same<T, __nv_bfloat16>::value;
-  TcPlan pl{};
   plan_kernel<<<1, 1024, 0, st>>>(p, (int*)(ws + w.plan));
-  if (TC) {
-    pl = {w.pairs, (int*)(ws + w.ps), (long long*)(ws + w.us), (float*)(ws + w.pm), (float*)(ws + w.pl),
-          (float*)(ws + w.pacc), (int*)(ws + w.err)};
-    plan_tc_kernel<<<1, 1024, 0, st>>>(p, pl);
-  }
   prep<<<dim3(w.nch, p.c.heads), NT, s1, st>>>(p, w, ws);
   scan<<<(unsigned)(p.c.slots * p.c.heads + w.nch * p.hq), NT, s2, st>>>(p, w, ws);
-  if (TC) {
-    if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attend_tc(p, pl, ws + w.zq, st)) != cudaSuccess) return e;
-  } else {
-    att<<<dim3(w.nch, p.hq, w.nsplit), NT, s3, st>>>(p, w, ws);
-  }
+  att<<<dim3(w.nch, p.hq, w.nsplit), NT, s3, st>>>(p, w, ws);
   rew<<<608, NT, s4, st>>>(p, w, ws);
-  if (TC) merge_tc_kernel<D><<<dim3(w.nch, p.hq), NT, 0, st>>>(p, w, pl, ws);
-  else merge_kernel<T, D><<<dim3(w.nch, p.hq), NT, 0, st>>>(p, w, ws);
+  merge_kernel<D><<<dim3(w.nch, p.hq), NT, 0, st>>>(p, w, ws);
   return cudaGetLastError();
 }
 
@@ -739,15 +606,12 @@ cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
 size_t paged_chunk_ws_bytes(const PagedArgs& p) { return chunk_ws(p).total; }
 
 cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st) {
-  if (p.c.head_dim == kHeadDim)
-    return p.c.cache_dtype == PATH_BF16 ? chunk_t<__nv_bfloat16, kHeadDim>(p, ws, st) : chunk_t<float, kHeadDim>(p, ws, st);
-  return p.c.cache_dtype == PATH_BF16 ? chunk_t<__nv_bfloat16, kHeadDimWide>(p, ws, st)
-                                      : chunk_t<float, kHeadDimWide>(p, ws, st);
+  return p.c.head_dim == kHeadDim ? chunk_t<kHeadDim>(p, ws, st) : chunk_t<kHeadDimWide>(p, ws, st);
 }
 
 size_t paged_ws_bytes(const PagedArgs& p) {
   if (p.c.cache_dtype != PATH_BF16) return paged_chunk_ws_bytes(p);
-  return paged_token_ws_bytes(p) + (p.max_new > 1 ? paged_chunk_ws_bytes(p) : 0);
+  return paged_token_ws_bytes(p) + (p.max_new > 1 ? paged_new_ws_bytes(p) : 0);
 }
 cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st) {
   if (p.c.cache_dtype != PATH_BF16) return launch_paged_chunk(p, ws, st);
@@ -755,7 +619,7 @@ cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st) {
   if (e != cudaSuccess || p.max_new <= 1) return e;
   PagedArgs more = p;
   more.min_new = 2;
-  return launch_paged_chunk(more, ws + paged_token_ws_bytes(p), st);
+  return launch_paged_new(more, ws + paged_token_ws_bytes(p), st);
 }
 
 }  // namespace pathattn

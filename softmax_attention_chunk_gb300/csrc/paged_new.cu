@@ -1,0 +1,953 @@
+// Paged serving of bf16 caches: prompt chunks (slots with more new tokens than the streaming kernels take).
+//
+// Mathematics (paged_chunk.cu has the formulas): the new tokens of a slot are cut into UT chunks of 64 and blocks
+// of 256 (four chunks).  A chain over all earlier chunks per query tile would cost a D x D product per step;
+// instead
+//  * inside its block a query chunk meets the earlier chunks right to left (at most three steps) and arrives at the
+//    block's start: zs, and the softmax state so far;
+//  * the keys of a block are carried on: to the block's end, then through every later block,
+//    rows <- rows F_block, and a copy is kept at each block start ("version").  For the queries of block b
+//    the keys of all earlier blocks, in version b, are plain rows: attention without transport;
+//  * rows of the identity carried the same way are the products G_b = F_0 ... F_(b-1), which move zs to the
+//    start of the call (z = zs G_b^T, for the cached rows), and at the end M, by which the cached rows are
+//    multiplied.
+// So all attention but the 256-token diagonal runs in the tensor-core kernel (paged_tc.cu).
+//
+// Roundings: F, the carried rows and M are held as bf16 pairs (high + rest, about 16 bits; products of three terms),
+// so chains of blocks do not accumulate 8-bit rounding; z, zs, the versions and P are rounded to bf16 once, as
+// tensor-core operands.
+//
+// These kernels are small next to the attention (2048 tokens, 32 heads, D = 128: about 15 of 1200 GFLOP) and bound
+// by latency, so they run 16x8x16 warp MMAs on tiles in shared memory, one block per chunk, head and task.
+#include "paged_tc.h"
+#include "dev_common.cuh"
+#include "mma_common.cuh"
+#include "smem_mm.cuh"
+
+namespace pathattn {
+namespace {
+
+constexpr int C = 64;            // UT chunk
+constexpr int MB = kTcBlockTokens;  // tokens of a block: 256
+constexpr int CPB = MB / C;      // chunks of a block
+
+using bf16 = __nv_bfloat16;
+
+// ---- warp tiles ----
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"((uint32_t)__cvta_generic_to_shared(p)));
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], const void* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"((uint32_t)__cvta_generic_to_shared(p)));
+}
+// c[NT][4] (16 x 8 NT) += A (KS fragments of 16 columns) B; B in shared memory as [n][k] rows (T = false) or [k][n]
+// rows (T = true) of ld elements.
+template <int NT, int KS, bool T>
+__device__ __forceinline__ void warp_mm(float (&c)[NT][4], const uint32_t (&a)[KS][4], const bf16* b, int ld) {
+  const int lane = threadIdx.x & 31, mat = lane >> 3, row = lane & 7;
+#pragma unroll
+  for (int k = 0; k < KS; ++k)
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t r[4];
+      if (T) ldm4t(r, b + (16 * k + (mat & 1) * 8 + row) * ld + 8 * n + (mat >> 1) * 8);
+      else ldm4(r, b + (8 * n + (mat >> 1) * 8 + row) * ld + 16 * k + (mat & 1) * 8);
+      mma_bf16(c[n], a[k][0], a[k][1], a[k][2], a[k][3], r[0], r[1]);
+      mma_bf16(c[n + 1], a[k][0], a[k][1], a[k][2], a[k][3], r[2], r[3]);
+    }
+}
+template <int KS>
+__device__ __forceinline__ void load_a(uint32_t (&a)[KS][4], const bf16* t, int ld, int m0) {
+  const int lane = threadIdx.x & 31, mat = lane >> 3, row = lane & 7;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) ldm4(a[k], t + (m0 + (mat & 1) * 8 + row) * ld + 16 * k + (mat >> 1) * 8);
+}
+// Accumulators as A fragments: rounded, or high + rest.
+template <int KS>
+__device__ __forceinline__ void to_a(uint32_t (&a)[KS][4], const float (&c)[2 * KS][4]) {
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    a[k][0] = pack2(c[2 * k][0], c[2 * k][1]);
+    a[k][1] = pack2(c[2 * k][2], c[2 * k][3]);
+    a[k][2] = pack2(c[2 * k + 1][0], c[2 * k + 1][1]);
+    a[k][3] = pack2(c[2 * k + 1][2], c[2 * k + 1][3]);
+  }
+}
+template <int KS>
+__device__ __forceinline__ void to_a2(uint32_t (&hi)[KS][4], uint32_t (&lo)[KS][4], const float (&c)[2 * KS][4]) {
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    split2(c[2 * k][0], c[2 * k][1], hi[k][0], lo[k][0]);
+    split2(c[2 * k][2], c[2 * k][3], hi[k][1], lo[k][1]);
+    split2(c[2 * k + 1][0], c[2 * k + 1][1], hi[k][2], lo[k][2]);
+    split2(c[2 * k + 1][2], c[2 * k + 1][3], hi[k][3], lo[k][3]);
+  }
+}
+// rows x D bf16 from global (row pitch in elements) to shared memory, rows >= `have` zero; asynchronous.
+template <int D, int LD, int THREADS>
+__device__ __forceinline__ void fetch(bf16* dst, const bf16* src, size_t pitch, int rows, int have) {
+  for (int e = threadIdx.x; e < rows * (D / 8); e += THREADS) {
+    const int r = e / (D / 8), x = e % (D / 8) * 8;
+    const bool ok = r < have;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + r * LD + x)),
+                 "l"(src + (ok ? (size_t)r * pitch + x : 0)), "r"(ok ? 16 : 0)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory"); }
+
+// ---- workspace ----
+struct NewWs {
+  int nch, nblk;           // chunks and blocks of any legal pass
+  size_t cstart, bstart, pstart, ustart, nstart, vstart, rstart;  // plan (TcPlan)
+  size_t nx, nuw;          // -X [nch][H][64][64], -U W [nch][H][64][D]
+  size_t kr, f;            // K-> [2][nch][H][64][D], F [2][nch][H][D][D] (high, rest)
+  size_t ke, fb;           // keys at their block's end [2][nblk][H][256][D], block products [2][nblk][H][D][D]
+  size_t gb, mm;           // G_b [2][nblk][H][D][D], M [2][slots][H][D][D]
+  size_t ver;              // versions: rows [D]
+  size_t cn;               // forget gate: sums since the start of the call [H][nblk * 256]
+  size_t zs, z;            // queries at the block's and at the call's start [H][pairs][256][D]
+  size_t m, l, acc;        // the diagonal's state [nch][hq][64](, [D])
+  size_t pm, pl, pacc;     // parts of the tensor-core attention
+  size_t err, total;
+  long long ver_rows;
+  int pairs;
+};
+NewWs new_ws(const PagedArgs& p) {
+  NewWs w{};
+  const size_t D = p.c.head_dim, H = p.c.heads, hq = p.hq;
+  const long long live = p.c.slots < p.total ? p.c.slots : p.total;
+  const long long most = p.max_new < kTcPassTokens ? p.max_new : kTcPassTokens;  // new tokens of a slot in a pass
+  const long long tokens = p.total < most * live ? p.total : most * live;
+  auto parts_of = [&](long long x) { const long long n = (tokens + (x - 1) * live) / x; return n < 1 ? 1LL : n; };
+  w.nch = (int)parts_of(C);
+  w.nblk = (int)parts_of(MB);
+  const long long np = (tokens * p.G + (kTcPair - 1) * live) / kTcPair;
+  w.pairs = (int)(np < 1 ? 1 : np);
+  const long long blk = (most + MB - 1) / MB;
+  w.ver_rows = (long long)H * w.nblk * (blk > 1 ? blk - 1 : 0) * (MB / 2);
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, 256); return o; };
+  const size_t S1 = p.c.slots + 1;
+  w.cstart = take(S1 * 4);
+  w.bstart = take(S1 * 4);
+  w.pstart = take(S1 * 4);
+  w.rstart = take(S1 * 4);
+  w.vstart = take(S1 * 8);
+  w.ustart = take(S1 * 8);
+  w.nstart = take(S1 * 8);
+  w.nx = take((size_t)w.nch * H * C * C * 2);
+  w.nuw = take((size_t)w.nch * H * C * D * 2);
+  w.kr = take((size_t)2 * w.nch * H * C * D * 2);
+  w.f = take((size_t)2 * w.nch * H * D * D * 2);
+  w.ke = take((size_t)2 * w.nblk * H * MB * D * 2);
+  w.fb = take((size_t)2 * w.nblk * H * D * D * 2);
+  w.gb = take((size_t)2 * w.nblk * H * D * D * 2);
+  w.mm = take((size_t)2 * p.c.slots * H * D * D * 2);
+  w.ver = take((size_t)w.ver_rows * D * 2);
+  w.cn = take((size_t)H * w.nblk * MB * 4);
+  w.zs = take((size_t)H * w.pairs * kTcPair * D * 2);
+  w.z = take((size_t)H * w.pairs * kTcPair * D * 2);
+  w.m = take((size_t)w.nch * hq * C * 4);
+  w.l = take((size_t)w.nch * hq * C * 4);
+  w.acc = take((size_t)w.nch * hq * C * D * 4);
+  const size_t parts = 2 * (size_t)H * w.pairs + kTcBlocks;
+  w.pm = take(parts * kTcPair * 4);
+  w.pl = take(parts * kTcPair * 4);
+  w.pacc = take(parts * kTcPair * D * 4);
+  w.err = take(4);
+  w.total = off;
+  return w;
+}
+
+// ---- plan ----
+// Exclusive prefix sums over the slots, all at once: chunks, blocks, query pairs, rewrite tiles, version rows, units.
+__global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool report) {
+  constexpr int N = 7;
+  __shared__ long long wsum[N][32], carry[N];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < N) carry[tid] = 0;
+  if (tid == 0) *pl.err = 0;
+  __syncthreads();
+  for (int base = 0; base < p.c.slots; base += 1024) {
+    const int b = base + tid;
+    long long v[N] = {0, 0, 0, 0, 0, 0, 0}, x[N];
+    if (b < p.c.slots) {
+      const SlotSpan s = pass_span(p, b);
+      if (report && s.code) paged_error(p.c.status, s.code);
+      if (s.n > 0) {
+        const long long H = p.c.heads, np = ((long long)s.n * p.G + kTcPair - 1) / kTcPair, nb = (s.n + MB - 1) / MB;
+        v[0] = (s.n + C - 1) / C;
+        v[1] = nb;
+        v[2] = np;
+        v[3] = live_tiles(s.t0, p.window, p.sinks, kRewriteRows).count;
+        v[4] = H * (MB / 2) * nb * (nb - 1);
+        v[5] = np * H * live_tiles(s.t0, p.window, p.sinks, kTcKeys).count;
+        v[6] = H * new_units(np, p.G);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      x[i] = v[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, x[i], o);
+        if (lane >= o) x[i] += a;
+      }
+      if (lane == 31) wsum[i][warp] = x[i];
+    }
+    __syncthreads();
+    if (warp < N) {  // warp i adds up row i
+      long long t = wsum[warp][lane], y = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += a;
+      }
+      const long long c0 = carry[warp];
+      wsum[warp][lane] = c0 + y - t;
+      __syncwarp();
+      if (lane == 31) carry[warp] = c0 + y;
+    }
+    __syncthreads();
+    if (b < p.c.slots) {
+      long long e[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = wsum[i][warp] + x[i] - v[i];
+      pl.cstart[b] = (int)e[0];
+      pl.bstart[b] = (int)e[1];
+      pl.pstart[b] = (int)e[2];
+      pl.rstart[b] = (int)e[3];
+      pl.vstart[b] = e[4];
+      pl.ustart[b] = e[5];
+      pl.nstart[b] = e[6];
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    const int S = p.c.slots;
+    pl.cstart[S] = (int)carry[0];
+    pl.bstart[S] = (int)carry[1];
+    pl.pstart[S] = (int)carry[2];
+    pl.rstart[S] = (int)carry[3];
+    pl.vstart[S] = carry[4];
+    pl.ustart[S] = carry[5];
+    pl.nstart[S] = carry[6];
+  }
+}
+__device__ __forceinline__ int owner(const int* start, int slots, int x) {
+  int lo = 0, hi = slots;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ---- chunk preparation: one block per (chunk, key head) ----
+constexpr int PT = 512;
+template <int D>
+struct PrepSmem {
+  static constexpr int DS = D + 4, BS = C + 4;
+  static constexpr int kW = 0, kK = kW + C * DS, kY = kK + C * DS, kU = kY + C * DS, kG = kU + C * BS, kN = kG + C * BS;
+  static constexpr int kX = kN + C * BS, kBeta = kX + C * BS, total = kBeta + C;
+};
+template <int D>
+__global__ void __launch_bounds__(PT) prep_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  extern __shared__ float sm[];
+  using S = PrepSmem<D>;
+  constexpr int DS = S::DS, BS = S::BS;
+  float *sW = sm + S::kW, *sK = sm + S::kK, *sY = sm + S::kY, *sU = sm + S::kU, *sG = sm + S::kG, *sN = sm + S::kN;
+  float *sX = sm + S::kX, *sBeta = sm + S::kBeta;
+  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, H = p.c.heads;
+  if (c >= pl.cstart[p.c.slots]) return;
+  const int b = owner(pl.cstart, p.c.slots, c);
+  const SlotSpan sp = pass_span(p, b);
+  const int r0 = (c - pl.cstart[b]) * C, rows = min(C, sp.n - r0);
+  const size_t tok0 = (size_t)sp.q0 + r0;
+  for (int e = tid; e < C * D / 8; e += PT) {
+    const int r = e / (D / 8), x = e % (D / 8) * 8;
+    uint4 a = make_uint4(0, 0, 0, 0), k = a;
+    if (r < rows) {
+      a = *reinterpret_cast<const uint4*>((const bf16*)p.w + ((tok0 + r) * H + h) * D + x);
+      k = *reinterpret_cast<const uint4*>((const bf16*)p.k + ((tok0 + r) * H + h) * D + x);
+    }
+    const uint32_t aa[4] = {a.x, a.y, a.z, a.w}, kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sW[r * DS + x + 2 * i] = lo_f(aa[i]);
+      sW[r * DS + x + 2 * i + 1] = hi_f(aa[i]);
+      sK[r * DS + x + 2 * i] = lo_f(kk[i]);
+      sK[r * DS + x + 2 * i + 1] = hi_f(kk[i]);
+    }
+  }
+  if (tid < C) sBeta[tid] = tid < rows ? clamp_beta(p.beta[(tok0 + tid) * H + h]) : 0.f;
+  __syncthreads();
+  smem_mm<C, C, D, false, true, true>(sW, DS, sW, DS, [&](int i, int j, float x) { sG[i * BS + j] = j < i ? x : 0.f; });
+  smem_mm<C, C, D, false, true, true>(sW, DS, sK, DS, [&](int i, int j, float x) { sN[i * BS + j] = j < i ? x : 0.f; });
+  for (int e = tid; e < C * C; e += PT) sU[(e / C) * BS + e % C] = 0.f;
+  __syncthreads();
+  // U, block inversion: the two diagonal 32-row blocks by forward substitution (one warp each, one column per
+  // lane), then U21 = -U22 G21 U11
+  if (tid < 64) {
+    const int o = tid & 32, col = tid & 31;
+    float u[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float a0 = (col == i) ? 1.f : 0.f, a1 = 0.f;
+#pragma unroll
+      for (int m = 0; m + 1 < i; m += 2) {
+        a0 -= sG[(o + i) * BS + o + m] * u[m];
+        a1 -= sG[(o + i) * BS + o + m + 1] * u[m + 1];
+      }
+      if (i & 1) a0 -= sG[(o + i) * BS + o + i - 1] * u[i - 1];
+      u[i] = sBeta[o + i] * (a0 + a1);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sU[(o + i) * BS + o + col] = u[i];
+  }
+  __syncthreads();
+  smem_mm<32, 32, 32, false, false, true>(sG + 32 * BS, BS, sU, BS, [&](int i, int j, float x) { sX[i * BS + j] = x; });
+  __syncthreads();
+  smem_mm<32, 32, 32, false, false, true>(sU + 32 * BS + 32, BS, sX, BS,
+                                          [&](int i, int j, float x) { sU[(32 + i) * BS + j] = -x; });
+  __syncthreads();
+  const size_t cc = (size_t)c * H + h;
+  bf16* nuw = (bf16*)(ws + w.nuw) + cc * C * D;
+  smem_mm<C, C, C, false, false, true>(sU, BS, sN, BS, [&](int i, int j, float x) {
+    sX[i * BS + j] = x;
+    ((bf16*)(ws + w.nx))[cc * C * C + i * C + j] = __float2bfloat16_rn(-x);
+  });
+  smem_mm<C, D, C, false, false, true>(sU, BS, sW, DS, [&](int i, int j, float x) { nuw[i * D + j] = __float2bfloat16_rn(-x); });
+  smem_mm<C, D, C, true, false, true>(sU, BS, sW, DS, [&](int i, int j, float x) { sY[i * DS + j] = x; });
+  __syncthreads();
+  auto two = [](bf16* hi, bf16* lo, size_t at, float x) {
+    const bf16 a = __float2bfloat16_rn(x);
+    hi[at] = a;
+    lo[at] = __float2bfloat16_rn(x - __bfloat162float(a));
+  };
+  bf16 *krh = (bf16*)(ws + w.kr), *krl = krh + (size_t)w.nch * H * C * D;
+  bf16 *fh = (bf16*)(ws + w.f), *fl = fh + (size_t)w.nch * H * D * D;
+  smem_mm<C, D, C, true, false, true>(sX, BS, sW, DS,
+                                      [&](int j, int n, float x) { two(krh, krl, cc * C * D + j * D + n, sK[j * DS + n] - x); });
+  smem_mm<D, D, C, true, false, true>(sW, DS, sY, DS,
+                                      [&](int n, int k, float x) { two(fh, fl, cc * D * D + n * D + k, (n == k ? 1.f : 0.f) - x); });
+}
+
+// ---- carried rows ----
+constexpr int WT = 128;
+template <int D>
+constexpr size_t carry_smem() { return (size_t)2 * D * (D + 8) * 2; }
+// A slab of 64 rows (16 per warp) in fp32 accumulators: rows <- rows F, F as a pair of [D][D] matrices.
+template <int D>
+struct Slab {
+  float c[D / 8][4];
+  __device__ __forceinline__ void load(const bf16* hi, const bf16* lo) {  // [64][D]
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const size_t at = (size_t)(r0 + 8 * y) * D + 8 * n + 2 * t;
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(hi + at), e = *reinterpret_cast<const uint32_t*>(lo + at);
+        c[n][2 * y] = lo_f(a) + lo_f(e);
+        c[n][2 * y + 1] = hi_f(a) + hi_f(e);
+      }
+  }
+  __device__ __forceinline__ void times(const bf16* fh, const bf16* fl, bf16* sm) {
+    constexpr int LD = D + 8;
+    bf16 *sh = sm, *sl = sm + D * LD;
+    __syncthreads();
+    fetch<D, LD, WT>(sh, fh, D, D, D);
+    fetch<D, LD, WT>(sl, fl, D, D, D);
+    uint32_t ah[D / 16][4], al[D / 16][4];
+    to_a2(ah, al, c);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+    fetch_wait();
+    __syncthreads();
+    warp_mm<D / 8, D / 16, true>(c, ah, sh, LD);
+    warp_mm<D / 8, D / 16, true>(c, al, sh, LD);
+    warp_mm<D / 8, D / 16, true>(c, ah, sl, LD);
+  }
+  // rows r of `rows` as a pair, or (lo null) rounded
+  __device__ __forceinline__ void store(bf16* hi, bf16* lo, int rows = 64) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if (r0 + 8 * y >= rows) continue;
+        const size_t at = (size_t)(r0 + 8 * y) * D + 8 * n + 2 * t;
+        uint32_t a, e;
+        split2(c[n][2 * y], c[n][2 * y + 1], a, e);
+        *reinterpret_cast<uint32_t*>(hi + at) = a;
+        if (lo) *reinterpret_cast<uint32_t*>(lo + at) = e;
+      }
+  }
+};
+
+// Level 1, one block per (block, key head, slab): slabs 0..3 are the block's chunks of keys, carried to the
+// block's end; the others rows of the block product.
+template <int D>
+__device__ void carry_in_block(const PagedArgs& p, const NewWs& w, const TcPlan& pl, char* ws, bf16* sm, int blk, int h, int slab) {
+  const int H = p.c.heads;
+  const int b = owner(pl.bstart, p.c.slots, blk);
+  const SlotSpan sp = pass_span(p, b);
+  const int lb = blk - pl.bstart[b], nch = (min(MB, sp.n - lb * MB) + C - 1) / C, c0 = pl.cstart[b] + lb * CPB;
+  if (slab < CPB && slab >= nch) return;
+  const size_t fstep = (size_t)w.nch * H * D * D, kstep = (size_t)w.nch * H * C * D;
+  const bf16 *fh = (const bf16*)(ws + w.f), *kr = (const bf16*)(ws + w.kr);
+  Slab<D> s;
+  int c = c0;
+  if (slab < CPB) {
+    c = c0 + slab;
+    const bf16* at = kr + ((size_t)c * H + h) * C * D;
+    s.load(at, at + kstep);
+  } else {
+    const bf16* at = fh + ((size_t)c * H + h) * D * D + (size_t)(slab - CPB) * 64 * D;
+    s.load(at, at + fstep);
+  }
+  for (++c; c < c0 + nch; ++c) {
+    const bf16* at = fh + ((size_t)c * H + h) * D * D;
+    s.times(at, at + fstep, sm);
+  }
+  const size_t bb = (size_t)blk * H + h;
+  if (slab < CPB) {
+    bf16* at = (bf16*)(ws + w.ke) + (bb * MB + slab * C) * D;
+    s.store(at, at + (size_t)w.nblk * H * MB * D);
+  } else {
+    bf16* at = (bf16*)(ws + w.fb) + bb * D * D + (size_t)(slab - CPB) * 64 * D;
+    s.store(at, at + (size_t)w.nblk * H * D * D);
+  }
+}
+
+// Level 2: through the later blocks of the slot, a copy at every block start; at the end into the pages, or M.
+template <int D>
+__global__ void __launch_bounds__(WT) carry_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  bf16* sm = (bf16*)smem;
+  const int blk = blockIdx.x, h = blockIdx.y, slab = blockIdx.z, H = p.c.heads;
+  if (blk >= pl.bstart[p.c.slots]) return;
+  const int b = owner(pl.bstart, p.c.slots, blk);
+  const SlotSpan sp = pass_span(p, b);
+  const int b0 = pl.bstart[b], lb = blk - b0, nb = (sp.n + MB - 1) / MB;
+  const int rows = slab < CPB ? min(C, sp.n - lb * MB - slab * C) : 64;
+  if (rows <= 0 || (slab >= CPB && lb > 0)) return;  // (the slot's first block carries the identity)
+  const size_t fstep = (size_t)w.nblk * H * D * D, kstep = (size_t)w.nblk * H * MB * D;
+  const size_t bb = (size_t)blk * H + h;
+  const int ir = (slab - CPB) * 64;
+  Slab<D> s;
+  if (slab < CPB) {
+    const bf16* at = (const bf16*)(ws + w.ke) + (bb * MB + slab * C) * D;
+    s.load(at, at + kstep);
+  } else {
+    const bf16* at = (const bf16*)(ws + w.fb) + bb * D * D + (size_t)ir * D;
+    s.load(at, at + fstep);
+  }
+  for (int x = lb + 1; x < nb; ++x) {
+    // rows at the start of block x
+    if (slab < CPB) {
+      // versions of a slot: per head, blocks 1..: version x has 256 x rows and lies behind 128 x (x - 1) rows
+      const long long v = pl.vstart[b] + (long long)h * (MB / 2) * nb * (nb - 1) + (long long)(MB / 2) * x * (x - 1) + lb * MB + slab * C;
+      s.store((bf16*)(ws + w.ver) + v * D, nullptr);
+    } else {
+      bf16* at = (bf16*)(ws + w.gb) + ((size_t)(b0 + x) * H + h) * D * D + (size_t)ir * D;
+      s.store(at, at + fstep);
+    }
+    const bf16* at = (const bf16*)(ws + w.fb) + ((size_t)(b0 + x) * H + h) * D * D;
+    s.times(at, at + fstep, sm);
+  }
+  if (slab >= CPB) {
+    bf16* at = (bf16*)(ws + w.mm) + ((size_t)b * H + h) * D * D + (size_t)ir * D;
+    s.store(at, at + (size_t)p.c.slots * H * D * D);
+    return;
+  }
+  // the appended rows
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, r0 = (threadIdx.x >> 5) * 16 + g;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int r = r0 + 8 * y;
+    if (r >= rows) continue;
+    const long long at = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0 + lb * MB + slab * C + r);
+    if (at < 0) {
+      paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+      continue;
+    }
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+      *reinterpret_cast<uint32_t*>((bf16*)p.c.k_pool + at * D + 8 * n + 2 * t) = pack2(s.c[n][2 * y], s.c[n][2 * y + 1]);
+  }
+}
+
+// Sums of log f since the start of the pass, and the running sums of the appended rows: one block per (slot, head).
+__device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, char* ws, int b, int h) {
+  __shared__ float wsum[WT / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.c.heads;
+  const SlotSpan sp = pass_span(p, b);
+  if (sp.n == 0) return;
+  const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
+  const float a0 = last >= 0 ? p.c.a_pool[last] : 0.f;
+  float* cn = (float*)(ws + w.cn) + ((size_t)h * w.nblk + pl.bstart[b]) * MB;
+  double carry = 0.0;
+  for (int base = 0; base < sp.n; base += WT) {
+    const int r = base + tid;
+    const float v = r < sp.n ? p.log_f[((size_t)sp.q0 + r) * H + h] : 0.f;
+    float x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float a = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += a;
+    }
+    __syncthreads();
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    float before = 0.f, all = 0.f;
+#pragma unroll
+    for (int i = 0; i < WT / 32; ++i) {
+      if (i < warp) before += wsum[i];
+      all += wsum[i];
+    }
+    if (r < sp.n) {
+      const double c = carry + before + x;
+      cn[r] = (float)c;
+      const long long at = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r);
+      if (at >= 0) p.c.a_pool[at] = (float)(a0 + c);
+    }
+    carry += all;
+  }
+}
+
+// Blocks: (block, head, slab) of level 1, then (slot, head) of the gate's sums.
+template <int D>
+__global__ void __launch_bounds__(WT) carry_in_block_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int slabs = CPB + D / 64, H = p.c.heads;
+  const int x = blockIdx.x, n1 = w.nblk * H * slabs;
+  if (x >= n1) {
+    gate_sums(p, w, pl, ws, (x - n1) / H, (x - n1) % H);
+    return;
+  }
+  const int blk = x / (H * slabs), rest = x % (H * slabs);
+  if (blk >= pl.bstart[p.c.slots]) return;
+  carry_in_block<D>(p, w, pl, ws, (bf16*)smem, blk, rest / slabs, rest % slabs);
+}
+
+// ---- queries: diagonal chunk and the earlier chunks of the block; one block per (chunk, query head) ----
+template <int D>
+struct QSmem {
+  static constexpr int LD = D + 8, LX = C + 8, T = C * LD;  // one [64][D] tile
+  static constexpr int kQ = 0, kW = T, kK = 2 * T, kV = 3 * T, kUW = 4 * T, kX = 5 * T;
+  static constexpr int kFh = 2 * T, kFl = kFh + D * LD;     // chain: keys at 0, values at T, F behind them
+  static constexpr int end1 = kX + C * LX, end2 = kFl + D * LD;
+  static constexpr size_t bytes = (size_t)(end1 > end2 ? end1 : end2) * 2;
+};
+// Online softmax of the scores of 64 keys (16 rows per warp, log2 domain, hidden ones -inf): p as A fragments.
+__device__ __forceinline__ void softmax64(float (&s)[8][4], float (&m)[2], float (&l)[2], float (&corr)[2], uint32_t (&pa)[4][4]) {
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * y], s[n][2 * y + 1]));
+    mx = group_max<4>(mx);
+    const float mn = fmaxf(m[y], mx);
+    corr[y] = mn == -INFINITY ? 1.f : fast_exp2(m[y] - mn);
+    m[y] = mn;
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    float sum = 0.f;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      s[n][2 * y] = fast_exp2(s[n][2 * y] - mu);
+      s[n][2 * y + 1] = fast_exp2(s[n][2 * y + 1] - mu);
+      sum += s[n][2 * y] + s[n][2 * y + 1];
+    }
+    l[y] = l[y] * corr[y] + sum;
+  }
+  to_a(pa, s);
+}
+template <int D, bool FOX>
+__global__ void __launch_bounds__(WT) query_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  bf16* sm = (bf16*)smem;
+  using S = QSmem<D>;
+  constexpr int LD = S::LD, LX = S::LX;
+  const int c = blockIdx.x, qh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int H = p.c.heads, G = p.G, h = qh / G;
+  if (c >= pl.cstart[p.c.slots]) return;
+  const int b = owner(pl.cstart, p.c.slots, c);
+  const SlotSpan sp = pass_span(p, b);
+  const int lc = c - pl.cstart[b], r0 = lc * C, rows = min(C, sp.n - r0);
+  const size_t cc = (size_t)c * H + h, tok = (size_t)sp.q0 + r0;
+  fetch<D, LD, WT>(sm + S::kQ, (const bf16*)p.q + (tok * p.hq + qh) * D, (size_t)p.hq * D, C, rows);
+  fetch<D, LD, WT>(sm + S::kW, (const bf16*)p.w + (tok * H + h) * D, (size_t)H * D, C, rows);
+  fetch<D, LD, WT>(sm + S::kK, (const bf16*)p.k + (tok * H + h) * D, (size_t)H * D, C, rows);
+  fetch<D, LD, WT>(sm + S::kV, (const bf16*)p.v + (tok * H + h) * D, (size_t)H * D, C, rows);
+  fetch<D, LD, WT>(sm + S::kUW, (const bf16*)(ws + w.nuw) + cc * C * D, D, C, C);
+  fetch<C, LX, WT>(sm + S::kX, (const bf16*)(ws + w.nx) + cc * C * C, C, C, C);
+  fetch_wait();
+  __syncthreads();
+  if (qh % G == 0)  // the values join the cache
+    for (int e = tid; e < rows * (D / 8); e += WT) {
+      const int r = e / (D / 8), x = e % (D / 8) * 8;
+      const long long at = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r0 + r);
+      if (at >= 0) *reinterpret_cast<uint4*>((bf16*)p.c.v_pool + at * D + x) = *reinterpret_cast<const uint4*>(sm + S::kV + r * LD + x);
+      else paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+    }
+  const int ra = warp * 16 + g;  // this lane's rows: ra, ra + 8
+  float ci[2] = {0.f, 0.f};
+  const float* cn = (const float*)(ws + w.cn) + ((size_t)h * w.nblk + pl.bstart[b]) * MB;
+  if (FOX)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) ci[y] = ra + 8 * y < rows ? cn[r0 + ra + 8 * y] : 0.f;
+  // scores in the log2 domain of the keys of local chunk x, hidden ones -inf
+  auto finish = [&](float (&s)[8][4], int x) {
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = r0 + ra + (e >> 1) * 8, j = x * C + 8 * n + 2 * t + (e & 1);
+        float v = s[n][e] * p.scl;
+        if (FOX && j <= i && j < sp.n) v += (ci[e >> 1] - cn[j]) * kLog2e;
+        if (j > i || !sees(p.window, p.sinks, sp.t0 + i, sp.t0 + j)) v = -INFINITY;
+        s[n][e] = v;
+      }
+  };
+  float o[D / 8][4], z[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, corr[2];
+  uint32_t pa[4][4];
+  {
+    uint32_t qa[D / 16][4], mh[4][4], ml[4][4];
+    load_a(qa, sm + S::kQ, LD, warp * 16);
+    float s1[8][4], s[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s1[n][e] = s[n][e] = 0.f;
+    warp_mm<8, D / 16, false>(s1, qa, sm + S::kW, LD);
+    warp_mm<8, D / 16, false>(s, qa, sm + S::kK, LD);
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (8 * n + 2 * t + (e & 1) > ra + (e >> 1) * 8) s1[n][e] = 0.f;  // lower(Q W^T)
+    to_a2(mh, ml, s1);
+    warp_mm<8, 4, true>(s, mh, sm + S::kX, LX);
+    warp_mm<8, 4, true>(s, ml, sm + S::kX, LX);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {  // the fragment's registers as accumulators
+        z[2 * k + (y >> 1)][2 * (y & 1)] = lo_f(qa[k][y]);
+        z[2 * k + (y >> 1)][2 * (y & 1) + 1] = hi_f(qa[k][y]);
+      }
+    warp_mm<D / 8, 4, true>(z, mh, sm + S::kUW, LD);
+    warp_mm<D / 8, 4, true>(z, ml, sm + S::kUW, LD);
+    finish(s, lc);
+    softmax64(s, m, l, corr, pa);
+  }
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  warp_mm<D / 8, 4, true>(o, pa, sm + S::kV, LD);
+  for (int x = lc - 1; x >= lc / CPB * CPB; --x) {
+    const size_t c2 = (size_t)(c - lc + x) * H + h;
+    const bf16* fh = (const bf16*)(ws + w.f) + c2 * D * D;
+    __syncthreads();
+    fetch<D, LD, WT>(sm, (const bf16*)(ws + w.kr) + c2 * C * D, D, C, C);
+    fetch<D, LD, WT>(sm + S::T, (const bf16*)p.v + (((size_t)sp.q0 + x * C) * H + h) * D, (size_t)H * D, C, C);
+    fetch<D, LD, WT>(sm + S::kFh, fh, D, D, D);
+    fetch<D, LD, WT>(sm + S::kFl, fh + (size_t)w.nch * H * D * D, D, D, D);
+    uint32_t za[D / 16][4];
+    to_a(za, z);
+    fetch_wait();
+    __syncthreads();
+    float s[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    warp_mm<8, D / 16, false>(s, za, sm, LD);
+    finish(s, x);
+    softmax64(s, m, l, corr, pa);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] *= corr[e >> 1];
+    warp_mm<D / 8, 4, true>(o, pa, sm + S::T, LD);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
+    warp_mm<D / 8, D / 16, false>(z, za, sm + S::kFh, LD);
+    warp_mm<D / 8, D / 16, false>(z, za, sm + S::kFl, LD);
+  }
+  const size_t st = ((size_t)c * p.hq + qh) * C;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int r = ra + 8 * y;
+    const float ls = group_sum<4>(l[y]);  // (all lanes: before any leaves)
+    if (r >= rows) continue;
+    if (t == 0) {
+      ((float*)(ws + w.m))[st + r] = m[y];
+      ((float*)(ws + w.l))[st + r] = ls;
+    }
+    float* acc = (float*)(ws + w.acc) + (st + r) * D;
+    const size_t zr = (((size_t)h * w.pairs + pl.pstart[b]) * kTcPair + (size_t)(r0 + r) * G + qh % G) * D;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      *reinterpret_cast<float2*>(acc + 8 * n + 2 * t) = make_float2(o[n][2 * y], o[n][2 * y + 1]);
+      const uint32_t zz = pack2(z[n][2 * y], z[n][2 * y + 1]);
+      *reinterpret_cast<uint32_t*>((bf16*)(ws + w.zs) + zr + 8 * n + 2 * t) = zz;
+      if (lc < CPB) *reinterpret_cast<uint32_t*>((bf16*)(ws + w.z) + zr + 8 * n + 2 * t) = zz;
+    }
+  }
+}
+
+// z = zs G_b^T for the query pairs behind the first block: one block per (64 rows of a pair, head).
+template <int D>
+__global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  bf16* sm = (bf16*)smem;
+  constexpr int LD = D + 8;
+  const int pr = blockIdx.x / 4, q = blockIdx.x % 4, h = blockIdx.y, H = p.c.heads;
+  if (pr >= pl.pstart[p.c.slots]) return;
+  const int b = owner(pl.pstart, p.c.slots, pr);
+  const SlotSpan sp = pass_span(p, b);
+  const int lp = pr - pl.pstart[b], blk = lp / p.G;
+  if (blk == 0 || lp * kTcPair + q * 64 >= sp.n * p.G) return;
+  const bf16* gh = (const bf16*)(ws + w.gb) + ((size_t)(pl.bstart[b] + blk) * H + h) * D * D;
+  const size_t row = ((size_t)h * w.pairs + pr) * kTcPair + q * 64;
+  bf16* sz = sm + 2 * D * LD;
+  fetch<D, LD, WT>(sm, gh, D, D, D);
+  fetch<D, LD, WT>(sm + D * LD, gh + (size_t)w.nblk * H * D * D, D, D, D);
+  fetch<D, LD, WT>(sz, (const bf16*)(ws + w.zs) + row * D, D, 64, 64);
+  fetch_wait();
+  __syncthreads();
+  uint32_t a[D / 16][4];
+  load_a(a, sz, LD, (threadIdx.x >> 5) * 16);
+  Slab<D> s;
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) s.c[n][0] = s.c[n][1] = s.c[n][2] = s.c[n][3] = 0.f;
+  warp_mm<D / 8, D / 16, false>(s.c, a, sm, LD);
+  warp_mm<D / 8, D / 16, false>(s.c, a, sm + D * LD, LD);
+  s.store((bf16*)(ws + w.z) + row * D, nullptr);
+}
+
+// ---- cached rows: k <- k M ----
+// HBM-bound: every warp streams tiles of 32 rows through registers (a lane's 16-byte pieces are A fragments, as in
+// paged_token.cu), M as a bf16 pair in shared memory, its columns permuted inside 32 so that a lane's results
+// are the piece it read.
+constexpr int RT = 256;
+template <int D>
+__global__ void __launch_bounds__(RT, D == 64 ? 2 : 1) rewrite_kernel(PagedArgs p, NewWs w, TcPlan pl, const char* __restrict__ ws) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  bf16* sm = (bf16*)smem;
+  constexpr int LD = D + 8, KB = D / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, H = p.c.heads, P = p.c.page_size;
+  const int mat = lane >> 3, row = lane & 7;
+  // units: (slot, head, tile); a block takes a run, its warps the tiles of one (slot, head) in turn
+  const long long units = (long long)pl.rstart[p.c.slots] * H;
+  const long long per = (units + gridDim.x - 1) / gridDim.x, u0 = per * blockIdx.x, u1 = u0 + per < units ? u0 + per : units;
+  for (long long u = u0; u < u1;) {
+    const int b = owner(pl.rstart, p.c.slots, (int)(u / H));
+    const SlotSpan sp = pass_span(p, b);
+    const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, kRewriteRows);
+    const long long in = u - (long long)pl.rstart[b] * H;
+    const int h = (int)(in / lt.count), i0 = (int)(in % lt.count);
+    const long long left = u1 - u;
+    const int i1 = left < lt.count - i0 ? i0 + (int)left : lt.count;
+    const bf16* mh = (const bf16*)(ws + w.mm) + ((size_t)b * H + h) * D * D;
+    const bf16* ml = mh + (size_t)p.c.slots * H * D * D;
+    __syncthreads();
+    for (int e = tid; e < D * D / 2; e += RT) {
+      const int k = e / (D / 2), d = e % (D / 2) * 2;
+      const int at = k * LD + (d & ~31) + 8 * ((d % 8) / 2) + 2 * ((d % 32) / 8);
+      *reinterpret_cast<uint32_t*>(sm + at) = *reinterpret_cast<const uint32_t*>(mh + k * D + d);
+      *reinterpret_cast<uint32_t*>(sm + D * LD + at) = *reinterpret_cast<const uint32_t*>(ml + k * D + d);
+    }
+    __syncthreads();
+    for (int i = i0 + warp; i < i1; i += RT / 32) {
+      const int j0 = live_tile(lt, i) * kRewriteRows;
+      bf16* rp[4];
+      bool keep[4];
+      uint4 k4[4][KB];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {  // rows g + 8 y
+        const int j = j0 + g + 8 * y;
+        keep[y] = j < sp.t0 && sees(p.window, p.sinks, sp.t0 + sp.n, j);
+        rp[y] = nullptr;
+        if (keep[y]) {
+          const int pg = __ldg(p.c.k_table + (size_t)b * p.c.table_width + j / P);
+          if ((unsigned)pg < (unsigned)p.c.k_pages) rp[y] = (bf16*)p.c.k_pool + (((long long)pg * H + h) * P + j % P) * D + 8 * t;
+          else paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+        }
+#pragma unroll
+        for (int x = 0; x < KB; ++x) k4[y][x] = rp[y] ? *reinterpret_cast<const uint4*>(rp[y] + 32 * x) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int xo = 0; xo < KB; ++xo) {  // 32 output columns at a time
+        float c[2][4][4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) c[y][n][0] = c[y][n][1] = c[y][n][2] = c[y][n][3] = 0.f;
+#pragma unroll
+        for (int x = 0; x < KB; ++x) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint4 lo = k4[2 * y][x], hi = k4[2 * y + 1][x];
+              a[y][0] = e ? lo.z : lo.x;
+              a[y][1] = e ? hi.z : hi.x;
+              a[y][2] = e ? lo.w : lo.y;
+              a[y][3] = e ? hi.w : hi.y;
+            }
+            // rows of M for the summation order of the pieces: index 2t' + f (+ 8) is column 8 t' + 4 e + f (+ 2)
+            const int kr = 32 * x + 8 * (row >> 1) + 4 * e + (row & 1) + 2 * (mat & 1);
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+              for (int n = 0; n < 4; n += 2) {
+                uint32_t r[4];
+                ldm4t(r, sm + v * D * LD + kr * LD + 32 * xo + 8 * n + (mat >> 1) * 8);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  mma_bf16(c[y][n], a[y][0], a[y][1], a[y][2], a[y][3], r[0], r[1]);
+                  mma_bf16(c[y][n + 1], a[y][0], a[y][1], a[y][2], a[y][3], r[2], r[3]);
+                }
+              }
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (rp[2 * y + e])
+              *reinterpret_cast<uint4*>(rp[2 * y + e] + 32 * xo) =
+                  make_uint4(pack2(c[y][0][2 * e], c[y][0][2 * e + 1]), pack2(c[y][1][2 * e], c[y][1][2 * e + 1]),
+                             pack2(c[y][2][2 * e], c[y][2][2 * e + 1]), pack2(c[y][3][2 * e], c[y][3][2 * e + 1]));
+      }
+    }
+    u += i1 - i0;
+  }
+}
+
+// ---- merge: the diagonal's state, earlier blocks' parts, cached parts; one warp per (token, query head) ----
+constexpr int GT = 256;
+template <int D>
+__global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan pl, const char* __restrict__ ws) {
+  constexpr int V = D / 32;
+  const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (c == 0 && qh == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
+  if (c >= pl.cstart[p.c.slots]) return;
+  const int b = owner(pl.cstart, p.c.slots, c), H = p.c.heads;
+  const SlotSpan sp = pass_span(p, b);
+  const int lc = c - pl.cstart[b], rows = min(C, sp.n - lc * C), h = qh / p.G, g = qh % p.G;
+  const int kt = live_tiles(sp.t0, p.window, p.sinks, kTcKeys).count;
+  const int np = pl.pstart[b + 1] - pl.pstart[b];
+  const long long cached = pl.ustart[p.c.slots], per = units_per_block(pl, p.c.slots);
+  for (int r = warp; r < rows; r += GT / 32) {
+    const size_t row = ((size_t)c * p.hq + qh) * C + r;
+    const int R = (lc * C + r) * p.G + g, pair = R / kTcPair, blk = pair / p.G;
+    const float bias = p.log_f ? ((const float*)(ws + w.cn))[((size_t)h * w.nblk + pl.bstart[b]) * MB + lc * C + r] * kLog2e : 0.f;
+    const long long which = (long long)h * np + pair, item = (long long)pl.pstart[b] * H + which;
+    // parts: [f1, e1] cached, [f2, e2] new
+    long long f1 = 0, e1 = -1, f2 = 0, e2 = -1;
+    if (kt > 0) {
+      const long long us = pl.ustart[b] + which * kt;
+      f1 = us / per;
+      e1 = (us + kt - 1) / per;
+    }
+    if (blk > 0) {
+      const long long us = cached + pl.nstart[b] + h * new_units(np, p.G) + new_units((long long)blk * p.G, p.G) +
+                           (long long)(pair - blk * p.G) * (2 * blk);
+      f2 = us / per;
+      e2 = (us + 2 * blk - 1) / per;
+    }
+    const long long base1 = item, base2 = (long long)H * pl.pairs + item;
+    const int n1 = (int)(e1 - f1 + 1), n2 = (int)(e2 - f2 + 1);
+    auto at = [&](int x) { return (size_t)(x < n1 ? base1 + f1 + x : base2 + f2 + (x - n1)) * kTcPair + R % kTcPair; };
+    const float m0 = ((const float*)(ws + w.m))[row];
+    float M = m0;
+    for (int x = lane; x < n1 + n2; x += 32) M = fmaxf(M, pl.m[at(x)] + bias);
+    M = group_max<32>(M);
+    float f = fast_exp2(m0 - M);
+    float l = ((const float*)(ws + w.l))[row] * f, a[V];
+#pragma unroll
+    for (int y = 0; y < V; ++y) a[y] = ((const float*)(ws + w.acc))[row * D + y * 32 + lane] * f;
+    for (int x = 0; x < n1 + n2; ++x) {
+      const float ms = pl.m[at(x)];
+      if (ms == -INFINITY) continue;
+      f = fast_exp2(ms + bias - M);
+      l += pl.l[at(x)] * f;
+#pragma unroll
+      for (int y = 0; y < V; ++y) a[y] += pl.acc[at(x) * D + y * 32 + lane] * f;
+    }
+    bf16* o = (bf16*)p.o + (((size_t)sp.q0 + lc * C + r) * p.hq + qh) * D;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int y = 0; y < V; ++y) o[y * 32 + lane] = __float2bfloat16_rn(a[y] * inv);
+  }
+}
+
+template <int D>
+cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
+  const NewWs w = new_ws(p);
+  const int H = p.c.heads;
+  const bool fox = p.log_f != nullptr;
+  cudaError_t e;
+  auto prep = prep_kernel<D>;
+  auto c1 = carry_in_block_kernel<D>;
+  auto c2 = carry_kernel<D>;
+  auto qk = fox ? query_kernel<D, true> : query_kernel<D, false>;
+  auto sk = start_kernel<D>;
+  auto rw = rewrite_kernel<D>;
+  const size_t s1 = (size_t)PrepSmem<D>::total * 4, s2 = carry_smem<D>(), s3 = QSmem<D>::bytes;
+  const size_t s4 = (size_t)(2 * D + 64) * (D + 8) * 2, s5 = (size_t)2 * D * (D + 8) * 2;
+  const auto big = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute(prep, big, (int)s1)) != cudaSuccess || (e = cudaFuncSetAttribute(c1, big, (int)s2)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(c2, big, (int)s2)) != cudaSuccess || (e = cudaFuncSetAttribute(qk, big, (int)s3)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(sk, big, (int)s4)) != cudaSuccess || (e = cudaFuncSetAttribute(rw, big, (int)s5)) != cudaSuccess)
+    return e;
+  TcPlan pl{};
+  pl.pairs = w.pairs;
+  pl.blocks = w.nblk;
+  pl.cstart = (int*)(ws + w.cstart);
+  pl.bstart = (int*)(ws + w.bstart);
+  pl.pstart = (int*)(ws + w.pstart);
+  pl.rstart = (int*)(ws + w.rstart);
+  pl.vstart = (long long*)(ws + w.vstart);
+  pl.ustart = (long long*)(ws + w.ustart);
+  pl.nstart = (long long*)(ws + w.nstart);
+  pl.m = (float*)(ws + w.pm);
+  pl.l = (float*)(ws + w.pl);
+  pl.acc = (float*)(ws + w.pacc);
+  pl.cn = (const float*)(ws + w.cn);
+  pl.z = ws + w.z;
+  pl.zs = ws + w.zs;
+  pl.ver = ws + w.ver;
+  pl.ver_rows = w.ver_rows;
+  pl.err = (int*)(ws + w.err);
+  const bool many = p.max_new > MB;  // a slot may have a second block
+  for (p.skip = 0; p.skip < p.max_new; p.skip += kTcPassTokens) {
+    plan_kernel<<<1, 1024, 0, st>>>(p, pl, p.skip == 0);
+    prep<<<dim3(w.nch, H), PT, s1, st>>>(p, w, pl, ws);
+    c1<<<(unsigned)(w.nblk * H * (CPB + D / 64) + (fox ? p.c.slots * H : 0)), WT, s2, st>>>(p, w, pl, ws);
+    qk<<<dim3(w.nch, p.hq), WT, s3, st>>>(p, w, pl, ws);
+    c2<<<dim3(w.nblk, H, CPB + D / 64), WT, s2, st>>>(p, w, pl, ws);
+    if (many) sk<<<dim3(w.pairs * 4, H), WT, s4, st>>>(p, w, pl, ws);
+    if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attend_tc(p, pl, st)) != cudaSuccess) return e;
+    rw<<<152 * (D == 64 ? 2 : 1), RT, s5, st>>>(p, w, pl, ws);
+    merge_kernel<D><<<dim3(w.nch, p.hq), GT, 0, st>>>(p, w, pl, ws);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t paged_new_ws_bytes(const PagedArgs& p) { return new_ws(p).total; }
+cudaError_t launch_paged_new(const PagedArgs& p, char* ws, cudaStream_t st) {
+  return p.c.head_dim == kHeadDim ? new_t<kHeadDim>(p, ws, st) : new_t<kHeadDimWide>(p, ws, st);
+}
+
+}  // namespace pathattn

@@ -51,50 +51,82 @@ struct __align__(1024) TcSmem {
   uint32_t tmem_base;
 };
 
-// A run's share of one query pair.
+// A run's share of one query pair: over cached rows, or over the slot's own earlier blocks.
 struct Segment {
+  bool own;                 // earlier blocks: keys in the version of the pair's block, values as packed
   int b, h, pair, rows;     // rows of the pair (1..256)
-  int i0, i1;               // live key tiles
-  long long item;           // number of the (slot, head, pair)
+  int i0, i1;               // key tiles
+  int t0;                   // rows there are: cached ones, or new ones before the block
+  int base;                 // position of row 0: 0, or that of the first new token
+  long long item, ver;      // number of the item; own: first row of the version
   SlotSpan sp;
   LiveTiles lt;
 };
+__device__ __forceinline__ int find(const long long* start, int slots, long long u) {
+  int lo = 0, hi = slots;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
 // The segment that starts at unit u, and the first unit behind it.
 __device__ __forceinline__ Segment segment_at(const PagedArgs& p, const TcPlan& pl, long long u, long long u1, long long* next) {
   Segment s;
-  int lo = 0, hi = p.c.slots;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pl.ustart[mid] <= u) lo = mid; else hi = mid;
-  }
-  s.b = lo;
-  s.sp = slot_span(p, s.b);  // (a slot with units has tokens)
-  s.lt = live_tiles(s.sp.t0, p.window, p.sinks, KT);
+  const long long cached = pl.ustart[p.c.slots];
+  s.own = u >= cached;
+  s.b = find(s.own ? pl.nstart : pl.ustart, p.c.slots, s.own ? u - cached : u);
+  s.sp = pass_span(p, s.b);
   const int np = pl.pstart[s.b + 1] - pl.pstart[s.b];
-  const long long in = u - pl.ustart[s.b];
-  const int which = (int)(in / s.lt.count);  // (head, pair), head-major
-  s.h = which / np;
-  s.pair = which % np;
-  s.i0 = (int)(in % s.lt.count);
+  int count;
+  if (!s.own) {
+    s.lt = live_tiles(s.sp.t0, p.window, p.sinks, KT);
+    count = s.lt.count;
+    const long long in = u - pl.ustart[s.b];
+    const int which = (int)(in / count);  // (head, pair), head-major
+    s.h = which / np;
+    s.pair = which % np;
+    s.i0 = (int)(in % count);
+    s.t0 = s.sp.t0;
+    s.base = 0;
+    s.ver = 0;
+  } else {
+    const long long each = new_units(np, p.G), in = u - cached - pl.nstart[s.b];
+    s.h = (int)(in / each);
+    long long r = in % each;
+    int m = 1;  // block m: units new_units(m G) and up
+    while ((m + 1) * p.G < np && new_units((long long)(m + 1) * p.G, p.G) <= r) ++m;
+    r -= new_units((long long)m * p.G, p.G);
+    count = 2 * m;
+    s.pair = m * p.G + (int)(r / count);
+    s.i0 = (int)(r % count);
+    s.t0 = m * kTcBlockTokens;
+    s.base = s.sp.t0;
+    s.lt = LiveTiles{count, 0, count};
+    const long long nb = (s.sp.n + kTcBlockTokens - 1) / kTcBlockTokens;
+    s.ver = pl.vstart[s.b] + s.h * (kTcBlockTokens / 2) * nb * (nb - 1) + (long long)(kTcBlockTokens / 2) * m * (m - 1);
+  }
   const long long left = u1 - u;
-  s.i1 = left < s.lt.count - s.i0 ? s.i0 + (int)left : s.lt.count;
+  s.i1 = left < count - s.i0 ? s.i0 + (int)left : count;
   s.rows = min(256, s.sp.n * p.G - s.pair * 256);
-  s.item = (long long)pl.pstart[s.b] * p.c.heads + which;
+  s.item = (long long)pl.pstart[s.b] * p.c.heads + (long long)s.h * np + s.pair + (s.own ? (long long)p.c.heads * pl.pairs : 0);
   *next = u + (s.i1 - s.i0);
   return s;
 }
 
 template <int D, bool FOX>
 __global__ void __launch_bounds__(NTHREADS, 1)
-    attend_tc_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const PagedArgs p, const TcPlan pl) {
+    attend_tc_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_zs,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_ver, const __grid_constant__ CUtensorMap tm_new, const PagedArgs p,
+                     const TcPlan pl) {
   extern __shared__ uint8_t smem_raw[];
   using Smem = TcSmem<D, FOX>;
   constexpr int X = Smem::X, NBUF = Smem::NBUF;
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long units = pl.ustart[p.c.slots];
-  const long long per = (units + gridDim.x - 1) / gridDim.x;
+  const long long units = pl.ustart[p.c.slots] + pl.nstart[p.c.slots];
+  const long long per = units_per_block(pl, p.c.slots);
   const long long u0 = per * blockIdx.x, u1 = u0 + per < units ? u0 + per : units;
   if (u0 >= u1) return;
   if (tid == 0) {
@@ -122,7 +154,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   if (warp == 8) {
     // ---------------- producer: Z once per segment, key and value tiles ----------------
-    const int P = p.c.page_size, RB = P < KT ? P : KT, nl = KT / RB, sub = RB / 16;
+    const int P = p.c.page_size, RB = P < KT ? P : KT, nl = KT / RB;
     int n = 0, kk = 0, seg = 0;  // buffers, key tiles and segments so far
     bool ok = true;
     for (long long u = u0; ok && u < u1;) {
@@ -134,7 +166,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int zr = (g.h * pl.pairs + pl.pstart[g.b] + g.pair) * 256;
         mbar_arrive_expect_tx(&s.z_full, (uint32_t)tiles * X * TILE);
         for (int t = 0; t < tiles; ++t)
-          for (int x = 0; x < X; ++x) tma_load_2d(s.z[t][x], &tm_z, 64 * x, zr + 128 * t, &s.z_full);
+          for (int x = 0; x < X; ++x) tma_load_2d(s.z[t][x], g.own ? &tm_zs : &tm_z, 64 * x, zr + 128 * t, &s.z_full);
       }
       ++seg;
       // the pair's first token sees the farthest back
@@ -143,8 +175,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int j0 = live_tile(g.lt, i) * KT;
         const int j = j0 + 16 * lane;
         int kp = -1, vp = -1;
-        bool here = lane < 8 && j < g.sp.t0 && (p.window <= 0 || j < p.sinks || j + 15 > p_min - p.window);
-        if (here) {
+        bool here = lane < 8 && j < g.t0 &&
+                    (p.window <= 0 || g.base + j < p.sinks || g.base + j + 15 > p_min - p.window);
+        if (here && !g.own) {
           kp = p.c.k_table[(size_t)g.b * p.c.table_width + j / P];
           vp = p.c.v_table[(size_t)g.b * p.c.table_width + j / P];
           if ((unsigned)kp >= (unsigned)p.c.k_pages || (unsigned)vp >= (unsigned)p.c.v_pages) {
@@ -153,9 +186,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
         const uint32_t groups = __ballot_sync(0xffffffffu, here);
-        // lane l brings piece l: the first group of it that is there names the page
-        const uint32_t mine = lane < nl ? (groups >> (lane * sub)) & ((1u << sub) - 1) : 0u;
-        const int from = lane < nl && mine ? lane * sub + __ffs(mine) - 1 : lane;
+        // lane l brings piece l of the tile: a page's rows (the first group that is there names the page), or the
+        // whole tile of an earlier block
+        const int pr = g.own ? KT : RB, pieces = g.own ? 1 : nl, sub = pr / 16;
+        const uint32_t mine = lane < pieces ? (groups >> (lane * sub)) & ((1u << sub) - 1) : 0u;
+        const int from = mine ? lane * sub + __ffs(mine) - 1 : lane;
         kp = __shfl_sync(0xffffffffu, kp, from);
         vp = __shfl_sync(0xffffffffu, vp, from);
         const uint32_t loads = __popc(__ballot_sync(0xffffffffu, mine != 0));
@@ -165,26 +200,32 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!ok) break;
         if (lane == 0) {
           s.okmask[ib] = groups;
-          if (FOX) mbar_arrive_expect_tx(&s.info[ib], loads * RB * 4);
+          if (FOX) mbar_arrive_expect_tx(&s.info[ib], loads * pr * 4);
           else mbar_arrive(&s.info[ib]);
-          mbar_arrive_expect_tx(&s.full[kb], loads * RB * 128 * X);
+          mbar_arrive_expect_tx(&s.full[kb], loads * pr * 128 * X);
         }
         __syncwarp();
         if (mine) {
+          const int y = g.own ? (int)(g.ver + j0) : (kp * p.c.heads + g.h) * P + in;
+          const void* map = g.own ? (const void*)&tm_ver : (const void*)&tm_k;
 #pragma unroll
-          for (int x = 0; x < X; ++x)
-            tma_load_2d(s.buf[kb][x] + lane * RB * 128, &tm_k, 64 * x, (kp * p.c.heads + g.h) * P + in, &s.full[kb]);
-          if (FOX)
-            bulk_load(s.aj[ib] + lane * RB, p.c.a_pool + ((size_t)vp * p.c.heads + g.h) * P + in, RB * 4, &s.info[ib]);
+          for (int x = 0; x < X; ++x) tma_load_2d(s.buf[kb][x] + lane * pr * 128, map, 64 * x, y, &s.full[kb]);
+          if (FOX) {
+            const float* a = g.own ? pl.cn + ((size_t)g.h * pl.blocks + pl.bstart[g.b]) * kTcBlockTokens + j0
+                                   : p.c.a_pool + ((size_t)vp * p.c.heads + g.h) * P + in;
+            bulk_load(s.aj[ib] + lane * pr, a, pr * 4, &s.info[ib]);
+          }
         }
         if (n + 1 >= NBUF) ok = mbar_wait_lean(&s.empty[vb], ((n + 1) / NBUF - 1) & 1, err, 3);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&s.full[vb], loads * RB * 128 * X);
+        if (lane == 0) mbar_arrive_expect_tx(&s.full[vb], loads * pr * 128 * X);
         __syncwarp();
         if (mine) {
+          const int y = g.own ? g.sp.q0 + j0 : (vp * p.c.heads + g.h) * P + in;
+          const void* map = g.own ? (const void*)&tm_new : (const void*)&tm_v;
+          const int x0 = g.own ? g.h * D : 0;
 #pragma unroll
-          for (int x = 0; x < X; ++x)
-            tma_load_2d(s.buf[vb][x] + lane * RB * 128, &tm_v, 64 * x, (vp * p.c.heads + g.h) * P + in, &s.full[vb]);
+          for (int x = 0; x < X; ++x) tma_load_2d(s.buf[vb][x] + lane * pr * 128, map, x0 + 64 * x, y, &s.full[vb]);
         }
         n += 2;
       }
@@ -244,9 +285,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // (the tile's mask: written by the producer before it arrived for the key buffer, which this warp has
         // waited for)
         const uint32_t groups = *reinterpret_cast<volatile uint32_t*>(&s.okmask[kk % NINFO]);
-        if (groups != 0xffu || j0 + KT > g.sp.t0) {
+        if (groups != 0xffu || j0 + KT > g.t0) {
           for (int r = lane >> 3; r < KT; r += 4)
-            if (!(groups >> (r >> 4) & 1) || j0 + r >= g.sp.t0)
+            if (!(groups >> (r >> 4) & 1) || j0 + r >= g.t0)
 #pragma unroll
               for (int x = 0; x < X; ++x) *reinterpret_cast<uint4*>(s.buf[vb][x] + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
@@ -296,7 +337,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // positions of this warp's tile: a tile of keys that all of them see needs no mask
       const int p_max = g.sp.t0 + (g.pair * 256 + 128 * t + 127) / p.G;
       float a_last = 0.f;
-      if (FOX && g.sp.t0 > 0) {
+      if (FOX && !g.own && g.sp.t0 > 0) {  // (own rows: the sums start at 0)
         const long long row = pool_row(p.c, p.c.v_table, p.c.v_pages, g.b, g.h, g.sp.t0 - 1);
         if (row >= 0) a_last = p.c.a_pool[row];
       }
@@ -308,8 +349,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc_fence_after();
         const int j0 = live_tile(g.lt, g.i0 + k) * KT;
         const uint32_t groups = s.okmask[kk % NINFO];
-        const bool mask = groups != 0xffu || j0 + KT > g.sp.t0 ||
-                          (p.window > 0 && j0 + KT > p.sinks && j0 <= p_max - p.window);
+        const bool mask = groups != 0xffu || j0 + KT > g.t0 ||
+                          (p.window > 0 && g.base + j0 + KT > p.sinks && g.base + j0 <= p_max - p.window);
         const bool logd = FOX || mask;  // scores in the log2 domain with biases and hidden ones -inf; else raw
         const float f = logd ? 1.f : p.scl;
         // 32 scores of the row; read twice (maximum, probabilities): TMEM has the room, the registers have not
@@ -326,7 +367,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int jj = 32 * q + j;
-              if (!(groups >> (jj >> 4) & 1) || j0 + jj >= g.sp.t0 || !sees(p.window, p.sinks, pos, j0 + jj))
+              if (!(groups >> (jj >> 4) & 1) || j0 + jj >= g.t0 || !sees(p.window, p.sinks, pos, g.base + j0 + jj))
                 x[j] = 0xff800000u;
             }
           }
@@ -436,12 +477,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// 2-D map over [rows][D] bf16 with 128-byte swizzled boxes of box_rows x 64.
-bool make_map(CUtensorMap* m, const void* base, int D, uint64_t rows, uint32_t box_rows) {
+// 2-D map over `rows` rows of `cols` bf16 with 128-byte swizzled boxes of box_rows x 64.
+bool make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)D, rows};
-  cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * 2};
   cuuint32_t box[2] = {64, box_rows};
   cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
@@ -450,27 +491,31 @@ bool make_map(CUtensorMap* m, const void* base, int D, uint64_t rows, uint32_t b
 }
 
 template <int D, bool FOX>
-cudaError_t attend_t(const PagedArgs& p, const TcPlan& pl, const void* z, cudaStream_t st) {
-  CUtensorMap mz, mk, mv;
+cudaError_t attend_t(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
+  CUtensorMap mz, mzs, mk, mv, mver, mnew;
   const int P = p.c.page_size, RB = P < KT ? P : KT;
-  if (!make_map(&mz, z, D, (uint64_t)p.c.heads * pl.pairs * 256, 128) ||
+  const uint64_t zrows = (uint64_t)p.c.heads * pl.pairs * kTcPair;
+  const bool own = pl.ver_rows > 0;  // (no version rows: no slot has a second block, the maps are not used)
+  if (!make_map(&mz, pl.z, D, zrows, 128) || !make_map(&mzs, pl.zs, D, zrows, 128) ||
       !make_map(&mk, p.c.k_pool, D, (uint64_t)p.c.k_pages * p.c.heads * P, RB) ||
-      !make_map(&mv, p.c.v_pool, D, (uint64_t)p.c.v_pages * p.c.heads * P, RB))
+      !make_map(&mv, p.c.v_pool, D, (uint64_t)p.c.v_pages * p.c.heads * P, RB) ||
+      !make_map(&mver, own ? pl.ver : pl.z, D, own ? (uint64_t)pl.ver_rows : zrows, KT) ||
+      !make_map(&mnew, p.v, (uint64_t)p.c.heads * D, (uint64_t)p.total, KT))
     return cudaErrorInvalidValue;
   auto kern = attend_tc_kernel<D, FOX>;
   const size_t smem = sizeof(TcSmem<D, FOX>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<kTcBlocks, NTHREADS, smem, st>>>(mz, mk, mv, p, pl);
+  kern<<<kTcBlocks, NTHREADS, smem, st>>>(mz, mzs, mk, mv, mver, mnew, p, pl);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attend_tc(const PagedArgs& p, const TcPlan& pl, const void* z, cudaStream_t st) {
+cudaError_t launch_attend_tc(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
   const bool fox = p.log_f != nullptr;
-  if (p.c.head_dim == kHeadDim) return fox ? attend_t<kHeadDim, true>(p, pl, z, st) : attend_t<kHeadDim, false>(p, pl, z, st);
-  return fox ? attend_t<kHeadDimWide, true>(p, pl, z, st) : attend_t<kHeadDimWide, false>(p, pl, z, st);
+  if (p.c.head_dim == kHeadDim) return fox ? attend_t<kHeadDim, true>(p, pl, st) : attend_t<kHeadDim, false>(p, pl, st);
+  return fox ? attend_t<kHeadDimWide, true>(p, pl, st) : attend_t<kHeadDimWide, false>(p, pl, st);
 }
 
 }  // namespace pathattn

@@ -5,19 +5,53 @@
 
 namespace pathattn {
 
-constexpr int kTcKeys = 128;     // cached rows per step
-constexpr int kTcPair = 256;     // query rows of a block: two 128-row tiles
-constexpr int kTcBlocks = 152;   // one persistent block per SM
+constexpr int kTcKeys = 128;         // cached rows per step
+constexpr int kTcPair = 256;         // query rows of a block: two 128-row tiles
+constexpr int kTcBlocks = 152;       // one persistent block per SM
+constexpr int kTcBlockTokens = 256;  // new tokens that share one version of the earlier new keys
+constexpr int kTcPassTokens = 4096;  // new tokens of a slot per pass: bounds the versions (their rows grow with its square)
+constexpr int kRewriteRows = 32;     // cached rows per rewrite tile
 
-// Plan and parts of the tensor-core attention (device pointers into the workspace).
+// Plan, operands and parts of a pass (device pointers into the workspace).  Row i G + g of a (slot, key head)
+// is head g of new token i; 256 rows are a pair, G pairs hold the tokens of a block.
 struct TcPlan {
-  int pairs;                // query pairs that a head's z holds room for (at least those of any legal call)
-  int* pstart;              // [slots + 1]: first query pair of each slot
-  long long* ustart;        // [slots + 1]: first (head, pair, key tile) unit of each slot
-  float *m, *l, *acc;       // parts [heads * pairs + kTcBlocks][256](, [D]): block c's share of item i is part i + c
+  int pairs, blocks;        // query pairs of a head and blocks that the arrays hold
+  int *cstart, *bstart;     // [slots + 1]: first chunk, first block of each slot
+  int *pstart, *rstart;     // first query pair, first rewrite tile
+  long long* vstart;        // first version row
+  long long* ustart;        // first (head, pair, key tile) unit over cached rows; entry `slots`: their number
+  long long* nstart;        // the same over the slot's own earlier blocks; these units follow the cached ones
+  float *m, *l, *acc;       // parts [..][256](, [D]): block c's share of item i is part i + c; items: (slot, head,
+                            // pair) over cached rows, then heads * pairs later over earlier blocks
+  const float* cn;          // sums of log f since the start of the pass [heads][blocks * 256]
+  const void *z, *zs;       // queries at the start of the pass and of their block [heads][pairs][256][D]
+  const void* ver;          // version rows
+  long long ver_rows;
   int* err;                 // first wait that gave up
 };
 
-cudaError_t launch_attend_tc(const PagedArgs& p, const TcPlan& pl, const void* z, cudaStream_t st);
+// Key tiles that the first `pairs` pairs of a slot meet in earlier blocks: a pair of block m meets 2 m.
+PATH_HD long long new_units(long long pairs, int G) {
+  const long long m = pairs / G, rest = pairs % G;
+  return G * m * (m - 1) + 2 * rest * m;
+}
+
+#ifdef __CUDACC__
+// The new tokens of a slot in this pass; slots with fewer than min_new have none.
+__device__ __forceinline__ SlotSpan pass_span(const PagedArgs& p, int b) {
+  SlotSpan s = slot_span(p, b);
+  if (s.n < p.min_new) s.n = 0;
+  const int n = s.n - p.skip;
+  s.q0 += p.skip;
+  s.t0 += p.skip;
+  s.n = n < 0 ? 0 : n < kTcPassTokens ? n : kTcPassTokens;
+  return s;
+}
+__device__ __forceinline__ long long units_per_block(const TcPlan& pl, int slots) {
+  return (pl.ustart[slots] + pl.nstart[slots] + kTcBlocks - 1) / kTcBlocks;
+}
+#endif
+
+cudaError_t launch_attend_tc(const PagedArgs& p, const TcPlan& pl, cudaStream_t st);
 
 }  // namespace pathattn
