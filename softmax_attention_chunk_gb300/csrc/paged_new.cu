@@ -103,7 +103,7 @@ __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.commit_gro
 // ---- workspace ----
 struct NewWs {
   int nch, nblk;           // chunks and blocks of any legal pass
-  size_t cstart, bstart, pstart, ustart, nstart, vstart, rstart;  // plan (TcPlan)
+  size_t cstart, bstart, pstart, ustart, vstart, rstart;  // plan (TcPlan)
   size_t nx, nuw;          // -X [nch][H][64][64], -U W [nch][H][64][D]
   size_t kr, f;            // K-> [2][nch][H][64][D], F [2][nch][H][D][D] (high, rest)
   size_t ke, fb;           // keys at their block's end [2][nblk][H][256][D], block products [2][nblk][H][D][D]
@@ -139,7 +139,6 @@ NewWs new_ws(const PagedArgs& p) {
   w.rstart = take(S1 * 4);
   w.vstart = take(S1 * 8);
   w.ustart = take(S1 * 8);
-  w.nstart = take(S1 * 8);
   w.nx = take((size_t)w.nch * H * C * C * 2);
   w.nuw = take((size_t)w.nch * H * C * D * 2);
   w.kr = take((size_t)2 * w.nch * H * C * D * 2);
@@ -167,7 +166,7 @@ NewWs new_ws(const PagedArgs& p) {
 // ---- plan ----
 // Exclusive prefix sums over the slots, all at once: chunks, blocks, query pairs, rewrite tiles, version rows, units.
 __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool report) {
-  constexpr int N = 7;
+  constexpr int N = 6;
   __shared__ long long wsum[N][32], carry[N];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < N) carry[tid] = 0;
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
   __syncthreads();
   for (int base = 0; base < p.c.slots; base += 1024) {
     const int b = base + tid;
-    long long v[N] = {0, 0, 0, 0, 0, 0, 0}, x[N];
+    long long v[N] = {0, 0, 0, 0, 0, 0}, x[N];
     if (b < p.c.slots) {
       const SlotSpan s = pass_span(p, b);
       if (report && s.code) paged_error(p.c.status, s.code);
@@ -186,8 +185,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
         v[2] = np;
         v[3] = live_tiles(s.t0, p.window, p.sinks, kRewriteRows).count;
         v[4] = H * (MB / 2) * nb * (nb - 1);
-        v[5] = np * H * live_tiles(s.t0, p.window, p.sinks, kTcKeys).count;
-        v[6] = H * new_units(np, p.G);
+        v[5] = H * (np * live_tiles(s.t0, p.window, p.sinks, kTcKeys).count + new_units(np, p.G));
       }
     }
 #pragma unroll
@@ -224,7 +222,6 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
       pl.rstart[b] = (int)e[3];
       pl.vstart[b] = e[4];
       pl.ustart[b] = e[5];
-      pl.nstart[b] = e[6];
     }
     __syncthreads();
   }
@@ -236,7 +233,6 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
     pl.rstart[S] = (int)carry[3];
     pl.vstart[S] = carry[4];
     pl.ustart[S] = carry[5];
-    pl.nstart[S] = carry[6];
   }
 }
 __device__ __forceinline__ int owner(const int* start, int slots, int x) {
@@ -845,26 +841,23 @@ __global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan 
   const int lc = c - pl.cstart[b], rows = min(C, sp.n - lc * C), h = qh / p.G, g = qh % p.G;
   const int kt = live_tiles(sp.t0, p.window, p.sinks, kTcKeys).count;
   const int np = pl.pstart[b + 1] - pl.pstart[b];
-  const long long cached = pl.ustart[p.c.slots], per = units_per_block(pl, p.c.slots);
+  const long long per = units_per_block(pl, p.c.slots);
   for (int r = warp; r < rows; r += GT / 32) {
     const size_t row = ((size_t)c * p.hq + qh) * C + r;
     const int R = (lc * C + r) * p.G + g, pair = R / kTcPair, blk = pair / p.G;
     const float bias = p.log_f ? ((const float*)(ws + w.cn))[((size_t)h * w.nblk + pl.bstart[b]) * MB + lc * C + r] * kLog2e : 0.f;
-    const long long which = (long long)h * np + pair, item = (long long)pl.pstart[b] * H + which;
-    // parts: [f1, e1] cached, [f2, e2] new
+    // the pair's units: cached tiles, then those of earlier blocks; parts [f1, e1] and [f2, e2]
+    const long long us = pl.ustart[b] + h * ((long long)np * kt + new_units(np, p.G)) + (long long)pair * kt + new_units(pair, p.G);
+    const long long base1 = 2 * ((long long)pl.pstart[b] * H + (long long)h * np + pair), base2 = base1 + 1;
     long long f1 = 0, e1 = -1, f2 = 0, e2 = -1;
     if (kt > 0) {
-      const long long us = pl.ustart[b] + which * kt;
       f1 = us / per;
       e1 = (us + kt - 1) / per;
     }
     if (blk > 0) {
-      const long long us = cached + pl.nstart[b] + h * new_units(np, p.G) + new_units((long long)blk * p.G, p.G) +
-                           (long long)(pair - blk * p.G) * (2 * blk);
-      f2 = us / per;
-      e2 = (us + 2 * blk - 1) / per;
+      f2 = (us + kt) / per;
+      e2 = (us + kt + 2 * blk - 1) / per;
     }
-    const long long base1 = item, base2 = (long long)H * pl.pairs + item;
     const int n1 = (int)(e1 - f1 + 1), n2 = (int)(e2 - f2 + 1);
     auto at = [&](int x) { return (size_t)(x < n1 ? base1 + f1 + x : base2 + f2 + (x - n1)) * kTcPair + R % kTcPair; };
     const float m0 = ((const float*)(ws + w.m))[row];
@@ -918,7 +911,6 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
   pl.rstart = (int*)(ws + w.rstart);
   pl.vstart = (long long*)(ws + w.vstart);
   pl.ustart = (long long*)(ws + w.ustart);
-  pl.nstart = (long long*)(ws + w.nstart);
   pl.m = (float*)(ws + w.pm);
   pl.l = (float*)(ws + w.pl);
   pl.acc = (float*)(ws + w.pacc);

@@ -23,6 +23,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 namespace pathattn {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
@@ -62,44 +64,36 @@ struct Segment {
   SlotSpan sp;
   LiveTiles lt;
 };
-__device__ __forceinline__ int find(const long long* start, int slots, long long u) {
-  int lo = 0, hi = slots;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= u) lo = mid; else hi = mid;
-  }
-  return lo;
-}
 // The segment that starts at unit u, and the first unit behind it.
 __device__ __forceinline__ Segment segment_at(const PagedArgs& p, const TcPlan& pl, long long u, long long u1, long long* next) {
   Segment s;
-  const long long cached = pl.ustart[p.c.slots];
-  s.own = u >= cached;
-  s.b = find(s.own ? pl.nstart : pl.ustart, p.c.slots, s.own ? u - cached : u);
+  int lo = 0, hi = p.c.slots;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.ustart[mid] <= u) lo = mid; else hi = mid;
+  }
+  s.b = lo;
   s.sp = pass_span(p, s.b);
-  const int np = pl.pstart[s.b + 1] - pl.pstart[s.b];
-  int count;
+  s.lt = live_tiles(s.sp.t0, p.window, p.sinks, KT);
+  const int np = pl.pstart[s.b + 1] - pl.pstart[s.b], kt = s.lt.count, G = p.G;
+  const long long each = (long long)np * kt + new_units(np, G), in = u - pl.ustart[s.b];
+  s.h = (int)(in / each);
+  long long r = in % each;
+  int m = 0;  // the pair's block: its units start behind those of m G pairs
+  while ((m + 1) * G < np && (long long)(m + 1) * G * kt + new_units((long long)(m + 1) * G, G) <= r) ++m;
+  r -= (long long)m * G * kt + new_units((long long)m * G, G);
+  const int of_pair = kt + 2 * m;
+  s.pair = m * G + (int)(r / of_pair);
+  s.i0 = (int)(r % of_pair);
+  s.own = s.i0 >= kt;
+  int count = kt;
   if (!s.own) {
-    s.lt = live_tiles(s.sp.t0, p.window, p.sinks, KT);
-    count = s.lt.count;
-    const long long in = u - pl.ustart[s.b];
-    const int which = (int)(in / count);  // (head, pair), head-major
-    s.h = which / np;
-    s.pair = which % np;
-    s.i0 = (int)(in % count);
     s.t0 = s.sp.t0;
     s.base = 0;
     s.ver = 0;
   } else {
-    const long long each = new_units(np, p.G), in = u - cached - pl.nstart[s.b];
-    s.h = (int)(in / each);
-    long long r = in % each;
-    int m = 1;  // block m: units new_units(m G) and up
-    while ((m + 1) * p.G < np && new_units((long long)(m + 1) * p.G, p.G) <= r) ++m;
-    r -= new_units((long long)m * p.G, p.G);
+    s.i0 -= kt;
     count = 2 * m;
-    s.pair = m * p.G + (int)(r / count);
-    s.i0 = (int)(r % count);
     s.t0 = m * kTcBlockTokens;
     s.base = s.sp.t0;
     s.lt = LiveTiles{count, 0, count};
@@ -108,8 +102,8 @@ __device__ __forceinline__ Segment segment_at(const PagedArgs& p, const TcPlan& 
   }
   const long long left = u1 - u;
   s.i1 = left < count - s.i0 ? s.i0 + (int)left : count;
-  s.rows = min(256, s.sp.n * p.G - s.pair * 256);
-  s.item = (long long)pl.pstart[s.b] * p.c.heads + (long long)s.h * np + s.pair + (s.own ? (long long)p.c.heads * pl.pairs : 0);
+  s.rows = min(256, s.sp.n * G - s.pair * 256);
+  s.item = 2 * ((long long)pl.pstart[s.b] * p.c.heads + (long long)s.h * np + s.pair) + (s.own ? 1 : 0);
   *next = u + (s.i1 - s.i0);
   return s;
 }
@@ -125,7 +119,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   constexpr int X = Smem::X, NBUF = Smem::NBUF;
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long units = pl.ustart[p.c.slots] + pl.nstart[p.c.slots];
+  const long long units = pl.ustart[p.c.slots];
   const long long per = units_per_block(pl, p.c.slots);
   const long long u0 = per * blockIdx.x, u1 = u0 + per < units ? u0 + per : units;
   if (u0 >= u1) return;
@@ -351,7 +345,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint32_t groups = s.okmask[kk % NINFO];
         const bool mask = groups != 0xffu || j0 + KT > g.t0 ||
                           (p.window > 0 && g.base + j0 + KT > p.sinks && g.base + j0 <= p_max - p.window);
-        const bool logd = FOX || mask;  // scores in the log2 domain with biases and hidden ones -inf; else raw
+        uint64_t acc[2] = {0ull, 0ull};
+        // bits of the keys 32 q .. 32 q + 31 that the row sees: there, and a first token or in the window
+        auto visible = [&](int q) {
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+          const int o = j0 + 32 * q;
+          uint32_t w = below(g.t0 - o);
+          w &= ((groups >> (2 * q) & 1) ? 0xffffu : 0u) | ((groups >> (2 * q + 1) & 1) ? 0xffff0000u : 0u);
+          if (p.window > 0) w &= below(p.sinks - (g.base + o)) | ~below(pos - p.window + 1 - (g.base + o));
+          return w;
+        };
+        // (two instances: the masks of the rare tiles stay out of the others' instructions)
+        auto step = [&](auto masked) {
+        constexpr bool MASK = decltype(masked)::value;
+        constexpr bool logd = FOX || MASK;  // scores in the log2 domain with biases and hidden ones -inf; else raw
         const float f = logd ? 1.f : p.scl;
         // 32 scores of the row; read twice (maximum, probabilities): TMEM has the room, the registers have not
         auto scores = [&](int q, uint32_t (&x)[32]) {
@@ -359,17 +366,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               x[j] = __float_as_uint(fmaf(a_last - s.aj[kk % NINFO][32 * q + j], kLog2e, __uint_as_float(x[j]) * p.scl));
-          } else if (mask) {
+          } else if (MASK) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * p.scl);
           }
-          if (mask) {
+          if (MASK) {
+            const uint32_t w = visible(q);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int jj = 32 * q + j;
-              if (!(groups >> (jj >> 4) & 1) || j0 + jj >= g.t0 || !sees(p.window, p.sinks, pos, g.base + j0 + jj))
-                x[j] = 0xff800000u;
-            }
+            for (int j = 0; j < 32; ++j) x[j] = (w >> j & 1) ? x[j] : 0xff800000u;
           }
         };
         float e0, e1;
@@ -417,7 +421,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
         const float mu = m == -INFINITY ? 0.f : m;
-        uint64_t acc[2] = {0ull, 0ull};
         const uint64_t nm = f2(-mu, -mu), sc = f2(f, f);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -435,6 +438,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           tmem_st16(c_s + 16 * q, pk);  // (over scores that this row has read)
         }
+        };
+        if (mask) step(std::true_type{});
+        else step(std::false_type{});
         float s0, s1, s2, s3;
         f2_split(acc[0], s0, s1);
         f2_split(acc[1], s2, s3);

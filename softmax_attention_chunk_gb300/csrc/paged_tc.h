@@ -19,10 +19,9 @@ struct TcPlan {
   int *cstart, *bstart;     // [slots + 1]: first chunk, first block of each slot
   int *pstart, *rstart;     // first query pair, first rewrite tile
   long long* vstart;        // first version row
-  long long* ustart;        // first (head, pair, key tile) unit over cached rows; entry `slots`: their number
-  long long* nstart;        // the same over the slot's own earlier blocks; these units follow the cached ones
-  float *m, *l, *acc;       // parts [..][256](, [D]): block c's share of item i is part i + c; items: (slot, head,
-                            // pair) over cached rows, then heads * pairs later over earlier blocks
+  long long* ustart;        // first (head, pair, key tile) unit: a pair's cached tiles, then those of earlier blocks
+  float *m, *l, *acc;       // parts [..][256](, [D]): thread block c's share of item i is part i + c; the items of
+                            // query pair x of the list of all (slot, head, pair): 2 x cached, 2 x + 1 own
   const float* cn;          // sums of log f since the start of the pass [heads][blocks * 256]
   const void *z, *zs;       // queries at the start of the pass and of their block [heads][pairs][256][D]
   const void* ver;          // version rows
@@ -48,7 +47,7 @@ __device__ __forceinline__ SlotSpan pass_span(const PagedArgs& p, int b) {
   return s;
 }
 __device__ __forceinline__ long long units_per_block(const TcPlan& pl, int slots) {
-  return (pl.ustart[slots] + pl.nstart[slots] + kTcBlocks - 1) / kTcBlocks;
+  return (pl.ustart[slots] + kTcBlocks - 1) / kTcBlocks;
 }
 #endif
 
