@@ -110,7 +110,8 @@ cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st);
 size_t paged_chunk_ws_bytes(const PagedArgs& p);
 cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st);
 
-// Slots with one new token, bf16.
+// Slots with one new token, bf16; where paged_drafts() holds, all slots of the call.
+bool paged_drafts(const PagedArgs& p);
 size_t paged_token_ws_bytes(const PagedArgs& p);
 cudaError_t launch_paged_token(const PagedArgs& p, char* ws, cudaStream_t st);
 

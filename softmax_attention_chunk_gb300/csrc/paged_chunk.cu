@@ -611,12 +611,12 @@ cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st) {
 
 size_t paged_ws_bytes(const PagedArgs& p) {
   if (p.c.cache_dtype != PATH_BF16) return paged_chunk_ws_bytes(p);
-  return paged_token_ws_bytes(p) + (p.max_new > 1 ? paged_new_ws_bytes(p) : 0);
+  return paged_token_ws_bytes(p) + (p.max_new > 1 && !paged_drafts(p) ? paged_new_ws_bytes(p) : 0);
 }
 cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st) {
   if (p.c.cache_dtype != PATH_BF16) return launch_paged_chunk(p, ws, st);
   const cudaError_t e = launch_paged_token(p, ws, st);
-  if (e != cudaSuccess || p.max_new <= 1) return e;
+  if (e != cudaSuccess || p.max_new <= 1 || paged_drafts(p)) return e;
   PagedArgs more = p;
   more.min_new = 2;
   return launch_paged_new(more, ws + paged_token_ws_bytes(p), st);

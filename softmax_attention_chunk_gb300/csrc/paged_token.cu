@@ -47,7 +47,7 @@ constexpr int blocks_per_sm(int D, int nq8) { return D == 64 ? (nq8 == 1 ? 4 : n
 enum { kOnlyOne = 0, kDrafts = 1 };
 
 template <int D, int NQ8>
-constexpr int frag_words() {  // uint32 per lane of one (slot, head): z high and rest, W, Y high and rest
+__host__ __device__ constexpr int frag_words() {  // uint32 per lane of one (slot, head): z high and rest, W, Y high and rest
   return NQ8 * (D / 8) * 2 + 2 * (D / 8) + 2 * (D / 8) * 2;
 }
 int token_nq(const PagedArgs& p, int n) {  // query columns for slots of at most n tokens
@@ -126,7 +126,8 @@ __device__ __forceinline__ int find_slot(const int* start, int slots, int u) {
   }
   return lo;
 }
-__device__ __forceinline__ int first_unit(int w, int units, int warps) { return (int)((long long)units * w / warps); }
+// Units of a warp's run.
+__device__ __forceinline__ int run_length(int units, int warps) { return (units + warps - 1) / warps; }
 
 __device__ __forceinline__ uint4 ld16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 
@@ -158,7 +159,8 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
     start = (const int*)(ws + w.ustart);
   }
   const int units = start[p.c.slots];
-  const int u0 = first_unit(warp, units, warps), u1 = first_unit(warp + 1, units, warps);
+  const int run = run_length(units, warps);
+  const int u0 = warp * run, u1 = min(u0 + run, units);
   if (u0 >= u1) return;
 
   const __nv_bfloat16* kpool = (const __nv_bfloat16*)p.c.k_pool;
@@ -589,11 +591,233 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
   }
 }
 
-// Merge of the partial states: one block per (slot, head), one warp per query column, runs in list order.
+// ---- draft tokens: the n <= 16 new tokens of a (slot, head) among themselves ----
+// One block each; a few thousand multiply-adds in fp32.  Writes what the streaming warps hold in registers (z, W, -Y
+// in the lane order of their B fragments), the new tokens' own softmax state, and the appended rows.
+constexpr int DT = 128, DN = 16;
+template <int D>
+struct DraftSmem {
+  float w[DN][D + 4], k[DN][D + 4], v[DN][D + 4], y[DN][D + 4];
+  float q[32][D + 4];
+  float g[DN][DN + 1], n[DN][DN + 1], u[DN][DN + 1], x[DN][DN + 1];
+  float m1[32][DN + 1], a[32][DN + 1], s[32][DN + 1];
+  float beta[DN], lf[DN];
+};
+template <int D, bool FOX>
+__global__ void __launch_bounds__(DT) draft_prep_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  DraftSmem<D>& sm = *reinterpret_cast<DraftSmem<D>*>(smem_raw);
+  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, H = p.c.heads, G = p.G;
+  const SlotSpan sp = slot_span(p, b);
+  if (sp.n == 0) return;
+  const int n = sp.n, cols = n * G;
+  const __nv_bfloat16 *gq = (const __nv_bfloat16*)p.q, *gk = (const __nv_bfloat16*)p.k;
+  const __nv_bfloat16 *gv = (const __nv_bfloat16*)p.v, *gw = (const __nv_bfloat16*)p.w;
+  auto row8 = [&](float* dst, const __nv_bfloat16* src) {
+    const uint4 r = ld16(src);
+    const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dst[2 * i] = lo_f(rr[i]);
+      dst[2 * i + 1] = hi_f(rr[i]);
+    }
+  };
+  for (int e = tid; e < DN * (D / 8); e += DT) {
+    const int r = e / (D / 8), x = e % (D / 8) * 8;
+    if (r < n) {
+      const size_t at = (((size_t)sp.q0 + r) * H + h) * D + x;
+      row8(&sm.w[r][x], gw + at);
+      row8(&sm.k[r][x], gk + at);
+      row8(&sm.v[r][x], gv + at);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sm.w[r][x + i] = sm.k[r][x + i] = sm.v[r][x + i] = 0.f;
+    }
+  }
+  for (int e = tid; e < cols * (D / 8); e += DT) {
+    const int r = e / (D / 8), x = e % (D / 8) * 8;
+    row8(&sm.q[r][x], gq + (((size_t)sp.q0 + r / G) * p.hq + h * G + r % G) * D + x);
+  }
+  if (tid < DN) {
+    sm.beta[tid] = tid < n ? clamp_beta(p.beta[((size_t)sp.q0 + tid) * H + h]) : 0.f;
+    float a = 0.f;
+    if (FOX)
+      for (int i = 0; i <= tid && i < n; ++i) a += p.log_f[((size_t)sp.q0 + i) * H + h];
+    sm.lf[tid] = a;
+  }
+  __syncthreads();
+  auto dot = [](const float* a, const float* c) {
+    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < D; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(a + i), y = *reinterpret_cast<const float4*>(c + i);
+      s0 = fmaf(x.x, y.x, s0);
+      s1 = fmaf(x.y, y.y, s1);
+      s2 = fmaf(x.z, y.z, s2);
+      s3 = fmaf(x.w, y.w, s3);
+    }
+    return (s0 + s1) + (s2 + s3);
+  };
+  const int n2 = n * n;
+  for (int e = tid; e < 2 * (n2 + cols * n); e += DT) {  // the four kinds of products of rows
+    if (e < n2) {
+      const int i = e / n, j = e % n;
+      sm.g[i][j] = j < i ? dot(sm.w[i], sm.w[j]) : 0.f;
+    } else if (e < 2 * n2) {
+      const int i = (e - n2) / n, j = (e - n2) % n;
+      sm.n[i][j] = j < i ? dot(sm.w[i], sm.k[j]) : 0.f;
+    } else {
+      const int r = e - 2 * n2, which = r / (cols * n), c = r % (cols * n) / n, j = r % n;
+      const bool in = j <= c / G;
+      if (which == 0) sm.m1[c][j] = in ? dot(sm.q[c], sm.w[j]) : 0.f;
+      else sm.s[c][j] = in ? dot(sm.q[c], sm.k[j]) : 0.f;
+    }
+  }
+  __syncthreads();
+  if (tid < DN) {  // U, one column per lane
+    for (int i = 0; i < n; ++i) {
+      float a = tid == i ? 1.f : 0.f;
+      for (int m = tid; m < i; ++m) a -= sm.g[i][m] * sm.u[m][tid];
+      sm.u[i][tid] = tid <= i ? sm.beta[i] * a : 0.f;
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < n2 + cols * n; e += DT) {
+    if (e < n2) {
+      const int i = e / n, j = e % n;
+      float a = 0.f;
+      for (int m = j + 1; m <= i; ++m) a += sm.u[i][m] * sm.n[m][j];
+      sm.x[i][j] = a;
+    } else {
+      const int c = (e - n2) / n, j = (e - n2) % n;
+      float a = 0.f;
+      for (int m = j; m < n; ++m) a += sm.m1[c][m] * sm.u[m][j];
+      sm.a[c][j] = a;
+    }
+  }
+  __syncthreads();
+  const size_t item = (size_t)b * H + h;
+  // scores of the new tokens among themselves and their softmax: 4 lanes per column
+  {
+    const int c = tid >> 2, sub = tid & 3;
+    const int i = c < cols ? c / G : 0;
+    float s[4], mx = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int j = sub + 4 * x;
+      s[x] = -INFINITY;
+      if (c < cols && j <= i && sees(p.window, p.sinks, sp.t0 + i, sp.t0 + j)) {
+        float v = sm.s[c][j];
+        for (int m = j + 1; m <= i; ++m) v -= sm.a[c][m] * sm.n[m][j];
+        s[x] = v * p.scl + (FOX ? (sm.lf[i] - sm.lf[j]) * kLog2e : 0.f);
+      }
+      mx = fmaxf(mx, s[x]);
+    }
+    mx = group_max<4>(mx);
+    float l = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float e = s[x] == -INFINITY ? 0.f : fast_exp2(s[x] - mx);
+      l += e;
+      s[x] = e;
+    }
+    l = group_sum<4>(l);
+    __syncthreads();
+    if (c < cols) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sm.s[c][sub + 4 * x] = s[x];
+      if (sub == 0) {
+        ((float*)(ws + w.sm))[item * w.nq + c] = mx;
+        ((float*)(ws + w.sl))[item * w.nq + c] = l;
+      }
+    }
+  }
+  // Y = U^T W; z = q - A W over q; the appended keys k - X^T W
+  for (int e = tid; e < DN * D; e += DT) {
+    const int r = e / D, x = e % D;
+    float y = 0.f;
+    for (int m = r; m < n; ++m) y += sm.u[m][r] * sm.w[m][x];
+    sm.y[r][x] = r < n ? y : 0.f;
+    if (r < n) {
+      float kx = sm.k[r][x];
+      for (int m = r + 1; m < n; ++m) kx -= sm.x[m][r] * sm.w[m][x];
+      const long long kr = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0 + r);
+      const long long vr = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r);
+      if (kr < 0 || vr < 0) {
+        if (x == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+      } else {
+        ((__nv_bfloat16*)p.c.k_pool)[kr * D + x] = __float2bfloat16_rn(kx);
+        ((__nv_bfloat16*)p.c.v_pool)[vr * D + x] = __float2bfloat16_rn(sm.v[r][x]);
+        if (FOX && x == 0) {
+          const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
+          p.c.a_pool[vr] = (last >= 0 ? p.c.a_pool[last] : 0.f) + sm.lf[r];
+        }
+      }
+    }
+  }
+  for (int e = tid; e < cols * D; e += DT) {
+    const int c = e / D, x = e % D;
+    float z = sm.q[c][x];
+    for (int m = 0; m <= c / G; ++m) z -= sm.a[c][m] * sm.w[m][x];
+    sm.q[c][x] = z;
+  }
+  __syncthreads();
+  float* sacc = (float*)(ws + w.sacc) + item * w.nq * D;
+  for (int e = tid; e < w.nq * D; e += DT) {
+    const int c = e / D, x = e % D;
+    float a = 0.f;
+    if (c < cols)
+      for (int j = 0; j <= c / G; ++j) a += sm.s[c][j] * sm.v[j][x];
+    sacc[e] = a;
+  }
+  if (tid < w.nq && tid >= cols) {  // columns without a query
+    ((float*)(ws + w.sm))[item * w.nq + tid] = -INFINITY;
+    ((float*)(ws + w.sl))[item * w.nq + tid] = 0.f;
+  }
+  // fragments
+  const int nq8 = w.nq / 8, words = nq8 * (D / 8) * 2 + 2 * (D / 8) + 2 * (D / 8) * 2;
+  uint2* f = reinterpret_cast<uint2*>((uint32_t*)(ws + w.frag) + item * 32 * words);
+  const int lane = tid & 31, g = lane >> 2, t = lane & 3;
+  for (int k = tid >> 5; k < (nq8 + 2) * (D / 16); k += DT / 32) {
+    const int q = k / (D / 16), y = k % (D / 16), d0 = 32 * (y >> 1) + 8 * t + 4 * (y & 1);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (q < nq8) {
+      const int c = 8 * q + g;
+      if (c < cols)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = sm.q[c][d0 + i];
+      uint2 hi, lo;
+      split2(v[0], v[1], hi.x, lo.x);
+      split2(v[2], v[3], hi.y, lo.y);
+      f[((2 * q) * (D / 16) + y) * 32 + lane] = hi;
+      f[((2 * q + 1) * (D / 16) + y) * 32 + lane] = lo;
+    } else {
+      const int r = 8 * (q - nq8) + g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = sm.w[r][d0 + i];
+      f[((2 * nq8 + q - nq8) * (D / 16) + y) * 32 + lane] = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+    }
+  }
+  f += (2 * nq8 + 2) * (D / 16) * 32;
+  for (int k = tid >> 5; k < D / 8; k += DT / 32) {
+    const int d = 32 * (k >> 2) + 8 * (g >> 1) + 2 * (k & 3) + (g & 1);
+    uint2 hi, lo;
+    split2(-sm.y[2 * t][d], -sm.y[2 * t + 1][d], hi.x, lo.x);
+    split2(-sm.y[2 * t + 8][d], -sm.y[2 * t + 9][d], hi.y, lo.y);
+    f[k * 32 + lane] = hi;
+    f[(D / 8 + k) * 32 + lane] = lo;
+  }
+}
+
+// Merge of the partial states: one block per (slot, head).  D / 4 lanes share a query column, groups of lanes the
+// columns, or (few columns) the runs of a column; sums in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(NT) token_merge_kernel(PagedArgs p, TokenWs w, const char* __restrict__ ws, int mode, int warps) {
+  constexpr int L = D / 4, GR = NT / L;
   __shared__ int s_start[kSmemSlots + 1];
-  const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  __shared__ float4 s_acc[GR][L];
+  __shared__ float s_l[GR];
+  const int b = blockIdx.x, h = blockIdx.y, gr = threadIdx.x / L, x = threadIdx.x % L;
   const SlotSpan sp = slot_span(p, b);
   if (sp.n == 0 || (mode == kOnlyOne && sp.n != 1)) return;
   const int* start;
@@ -603,42 +827,54 @@ __global__ void __launch_bounds__(NT) token_merge_kernel(PagedArgs p, TokenWs w,
   } else {
     start = (const int*)(ws + w.ustart);
   }
-  const int units = start[p.c.slots];
-  const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, RT);
-  const int per = lt.count > 0 ? lt.count : 1;
-  const int s0 = start[b] + h * per, e0 = s0 + per;
-  // the runs that hold units s0 and e0 - 1
-  auto run_of = [&](int u) {
-    int r = (int)(((long long)u * warps) / units);
-    while (first_unit(r + 1, units, warps) <= u) ++r;
-    while (first_unit(r, units, warps) > u) --r;
-    return r;
-  };
-  const int ra = run_of(s0), rb = run_of(e0 - 1);
-  if (ra == rb) return;  // written by its run
+  const int run = run_length(start[p.c.slots], warps);
+  const int kt = live_tiles(sp.t0, p.window, p.sinks, RT).count;
+  const int per = kt > 0 ? kt : 1;
+  const int s0 = start[b] + h * per, ra = s0 / run, n = (s0 + per - 1) / run - ra + 1;  // runs that hold the item
+  if (n == 1) return;  // written by its run
   const float *gm = (const float*)(ws + w.m), *gl = (const float*)(ws + w.l), *ga = (const float*)(ws + w.acc);
-  const int lead = first_unit(ra, units, warps) == s0 ? 0 : 1;  // the place of run ra's part
-  for (int col = wid; col < sp.n * p.G; col += WARPS) {
-    auto at = [&](int r) { return ((size_t)2 * r + (r == ra ? lead : 0)) * w.nq + col; };
-    float M = -INFINITY;
-    for (int r = ra + lane; r <= rb; r += 32)
-      if (first_unit(r, units, warps) < first_unit(r + 1, units, warps)) M = fmaxf(M, gm[at(r)]);
-    M = group_max<32>(M);
-    float l = 0.f, a[D / 32];
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x) a[x] = 0.f;
-    for (int r = ra; r <= rb; ++r) {
-      if (first_unit(r, units, warps) >= first_unit(r + 1, units, warps)) continue;  // an empty run
-      const float ms = gm[at(r)];
-      const float f = ms == -INFINITY ? 0.f : fast_exp2(ms - M);
-      l += gl[at(r)] * f;
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) a[x] += ga[at(r) * D + x * 32 + lane] * f;
+  const int lead = ra * run == s0 ? 0 : 1;  // the place of the first run's part
+  const int cols = sp.n * p.G;
+  int cs = 1;
+  while (cs < cols && cs < GR) cs *= 2;
+  for (int c0 = 0; c0 < cols; c0 += cs) {
+    const int col = c0 + gr % cs, pg = gr / cs, pn = GR / cs;
+    auto at = [&](int r) { return ((size_t)2 * (ra + r) + (r == 0 ? lead : 0)) * w.nq + col; };
+    float M = -INFINITY, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < cols)
+      for (int r = x; r < n; r += L) M = fmaxf(M, gm[at(r)]);
+    M = group_max<L>(M);
+    if (col < cols) {
+#pragma unroll 4
+      for (int r = pg; r < n; r += pn) {
+        const float ms = gm[at(r)];
+        const float f = ms == -INFINITY ? 0.f : fast_exp2(ms - M);
+        const float4 v = *reinterpret_cast<const float4*>(ga + at(r) * D + 4 * x);
+        l += gl[at(r)] * f;
+        a.x += v.x * f;
+        a.y += v.y * f;
+        a.z += v.z * f;
+        a.w += v.w * f;
+      }
     }
-    __nv_bfloat16* o = (__nv_bfloat16*)p.o + (((size_t)sp.q0 + col / p.G) * p.hq + h * p.G + col % p.G) * D;
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x) o[x * 32 + lane] = __float2bfloat16_rn(a[x] * inv);
+    __syncthreads();
+    s_acc[gr][x] = a;
+    if (x == 0) s_l[gr] = l;
+    __syncthreads();
+    if (pg == 0 && col < cols) {
+      for (int y = 1; y < pn; ++y) {
+        const float4 v = s_acc[gr + y * cs][x];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+        l += s_l[gr + y * cs];
+      }
+      const float inv = 1.f / l;
+      __nv_bfloat16* o = (__nv_bfloat16*)p.o + (((size_t)sp.q0 + col / p.G) * p.hq + h * p.G + col % p.G) * D + 4 * x;
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack2(a.x * inv, a.y * inv), pack2(a.z * inv, a.w * inv));
+    }
   }
 }
 
@@ -646,23 +882,34 @@ template <int D, int NQ8, bool ONE, bool FOX>
 cudaError_t token_t(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
   const int mode = ONE ? kOnlyOne : kDrafts;
   if (p.c.slots > kSmemSlots) unit_starts_kernel<<<1, 1024, 0, st>>>(p, mode, (int*)(ws + w.ustart));
+  if (!ONE) {
+    auto prep = draft_prep_kernel<D, FOX>;
+    const cudaError_t e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(DraftSmem<D>));
+    if (e != cudaSuccess) return e;
+    prep<<<dim3(p.c.slots, p.c.heads), DT, sizeof(DraftSmem<D>), st>>>(p, w, ws);
+  }
   token_kernel<D, NQ8, ONE, FOX><<<w.blocks, NT, 0, st>>>(p, w, ws);
   token_merge_kernel<D><<<dim3(p.c.slots, p.c.heads), NT, 0, st>>>(p, w, ws, mode, w.blocks * WARPS);
   return cudaGetLastError();
 }
 template <int D, bool FOX>
-cudaError_t token_d(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
-  return w.nq == 8 ? token_t<D, 1, true, FOX>(p, w, ws, st) : token_t<D, 2, true, FOX>(p, w, ws, st);
+cudaError_t token_d(const PagedArgs& p, const TokenWs& w, bool drafts, char* ws, cudaStream_t st) {
+  if (!drafts) return w.nq == 8 ? token_t<D, 1, true, FOX>(p, w, ws, st) : token_t<D, 2, true, FOX>(p, w, ws, st);
+  if (w.nq == 8) return token_t<D, 1, false, FOX>(p, w, ws, st);
+  if (w.nq == 16) return token_t<D, 2, false, FOX>(p, w, ws, st);
+  return token_t<D, 4, false, FOX>(p, w, ws, st);
 }
 
 }  // namespace
 
-size_t paged_token_ws_bytes(const PagedArgs& p) { return token_ws(p, 1).total; }
+bool paged_drafts(const PagedArgs& p) { return p.max_new > 1 && p.max_new <= DN && p.max_new * p.G <= 32; }
+size_t paged_token_ws_bytes(const PagedArgs& p) { return token_ws(p, paged_drafts(p) ? p.max_new : 1).total; }
 cudaError_t launch_paged_token(const PagedArgs& p, char* ws, cudaStream_t st) {
-  const TokenWs w = token_ws(p, 1);
-  const bool fox = p.log_f != nullptr;
-  if (p.c.head_dim == kHeadDim) return fox ? token_d<kHeadDim, true>(p, w, ws, st) : token_d<kHeadDim, false>(p, w, ws, st);
-  return fox ? token_d<kHeadDimWide, true>(p, w, ws, st) : token_d<kHeadDimWide, false>(p, w, ws, st);
+  const bool drafts = paged_drafts(p), fox = p.log_f != nullptr;
+  const TokenWs w = token_ws(p, drafts ? p.max_new : 1);
+  if (p.c.head_dim == kHeadDim)
+    return fox ? token_d<kHeadDim, true>(p, w, drafts, ws, st) : token_d<kHeadDim, false>(p, w, drafts, ws, st);
+  return fox ? token_d<kHeadDimWide, true>(p, w, drafts, ws, st) : token_d<kHeadDimWide, false>(p, w, drafts, ws, st);
 }
 
 }  // namespace pathattn
