@@ -139,10 +139,11 @@ struct State {
   float m[NQ8][2], l[NQ8][2];  // reference (the same in all lanes of a column), this lane's share of the sum
 };
 
-// ONE: every slot of the list has one token.  Otherwise the fragments come from draft_prep_kernel.
-template <int D, int NQ8, bool ONE, bool FOX>
+// NT8 = 0: every slot of the list has one token.  Otherwise NT8 tiles of 8 tokens, fragments from draft_prep_kernel.
+template <int D, int NQ8, int NT8, bool FOX>
 __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
   __shared__ int s_start[kSmemSlots + 1];
+  constexpr bool ONE = NT8 == 0;
   // z in B fragment order: registers where they are few, else one copy per warp in shared memory
   constexpr bool ZS = ONE && (D == 128 || NQ8 > 1);
   __shared__ uint4 s_z[ZS ? WARPS : 1][ZS ? NQ8 * 2 * (D / 32) : 1][32];
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
       const int j0 = live_tile(lt, i) * RT;
       const bool cur = ok;
       if (!cur && lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
-      float s[NQ8][4], c[ONE ? 1 : 2][4];
+      float s[NQ8][4], c[ONE ? 1 : NT8][4];
       // whole: every row of the tile is there, seen by every token and kept
       const bool whole = j0 + RT <= sp.t0 && (p.window <= 0 || j0 > sp.t0 + n - p.window || j0 + RT <= p.sinks);
       const long long kat = krow;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
 #pragma unroll
         for (int q = 0; q < NQ8; ++q) s[q][0] = s[q][1] = s[q][2] = s[q][3] = 0.f;
 #pragma unroll
-        for (int q = 0; q < (ONE ? 1 : 2); ++q) c[q][0] = c[q][1] = c[q][2] = c[q][3] = 0.f;
+        for (int q = 0; q < (ONE ? 1 : NT8); ++q) c[q][0] = c[q][1] = c[q][2] = c[q][3] = 0.f;
 #pragma unroll
         for (int x = 0; x < KB; ++x) {
           const uint32_t r0[4] = {kr[0][x].x, kr[0][x].y, kr[0][x].z, kr[0][x].w};
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
                 mma_bf16(s[q], a0, a1, a2, a3, zlv.x, zlv.y);
               }
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
+              for (int q = 0; q < NT8; ++q) {
                 const uint2 wv = __ldg(f + ((2 * NQ8 + q) * (D / 16) + k) * 32);
                 mma_bf16(c[q], a0, a1, a2, a3, wv.x, wv.y);
               }
@@ -433,11 +434,15 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
             if (keep1) *reinterpret_cast<uint4*>(dst + (size_t)(g + 8) * D + 32 * x) = make_uint4(r1[0], r1[1], r1[2], r1[3]);
           }
         } else {
-          uint32_t ah[4], al[4];  // c as an A fragment over 16 tokens
+          // c as A fragments.  16 tokens: high and rest apart, c Y = ch Yh + cl Yh + ch Yl.  8 tokens: the 16
+          // columns are high and rest, against Yh twice, and high again against Yl
+          uint32_t ah[4], al[4];
           split2(c[0][0], c[0][1], ah[0], al[0]);
           split2(c[0][2], c[0][3], ah[1], al[1]);
-          split2(c[1][0], c[1][1], ah[2], al[2]);
-          split2(c[1][2], c[1][3], ah[3], al[3]);
+          if constexpr (NT8 == 2) {
+            split2(c[1][0], c[1][1], ah[2], al[2]);
+            split2(c[1][2], c[1][3], ah[3], al[3]);
+          }
           const uint2* f = reinterpret_cast<const uint2*>(frag) + (2 * NQ8 + 2) * (D / 16) * 32 + lane;
 #pragma unroll
           for (int x = 0; x < KB; ++x) {
@@ -447,9 +452,14 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
             for (int y = 0; y < 4; ++y) {
               float k4[4] = {lo_f(r0[y]), hi_f(r0[y]), lo_f(r1[y]), hi_f(r1[y])};
               const uint2 yh = __ldg(f + (4 * x + y) * 32), yl = __ldg(f + (D / 8 + 4 * x + y) * 32);  // -Y
-              mma_bf16(k4, ah[0], ah[1], ah[2], ah[3], yh.x, yh.y);
-              mma_bf16(k4, al[0], al[1], al[2], al[3], yh.x, yh.y);
-              mma_bf16(k4, ah[0], ah[1], ah[2], ah[3], yl.x, yl.y);
+              if constexpr (NT8 == 2) {
+                mma_bf16(k4, ah[0], ah[1], ah[2], ah[3], yh.x, yh.y);
+                mma_bf16(k4, al[0], al[1], al[2], al[3], yh.x, yh.y);
+                mma_bf16(k4, ah[0], ah[1], ah[2], ah[3], yl.x, yl.y);
+              } else {
+                mma_bf16(k4, ah[0], ah[1], al[0], al[1], yh.x, yh.x);
+                mma_bf16_k8(k4, ah[0], ah[1], yl.x);
+              }
               r0[y] = pack2(k4[0], k4[1]);
               r1[y] = pack2(k4[2], k4[3]);
             }
@@ -809,20 +819,28 @@ __global__ void __launch_bounds__(DT) draft_prep_kernel(PagedArgs p, TokenWs w, 
   }
 }
 
-// Merge of the partial states: one block per (slot, head).  D / 4 lanes share a query column, groups of lanes the
-// columns, or (few columns) the runs of a column; sums in a fixed order.
+// Merge of the partial states: one block per (slot, head, cs query columns).  D / 4 lanes share a column; groups of
+// lanes take the columns and, where these are few, share the runs of a column; sums in a fixed order.
+constexpr int MT = 256;
+constexpr int merge_columns(int D, int cols) {  // a power of two, at most the groups of a block
+  int cs = 1;
+  while (cs < cols && cs < MT / (D / 4) / 4) cs *= 2;
+  return cs;
+}
 template <int D>
-__global__ void __launch_bounds__(NT) token_merge_kernel(PagedArgs p, TokenWs w, const char* __restrict__ ws, int mode, int warps) {
-  constexpr int L = D / 4, GR = NT / L;
+__global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w, const char* __restrict__ ws, int mode, int warps,
+                                                         int cs) {
+  constexpr int L = D / 4, GR = MT / L;
   __shared__ int s_start[kSmemSlots + 1];
   __shared__ float4 s_acc[GR][L];
   __shared__ float s_l[GR];
   const int b = blockIdx.x, h = blockIdx.y, gr = threadIdx.x / L, x = threadIdx.x % L;
   const SlotSpan sp = slot_span(p, b);
-  if (sp.n == 0 || (mode == kOnlyOne && sp.n != 1)) return;
+  const int cols = sp.n * p.G, c0 = blockIdx.z * cs;
+  if (sp.n == 0 || (mode == kOnlyOne && sp.n != 1) || c0 >= cols) return;
   const int* start;
   if (p.c.slots <= kSmemSlots) {
-    unit_starts<NT>(p, mode, false, s_start);
+    unit_starts<MT>(p, mode, false, s_start);
     start = s_start;
   } else {
     start = (const int*)(ws + w.ustart);
@@ -834,10 +852,7 @@ __global__ void __launch_bounds__(NT) token_merge_kernel(PagedArgs p, TokenWs w,
   if (n == 1) return;  // written by its run
   const float *gm = (const float*)(ws + w.m), *gl = (const float*)(ws + w.l), *ga = (const float*)(ws + w.acc);
   const int lead = ra * run == s0 ? 0 : 1;  // the place of the first run's part
-  const int cols = sp.n * p.G;
-  int cs = 1;
-  while (cs < cols && cs < GR) cs *= 2;
-  for (int c0 = 0; c0 < cols; c0 += cs) {
+  {
     const int col = c0 + gr % cs, pg = gr / cs, pn = GR / cs;
     auto at = [&](int r) { return ((size_t)2 * (ra + r) + (r == 0 ? lead : 0)) * w.nq + col; };
     float M = -INFINITY, l = 0.f;
@@ -858,7 +873,6 @@ __global__ void __launch_bounds__(NT) token_merge_kernel(PagedArgs p, TokenWs w,
         a.w += v.w * f;
       }
     }
-    __syncthreads();
     s_acc[gr][x] = a;
     if (x == 0) s_l[gr] = l;
     __syncthreads();
@@ -878,8 +892,9 @@ __global__ void __launch_bounds__(NT) token_merge_kernel(PagedArgs p, TokenWs w,
   }
 }
 
-template <int D, int NQ8, bool ONE, bool FOX>
+template <int D, int NQ8, int NT8, bool FOX>
 cudaError_t token_t(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
+  constexpr bool ONE = NT8 == 0;
   const int mode = ONE ? kOnlyOne : kDrafts;
   if (p.c.slots > kSmemSlots) unit_starts_kernel<<<1, 1024, 0, st>>>(p, mode, (int*)(ws + w.ustart));
   if (!ONE) {
@@ -888,16 +903,19 @@ cudaError_t token_t(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t
     if (e != cudaSuccess) return e;
     prep<<<dim3(p.c.slots, p.c.heads), DT, sizeof(DraftSmem<D>), st>>>(p, w, ws);
   }
-  token_kernel<D, NQ8, ONE, FOX><<<w.blocks, NT, 0, st>>>(p, w, ws);
-  token_merge_kernel<D><<<dim3(p.c.slots, p.c.heads), NT, 0, st>>>(p, w, ws, mode, w.blocks * WARPS);
+  token_kernel<D, NQ8, NT8, FOX><<<w.blocks, NT, 0, st>>>(p, w, ws);
+  const int cols = (ONE ? 1 : p.max_new) * p.G, cs = merge_columns(D, cols);
+  token_merge_kernel<D><<<dim3(p.c.slots, p.c.heads, (cols + cs - 1) / cs), MT, 0, st>>>(p, w, ws, mode, w.blocks * WARPS, cs);
   return cudaGetLastError();
 }
 template <int D, bool FOX>
 cudaError_t token_d(const PagedArgs& p, const TokenWs& w, bool drafts, char* ws, cudaStream_t st) {
-  if (!drafts) return w.nq == 8 ? token_t<D, 1, true, FOX>(p, w, ws, st) : token_t<D, 2, true, FOX>(p, w, ws, st);
-  if (w.nq == 8) return token_t<D, 1, false, FOX>(p, w, ws, st);
-  if (w.nq == 16) return token_t<D, 2, false, FOX>(p, w, ws, st);
-  return token_t<D, 4, false, FOX>(p, w, ws, st);
+  if (!drafts) return w.nq == 8 ? token_t<D, 1, 0, FOX>(p, w, ws, st) : token_t<D, 2, 0, FOX>(p, w, ws, st);
+  if (p.max_new <= 8) {
+    if (w.nq == 8) return token_t<D, 1, 1, FOX>(p, w, ws, st);
+    return w.nq == 16 ? token_t<D, 2, 1, FOX>(p, w, ws, st) : token_t<D, 4, 1, FOX>(p, w, ws, st);
+  }
+  return w.nq == 16 ? token_t<D, 2, 2, FOX>(p, w, ws, st) : token_t<D, 4, 2, FOX>(p, w, ws, st);
 }
 
 }  // namespace

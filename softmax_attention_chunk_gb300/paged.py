@@ -83,6 +83,8 @@ class PagedCache:
         self.c = pa.path_paged_cache_t(slots, H, d, P, width, kp, vp, pa._DT[k_pool.dtype], p(k_pool), p(v_pool),
                                        p(a_pool), p(k_table), p(v_table), p(seq_len), p(k_ref), p(v_ref),
                                        p(self.status))
+        self._index = self.device.index
+        self._plans = {}
         self._pages_bytes = pa.path_pages_workspace_size(self.c)
         if self._pages_bytes == 0:
             raise ValueError("unsupported cache (head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; sizes in range)")
@@ -113,10 +115,17 @@ class PagedCache:
             raise ValueError(f"without q_start there is one token per slot: {N} tokens for {self.slots} slots")
         if max_new is None:
             max_new = 1 if q_start is None else N
-        desc = pa.path_paged_desc_t(hq, N, int(max_new), float(scale), int(window), int(sinks))
-        n = pa.path_paged_workspace_size(self.c, desc)
-        if n == 0:
-            raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens, window {window}, sinks {sinks}")
+        key = (hq, N, max_new, scale, window, sinks)
+        plan = self._plans.get(key)
+        if plan is None:  # descriptor and workspace size of calls of these sizes
+            desc = pa.path_paged_desc_t(hq, N, int(max_new), float(scale), int(window), int(sinks))
+            n = pa.path_paged_workspace_size(self.c, desc)
+            if n == 0:
+                raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens, window {window}, sinks {sinks}")
+            if len(self._plans) >= 1024:
+                self._plans.clear()
+            plan = self._plans[key] = (desc, n)
+        desc, n = plan
         if out is None:
             out = torch.empty_like(q)
         else:
@@ -126,22 +135,19 @@ class PagedCache:
         if ws is None:
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
         p = pa._p
-        with self._on():
-            rc = pa.path_paged_extend(self.c, desc, p(q_start), p(q), p(k), p(v), p(w), p(beta), p(log_f), p(out),
-                                      p(ws), ws.numel(), pa._stream())
-        pa._check(rc, "path_paged_extend")
+        self._call(pa.path_paged_extend, desc, p(q_start), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
+                   beta.data_ptr(), p(log_f), out.data_ptr(), ws.data_ptr(), ws.numel())
         return out
 
     def advance(self, q_start=None):
         """seq_len grows by the new tokens of an extend with the same q_start."""
         if q_start is not None:
             self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
-        with self._on():
-            pa._check(pa.path_paged_advance(self.c, pa._p(q_start), pa._stream()), "path_paged_advance")
+        self._call(pa.path_paged_advance, pa._p(q_start))
 
     def check(self):
         """Raises RuntimeError with what the device recorded since the last check; synchronises."""
-        with self._on():
+        with torch.cuda.device(self.device):
             rc, code = pa.path_paged_status(self.c, pa._stream())
         if rc != pa.PATH_OK:
             what = CODES.get(code, f"a kernel's bounded wait gave up (code {code})" if code else "")
@@ -181,16 +187,21 @@ class PagedCache:
     # ---- helpers ----
     def _pages(self, name, *args):
         ws = torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
-        with self._on():
-            rc = getattr(pa, "path_pages_" + name)(self.c, *args, pa._p(ws), ws.numel(), pa._stream())
-        pa._check(rc, "path_pages_" + name)
+        self._call(getattr(pa, "path_pages_" + name), *args, ws.data_ptr(), ws.numel())
 
-    def _on(self):
-        return torch.cuda.device(self.device)
+    def _call(self, fn, *args):
+        """fn(cache, *args, stream) on the current stream of the cache's device; raises on a status."""
+        if torch._C._cuda_getDevice() == self._index:  # (as torch.cuda.current_device, without its checks)
+            rc = fn(self.c, *args, torch._C._cuda_getCurrentRawStream(self._index))
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(self.c, *args, pa._stream())
+        if rc != pa.PATH_OK:
+            pa._check(rc, fn.__name__)
 
     def _need(self, t, dtype, shape, name):
-        pa._need(t, dtype, shape, name)
-        if t.device != self.device:
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != self.device:
+            pa._need(t, dtype, shape, name)
             raise ValueError(f"{name} lies on {t.device}, the cache on {self.device}")
 
     def _list(self, t, name):
