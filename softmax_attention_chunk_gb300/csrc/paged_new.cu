@@ -22,7 +22,6 @@
 #include "paged_tc.h"
 #include "dev_common.cuh"
 #include "mma_common.cuh"
-#include "smem_mm.cuh"
 
 namespace pathattn {
 namespace {
@@ -245,47 +244,81 @@ __device__ __forceinline__ int owner(const int* start, int slots, int x) {
 }
 
 // ---- chunk preparation: one block per (chunk, key head) ----
-constexpr int PT = 512;
+// W and K are bf16 as given, so their products are exact up to the fp32 sums; U, N, X, Y enter later products as pairs.
+constexpr int PT = 256;
 template <int D>
 struct PrepSmem {
-  static constexpr int DS = D + 4, BS = C + 4;
-  static constexpr int kW = 0, kK = kW + C * DS, kY = kK + C * DS, kU = kY + C * DS, kG = kU + C * BS, kN = kG + C * BS;
-  static constexpr int kX = kN + C * BS, kBeta = kX + C * BS, total = kBeta + C;
+  static constexpr int LD = D + 8, LX = C + 8;
+  bf16 w[C][LD], k[C][LD], yh[C][LD], yl[C][LD];
+  bf16 uh[C][LX], ul[C][LX], nh[C][LX], nl[C][LX], xh[C][LX], xl[C][LX];
+  float g[C][C + 1], u[C][C + 1], t[32][33];
+  float beta[C];
 };
+// A fragments of the transpose of a tile stored as [k][m] rows.
+template <int KS>
+__device__ __forceinline__ void load_at(uint32_t (&a)[KS][4], const bf16* t, int ld, int m0) {
+  const int lane = threadIdx.x & 31, mat = lane >> 3, row = lane & 7;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) ldm4t(a[k], t + (16 * k + (mat >> 1) * 8 + row) * ld + m0 + (mat & 1) * 8);
+}
+template <int NT>
+__device__ __forceinline__ void zero(float (&c)[NT][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+}
+// Accumulators at (m0, n0) as a pair of bf16 tiles (or, lo null, rounded) with row pitch ld.
+template <int NT>
+__device__ __forceinline__ void put_pair(const float (&c)[NT][4], bf16* hi, bf16* lo, int ld, int m0, int n0) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      uint32_t a, e;
+      split2(c[n][2 * y], c[n][2 * y + 1], a, e);
+      const size_t at = (size_t)(m0 + g + 8 * y) * ld + n0 + 8 * n + 2 * t;
+      *reinterpret_cast<uint32_t*>(hi + at) = a;
+      if (lo) *reinterpret_cast<uint32_t*>(lo + at) = e;
+    }
+}
 template <int D>
 __global__ void __launch_bounds__(PT) prep_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) uint8_t smem[];
   using S = PrepSmem<D>;
-  constexpr int DS = S::DS, BS = S::BS;
-  float *sW = sm + S::kW, *sK = sm + S::kK, *sY = sm + S::kY, *sU = sm + S::kU, *sG = sm + S::kG, *sN = sm + S::kN;
-  float *sX = sm + S::kX, *sBeta = sm + S::kBeta;
-  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, H = p.c.heads;
+  S& s = *reinterpret_cast<S*>(smem);
+  constexpr int LD = S::LD, LX = S::LX;
+  const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.c.heads;
+  const int g = lane >> 2, t = lane & 3;
   if (c >= pl.cstart[p.c.slots]) return;
   const int b = owner(pl.cstart, p.c.slots, c);
   const SlotSpan sp = pass_span(p, b);
   const int r0 = (c - pl.cstart[b]) * C, rows = min(C, sp.n - r0);
   const size_t tok0 = (size_t)sp.q0 + r0;
-  for (int e = tid; e < C * D / 8; e += PT) {
-    const int r = e / (D / 8), x = e % (D / 8) * 8;
-    uint4 a = make_uint4(0, 0, 0, 0), k = a;
-    if (r < rows) {
-      a = *reinterpret_cast<const uint4*>((const bf16*)p.w + ((tok0 + r) * H + h) * D + x);
-      k = *reinterpret_cast<const uint4*>((const bf16*)p.k + ((tok0 + r) * H + h) * D + x);
-    }
-    const uint32_t aa[4] = {a.x, a.y, a.z, a.w}, kk[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sW[r * DS + x + 2 * i] = lo_f(aa[i]);
-      sW[r * DS + x + 2 * i + 1] = hi_f(aa[i]);
-      sK[r * DS + x + 2 * i] = lo_f(kk[i]);
-      sK[r * DS + x + 2 * i + 1] = hi_f(kk[i]);
-    }
-  }
-  if (tid < C) sBeta[tid] = tid < rows ? clamp_beta(p.beta[(tok0 + tid) * H + h]) : 0.f;
+  fetch<D, LD, PT>(&s.w[0][0], (const bf16*)p.w + (tok0 * H + h) * D, (size_t)H * D, C, rows);
+  fetch<D, LD, PT>(&s.k[0][0], (const bf16*)p.k + (tok0 * H + h) * D, (size_t)H * D, C, rows);
+  if (tid < C) s.beta[tid] = tid < rows ? clamp_beta(p.beta[(tok0 + tid) * H + h]) : 0.f;
+  for (int e = tid; e < C * C; e += PT) s.u[e / C][e % C] = 0.f;
+  fetch_wait();
   __syncthreads();
-  smem_mm<C, C, D, false, true, true>(sW, DS, sW, DS, [&](int i, int j, float x) { sG[i * BS + j] = j < i ? x : 0.f; });
-  smem_mm<C, C, D, false, true, true>(sW, DS, sK, DS, [&](int i, int j, float x) { sN[i * BS + j] = j < i ? x : 0.f; });
-  for (int e = tid; e < C * C; e += PT) sU[(e / C) * BS + e % C] = 0.f;
+  const int m0 = (warp & 3) * 16, nh = warp >> 2;  // this warp's 16 rows and column half of a 64-row product
+  {
+    uint32_t a[D / 16][4];
+    float x[4][4], y[4][4];
+    load_a(a, &s.w[0][0], LD, m0);
+    zero(x);
+    zero(y);
+    warp_mm<4, D / 16, false>(x, a, &s.w[32 * nh][0], LD);  // W W^T
+    warp_mm<4, D / 16, false>(y, a, &s.k[32 * nh][0], LD);  // W K^T
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = m0 + g + (e >> 1) * 8, j = 32 * nh + 8 * n + 2 * t + (e & 1);
+        s.g[i][j] = x[n][e];
+        if (j >= i) y[n][e] = 0.f;
+      }
+    put_pair(y, &s.nh[0][0], &s.nl[0][0], LX, m0, 32 * nh);
+  }
   __syncthreads();
   // U, block inversion: the two diagonal 32-row blocks by forward substitution (one warp each, one column per
   // lane), then U21 = -U22 G21 U11
@@ -294,44 +327,122 @@ __global__ void __launch_bounds__(PT) prep_kernel(PagedArgs p, NewWs w, TcPlan p
     float u[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      float a0 = (col == i) ? 1.f : 0.f, a1 = 0.f;
+      float a0 = (col == i) ? 1.f : 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
-      for (int m = 0; m + 1 < i; m += 2) {
-        a0 -= sG[(o + i) * BS + o + m] * u[m];
-        a1 -= sG[(o + i) * BS + o + m + 1] * u[m + 1];
+      for (int m = 0; m < i; ++m) {
+        const float x = s.g[o + i][o + m] * u[m];
+        if ((m & 3) == 0) a0 -= x;
+        else if ((m & 3) == 1) a1 -= x;
+        else if ((m & 3) == 2) a2 -= x;
+        else a3 -= x;
       }
-      if (i & 1) a0 -= sG[(o + i) * BS + o + i - 1] * u[i - 1];
-      u[i] = sBeta[o + i] * (a0 + a1);
+      u[i] = s.beta[o + i] * ((a0 + a1) + (a2 + a3));
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sU[(o + i) * BS + o + col] = u[i];
+    for (int i = 0; i < 32; ++i) s.u[o + i][o + col] = u[i];
   }
   __syncthreads();
-  smem_mm<32, 32, 32, false, false, true>(sG + 32 * BS, BS, sU, BS, [&](int i, int j, float x) { sX[i * BS + j] = x; });
+  const int i4 = tid >> 3, j4 = (tid & 7) * 4;  // one row, four columns per thread of a 32 x 32 product
+  {
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int m = 0; m < 32; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = fmaf(s.g[32 + i4][m], s.u[m][j4 + e], a[e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s.t[i4][j4 + e] = a[e];
+  }
   __syncthreads();
-  smem_mm<32, 32, 32, false, false, true>(sU + 32 * BS + 32, BS, sX, BS,
-                                          [&](int i, int j, float x) { sU[(32 + i) * BS + j] = -x; });
+  {
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int m = 0; m < 32; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = fmaf(s.u[32 + i4][32 + m], s.t[m][j4 + e], a[e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s.u[32 + i4][j4 + e] = -a[e];
+  }
+  __syncthreads();
+  for (int e = tid; e < C * C / 2; e += PT) {
+    const int i = e / (C / 2), j = e % (C / 2) * 2;
+    uint32_t hi, lo;
+    split2(s.u[i][j], s.u[i][j + 1], hi, lo);
+    *reinterpret_cast<uint32_t*>(&s.uh[i][j]) = hi;
+    *reinterpret_cast<uint32_t*>(&s.ul[i][j]) = lo;
+  }
   __syncthreads();
   const size_t cc = (size_t)c * H + h;
-  bf16* nuw = (bf16*)(ws + w.nuw) + cc * C * D;
-  smem_mm<C, C, C, false, false, true>(sU, BS, sN, BS, [&](int i, int j, float x) {
-    sX[i * BS + j] = x;
-    ((bf16*)(ws + w.nx))[cc * C * C + i * C + j] = __float2bfloat16_rn(-x);
-  });
-  smem_mm<C, D, C, false, false, true>(sU, BS, sW, DS, [&](int i, int j, float x) { nuw[i * D + j] = __float2bfloat16_rn(-x); });
-  smem_mm<C, D, C, true, false, true>(sU, BS, sW, DS, [&](int i, int j, float x) { sY[i * DS + j] = x; });
+  constexpr int NH = D / 16;  // 8-column tiles of half a row
+  {
+    uint32_t ah[4][4], al[4][4];
+    load_a(ah, &s.uh[0][0], LX, m0);
+    load_a(al, &s.ul[0][0], LX, m0);
+    float x[4][4];
+    zero(x);
+    warp_mm<4, 4, true>(x, ah, &s.nh[0][32 * nh], LX);  // X = U N
+    warp_mm<4, 4, true>(x, al, &s.nh[0][32 * nh], LX);
+    warp_mm<4, 4, true>(x, ah, &s.nl[0][32 * nh], LX);
+    put_pair(x, &s.xh[0][0], &s.xl[0][0], LX, m0, 32 * nh);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[n][e] = -x[n][e];
+    put_pair(x, (bf16*)(ws + w.nx) + cc * C * C, (bf16*)nullptr, C, m0, 32 * nh);
+    float y[NH][4];
+    zero(y);
+    warp_mm<NH, 4, true>(y, ah, &s.w[0][8 * NH * nh], LD);  // U W
+    warp_mm<NH, 4, true>(y, al, &s.w[0][8 * NH * nh], LD);
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[n][e] = -y[n][e];
+    put_pair(y, (bf16*)(ws + w.nuw) + cc * C * D, (bf16*)nullptr, D, m0, 8 * NH * nh);
+    load_at(ah, &s.uh[0][0], LX, m0);
+    load_at(al, &s.ul[0][0], LX, m0);
+    zero(y);
+    warp_mm<NH, 4, true>(y, ah, &s.w[0][8 * NH * nh], LD);  // Y = U^T W
+    warp_mm<NH, 4, true>(y, al, &s.w[0][8 * NH * nh], LD);
+    put_pair(y, &s.yh[0][0], &s.yl[0][0], LD, m0, 8 * NH * nh);
+  }
   __syncthreads();
-  auto two = [](bf16* hi, bf16* lo, size_t at, float x) {
-    const bf16 a = __float2bfloat16_rn(x);
-    hi[at] = a;
-    lo[at] = __float2bfloat16_rn(x - __bfloat162float(a));
-  };
-  bf16 *krh = (bf16*)(ws + w.kr), *krl = krh + (size_t)w.nch * H * C * D;
-  bf16 *fh = (bf16*)(ws + w.f), *fl = fh + (size_t)w.nch * H * D * D;
-  smem_mm<C, D, C, true, false, true>(sX, BS, sW, DS,
-                                      [&](int j, int n, float x) { two(krh, krl, cc * C * D + j * D + n, sK[j * DS + n] - x); });
-  smem_mm<D, D, C, true, false, true>(sW, DS, sY, DS,
-                                      [&](int n, int k, float x) { two(fh, fl, cc * D * D + n * D + k, (n == k ? 1.f : 0.f) - x); });
+  {
+    uint32_t ah[4][4], al[4][4];
+    load_at(ah, &s.xh[0][0], LX, m0);
+    load_at(al, &s.xl[0][0], LX, m0);
+    float y[NH][4];
+    zero(y);
+    warp_mm<NH, 4, true>(y, ah, &s.w[0][8 * NH * nh], LD);  // X^T W
+    warp_mm<NH, 4, true>(y, al, &s.w[0][8 * NH * nh], LD);
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t kk = *reinterpret_cast<const uint32_t*>(&s.k[m0 + g + 8 * v][8 * NH * nh + 8 * n + 2 * t]);
+        y[n][2 * v] = lo_f(kk) - y[n][2 * v];
+        y[n][2 * v + 1] = hi_f(kk) - y[n][2 * v + 1];
+      }
+    bf16* kr = (bf16*)(ws + w.kr) + cc * C * D;
+    put_pair(y, kr, kr + (size_t)w.nch * H * C * D, D, m0, 8 * NH * nh);
+  }
+  // F = I - W^T Y: D rows over the warps
+  bf16* f = (bf16*)(ws + w.f) + cc * D * D;
+  for (int tile = warp; tile < D / 16 * 2; tile += PT / 32) {
+    const int fm = tile / 2 * 16, fn = tile % 2;
+    uint32_t a[4][4];
+    load_at(a, &s.w[0][0], LD, fm);
+    float y[NH][4];
+    zero(y);
+    warp_mm<NH, 4, true>(y, a, &s.yh[0][8 * NH * fn], LD);
+    warp_mm<NH, 4, true>(y, a, &s.yl[0][8 * NH * fn], LD);
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = fm + g + (e >> 1) * 8, j = 8 * NH * fn + 8 * n + 2 * t + (e & 1);
+        y[n][e] = (i == j ? 1.f : 0.f) - y[n][e];
+      }
+    put_pair(y, f, f + (size_t)w.nch * H * D * D, D, fm, 8 * NH * fn);
+  }
 }
 
 // ---- carried rows ----
@@ -832,54 +943,66 @@ __global__ void __launch_bounds__(RT, D == 64 ? 2 : 1) rewrite_kernel(PagedArgs 
 constexpr int GT = 256;
 template <int D>
 __global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan pl, const char* __restrict__ ws) {
-  constexpr int V = D / 32;
-  const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (c == 0 && qh == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
+  constexpr int L = D / 4, PG = 32 / L;  // lanes of a row; parts summed side by side
+  const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x4 = lane % L * 4, pg = lane / L;
+  if (c == 0 && qh == 0 && blockIdx.z == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
   if (c >= pl.cstart[p.c.slots]) return;
   const int b = owner(pl.cstart, p.c.slots, c), H = p.c.heads;
   const SlotSpan sp = pass_span(p, b);
   const int lc = c - pl.cstart[b], rows = min(C, sp.n - lc * C), h = qh / p.G, g = qh % p.G;
+  const int r = blockIdx.z * (GT / 32) + warp;
+  if (r >= rows) return;
   const int kt = live_tiles(sp.t0, p.window, p.sinks, kTcKeys).count;
   const int np = pl.pstart[b + 1] - pl.pstart[b];
   const long long per = units_per_block(pl, p.c.slots);
-  for (int r = warp; r < rows; r += GT / 32) {
-    const size_t row = ((size_t)c * p.hq + qh) * C + r;
-    const int R = (lc * C + r) * p.G + g, pair = R / kTcPair, blk = pair / p.G;
-    const float bias = p.log_f ? ((const float*)(ws + w.cn))[((size_t)h * w.nblk + pl.bstart[b]) * MB + lc * C + r] * kLog2e : 0.f;
-    // the pair's units: cached tiles, then those of earlier blocks; parts [f1, e1] and [f2, e2]
-    const long long us = pl.ustart[b] + h * ((long long)np * kt + new_units(np, p.G)) + (long long)pair * kt + new_units(pair, p.G);
-    const long long base1 = 2 * ((long long)pl.pstart[b] * H + (long long)h * np + pair), base2 = base1 + 1;
-    long long f1 = 0, e1 = -1, f2 = 0, e2 = -1;
-    if (kt > 0) {
-      f1 = us / per;
-      e1 = (us + kt - 1) / per;
-    }
-    if (blk > 0) {
-      f2 = (us + kt) / per;
-      e2 = (us + kt + 2 * blk - 1) / per;
-    }
-    const int n1 = (int)(e1 - f1 + 1), n2 = (int)(e2 - f2 + 1);
-    auto at = [&](int x) { return (size_t)(x < n1 ? base1 + f1 + x : base2 + f2 + (x - n1)) * kTcPair + R % kTcPair; };
-    const float m0 = ((const float*)(ws + w.m))[row];
-    float M = m0;
-    for (int x = lane; x < n1 + n2; x += 32) M = fmaxf(M, pl.m[at(x)] + bias);
-    M = group_max<32>(M);
-    float f = fast_exp2(m0 - M);
-    float l = ((const float*)(ws + w.l))[row] * f, a[V];
-#pragma unroll
-    for (int y = 0; y < V; ++y) a[y] = ((const float*)(ws + w.acc))[row * D + y * 32 + lane] * f;
-    for (int x = 0; x < n1 + n2; ++x) {
-      const float ms = pl.m[at(x)];
-      if (ms == -INFINITY) continue;
-      f = fast_exp2(ms + bias - M);
-      l += pl.l[at(x)] * f;
-#pragma unroll
-      for (int y = 0; y < V; ++y) a[y] += pl.acc[at(x) * D + y * 32 + lane] * f;
-    }
-    bf16* o = (bf16*)p.o + (((size_t)sp.q0 + lc * C + r) * p.hq + qh) * D;
+  const size_t row = ((size_t)c * p.hq + qh) * C + r;
+  const int R = (lc * C + r) * p.G + g, pair = R / kTcPair, blk = pair / p.G;
+  const float m0 = ((const float*)(ws + w.m))[row];
+  const float4 v0 = *reinterpret_cast<const float4*>((const float*)(ws + w.acc) + row * D + x4);
+  const float bias = p.log_f ? ((const float*)(ws + w.cn))[((size_t)h * w.nblk + pl.bstart[b]) * MB + lc * C + r] * kLog2e : 0.f;
+  // the pair's units: cached tiles, then those of earlier blocks; parts [f1, e1] and [f2, e2]
+  const long long us = pl.ustart[b] + h * ((long long)np * kt + new_units(np, p.G)) + (long long)pair * kt + new_units(pair, p.G);
+  const long long base1 = 2 * ((long long)pl.pstart[b] * H + (long long)h * np + pair), base2 = base1 + 1;
+  long long f1 = 0, e1 = -1, f2 = 0, e2 = -1;
+  if (kt > 0) {
+    f1 = us / per;
+    e1 = (us + kt - 1) / per;
+  }
+  if (blk > 0) {
+    f2 = (us + kt) / per;
+    e2 = (us + kt + 2 * blk - 1) / per;
+  }
+  const int n1 = (int)(e1 - f1 + 1), n = n1 + (int)(e2 - f2 + 1);
+  auto at = [&](int x) { return (size_t)(x < n1 ? base1 + f1 + x : base2 + f2 + (x - n1)) * kTcPair + R % kTcPair; };
+  float M = m0;
+  for (int x = lane; x < n; x += 32) M = fmaxf(M, pl.m[at(x)] + bias);
+  M = group_max<32>(M);
+  float f = pg == 0 ? fast_exp2(m0 - M) : 0.f;
+  float l = ((const float*)(ws + w.l))[row] * f;
+  float4 a = make_float4(v0.x * f, v0.y * f, v0.z * f, v0.w * f);
+#pragma unroll 4
+  for (int x = pg; x < n; x += PG) {
+    const float ms = pl.m[at(x)];
+    const float4 v = *reinterpret_cast<const float4*>(pl.acc + at(x) * D + x4);
+    if (ms == -INFINITY) continue;  // (a part that saw nothing)
+    f = fast_exp2(ms + bias - M);
+    l += pl.l[at(x)] * f;
+    a.x += v.x * f;
+    a.y += v.y * f;
+    a.z += v.z * f;
+    a.w += v.w * f;
+  }
+  if (PG == 2) {
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+    a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
+    a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+  }
+  if (pg == 0) {
     const float inv = 1.f / l;
-#pragma unroll
-    for (int y = 0; y < V; ++y) o[y * 32 + lane] = __float2bfloat16_rn(a[y] * inv);
+    bf16* o = (bf16*)p.o + (((size_t)sp.q0 + lc * C + r) * p.hq + qh) * D + x4;
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack2(a.x * inv, a.y * inv), pack2(a.z * inv, a.w * inv));
   }
 }
 
@@ -895,7 +1018,7 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
   auto qk = fox ? query_kernel<D, true> : query_kernel<D, false>;
   auto sk = start_kernel<D>;
   auto rw = rewrite_kernel<D>;
-  const size_t s1 = (size_t)PrepSmem<D>::total * 4, s2 = carry_smem<D>(), s3 = QSmem<D>::bytes;
+  const size_t s1 = sizeof(PrepSmem<D>), s2 = carry_smem<D>(), s3 = QSmem<D>::bytes;
   const size_t s4 = (size_t)(2 * D + 64) * (D + 8) * 2, s5 = (size_t)2 * D * (D + 8) * 2;
   const auto big = cudaFuncAttributeMaxDynamicSharedMemorySize;
   if ((e = cudaFuncSetAttribute(prep, big, (int)s1)) != cudaSuccess || (e = cudaFuncSetAttribute(c1, big, (int)s2)) != cudaSuccess ||
@@ -930,7 +1053,7 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
     if (many) sk<<<dim3(w.pairs * 4, H), WT, s4, st>>>(p, w, pl, ws);
     if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attend_tc(p, pl, st)) != cudaSuccess) return e;
     rw<<<152 * (D == 64 ? 2 : 1), RT, s5, st>>>(p, w, pl, ws);
-    merge_kernel<D><<<dim3(w.nch, p.hq), GT, 0, st>>>(p, w, pl, ws);
+    merge_kernel<D><<<dim3(w.nch, p.hq, C / (GT / 32)), GT, 0, st>>>(p, w, pl, ws);
   }
   return cudaGetLastError();
 }

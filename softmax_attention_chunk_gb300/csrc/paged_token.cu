@@ -40,8 +40,9 @@ struct TokenWs {
 };
 
 // Blocks per SM: what the registers of the operands in flight (32 at head dim 64, 64 at 128) and of the
-// accumulators (D NQ8 / 4) leave without spills.
-constexpr int blocks_per_sm(int D, int nq8) { return D == 64 ? (nq8 == 1 ? 4 : nq8 == 2 ? 3 : 2) : (nq8 == 1 ? 3 : 2); }
+// accumulators (D NQ8 / 4) leave without spills.  One token, one query column tile, 4 x 32768 rows: head dim 64 with
+// 4 / 3 / 2 blocks 130 / 141 / 172 us, head dim 128 with 2 / 3 blocks 132 / 156 us (floor 120).
+constexpr int blocks_per_sm(int D, int nq8) { return D == 64 ? (nq8 == 1 ? 4 : nq8 == 2 ? 3 : 2) : 2; }
 
 // Which slots the kernels here take: by the tokens of a slot.
 enum { kOnlyOne = 0, kDrafts = 1 };
@@ -79,13 +80,15 @@ TokenWs token_ws(const PagedArgs& p, int n) {
   return w;
 }
 
-// Units of a slot: its live tiles for every head, at least one per head (the new tokens themselves).
+// Units of a (slot, head): kSetup that stand for the time a warp needs to begin it (no work, so that runs over many
+// short sequences are not longer than others), then its live tiles, at least one (the new tokens themselves).
+constexpr int kSetup = 2;
 __device__ __forceinline__ int slot_units(const PagedArgs& p, int b, int mode, bool report) {
   const SlotSpan s = slot_span(p, b);
   if (report && s.code) paged_error(p.c.status, s.code);
   if (s.n == 0 || (mode == kOnlyOne && s.n != 1)) return 0;
   const int nt = live_tiles(s.t0, p.window, p.sinks, RT).count;
-  return (nt > 0 ? nt : 1) * p.c.heads;
+  return (kSetup + (nt > 0 ? nt : 1)) * p.c.heads;
 }
 // First unit of each slot, by the whole block; out may be shared memory.
 template <int THREADS>
@@ -172,10 +175,12 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
     while (start[b + 1] <= u) ++b;  // slots without units are passed over
     const SlotSpan sp = slot_span(p, b);
     const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, RT);
-    const int per = lt.count > 0 ? lt.count : 1;
+    const int per = kSetup + (lt.count > 0 ? lt.count : 1);
     const int h = (u - start[b]) / per;
-    const int s0 = start[b] + h * per;           // the item's first unit
-    const int e0 = s0 + per;                     // and the one behind it
+    const int s0 = start[b] + h * per + kSetup;  // the item's first unit with work
+    const int e0 = s0 + per - kSetup;            // and the one behind it
+    if (u < s0) u = s0;
+    if (u >= u1) break;
     const int ue = e0 < u1 ? e0 : u1;
     const int n = ONE ? 1 : sp.n;
     const int cols = n * G;
@@ -561,7 +566,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
 
     // ---- the item's end or the run's: output, or a partial state ----
     const bool complete = u == s0 && ue == e0;
-    const size_t slot = ((size_t)2 * warp + (u == u0 ? 0 : 1)) * w.nq;
+    const size_t slot = ((size_t)2 * warp + (u0 >= s0 - kSetup ? 0 : 1)) * w.nq;  // the run's first item, or its last
 #pragma unroll
     for (int q = 0; q < NQ8; ++q)
 #pragma unroll
@@ -847,11 +852,11 @@ __global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w,
   }
   const int run = run_length(start[p.c.slots], warps);
   const int kt = live_tiles(sp.t0, p.window, p.sinks, RT).count;
-  const int per = kt > 0 ? kt : 1;
-  const int s0 = start[b] + h * per, ra = s0 / run, n = (s0 + per - 1) / run - ra + 1;  // runs that hold the item
+  const int each = kt > 0 ? kt : 1;
+  const int s0 = start[b] + h * (kSetup + each) + kSetup, ra = s0 / run, n = (s0 + each - 1) / run - ra + 1;  // the item's runs
   if (n == 1) return;  // written by its run
   const float *gm = (const float*)(ws + w.m), *gl = (const float*)(ws + w.l), *ga = (const float*)(ws + w.acc);
-  const int lead = ra * run == s0 ? 0 : 1;  // the place of the first run's part
+  const int lead = ra * run >= s0 - kSetup ? 0 : 1;  // the place of the first run's part
   {
     const int col = c0 + gr % cs, pg = gr / cs, pn = GR / cs;
     auto at = [&](int r) { return ((size_t)2 * (ra + r) + (r == 0 ? lead : 0)) * w.nq + col; };
