@@ -535,10 +535,8 @@ __device__ void carry_in_block(const PagedArgs& p, const NewWs& w, const TcPlan&
 
 // Level 2: through the later blocks of the slot, a copy at every block start; at the end into the pages, or M.
 template <int D>
-__global__ void __launch_bounds__(WT) carry_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  bf16* sm = (bf16*)smem;
-  const int blk = blockIdx.x, h = blockIdx.y, slab = blockIdx.z, H = p.c.heads;
+__device__ void carry_on(const PagedArgs& p, const NewWs& w, const TcPlan& pl, char* ws, bf16* sm, int blk, int h, int slab) {
+  const int H = p.c.heads;
   if (blk >= pl.bstart[p.c.slots]) return;
   const int b = owner(pl.bstart, p.c.slots, blk);
   const SlotSpan sp = pass_span(p, b);
@@ -676,13 +674,22 @@ __device__ __forceinline__ void softmax64(float (&s)[8][4], float (&m)[2], float
   }
   to_a(pa, s);
 }
+// The first thread blocks carry keys on (level 2: the longest chains, and independent of the queries).
 template <int D, bool FOX>
 __global__ void __launch_bounds__(WT) query_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* sm = (bf16*)smem;
   using S = QSmem<D>;
   constexpr int LD = S::LD, LX = S::LX;
-  const int c = blockIdx.x, qh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int slabs = CPB + D / 64, carries = w.nblk * p.c.heads * slabs;
+  if ((int)blockIdx.x < carries) {
+    const int x = blockIdx.x;
+    // slabs of the identity first, then by block: chains fall in length
+    const int per = p.c.heads * slabs;
+    carry_on<D>(p, w, pl, ws, sm, x / per, x % per / slabs, slabs - 1 - x % slabs);
+    return;
+  }
+  const int c = (blockIdx.x - carries) / p.hq, qh = (blockIdx.x - carries) % p.hq, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int H = p.c.heads, G = p.G, h = qh / G;
   if (c >= pl.cstart[p.c.slots]) return;
   const int b = owner(pl.cstart, p.c.slots, c);
@@ -838,107 +845,6 @@ __global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan 
   s.store((bf16*)(ws + w.z) + row * D, nullptr);
 }
 
-// ---- cached rows: k <- k M ----
-// HBM-bound: every warp streams tiles of 32 rows through registers (a lane's 16-byte pieces are A fragments, as in
-// paged_token.cu), M as a bf16 pair in shared memory, its columns permuted inside 32 so that a lane's results
-// are the piece it read.
-constexpr int RT = 256;
-template <int D>
-__global__ void __launch_bounds__(RT, D == 64 ? 2 : 1) rewrite_kernel(PagedArgs p, NewWs w, TcPlan pl, const char* __restrict__ ws) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  bf16* sm = (bf16*)smem;
-  constexpr int LD = D + 8, KB = D / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, H = p.c.heads, P = p.c.page_size;
-  const int mat = lane >> 3, row = lane & 7;
-  // units: (slot, head, tile); a block takes a run, its warps the tiles of one (slot, head) in turn
-  const long long units = (long long)pl.rstart[p.c.slots] * H;
-  const long long per = (units + gridDim.x - 1) / gridDim.x, u0 = per * blockIdx.x, u1 = u0 + per < units ? u0 + per : units;
-  for (long long u = u0; u < u1;) {
-    const int b = owner(pl.rstart, p.c.slots, (int)(u / H));
-    const SlotSpan sp = pass_span(p, b);
-    const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, kRewriteRows);
-    const long long in = u - (long long)pl.rstart[b] * H;
-    const int h = (int)(in / lt.count), i0 = (int)(in % lt.count);
-    const long long left = u1 - u;
-    const int i1 = left < lt.count - i0 ? i0 + (int)left : lt.count;
-    const bf16* mh = (const bf16*)(ws + w.mm) + ((size_t)b * H + h) * D * D;
-    const bf16* ml = mh + (size_t)p.c.slots * H * D * D;
-    __syncthreads();
-    for (int e = tid; e < D * D / 2; e += RT) {
-      const int k = e / (D / 2), d = e % (D / 2) * 2;
-      const int at = k * LD + (d & ~31) + 8 * ((d % 8) / 2) + 2 * ((d % 32) / 8);
-      *reinterpret_cast<uint32_t*>(sm + at) = *reinterpret_cast<const uint32_t*>(mh + k * D + d);
-      *reinterpret_cast<uint32_t*>(sm + D * LD + at) = *reinterpret_cast<const uint32_t*>(ml + k * D + d);
-    }
-    __syncthreads();
-    for (int i = i0 + warp; i < i1; i += RT / 32) {
-      const int j0 = live_tile(lt, i) * kRewriteRows;
-      bf16* rp[4];
-      bool keep[4];
-      uint4 k4[4][KB];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {  // rows g + 8 y
-        const int j = j0 + g + 8 * y;
-        keep[y] = j < sp.t0 && sees(p.window, p.sinks, sp.t0 + sp.n, j);
-        rp[y] = nullptr;
-        if (keep[y]) {
-          const int pg = __ldg(p.c.k_table + (size_t)b * p.c.table_width + j / P);
-          if ((unsigned)pg < (unsigned)p.c.k_pages) rp[y] = (bf16*)p.c.k_pool + (((long long)pg * H + h) * P + j % P) * D + 8 * t;
-          else paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
-        }
-#pragma unroll
-        for (int x = 0; x < KB; ++x) k4[y][x] = rp[y] ? *reinterpret_cast<const uint4*>(rp[y] + 32 * x) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int xo = 0; xo < KB; ++xo) {  // 32 output columns at a time
-        float c[2][4][4];
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int n = 0; n < 4; ++n) c[y][n][0] = c[y][n][1] = c[y][n][2] = c[y][n][3] = 0.f;
-#pragma unroll
-        for (int x = 0; x < KB; ++x) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t a[2][4];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint4 lo = k4[2 * y][x], hi = k4[2 * y + 1][x];
-              a[y][0] = e ? lo.z : lo.x;
-              a[y][1] = e ? hi.z : hi.x;
-              a[y][2] = e ? lo.w : lo.y;
-              a[y][3] = e ? hi.w : hi.y;
-            }
-            // rows of M for the summation order of the pieces: index 2t' + f (+ 8) is column 8 t' + 4 e + f (+ 2)
-            const int kr = 32 * x + 8 * (row >> 1) + 4 * e + (row & 1) + 2 * (mat & 1);
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-              for (int n = 0; n < 4; n += 2) {
-                uint32_t r[4];
-                ldm4t(r, sm + v * D * LD + kr * LD + 32 * xo + 8 * n + (mat >> 1) * 8);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  mma_bf16(c[y][n], a[y][0], a[y][1], a[y][2], a[y][3], r[0], r[1]);
-                  mma_bf16(c[y][n + 1], a[y][0], a[y][1], a[y][2], a[y][3], r[2], r[3]);
-                }
-              }
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (rp[2 * y + e])
-              *reinterpret_cast<uint4*>(rp[2 * y + e] + 32 * xo) =
-                  make_uint4(pack2(c[y][0][2 * e], c[y][0][2 * e + 1]), pack2(c[y][1][2 * e], c[y][1][2 * e + 1]),
-                             pack2(c[y][2][2 * e], c[y][2][2 * e + 1]), pack2(c[y][3][2 * e], c[y][3][2 * e + 1]));
-      }
-    }
-    u += i1 - i0;
-  }
-}
-
 // ---- merge: the diagonal's state, earlier blocks' parts, cached parts; one warp per (token, query head) ----
 constexpr int GT = 256;
 template <int D>
@@ -1014,16 +920,14 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
   cudaError_t e;
   auto prep = prep_kernel<D>;
   auto c1 = carry_in_block_kernel<D>;
-  auto c2 = carry_kernel<D>;
   auto qk = fox ? query_kernel<D, true> : query_kernel<D, false>;
   auto sk = start_kernel<D>;
-  auto rw = rewrite_kernel<D>;
   const size_t s1 = sizeof(PrepSmem<D>), s2 = carry_smem<D>(), s3 = QSmem<D>::bytes;
-  const size_t s4 = (size_t)(2 * D + 64) * (D + 8) * 2, s5 = (size_t)2 * D * (D + 8) * 2;
+  const size_t s4 = (size_t)(2 * D + 64) * (D + 8) * 2;
   const auto big = cudaFuncAttributeMaxDynamicSharedMemorySize;
   if ((e = cudaFuncSetAttribute(prep, big, (int)s1)) != cudaSuccess || (e = cudaFuncSetAttribute(c1, big, (int)s2)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(c2, big, (int)s2)) != cudaSuccess || (e = cudaFuncSetAttribute(qk, big, (int)s3)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(sk, big, (int)s4)) != cudaSuccess || (e = cudaFuncSetAttribute(rw, big, (int)s5)) != cudaSuccess)
+      (e = cudaFuncSetAttribute(qk, big, (int)(s3 > s2 ? s3 : s2))) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(sk, big, (int)s4)) != cudaSuccess)
     return e;
   TcPlan pl{};
   pl.pairs = w.pairs;
@@ -1042,17 +946,17 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
   pl.zs = ws + w.zs;
   pl.ver = ws + w.ver;
   pl.ver_rows = w.ver_rows;
+  pl.mm = ws + w.mm;
   pl.err = (int*)(ws + w.err);
   const bool many = p.max_new > MB;  // a slot may have a second block
   for (p.skip = 0; p.skip < p.max_new; p.skip += kTcPassTokens) {
     plan_kernel<<<1, 1024, 0, st>>>(p, pl, p.skip == 0);
     prep<<<dim3(w.nch, H), PT, s1, st>>>(p, w, pl, ws);
     c1<<<(unsigned)(w.nblk * H * (CPB + D / 64) + (fox ? p.c.slots * H : 0)), WT, s2, st>>>(p, w, pl, ws);
-    qk<<<dim3(w.nch, p.hq), WT, s3, st>>>(p, w, pl, ws);
-    c2<<<dim3(w.nblk, H, CPB + D / 64), WT, s2, st>>>(p, w, pl, ws);
+    qk<<<(unsigned)(w.nblk * H * (CPB + D / 64) + w.nch * p.hq), WT, s3 > s2 ? s3 : s2, st>>>(p, w, pl, ws);
     if (many) sk<<<dim3(w.pairs * 4, H), WT, s4, st>>>(p, w, pl, ws);
     if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attend_tc(p, pl, st)) != cudaSuccess) return e;
-    rw<<<152 * (D == 64 ? 2 : 1), RT, s5, st>>>(p, w, pl, ws);
+    if ((e = launch_rewrite_tc(p, pl, st)) != cudaSuccess) return e;
     merge_kernel<D><<<dim3(w.nch, p.hq, C / (GT / 32)), GT, 0, st>>>(p, w, pl, ws);
   }
   return cudaGetLastError();

@@ -483,6 +483,195 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
+// ---- cached rows: k <- k M ----
+// Bound: HBM (each key read and written once, 4 D bytes) against 2 D^2 multiply-adds per row, M being a bf16 pair
+// (high + rest: the only rounding left is the stored key's).  As warp MMAs these took 88 us for 8 x 32768 rows at
+// head dim 128 where the bytes take 20; tcgen05 has four times their rate.  A persistent block per SM: a tile of 128
+// rows by TMA, K M_high + K M_rest into one of two TMEM accumulators, one thread per row rounds and stores.
+template <int D>
+struct __align__(1024) RewSmem {
+  static constexpr int X = D / 64;
+  static constexpr int NBUF = D == 64 ? 8 : 4;
+  uint8_t m[2][X][D * 128];     // M high, M rest: [D rows][64] per column half
+  uint8_t buf[NBUF][X][TILE];
+  uint64_t full[NBUF], empty[NBUF], m_full, m_empty, acc_full[2], acc_free[2];
+  uint32_t tmem_base;
+};
+struct RewSegment {
+  int b, h, i0, i1;
+  SlotSpan sp;
+  LiveTiles lt;
+};
+__device__ __forceinline__ RewSegment rew_segment(const PagedArgs& p, const TcPlan& pl, long long u, long long u1, long long* next) {
+  RewSegment s;
+  int lo = 0, hi = p.c.slots;
+  const int at = (int)(u / p.c.heads);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.rstart[mid] <= at) lo = mid; else hi = mid;
+  }
+  s.b = lo;
+  s.sp = pass_span(p, s.b);
+  s.lt = live_tiles(s.sp.t0, p.window, p.sinks, kRewriteRows);
+  const long long in = u - (long long)pl.rstart[s.b] * p.c.heads;
+  s.h = (int)(in / s.lt.count);
+  s.i0 = (int)(in % s.lt.count);
+  const long long left = u1 - u;
+  s.i1 = left < s.lt.count - s.i0 ? s.i0 + (int)left : s.lt.count;
+  *next = u + (s.i1 - s.i0);
+  return s;
+}
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    rewrite_tc_kernel(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_k, const PagedArgs p,
+                      const TcPlan pl) {
+  extern __shared__ uint8_t smem_raw[];
+  using Smem = RewSmem<D>;
+  constexpr int X = Smem::X, NBUF = Smem::NBUF;
+  constexpr uint32_t COLS = D == 64 ? 128 : 256;
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = p.c.page_size;
+  const long long units = (long long)pl.rstart[p.c.slots] * p.c.heads, per = (units + gridDim.x - 1) / gridDim.x;
+  const long long u0 = per * blockIdx.x, u1 = u0 + per < units ? u0 + per : units;
+  if (u0 >= u1) return;
+  if (tid == 0) {
+    for (int i = 0; i < NBUF; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    mbar_init(&s.m_full, 1);
+    mbar_init(&s.m_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s.acc_full[t], 1);
+      mbar_init(&s.acc_free[t], 128);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(&s.tmem_base, COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = s.tmem_base;
+  int* err = pl.err;
+  // whether a later token sees row j of the cached rows
+  auto keep = [&](const RewSegment& g, int j) { return j < g.sp.t0 && sees(p.window, p.sinks, g.sp.t0 + g.sp.n, j); };
+
+  if (warp == 8) {
+    const int RB = P < KT ? P : KT, nl = KT / RB;
+    int n = 0, seg = 0;
+    bool ok = true;
+    for (long long u = u0; ok && u < u1; ++seg) {
+      const RewSegment g = rew_segment(p, pl, u, u1, &u);
+      if (seg > 0) ok = mbar_wait_lean(&s.m_empty, (seg - 1) & 1, err, 20);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s.m_full, 2 * X * D * 128);
+        for (int v = 0; v < 2; ++v)
+          for (int x = 0; x < X; ++x)
+            tma_load_2d(s.m[v][x], &tm_m, 64 * x, ((v * p.c.slots + g.b) * p.c.heads + g.h) * D, &s.m_full);
+      }
+      for (int i = g.i0; i < g.i1; ++i, ++n) {
+        const int j = live_tile(g.lt, i) * KT + lane * RB;
+        // a piece comes if its page is there and a row of it is kept (rows of a piece are neighbours: its first tokens,
+        // or its end, are the ones that may still be seen)
+        int kp = -1;
+        if (lane < nl && j < g.sp.t0 && (keep(g, j) || keep(g, min(j + RB, g.sp.t0) - 1))) {
+          kp = p.c.k_table[(size_t)g.b * p.c.table_width + j / P];
+          if ((unsigned)kp >= (unsigned)p.c.k_pages) {
+            kp = -1;
+            paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+          }
+        }
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, kp >= 0));
+        const int kb = n % NBUF;
+        if (n >= NBUF) ok = mbar_wait_lean(&s.empty[kb], (n / NBUF - 1) & 1, err, 21);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&s.full[kb], loads * RB * 128 * X);
+        __syncwarp();
+        if (kp >= 0)
+#pragma unroll
+          for (int x = 0; x < X; ++x)
+            tma_load_2d(s.buf[kb][x] + lane * RB * 128, &tm_k, 64 * x, (kp * p.c.heads + g.h) * P + j % P, &s.full[kb]);
+      }
+    }
+    if (!ok) {  // (bounded: no copy may land once the block has gone)
+      if (seg > 0) mbar_wait_ns(&s.m_full, (seg - 1) & 1, nullptr, 0, 1000000ull);
+      mbar_wait_ns(&s.m_full, seg & 1, nullptr, 0, 1000000ull);
+      for (int i = n > NBUF ? n - NBUF : 0; i <= n; ++i) mbar_wait_ns(&s.full[i % NBUF], (i / NBUF) & 1, nullptr, 0, 1000000ull);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, D, 0, 1);
+      const uint64_t da = sdesc_sw128(smem_u32(s.buf[0][0]), 1024, 16);
+      const uint64_t db = sdesc_sw128(smem_u32(s.m[0][0]), 1024, D * 128);
+      int n = 0, seg = 0;
+      bool ok = true;
+      for (long long u = u0; ok && u < u1; ++seg) {
+        const RewSegment g = rew_segment(p, pl, u, u1, &u);
+        ok = mbar_wait_lean(&s.m_full, seg & 1, err, 22);
+        for (int i = g.i0; ok && i < g.i1; ++i, ++n) {
+          const int kb = n % NBUF, t = n & 1;
+          ok = mbar_wait_lean(&s.full[kb], (n / NBUF) & 1, err, 23);
+          if (ok && n >= 2) ok = mbar_wait_lean(&s.acc_free[t], (n / 2 - 1) & 1, err, 24);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tb + D * t, da + (uint64_t)((kb * X + k / 4) * (TILE / 16) + 2 * (k % 4)),
+                     db + (uint64_t)(v * X * (D * 128 / 16) + 128 * k), idesc, (v | k) ? 1u : 0u);
+          mma_commit(&s.empty[kb]);
+          mma_commit(&s.acc_full[t]);
+        }
+        if (ok) mma_commit(&s.m_empty);
+      }
+    }
+  } else {
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t c_a = tb + ((uint32_t)((warp & 3) * 32) << 16) + D * t;
+    int n = 0;
+    bool ok = true;
+    for (long long u = u0; ok && u < u1;) {
+      const RewSegment g = rew_segment(p, pl, u, u1, &u);
+      for (int i = g.i0; ok && i < g.i1; ++i, ++n) {
+        if ((n & 1) != t) continue;
+        const int j = live_tile(g.lt, i) * KT + r;
+        __nv_bfloat16* dst = nullptr;
+        if (keep(g, j)) {
+          const long long at = pool_row(p.c, p.c.k_table, p.c.k_pages, g.b, g.h, j);
+          if (at >= 0) dst = (__nv_bfloat16*)p.c.k_pool + at * D;
+        }
+        ok = mbar_wait_lean(&s.acc_full[t], (n / 2) & 1, err, 25);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t x[32];
+          tmem_ld32(c_a + 32 * q, x);
+          tmem_ld_wait();
+          if (dst)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<uint4*>(dst + 32 * q + 8 * y) =
+                  make_uint4(pack_bf16(__uint_as_float(x[8 * y]), __uint_as_float(x[8 * y + 1])),
+                             pack_bf16(__uint_as_float(x[8 * y + 2]), __uint_as_float(x[8 * y + 3])),
+                             pack_bf16(__uint_as_float(x[8 * y + 4]), __uint_as_float(x[8 * y + 5])),
+                             pack_bf16(__uint_as_float(x[8 * y + 6]), __uint_as_float(x[8 * y + 7])));
+        }
+        tc_fence_before();
+        mbar_arrive(&s.acc_free[t]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tb, COLS);
+  }
+}
+
 // 2-D map over `rows` rows of `cols` bf16 with 128-byte swizzled boxes of box_rows x 64.
 bool make_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
   auto enc = tensor_map_encoder();
@@ -516,7 +705,26 @@ cudaError_t attend_t(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t rewrite_t(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
+  CUtensorMap mm, mk;
+  const int P = p.c.page_size, RB = P < KT ? P : KT;
+  if (!make_map(&mm, pl.mm, D, (uint64_t)2 * p.c.slots * p.c.heads * D, D) ||
+      !make_map(&mk, p.c.k_pool, D, (uint64_t)p.c.k_pages * p.c.heads * P, RB))
+    return cudaErrorInvalidValue;
+  auto kern = rewrite_tc_kernel<D>;
+  const size_t smem = sizeof(RewSmem<D>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<kTcBlocks, NTHREADS, smem, st>>>(mm, mk, p, pl);
+  return cudaGetLastError();
+}
+
 }  // namespace
+
+cudaError_t launch_rewrite_tc(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
+  return p.c.head_dim == kHeadDim ? rewrite_t<kHeadDim>(p, pl, st) : rewrite_t<kHeadDimWide>(p, pl, st);
+}
 
 cudaError_t launch_attend_tc(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
   const bool fox = p.log_f != nullptr;

@@ -10,7 +10,7 @@ constexpr int kTcPair = 256;         // query rows of a block: two 128-row tiles
 constexpr int kTcBlocks = 152;       // one persistent block per SM
 constexpr int kTcBlockTokens = 256;  // new tokens that share one version of the earlier new keys
 constexpr int kTcPassTokens = 4096;  // new tokens of a slot per pass: bounds the versions (their rows grow with its square)
-constexpr int kRewriteRows = 32;     // cached rows per rewrite tile
+constexpr int kRewriteRows = 128;    // cached rows per rewrite tile
 
 // Plan, operands and parts of a pass (device pointers into the workspace).  Row i G + g of a (slot, key head)
 // is head g of new token i; 256 rows are a pair, G pairs hold the tokens of a block.
@@ -25,6 +25,7 @@ struct TcPlan {
   const float* cn;          // sums of log f since the start of the pass [heads][blocks * 256]
   const void *z, *zs;       // queries at the start of the pass and of their block [heads][pairs][256][D]
   const void* ver;          // version rows
+  const void* mm;           // M: [high, rest][slots][heads][D][D]
   long long ver_rows;
   int* err;                 // first wait that gave up
 };
@@ -51,6 +52,7 @@ __device__ __forceinline__ long long units_per_block(const TcPlan& pl, int slots
 }
 #endif
 
+cudaError_t launch_rewrite_tc(const PagedArgs& p, const TcPlan& pl, cudaStream_t st);
 cudaError_t launch_attend_tc(const PagedArgs& p, const TcPlan& pl, cudaStream_t st);
 
 }  // namespace pathattn
