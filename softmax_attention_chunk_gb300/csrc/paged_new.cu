@@ -249,9 +249,12 @@ constexpr int PT = 256;
 template <int D>
 struct PrepSmem {
   static constexpr int LD = D + 8, LX = C + 8;
-  bf16 w[C][LD], k[C][LD], yh[C][LD], yl[C][LD];
-  bf16 uh[C][LX], ul[C][LX], nh[C][LX], nl[C][LX], xh[C][LX], xl[C][LX];
-  float g[C][C + 1], u[C][C + 1], t[32][33];
+  bf16 w[C][LD], k[C][LD];
+  union {
+    struct { float g[C][C + 1], u[C][C + 1], t[32][33]; };  // until U is split
+    struct { bf16 yh[C][LD], yl[C][LD]; };                   // from then on
+  };
+  bf16 uh[C][LX], ul[C][LX], nh[C][LX], nl[C][LX];           // (X takes the place of N)
   float beta[C];
 };
 // A fragments of the transpose of a tile stored as [k][m] rows.
@@ -282,7 +285,7 @@ __device__ __forceinline__ void put_pair(const float (&c)[NT][4], bf16* hi, bf16
     }
 }
 template <int D>
-__global__ void __launch_bounds__(PT) prep_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+__global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
   extern __shared__ __align__(16) uint8_t smem[];
   using S = PrepSmem<D>;
   S& s = *reinterpret_cast<S*>(smem);
@@ -382,7 +385,8 @@ __global__ void __launch_bounds__(PT) prep_kernel(PagedArgs p, NewWs w, TcPlan p
     warp_mm<4, 4, true>(x, ah, &s.nh[0][32 * nh], LX);  // X = U N
     warp_mm<4, 4, true>(x, al, &s.nh[0][32 * nh], LX);
     warp_mm<4, 4, true>(x, ah, &s.nl[0][32 * nh], LX);
-    put_pair(x, &s.xh[0][0], &s.xl[0][0], LX, m0, 32 * nh);
+    __syncthreads();  // (every warp has read N)
+    put_pair(x, &s.nh[0][0], &s.nl[0][0], LX, m0, 32 * nh);
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -407,8 +411,8 @@ __global__ void __launch_bounds__(PT) prep_kernel(PagedArgs p, NewWs w, TcPlan p
   __syncthreads();
   {
     uint32_t ah[4][4], al[4][4];
-    load_at(ah, &s.xh[0][0], LX, m0);
-    load_at(al, &s.xl[0][0], LX, m0);
+    load_at(ah, &s.nh[0][0], LX, m0);
+    load_at(al, &s.nl[0][0], LX, m0);
     float y[NH][4];
     zero(y);
     warp_mm<NH, 4, true>(y, ah, &s.w[0][8 * NH * nh], LD);  // X^T W
@@ -676,7 +680,7 @@ __device__ __forceinline__ void softmax64(float (&s)[8][4], float (&m)[2], float
 }
 // The first thread blocks carry keys on (level 2: the longest chains, and independent of the queries).
 template <int D, bool FOX>
-__global__ void __launch_bounds__(WT) query_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+__global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* sm = (bf16*)smem;
   using S = QSmem<D>;
@@ -851,64 +855,73 @@ template <int D>
 __global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan pl, const char* __restrict__ ws) {
   constexpr int L = D / 4, PG = 32 / L;  // lanes of a row; parts summed side by side
   const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x4 = lane % L * 4, pg = lane / L;
-  if (c == 0 && qh == 0 && blockIdx.z == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
+  if (c == 0 && qh == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
   if (c >= pl.cstart[p.c.slots]) return;
   const int b = owner(pl.cstart, p.c.slots, c), H = p.c.heads;
   const SlotSpan sp = pass_span(p, b);
   const int lc = c - pl.cstart[b], rows = min(C, sp.n - lc * C), h = qh / p.G, g = qh % p.G;
-  const int r = blockIdx.z * (GT / 32) + warp;
-  if (r >= rows) return;
   const int kt = live_tiles(sp.t0, p.window, p.sinks, kTcKeys).count;
   const int np = pl.pstart[b + 1] - pl.pstart[b];
   const long long per = units_per_block(pl, p.c.slots);
-  const size_t row = ((size_t)c * p.hq + qh) * C + r;
-  const int R = (lc * C + r) * p.G + g, pair = R / kTcPair, blk = pair / p.G;
-  const float m0 = ((const float*)(ws + w.m))[row];
-  const float4 v0 = *reinterpret_cast<const float4*>((const float*)(ws + w.acc) + row * D + x4);
-  const float bias = p.log_f ? ((const float*)(ws + w.cn))[((size_t)h * w.nblk + pl.bstart[b]) * MB + lc * C + r] * kLog2e : 0.f;
-  // the pair's units: cached tiles, then those of earlier blocks; parts [f1, e1] and [f2, e2]
-  const long long us = pl.ustart[b] + h * ((long long)np * kt + new_units(np, p.G)) + (long long)pair * kt + new_units(pair, p.G);
-  const long long base1 = 2 * ((long long)pl.pstart[b] * H + (long long)h * np + pair), base2 = base1 + 1;
-  long long f1 = 0, e1 = -1, f2 = 0, e2 = -1;
-  if (kt > 0) {
-    f1 = us / per;
-    e1 = (us + kt - 1) / per;
-  }
-  if (blk > 0) {
-    f2 = (us + kt) / per;
-    e2 = (us + kt + 2 * blk - 1) / per;
-  }
-  const int n1 = (int)(e1 - f1 + 1), n = n1 + (int)(e2 - f2 + 1);
-  auto at = [&](int x) { return (size_t)(x < n1 ? base1 + f1 + x : base2 + f2 + (x - n1)) * kTcPair + R % kTcPair; };
-  float M = m0;
-  for (int x = lane; x < n; x += 32) M = fmaxf(M, pl.m[at(x)] + bias);
-  M = group_max<32>(M);
-  float f = pg == 0 ? fast_exp2(m0 - M) : 0.f;
-  float l = ((const float*)(ws + w.l))[row] * f;
-  float4 a = make_float4(v0.x * f, v0.y * f, v0.z * f, v0.w * f);
+  const long long head = pl.ustart[b] + h * ((long long)np * kt + new_units(np, p.G));
+  const float* cn = (const float*)(ws + w.cn) + ((size_t)h * w.nblk + pl.bstart[b]) * MB + lc * C;
+  int pair = -1, n1 = 0, n = 0;
+  long long from1 = 0, from2 = 0;
+#pragma unroll 2
+  for (int r = warp; r < rows; r += GT / 32) {
+    const size_t row = ((size_t)c * p.hq + qh) * C + r;
+    const int R = (lc * C + r) * p.G + g;
+    const float m0 = ((const float*)(ws + w.m))[row], l0 = ((const float*)(ws + w.l))[row];
+    const float4 v0 = *reinterpret_cast<const float4*>((const float*)(ws + w.acc) + row * D + x4);
+    const float bias = p.log_f ? cn[r] * kLog2e : 0.f;
+    if (R / kTcPair != pair) {  // the pair's units: cached tiles, then those of earlier blocks; their parts
+      pair = R / kTcPair;
+      const int blk = pair / p.G;
+      const long long us = head + (long long)pair * kt + new_units(pair, p.G);
+      from1 = from2 = 2 * ((long long)pl.pstart[b] * H + (long long)h * np + pair);
+      n1 = n = 0;
+      if (kt > 0) {
+        const long long f = us / per;
+        n = n1 = (int)((us + kt - 1) / per - f + 1);
+        from1 += f;
+      }
+      if (blk > 0) {
+        const long long f = (us + kt) / per;
+        n += (int)((us + kt + 2 * blk - 1) / per - f + 1);
+        from2 += f + 1 - n1;
+      }
+    }
+    auto at = [&](int x) { return (size_t)((x < n1 ? from1 : from2) + x) * kTcPair + R % kTcPair; };
+    float M = m0;
+    for (int x = lane; x < n; x += 32) M = fmaxf(M, pl.m[at(x)] + bias);
+    M = group_max<32>(M);
+    float f = pg == 0 ? fast_exp2(m0 - M) : 0.f;
+    float l = l0 * f;
+    float4 a = make_float4(v0.x * f, v0.y * f, v0.z * f, v0.w * f);
 #pragma unroll 4
-  for (int x = pg; x < n; x += PG) {
-    const float ms = pl.m[at(x)];
-    const float4 v = *reinterpret_cast<const float4*>(pl.acc + at(x) * D + x4);
-    if (ms == -INFINITY) continue;  // (a part that saw nothing)
-    f = fast_exp2(ms + bias - M);
-    l += pl.l[at(x)] * f;
-    a.x += v.x * f;
-    a.y += v.y * f;
-    a.z += v.z * f;
-    a.w += v.w * f;
-  }
-  if (PG == 2) {
-    l += __shfl_xor_sync(0xffffffffu, l, 16);
-    a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
-    a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
-    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
-    a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
-  }
-  if (pg == 0) {
-    const float inv = 1.f / l;
-    bf16* o = (bf16*)p.o + (((size_t)sp.q0 + lc * C + r) * p.hq + qh) * D + x4;
-    *reinterpret_cast<uint2*>(o) = make_uint2(pack2(a.x * inv, a.y * inv), pack2(a.z * inv, a.w * inv));
+    for (int x = pg; x < n; x += PG) {
+      const float ms = pl.m[at(x)];
+      const float4 v = *reinterpret_cast<const float4*>(pl.acc + at(x) * D + x4);
+      if (ms == -INFINITY) continue;  // (a part that saw nothing)
+      f = fast_exp2(ms + bias - M);
+      l += pl.l[at(x)] * f;
+      a.x += v.x * f;
+      a.y += v.y * f;
+      a.z += v.z * f;
+      a.w += v.w * f;
+    }
+    if (PG == 2) {
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+      a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+      a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
+      a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+    }
+    if (pg == 0) {
+      const float inv = 1.f / l;
+      bf16* o = (bf16*)p.o + (((size_t)sp.q0 + lc * C + r) * p.hq + qh) * D + x4;
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack2(a.x * inv, a.y * inv), pack2(a.z * inv, a.w * inv));
+    }
   }
 }
 
@@ -957,7 +970,7 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
     if (many) sk<<<dim3(w.pairs * 4, H), WT, s4, st>>>(p, w, pl, ws);
     if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attend_tc(p, pl, st)) != cudaSuccess) return e;
     if ((e = launch_rewrite_tc(p, pl, st)) != cudaSuccess) return e;
-    merge_kernel<D><<<dim3(w.nch, p.hq, C / (GT / 32)), GT, 0, st>>>(p, w, pl, ws);
+    merge_kernel<D><<<dim3(w.nch, p.hq), GT, 0, st>>>(p, w, pl, ws);
   }
   return cudaGetLastError();
 }

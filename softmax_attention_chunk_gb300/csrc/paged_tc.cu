@@ -46,6 +46,7 @@ struct __align__(1024) TcSmem {
   uint8_t z[2][X][TILE];
   uint8_t buf[NBUF][X][TILE];
   float aj[FOX ? NINFO : 1][FOX ? KT : 1];  // forget gate: running sums of the tile's rows
+  alignas(16) float kbias[FOX ? 2 : 1][FOX ? 2 : 1][FOX ? KT : 4];  // the softmax threads' key biases (log2 units)
   uint32_t okmask[NINFO];       // 16-row groups of the tile that are there
   uint64_t info[NINFO];
   uint64_t full[NBUF], empty[NBUF];
@@ -319,7 +320,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t c_s = tb + lane_off + COL_S + 128 * t, c_o = tb + lane_off + COL_O + D * t;
     int kk = 0, ns = 0, os = 0;
     bool ok = true;
-    for (long long u = u0; ok && u < u1;) {
+    // (with the forget gate the tile's threads meet at a barrier every step: after a wait has given up they all walk
+    // on to the end, without further waits)
+    for (long long u = u0; (FOX || ok) && u < u1;) {
       const Segment g = segment_at(p, pl, u, u1, &u);
       const int nk = g.i1 - g.i0;
       if (t == 1 && g.rows <= 128) {  // no second tile
@@ -336,16 +339,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (row >= 0) a_last = p.c.a_pool[row];
       }
       float m = -INFINITY, l = 0.f;
-      for (int k = 0; ok && k < nk; ++k, ++kk, ++ns) {
+      for (int k = 0; (FOX || ok) && k < nk; ++k, ++kk, ++ns) {
         // (the scores first: with them the producer is known to be at most one phase of `info` ahead)
-        ok = mbar_wait_lean(&s.s_full[t], ns & 1, err, 10) && mbar_wait_lean(&s.info[kk % NINFO], (kk / NINFO) & 1, err, 11);
-        if (!ok) break;
+        ok = ok && mbar_wait_lean(&s.s_full[t], ns & 1, err, 10) && mbar_wait_lean(&s.info[kk % NINFO], (kk / NINFO) & 1, err, 11);
+        if (!FOX && !ok) break;
         tc_fence_after();
         const int j0 = live_tile(g.lt, g.i0 + k) * KT;
         const uint32_t groups = s.okmask[kk % NINFO];
         const bool mask = groups != 0xffu || j0 + KT > g.t0 ||
                           (p.window > 0 && g.base + j0 + KT > p.sinks && g.base + j0 <= p_max - p.window);
-        uint64_t acc[2] = {0ull, 0ull};
+        // forget gate: the keys' biases, one per thread of the tile, doubly buffered by the barrier of the next step
+        float* kb = s.kbias[FOX ? t : 0][FOX ? (ns & 1) : 0];
+        if (FOX) {
+          kb[r] = (a_last - s.aj[kk % NINFO][r]) * kLog2e;
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+        }
         // bits of the keys 32 q .. 32 q + 31 that the row sees: there, and a first token or in the window
         auto visible = [&](int q) {
           auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
@@ -355,104 +363,107 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (p.window > 0) w &= below(p.sinks - (g.base + o)) | ~below(pos - p.window + 1 - (g.base + o));
           return w;
         };
-        // (two instances: the masks of the rare tiles stay out of the others' instructions)
+        // One pass over the scores with the reference as it stands: probabilities (kept in registers, the scores stay
+        // in TMEM), row sum and maximum.  Where a score exceeds the reference by more than 2^8 (the first tile, and
+        // rarely later), the reference moves, O is rescaled and the pass is taken again.  (Two instances: the masks of
+        // the rare tiles stay out of the others' instructions.)
+        uint32_t pk[64];
+        float sum = 0.f;
         auto step = [&](auto masked) {
-        constexpr bool MASK = decltype(masked)::value;
-        constexpr bool logd = FOX || MASK;  // scores in the log2 domain with biases and hidden ones -inf; else raw
-        const float f = logd ? 1.f : p.scl;
-        // 32 scores of the row; read twice (maximum, probabilities): TMEM has the room, the registers have not
-        auto scores = [&](int q, uint32_t (&x)[32]) {
-          if (FOX) {
+          constexpr bool MASK = decltype(masked)::value;
+          constexpr bool logd = FOX || MASK;  // scores in the log2 domain with biases and hidden ones -inf; else raw
+          const float f = logd ? 1.f : p.scl;
+          const bool low = !logd && p.scl < 0.f;  // the largest exponent is the smallest score
+          for (int pass = 0; pass < 2; ++pass) {
+            float e0, e1;
+            e0 = e1 = low ? INFINITY : -INFINITY;
+            const float mu = m == -INFINITY ? 0.f : m;
+            uint64_t acc[2] = {0ull, 0ull};
+            const uint64_t nm = f2(-mu, -mu), sc = f2(f, f), scl2 = f2(p.scl, p.scl);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              x[j] = __float_as_uint(fmaf(a_last - s.aj[kk % NINFO][32 * q + j], kLog2e, __uint_as_float(x[j]) * p.scl));
-          } else if (MASK) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * p.scl);
-          }
-          if (MASK) {
-            const uint32_t w = visible(q);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = (w >> j & 1) ? x[j] : 0xff800000u;
-          }
-        };
-        float e0, e1;
-        const bool low = !logd && p.scl < 0.f;
-        e0 = e1 = low ? INFINITY : -INFINITY;
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          uint32_t x[32], y[32];
-          tmem_ld32(c_s + 32 * q, x);
-          tmem_ld32(c_s + 32 * q + 32, y);
-          tmem_ld_wait();
-          scores(q, x);
-          scores(q + 1, y);
-          if (low) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              e0 = min3(e0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-              e1 = min3(e1, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              e0 = max3(e0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-              e1 = max3(e1, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-            }
-          }
-        }
-        const float mx = (low ? fminf(e0, e1) : fmaxf(e0, e1)) * f;
-        const bool up = mx > m + kTau;
-        if (__any_sync(0xffffffffu, up)) {
-          const float mn = up ? fmaxf(m, mx) : m;
-          const float corr = up ? fast_exp2(m - mn) : 1.f;  // (m = -inf at first: 0)
-          m = mn;
-          l *= corr;
-          if (k > 0) {  // (S of this step was issued behind the last P V, which has completed with it)
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t ob[32];
-              tmem_ld32(c_o + 32 * q, ob);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t x[32];
+              tmem_ld32(c_s + 32 * q, x);
               tmem_ld_wait();
+              if (FOX) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) ob[j] = __float_as_uint(__uint_as_float(ob[j]) * corr);
-              tmem_st32(c_o + 32 * q, ob);
+                for (int j = 0; j < 32; j += 4) {
+                  const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(kb + 32 * q + j);
+                  float v0, v1, v2, v3;
+                  f2_split(f2_fma(f2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), scl2, bv.x), v0, v1);
+                  f2_split(f2_fma(f2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), scl2, bv.y), v2, v3);
+                  x[j] = __float_as_uint(v0);
+                  x[j + 1] = __float_as_uint(v1);
+                  x[j + 2] = __float_as_uint(v2);
+                  x[j + 3] = __float_as_uint(v3);
+                }
+              } else if (MASK) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * p.scl);
+              }
+              if (MASK) {
+                const uint32_t w = visible(q);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = (w >> j & 1) ? x[j] : 0xff800000u;
+              }
+              if (low) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  e0 = min3(e0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                  e1 = min3(e1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  e0 = max3(e0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                  e1 = max3(e1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float a0, a1;
+                f2_split(f2_fma(f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc, nm), a0, a1);
+                const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                acc[j & 1] = f2_add(acc[j & 1], f2(p0, p1));
+                pk[16 * q + j] = pack_bf16(p0, p1);
+              }
+            }
+            float s0, s1, s2, s3;
+            f2_split(acc[0], s0, s1);
+            f2_split(acc[1], s2, s3);
+            sum = (s0 + s1) + (s2 + s3);
+            const float mx = (low ? fminf(e0, e1) : fmaxf(e0, e1)) * f;
+            const bool up = mx > m + kTau;
+            if (!__any_sync(0xffffffffu, up)) break;
+            const float mn = up ? fmaxf(m, mx) : m;
+            const float corr = up ? fast_exp2(m - mn) : 1.f;  // (m = -inf at first: 0)
+            m = mn;
+            l *= corr;
+            if (k > 0) {  // (S of this step was issued behind the last P V, which has completed with it)
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t ob[32];
+                tmem_ld32(c_o + 32 * q, ob);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) ob[j] = __float_as_uint(__uint_as_float(ob[j]) * corr);
+                tmem_st32(c_o + 32 * q, ob);
+              }
             }
           }
-        }
-        const float mu = m == -INFINITY ? 0.f : m;
-        const uint64_t nm = f2(-mu, -mu), sc = f2(f, f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t x[32], pk[16];
-          tmem_ld32(c_s + 32 * q, x);
-          tmem_ld_wait();
-          scores(q, x);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float a0, a1;
-            f2_split(f2_fma(f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), sc, nm), a0, a1);
-            const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-            acc[j & 1] = f2_add(acc[j & 1], f2(p0, p1));
-            pk[j] = pack_bf16(p0, p1);
-          }
-          tmem_st16(c_s + 16 * q, pk);  // (over scores that this row has read)
-        }
         };
         if (mask) step(std::true_type{});
         else step(std::false_type{});
-        float s0, s1, s2, s3;
-        f2_split(acc[0], s0, s1);
-        f2_split(acc[1], s2, s3);
-        l += (s0 + s1) + (s2 + s3);
+        l += sum;
+        tmem_st32(c_s, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));  // over the scores
+        tmem_st32(c_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&s.p_ready[t]);
       }
-      if (!ok) break;
-      ok = mbar_wait_lean(&s.o_full[t], os & 1, err, 12);
+      ok = ok && mbar_wait_lean(&s.o_full[t], os & 1, err, 12);
       ++os;
-      if (!ok) break;
+      if (!FOX && !ok) break;
       tc_fence_after();
       const size_t row = (size_t)(g.item + blockIdx.x) * 256 + 128 * t + r;
       float* dst = pl.acc + row * D;
