@@ -94,6 +94,9 @@ PATH_HD LiveTiles live_tiles(int t0, int window, int sinks, int rows) {
   return l;
 }
 PATH_HD int live_tile(const LiveTiles& l, int i) { return i < l.nh ? i : i + l.skip; }
+// The same from the newest tile to the oldest: with a forget gate the largest scores come first, so the running
+// maximum of a softmax hardly moves after the first tile (oldest first it rises at every tile).
+PATH_HD int newest_tile(const LiveTiles& l, int i) { return live_tile(l, l.count - 1 - i); }
 
 #ifdef __CUDACC__
 __device__ __forceinline__ SlotSpan slot_span(const PagedArgs& p, int b) {

@@ -33,7 +33,7 @@ namespace {
 using namespace tc;
 
 constexpr int KT = kTcKeys;
-constexpr int NSOFT = 256, NTHREADS = NSOFT + 64;
+constexpr int NSOFT = 256, NTHREADS = NSOFT + 64, ATHREADS = NSOFT + 96;  // rewrite; attention
 constexpr int NINFO = 8;      // key tiles whose masks and biases are kept: more than the ring runs ahead
 constexpr float kTau = 8.f;   // lazy rescale threshold (log2 units)
 constexpr uint32_t COL_S = 0, COL_O = 256;  // two tiles each: S 128 columns, O D columns
@@ -109,8 +109,39 @@ __device__ __forceinline__ Segment segment_at(const PagedArgs& p, const TcPlan& 
   return s;
 }
 
+// A value that is the same in all lanes, in a uniform register (a warp reduction leaves its result in one): the
+// MMA takes its descriptors from uniform registers, and what is not known to be uniform is moved there anew for
+// every instruction.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+// The tcgen05 instructions of tc_common.cuh issued by one elected lane of a converged warp.
+__device__ __forceinline__ void mma_ss_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int D, bool FOX>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(ATHREADS, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_zs,
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_ver, const __grid_constant__ CUtensorMap tm_new, const PagedArgs p,
@@ -127,11 +158,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < NBUF; ++i) {
       mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 1);
+      mbar_init(&s.empty[i], 2);  // one arrival per query tile
     }
     for (int i = 0; i < NINFO; ++i) mbar_init(&s.info[i], 1);
     mbar_init(&s.z_full, 1);
-    mbar_init(&s.z_empty, 1);
+    mbar_init(&s.z_empty, 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s.s_full[t], 1);
       mbar_init(&s.p_ready[t], 128);
@@ -167,7 +198,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // the pair's first token sees the farthest back
       const int p_min = g.sp.t0 + g.pair * 256 / p.G;
       for (int i = g.i0; i < g.i1; ++i, ++kk) {
-        const int j0 = live_tile(g.lt, i) * KT;
+        const int j0 = newest_tile(g.lt, i) * KT;
         const int j = j0 + 16 * lane;
         int kp = -1, vp = -1;
         bool here = lane < 8 && j < g.t0 &&
@@ -231,56 +262,53 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int i = n > NBUF ? n - NBUF : 0; i < n + 2; ++i) mbar_wait_ns(&s.full[i % NBUF], (i / NBUF) & 1, nullptr, 0, 1000000ull);
       for (int i = kk > NINFO ? kk - NINFO : 0; i <= kk; ++i) mbar_wait_ns(&s.info[i % NINFO], (i / NINFO) & 1, nullptr, 0, 1000000ull);
     }
-  } else if (warp == 9) {
-    // ---------------- MMA issuer (the whole warp walks; lane 0 issues) ----------------
+  } else if (warp == 9 || warp == 10) {
+    // ---------------- MMA issuer of tile t (a converged warp; one elected lane issues) ----------------
+    const int t = warp - 9;
     const uint32_t idesc_s = idesc_bf16(128, KT, 0, 0), idesc_o = idesc_bf16(128, D, 0, 1);
-    const uint64_t dz = sdesc_sw128(smem_u32(s.z[0][0]), 1024, 16);
-    const uint64_t dk = sdesc_sw128(smem_u32(s.buf[0][0]), 1024, 16);
-    const uint64_t dv = sdesc_sw128(smem_u32(s.buf[0][0]), 1024, TILE);
-    int n = 0, kk = 0, seg = 0;
+    const uint64_t dz = sdesc_sw128(0, 1024, 16), dv = sdesc_sw128(0, 1024, TILE);
+    const uint32_t a_z = uniform(smem_u32(s.z[t][0]) >> 4), a_b = uniform(smem_u32(s.buf[0][0]) >> 4), tbu = uniform(tb);
+    const uint32_t d_s = tbu + COL_S + 128 * uniform(t), d_o = tbu + COL_O + D * uniform(t);
+    int n = 0, kk = 0, seg = 0, np = 0, os = 0;  // buffers, key tiles, segments; probability tiles and segments of this tile
     bool ok = true;
-    auto issue_s = [&](int t, int buf) {
-      if (lane == 0) {
-        const uint64_t a = dz + (uint64_t)(t * X * (TILE / 16)), b = dk + (uint64_t)(buf * X * (TILE / 16));
+    auto issue_s = [&](int buf) {
+      const uint64_t za = dz + a_z, kb = dz + a_b + uniform(buf * X * (TILE / 16));
 #pragma unroll
-        for (int x = 0; x < X; ++x)
+      for (int x = 0; x < X; ++x)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(tb + COL_S + 128 * t, a + (uint64_t)(x * (TILE / 16) + 2 * k), b + (uint64_t)(x * (TILE / 16) + 2 * k), idesc_s,
-                   (x | k) ? 1u : 0u);
-        mma_commit(&s.s_full[t]);
-      }
+        for (int k = 0; k < 4; ++k)
+          mma_ss_elect(d_s, za + (uint64_t)(x * (TILE / 16) + 2 * k), kb + (uint64_t)(x * (TILE / 16) + 2 * k), idesc_s, (x | k) ? 1u : 0u);
+      mma_commit_elect(&s.s_full[t]);
+      mma_commit_elect(&s.empty[buf]);
     };
-    auto issue_o = [&](int t, int buf, bool first) {
-      if (lane == 0) {
-        const uint64_t b = dv + (uint64_t)(buf * X * (TILE / 16));
-#pragma unroll
-        for (int k = 0; k < KT / 16; ++k)
-          mma_ts(tb + COL_O + D * t, tb + COL_S + 128 * t + 8 * k, b + (uint64_t)(128 * k), idesc_o, (first && k == 0) ? 0u : 1u);
-      }
-    };
-    int pr[2] = {0, 0};   // p_ready phases consumed
-    int os[2] = {0, 0};   // segments of each tile so far
-    for (long long u = u0; ok && u < u1;) {
+    for (long long u = u0; ok && u < u1; ++seg) {
       const Segment g = segment_at(p, pl, u, u1, &u);
-      const int tiles = g.rows > 128 ? 2 : 1, nk = g.i1 - g.i0;
+      const int nk = g.i1 - g.i0;
+      if (t == 1 && g.rows <= 128) {  // no second tile: the buffers' phases still end with this warp's arrivals
+        for (int k = 0; ok && k < 2 * nk; ++k) {
+          ok = mbar_wait_lean(&s.full[(n + k) % NBUF], ((n + k) / NBUF) & 1, err, 4);
+          if (ok && lane == 0) mbar_arrive(&s.empty[(n + k) % NBUF]);
+        }
+        if (ok) ok = mbar_wait_lean(&s.z_full, seg & 1, err, 4);
+        if (ok && lane == 0) mbar_arrive(&s.z_empty);
+        n += 2 * nk;
+        kk += nk;
+        continue;
+      }
       ok = mbar_wait_lean(&s.z_full, seg & 1, err, 4) && mbar_wait_lean(&s.full[n % NBUF], (n / NBUF) & 1, err, 5);
       if (!ok) break;
       tc_fence_after();
-      for (int t = 0; t < tiles; ++t) issue_s(t, n % NBUF);
-      if (lane == 0) {
-        mma_commit(&s.empty[n % NBUF]);
-        if (nk == 1) mma_commit(&s.z_empty);
-      }
+      issue_s(n % NBUF);
+      if (nk == 1) mma_commit_elect(&s.z_empty);
       for (int k = 0; ok && k < nk; ++k, ++kk, n += 2) {
         const int vb = (n + 1) % NBUF, nb = (n + 2) % NBUF;
         ok = mbar_wait_lean(&s.full[vb], ((n + 1) / NBUF) & 1, err, 6);
         if (!ok) break;
-        const int j0 = live_tile(g.lt, g.i0 + k) * KT;
+        const int j0 = newest_tile(g.lt, g.i0 + k) * KT;
         // (the tile's mask: written by the producer before it arrived for the key buffer, which this warp has
         // waited for)
         const uint32_t groups = *reinterpret_cast<volatile uint32_t*>(&s.okmask[kk % NINFO]);
-        if (groups != 0xffu || j0 + KT > g.t0) {
+        if (groups != 0xffu || j0 + KT > g.t0) {  // (both tiles' warps write the same zeros)
           for (int r = lane >> 3; r < KT; r += 4)
             if (!(groups >> (r >> 4) & 1) || j0 + r >= g.t0)
 #pragma unroll
@@ -288,30 +316,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        for (int t = 0; ok && t < tiles; ++t) {
-          ok = mbar_wait_lean(&s.p_ready[t], pr[t] & 1, err, 7);
-          if (ok && k == 0 && os[t] > 0) ok = mbar_wait_lean(&s.o_read[t], (os[t] - 1) & 1, err, 8);
-          if (!ok) break;
-          ++pr[t];
-          tc_fence_after();
-          issue_o(t, vb, k == 0);
-          if (t == tiles - 1 && lane == 0) mma_commit(&s.empty[vb]);
-          if (k + 1 < nk) {
-            if (t == 0) ok = mbar_wait_lean(&s.full[nb], ((n + 2) / NBUF) & 1, err, 9);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(t, nb);
-            if (t == tiles - 1 && lane == 0) {
-              mma_commit(&s.empty[nb]);
-              if (k + 2 == nk) mma_commit(&s.z_empty);
-            }
-          } else {
-            if (lane == 0) mma_commit(&s.o_full[t]);
-            ++os[t];
-          }
+        if (k + 1 < nk) ok = mbar_wait_lean(&s.full[nb], ((n + 2) / NBUF) & 1, err, 9);
+        ok = ok && mbar_wait_lean(&s.p_ready[t], np & 1, err, 7);
+        if (ok && k == 0 && os > 0) ok = mbar_wait_lean(&s.o_read[t], (os - 1) & 1, err, 8);
+        if (!ok) break;
+        ++np;
+        __syncwarp();
+        tc_fence_after();
+        const uint64_t vd = dv + a_b + uniform(vb * X * (TILE / 16));
+        const uint32_t first = uniform(k == 0 ? 0u : 1u);
+#pragma unroll
+        for (int y = 0; y < KT / 16; ++y)
+          mma_ts_elect(d_o, d_s + 8 * y, vd + (uint64_t)(128 * y), idesc_o, y == 0 ? first : 1u);
+        if (k + 1 == nk) mma_commit_elect(&s.o_full[t]);
+        if (k + 1 < nk) {
+          issue_s(nb);
+          if (k + 2 == nk) mma_commit_elect(&s.z_empty);
         }
+        mma_commit_elect(&s.empty[vb]);
       }
-      ++seg;
+      ++os;
     }
   } else {
     // ---------------- softmax: thread = row of tile warp / 4 ----------------
@@ -344,7 +368,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ok = ok && mbar_wait_lean(&s.s_full[t], ns & 1, err, 10) && mbar_wait_lean(&s.info[kk % NINFO], (kk / NINFO) & 1, err, 11);
         if (!FOX && !ok) break;
         tc_fence_after();
-        const int j0 = live_tile(g.lt, g.i0 + k) * KT;
+        const int j0 = newest_tile(g.lt, g.i0 + k) * KT;
         const uint32_t groups = s.okmask[kk % NINFO];
         const bool mask = groups != 0xffu || j0 + KT > g.t0 ||
                           (p.window > 0 && g.base + j0 + KT > p.sinks && g.base + j0 <= p_max - p.window);
@@ -712,7 +736,7 @@ cudaError_t attend_t(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
   const size_t smem = sizeof(TcSmem<D, FOX>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<kTcBlocks, NTHREADS, smem, st>>>(mz, mzs, mk, mv, mver, mnew, p, pl);
+  kern<<<kTcBlocks, ATHREADS, smem, st>>>(mz, mzs, mk, mv, mver, mnew, p, pl);
   return cudaGetLastError();
 }
 

@@ -313,11 +313,11 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
     const int i0 = u - s0, i1 = lt.count > 0 ? ue - s0 : i0;  // (no cached rows: nothing to stream)
     uint4 kr[2][KB], vr[4][CS];
     float aj[2] = {0.f, 0.f};
-    auto page = [&](const int* table, int i) { return __ldg(table + (size_t)b * p.c.table_width + live_tile(lt, i) * RT / P); };
+    auto page = [&](const int* table, int i) { return __ldg(table + (size_t)b * p.c.table_width + newest_tile(lt, i) * RT / P); };
     int kp = -1, vp = -1, kpn = -1, vpn = -1;  // pages of the current and the next tile
     long long krow = 0, vrow = 0;
     auto rows_of = [&](int i, int pk, int pv, long long& rk, long long& rv) {
-      const int in = live_tile(lt, i) * RT % P;
+      const int in = newest_tile(lt, i) * RT % P;
       rk = ((long long)pk * H + h) * P + in;
       rv = ((long long)pv * H + h) * P + in;
     };
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
       }
     }
     for (int i = i0; i < i1; ++i) {
-      const int j0 = live_tile(lt, i) * RT;
+      const int j0 = newest_tile(lt, i) * RT;
       const bool cur = ok;
       if (!cur && lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
       float s[NQ8][4], c[ONE ? 1 : NT8][4];
