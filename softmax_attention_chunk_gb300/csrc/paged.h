@@ -103,6 +103,27 @@ __device__ __forceinline__ SlotSpan slot_span(const PagedArgs& p, int b) {
   return slot_span_of(b, p.q_start, p.c.seq_len[b], p.total, p.max_new, p.c.table_width, p.c.page_size);
 }
 __device__ __forceinline__ void paged_error(int* status, int code) { atomicCAS(status, 0, code); }
+// Programmatic dependent launch: every kernel of a call begins with chain(), which waits until the kernel before it has
+// ended and lets the next one's blocks take their places meanwhile (they wait there).  The first statement of every
+// kernel, for all threads: a grid that ended without having waited would end the chain early.
+__device__ __forceinline__ void chain() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 #endif
 
 // ---- launchers ----

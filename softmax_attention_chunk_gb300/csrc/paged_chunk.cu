@@ -63,6 +63,7 @@ ChunkWs chunk_ws(const PagedArgs& p) {
 
 // First chunk and first live tile of every slot (exclusive prefix sums; entry `slots` holds the totals).
 __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict__ plan) {
+  chain();
   __shared__ int wsum[2][32];
   __shared__ int carry[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -119,6 +120,7 @@ struct PrepSmem {
 // One block per (chunk, key head).
 template <int D>
 __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+  chain();
   extern __shared__ float sm[];
   using S = PrepSmem<D>;
   constexpr int DS = S::DS, BS = S::BS;
@@ -405,6 +407,7 @@ constexpr size_t scan_walk_smem() {
 // Blocks [0, slots * H) walk keys, the others scan queries.
 template <int D>
 __global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+  chain();
   extern __shared__ float sm[];
   const int nw = p.c.slots * p.c.heads;
   if ((int)blockIdx.x < nw) {
@@ -419,6 +422,7 @@ __global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, c
 // Cached attention: one block per (chunk, query head, key range).
 template <int D>
 __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+  chain();
   extern __shared__ float sm[];
   using S = ScanSmem<D>;
   constexpr int DS = S::DS, KS = S::KS;
@@ -506,6 +510,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
 // k <- k M for the cached rows that a later token sees: blocks take runs of (live tile, head).
 template <int D>
 __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, const char* __restrict__ ws) {
+  chain();
   extern __shared__ float sm[];
   constexpr int DS = D + 4;
   float *sMm = sm, *sK = sMm + D * DS;
@@ -548,6 +553,7 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
 // Merge of the key ranges: one warp per (row, query head).
 template <int D>
 __global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const char* __restrict__ ws) {
+  chain();
   const int* cstart = (const int*)(ws + w.plan);
   const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (c >= cstart[p.c.slots]) return;
@@ -592,13 +598,13 @@ cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
   if ((e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(att, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s3)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(rew, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s4)) != cudaSuccess) return e;
-  plan_kernel<<<1, 1024, 0, st>>>(p, (int*)(ws + w.plan));
-  prep<<<dim3(w.nch, p.c.heads), NT, s1, st>>>(p, w, ws);
-  scan<<<(unsigned)(p.c.slots * p.c.heads + w.nch * p.hq), NT, s2, st>>>(p, w, ws);
-  att<<<dim3(w.nch, p.hq, w.nsplit), NT, s3, st>>>(p, w, ws);
-  rew<<<608, NT, s4, st>>>(p, w, ws);
-  merge_kernel<D><<<dim3(w.nch, p.hq), NT, 0, st>>>(p, w, ws);
-  return cudaGetLastError();
+  if ((e = launch_chained(plan_kernel, 1, 1024, 0, st, p, (int*)(ws + w.plan))) != cudaSuccess ||
+      (e = launch_chained(prep, dim3(w.nch, p.c.heads), NT, s1, st, p, w, ws)) != cudaSuccess ||
+      (e = launch_chained(scan, p.c.slots * p.c.heads + w.nch * p.hq, NT, s2, st, p, w, ws)) != cudaSuccess ||
+      (e = launch_chained(att, dim3(w.nch, p.hq, w.nsplit), NT, s3, st, p, w, ws)) != cudaSuccess ||
+      (e = launch_chained(rew, 608, NT, s4, st, p, w, ws)) != cudaSuccess)
+    return e;
+  return launch_chained(merge_kernel<D>, dim3(w.nch, p.hq), NT, 0, st, p, w, ws);
 }
 
 }  // namespace

@@ -165,6 +165,7 @@ NewWs new_ws(const PagedArgs& p) {
 // ---- plan ----
 // Exclusive prefix sums over the slots, all at once: chunks, blocks, query pairs, rewrite tiles, version rows, units.
 __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool report) {
+  chain();
   constexpr int N = 6;
   __shared__ long long wsum[N][32], carry[N];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -286,6 +287,7 @@ __device__ __forceinline__ void put_pair(const float (&c)[NT][4], bf16* hi, bf16
 }
 template <int D>
 __global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  chain();
   extern __shared__ __align__(16) uint8_t smem[];
   using S = PrepSmem<D>;
   S& s = *reinterpret_cast<S*>(smem);
@@ -634,6 +636,7 @@ __device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, 
 // Blocks: (block, head, slab) of level 1, then (slot, head) of the gate's sums.
 template <int D>
 __global__ void __launch_bounds__(WT) carry_in_block_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  chain();
   extern __shared__ __align__(16) uint8_t smem[];
   const int slabs = CPB + D / 64, H = p.c.heads;
   const int x = blockIdx.x, n1 = w.nblk * H * slabs;
@@ -681,6 +684,7 @@ __device__ __forceinline__ void softmax64(float (&s)[8][4], float (&m)[2], float
 // The first thread blocks carry keys on (level 2: the longest chains, and independent of the queries).
 template <int D, bool FOX>
 __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  chain();
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* sm = (bf16*)smem;
   using S = QSmem<D>;
@@ -822,6 +826,7 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
 // z = zs G_b^T for the query pairs behind the first block: one block per (64 rows of a pair, head).
 template <int D>
 __global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+  chain();
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* sm = (bf16*)smem;
   constexpr int LD = D + 8;
@@ -853,6 +858,7 @@ __global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan 
 constexpr int GT = 256;
 template <int D>
 __global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan pl, const char* __restrict__ ws) {
+  chain();
   constexpr int L = D / 4, PG = 32 / L;  // lanes of a row; parts summed side by side
   const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x4 = lane % L * 4, pg = lane / L;
   if (c == 0 && qh == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
@@ -892,26 +898,49 @@ __global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan 
       }
     }
     auto at = [&](int x) { return (size_t)((x < n1 ? from1 : from2) + x) * kTcPair + R % kTcPair; };
-    float M = m0;
-    for (int x = lane; x < n; x += 32) M = fmaxf(M, pl.m[at(x)] + bias);
+    // maxima and sums of up to 32 parts at a time, one per lane; the first parts' rows set out beside them
+    constexpr int AHEAD = 4 / PG;
+    float4 v[AHEAD];
+#pragma unroll
+    for (int y = 0; y < AHEAD; ++y)
+      v[y] = y * PG + pg < n ? *reinterpret_cast<const float4*>(pl.acc + at(y * PG + pg) * D + x4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float mx = lane < n ? pl.m[at(lane)] + bias : -INFINITY;
+    const float lx = lane < n ? pl.l[at(lane)] : 0.f;
+    float M = fmaxf(m0, mx);
+    for (int x = lane + 32; x < n; x += 32) M = fmaxf(M, pl.m[at(x)] + bias);
     M = group_max<32>(M);
-    float f = pg == 0 ? fast_exp2(m0 - M) : 0.f;
-    float l = l0 * f;
-    float4 a = make_float4(v0.x * f, v0.y * f, v0.z * f, v0.w * f);
-#pragma unroll 4
-    for (int x = pg; x < n; x += PG) {
-      const float ms = pl.m[at(x)];
-      const float4 v = *reinterpret_cast<const float4*>(pl.acc + at(x) * D + x4);
-      if (ms == -INFINITY) continue;  // (a part that saw nothing)
-      f = fast_exp2(ms + bias - M);
-      l += pl.l[at(x)] * f;
-      a.x += v.x * f;
-      a.y += v.y * f;
-      a.z += v.z * f;
-      a.w += v.w * f;
+    const float f0 = fast_exp2(m0 - M);
+    float4 a = pg == 0 ? make_float4(v0.x * f0, v0.y * f0, v0.z * f0, v0.w * f0) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float fx = mx == -INFINITY ? 0.f : fast_exp2(mx - M);  // (-inf: a part that saw nothing)
+    float l = lx * fx;
+#pragma unroll
+    for (int y = 0; y < AHEAD; ++y) {
+      const float f = __shfl_sync(0xffffffffu, fx, y * PG + pg);
+      a.x += v[y].x * f;
+      a.y += v[y].y * f;
+      a.z += v[y].z * f;
+      a.w += v[y].w * f;
     }
+    for (int x0 = AHEAD * PG; x0 < n; x0 += PG) {
+      const int x = x0 + pg;
+      float f;
+      if (x0 < 32) {
+        f = __shfl_sync(0xffffffffu, fx, x);
+      } else {
+        const float ms = x < n ? pl.m[at(x)] + bias : -INFINITY;
+        f = ms == -INFINITY ? 0.f : fast_exp2(ms - M);
+        if (lane % L == 0 && x < n) l += pl.l[at(x)] * f;
+      }
+      if (x < n) {
+        const float4 w4 = *reinterpret_cast<const float4*>(pl.acc + at(x) * D + x4);
+        a.x += w4.x * f;
+        a.y += w4.y * f;
+        a.z += w4.z * f;
+        a.w += w4.w * f;
+      }
+    }
+    l = group_sum<32>(l) + l0 * f0;
     if (PG == 2) {
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
       a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
       a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
       a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
@@ -963,16 +992,18 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
   pl.err = (int*)(ws + w.err);
   const bool many = p.max_new > MB;  // a slot may have a second block
   for (p.skip = 0; p.skip < p.max_new; p.skip += kTcPassTokens) {
-    plan_kernel<<<1, 1024, 0, st>>>(p, pl, p.skip == 0);
-    prep<<<dim3(w.nch, H), PT, s1, st>>>(p, w, pl, ws);
-    c1<<<(unsigned)(w.nblk * H * (CPB + D / 64) + (fox ? p.c.slots * H : 0)), WT, s2, st>>>(p, w, pl, ws);
-    qk<<<(unsigned)(w.nblk * H * (CPB + D / 64) + w.nch * p.hq), WT, s3 > s2 ? s3 : s2, st>>>(p, w, pl, ws);
-    if (many) sk<<<dim3(w.pairs * 4, H), WT, s4, st>>>(p, w, pl, ws);
-    if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_attend_tc(p, pl, st)) != cudaSuccess) return e;
-    if ((e = launch_rewrite_tc(p, pl, st)) != cudaSuccess) return e;
-    merge_kernel<D><<<dim3(w.nch, p.hq), GT, 0, st>>>(p, w, pl, ws);
+    const unsigned carries = (unsigned)(w.nblk * H * (CPB + D / 64));
+    if ((e = launch_chained(plan_kernel, 1, 1024, 0, st, p, pl, p.skip == 0)) != cudaSuccess ||
+        (e = launch_chained(prep, dim3(w.nch, H), PT, s1, st, p, w, pl, ws)) != cudaSuccess ||
+        (e = launch_chained(c1, carries + (fox ? p.c.slots * H : 0), WT, s2, st, p, w, pl, ws)) != cudaSuccess ||
+        (e = launch_chained(qk, carries + w.nch * p.hq, WT, s3 > s2 ? s3 : s2, st, p, w, pl, ws)) != cudaSuccess)
+      return e;
+    if (many && (e = launch_chained(sk, dim3(w.pairs * 4, H), WT, s4, st, p, w, pl, ws)) != cudaSuccess) return e;
+    if ((e = launch_attend_tc(p, pl, st)) != cudaSuccess || (e = launch_rewrite_tc(p, pl, st)) != cudaSuccess ||
+        (e = launch_chained(merge_kernel<D>, dim3(w.nch, p.hq), GT, 0, st, p, w, pl, ws)) != cudaSuccess)
+      return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace

@@ -120,6 +120,7 @@ __device__ bool bad_slots(const int* __restrict__ list, int count, const int* __
 
 // ---------------- reserve ----------------
 __global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const int* __restrict__ n_new, Lists w) {
+  chain();
   __shared__ BlockScan s;
   __shared__ int code;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = c.page_size;
@@ -208,6 +209,7 @@ __global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const
 // ---------------- fork ----------------
 __global__ void __launch_bounds__(NT) fork_kernel(path_paged_cache_t c, const int* __restrict__ parents,
                                                   const int* __restrict__ children, int count, Lists w) {
+  chain();
   __shared__ BlockScan s;
   __shared__ unsigned seen[(kMaxSlots + 31) / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = c.page_size;
@@ -318,6 +320,7 @@ __device__ __forceinline__ void drop(const path_paged_cache_t& c, int b, int x) 
   *vt = -1;
 }
 __global__ void __launch_bounds__(NT) free_kernel(path_paged_cache_t c, const int* __restrict__ list, int count) {
+  chain();
   __shared__ unsigned seen[(kMaxSlots + 31) / 32];
   if (bad_slots(list, count, c.seq_len, c.slots, true, seen)) {
     if (threadIdx.x == 0) paged_error(c.status, PATH_PAGED_BAD_SLOT);
@@ -332,6 +335,7 @@ __global__ void __launch_bounds__(NT) free_kernel(path_paged_cache_t c, const in
 // One block per slot: slots share no table row, and value counts fall by atomics (sums of ones: the order
 // does not matter).
 __global__ void __launch_bounds__(CT) trim_kernel(path_paged_cache_t c, int window, int sinks) {
+  chain();
   const int b = blockIdx.x, P = c.page_size, len = c.seq_len[b];
   if (len <= 0) return;
   // rows j with sinks <= j <= len - window are hidden from position len on
@@ -390,6 +394,7 @@ __device__ int dense_lists(int* __restrict__ ref, int pages, int* __restrict__ s
   return ns;
 }
 __global__ void __launch_bounds__(NT) compact_kernel(path_paged_cache_t c, Lists w) {
+  chain();
   __shared__ BlockScan s;
   int used;
   if (blockIdx.x == 0) {  // one block per pool
@@ -412,6 +417,7 @@ constexpr int kPiece = 8192;  // bytes of a page that one block copies at a time
 // Copies the listed pages; with `map` also rewrites the tables (entries at or above the number of pages
 // in use have moved).
 __global__ void __launch_bounds__(CT) copy_kernel(path_paged_cache_t c, Lists w, size_t page_bytes, int map) {
+  chain();
   const int nk = w.head[0], nv = w.head[1];
   const size_t abytes = c.a_pool ? (size_t)c.heads * c.page_size * 4 : 0;
   const long long pieces = (long long)((page_bytes + kPiece - 1) / kPiece);  // (a piece may be short)
@@ -461,6 +467,7 @@ __global__ void __launch_bounds__(CT) copy_kernel(path_paged_cache_t c, Lists w,
 }
 
 __global__ void advance_kernel(path_paged_cache_t c, const int* __restrict__ q_start) {
+  chain();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= c.slots) return;
   const int len = c.seq_len[b];
@@ -481,8 +488,7 @@ size_t page_bytes(const path_paged_cache_t& c) {
   return (size_t)c.heads * c.page_size * c.head_dim * (c.cache_dtype == PATH_BF16 ? 2 : 4);
 }
 cudaError_t copy_pages(const path_paged_cache_t& c, const Lists& w, int map, cudaStream_t st) {
-  copy_kernel<<<152 * 8, CT, 0, st>>>(c, w, page_bytes(c), map);
-  return cudaGetLastError();
+  return launch_chained(copy_kernel, 152 * 8, CT, 0, st, c, w, page_bytes(c), map);
 }
 
 }  // namespace
@@ -490,31 +496,29 @@ cudaError_t copy_pages(const path_paged_cache_t& c, const Lists& w, int map, cud
 size_t pages_ws_bytes(const path_paged_cache_t& c) { return pages_ws(c).total; }
 
 cudaError_t launch_pages_reserve(const path_paged_cache_t& c, const int* n_new, char* ws, cudaStream_t st) {
-  reserve_kernel<<<1, NT, 0, st>>>(c, n_new, lists(c, ws));
-  return cudaGetLastError();
+  return launch_chained(reserve_kernel, 1, NT, 0, st, c, n_new, lists(c, ws));
 }
 cudaError_t launch_pages_fork(const path_paged_cache_t& c, const int* parents, const int* children, int count, char* ws,
                               cudaStream_t st) {
   const Lists w = lists(c, ws);
-  fork_kernel<<<1, NT, 0, st>>>(c, parents, children, count, w);
+  const cudaError_t e = launch_chained(fork_kernel, 1, NT, 0, st, c, parents, children, count, w);
+  if (e != cudaSuccess) return e;
   return copy_pages(c, w, 0, st);
 }
 cudaError_t launch_pages_free(const path_paged_cache_t& c, const int* slots, int count, char*, cudaStream_t st) {
-  free_kernel<<<1, NT, 0, st>>>(c, slots, count);
-  return cudaGetLastError();
+  return launch_chained(free_kernel, 1, NT, 0, st, c, slots, count);
 }
 cudaError_t launch_pages_trim(const path_paged_cache_t& c, int window, int sinks, char*, cudaStream_t st) {
-  trim_kernel<<<(unsigned)c.slots, CT, 0, st>>>(c, window, sinks);
-  return cudaGetLastError();
+  return launch_chained(trim_kernel, (unsigned)c.slots, CT, 0, st, c, window, sinks);
 }
 cudaError_t launch_pages_compact(const path_paged_cache_t& c, char* ws, cudaStream_t st) {
   const Lists w = lists(c, ws);
-  compact_kernel<<<2, NT, 0, st>>>(c, w);
+  const cudaError_t e = launch_chained(compact_kernel, 2, NT, 0, st, c, w);
+  if (e != cudaSuccess) return e;
   return copy_pages(c, w, 1, st);
 }
 cudaError_t launch_paged_advance(const path_paged_cache_t& c, const int* q_start, cudaStream_t st) {
-  advance_kernel<<<(unsigned)((c.slots + 255) / 256), 256, 0, st>>>(c, q_start);
-  return cudaGetLastError();
+  return launch_chained(advance_kernel, (unsigned)((c.slots + 255) / 256), 256, 0, st, c, q_start);
 }
 
 }  // namespace pathattn

@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(ATHREADS, 1)
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_ver, const __grid_constant__ CUtensorMap tm_new, const PagedArgs p,
                      const TcPlan pl) {
+  chain();
   extern __shared__ uint8_t smem_raw[];
   using Smem = TcSmem<D, FOX>;
   constexpr int X = Smem::X, NBUF = Smem::NBUF;
@@ -560,6 +561,7 @@ template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1)
     rewrite_tc_kernel(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_k, const PagedArgs p,
                       const TcPlan pl) {
+  chain();
   extern __shared__ uint8_t smem_raw[];
   using Smem = RewSmem<D>;
   constexpr int X = Smem::X, NBUF = Smem::NBUF;
@@ -736,8 +738,7 @@ cudaError_t attend_t(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
   const size_t smem = sizeof(TcSmem<D, FOX>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<kTcBlocks, ATHREADS, smem, st>>>(mz, mzs, mk, mv, mver, mnew, p, pl);
-  return cudaGetLastError();
+  return launch_chained(kern, kTcBlocks, ATHREADS, smem, st, mz, mzs, mk, mv, mver, mnew, p, pl);
 }
 
 template <int D>
@@ -751,8 +752,7 @@ cudaError_t rewrite_t(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
   const size_t smem = sizeof(RewSmem<D>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<kTcBlocks, NTHREADS, smem, st>>>(mm, mk, p, pl);
-  return cudaGetLastError();
+  return launch_chained(kern, kTcBlocks, NTHREADS, smem, st, mm, mk, p, pl);
 }
 
 }  // namespace

@@ -119,6 +119,7 @@ __device__ void unit_starts(const PagedArgs& p, int mode, bool report, int* out)
   __syncthreads();
 }
 __global__ void __launch_bounds__(1024) unit_starts_kernel(PagedArgs p, int mode, int* out) {
+  chain();
   unit_starts<1024>(p, mode, true, out);
 }
 __device__ __forceinline__ int find_slot(const int* start, int slots, int u) {
@@ -145,6 +146,7 @@ struct State {
 // NT8 = 0: every slot of the list has one token.  Otherwise NT8 tiles of 8 tokens, fragments from draft_prep_kernel.
 template <int D, int NQ8, int NT8, bool FOX>
 __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
+  chain();
   __shared__ int s_start[kSmemSlots + 1];
   constexpr bool ONE = NT8 == 0;
   // z in B fragment order: registers where they are few, else one copy per warp in shared memory
@@ -620,6 +622,7 @@ struct DraftSmem {
 };
 template <int D, bool FOX>
 __global__ void __launch_bounds__(DT) draft_prep_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
+  chain();
   extern __shared__ __align__(16) uint8_t smem_raw[];
   DraftSmem<D>& sm = *reinterpret_cast<DraftSmem<D>*>(smem_raw);
   const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, H = p.c.heads, G = p.G;
@@ -835,6 +838,7 @@ constexpr int merge_columns(int D, int cols) {  // a power of two, at most the g
 template <int D>
 __global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w, const char* __restrict__ ws, int mode, int warps,
                                                          int cs) {
+  chain();
   constexpr int L = D / 4, GR = MT / L;
   __shared__ int s_start[kSmemSlots + 1];
   __shared__ float4 s_acc[GR][L];
@@ -901,17 +905,20 @@ template <int D, int NQ8, int NT8, bool FOX>
 cudaError_t token_t(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
   constexpr bool ONE = NT8 == 0;
   const int mode = ONE ? kOnlyOne : kDrafts;
-  if (p.c.slots > kSmemSlots) unit_starts_kernel<<<1, 1024, 0, st>>>(p, mode, (int*)(ws + w.ustart));
+  cudaError_t e;
+  if (p.c.slots > kSmemSlots &&
+      (e = launch_chained(unit_starts_kernel, 1, 1024, 0, st, p, mode, (int*)(ws + w.ustart))) != cudaSuccess)
+    return e;
   if (!ONE) {
     auto prep = draft_prep_kernel<D, FOX>;
-    const cudaError_t e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(DraftSmem<D>));
-    if (e != cudaSuccess) return e;
-    prep<<<dim3(p.c.slots, p.c.heads), DT, sizeof(DraftSmem<D>), st>>>(p, w, ws);
+    if ((e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(DraftSmem<D>))) != cudaSuccess ||
+        (e = launch_chained(prep, dim3(p.c.slots, p.c.heads), DT, sizeof(DraftSmem<D>), st, p, w, ws)) != cudaSuccess)
+      return e;
   }
-  token_kernel<D, NQ8, NT8, FOX><<<w.blocks, NT, 0, st>>>(p, w, ws);
+  if ((e = launch_chained(token_kernel<D, NQ8, NT8, FOX>, w.blocks, NT, 0, st, p, w, ws)) != cudaSuccess) return e;
   const int cols = (ONE ? 1 : p.max_new) * p.G, cs = merge_columns(D, cols);
-  token_merge_kernel<D><<<dim3(p.c.slots, p.c.heads, (cols + cs - 1) / cs), MT, 0, st>>>(p, w, ws, mode, w.blocks * WARPS, cs);
-  return cudaGetLastError();
+  return launch_chained(token_merge_kernel<D>, dim3(p.c.slots, p.c.heads, (cols + cs - 1) / cs), MT, 0, st, p, w, ws, mode,
+                        w.blocks * WARPS, cs);
 }
 template <int D, bool FOX>
 cudaError_t token_d(const PagedArgs& p, const TokenWs& w, bool drafts, char* ws, cudaStream_t st) {
