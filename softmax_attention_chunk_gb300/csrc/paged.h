@@ -20,7 +20,7 @@ struct PagedArgs {
   const void *q, *k, *v, *w;
   const float *beta, *log_f;
   void* o;
-  int min_new;          // prompt chunks: slots with fewer new tokens are left to the streaming kernels
+  int min_new;          // more tokens: slots with fewer new ones are left to the streaming kernels
   int skip;             // prompt chunks: new tokens of each slot that earlier passes have done
 };
 
@@ -134,7 +134,7 @@ cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st);
 size_t paged_chunk_ws_bytes(const PagedArgs& p);
 cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st);
 
-// Slots with one new token, bf16; where paged_drafts() holds, all slots of the call.
+// Slots with one new token; where paged_drafts() holds (bf16), all slots of the call.
 bool paged_drafts(const PagedArgs& p);
 size_t paged_token_ws_bytes(const PagedArgs& p);
 cudaError_t launch_paged_token(const PagedArgs& p, char* ws, cudaStream_t st);

@@ -14,7 +14,6 @@
 // block, cached attention split over key ranges, cached rewrite, and the merge of the splits.
 #include "paged.h"
 #include "dev_common.cuh"
-#include "smem_mm.cuh"
 
 namespace pathattn {
 namespace {
@@ -22,6 +21,65 @@ namespace {
 constexpr int NT = 256;
 constexpr int B = kPagedChunk;
 constexpr int KT = 64;  // cached rows per tile
+
+// C = op(A) op(B) of matrices in shared memory, fp32: op(A)(i, k) = TA ? A[k lda + i] : A[i lda + k], op(B)(k, j) = TB ?
+// B[j ldb + k] : B[k ldb + j].  2 x 4 results per thread, 16-byte loads along whichever index is contiguous; every
+// result goes to epi(i, j, value).
+template <int M, int N, int K, bool TA, bool TB, typename Epi>
+__device__ __forceinline__ void product(const float* A, int lda, const float* B, int ldb, Epi epi) {
+  static_assert(M % 2 == 0 && N % 4 == 0 && K % 4 == 0, "tile shape");
+  auto ld4 = [](const float* q) { return *reinterpret_cast<const float4*>(q); };
+  auto at = [](const float4& v, int e) { return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w; };
+  constexpr int TN = N / 4, TILES = M / 2 * TN;
+  for (int tile = threadIdx.x; tile < TILES; tile += NT) {
+    // columns of a thread lie TN apart where B is read along k (neighbouring threads then read neighbouring rows)
+    const int i0 = tile / TN * 2, jt = tile % TN;
+    float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 4
+    for (int k = 0; k < K; k += 4) {
+      float a[2][4];
+      if (TA) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = *reinterpret_cast<const float2*>(A + (k + e) * lda + i0);
+          a[0][e] = v.x;
+          a[1][e] = v.y;
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float4 v = ld4(A + (i0 + y) * lda + k);
+          a[y][0] = v.x; a[y][1] = v.y; a[y][2] = v.z; a[y][3] = v.w;
+        }
+      }
+      if (TB) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 v = ld4(B + (jt + j * TN) * ldb + k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            c[0][j] = fmaf(a[0][e], at(v, e), c[0][j]);
+            c[1][j] = fmaf(a[1][e], at(v, e), c[1][j]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 v = ld4(B + (k + e) * ldb + 4 * jt);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            c[0][j] = fmaf(a[0][e], at(v, j), c[0][j]);
+            c[1][j] = fmaf(a[1][e], at(v, j), c[1][j]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) epi(i0 + y, TB ? jt + j * TN : 4 * jt + j, c[y][j]);
+  }
+}
 
 // Workspace (element offsets are computed on the host and the device from the same sizes).
 struct ChunkWs {
@@ -61,6 +119,12 @@ ChunkWs chunk_ws(const PagedArgs& p) {
   return w;
 }
 
+__device__ __forceinline__ SlotSpan chunk_span(const PagedArgs& p, int b) {
+  SlotSpan s = slot_span(p, b);
+  if (s.n < p.min_new) s.n = 0;
+  return s;
+}
+
 // First chunk and first live tile of every slot (exclusive prefix sums; entry `slots` holds the totals).
 __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict__ plan) {
   chain();
@@ -75,7 +139,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict
     const int b = base + tid;
     int nc = 0, nt = 0;
     if (b < p.c.slots) {
-      const SlotSpan s = slot_span(p, b);
+      const SlotSpan s = chunk_span(p, b);
       if (s.code) paged_error(p.c.status, s.code);
       nc = (s.n + B - 1) / B;
       nt = s.n ? live_tiles(s.t0, p.window, p.sinks, KT).count : 0;
@@ -131,7 +195,7 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
   const int c = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, H = p.c.heads;
   if (c >= cstart[p.c.slots]) return;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
   const float *k = (const float*)p.k, *v = (const float*)p.v, *wv = (const float*)p.w, *q = (const float*)p.q;
   const size_t tok0 = (size_t)sp.q0 + r0;
@@ -155,8 +219,8 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
     sLf[tid] = a;
   }
   __syncthreads();
-  smem_mm<B, B, D, false, true, false>(sW, DS, sW, DS, [&](int i, int j, float x) { sG[i * BS + j] = j < i ? x : 0.f; });
-  smem_mm<B, B, D, false, true, false>(sW, DS, sK, DS, [&](int i, int j, float x) { sN[i * BS + j] = j < i ? x : 0.f; });
+  product<B, B, D, false, true>(sW, DS, sW, DS, [&](int i, int j, float x) { sG[i * BS + j] = j < i ? x : 0.f; });
+  product<B, B, D, false, true>(sW, DS, sK, DS, [&](int i, int j, float x) { sN[i * BS + j] = j < i ? x : 0.f; });
   __syncthreads();
   // U by forward substitution, one column per lane: u_i = beta_i (e_i - sum_{m<i} G_im u_m)
   if (tid < 32) {
@@ -176,14 +240,14 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
     for (int i = 0; i < 32; ++i) sU[i * BS + tid] = u[i];
   }
   __syncthreads();
-  smem_mm<B, B, B, false, false, false>(sU, BS, sN, BS, [&](int i, int j, float x) { sX[i * BS + j] = x; });
-  smem_mm<B, D, B, true, false, false>(sU, BS, sW, DS, [&](int m, int n, float x) { sY[m * DS + n] = x; });
+  product<B, B, B, false, false>(sU, BS, sN, BS, [&](int i, int j, float x) { sX[i * BS + j] = x; });
+  product<B, D, B, true, false>(sU, BS, sW, DS, [&](int m, int n, float x) { sY[m * DS + n] = x; });
   __syncthreads();
   {
     float* kr = (float*)(ws + w.kr) + ((size_t)c * H + h) * B * D;
     float* f = (float*)(ws + w.f) + ((size_t)c * H + h) * D * D;
-    smem_mm<B, D, B, true, false, false>(sX, BS, sW, DS, [&](int j, int n, float x) { kr[j * D + n] = sK[j * DS + n] - x; });
-    smem_mm<D, D, B, true, false, false>(sW, DS, sY, DS, [&](int n, int x, float y) { f[n * D + x] = (n == x ? 1.f : 0.f) - y; });
+    product<B, D, B, true, false>(sX, BS, sW, DS, [&](int j, int n, float x) { kr[j * D + n] = sK[j * DS + n] - x; });
+    product<D, D, B, true, false>(sW, DS, sY, DS, [&](int n, int x, float y) { f[n * D + x] = (n == x ? 1.f : 0.f) - y; });
     if (p.log_f && tid < B) ((float*)(ws + w.fa))[((size_t)c * H + h) * B + tid] = sLf[tid];
     if (p.log_f && tid == 0) ((float*)(ws + w.ft))[(size_t)c * H + h] = sLf[B - 1];
   }
@@ -195,15 +259,15 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
       sQ[r * DS + x] = r < rows ? (q[((tok0 + r) * p.hq + qh) * D + x]) : 0.f;
     }
     __syncthreads();
-    smem_mm<B, B, D, false, true, false>(sQ, DS, sW, DS, [&](int i, int j, float x) { sM1[i * BS + j] = j <= i ? x : 0.f; });
-    smem_mm<B, B, D, false, true, false>(sQ, DS, sK, DS, [&](int i, int j, float x) { sS[i * BS + j] = x; });
+    product<B, B, D, false, true>(sQ, DS, sW, DS, [&](int i, int j, float x) { sM1[i * BS + j] = j <= i ? x : 0.f; });
+    product<B, B, D, false, true>(sQ, DS, sK, DS, [&](int i, int j, float x) { sS[i * BS + j] = x; });
     __syncthreads();
-    smem_mm<B, B, B, false, false, false>(sM1, BS, sU, BS, [&](int i, int j, float x) { sA[i * BS + j] = x; });
-    smem_mm<B, B, B, false, false, false>(sM1, BS, sX, BS, [&](int i, int j, float x) { sS[i * BS + j] -= x; });
+    product<B, B, B, false, false>(sM1, BS, sU, BS, [&](int i, int j, float x) { sA[i * BS + j] = x; });
+    product<B, B, B, false, false>(sM1, BS, sX, BS, [&](int i, int j, float x) { sS[i * BS + j] -= x; });
     __syncthreads();
     const size_t row = ((size_t)c * p.hq + qh) * B;
     float* z = (float*)(ws + w.z) + row * D;
-    smem_mm<B, D, B, false, false, false>(sA, BS, sW, DS, [&](int i, int n, float x) { z[i * D + n] = sQ[i * DS + n] - x; });
+    product<B, D, B, false, false>(sA, BS, sW, DS, [&](int i, int n, float x) { z[i * D + n] = sQ[i * DS + n] - x; });
     // softmax of the diagonal chunk: 8 threads per row (log2 domain)
     const int r = tid >> 3, sub = tid & 7;
     float mx = -INFINITY;
@@ -229,7 +293,7 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
     }
     __syncthreads();
     float* acc = (float*)(ws + w.acc) + row * D;
-    smem_mm<B, D, B, false, false, false>(sS, BS, sV, DS, [&](int i, int n, float x) { acc[i * D + n] = x; });
+    product<B, D, B, false, false>(sS, BS, sV, DS, [&](int i, int n, float x) { acc[i * D + n] = x; });
   }
 }
 
@@ -278,7 +342,7 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads, h = qh / p.G;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   const int lc = c - cstart[b], rows = min(B, sp.n - lc * B);
   const size_t row = ((size_t)c * p.hq + qh) * B;
   float* z = (float*)(ws + w.z) + row * D;
@@ -313,7 +377,7 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     }
     for (int e = tid; e < D * D; e += NT) sF[(e / D) * DS + e % D] = f[e];
     __syncthreads();
-    smem_mm<B, B, D, false, true, false>(sZ, DS, sK, DS, [&](int i, int j, float x) {
+    product<B, B, D, false, true>(sZ, DS, sK, DS, [&](int i, int j, float x) {
       float s = -INFINITY;
       const int jn = c2 * B + j, in = lc * B + i;
       if (i < rows && sees(p.window, p.sinks, sp.t0 + in, sp.t0 + jn)) {
@@ -322,10 +386,10 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
       }
       sP[i * KS + j] = s;
     });
-    smem_mm<B, D, D, false, true, false>(sZ, DS, sF, DS, [&](int i, int n, float x) { sZn[i * DS + n] = x; });
+    product<B, D, D, false, true>(sZ, DS, sF, DS, [&](int i, int n, float x) { sZn[i * DS + n] = x; });
     __syncthreads();
     softmax_step<D>(sP, KS, B, sM, sAcc, DS);
-    smem_mm<B, D, B, false, false, false>(sP, KS, sV, DS, [&](int i, int n, float x) { sAcc[i * DS + n] += x; });
+    product<B, D, B, false, false>(sP, KS, sV, DS, [&](int i, int n, float x) { sAcc[i * DS + n] += x; });
     if (p.log_f && tid < B) sM[2 * B + tid] += ft[cc];
     float* t = sZ; sZ = sZn; sZn = t;
   }
@@ -348,7 +412,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   float *sR = sm, *sF = sR + D * DS, *sK = sF + D * DS;
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads;
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   if (sp.n == 0) return;
   const int nc = cstart[b + 1] - cstart[b];
   float* kp = (float*)p.c.k_pool;
@@ -383,7 +447,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     for (int e = tid; e < B * D; e += NT) sK[(e / D) * DS + e % D] = kr[e];
     for (int e = tid; e < D * D; e += NT) sF[(e / D) * DS + e % D] = f[e];
     __syncthreads();
-    smem_mm<B, D, D, false, false, false>(sK, DS, sR, DS, [&](int i, int n, float x) {
+    product<B, D, D, false, false>(sK, DS, sR, DS, [&](int i, int n, float x) {
       if (i < rows) {
         const long long at = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0 + lc * B + i);
         if (at >= 0) kp[at * D + n] = (lc == nc - 1 ? sK[i * DS + n] : x);
@@ -391,7 +455,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
       }
     });
     // R <- F_c R, by way of M's place in global memory until every thread has read R
-    smem_mm<D, D, D, false, false, false>(sF, DS, sR, DS, [&](int i, int n, float x) { mm[i * D + n] = x; });
+    product<D, D, D, false, false>(sF, DS, sR, DS, [&](int i, int n, float x) { mm[i * D + n] = x; });
     __syncthreads();
     for (int e = tid; e < D * D; e += NT) sR[(e / D) * DS + e % D] = mm[e];
   }
@@ -432,7 +496,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
   const int c = blockIdx.x, qh = blockIdx.y, split = blockIdx.z, tid = threadIdx.x;
   if (c >= cstart[p.c.slots]) return;
   const int h = qh / p.G, b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
   const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, KT);
   const int per = (lt.count + w.nsplit - 1) / w.nsplit;
@@ -489,7 +553,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
       if ((tid & 7) == 0) sB[r] = any ? (p.log_f ? a_last - p.c.a_pool[va] : 0.f) : -INFINITY;
     }
     __syncthreads();
-    smem_mm<B, KT, D, false, true, false>(sZ, DS, sK, DS, [&](int r, int j, float x) {
+    product<B, KT, D, false, true>(sZ, DS, sK, DS, [&](int r, int j, float x) {
       float s = -INFINITY;
       if (r < rows && sB[j] != -INFINITY && sees(p.window, p.sinks, sp.t0 + r0 + r, j0 + j))
         s = x * p.scl + (sB[j] + sM[2 * B + r]) * kLog2e;
@@ -497,7 +561,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
     });
     __syncthreads();
     softmax_step<D>(sP, KS, KT, sM, sAcc, DS);
-    smem_mm<B, D, KT, false, false, false>(sP, KS, sV, DS, [&](int r, int n, float x) { sAcc[r * DS + n] += x; });
+    product<B, D, KT, false, false>(sP, KS, sV, DS, [&](int r, int n, float x) { sAcc[r * DS + n] += x; });
   }
   __syncthreads();
   for (int e = tid; e < B * D; e += NT) acc[e] = sAcc[(e / D) * DS + e % D];
@@ -526,7 +590,7 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
     const int nt = tstart[b + 1] - tstart[b];
     const long long in = u - (long long)tstart[b] * H;
     const int h = (int)(in / nt), i = (int)(in % nt);
-    const SlotSpan sp = slot_span(p, b);
+    const SlotSpan sp = chunk_span(p, b);
     const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, KT);
     const int j0 = live_tile(lt, i) * KT;
     __syncthreads();
@@ -541,7 +605,7 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
       for (int x = tid & 7; x < D; x += 8) sK[r * DS + x] = at >= 0 ? (kp[at * D + x]) : 0.f;
     }
     __syncthreads();
-    smem_mm<KT, D, D, false, false, false>(sK, DS, sMm, DS, [&](int r, int n, float x) {
+    product<KT, D, D, false, false>(sK, DS, sMm, DS, [&](int r, int n, float x) {
       if (keep(j0 + r)) {
         const long long at = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j0 + r);
         if (at >= 0) kp[at * D + n] = (x);
@@ -558,7 +622,7 @@ __global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const
   const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (c >= cstart[p.c.slots]) return;
   const int b = owner(cstart, p.c.slots, c);
-  const SlotSpan sp = slot_span(p, b);
+  const SlotSpan sp = chunk_span(p, b);
   const int r0 = (c - cstart[b]) * B, rows = min(B, sp.n - r0);
   const float *gm = (const float*)(ws + w.m), *gl = (const float*)(ws + w.l), *ga = (const float*)(ws + w.acc);
   const size_t stride = (size_t)w.nch * p.hq * B;
@@ -616,16 +680,17 @@ cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st) {
 }
 
 size_t paged_ws_bytes(const PagedArgs& p) {
-  if (p.c.cache_dtype != PATH_BF16) return paged_chunk_ws_bytes(p);
-  return paged_token_ws_bytes(p) + (p.max_new > 1 && !paged_drafts(p) ? paged_new_ws_bytes(p) : 0);
+  size_t n = paged_token_ws_bytes(p);
+  if (p.max_new > 1 && !paged_drafts(p)) n += p.c.cache_dtype == PATH_BF16 ? paged_new_ws_bytes(p) : paged_chunk_ws_bytes(p);
+  return n;
 }
 cudaError_t launch_paged(const PagedArgs& p, char* ws, cudaStream_t st) {
-  if (p.c.cache_dtype != PATH_BF16) return launch_paged_chunk(p, ws, st);
   const cudaError_t e = launch_paged_token(p, ws, st);
   if (e != cudaSuccess || p.max_new <= 1 || paged_drafts(p)) return e;
   PagedArgs more = p;
   more.min_new = 2;
-  return launch_paged_new(more, ws + paged_token_ws_bytes(p), st);
+  char* rest = ws + paged_token_ws_bytes(p);
+  return p.c.cache_dtype == PATH_BF16 ? launch_paged_new(more, rest, st) : launch_paged_chunk(more, rest, st);
 }
 
 }  // namespace pathattn

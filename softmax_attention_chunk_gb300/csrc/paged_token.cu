@@ -1,4 +1,4 @@
-// Paged serving of bf16 caches, few new tokens per slot (one token, or draft tokens): one pass over the
+// Paged serving, few new tokens per slot (one token, or, bf16, draft tokens): one pass over the
 // cache that reads every key and value once and writes every key once.
 //
 // Mathematics: as in paged_chunk.cu, with the slot's n <= 16 new tokens as a single chunk.  Per key head
@@ -835,7 +835,7 @@ constexpr int merge_columns(int D, int cols) {  // a power of two, at most the g
   while (cs < cols && cs < MT / (D / 4) / 4) cs *= 2;
   return cs;
 }
-template <int D>
+template <typename T, int D>
 __global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w, const char* __restrict__ ws, int mode, int warps,
                                                          int cs) {
   chain();
@@ -895,10 +895,185 @@ __global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w,
         l += s_l[gr + y * cs];
       }
       const float inv = 1.f / l;
-      __nv_bfloat16* o = (__nv_bfloat16*)p.o + (((size_t)sp.q0 + col / p.G) * p.hq + h * p.G + col % p.G) * D + 4 * x;
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack2(a.x * inv, a.y * inv), pack2(a.z * inv, a.w * inv));
+      T* o = (T*)p.o + (((size_t)sp.q0 + col / p.G) * p.hq + h * p.G + col % p.G) * D + 4 * x;
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(o) = make_uint2(pack2(a.x * inv, a.y * inv), pack2(a.z * inv, a.w * inv));
+      else *reinterpret_cast<float4*>(o) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     }
   }
+}
+
+// ---- one token per slot, fp32 caches ----
+// The same runs of units on the CUDA cores (12 D bytes per cached row and head): D / 4 lanes share a row, 16 bytes each;
+// z . k, w . k and the softmax in fp32.  GP: query heads per key head, rounded up to a power of two.
+constexpr int blocks32(int D, int gp) { return gp <= 4 ? blocks_per_sm(D, 1) : 2; }
+template <int D, int GP, bool FOX>
+__global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
+  chain();
+  __shared__ int s_start[kSmemSlots + 1];
+  constexpr int L = D / 4, RW = 32 / L, AHEAD = 4;  // lanes of a row, rows side by side, row groups on the way
+  const int lane = threadIdx.x & 31, x4 = lane % L * 4, grp = lane / L;
+  const int warp = blockIdx.x * WARPS + (threadIdx.x >> 5), warps = gridDim.x * WARPS;
+  const int H = p.c.heads, G = p.G, P = p.c.page_size;
+  const int* start;
+  if (p.c.slots <= kSmemSlots) {
+    unit_starts<NT>(p, kOnlyOne, blockIdx.x == 0, s_start);
+    start = s_start;
+  } else {
+    start = (const int*)(ws + w.ustart);
+  }
+  const int units = start[p.c.slots], run = run_length(units, warps);
+  const int u0 = warp * run, u1 = min(u0 + run, units);
+  if (u0 >= u1) return;
+  auto ld4 = [](const float* q) { return *reinterpret_cast<const float4*>(q); };
+  auto dot4 = [](const float4& a, const float4& c) { return a.x * c.x + a.y * c.y + a.z * c.z + a.w * c.w; };
+  float *kpool = (float*)p.c.k_pool, *vpool = (float*)p.c.v_pool;
+  int b = find_slot(start, p.c.slots, u0);
+  int u = u0;
+  while (u < u1) {
+    while (start[b + 1] <= u) ++b;
+    const SlotSpan sp = slot_span(p, b);
+    const LiveTiles lt = live_tiles(sp.t0, p.window, p.sinks, RT);
+    const int per = kSetup + (lt.count > 0 ? lt.count : 1);
+    const int h = (u - start[b]) / per;
+    const int s0 = start[b] + h * per + kSetup, e0 = s0 + per - kSetup;
+    if (u < s0) u = s0;
+    if (u >= u1) break;
+    const int ue = e0 < u1 ? e0 : u1;
+    const bool head = u == s0;  // this run has the item's first unit: the new token itself
+    const size_t tok = (size_t)sp.q0 * H + h;
+    const float beta = clamp_beta(p.beta[tok]);
+    const float4 wv = ld4((const float*)p.w + tok * D + x4), kv = ld4((const float*)p.k + tok * D + x4);
+    const float4 vv = ld4((const float*)p.v + tok * D + x4);
+    float a_last = 0.f, lf = 0.f;
+    if (FOX) {
+      lf = p.log_f[tok];
+      const long long r = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
+      if (r >= 0) a_last = p.c.a_pool[r];
+    }
+    float4 z[GP], acc[GP];
+    float m[GP], l[GP];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      const float4 q = g < G ? ld4((const float*)p.q + ((size_t)sp.q0 * p.hq + h * G + g) * D + x4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float c = beta * group_sum<L>(dot4(q, wv)), s = group_sum<L>(dot4(q, kv)) * p.scl;
+      z[g] = make_float4(q.x - c * wv.x, q.y - c * wv.y, q.z - c * wv.z, q.w - c * wv.w);
+      const bool mine = head && grp == 0;
+      m[g] = mine ? s : -INFINITY;
+      l[g] = mine ? 1.f : 0.f;
+      acc[g] = mine ? vv : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (head) {
+      const long long kr = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0);
+      const long long vr = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0);
+      if (kr < 0 || vr < 0) {
+        if (lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+      } else {
+        if (grp == 0) {
+          *reinterpret_cast<float4*>(kpool + kr * D + x4) = kv;
+          *reinterpret_cast<float4*>(vpool + vr * D + x4) = vv;
+        }
+        if (FOX && lane == 0) p.c.a_pool[vr] = a_last + lf;
+      }
+    }
+    const int i0 = u - s0, i1 = lt.count > 0 ? ue - s0 : i0;
+    for (int i = i0; i < i1; ++i) {
+      const int j0 = newest_tile(lt, i) * RT;
+      const int kp = __ldg(p.c.k_table + (size_t)b * p.c.table_width + j0 / P);
+      const int vp = __ldg(p.c.v_table + (size_t)b * p.c.table_width + j0 / P);
+      if ((unsigned)kp >= (unsigned)p.c.k_pages || (unsigned)vp >= (unsigned)p.c.v_pages) {
+        if (lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+        continue;
+      }
+      float* krow = kpool + (((long long)kp * H + h) * P + j0 % P) * D + x4;
+      const long long vr0 = ((long long)vp * H + h) * P + j0 % P;
+      const float* vrow = vpool + vr0 * D + x4;
+#pragma unroll 1
+      for (int r0 = 0; r0 < RT; r0 += AHEAD * RW) {
+        float4 kk[AHEAD], va[AHEAD];
+        float aj[AHEAD];
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+          const int r = r0 + e * RW + grp;
+          kk[e] = ld4(krow + (size_t)r * D);
+          va[e] = ld4(vrow + (size_t)r * D);
+          aj[e] = FOX ? p.c.a_pool[vr0 + r] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+          const int r = r0 + e * RW + grp, j = j0 + r;
+          const float c = beta * group_sum<L>(dot4(kk[e], wv));
+          float s[GP];
+#pragma unroll
+          for (int g = 0; g < GP; ++g) s[g] = group_sum<L>(dot4(kk[e], z[g])) * p.scl;
+          if (j < sp.t0 && sees(p.window, p.sinks, sp.t0 + 1, j))
+            *reinterpret_cast<float4*>(krow + (size_t)r * D) =
+                make_float4(kk[e].x - c * wv.x, kk[e].y - c * wv.y, kk[e].z - c * wv.z, kk[e].w - c * wv.w);
+          if (j < sp.t0 && sees(p.window, p.sinks, sp.t0, j)) {  // (uniform in the row's lanes)
+            const float bias = FOX ? (a_last - aj[e] + lf) * kLog2e : 0.f;
+#pragma unroll
+            for (int g = 0; g < GP; ++g) {
+              const float v = s[g] + bias, mn = fmaxf(m[g], v);
+              const float f = fast_exp2(m[g] - mn), pr = fast_exp2(v - mn);
+              m[g] = mn;
+              l[g] = l[g] * f + pr;
+              acc[g] = make_float4(acc[g].x * f + pr * va[e].x, acc[g].y * f + pr * va[e].y, acc[g].z * f + pr * va[e].z,
+                                   acc[g].w * f + pr * va[e].w);
+            }
+          }
+        }
+      }
+    }
+    const bool complete = head && ue == e0;
+    const size_t slot = ((size_t)2 * warp + (u0 >= s0 - kSetup ? 0 : 1)) * w.nq;
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      if (RW == 2) {  // the two rows' states
+        const float mo = __shfl_xor_sync(0xffffffffu, m[g], 16), M = fmaxf(m[g], mo);
+        const float f = m[g] == -INFINITY ? 0.f : fast_exp2(m[g] - M);
+        l[g] *= f;
+        acc[g] = make_float4(acc[g].x * f, acc[g].y * f, acc[g].z * f, acc[g].w * f);
+        m[g] = M;
+        l[g] += __shfl_xor_sync(0xffffffffu, l[g], 16);
+        acc[g].x += __shfl_xor_sync(0xffffffffu, acc[g].x, 16);
+        acc[g].y += __shfl_xor_sync(0xffffffffu, acc[g].y, 16);
+        acc[g].z += __shfl_xor_sync(0xffffffffu, acc[g].z, 16);
+        acc[g].w += __shfl_xor_sync(0xffffffffu, acc[g].w, 16);
+      }
+      if (g >= G || grp != 0) continue;
+      if (complete) {
+        const float inv = 1.f / l[g];
+        *reinterpret_cast<float4*>((float*)p.o + ((size_t)sp.q0 * p.hq + h * G + g) * D + x4) =
+            make_float4(acc[g].x * inv, acc[g].y * inv, acc[g].z * inv, acc[g].w * inv);
+      } else {
+        if (x4 == 0) {
+          ((float*)(ws + w.m))[slot + g] = m[g];
+          ((float*)(ws + w.l))[slot + g] = l[g];
+        }
+        *reinterpret_cast<float4*>((float*)(ws + w.acc) + (slot + g) * D + x4) = acc[g];
+      }
+    }
+    u = ue;
+  }
+}
+template <int D, int GP, bool FOX>
+cudaError_t token32_t(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
+  cudaError_t e;
+  if (p.c.slots > kSmemSlots &&
+      (e = launch_chained(unit_starts_kernel, 1, 1024, 0, st, p, (int)kOnlyOne, (int*)(ws + w.ustart))) != cudaSuccess)
+    return e;
+  const int blocks = w.blocks < 152 * blocks32(D, GP) ? w.blocks : 152 * blocks32(D, GP);
+  if ((e = launch_chained(token32_kernel<D, GP, FOX>, blocks, NT, 0, st, p, w, ws)) != cudaSuccess) return e;
+  const int cs = merge_columns(D, p.G);
+  return launch_chained(token_merge_kernel<float, D>, dim3(p.c.slots, p.c.heads, (p.G + cs - 1) / cs), MT, 0, st, p, w, ws,
+                        (int)kOnlyOne, blocks * WARPS, cs);
+}
+template <int D, bool FOX>
+cudaError_t token32_d(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
+  if (p.G == 1) return token32_t<D, 1, FOX>(p, w, ws, st);
+  if (p.G == 2) return token32_t<D, 2, FOX>(p, w, ws, st);
+  if (p.G <= 4) return token32_t<D, 4, FOX>(p, w, ws, st);
+  if (p.G <= 8) return token32_t<D, 8, FOX>(p, w, ws, st);
+  return token32_t<D, 16, FOX>(p, w, ws, st);
 }
 
 template <int D, int NQ8, int NT8, bool FOX>
@@ -917,7 +1092,7 @@ cudaError_t token_t(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t
   }
   if ((e = launch_chained(token_kernel<D, NQ8, NT8, FOX>, w.blocks, NT, 0, st, p, w, ws)) != cudaSuccess) return e;
   const int cols = (ONE ? 1 : p.max_new) * p.G, cs = merge_columns(D, cols);
-  return launch_chained(token_merge_kernel<D>, dim3(p.c.slots, p.c.heads, (cols + cs - 1) / cs), MT, 0, st, p, w, ws, mode,
+  return launch_chained(token_merge_kernel<__nv_bfloat16, D>, dim3(p.c.slots, p.c.heads, (cols + cs - 1) / cs), MT, 0, st, p, w, ws, mode,
                         w.blocks * WARPS, cs);
 }
 template <int D, bool FOX>
@@ -932,11 +1107,15 @@ cudaError_t token_d(const PagedArgs& p, const TokenWs& w, bool drafts, char* ws,
 
 }  // namespace
 
-bool paged_drafts(const PagedArgs& p) { return p.max_new > 1 && p.max_new <= DN && p.max_new * p.G <= 32; }
+bool paged_drafts(const PagedArgs& p) { return p.c.cache_dtype == PATH_BF16 && p.max_new > 1 && p.max_new <= DN && p.max_new * p.G <= 32; }
 size_t paged_token_ws_bytes(const PagedArgs& p) { return token_ws(p, paged_drafts(p) ? p.max_new : 1).total; }
 cudaError_t launch_paged_token(const PagedArgs& p, char* ws, cudaStream_t st) {
   const bool drafts = paged_drafts(p), fox = p.log_f != nullptr;
   const TokenWs w = token_ws(p, drafts ? p.max_new : 1);
+  if (p.c.cache_dtype != PATH_BF16) {
+    if (p.c.head_dim == kHeadDim) return fox ? token32_d<kHeadDim, true>(p, w, ws, st) : token32_d<kHeadDim, false>(p, w, ws, st);
+    return fox ? token32_d<kHeadDimWide, true>(p, w, ws, st) : token32_d<kHeadDimWide, false>(p, w, ws, st);
+  }
   if (p.c.head_dim == kHeadDim)
     return fox ? token_d<kHeadDim, true>(p, w, drafts, ws, st) : token_d<kHeadDim, false>(p, w, drafts, ws, st);
   return fox ? token_d<kHeadDimWide, true>(p, w, drafts, ws, st) : token_d<kHeadDimWide, false>(p, w, drafts, ws, st);
