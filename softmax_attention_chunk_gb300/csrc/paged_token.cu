@@ -1100,14 +1100,23 @@ cudaError_t token_d(const PagedArgs& p, const TokenWs& w, bool drafts, char* ws,
   if (!drafts) return w.nq == 8 ? token_t<D, 1, 0, FOX>(p, w, ws, st) : token_t<D, 2, 0, FOX>(p, w, ws, st);
   if (p.max_new <= 8) {
     if (w.nq == 8) return token_t<D, 1, 1, FOX>(p, w, ws, st);
-    return w.nq == 16 ? token_t<D, 2, 1, FOX>(p, w, ws, st) : token_t<D, 4, 1, FOX>(p, w, ws, st);
+    if (w.nq == 16) return token_t<D, 2, 1, FOX>(p, w, ws, st);
+    if constexpr (D == 64) return token_t<D, 4, 1, FOX>(p, w, ws, st);
   }
-  return w.nq == 16 ? token_t<D, 2, 2, FOX>(p, w, ws, st) : token_t<D, 4, 2, FOX>(p, w, ws, st);
+  return token_t<D, 2, 2, FOX>(p, w, ws, st);
 }
 
 }  // namespace
 
-bool paged_drafts(const PagedArgs& p) { return p.c.cache_dtype == PATH_BF16 && p.max_new > 1 && p.max_new <= DN && p.max_new * p.G <= 32; }
+// Drafts go through the streaming pass while their columns' accumulators and fragments leave it fast enough: 16
+// columns (8 heads x 16 x 2000..8192 rows, 8 tokens, G = 2: head dim 64 102 us against 137 for the prompt chunk path, 128
+// 182 against 216), at head dim 64 up to 8 tokens also 32 (135 against 142).  Beyond that the chunk path's second
+// pass over the keys costs less (32 columns, head dim 128: 337 against 227; 16 tokens, head dim 64: 153 against 138).
+bool paged_drafts(const PagedArgs& p) {
+  if (p.c.cache_dtype != PATH_BF16 || p.max_new <= 1 || p.max_new > DN) return false;
+  const int cols = p.max_new * p.G;
+  return cols <= 16 || (p.c.head_dim == kHeadDim && p.max_new <= 8 && cols <= 32);
+}
 size_t paged_token_ws_bytes(const PagedArgs& p) { return token_ws(p, paged_drafts(p) ? p.max_new : 1).total; }
 cudaError_t launch_paged_token(const PagedArgs& p, char* ws, cudaStream_t st) {
   const bool drafts = paged_drafts(p), fox = p.log_f != nullptr;
