@@ -427,8 +427,10 @@ size_t path_paged_workspace_size(const path_paged_cache_t* cache, const path_pag
  * With H_t = I - beta_t w_t w_t^T, for every token at position p of a slot,
  *   o_p = sum_j softmax_j(scale k_j^T H_{j+1} ... H_p q_p  (+ a_p - a_j)) v_j   over the j <= p it sees;
  * afterwards the new rows are appended (keys transported to the last new token) and every cached key
- * that a later token sees is k_j <- H_last ... H_first k_j, rounded once per call.  Keys that the window
- * hides from every later token are left as they are; their table entries may be -1.
+ * that a later token sees is k_j <- H_last ... H_first k_j, rounded once per call (bf16: once for every
+ * 4096 new tokens of the slot, which are taken in that many passes).  Keys that the window hides from
+ * every later token are left as they are (new ones: as appended, or as the pass stored them); their
+ * table entries may be -1.
  * seq_len is read, not changed (path_paged_advance does that).  The pages must be there
  * (path_pages_reserve).  A slot whose row of q_start or length is bad is left out whole; rows whose
  * page is missing are treated as hidden and are not written; status gets the code.

@@ -95,14 +95,18 @@ def extend_ref(c, scale, window=0, sinks=0):
     return o.view(N, H * G, d), A.view(N, H * G, d), kp, vp, ap
 
 
-def check_extend(c, got, ref, scale, tokens=None):
+def check_extend(c, got, ref, scale, tokens=None, passes=1):
     """Compares o and the pools.  Tolerances, with u half a step of the storage type (bf16: products of bf16
     and TF32 operands, u_t = 2^-11 TF32's half step; fp32: u_t = u):
       o: the output's own rounding u |o|; the probabilities' rounding u A; scores off by at most
          e = scale (u + 4 u_t) |z| |k| (z rounded once; four chained products), which moves o by at most 2 e A;
          fp32 adds the sums of about d + 64 terms and ex2's 2^-22: 256 u in place of the u's.
       norms: roundings are independent, so the 2-norm of the error stays below 2 u |o| (three of them, rms u at
-         most each) and of a key row below u |k| + 2 u_t |k_before| (one rounding, two chained products)."""
+         most each) and of a key row below u |k| + 2 u_t |k_before| (one rounding, two chained products).
+    passes: a bf16 call carries the keys over 4096 tokens of a slot at a time, so that many times are the keys rounded
+    and the chained products behind them made: e's and the key rows' terms take that factor; two passes make the
+    independent roundings of o four, still 2 u |o|."""
+    assert passes in (1, 2)
     dt = c["dtype"]
     u = U[dt]
     o, A, kp, vp, ap = ref
@@ -112,10 +116,10 @@ def check_extend(c, got, ref, scale, tokens=None):
     knorm = max(float(torch.nan_to_num(c["k_pool"].double()).norm(dim=-1).max()), float(c["k"].double().norm(dim=-1).max()))
     zk = scale * float(c["q"].double().norm(dim=-1).max()) * knorm
     if dt == "bf16":
-        e = (u + 4 * 2.0 ** -11) * zk
+        e = passes * (u + 4 * 2.0 ** -11) * zk
         bound = u * o.abs() + (u + 2 * e) * A + 1e-30
         fro = 2 * u
-        kfro = u + 2 * 2.0 ** -11
+        kfro = passes * (u + 2 * 2.0 ** -11)
     else:
         e = 256 * u * max(1.0, zk)
         bound = 256 * u * o.abs() + (256 * u + 2 * e) * A + 1e-30
@@ -133,7 +137,7 @@ def check_extend(c, got, ref, scale, tokens=None):
     rel = float((k - kr).norm() / max(float(kr.norm()), 1e-30))
     assert rel <= kfro, rel
     big = float(kr.norm(dim=-1).max()) if kr.numel() else 0.0
-    assert float((k - kr).abs().max()) <= (u + 8 * (2.0 ** -11 if dt == "bf16" else 16 * u)) * max(big, 1.0)
+    assert float((k - kr).abs().max()) <= passes * (u + 8 * (2.0 ** -11 if dt == "bf16" else 16 * u)) * max(big, 1.0)
     assert torch.equal(torch.isnan(got["v"]), torch.isnan(vp))
     assert torch.equal(torch.nan_to_num(got["v"].double()), torch.nan_to_num(vp))
     if c["fox"]:
