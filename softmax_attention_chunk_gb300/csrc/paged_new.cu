@@ -59,23 +59,30 @@ __device__ __forceinline__ void warp_mm(float (&c)[NT][4], const uint32_t (&a)[K
       mma_bf16(c[n + 1], a[k][0], a[k][1], a[k][2], a[k][3], r[2], r[3]);
     }
 }
+// The same with A a pair (high, rest): every fragment of B is fetched once for both.
+template <int NT, int KS, bool T>
+__device__ __forceinline__ void warp_mm2(float (&c)[NT][4], const uint32_t (&a)[KS][4], const uint32_t (&e)[KS][4], const bf16* b, int ld) {
+  const int lane = threadIdx.x & 31, mat = lane >> 3, row = lane & 7;
+#pragma unroll
+  for (int k = 0; k < KS; ++k)
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t r[4];
+      if (T) ldm4t(r, b + (16 * k + (mat & 1) * 8 + row) * ld + 8 * n + (mat >> 1) * 8);
+      else ldm4(r, b + (8 * n + (mat >> 1) * 8 + row) * ld + 16 * k + (mat & 1) * 8);
+      mma_bf16(c[n], a[k][0], a[k][1], a[k][2], a[k][3], r[0], r[1]);
+      mma_bf16(c[n + 1], a[k][0], a[k][1], a[k][2], a[k][3], r[2], r[3]);
+      mma_bf16(c[n], e[k][0], e[k][1], e[k][2], e[k][3], r[0], r[1]);
+      mma_bf16(c[n + 1], e[k][0], e[k][1], e[k][2], e[k][3], r[2], r[3]);
+    }
+}
 template <int KS>
 __device__ __forceinline__ void load_a(uint32_t (&a)[KS][4], const bf16* t, int ld, int m0) {
   const int lane = threadIdx.x & 31, mat = lane >> 3, row = lane & 7;
 #pragma unroll
   for (int k = 0; k < KS; ++k) ldm4(a[k], t + (m0 + (mat & 1) * 8 + row) * ld + 16 * k + (mat >> 1) * 8);
 }
-// Accumulators as A fragments: rounded, or high + rest.
-template <int KS>
-__device__ __forceinline__ void to_a(uint32_t (&a)[KS][4], const float (&c)[2 * KS][4]) {
-#pragma unroll
-  for (int k = 0; k < KS; ++k) {
-    a[k][0] = pack2(c[2 * k][0], c[2 * k][1]);
-    a[k][1] = pack2(c[2 * k][2], c[2 * k][3]);
-    a[k][2] = pack2(c[2 * k + 1][0], c[2 * k + 1][1]);
-    a[k][3] = pack2(c[2 * k + 1][2], c[2 * k + 1][3]);
-  }
-}
+// Accumulators as A fragments, high + rest.
 template <int KS>
 __device__ __forceinline__ void to_a2(uint32_t (&hi)[KS][4], uint32_t (&lo)[KS][4], const float (&c)[2 * KS][4]) {
 #pragma unroll
@@ -384,8 +391,7 @@ __global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPla
     load_a(al, &s.ul[0][0], LX, m0);
     float x[4][4];
     zero(x);
-    warp_mm<4, 4, true>(x, ah, &s.nh[0][32 * nh], LX);  // X = U N
-    warp_mm<4, 4, true>(x, al, &s.nh[0][32 * nh], LX);
+    warp_mm2<4, 4, true>(x, ah, al, &s.nh[0][32 * nh], LX);  // X = U N
     warp_mm<4, 4, true>(x, ah, &s.nl[0][32 * nh], LX);
     __syncthreads();  // (every warp has read N)
     put_pair(x, &s.nh[0][0], &s.nl[0][0], LX, m0, 32 * nh);
@@ -396,8 +402,7 @@ __global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPla
     put_pair(x, (bf16*)(ws + w.nx) + cc * C * C, (bf16*)nullptr, C, m0, 32 * nh);
     float y[NH][4];
     zero(y);
-    warp_mm<NH, 4, true>(y, ah, &s.w[0][8 * NH * nh], LD);  // U W
-    warp_mm<NH, 4, true>(y, al, &s.w[0][8 * NH * nh], LD);
+    warp_mm2<NH, 4, true>(y, ah, al, &s.w[0][8 * NH * nh], LD);  // U W
 #pragma unroll
     for (int n = 0; n < NH; ++n)
 #pragma unroll
@@ -406,8 +411,7 @@ __global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPla
     load_at(ah, &s.uh[0][0], LX, m0);
     load_at(al, &s.ul[0][0], LX, m0);
     zero(y);
-    warp_mm<NH, 4, true>(y, ah, &s.w[0][8 * NH * nh], LD);  // Y = U^T W
-    warp_mm<NH, 4, true>(y, al, &s.w[0][8 * NH * nh], LD);
+    warp_mm2<NH, 4, true>(y, ah, al, &s.w[0][8 * NH * nh], LD);  // Y = U^T W
     put_pair(y, &s.yh[0][0], &s.yl[0][0], LD, m0, 8 * NH * nh);
   }
   __syncthreads();
@@ -417,8 +421,7 @@ __global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPla
     load_at(al, &s.nl[0][0], LX, m0);
     float y[NH][4];
     zero(y);
-    warp_mm<NH, 4, true>(y, ah, &s.w[0][8 * NH * nh], LD);  // X^T W
-    warp_mm<NH, 4, true>(y, al, &s.w[0][8 * NH * nh], LD);
+    warp_mm2<NH, 4, true>(y, ah, al, &s.w[0][8 * NH * nh], LD);  // X^T W
 #pragma unroll
     for (int n = 0; n < NH; ++n)
 #pragma unroll
@@ -483,8 +486,7 @@ struct Slab {
     for (int n = 0; n < D / 8; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
     fetch_wait();
     __syncthreads();
-    warp_mm<D / 8, D / 16, true>(c, ah, sh, LD);
-    warp_mm<D / 8, D / 16, true>(c, al, sh, LD);
+    warp_mm2<D / 8, D / 16, true>(c, ah, al, sh, LD);
     warp_mm<D / 8, D / 16, true>(c, ah, sl, LD);
   }
   // rows r of `rows` as a pair, or (lo null) rounded
@@ -658,8 +660,9 @@ struct QSmem {
   static constexpr int end1 = kX + C * LX, end2 = kFl + D * LD;
   static constexpr size_t bytes = (size_t)(end1 > end2 ? end1 : end2) * 2;
 };
-// Online softmax of the scores of 64 keys (16 rows per warp, log2 domain, hidden ones -inf): p as A fragments.
-__device__ __forceinline__ void softmax64(float (&s)[8][4], float (&m)[2], float (&l)[2], float (&corr)[2], uint32_t (&pa)[4][4]) {
+// Online softmax of the scores of 64 keys (16 rows per warp, log2 domain, hidden ones -inf): p as pairs of A fragments.
+__device__ __forceinline__ void softmax64(float (&s)[8][4], float (&m)[2], float (&l)[2], float (&corr)[2], uint32_t (&pa)[4][4],
+                                          uint32_t (&pb)[4][4]) {
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     float mx = -INFINITY;
@@ -679,7 +682,7 @@ __device__ __forceinline__ void softmax64(float (&s)[8][4], float (&m)[2], float
     }
     l[y] = l[y] * corr[y] + sum;
   }
-  to_a(pa, s);
+  to_a2(pa, pb, s);
 }
 // The first thread blocks carry keys on (level 2: the longest chains, and independent of the queries).
 template <int D, bool FOX>
@@ -739,7 +742,7 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
       }
   };
   float o[D / 8][4], z[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, corr[2];
-  uint32_t pa[4][4];
+  uint32_t pa[4][4], pb[4][4];
   {
     uint32_t qa[D / 16][4], mh[4][4], ml[4][4];
     load_a(qa, sm + S::kQ, LD, warp * 16);
@@ -756,8 +759,7 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
       for (int e = 0; e < 4; ++e)
         if (8 * n + 2 * t + (e & 1) > ra + (e >> 1) * 8) s1[n][e] = 0.f;  // lower(Q W^T)
     to_a2(mh, ml, s1);
-    warp_mm<8, 4, true>(s, mh, sm + S::kX, LX);
-    warp_mm<8, 4, true>(s, ml, sm + S::kX, LX);
+    warp_mm2<8, 4, true>(s, mh, ml, sm + S::kX, LX);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
@@ -765,14 +767,13 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
         z[2 * k + (y >> 1)][2 * (y & 1)] = lo_f(qa[k][y]);
         z[2 * k + (y >> 1)][2 * (y & 1) + 1] = hi_f(qa[k][y]);
       }
-    warp_mm<D / 8, 4, true>(z, mh, sm + S::kUW, LD);
-    warp_mm<D / 8, 4, true>(z, ml, sm + S::kUW, LD);
+    warp_mm2<D / 8, 4, true>(z, mh, ml, sm + S::kUW, LD);
     finish(s, lc);
-    softmax64(s, m, l, corr, pa);
+    softmax64(s, m, l, corr, pa, pb);
   }
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  warp_mm<D / 8, 4, true>(o, pa, sm + S::kV, LD);
+  warp_mm2<D / 8, 4, true>(o, pa, pb, sm + S::kV, LD);
   for (int x = lc - 1; x >= lc / CPB * CPB; --x) {
     const size_t c2 = (size_t)(c - lc + x) * H + h;
     const bf16* fh = (const bf16*)(ws + w.f) + c2 * D * D;
@@ -781,24 +782,24 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
     fetch<D, LD, WT>(sm + S::T, (const bf16*)p.v + (((size_t)sp.q0 + x * C) * H + h) * D, (size_t)H * D, C, C);
     fetch<D, LD, WT>(sm + S::kFh, fh, D, D, D);
     fetch<D, LD, WT>(sm + S::kFl, fh + (size_t)w.nch * H * D * D, D, D, D);
-    uint32_t za[D / 16][4];
-    to_a(za, z);
+    uint32_t za[D / 16][4], zb[D / 16][4];
+    to_a2(za, zb, z);
     fetch_wait();
     __syncthreads();
     float s[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-    warp_mm<8, D / 16, false>(s, za, sm, LD);
+    warp_mm2<8, D / 16, false>(s, za, zb, sm, LD);
     finish(s, x);
-    softmax64(s, m, l, corr, pa);
+    softmax64(s, m, l, corr, pa, pb);
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] *= corr[e >> 1];
-    warp_mm<D / 8, 4, true>(o, pa, sm + S::T, LD);
+    warp_mm2<D / 8, 4, true>(o, pa, pb, sm + S::T, LD);
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
-    warp_mm<D / 8, D / 16, false>(z, za, sm + S::kFh, LD);
+    warp_mm2<D / 8, D / 16, false>(z, za, zb, sm + S::kFh, LD);
     warp_mm<D / 8, D / 16, false>(z, za, sm + S::kFl, LD);
   }
   const size_t st = ((size_t)c * p.hq + qh) * C;
