@@ -110,13 +110,13 @@ __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.commit_gro
 struct NewWs {
   int nch, nblk;           // chunks and blocks of any legal pass
   size_t cstart, bstart, pstart, ustart, vstart, rstart;  // plan (TcPlan)
-  size_t nx, nuw;          // -X [nch][H][64][64], -U W [nch][H][64][D]
+  size_t nx, nuw;          // -X [nch][H][64][64], -U W [2][nch][H][64][D] (high, rest)
   size_t kr, f;            // K-> [2][nch][H][64][D], F [2][nch][H][D][D] (high, rest)
   size_t ke, fb;           // keys at their block's end [2][nblk][H][256][D], block products [2][nblk][H][D][D]
   size_t gb, mm;           // G_b [2][nblk][H][D][D], M [2][slots][H][D][D]
   size_t ver;              // versions: rows [D]
   size_t cn;               // forget gate: sums since the start of the call [H][nblk * 256]
-  size_t zs, z;            // queries at the block's and at the call's start [H][pairs][256][D]
+  size_t zs, z;            // queries at the block's and at the call's start [2][H][pairs][256][D] (rest: TcPlan)
   size_t m, l, acc;        // the diagonal's state [nch][hq][64](, [D])
   size_t pm, pl, pacc;     // parts of the tensor-core attention
   size_t err, total;
@@ -146,7 +146,7 @@ NewWs new_ws(const PagedArgs& p) {
   w.vstart = take(S1 * 8);
   w.ustart = take(S1 * 8);
   w.nx = take((size_t)w.nch * H * C * C * 2);
-  w.nuw = take((size_t)w.nch * H * C * D * 2);
+  w.nuw = take((size_t)2 * w.nch * H * C * D * 2);
   w.kr = take((size_t)2 * w.nch * H * C * D * 2);
   w.f = take((size_t)2 * w.nch * H * D * D * 2);
   w.ke = take((size_t)2 * w.nblk * H * MB * D * 2);
@@ -155,8 +155,8 @@ NewWs new_ws(const PagedArgs& p) {
   w.mm = take((size_t)2 * p.c.slots * H * D * D * 2);
   w.ver = take((size_t)w.ver_rows * D * 2);
   w.cn = take((size_t)H * w.nblk * MB * 4);
-  w.zs = take((size_t)H * w.pairs * kTcPair * D * 2);
-  w.z = take((size_t)H * w.pairs * kTcPair * D * 2);
+  w.zs = take((size_t)2 * H * w.pairs * kTcPair * D * 2);
+  w.z = take((size_t)2 * H * w.pairs * kTcPair * D * 2);
   w.m = take((size_t)w.nch * hq * C * 4);
   w.l = take((size_t)w.nch * hq * C * 4);
   w.acc = take((size_t)w.nch * hq * C * D * 4);
@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPla
     for (int n = 0; n < NH; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[n][e] = -y[n][e];
-    put_pair(y, (bf16*)(ws + w.nuw) + cc * C * D, (bf16*)nullptr, D, m0, 8 * NH * nh);
+    bf16* uw = (bf16*)(ws + w.nuw) + cc * C * D;
+    put_pair(y, uw, uw + (size_t)w.nch * H * C * D, D, m0, 8 * NH * nh);
     load_at(ah, &s.uh[0][0], LX, m0);
     load_at(al, &s.ul[0][0], LX, m0);
     zero(y);
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(WT) carry_in_block_kernel(PagedArgs p, NewWs w
 template <int D>
 struct QSmem {
   static constexpr int LD = D + 8, LX = C + 8, T = C * LD;  // one [64][D] tile
-  static constexpr int kQ = 0, kW = T, kK = 2 * T, kV = 3 * T, kUW = 4 * T, kX = 5 * T;
+  static constexpr int kQ = 0, kW = T, kK = 2 * T, kV = 3 * T, kUW = 4 * T, kUWl = 5 * T, kX = 6 * T;
   static constexpr int kFh = 2 * T, kFl = kFh + D * LD;     // chain: keys at 0, values at T, F behind them
   static constexpr int end1 = kX + C * LX, end2 = kFl + D * LD;
   static constexpr size_t bytes = (size_t)(end1 > end2 ? end1 : end2) * 2;
@@ -712,6 +713,7 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
   fetch<D, LD, WT>(sm + S::kK, (const bf16*)p.k + (tok * H + h) * D, (size_t)H * D, C, rows);
   fetch<D, LD, WT>(sm + S::kV, (const bf16*)p.v + (tok * H + h) * D, (size_t)H * D, C, rows);
   fetch<D, LD, WT>(sm + S::kUW, (const bf16*)(ws + w.nuw) + cc * C * D, D, C, C);
+  fetch<D, LD, WT>(sm + S::kUWl, (const bf16*)(ws + w.nuw) + ((size_t)w.nch * H + cc) * C * D, D, C, C);
   fetch<C, LX, WT>(sm + S::kX, (const bf16*)(ws + w.nx) + cc * C * C, C, C, C);
   fetch_wait();
   __syncthreads();
@@ -768,6 +770,7 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
         z[2 * k + (y >> 1)][2 * (y & 1) + 1] = hi_f(qa[k][y]);
       }
     warp_mm2<D / 8, 4, true>(z, mh, ml, sm + S::kUW, LD);
+    warp_mm<D / 8, 4, true>(z, mh, sm + S::kUWl, LD);
     finish(s, lc);
     softmax64(s, m, l, corr, pa, pb);
   }
@@ -813,13 +816,21 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
       ((float*)(ws + w.l))[st + r] = ls;
     }
     float* acc = (float*)(ws + w.acc) + (st + r) * D;
-    const size_t zr = (((size_t)h * w.pairs + pl.pstart[b]) * kTcPair + (size_t)(r0 + r) * G + qh % G) * D;
+    const int R = (r0 + r) * G + qh % G;
+    const size_t zr = (((size_t)h * w.pairs + pl.pstart[b]) * kTcPair + R) * D, zstep = (size_t)H * w.pairs * kTcPair * D;
+    const bool rest = D == 64 || sp.n * G - R / kTcPair * kTcPair <= kTcPair / 2;
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) {
       *reinterpret_cast<float2*>(acc + 8 * n + 2 * t) = make_float2(o[n][2 * y], o[n][2 * y + 1]);
-      const uint32_t zz = pack2(z[n][2 * y], z[n][2 * y + 1]);
-      *reinterpret_cast<uint32_t*>((bf16*)(ws + w.zs) + zr + 8 * n + 2 * t) = zz;
-      if (lc < CPB) *reinterpret_cast<uint32_t*>((bf16*)(ws + w.z) + zr + 8 * n + 2 * t) = zz;
+      uint32_t zz, ze;
+      split2(z[n][2 * y], z[n][2 * y + 1], zz, ze);
+      const size_t at = zr + 8 * n + 2 * t;
+      *reinterpret_cast<uint32_t*>((bf16*)(ws + w.zs) + at) = zz;
+      if (lc < CPB) *reinterpret_cast<uint32_t*>((bf16*)(ws + w.z) + at) = zz;
+      if (rest) {
+        *reinterpret_cast<uint32_t*>((bf16*)(ws + w.zs) + zstep + at) = ze;
+        if (lc < CPB) *reinterpret_cast<uint32_t*>((bf16*)(ws + w.z) + zstep + at) = ze;
+      }
     }
   }
 }
@@ -839,20 +850,27 @@ __global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan 
   if (blk == 0 || lp * kTcPair + q * 64 >= sp.n * p.G) return;
   const bf16* gh = (const bf16*)(ws + w.gb) + ((size_t)(pl.bstart[b] + blk) * H + h) * D * D;
   const size_t row = ((size_t)h * w.pairs + pr) * kTcPair + q * 64;
-  bf16* sz = sm + 2 * D * LD;
+  const size_t zstep = (size_t)H * w.pairs * kTcPair * D;
+  const bool rest = D == 64 || sp.n * p.G - lp * kTcPair <= kTcPair / 2;
+  bf16 *sz = sm + 2 * D * LD, *se = sz + 64 * LD;
   fetch<D, LD, WT>(sm, gh, D, D, D);
   fetch<D, LD, WT>(sm + D * LD, gh + (size_t)w.nblk * H * D * D, D, D, D);
   fetch<D, LD, WT>(sz, (const bf16*)(ws + w.zs) + row * D, D, 64, 64);
+  if (rest) fetch<D, LD, WT>(se, (const bf16*)(ws + w.zs) + zstep + row * D, D, 64, 64);
   fetch_wait();
   __syncthreads();
   uint32_t a[D / 16][4];
-  load_a(a, sz, LD, (threadIdx.x >> 5) * 16);
   Slab<D> s;
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n) s.c[n][0] = s.c[n][1] = s.c[n][2] = s.c[n][3] = 0.f;
+  zero(s.c);
+  if (rest) {
+    load_a(a, se, LD, (threadIdx.x >> 5) * 16);
+    warp_mm<D / 8, D / 16, false>(s.c, a, sm, LD);
+  }
+  load_a(a, sz, LD, (threadIdx.x >> 5) * 16);
   warp_mm<D / 8, D / 16, false>(s.c, a, sm, LD);
   warp_mm<D / 8, D / 16, false>(s.c, a, sm + D * LD, LD);
-  s.store((bf16*)(ws + w.z) + row * D, nullptr);
+  bf16* z = (bf16*)(ws + w.z) + row * D;
+  s.store(z, rest ? z + zstep : nullptr);
 }
 
 // ---- merge: the diagonal's state, earlier blocks' parts, cached parts; one warp per (token, query head) ----
@@ -966,7 +984,7 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
   auto qk = fox ? query_kernel<D, true> : query_kernel<D, false>;
   auto sk = start_kernel<D>;
   const size_t s1 = sizeof(PrepSmem<D>), s2 = carry_smem<D>(), s3 = QSmem<D>::bytes;
-  const size_t s4 = (size_t)(2 * D + 64) * (D + 8) * 2;
+  const size_t s4 = (size_t)(2 * D + 128) * (D + 8) * 2;
   const auto big = cudaFuncAttributeMaxDynamicSharedMemorySize;
   if ((e = cudaFuncSetAttribute(prep, big, (int)s1)) != cudaSuccess || (e = cudaFuncSetAttribute(c1, big, (int)s2)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(qk, big, (int)(s3 > s2 ? s3 : s2))) != cudaSuccess ||

@@ -42,8 +42,9 @@ constexpr uint32_t TILE = 128 * 128;        // bytes of a 128 x 64 bf16 tile
 template <int D, bool FOX>
 struct __align__(1024) TcSmem {
   static constexpr int X = D / 64;
-  static constexpr int NBUF = D == 64 ? 10 : FOX ? 4 : 5;  // what 227 KB hold
-  uint8_t z[2][X][TILE];
+  static constexpr int NBUF = D == 64 ? 8 : FOX ? 4 : 5;  // what 227 KB hold
+  static constexpr int ZT = D == 64 ? 4 : 2;  // query tiles: two, and (D = 64) what rounding left of them
+  uint8_t z[ZT][X][TILE];
   uint8_t buf[NBUF][X][TILE];
   float aj[FOX ? NINFO : 1][FOX ? KT : 1];  // forget gate: running sums of the tile's rows
   alignas(16) float kbias[FOX ? 2 : 1][FOX ? 2 : 1][FOX ? KT : 4];  // the softmax threads' key biases (log2 units)
@@ -188,12 +189,14 @@ __global__ void __launch_bounds__(ATHREADS, 1)
       const Segment g = segment_at(p, pl, u, u1, &u);
       if (seg > 0) ok = mbar_wait_lean(&s.z_empty, (seg - 1) & 1, err, 1);
       if (!ok) break;
-      const int tiles = g.rows > 128 ? 2 : 1;
       if (lane == 0) {
-        const int zr = (g.h * pl.pairs + pl.pstart[g.b] + g.pair) * 256;
-        mbar_arrive_expect_tx(&s.z_full, (uint32_t)tiles * X * TILE);
-        for (int t = 0; t < tiles; ++t)
-          for (int x = 0; x < X; ++x) tma_load_2d(s.z[t][x], g.own ? &tm_zs : &tm_z, 64 * x, zr + 128 * t, &s.z_full);
+        // rows 0..127, 128..255 and the rests, or (D = 128) of up to 128 rows the rest in the place of the second tile
+        const int zr = (g.h * pl.pairs + pl.pstart[g.b] + g.pair) * 256, ze = p.c.heads * pl.pairs * 256 + zr;
+        mbar_arrive_expect_tx(&s.z_full, Smem::ZT * X * TILE);
+        for (int i = 0; i < Smem::ZT; ++i)
+          for (int x = 0; x < X; ++x)
+            tma_load_2d(s.z[i][x], g.own ? &tm_zs : &tm_z, 64 * x,
+                        D == 64 ? (i < 2 ? zr : ze) + i % 2 * 128 : i == 0 ? zr : g.rows > 128 ? zr + 128 : ze, &s.z_full);
       }
       ++seg;
       // the pair's first token sees the farthest back
@@ -272,13 +275,19 @@ __global__ void __launch_bounds__(ATHREADS, 1)
     const uint32_t d_s = tbu + COL_S + 128 * uniform(t), d_o = tbu + COL_O + D * uniform(t);
     int n = 0, kk = 0, seg = 0, np = 0, os = 0;  // buffers, key tiles, segments; probability tiles and segments of this tile
     bool ok = true;
-    auto issue_s = [&](int buf) {
+    auto issue_s = [&](int buf, bool rest) {
       const uint64_t za = dz + a_z, kb = dz + a_b + uniform(buf * X * (TILE / 16));
 #pragma unroll
       for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mma_ss_elect(d_s, za + (uint64_t)(x * (TILE / 16) + 2 * k), kb + (uint64_t)(x * (TILE / 16) + 2 * k), idesc_s, (x | k) ? 1u : 0u);
+      if (rest)  // two tiles on, or in the second's place
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss_elect(d_s, za + (uint64_t)((2 + x) * (TILE / 16) + 2 * k), kb + (uint64_t)(x * (TILE / 16) + 2 * k), idesc_s, 1u);
       mma_commit_elect(&s.s_full[t]);
       mma_commit_elect(&s.empty[buf]);
     };
@@ -299,7 +308,8 @@ __global__ void __launch_bounds__(ATHREADS, 1)
       ok = mbar_wait_lean(&s.z_full, seg & 1, err, 4) && mbar_wait_lean(&s.full[n % NBUF], (n / NBUF) & 1, err, 5);
       if (!ok) break;
       tc_fence_after();
-      issue_s(n % NBUF);
+      const bool rest = D == 64 || g.rows <= 128;
+      issue_s(n % NBUF, rest);
       if (nk == 1) mma_commit_elect(&s.z_empty);
       for (int k = 0; ok && k < nk; ++k, ++kk, n += 2) {
         const int vb = (n + 1) % NBUF, nb = (n + 2) % NBUF;
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__(ATHREADS, 1)
           mma_ts_elect(d_o, d_s + 8 * y, vd + (uint64_t)(128 * y), idesc_o, y == 0 ? first : 1u);
         if (k + 1 == nk) mma_commit_elect(&s.o_full[t]);
         if (k + 1 < nk) {
-          issue_s(nb);
+          issue_s(nb, rest);
           if (k + 2 == nk) mma_commit_elect(&s.z_empty);
         }
         mma_commit_elect(&s.empty[vb]);
@@ -727,8 +737,9 @@ cudaError_t attend_t(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
   CUtensorMap mz, mzs, mk, mv, mver, mnew;
   const int P = p.c.page_size, RB = P < KT ? P : KT;
   const uint64_t zrows = (uint64_t)p.c.heads * pl.pairs * kTcPair;
+  const uint64_t zall = 2 * zrows;  // (rounded, rest)
   const bool own = pl.ver_rows > 0;  // (no version rows: no slot has a second block, the maps are not used)
-  if (!make_map(&mz, pl.z, D, zrows, 128) || !make_map(&mzs, pl.zs, D, zrows, 128) ||
+  if (!make_map(&mz, pl.z, D, zall, 128) || !make_map(&mzs, pl.zs, D, zall, 128) ||
       !make_map(&mk, p.c.k_pool, D, (uint64_t)p.c.k_pages * p.c.heads * P, RB) ||
       !make_map(&mv, p.c.v_pool, D, (uint64_t)p.c.v_pages * p.c.heads * P, RB) ||
       !make_map(&mver, own ? pl.ver : pl.z, D, own ? (uint64_t)pl.ver_rows : zrows, KT) ||

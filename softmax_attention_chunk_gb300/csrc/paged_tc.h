@@ -23,7 +23,8 @@ struct TcPlan {
   float *m, *l, *acc;       // parts [..][256](, [D]): thread block c's share of item i is part i + c; the items of
                             // query pair x of the list of all (slot, head, pair): 2 x cached, 2 x + 1 own
   const float* cn;          // sums of log f since the start of the pass [heads][blocks * 256]
-  const void *z, *zs;       // queries at the start of the pass and of their block [heads][pairs][256][D]
+  const void *z, *zs;       // queries at the start of the pass and of their block [rounded, rest][heads][pairs][256][D]; the
+                            // rest at head dim 128 only of pairs with up to 128 rows
   const void* ver;          // version rows
   const void* mm;           // M: [high, rest][slots][heads][D][D]
   long long ver_rows;
