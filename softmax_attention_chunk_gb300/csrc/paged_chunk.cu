@@ -12,6 +12,10 @@
 //
 // Six launches: plan (lengths, chunk list), chunk preparation, then one of {query scan, key walk} per
 // block, cached attention split over key ranges, cached rewrite, and the merge of the splits.
+//
+// Bound: fp32 multiply-adds and shared-memory reads of the products (no fp32 tensor path keeps 24 bits); products keep
+// 2 x 4 results per thread (262 -> 184 us for 3 slots of 5 to 97 tokens over up to 1500 rows x 8 heads, head dim 64:
+// the chain of six launches with few blocks each, every one a chain of products).
 #include "paged.h"
 #include "dev_common.cuh"
 
@@ -130,10 +134,12 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict
   chain();
   __shared__ int wsum[2][32];
   __shared__ int carry[2];
+  __shared__ unsigned long long tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* cstart = plan;
   int* tstart = plan + p.c.slots + 1;
   if (tid < 2) carry[tid] = 0;
+  if (tid == 0) tokens = 0;
   __syncthreads();
   for (int base = 0; base < p.c.slots; base += 1024) {
     const int b = base + tid;
@@ -142,6 +148,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict
       const SlotSpan s = chunk_span(p, b);
       if (s.code) paged_error(p.c.status, s.code);
       nc = (s.n + B - 1) / B;
+      if (s.n) atomicAdd(&tokens, (unsigned long long)s.n);
       nt = s.n ? live_tiles(s.t0, p.window, p.sinks, KT).count : 0;
     }
     int ic = nc, it = nt;
@@ -160,6 +167,12 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict
     __syncthreads();
   }
   if (tid == 0) { cstart[p.c.slots] = carry[0]; tstart[p.c.slots] = carry[1]; }
+  // rows of q_start that overlap: more tokens than the workspace is for
+  if (tokens > (unsigned long long)p.total) {
+    if (tid == 0) paged_error(p.c.status, PATH_PAGED_BAD_START);
+    __syncthreads();
+    for (int b = tid; b <= p.c.slots; b += 1024) cstart[b] = tstart[b] = 0;
+  }
 }
 
 // The slot that owns entry x of a prefix array with x < start[slots].
@@ -413,7 +426,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads;
   const SlotSpan sp = chunk_span(p, b);
-  if (sp.n == 0) return;
+  if (sp.n == 0 || cstart[p.c.slots] == 0) return;
   const int nc = cstart[b + 1] - cstart[b];
   float* kp = (float*)p.c.k_pool;
   float* vp = (float*)p.c.v_pool;
@@ -427,13 +440,30 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     }
     for (int x = tid & 15; x < D; x += 16) vp[at * D + x] = v[(((size_t)sp.q0 + r) * H + h) * D + x];
   }
-  if (p.log_f && tid == 0) {
+  if (p.log_f) {
+    __shared__ float wsum[NT / 32];
     const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
     double a = last >= 0 ? p.c.a_pool[last] : 0.0;
-    for (int r = 0; r < sp.n; ++r) {
-      a += p.log_f[((size_t)sp.q0 + r) * H + h];
-      const long long at = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r);
-      if (at >= 0) p.c.a_pool[at] = (float)a;
+    for (int base = 0; base < sp.n; base += NT) {
+      const int r = base + tid;
+      float x = r < sp.n ? p.log_f[((size_t)sp.q0 + r) * H + h] : 0.f;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((tid & 31) >= o) x += y;
+      }
+      __syncthreads();
+      if ((tid & 31) == 31) wsum[tid >> 5] = x;
+      __syncthreads();
+      float before = 0.f, all = 0.f;
+#pragma unroll
+      for (int i = 0; i < NT / 32; ++i) {
+        if (i < tid >> 5) before += wsum[i];
+        all += wsum[i];
+      }
+      const long long at = r < sp.n ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r) : -1;
+      if (at >= 0) p.c.a_pool[at] = (float)(a + before + x);
+      a += all;
     }
   }
   for (int e = tid; e < D * D; e += NT) sR[(e / D) * DS + e % D] = (e / D == e % D) ? 1.f : 0.f;

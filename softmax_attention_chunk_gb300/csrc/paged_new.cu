@@ -13,12 +13,16 @@
 //    multiplied.
 // So all attention but the 256-token diagonal runs in the tensor-core kernel (paged_tc.cu).
 //
-// Roundings: F, the carried rows and M are held as bf16 pairs (high + rest, about 16 bits; products of three terms),
-// so chains of blocks do not accumulate 8-bit rounding; z, zs, the versions and P are rounded to bf16 once, as
-// tensor-core operands.
+// Roundings: U W, F, the carried rows and M are held as bf16 pairs (high + rest, about 16 bits; products of three
+// terms), and so are z and P within the block, so chains of chunks and blocks do not accumulate 8-bit rounding.  Rounded to bf16
+// once, as tensor-core operands: the versions, X (it moves scores inside one chunk only), and z and P for the rows
+// of earlier blocks and the cached ones as paged_tc.cu says.  Cached keys are exact as stored.
 //
 // These kernels are small next to the attention (2048 tokens, 32 heads, D = 128: about 15 of 1200 GFLOP) and bound
-// by latency, so they run 16x8x16 warp MMAs on tiles in shared memory, one block per chunk, head and task.
+// by latency, so they run 16x8x16 warp MMAs on tiles in shared memory, one block per chunk, head and task.  At that
+// size, over 32768 cached rows, one after the other: preparation 29 us, carrying in the block 29, queries with the
+// carrying on beside them 125 (tensor pipe 41 %, 8 warps per SM), start 23, rewrite 28, merge 34, attention 726; their
+// chained launches overlap to 1003 us for the call.  512 tokens x 32 heads over 8000 at D = 64: 20, 10, 30, 5, 20, 16 and 69.
 #include "paged_tc.h"
 #include "dev_common.cuh"
 #include "mma_common.cuh"
@@ -175,9 +179,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
   chain();
   constexpr int N = 6;
   __shared__ long long wsum[N][32], carry[N];
+  __shared__ unsigned long long tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < N) carry[tid] = 0;
-  if (tid == 0) *pl.err = 0;
+  if (tid == 0) {
+    *pl.err = 0;
+    tokens = 0;
+  }
   __syncthreads();
   for (int base = 0; base < p.c.slots; base += 1024) {
     const int b = base + tid;
@@ -186,6 +194,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
       const SlotSpan s = pass_span(p, b);
       if (report && s.code) paged_error(p.c.status, s.code);
       if (s.n > 0) {
+        atomicAdd(&tokens, (unsigned long long)s.n);
         const long long H = p.c.heads, np = ((long long)s.n * p.G + kTcPair - 1) / kTcPair, nb = (s.n + MB - 1) / MB;
         v[0] = (s.n + C - 1) / C;
         v[1] = nb;
@@ -232,14 +241,23 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
     }
     __syncthreads();
   }
+  const int S = p.c.slots;
   if (tid == 0) {
-    const int S = p.c.slots;
     pl.cstart[S] = (int)carry[0];
     pl.bstart[S] = (int)carry[1];
     pl.pstart[S] = (int)carry[2];
     pl.rstart[S] = (int)carry[3];
     pl.vstart[S] = carry[4];
     pl.ustart[S] = carry[5];
+  }
+  // rows of q_start that overlap: more tokens than the workspace is for
+  if (tokens > (unsigned long long)p.total) {
+    if (tid == 0) paged_error(p.c.status, PATH_PAGED_BAD_START);
+    __syncthreads();
+    for (int b = tid; b <= S; b += 1024) {
+      pl.cstart[b] = pl.bstart[b] = pl.pstart[b] = pl.rstart[b] = 0;
+      pl.vstart[b] = pl.ustart[b] = 0;
+    }
   }
 }
 __device__ __forceinline__ int owner(const int* start, int slots, int x) {
@@ -603,7 +621,7 @@ __device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, 
   __shared__ float wsum[WT / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.c.heads;
   const SlotSpan sp = pass_span(p, b);
-  if (sp.n == 0) return;
+  if (sp.n == 0 || pl.cstart[p.c.slots] == 0) return;
   const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
   const float a0 = last >= 0 ? p.c.a_pool[last] : 0.f;
   float* cn = (float*)(ws + w.cn) + ((size_t)h * w.nblk + pl.bstart[b]) * MB;

@@ -11,10 +11,24 @@
 //   S = Z K^T (both operands in shared memory), softmax by one thread per row, P (bf16) over the first half of S in
 //   TMEM, O += P V with P as the TMEM operand.
 // Warp 8 brings key and value tiles by TMA, one box per page piece (pages of 16 to 256 rows; the 128-byte swizzle
-// repeats every 8 rows), into a ring; warp 9 issues the MMAs and clears value rows that hold no cached token (their
-// probabilities are 0, but 0 times what lies there has to be 0).  The (slot, head, query pair, key tile) units of a
+// repeats every 8 rows), into a ring, newest tiles first (with a forget gate the recent keys hold the maximum: oldest
+// first, the reference rose at every step, 406 -> 296 us for 2048 tokens over 16384 with the gate).  Warps 9 and 10
+// issue the MMAs of one query tile each and clear value rows that hold no cached token (their probabilities are 0,
+// but 0 times what lies there has to be 0).  The (slot, head, query pair, key tile) units of a
 // call are one list cut into equal runs, one per block; a run's share of a query pair leaves its softmax state in
 // a part of the workspace, merged in list order by merge kernel with the new tokens' own state.
+//
+// Roundings: P to bf16 (its row sums are of the unrounded values), as the MMA takes it beside bf16 values.  z is a
+// bf16 pair (rounded, rest; a second product into S) at head dim 64, where the tensor cores have the time (512 tokens over
+// 8000 x 32 heads: 171 -> 179 us for the whole call), and at 128 for pairs of up to 128 rows, whose rest lies in the
+// second tile's place; else it is rounded once.  With both, what is left of o's error is that of two bf16 roundings.
+//
+// Measured: 2048 tokens x 32 heads over 32768 rows at head dim 128 (1.1 TFLOP) 726 us, 1.5 PFLOP/s, 78 % of a large
+// library product (tensor pipe 60 % of its cycles); 2048 x 32 over 16384 at head dim 64 (275 GFLOP) 370 us, 0.74 PFLOP/s:
+// tensor pipe 48 %, exponentials 33 %, issue 39 %, no unit saturated, each tile's chain of score product, softmax and
+// value product a latency.  Tried and slower (the 1.1 TFLOP case's whole call, 1003 us): two threads per row 1441,
+// maximum first and a second pass for the exponentials 1297, loads of the next scores under way 1020, key steps of
+// 64 1027 against 862 at the time; P as a bf16 pair 1707; a third score buffer at head dim 64 gained nothing.
 #include "paged_tc.h"
 #include "dev_common.cuh"
 #include "tc_common.cuh"

@@ -17,6 +17,12 @@
 //    1 to 32 and a trip through shared memory; here the tensor work stays far below the memory time;
 //  * z, P and c are held as bf16 pairs (high + rest, about 16 bits), so that the only rounding to 8 bits is the
 //    one that the cache and the output need: the extra MMAs are free under the memory bound.
+// Measured: 4 x 32 heads x 32000 rows, head dim 64, 252 us (6.2 TB/s, 93 % of a copy's rate); 48 ragged sequences up
+// to 4096 x 8 key heads, head dim 128, 4 heads per key head, 111 us (5.5 TB/s, 82 %: 250 registers leave 8 warps
+// per SM, and a warp's loads wait on one another's tiles).  Value and key pieces through a ring in shared memory
+// (cp.async, 2 to 4 tiles ahead): 278 us in place of 244 for the former's kernel.  16 x 8 heads x 5000 rows, 8 draft
+// tokens of 2 heads, head dim 64: 90 us (floor 38: the two preparing and merging launches, and 12 warps per SM beside
+// 168 registers of operands and accumulators; DRAM 43 %).
 #include "paged.h"
 #include "dev_common.cuh"
 #include "mma_common.cuh"

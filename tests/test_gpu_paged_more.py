@@ -216,3 +216,27 @@ def test_two_captured_steps_of_one_cache(cuda_lib):
         t = [x + 1 for x in t]
     assert cache.seq_len.tolist() == t
     cache.check()
+
+
+@pytest.mark.parametrize("dtype,fox", [("bf16", False), ("bf16", True), ("fp32", True)])
+def test_overlapping_ranges_stay_in_bounds(cuda_lib, dtype, fox):
+    """q_start rows that each look right but name more tokens together than there are: these slots are left out."""
+    c = R.make_case(dtype, 64, 4, 2, 16, [40] * 9, [30] * 9, fox, seed=61, width_slack=30)
+    N = 270
+    bad = dict(c, q_start=torch.tensor([0, N, 0, N, 0, N, 0, N, 0, N], dtype=torch.int32))
+    out = torch.full((N, 4, 64), 3.0, dtype=R.DT[dtype], device=DEV)
+    got, cache = run(bad, 0.125, out=out, max_new=N)
+    assert (got["o"] == 3).all()
+    assert torch.equal(torch.nan_to_num(got["k"]), torch.nan_to_num(c["k_pool"]))
+    with pytest.raises(RuntimeError, match="q_start"):
+        cache.check()
+    got, cache = run(c, 0.125)
+    R.check_extend(c, got, R.extend_ref(c, 0.125), 0.125)
+    cache.check()
+
+
+def test_long_fp32_prompt_with_the_gate(cuda_lib):
+    c = R.make_case("fp32", 64, 2, 1, 16, [70, 5], [600, 300], True, seed=62)
+    got, cache = run(c, 0.125)
+    R.check_extend(c, got, R.extend_ref(c, 0.125), 0.125)
+    cache.check()
