@@ -892,13 +892,16 @@ __global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan 
 }
 
 // ---- merge: the diagonal's state, earlier blocks' parts, cached parts; one warp per (token, query head) ----
+// Bound: the parts' bytes (2048 tokens x 32 heads at head dim 128: 150 MB, from L2), and where there are few chunks the
+// latency of a row's loads.  Rows of a block: a chunk's 64, or 16 below 1024 (chunk, head) pairs (4 x 100 tokens x 8 heads
+// 230 -> 220 us for the call; 16 x 1700 x 32, with 13000 pairs, 1810 with 64 and 1923 with 16).
 constexpr int GT = 256;
 template <int D>
-__global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan pl, const char* __restrict__ ws) {
+__global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan pl, int GR, const char* __restrict__ ws) {
   chain();
   constexpr int L = D / 4, PG = 32 / L;  // lanes of a row; parts summed side by side
-  const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x4 = lane % L * 4, pg = lane / L;
-  if (c == 0 && qh == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
+  const int c = blockIdx.x / (C / GR), qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x4 = lane % L * 4, pg = lane / L;
+  if (blockIdx.x == 0 && qh == 0 && threadIdx.x == 0 && *pl.err) paged_error(p.c.status, PATH_PAGED_WAIT + *pl.err);
   if (c >= pl.cstart[p.c.slots]) return;
   const int b = owner(pl.cstart, p.c.slots, c), H = p.c.heads;
   const SlotSpan sp = pass_span(p, b);
@@ -911,7 +914,7 @@ __global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan 
   int pair = -1, n1 = 0, n = 0;
   long long from1 = 0, from2 = 0;
 #pragma unroll 2
-  for (int r = warp; r < rows; r += GT / 32) {
+  for (int r = blockIdx.x % (C / GR) * GR + warp, r1 = min(rows, r - warp + GR); r < r1; r += GT / 32) {
     const size_t row = ((size_t)c * p.hq + qh) * C + r;
     const int R = (lc * C + r) * p.G + g;
     const float m0 = ((const float*)(ws + w.m))[row], l0 = ((const float*)(ws + w.l))[row];
@@ -1036,8 +1039,9 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
         (e = launch_chained(qk, carries + w.nch * p.hq, WT, s3 > s2 ? s3 : s2, st, p, w, pl, ws)) != cudaSuccess)
       return e;
     if (many && (e = launch_chained(sk, dim3(w.pairs * 4, H), WT, s4, st, p, w, pl, ws)) != cudaSuccess) return e;
+    const int gr = (long long)w.nch * p.hq < 1024 ? 16 : C;
     if ((e = launch_attend_tc(p, pl, st)) != cudaSuccess || (e = launch_rewrite_tc(p, pl, st)) != cudaSuccess ||
-        (e = launch_chained(merge_kernel<D>, dim3(w.nch, p.hq), GT, 0, st, p, w, pl, ws)) != cudaSuccess)
+        (e = launch_chained(merge_kernel<D>, dim3(w.nch * (C / gr), p.hq), GT, 0, st, p, w, pl, gr, ws)) != cudaSuccess)
       return e;
   }
   return cudaSuccess;
