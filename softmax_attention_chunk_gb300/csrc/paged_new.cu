@@ -108,6 +108,10 @@ __device__ __forceinline__ void fetch(bf16* dst, const bf16* src, size_t pitch, 
                  : "memory");
   }
 }
+// Fetches so far form a group; all but the newest N groups have arrived.
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory"); }
 
 // ---- workspace ----
@@ -795,17 +799,29 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
   warp_mm2<D / 8, 4, true>(o, pa, pb, sm + S::kV, LD);
-  for (int x = lc - 1; x >= lc / CPB * CPB; --x) {
-    const size_t c2 = (size_t)(c - lc + x) * H + h;
-    const bf16* fh = (const bf16*)(ws + w.f) + c2 * D * D;
-    __syncthreads();
-    fetch<D, LD, WT>(sm, (const bf16*)(ws + w.kr) + c2 * C * D, D, C, C);
+  // The earlier chunks of the block: keys and values of the next one are fetched while F is applied, its F while the
+  // scores are worked on.
+  const int first = lc / CPB * CPB;
+  auto fetch_rows = [&](int x) {
+    fetch<D, LD, WT>(sm, (const bf16*)(ws + w.kr) + ((size_t)(c - lc + x) * H + h) * C * D, D, C, C);
     fetch<D, LD, WT>(sm + S::T, (const bf16*)p.v + (((size_t)sp.q0 + x * C) * H + h) * D, (size_t)H * D, C, C);
+  };
+  auto fetch_f = [&](int x) {
+    const bf16* fh = (const bf16*)(ws + w.f) + ((size_t)(c - lc + x) * H + h) * D * D;
     fetch<D, LD, WT>(sm + S::kFh, fh, D, D, D);
     fetch<D, LD, WT>(sm + S::kFl, fh + (size_t)w.nch * H * D * D, D, D, D);
+  };
+  if (lc > first) {
+    __syncthreads();
+    fetch_rows(lc - 1);
+    fetch_commit();
+    fetch_f(lc - 1);
+    fetch_commit();
+  }
+  for (int x = lc - 1; x >= first; --x) {
     uint32_t za[D / 16][4], zb[D / 16][4];
     to_a2(za, zb, z);
-    fetch_wait();
+    fetch_wait_but<1>();
     __syncthreads();
     float s[8][4];
 #pragma unroll
@@ -818,10 +834,20 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] *= corr[e >> 1];
     warp_mm2<D / 8, 4, true>(o, pa, pb, sm + S::T, LD);
+    __syncthreads();
+    if (x > first) fetch_rows(x - 1);
+    fetch_commit();
+    fetch_wait_but<1>();
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
     warp_mm2<D / 8, D / 16, false>(z, za, zb, sm + S::kFh, LD);
     warp_mm<D / 8, D / 16, false>(z, za, sm + S::kFl, LD);
+    if (x > first) {
+      __syncthreads();
+      fetch_f(x - 1);
+    }
+    fetch_commit();
   }
   const size_t st = ((size_t)c * p.hq + qh) * C;
 #pragma unroll
