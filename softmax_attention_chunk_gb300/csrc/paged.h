@@ -105,7 +105,9 @@ __device__ __forceinline__ SlotSpan slot_span(const PagedArgs& p, int b) {
 __device__ __forceinline__ void paged_error(int* status, int code) { atomicCAS(status, 0, code); }
 // Programmatic dependent launch: every kernel of a call begins with chain(), which waits until the kernel before it has
 // ended and lets the next one's blocks take their places meanwhile (they wait there).  The first statement of every
-// kernel, for all threads: a grid that ended without having waited would end the chain early.
+// kernel, for all threads: a grid that ended without having waited would end the chain early.  Pointers to what earlier
+// kernels write are not __restrict__ and not read with __ldg: such loads may pass the wait or find a line that the kernel
+// before has left in the read-only path.
 __device__ __forceinline__ void chain() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

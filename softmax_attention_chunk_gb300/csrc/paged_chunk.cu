@@ -130,7 +130,7 @@ __device__ __forceinline__ SlotSpan chunk_span(const PagedArgs& p, int b) {
 }
 
 // First chunk and first live tile of every slot (exclusive prefix sums; entry `slots` holds the totals).
-__global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* __restrict__ plan) {
+__global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* plan) {
   chain();
   __shared__ int wsum[2][32];
   __shared__ int carry[2];
@@ -196,7 +196,7 @@ struct PrepSmem {
 
 // One block per (chunk, key head).
 template <int D>
-__global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+__global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* ws) {
   chain();
   extern __shared__ float sm[];
   using S = PrepSmem<D>;
@@ -500,7 +500,7 @@ constexpr size_t scan_walk_smem() {
 
 // Blocks [0, slots * H) walk keys, the others scan queries.
 template <int D>
-__global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+__global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, char* ws) {
   chain();
   extern __shared__ float sm[];
   const int nw = p.c.slots * p.c.heads;
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, c
 
 // Cached attention: one block per (chunk, query head, key range).
 template <int D>
-__global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char* __restrict__ ws) {
+__global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char* ws) {
   chain();
   extern __shared__ float sm[];
   using S = ScanSmem<D>;
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
 
 // k <- k M for the cached rows that a later token sees: blocks take runs of (live tile, head).
 template <int D>
-__global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, const char* __restrict__ ws) {
+__global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, const char* ws) {
   chain();
   extern __shared__ float sm[];
   constexpr int DS = D + 4;
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
 
 // Merge of the key ranges: one warp per (row, query head).
 template <int D>
-__global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const char* __restrict__ ws) {
+__global__ void __launch_bounds__(NT) merge_kernel(PagedArgs p, ChunkWs w, const char* ws) {
   chain();
   const int* cstart = (const int*)(ws + w.plan);
   const int c = blockIdx.x, qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -315,7 +315,7 @@ __device__ __forceinline__ void put_pair(const float (&c)[NT][4], bf16* hi, bf16
     }
 }
 template <int D>
-__global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+__global__ void __launch_bounds__(PT, 2) prep_kernel(PagedArgs p, NewWs w, TcPlan pl, char* ws) {
   chain();
   extern __shared__ __align__(16) uint8_t smem[];
   using S = PrepSmem<D>;
@@ -660,7 +660,7 @@ __device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, 
 
 // Blocks: (block, head, slab) of level 1, then (slot, head) of the gate's sums.
 template <int D>
-__global__ void __launch_bounds__(WT) carry_in_block_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+__global__ void __launch_bounds__(WT) carry_in_block_kernel(PagedArgs p, NewWs w, TcPlan pl, char* ws) {
   chain();
   extern __shared__ __align__(16) uint8_t smem[];
   const int slabs = CPB + D / 64, H = p.c.heads;
@@ -709,7 +709,7 @@ __device__ __forceinline__ void softmax64(float (&s)[8][4], float (&m)[2], float
 }
 // The first thread blocks carry keys on (level 2: the longest chains, and independent of the queries).
 template <int D, bool FOX>
-__global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+__global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p, NewWs w, TcPlan pl, char* ws) {
   chain();
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* sm = (bf16*)smem;
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(WT, D == 64 ? 3 : 2) query_kernel(PagedArgs p,
 
 // z = zs G_b^T for the query pairs behind the first block: one block per (64 rows of a pair, head).
 template <int D>
-__global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan pl, char* __restrict__ ws) {
+__global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan pl, char* ws) {
   chain();
   extern __shared__ __align__(16) uint8_t smem[];
   bf16* sm = (bf16*)smem;
@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(WT) start_kernel(PagedArgs p, NewWs w, TcPlan 
 // 230 -> 220 us for the call; 16 x 1700 x 32, with 13000 pairs, 1810 with 64 and 1923 with 16).
 constexpr int GT = 256;
 template <int D>
-__global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan pl, int GR, const char* __restrict__ ws) {
+__global__ void __launch_bounds__(GT) merge_kernel(PagedArgs p, NewWs w, TcPlan pl, int GR, const char* ws) {
   chain();
   constexpr int L = D / 4, PG = 32 / L;  // lanes of a row; parts summed side by side
   const int c = blockIdx.x / (C / GR), qh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x4 = lane % L * 4, pg = lane / L;

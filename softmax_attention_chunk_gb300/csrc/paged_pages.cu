@@ -79,7 +79,7 @@ __device__ int block_scan(int x, BlockScan& s, int* total) {
 
 // The numbers of the first `need` pages with ref == 0, in rising order, into out; returns how many were
 // found (fewer: the pool has no more).
-__device__ int lowest_free(const int* __restrict__ ref, int pages, int need, int* __restrict__ out, BlockScan& s) {
+__device__ int lowest_free(const int* ref, int pages, int need, int* out, BlockScan& s) {
   constexpr int PER = 8;
   int have = 0;
   for (int base = 0; base < pages && have < need; base += NT * PER) {
@@ -104,7 +104,7 @@ __device__ int lowest_free(const int* __restrict__ ref, int pages, int need, int
 }
 
 // Whether an entry of list[0, count) is no slot, is listed twice, or has not seq_len >= 0 (used) or < 0.
-__device__ bool bad_slots(const int* __restrict__ list, int count, const int* __restrict__ seq_len, int slots, bool used,
+__device__ bool bad_slots(const int* list, int count, const int* seq_len, int slots, bool used,
                           unsigned* seen) {
   for (int i = threadIdx.x; i < (slots + 31) / 32; i += NT) seen[i] = 0;
   __syncthreads();
@@ -122,7 +122,7 @@ __device__ bool bad_slots(const int* __restrict__ list, int count, const int* __
 }
 
 // ---------------- reserve ----------------
-__global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const int* __restrict__ n_new, Lists w) {
+__global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const int* n_new, Lists w) {
   chain();
   __shared__ BlockScan s;
   __shared__ int code;
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const
 }
 
 // ---------------- fork ----------------
-__global__ void __launch_bounds__(NT) fork_kernel(path_paged_cache_t c, const int* __restrict__ parents,
-                                                  const int* __restrict__ children, int count, Lists w) {
+__global__ void __launch_bounds__(NT) fork_kernel(path_paged_cache_t c, const int* parents,
+                                                  const int* children, int count, Lists w) {
   chain();
   __shared__ BlockScan s;
   __shared__ unsigned seen[(kMaxSlots + 31) / 32];
@@ -322,7 +322,7 @@ __device__ __forceinline__ void drop(const path_paged_cache_t& c, int b, int x) 
   *kt = -1;
   *vt = -1;
 }
-__global__ void __launch_bounds__(NT) free_kernel(path_paged_cache_t c, const int* __restrict__ list, int count) {
+__global__ void __launch_bounds__(NT) free_kernel(path_paged_cache_t c, const int* list, int count) {
   chain();
   __shared__ unsigned seen[(kMaxSlots + 31) / 32];
   if (bad_slots(list, count, c.seq_len, c.slots, true, seen)) {
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(CT) trim_kernel(path_paged_cache_t c, int wind
 
 // ---------------- compact ----------------
 // Pool by pool: pages in use above the number of used ones, and holes below it, both in rising order.
-__device__ int dense_lists(int* __restrict__ ref, int pages, int* __restrict__ src, int* __restrict__ dst, int* __restrict__ map,
+__device__ int dense_lists(int* ref, int pages, int* src, int* dst, int* map,
                            int* used_out, BlockScan& s) {
   constexpr int PER = 8;
   int used = 0;
@@ -381,6 +381,7 @@ __device__ int dense_lists(int* __restrict__ ref, int pages, int* __restrict__ s
       const int pg = p0 + i;
       const bool u = bits >> i & 1;
       if (!u && pg < used) dst[ad++] = pg;
+      if (!u && pg >= used && pg < pages) map[pg] = pg;  // (named by a table all the same: left)
       if (u && pg >= used) src[as++] = pg;
     }
     nd += t1;
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(CT) copy_kernel(path_paged_cache_t c, Lists w,
   }
 }
 
-__global__ void advance_kernel(path_paged_cache_t c, const int* __restrict__ q_start) {
+__global__ void advance_kernel(path_paged_cache_t c, const int* q_start) {
   chain();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= c.slots) return;

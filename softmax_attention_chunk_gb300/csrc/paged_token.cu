@@ -151,7 +151,7 @@ struct State {
 
 // NT8 = 0: every slot of the list has one token.  Otherwise NT8 tiles of 8 tokens, fragments from draft_prep_kernel.
 template <int D, int NQ8, int NT8, bool FOX>
-__global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
+__global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedArgs p, TokenWs w, char* ws) {
   chain();
   __shared__ int s_start[kSmemSlots + 1];
   constexpr bool ONE = NT8 == 0;
@@ -303,13 +303,13 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const size_t at = item * w.nq + 8 * q + 2 * t + e;
-          st.m[q][e] = u == s0 ? __ldg((const float*)(ws + w.sm) + at) : -INFINITY;
-          st.l[q][e] = u == s0 && g == 0 ? __ldg((const float*)(ws + w.sl) + at) : 0.f;
+          st.m[q][e] = u == s0 ? ((const float*)(ws + w.sm))[at] : -INFINITY;
+          st.l[q][e] = u == s0 && g == 0 ? ((const float*)(ws + w.sl))[at] : 0.f;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             float2 v = make_float2(0.f, 0.f);
             if (u == s0)
-              v = __ldg(reinterpret_cast<const float2*>((const float*)(ws + w.sacc) + at * D + 64 * (j / 4) + 8 * g + 2 * (j % 4)));
+              v = *reinterpret_cast<const float2*>((const float*)(ws + w.sacc) + at * D + 64 * (j / 4) + 8 * g + 2 * (j % 4));
             st.acc[q][j][e] = v.x;
             st.acc[q][j][2 + e] = v.y;
           }
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
     const int i0 = u - s0, i1 = lt.count > 0 ? ue - s0 : i0;  // (no cached rows: nothing to stream)
     uint4 kr[2][KB], vr[4][CS];
     float aj[2] = {0.f, 0.f};
-    auto page = [&](const int* table, int i) { return __ldg(table + (size_t)b * p.c.table_width + newest_tile(lt, i) * RT / P); };
+    auto page = [&](const int* table, int i) { return table[(size_t)b * p.c.table_width + newest_tile(lt, i) * RT / P]; };
     int kp = -1, vp = -1, kpn = -1, vpn = -1;  // pages of the current and the next tile
     long long krow = 0, vrow = 0;
     auto rows_of = [&](int i, int pk, int pv, long long& rk, long long& rv) {
@@ -412,13 +412,13 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
               const int k = 2 * x + y;
 #pragma unroll
               for (int q = 0; q < NQ8; ++q) {
-                const uint2 zhv = __ldg(f + ((2 * q) * (D / 16) + k) * 32), zlv = __ldg(f + ((2 * q + 1) * (D / 16) + k) * 32);
+                const uint2 zhv = f[((2 * q) * (D / 16) + k) * 32], zlv = f[((2 * q + 1) * (D / 16) + k) * 32];
                 mma_bf16(s[q], a0, a1, a2, a3, zhv.x, zhv.y);
                 mma_bf16(s[q], a0, a1, a2, a3, zlv.x, zlv.y);
               }
 #pragma unroll
               for (int q = 0; q < NT8; ++q) {
-                const uint2 wv = __ldg(f + ((2 * NQ8 + q) * (D / 16) + k) * 32);
+                const uint2 wv = f[((2 * NQ8 + q) * (D / 16) + k) * 32];
                 mma_bf16(c[q], a0, a1, a2, a3, wv.x, wv.y);
               }
             }
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               float k4[4] = {lo_f(r0[y]), hi_f(r0[y]), lo_f(r1[y]), hi_f(r1[y])};
-              const uint2 yh = __ldg(f + (4 * x + y) * 32), yl = __ldg(f + (D / 8 + 4 * x + y) * 32);  // -Y
+              const uint2 yh = f[(4 * x + y) * 32], yl = f[(D / 8 + 4 * x + y) * 32];  // -Y
               if constexpr (NT8 == 2) {
                 mma_bf16(k4, ah[0], ah[1], ah[2], ah[3], yh.x, yh.y);
                 mma_bf16(k4, al[0], al[1], al[2], al[3], yh.x, yh.y);
@@ -628,7 +628,7 @@ struct DraftSmem {
   long long kr[DN], vr[DN];  // the appended rows' places
 };
 template <int D, bool FOX>
-__global__ void __launch_bounds__(DT) draft_prep_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
+__global__ void __launch_bounds__(DT) draft_prep_kernel(PagedArgs p, TokenWs w, char* ws) {
   chain();
   extern __shared__ __align__(16) uint8_t smem_raw[];
   DraftSmem<D>& sm = *reinterpret_cast<DraftSmem<D>*>(smem_raw);
@@ -846,7 +846,7 @@ constexpr int merge_columns(int D, int cols) {  // a power of two, at most the g
   return cs;
 }
 template <typename T, int D>
-__global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w, const char* __restrict__ ws, int mode, int warps,
+__global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w, const char* ws, int mode, int warps,
                                                          int cs) {
   chain();
   constexpr int L = D / 4, GR = MT / L;
@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w,
 // z . k, w . k and the softmax in fp32.  GP: query heads per key head, rounded up to a power of two.
 constexpr int blocks32(int D, int gp) { return gp <= 4 ? blocks_per_sm(D, 1) : 2; }
 template <int D, int GP, bool FOX>
-__global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs p, TokenWs w, char* __restrict__ ws) {
+__global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs p, TokenWs w, char* ws) {
   chain();
   __shared__ int s_start[kSmemSlots + 1];
   constexpr int L = D / 4, RW = 32 / L, AHEAD = 4;  // lanes of a row, rows side by side, row groups on the way
@@ -988,8 +988,8 @@ __global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs 
     const int i0 = u - s0, i1 = lt.count > 0 ? ue - s0 : i0;
     for (int i = i0; i < i1; ++i) {
       const int j0 = newest_tile(lt, i) * RT;
-      const int kp = __ldg(p.c.k_table + (size_t)b * p.c.table_width + j0 / P);
-      const int vp = __ldg(p.c.v_table + (size_t)b * p.c.table_width + j0 / P);
+      const int kp = p.c.k_table[(size_t)b * p.c.table_width + j0 / P];
+      const int vp = p.c.v_table[(size_t)b * p.c.table_width + j0 / P];
       if ((unsigned)kp >= (unsigned)p.c.k_pages || (unsigned)vp >= (unsigned)p.c.v_pages) {
         if (lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
         continue;

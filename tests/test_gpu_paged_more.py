@@ -240,3 +240,14 @@ def test_long_fp32_prompt_with_the_gate(cuda_lib):
     got, cache = run(c, 0.125)
     R.check_extend(c, got, R.extend_ref(c, 0.125), 0.125)
     cache.check()
+
+
+@pytest.mark.parametrize("dtype,max_new", [("bf16", 5), ("bf16", 40), ("fp32", 5)])
+def test_one_token_per_slot_with_a_generous_max_new(cuda_lib, dtype, max_new):
+    c = R.make_case(dtype, 64, 4, 2, 32, [40, 0, 129, 64, 7, 300], [1] * 6, seed=63)
+    cache = to_cache(c)
+    ins = [c[x].to(DEV) for x in ("q", "k", "v", "w", "beta")]
+    o = cache.extend(*ins, max_new=max_new, scale=0.125)
+    torch.cuda.synchronize()
+    R.check_extend(c, dict(o=o.cpu(), k=cache.k_pool.cpu(), v=cache.v_pool.cpu()), R.extend_ref(c, 0.125), 0.125)
+    cache.check()
