@@ -318,6 +318,24 @@ struct ScanSmem {
   static constexpr int kM = kP + B * KS, kBias = kM + B * 3, attend = kBias + KT;  // kM: maximum, sum, row bias
 };
 
+// R rows of D floats between memory (row pitch in floats) and a tile in shared memory (row pitch ds), 16 bytes at a time.
+template <int R, int D>
+__device__ __forceinline__ void tile_in(float* dst, int ds, const float* src, size_t pitch) {
+#pragma unroll
+  for (int i = 0; i < R * (D / 4) / NT; ++i) {
+    const int e = i * NT + threadIdx.x, r = e / (D / 4), x = e % (D / 4) * 4;
+    *reinterpret_cast<float4*>(dst + r * ds + x) = *reinterpret_cast<const float4*>(src + (size_t)r * pitch + x);
+  }
+}
+template <int R, int D>
+__device__ __forceinline__ void tile_out(float* dst, const float* src, int ds) {
+#pragma unroll
+  for (int i = 0; i < R * (D / 4) / NT; ++i) {
+    const int e = i * NT + threadIdx.x, r = e / (D / 4), x = e % (D / 4) * 4;
+    *reinterpret_cast<float4*>(dst + (size_t)r * D + x) = *reinterpret_cast<const float4*>(src + r * ds + x);
+  }
+}
+
 // Online softmax of the score tile sP [B][nk] (already masked, log2 domain): probabilities replace the
 // scores, the row's maximum and sum are updated and acc rescaled.  All threads; ends with a barrier.
 template <int D>
@@ -367,10 +385,8 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     if (p.log_f && tid < B) ((float*)(ws + w.qb))[row + tid] = fa[((size_t)c * H + h) * B + tid];
     return;
   }
-  for (int e = tid; e < B * D; e += NT) {
-    sZ[(e / D) * DS + e % D] = z[e];
-    sAcc[(e / D) * DS + e % D] = acc[e];
-  }
+  tile_in<B, D>(sZ, DS, z, D);
+  tile_in<B, D>(sAcc, DS, acc, D);
   if (tid < B) {
     sM[tid] = gm[tid];
     sM[B + tid] = gl[tid];
@@ -383,12 +399,9 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     const float* f = (const float*)(ws + w.f) + cc * D * D;
     const size_t tok = (size_t)sp.q0 + (size_t)c2 * B;
     __syncthreads();
-    for (int e = tid; e < B * D; e += NT) {
-      const int r = e / D, x = e % D;
-      sK[r * DS + x] = kr[e];
-      sV[r * DS + x] = (v[((tok + r) * H + h) * D + x]);  // an earlier chunk is full
-    }
-    for (int e = tid; e < D * D; e += NT) sF[(e / D) * DS + e % D] = f[e];
+    tile_in<B, D>(sK, DS, kr, D);
+    tile_in<B, D>(sV, DS, v + (tok * H + h) * D, (size_t)H * D);  // (an earlier chunk is full)
+    tile_in<D, D>(sF, DS, f, D);
     __syncthreads();
     product<B, B, D, false, true>(sZ, DS, sK, DS, [&](int i, int j, float x) {
       float s = -INFINITY;
@@ -407,10 +420,8 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     float* t = sZ; sZ = sZn; sZn = t;
   }
   __syncthreads();
-  for (int e = tid; e < B * D; e += NT) {
-    z[e] = sZ[(e / D) * DS + e % D];
-    acc[e] = sAcc[(e / D) * DS + e % D];
-  }
+  tile_out<B, D>(z, sZ, DS);
+  tile_out<B, D>(acc, sAcc, DS);
   if (tid < B) {
     gm[tid] = sM[tid];
     gl[tid] = sM[B + tid];
@@ -474,8 +485,8 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     const float* f = (const float*)(ws + w.f) + cc * D * D;
     const int rows = min(B, sp.n - lc * B);
     __syncthreads();
-    for (int e = tid; e < B * D; e += NT) sK[(e / D) * DS + e % D] = kr[e];
-    for (int e = tid; e < D * D; e += NT) sF[(e / D) * DS + e % D] = f[e];
+    tile_in<B, D>(sK, DS, kr, D);
+    tile_in<D, D>(sF, DS, f, D);
     __syncthreads();
     product<B, D, D, false, false>(sK, DS, sR, DS, [&](int i, int n, float x) {
       if (i < rows) {
@@ -487,7 +498,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     // R <- F_c R, by way of M's place in global memory until every thread has read R
     product<D, D, D, false, false>(sF, DS, sR, DS, [&](int i, int n, float x) { mm[i * D + n] = x; });
     __syncthreads();
-    for (int e = tid; e < D * D; e += NT) sR[(e / D) * DS + e % D] = mm[e];
+    tile_in<D, D>(sR, DS, mm, D);
   }
 }
 
@@ -544,10 +555,10 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
     return;
   }
   const float* z = (const float*)(ws + w.z) + row0 * D;
-  for (int e = tid; e < B * D; e += NT) {
-    sZ[(e / D) * DS + e % D] = z[e];
-    sAcc[(e / D) * DS + e % D] = split == 0 ? acc[e] : 0.f;
-  }
+  tile_in<B, D>(sZ, DS, z, D);
+  if (split == 0) tile_in<B, D>(sAcc, DS, acc, D);
+  else
+    for (int e = tid; e < B * D; e += NT) sAcc[(e / D) * DS + e % D] = 0.f;
   if (tid < B) {
     sM[tid] = split == 0 ? gm[tid] : -INFINITY;
     sM[B + tid] = split == 0 ? gl[tid] : 0.f;
@@ -563,8 +574,9 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
   for (int i = i0; i < i1; ++i) {
     const int j0 = live_tile(lt, i) * KT;
     __syncthreads();
-    for (int r = tid >> 3; r < KT; r += NT / 8) {
-      const int j = j0 + r;
+#pragma unroll
+    for (int r0t = 0; r0t < KT; r0t += NT / 8) {
+      const int r = r0t + (tid >> 3), j = j0 + r;
       // a row that no query of the chunk sees is not looked up (its page may be gone)
       bool any = j < sp.t0 && sees(p.window, p.sinks, sp.t0 + r0, j);
       long long ka = -1, va = -1;
@@ -576,9 +588,11 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
           paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
         }
       }
-      for (int x = tid & 7; x < D; x += 8) {
-        sK[r * DS + x] = any ? (kp[ka * D + x]) : 0.f;
-        sV[r * DS + x] = any ? (vp[va * D + x]) : 0.f;
+#pragma unroll
+      for (int x = (tid & 7) * 4; x < D; x += 32) {
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(sK + r * DS + x) = any ? *reinterpret_cast<const float4*>(kp + ka * D + x) : none;
+        *reinterpret_cast<float4*>(sV + r * DS + x) = any ? *reinterpret_cast<const float4*>(vp + va * D + x) : none;
       }
       if ((tid & 7) == 0) sB[r] = any ? (p.log_f ? a_last - p.c.a_pool[va] : 0.f) : -INFINITY;
     }
@@ -594,7 +608,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
     product<B, D, KT, false, false>(sP, KS, sV, DS, [&](int r, int n, float x) { sAcc[r * DS + n] += x; });
   }
   __syncthreads();
-  for (int e = tid; e < B * D; e += NT) acc[e] = sAcc[(e / D) * DS + e % D];
+  tile_out<B, D>(acc, sAcc, DS);
   if (tid < B) {
     gm[tid] = sM[tid];
     gl[tid] = sM[B + tid];
@@ -626,13 +640,16 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
     __syncthreads();
     if (have != b * H + h) {
       const float* mm = (const float*)(ws + w.mm) + ((size_t)b * H + h) * D * D;
-      for (int e = tid; e < D * D; e += NT) sMm[(e / D) * DS + e % D] = mm[e];
+      tile_in<D, D>(sMm, DS, mm, D);
       have = b * H + h;
     }
     auto keep = [&](int j) { return j < sp.t0 && sees(p.window, p.sinks, sp.t0 + sp.n, j); };
     for (int r = tid >> 3; r < KT; r += NT / 8) {
       const long long at = keep(j0 + r) ? pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j0 + r) : -1;
-      for (int x = tid & 7; x < D; x += 8) sK[r * DS + x] = at >= 0 ? (kp[at * D + x]) : 0.f;
+#pragma unroll
+      for (int x = (tid & 7) * 4; x < D; x += 32)
+        *reinterpret_cast<float4*>(sK + r * DS + x) =
+            at >= 0 ? *reinterpret_cast<const float4*>(kp + at * D + x) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __syncthreads();
     product<KT, D, D, false, false>(sK, DS, sMm, DS, [&](int r, int n, float x) {
