@@ -15,8 +15,8 @@
 //
 // Bound: fp32 multiply-adds and shared-memory reads of the products (no fp32 tensor path keeps 24 bits); products keep
 // 2 x 4 results per thread, tiles move 16 bytes at a time, the merge takes a row's ranges side by side (262 -> 184 -> 140 ->
-// 116 us for 3 slots of 5 to 97 tokens over up to 1500 rows x 8 heads, head dim 64: what is left is a chain of six
-// launches with few blocks each, every one a chain of products; attention 38, scan and walk 33, rewrite 17).
+// 116 -> 105 us for 3 slots of 5 to 97 tokens over up to 1500 rows x 8 heads, head dim 64: what is left is a chain of six
+// launches with few blocks each, every one a chain of products; attention 25, scan and walk 33, rewrite 17).
 #include "paged.h"
 #include "dev_common.cuh"
 
@@ -318,10 +318,10 @@ __global__ void __launch_bounds__(NT) prep_kernel(PagedArgs p, ChunkWs w, char* 
 
 template <int D>
 struct ScanSmem {
-  static constexpr int DS = D + 4, KS = KT + 4;
-  static constexpr int kZ = 0, kZn = kZ + B * DS, kK = kZn + B * DS, kV = kK + KT * DS, kAcc = kV + KT * DS;
+  static constexpr int DS = D + 4, KS = B + 4;
+  static constexpr int kZ = 0, kZn = kZ + B * DS, kK = kZn + B * DS, kV = kK + B * DS, kAcc = kV + B * DS;
   static constexpr int kP = kAcc + B * DS;
-  static constexpr int kM = kP + B * KS, kBias = kM + B * 3, attend = kBias + KT;  // kM: maximum, sum, row bias
+  static constexpr int kM = kP + B * KS, kF = kM + B * 3;  // kM: maximum, sum, row bias
 };
 
 // R rows of D floats between memory (row pitch in floats) and a tile in shared memory (row pitch ds), 16 bytes at a time.
@@ -375,7 +375,7 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   using S = ScanSmem<D>;
   constexpr int DS = S::DS, KS = S::KS;
   float *sZ = sm + S::kZ, *sZn = sm + S::kZn, *sK = sm + S::kK, *sV = sm + S::kV, *sAcc = sm + S::kAcc;
-  float *sP = sm + S::kP, *sM = sm + S::kM, *sF = sm + S::attend;
+  float *sP = sm + S::kP, *sM = sm + S::kM, *sF = sm + S::kF;
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads, h = qh / p.G;
   const int b = owner(cstart, p.c.slots, c);
@@ -510,7 +510,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
 
 template <int D>
 constexpr size_t scan_walk_smem() {
-  constexpr size_t scan = (size_t)(ScanSmem<D>::attend + D * (D + 4)) * 4;
+  constexpr size_t scan = (size_t)(ScanSmem<D>::kF + D * (D + 4)) * 4;
   constexpr size_t walk = (size_t)(2 * D + B) * (D + 4) * 4;
   return scan > walk ? scan : walk;
 }
@@ -530,17 +530,28 @@ __global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, c
   scan_block<D>(p, w, ws, sm, c, x % p.hq);
 }
 
-// Cached attention: one block per (chunk, query head, key range).
+// Cached attention: one block per (chunk, query head, key range).  A warp owns 8 query rows, its lanes two of a tile's
+// 64 keys each: scores, softmax and (by columns) the output stay in registers, and only the probabilities pass through
+// shared memory, within the warp.  Keys and values arrive by asynchronous copies behind the other product.  Bound: the
+// products' shared-memory reads (per 64 multiply-adds of a thread 10 to 12 reads of 16 bytes, 4 cycles of the SM each for
+// a warp): 2 x 150 tokens x 32 heads over 8100 rows, head dim 64 (20 GFLOP), 867 us, 23 TFLOP/s; with 2 x 4 results per
+// thread and the softmax in shared memory the smaller case above took 38 us here in place of 25.
+constexpr int AT = 128;  // threads
 template <int D>
-__global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char* ws) {
+struct AttendSmem {
+  static constexpr int DS = D + 4, PS = KT + 4;
+  static constexpr int kZ = 0, kK = kZ + B * DS, kV = kK + KT * DS, kP = kV + KT * DS, kBias = kP + B * PS;
+  static constexpr int kRow = kBias + 2 * KT, total = kRow + 2 * 2 * 2 * KT;  // places: two 64-bit ones per row and tile
+};
+template <int D>
+__global__ void __launch_bounds__(AT, D == 64 ? 4 : 2) attend_kernel(PagedArgs p, ChunkWs w, char* ws) {
   chain();
-  extern __shared__ float sm[];
-  using S = ScanSmem<D>;
-  constexpr int DS = S::DS, KS = S::KS;
-  float *sZ = sm + S::kZ, *sK = sm + S::kK, *sV = sm + S::kV, *sAcc = sm + S::kAcc, *sP = sm + S::kP, *sM = sm + S::kM;
-  float* sB = sm + S::kBias;  // key biases a_last - a_j; hidden rows -inf
+  extern __shared__ __align__(16) float sm[];
+  using S = AttendSmem<D>;
+  constexpr int DS = S::DS, PS = S::PS, V = D / 32;  // V: columns of a lane
+  float *sZ = sm + S::kZ, *sK = sm + S::kK, *sV = sm + S::kV, *sP = sm + S::kP;
   const int* cstart = (const int*)(ws + w.plan);
-  const int c = blockIdx.x, qh = blockIdx.y, split = blockIdx.z, tid = threadIdx.x;
+  const int c = blockIdx.x, qh = blockIdx.y, split = blockIdx.z, tid = threadIdx.x, lane = tid & 31, w8 = tid / 32 * 8;
   if (c >= cstart[p.c.slots]) return;
   const int h = qh / p.G, b = owner(cstart, p.c.slots, c);
   const SlotSpan sp = chunk_span(p, b);
@@ -551,7 +562,7 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
   const size_t row0 = ((size_t)c * p.hq + qh) * B;
   const size_t row = (size_t)split * w.nch * p.hq * B + row0;
   if (split == 0 && i0 >= i1) return;  // the new tokens' state stands
-  float* acc = (float*)(ws + w.acc) + row * D;
+  float* acc_out = (float*)(ws + w.acc) + row * D;
   float *gm = (float*)(ws + w.m) + row, *gl = (float*)(ws + w.l) + row;
   if (i0 >= i1) {
     if (tid < B) {
@@ -560,64 +571,131 @@ __global__ void __launch_bounds__(NT) attend_kernel(PagedArgs p, ChunkWs w, char
     }
     return;
   }
-  const float* z = (const float*)(ws + w.z) + row0 * D;
-  tile_in<B, D>(sZ, DS, z, D);
-  if (split == 0) tile_in<B, D>(sAcc, DS, acc, D);
-  else
-    for (int e = tid; e < B * D; e += NT) sAcc[(e / D) * DS + e % D] = 0.f;
-  if (tid < B) {
-    sM[tid] = split == 0 ? gm[tid] : -INFINITY;
-    sM[B + tid] = split == 0 ? gl[tid] : 0.f;
-    sM[2 * B + tid] = p.log_f ? ((const float*)(ws + w.qb))[row0 + tid] : 0.f;
-  }
+  const float *kp = (const float*)p.c.k_pool, *vp = (const float*)p.c.v_pool;
   float a_last = 0.f;
   if (p.log_f) {
     const long long last = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1);
     if (last >= 0) a_last = p.c.a_pool[last];
   }
-  const float* kp = (const float*)p.c.k_pool;
-  const float* vp = (const float*)p.c.v_pool;
+  long long* place = reinterpret_cast<long long*>(sm + S::kRow);  // [tile parity][key, value][row]: the pools' rows, or -1
+  // Places and biases (a_last - a_j; hidden rows -inf) of tile i.  A row that no query of the chunk sees is not looked up
+  // (its page may be gone); a row is there only with both its key and its value.
+  auto look = [&](int i) {
+    if (tid >= KT || i >= i1) return;
+    const int j = live_tile(lt, i) * KT + tid, at = (i & 1) * 2 * KT + tid;
+    long long ka = -1, va = -1;
+    if (j < sp.t0 && sees(p.window, p.sinks, sp.t0 + r0, j)) {
+      ka = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j);
+      va = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, j);
+      if (ka < 0 || va < 0) {
+        ka = va = -1;
+        paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+      }
+    }
+    place[at] = ka;
+    place[at + KT] = va;
+    sm[S::kBias + (i & 1) * KT + tid] = va < 0 ? -INFINITY : p.log_f ? a_last - p.c.a_pool[va] : 0.f;
+  };
+  auto fetch = [&](float* dst, const float* pool, int i, int value) {
+    const long long* from = place + ((i & 1) * 2 + value) * KT;
+#pragma unroll
+    for (int y = 0; y < KT * (D / 4) / AT; ++y) {
+      const int e = y * AT + tid, r = e / (D / 4), x = e % (D / 4) * 4;
+      const long long at = from[r];
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + r * DS + x)),
+                   "l"(pool + (at >= 0 ? at * D + x : 0)), "r"(at >= 0 ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  look(i0);
+  __syncthreads();
+  fetch(sK, kp, i0, 0);
+  fetch(sV, vp, i0, 1);
+  look(i0 + 1);
+  const float* z = (const float*)(ws + w.z) + row0 * D;
+  for (int e = tid; e < B * (D / 4); e += AT) {
+    const int r = e / (D / 4), x = e % (D / 4) * 4;
+    *reinterpret_cast<float4*>(sZ + r * DS + x) = *reinterpret_cast<const float4*>(z + r * D + x);
+  }
+  float m[8], l[8], qb[8], acc[8][V];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    m[r] = split == 0 ? gm[w8 + r] : -INFINITY;
+    l[r] = split == 0 && lane == 0 ? gl[w8 + r] : 0.f;
+    qb[r] = p.log_f ? ((const float*)(ws + w.qb))[row0 + w8 + r] : 0.f;
+#pragma unroll
+    for (int x = 0; x < V; ++x) acc[r][x] = split == 0 ? acc_out[(w8 + r) * D + lane * V + x] : 0.f;
+  }
+  auto ld4 = [](const float* q) { return *reinterpret_cast<const float4*>(q); };
   for (int i = i0; i < i1; ++i) {
     const int j0 = live_tile(lt, i) * KT;
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
+    float s[8][2];
 #pragma unroll
-    for (int r0t = 0; r0t < KT; r0t += NT / 8) {
-      const int r = r0t + (tid >> 3), j = j0 + r;
-      // a row that no query of the chunk sees is not looked up (its page may be gone)
-      bool any = j < sp.t0 && sees(p.window, p.sinks, sp.t0 + r0, j);
-      long long ka = -1, va = -1;
-      if (any) {
-        ka = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, j);
-        va = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, j);
-        if (ka < 0 || va < 0) {
-          any = false;
-          paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+    for (int r = 0; r < 8; ++r) s[r][0] = s[r][1] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < D; k += 4) {
+      const float4 k0 = ld4(sK + lane * DS + k), k1 = ld4(sK + (lane + 32) * DS + k);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float4 q = ld4(sZ + (w8 + r) * DS + k);
+        s[r][0] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, fmaf(q.z, k0.z, fmaf(q.w, k0.w, s[r][0]))));
+        s[r][1] = fmaf(q.x, k1.x, fmaf(q.y, k1.y, fmaf(q.z, k1.z, fmaf(q.w, k1.w, s[r][1]))));
+      }
+    }
+    const float* sB = sm + S::kBias + (i & 1) * KT;
+    const float b0 = sB[lane], b1 = sB[lane + 32];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int pos = sp.t0 + r0 + w8 + r;
+      const float x0 = b0 != -INFINITY && sees(p.window, p.sinks, pos, j0 + lane) ? s[r][0] * p.scl + (b0 + qb[r]) * kLog2e : -INFINITY;
+      const float x1 = b1 != -INFINITY && sees(p.window, p.sinks, pos, j0 + lane + 32) ? s[r][1] * p.scl + (b1 + qb[r]) * kLog2e : -INFINITY;
+      const float mn = fmaxf(m[r], group_max<32>(fmaxf(x0, x1)));
+      const float corr = mn == -INFINITY ? 1.f : fast_exp2(m[r] - mn);
+      const float e0 = x0 == -INFINITY ? 0.f : fast_exp2(x0 - mn), e1 = x1 == -INFINITY ? 0.f : fast_exp2(x1 - mn);
+      m[r] = mn;
+      l[r] = l[r] * corr + e0 + e1;
+      sP[(w8 + r) * PS + lane] = e0;
+      sP[(w8 + r) * PS + lane + 32] = e1;
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[r][x] *= corr;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    if (i + 1 < i1) fetch(sK, kp, i + 1, 0);
+#pragma unroll 2
+    for (int k = 0; k < KT; k += 4) {
+      float v[4][V];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int x = 0; x < V; x += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(sV + (k + e) * DS + lane * V + x);
+          v[e][x] = y.x;
+          v[e][x + 1] = y.y;
         }
-      }
 #pragma unroll
-      for (int x = (tid & 7) * 4; x < D; x += 32) {
-        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(sK + r * DS + x) = any ? *reinterpret_cast<const float4*>(kp + ka * D + x) : none;
-        *reinterpret_cast<float4*>(sV + r * DS + x) = any ? *reinterpret_cast<const float4*>(vp + va * D + x) : none;
+      for (int r = 0; r < 8; ++r) {
+        const float4 q = ld4(sP + (w8 + r) * PS + k);
+#pragma unroll
+        for (int x = 0; x < V; ++x) acc[r][x] = fmaf(q.x, v[0][x], fmaf(q.y, v[1][x], fmaf(q.z, v[2][x], fmaf(q.w, v[3][x], acc[r][x]))));
       }
-      if ((tid & 7) == 0) sB[r] = any ? (p.log_f ? a_last - p.c.a_pool[va] : 0.f) : -INFINITY;
     }
     __syncthreads();
-    product<B, KT, D, false, true>(sZ, DS, sK, DS, [&](int r, int j, float x) {
-      float s = -INFINITY;
-      if (r < rows && sB[j] != -INFINITY && sees(p.window, p.sinks, sp.t0 + r0 + r, j0 + j))
-        s = x * p.scl + (sB[j] + sM[2 * B + r]) * kLog2e;
-      sP[r * KS + j] = s;
-    });
-    __syncthreads();
-    softmax_step<D>(sP, KS, KT, sM, sAcc, DS);
-    product<B, D, KT, false, false>(sP, KS, sV, DS, [&](int r, int n, float x) { sAcc[r * DS + n] += x; });
+    if (i + 1 < i1) fetch(sV, vp, i + 1, 1);
+    look(i + 2);
   }
-  __syncthreads();
-  tile_out<B, D>(acc, sAcc, DS);
-  if (tid < B) {
-    gm[tid] = sM[tid];
-    gl[tid] = sM[B + tid];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const float ls = group_sum<32>(l[r]);
+    if (lane == 0) {
+      gm[w8 + r] = m[r];
+      gl[w8 + r] = ls;
+    }
+#pragma unroll
+    for (int x = 0; x < V; ++x) acc_out[(w8 + r) * D + lane * V + x] = acc[r][x];
   }
 }
 
@@ -719,7 +797,7 @@ cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
   auto att = attend_kernel<D>;
   auto rew = rewrite_kernel<D>;
   const size_t s1 = (size_t)PrepSmem<D>::total * 4, s2 = scan_walk_smem<D>();
-  const size_t s3 = (size_t)ScanSmem<D>::attend * 4, s4 = (size_t)(D + KT) * (D + 4) * 4;
+  const size_t s3 = (size_t)AttendSmem<D>::total * 4, s4 = (size_t)(D + KT) * (D + 4) * 4;
   if ((e = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s1)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(att, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s3)) != cudaSuccess) return e;
@@ -727,7 +805,7 @@ cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
   if ((e = launch_chained(plan_kernel, 1, 1024, 0, st, p, (int*)(ws + w.plan))) != cudaSuccess ||
       (e = launch_chained(prep, dim3(w.nch, p.c.heads), NT, s1, st, p, w, ws)) != cudaSuccess ||
       (e = launch_chained(scan, p.c.slots * p.c.heads + w.nch * p.hq, NT, s2, st, p, w, ws)) != cudaSuccess ||
-      (e = launch_chained(att, dim3(w.nch, p.hq, w.nsplit), NT, s3, st, p, w, ws)) != cudaSuccess ||
+      (e = launch_chained(att, dim3(w.nch, p.hq, w.nsplit), AT, s3, st, p, w, ws)) != cudaSuccess ||
       (e = launch_chained(rew, 608, NT, s4, st, p, w, ws)) != cudaSuccess)
     return e;
   return launch_chained(merge_kernel<D>, dim3(w.nch * (B / (NT / 32)), p.hq), NT, 0, st, p, w, ws);
