@@ -27,8 +27,9 @@
 // library product (tensor pipe 60 % of its cycles); 2048 x 32 over 16384 at head dim 64 (275 GFLOP) 370 us, 0.74 PFLOP/s:
 // tensor pipe 48 %, exponentials 33 %, issue 39 %, no unit saturated, each tile's chain of score product, softmax and
 // value product a latency.  Tried and slower (the 1.1 TFLOP case's whole call, 1003 us): two threads per row 1441,
-// maximum first and a second pass for the exponentials 1297, loads of the next scores under way 1020, key steps of
-// 64 1027 against 862 at the time; P as a bf16 pair 1707; a third score buffer at head dim 64 gained nothing.
+// maximum first and a second pass for the exponentials 1297, loads of the next scores under way 1020, the second tile
+// half a step behind 1064, P as a bf16 pair 1707, key steps of 64 (attention) 1027 against 862 at the time.  Copies at head
+// dim 64 without the exponentials, the TMEM loads or nearly all MMAs take 1.05, 1.08 and 0.87 of the time.
 #include "paged_tc.h"
 #include "dev_common.cuh"
 #include "tc_common.cuh"
