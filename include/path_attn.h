@@ -436,6 +436,7 @@ size_t path_paged_workspace_size(const path_paged_cache_t* cache, const path_pag
  * page is missing are treated as hidden and are not written; status gets the code.  Ranges of q_start
  * that overlap mix those slots' results; with more tokens in them than total_tokens, slots with several
  * tokens are left out and status gets PATH_PAGED_BAD_START.
+ * o must not overlap the inputs or the pools.
  * Pool rows behind seq_len and pages that no table names may hold anything.  An infinity or NaN in a
  * slot's own tokens or cached rows may reach any output of that slot, never another slot's.
  * ws: at least path_paged_workspace_size(cache, desc) bytes, 256-byte aligned.  Two calls that may

@@ -96,7 +96,8 @@ class PagedCache:
         heads, head_dim], beta and log_f [tokens, heads] float32 (log_f exactly for a cache with fox).  q_start
         (int32 [slots + 1]): slot b's tokens are q_start[b] .. q_start[b + 1] - 1, at most max_new of them
         (default: all); without it, token b is slot b's.  window > 0 hides all but the last `window` tokens and
-        the first `sinks`.  The cache's keys are rewritten and the new rows appended; seq_len is not changed."""
+        the first `sinks`.  The cache's keys are rewritten and the new rows appended; seq_len is not changed.  out
+        must not overlap the other tensors."""
         if q.dim() != 3:
             raise ValueError(f"q: expected [tokens, heads_q, head_dim], got {tuple(q.shape)}")
         N, hq, d = q.shape
