@@ -391,6 +391,9 @@ typedef struct {
   int* k_ref;       /* [k_pages]: 1 in use, 0 free */
   int* v_ref;       /* [v_pages]: sequences that hold the page, 0 free */
   int* status;      /* one int: the first PATH_PAGED_* code since it was last cleared (start it at 0) */
+  int* extended;    /* [slots] or NULL: tokens that the last path_paged_extend of a slot gave it and no
+                       path_paged_advance has counted yet; -1: it left the slot out (start it at 0).
+                       NULL: advance cannot tell and counts what its q_start says */
 } path_paged_cache_t;
 
 /* Codes of the status word: what a call found on the device.  None of them makes a kernel leave its
@@ -400,7 +403,8 @@ enum {
   PATH_PAGED_CAPACITY = 2,    /* a sequence would outgrow table_width * page_size */
   PATH_PAGED_BAD_SLOT = 3,    /* slot out of range, listed twice, empty where it must not be, or in use */
   PATH_PAGED_NO_PAGES = 4,    /* not enough free pages */
-  PATH_PAGED_BAD_START = 5,   /* q_start falls, leaves [0, total_tokens] or exceeds max_new */
+  PATH_PAGED_BAD_START = 5,   /* q_start falls, leaves [0, total_tokens] or exceeds max_new; advance: it
+                                 is not what extend was given */
   PATH_PAGED_WAIT = 64        /* and above: a bounded wait of a tensor-core kernel gave up */
 };
 
@@ -432,10 +436,14 @@ size_t path_paged_workspace_size(const path_paged_cache_t* cache, const path_pag
  * every later token are left as they are (new ones: as appended, or as the pass stored them); their
  * table entries may be -1.
  * seq_len is read, not changed (path_paged_advance does that).  The pages must be there
- * (path_pages_reserve).  A slot whose row of q_start or length is bad is left out whole; rows whose
- * page is missing are treated as hidden and are not written; status gets the code.  Ranges of q_start
- * that overlap mix those slots' results; with more tokens in them than total_tokens, slots with several
- * tokens are left out and status gets PATH_PAGED_BAD_START.
+ * (path_pages_reserve).  A slot whose row of q_start or length is bad, or that lacks a page for one of
+ * its new tokens, is left out whole: nothing of it is read into o or written, and advance passes it
+ * over.  Cached rows whose page is missing are treated as hidden and are not written.  Status gets the
+ * code.  Ranges of q_start that overlap mix those slots' results; with more tokens in them than
+ * total_tokens, slots with several tokens are left out and status gets PATH_PAGED_BAD_START.
+ * The cached keys pass all tokens of the call, and nothing takes that back: draft tokens of which
+ * some may be rejected are given to a fork of their sequence (path_pages_fork), and those accepted then
+ * to the sequence itself (or, where all are, the fork stays in its place).
  * o must not overlap the inputs or the pools.
  * Pool rows behind seq_len and pages that no table names may hold anything.  An infinity or NaN in a
  * slot's own tokens or cached rows may reach any output of that slot, never another slot's.
@@ -446,7 +454,12 @@ int path_paged_extend(const path_paged_cache_t* cache, const path_paged_desc_t* 
                       const void* q, const void* k, const void* v, const void* w, const float* beta,
                       const float* log_f, void* o, void* ws, size_t ws_bytes, void* stream);
 
-/* seq_len[b] += q_start[b + 1] - q_start[b] for the slots in use (q_start NULL: += 1). */
+/*
+ * seq_len[b] += q_start[b + 1] - q_start[b] for the slots in use (q_start NULL: += 1), with the q_start
+ * of the extend before it.  A slot that extend left out is passed over; one that it gave another number of
+ * tokens gets PATH_PAGED_BAD_START and keeps its length.  Without an extend before it (rows that the
+ * caller wrote itself) the rows' pages have to be there (PATH_PAGED_BAD_PAGE).
+ */
 int path_paged_advance(const path_paged_cache_t* cache, const int* q_start, void* stream);
 
 /*

@@ -69,6 +69,15 @@ PATH_HD long long pool_row(const path_paged_cache_t& c, const int* table, int pa
   if ((unsigned)pg >= (unsigned)pages) return -1;
   return ((long long)pg * c.heads + h) * c.page_size + j % c.page_size;
 }
+// Whether there are pages of both pools for rows t0 .. t0 + n - 1 of slot b, by one thread.
+PATH_HD bool rows_there(const path_paged_cache_t& c, int b, int t0, int n) {
+  bool ok = true;
+  for (int x = t0 / c.page_size; n > 0 && x <= (t0 + n - 1) / c.page_size; ++x) {
+    const size_t at = (size_t)b * c.table_width + x;
+    ok &= (unsigned)c.k_table[at] < (unsigned)c.k_pages && (unsigned)c.v_table[at] < (unsigned)c.v_pages;
+  }
+  return ok;
+}
 // Whether the token at position pq sees row j <= pq (window 0: all).
 PATH_HD bool sees(int window, int sinks, int pq, int j) { return window <= 0 || j > pq - window || j < sinks; }
 
@@ -103,6 +112,35 @@ __device__ __forceinline__ SlotSpan slot_span(const PagedArgs& p, int b) {
   return slot_span_of(b, p.q_start, p.c.seq_len[b], p.total, p.max_new, p.c.table_width, p.c.page_size);
 }
 __device__ __forceinline__ void paged_error(int* status, int code) { atomicCAS(status, 0, code); }
+// What a call did with slot b, for path_paged_advance: its new tokens, or -1 where it was left out.
+__device__ __forceinline__ void note_extended(const path_paged_cache_t& c, int b, int n) {
+  if (c.extended) c.extended[b] = n;
+}
+// rows_there() by a warp, for as many rows as there may be.
+__device__ __forceinline__ bool rows_there_warp(const path_paged_cache_t& c, int b, int t0, int n) {
+  bool ok = true;
+  for (int x = t0 / c.page_size + (threadIdx.x & 31); x <= (t0 + n - 1) / c.page_size; x += 32) {
+    const size_t at = (size_t)b * c.table_width + x;
+    ok &= (unsigned)c.k_table[at] < (unsigned)c.k_pages && (unsigned)c.v_table[at] < (unsigned)c.v_pages;
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+// The planning kernels' look at a slot with several new tokens, by a whole warp (one slot per lane, s.n > 0 where the lane
+// has such a slot): clears s.n where a page for one of all its new tokens (t0, n: of the call) is missing.
+__device__ __forceinline__ void leave_out_pageless(const path_paged_cache_t& c, int b, int t0, int n, SlotSpan& s, bool report) {
+  unsigned look = __ballot_sync(0xffffffffu, s.n > 0);
+  while (look) {
+    const int lane = __ffs(look) - 1;
+    look &= look - 1;
+    const bool ok = rows_there_warp(c, __shfl_sync(0xffffffffu, b, lane), __shfl_sync(0xffffffffu, t0, lane),
+                                    __shfl_sync(0xffffffffu, n, lane));
+    if (!ok && lane == (int)(threadIdx.x & 31)) {
+      s.n = 0;
+      s.code = PATH_PAGED_BAD_PAGE;
+      if (report) paged_error(c.status, s.code);
+    }
+  }
+}
 // Programmatic dependent launch: every kernel of a call begins with chain(), which waits until the kernel before it has
 // ended and lets the next one's blocks take their places meanwhile (they wait there).  The first statement of every
 // kernel, for all threads: a grid that ended without having waited would end the chain early.  Pointers to what earlier

@@ -145,9 +145,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* plan) {
   for (int base = 0; base < p.c.slots; base += 1024) {
     const int b = base + tid;
     int nc = 0, nt = 0;
+    SlotSpan s{};
     if (b < p.c.slots) {
-      const SlotSpan s = chunk_span(p, b);
+      s = chunk_span(p, b);
       if (s.code) paged_error(p.c.status, s.code);
+    }
+    const int n = s.n;
+    leave_out_pageless(p.c, b, s.t0, n, s, true);
+    if (b < p.c.slots) {
+      if (n > 0) note_extended(p.c, b, s.n > 0 ? n : -1);
       nc = (s.n + B - 1) / B;
       if (s.n) atomicAdd(&tokens, (unsigned long long)s.n);
       nt = s.n ? live_tiles(s.t0, p.window, p.sinks, KT).count : 0;
@@ -172,7 +178,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* plan) {
   if (tokens > (unsigned long long)p.total) {
     if (tid == 0) paged_error(p.c.status, PATH_PAGED_BAD_START);
     __syncthreads();
-    for (int b = tid; b <= p.c.slots; b += 1024) cstart[b] = tstart[b] = 0;
+    for (int b = tid; b <= p.c.slots; b += 1024) {
+      if (b < p.c.slots && chunk_span(p, b).n > 0) note_extended(p.c, b, -1);
+      cstart[b] = tstart[b] = 0;
+    }
   }
 }
 
@@ -443,8 +452,8 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   const int* cstart = (const int*)(ws + w.plan);
   const int tid = threadIdx.x, H = p.c.heads;
   const SlotSpan sp = chunk_span(p, b);
-  if (sp.n == 0 || cstart[p.c.slots] == 0) return;
   const int nc = cstart[b + 1] - cstart[b];
+  if (nc == 0) return;  // no new tokens, or left out
   float* kp = (float*)p.c.k_pool;
   float* vp = (float*)p.c.v_pool;
   const float* v = (const float*)p.v;

@@ -194,9 +194,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
   for (int base = 0; base < p.c.slots; base += 1024) {
     const int b = base + tid;
     long long v[N] = {0, 0, 0, 0, 0, 0}, x[N];
+    SlotSpan all{}, s{};
     if (b < p.c.slots) {
-      const SlotSpan s = pass_span(p, b);
+      all = slot_span(p, b);
+      s = pass_part(p, all);
       if (report && s.code) paged_error(p.c.status, s.code);
+    }
+    leave_out_pageless(p.c, b, all.t0, all.n, s, report);
+    if (b < p.c.slots) {
+      if (report && all.n >= p.min_new) note_extended(p.c, b, s.n > 0 ? all.n : -1);
       if (s.n > 0) {
         atomicAdd(&tokens, (unsigned long long)s.n);
         const long long H = p.c.heads, np = ((long long)s.n * p.G + kTcPair - 1) / kTcPair, nb = (s.n + MB - 1) / MB;
@@ -259,6 +265,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
     if (tid == 0) paged_error(p.c.status, PATH_PAGED_BAD_START);
     __syncthreads();
     for (int b = tid; b <= S; b += 1024) {
+      if (report && b < S && slot_span(p, b).n >= p.min_new) note_extended(p.c, b, -1);
       pl.cstart[b] = pl.bstart[b] = pl.pstart[b] = pl.rstart[b] = 0;
       pl.vstart[b] = pl.ustart[b] = 0;
     }
@@ -625,7 +632,7 @@ __device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, 
   __shared__ float wsum[WT / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.c.heads;
   const SlotSpan sp = pass_span(p, b);
-  if (sp.n == 0 || pl.cstart[p.c.slots] == 0) return;
+  if (pl.cstart[b + 1] == pl.cstart[b]) return;  // no new tokens, or left out
   const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
   const float a0 = last >= 0 ? p.c.a_pool[last] : 0.f;
   float* cn = (float*)(ws + w.cn) + ((size_t)h * w.nblk + pl.bstart[b]) * MB;

@@ -205,7 +205,10 @@ __global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const
       av += __popc(mv);
     }
     __syncwarp();
-    if (lane == 0 && c.seq_len[b] < 0 && asked(b) > 0) c.seq_len[b] = 0;
+    if (lane == 0 && c.seq_len[b] < 0 && asked(b) > 0) {
+      c.seq_len[b] = 0;
+      note_extended(c, b, 0);
+    }
   }
 }
 
@@ -303,7 +306,10 @@ __global__ void __launch_bounds__(NT) fork_kernel(path_paged_cache_t c, const in
       ak += __popc(mk);
       av += __popc(mv);
     }
-    if (lane == 0) c.seq_len[ch] = len;
+    if (lane == 0) {
+      c.seq_len[ch] = len;
+      note_extended(c, ch, 0);
+    }
   }
   if (tid == 0) {
     w.head[0] = needk;
@@ -332,7 +338,10 @@ __global__ void __launch_bounds__(NT) free_kernel(path_paged_cache_t c, const in
   for (int i = threadIdx.x >> 5; i < count; i += NW) {
     const int b = list[i];
     for (int x = threadIdx.x & 31; x < c.table_width; x += 32) drop(c, b, x);
-    if ((threadIdx.x & 31) == 0) c.seq_len[b] = -1;
+    if ((threadIdx.x & 31) == 0) {
+      c.seq_len[b] = -1;
+      note_extended(c, b, 0);
+    }
   }
 }
 // One block per slot: slots share no table row, and value counts fall by atomics (sums of ones: the order
@@ -477,15 +486,22 @@ __global__ void advance_kernel(path_paged_cache_t c, const int* q_start) {
   const int len = c.seq_len[b];
   if (len < 0) return;
   const long long n = q_start ? (long long)q_start[b + 1] - q_start[b] : 1;
-  if (n < 0) {
-    paged_error(c.status, PATH_PAGED_BAD_START);
+  if (n == 0) return;  // (what another call gave the slot keeps waiting)
+  const int given = c.extended ? c.extended[b] : 0;
+  if (given < 0) {  // left out: extend has recorded why
+    c.extended[b] = 0;
     return;
   }
-  if (len + n > (long long)c.table_width * c.page_size) {
-    paged_error(c.status, PATH_PAGED_CAPACITY);
+  int code = 0;
+  if (n < 0 || (given > 0 && n != given)) code = PATH_PAGED_BAD_START;
+  else if (len + n > (long long)c.table_width * c.page_size) code = PATH_PAGED_CAPACITY;
+  else if (given == 0 && !rows_there(c, b, len, (int)n)) code = PATH_PAGED_BAD_PAGE;  // (no extend has looked)
+  if (code) {
+    paged_error(c.status, code);
     return;
   }
   c.seq_len[b] = (int)(len + n);
+  note_extended(c, b, 0);
 }
 
 size_t page_bytes(const path_paged_cache_t& c) {

@@ -38,9 +38,8 @@ PATH_HD long long new_units(long long pairs, int G) {
 }
 
 #ifdef __CUDACC__
-// The new tokens of a slot in this pass; slots with fewer than min_new have none.
-__device__ __forceinline__ SlotSpan pass_span(const PagedArgs& p, int b) {
-  SlotSpan s = slot_span(p, b);
+// The new tokens of a slot (of the whole call: s) in this pass; slots with fewer than min_new have none.
+__device__ __forceinline__ SlotSpan pass_part(const PagedArgs& p, SlotSpan s) {
   if (s.n < p.min_new) s.n = 0;
   const int n = s.n - p.skip;
   s.q0 += p.skip;
@@ -48,6 +47,7 @@ __device__ __forceinline__ SlotSpan pass_span(const PagedArgs& p, int b) {
   s.n = n < 0 ? 0 : n < kTcPassTokens ? n : kTcPassTokens;
   return s;
 }
+__device__ __forceinline__ SlotSpan pass_span(const PagedArgs& p, int b) { return pass_part(p, slot_span(p, b)); }
 __device__ __forceinline__ long long units_per_block(const TcPlan& pl, int slots) {
   return (pl.ustart[slots] + kTcBlocks - 1) / kTcBlocks;
 }

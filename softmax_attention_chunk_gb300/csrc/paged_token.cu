@@ -86,13 +86,19 @@ TokenWs token_ws(const PagedArgs& p, int n) {
   return w;
 }
 
-// Units of a (slot, head): kSetup that stand for the time a warp needs to begin it (no work, so that runs over many
+// Units of a (slot, head), none where the slot is left out (a bad row, no page for one of its at most 16 new tokens):
+// kSetup that stand for the time a warp needs to begin it (no work, so that runs over many
 // short sequences are not longer than others), then its live tiles, at least one (the new tokens themselves).
 constexpr int kSetup = 2;
 __device__ __forceinline__ int slot_units(const PagedArgs& p, int b, int mode, bool report) {
   const SlotSpan s = slot_span(p, b);
-  if (report && s.code) paged_error(p.c.status, s.code);
-  if (s.n == 0 || (mode == kOnlyOne && s.n != 1)) return 0;
+  const bool mine = s.n > 0 && (mode != kOnlyOne || s.n == 1);
+  const bool there = !mine || rows_there(p.c, b, s.t0, s.n);
+  if (report && (s.code || mine)) {
+    if (s.code || !there) paged_error(p.c.status, s.code ? s.code : (int)PATH_PAGED_BAD_PAGE);
+    note_extended(p.c, b, s.code || !there ? -1 : s.n);
+  }
+  if (!mine || !there) return 0;
   const int nt = live_tiles(s.t0, p.window, p.sinks, RT).count;
   return (kSetup + (nt > 0 ? nt : 1)) * p.c.heads;
 }
@@ -284,15 +290,11 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
       if (u == s0) {  // the new row joins the cache
         const long long kr = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0);
         const long long vr = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0);
-        if (kr < 0 || vr < 0) {
-          if (lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
-        } else {
-          if (lane < D / 8) {
-            *reinterpret_cast<uint4*>((__nv_bfloat16*)p.c.k_pool + kr * D + lane * 8) = ld16((const __nv_bfloat16*)p.k + tok * D + lane * 8);
-            *reinterpret_cast<uint4*>((__nv_bfloat16*)p.c.v_pool + vr * D + lane * 8) = ld16((const __nv_bfloat16*)p.v + tok * D + lane * 8);
-          }
-          if (FOX && lane == 0) p.c.a_pool[vr] = a_last + p.log_f[tok];
+        if (lane < D / 8) {
+          *reinterpret_cast<uint4*>((__nv_bfloat16*)p.c.k_pool + kr * D + lane * 8) = ld16((const __nv_bfloat16*)p.k + tok * D + lane * 8);
+          *reinterpret_cast<uint4*>((__nv_bfloat16*)p.c.v_pool + vr * D + lane * 8) = ld16((const __nv_bfloat16*)p.v + tok * D + lane * 8);
         }
+        if (FOX && lane == 0) p.c.a_pool[vr] = a_last + p.log_f[tok];
       }
     } else {
       const size_t item = (size_t)b * H + h;
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(DT) draft_prep_kernel(PagedArgs p, TokenWs w, 
       sm.vr[tid] = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + tid);
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(tid < n && (sm.kr[tid] < 0 || sm.vr[tid] < 0))) return;  // left out, which the streaming pass reports
   auto dot = [](const float* a, const float* c) {
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll 8
@@ -771,15 +773,11 @@ __global__ void __launch_bounds__(DT) draft_prep_kernel(PagedArgs p, TokenWs w, 
       float kx = sm.k[r][x];
       for (int m = r + 1; m < n; ++m) kx -= sm.x[m][r] * sm.w[m][x];
       const long long kr = sm.kr[r], vr = sm.vr[r];
-      if (kr < 0 || vr < 0) {
-        if (x == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
-      } else {
-        ((__nv_bfloat16*)p.c.k_pool)[kr * D + x] = __float2bfloat16_rn(kx);
-        ((__nv_bfloat16*)p.c.v_pool)[vr * D + x] = __float2bfloat16_rn(sm.v[r][x]);
-        if (FOX && x == 0) {
-          const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
-          p.c.a_pool[vr] = (last >= 0 ? p.c.a_pool[last] : 0.f) + sm.lf[r];
-        }
+      ((__nv_bfloat16*)p.c.k_pool)[kr * D + x] = __float2bfloat16_rn(kx);
+      ((__nv_bfloat16*)p.c.v_pool)[vr * D + x] = __float2bfloat16_rn(sm.v[r][x]);
+      if (FOX && x == 0) {
+        const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
+        p.c.a_pool[vr] = (last >= 0 ? p.c.a_pool[last] : 0.f) + sm.lf[r];
       }
     }
   }
@@ -864,6 +862,7 @@ __global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w,
   } else {
     start = (const int*)(ws + w.ustart);
   }
+  if (start[b + 1] == start[b]) return;  // left out
   const int run = run_length(start[p.c.slots], warps);
   const int kt = live_tiles(sp.t0, p.window, p.sinks, RT).count;
   const int each = kt > 0 ? kt : 1;
@@ -975,15 +974,11 @@ __global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs 
     if (head) {
       const long long kr = pool_row(p.c, p.c.k_table, p.c.k_pages, b, h, sp.t0);
       const long long vr = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0);
-      if (kr < 0 || vr < 0) {
-        if (lane == 0) paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
-      } else {
-        if (grp == 0) {
-          *reinterpret_cast<float4*>(kpool + kr * D + x4) = kv;
-          *reinterpret_cast<float4*>(vpool + vr * D + x4) = vv;
-        }
-        if (FOX && lane == 0) p.c.a_pool[vr] = a_last + lf;
+      if (grp == 0) {
+        *reinterpret_cast<float4*>(kpool + kr * D + x4) = kv;
+        *reinterpret_cast<float4*>(vpool + vr * D + x4) = vv;
       }
+      if (FOX && lane == 0) p.c.a_pool[vr] = a_last + lf;
     }
     const int i0 = u - s0, i1 = lt.count > 0 ? ue - s0 : i0;
     for (int i = i0; i < i1; ++i) {

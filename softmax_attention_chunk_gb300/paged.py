@@ -11,7 +11,12 @@ tokens over it, and the management of its pages.
     cache.check()                                         # raises what the device found, if anything
 
 Keys are held transported to the newest position, so a step rewrites every key of its sequence and key
-pages are never shared; value pages are (fork).  Argument marshalling only: every step runs in the CUDA
+pages are never shared; value pages are (fork).  What a step did to them cannot be taken back: draft tokens that
+may be rejected are checked on a fork,
+    cache.fork(parent, child); cache.reserve(n); o = cache.extend(..., q_start=for_child, max_new=m)
+    cache.free(child); o = cache.extend(..., q_start=accepted_for_parent)   # or keep the child, if all are accepted
+and advance() takes the tokens of an extend whole or not at all.  A slot that extend leaves out (its tokens'
+pages are missing after a refused reserve, say) is passed over by advance().  Argument marshalling only: every step runs in the CUDA
 library, on the current stream of the cache's device, without synchronising (check() does).  Calls that
 change one cache must be ordered on one stream.  A call can be captured into a CUDA graph: it reads
 lengths, tables and lists on the device.
@@ -24,7 +29,7 @@ from . import path_attn as pa
 
 CODES = {1: "a needed page-table entry is not a page of the pool", 2: "a sequence would outgrow its table row",
          3: "slot out of range, listed twice, empty where it must not be, or in use", 4: "not enough free pages",
-         5: "q_start falls, leaves the packed tokens or exceeds max_new"}
+         5: "q_start falls, leaves the packed tokens, exceeds max_new, or (advance) is not what extend was given"}
 
 
 class PagedCache:
@@ -50,13 +55,14 @@ class PagedCache:
                    torch.zeros(v_pages, heads, page_size, dtype=torch.float32, device=device) if fox else None)
 
     @classmethod
-    def from_tensors(cls, k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool=None):
-        """A cache over tensors that exist already (kept, not copied)."""
+    def from_tensors(cls, k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool=None, extended=None):
+        """A cache over tensors that exist already (kept, not copied).  extended (int32 [slots]; default: zeros) is
+        what extend leaves for advance: a second handle of one cache takes the first one's."""
         self = cls.__new__(cls)
-        self._bind(k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool)
+        self._bind(k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended)
         return self
 
-    def _bind(self, k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool):
+    def _bind(self, k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended=None):
         if k_pool.dim() != 4 or v_pool.dim() != 4 or k_table.dim() != 2:
             raise ValueError("pools are [pages, heads, page_size, head_dim], tables [slots, table_width]")
         kp, H, P, d = k_pool.shape
@@ -72,17 +78,21 @@ class PagedCache:
         if a_pool is not None:
             pa._need(a_pool, torch.float32, (vp, H, P), "a_pool")
         self.device = k_pool.device
-        for t in (v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool):
+        if extended is None:
+            extended = torch.zeros(slots, dtype=torch.int32, device=self.device)
+        pa._need(extended, torch.int32, (slots,), "extended")
+        for t in (v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended):
             if t is not None and t.device != self.device:
                 raise ValueError("the tensors of a cache lie on one device")
         self.k_pool, self.v_pool, self.a_pool = k_pool, v_pool, a_pool
         self.k_table, self.v_table, self.seq_len, self.k_ref, self.v_ref = k_table, v_table, seq_len, k_ref, v_ref
+        self.extended = extended
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.slots, self.heads, self.head_dim, self.page_size, self.dtype = slots, H, d, P, k_pool.dtype
         p = pa._p
         self.c = pa.path_paged_cache_t(slots, H, d, P, width, kp, vp, pa._DT[k_pool.dtype], p(k_pool), p(v_pool),
                                        p(a_pool), p(k_table), p(v_table), p(seq_len), p(k_ref), p(v_ref),
-                                       p(self.status))
+                                       p(self.status), p(extended))
         self._index = self.device.index
         self._plans = {}
         self._pages_bytes = pa.path_pages_workspace_size(self.c)
@@ -141,7 +151,8 @@ class PagedCache:
         return out
 
     def advance(self, q_start=None):
-        """seq_len grows by the new tokens of an extend with the same q_start."""
+        """seq_len grows by the new tokens of an extend with the same q_start (check() reports another one); slots
+        that it left out are passed over.  Without an extend before it: by rows that the caller wrote itself."""
         if q_start is not None:
             self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
         self._call(pa.path_paged_advance, pa._p(q_start))
