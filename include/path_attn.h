@@ -394,6 +394,9 @@ typedef struct {
   int* extended;    /* [slots] or NULL: tokens that the last path_paged_extend of a slot gave it and no
                        path_paged_advance has counted yet; -1: it left the slot out (start it at 0).
                        NULL: advance cannot tell and counts what its q_start says */
+  float* a_rest;    /* as a_pool, or NULL: what rounding the running sums to fp32 left of them (0 where the
+                       caller fills a_pool itself).  NULL: every call rounds the sums it appends by up to
+                       2^-24 of their size, which far into a sequence is more than a token adds */
 } path_paged_cache_t;
 
 /* Codes of the status word: what a call found on the device.  None of them makes a kernel leave its

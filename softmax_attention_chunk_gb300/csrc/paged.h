@@ -112,6 +112,18 @@ __device__ __forceinline__ SlotSpan slot_span(const PagedArgs& p, int b) {
   return slot_span_of(b, p.q_start, p.c.seq_len[b], p.total, p.max_new, p.c.table_width, p.c.page_size);
 }
 __device__ __forceinline__ void paged_error(int* status, int code) { atomicCAS(status, 0, code); }
+// Running sum of log f at a row of the value pool: a pair of fp32 numbers (48 bits) where the cache has a place for the
+// rest.  The sums are absolute, so that pages can be shared, and grow with the position: after a million tokens fp32
+// alone would lose a log f of 0.01 whole.
+__device__ __forceinline__ double load_sum(const path_paged_cache_t& c, long long at) {
+  return c.a_rest ? (double)c.a_pool[at] + c.a_rest[at] : c.a_pool[at];
+}
+__device__ __forceinline__ void store_sum(const path_paged_cache_t& c, long long at, double a) {
+  const float hi = (float)a;
+  c.a_pool[at] = hi;
+  if (c.a_rest) c.a_rest[at] = isfinite(hi) ? (float)(a - hi) : 0.f;
+}
+__device__ __forceinline__ float sum_rest(const path_paged_cache_t& c, long long at) { return c.a_rest ? c.a_rest[at] : 0.f; }
 // What a call did with slot b, for path_paged_advance: its new tokens, or -1 where it was left out.
 __device__ __forceinline__ void note_extended(const path_paged_cache_t& c, int b, int n) {
   if (c.extended) c.extended[b] = n;

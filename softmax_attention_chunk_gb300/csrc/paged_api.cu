@@ -31,7 +31,8 @@ int check_cache(const path_paged_cache_t* c) {
   if (rc != PATH_OK) return rc;
   if (!aligned(c->k_pool, 16) || !aligned(c->v_pool, 16) || (c->a_pool && !aligned(c->a_pool, 16))) return PATH_ERR_INVALID_ARG;
   if (!aligned(c->k_table, 4) || !aligned(c->v_table, 4) || !aligned(c->seq_len, 4) || !aligned(c->k_ref, 4) ||
-      !aligned(c->v_ref, 4) || !aligned(c->status, 4) || (c->extended && !aligned(c->extended, 4)))
+      !aligned(c->v_ref, 4) || !aligned(c->status, 4) || (c->extended && !aligned(c->extended, 4)) ||
+      (c->a_rest && !aligned(c->a_rest, 16)))
     return PATH_ERR_INVALID_ARG;
   return PATH_OK;
 }

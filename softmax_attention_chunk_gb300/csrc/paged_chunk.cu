@@ -469,7 +469,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   if (p.log_f) {
     __shared__ float wsum[NT / 32];
     const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
-    double a = last >= 0 ? p.c.a_pool[last] : 0.0;
+    double a = last >= 0 ? load_sum(p.c, last) : 0.0;
     for (int base = 0; base < sp.n; base += NT) {
       const int r = base + tid;
       float x = r < sp.n ? p.log_f[((size_t)sp.q0 + r) * H + h] : 0.f;
@@ -488,7 +488,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
         all += wsum[i];
       }
       const long long at = r < sp.n ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r) : -1;
-      if (at >= 0) p.c.a_pool[at] = (float)(a + before + x);
+      if (at >= 0) store_sum(p.c, at, a + before + x);
       a += all;
     }
   }
@@ -581,10 +581,13 @@ __global__ void __launch_bounds__(AT, D == 64 ? 4 : 2) attend_kernel(PagedArgs p
     return;
   }
   const float *kp = (const float*)p.c.k_pool, *vp = (const float*)p.c.v_pool;
-  float a_last = 0.f;
+  float a_last = 0.f, a_more = 0.f;  // the last row's sum, a pair
   if (p.log_f) {
     const long long last = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1);
-    if (last >= 0) a_last = p.c.a_pool[last];
+    if (last >= 0) {
+      a_last = p.c.a_pool[last];
+      a_more = sum_rest(p.c, last);
+    }
   }
   long long* place = reinterpret_cast<long long*>(sm + S::kRow);  // [tile parity][key, value][row]: the pools' rows, or -1
   // Places and biases (a_last - a_j; hidden rows -inf) of tile i.  A row that no query of the chunk sees is not looked up
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(AT, D == 64 ? 4 : 2) attend_kernel(PagedArgs p
     }
     place[at] = ka;
     place[at + KT] = va;
-    sm[S::kBias + (i & 1) * KT + tid] = va < 0 ? -INFINITY : p.log_f ? a_last - p.c.a_pool[va] : 0.f;
+    sm[S::kBias + (i & 1) * KT + tid] = va < 0 ? -INFINITY : p.log_f ? (a_last - p.c.a_pool[va]) + (a_more - sum_rest(p.c, va)) : 0.f;
   };
   auto fetch = [&](float* dst, const float* pool, int i, int value) {
     const long long* from = place + ((i & 1) * 2 + value) * KT;

@@ -634,7 +634,7 @@ __device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, 
   const SlotSpan sp = pass_span(p, b);
   if (pl.cstart[b + 1] == pl.cstart[b]) return;  // no new tokens, or left out
   const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
-  const float a0 = last >= 0 ? p.c.a_pool[last] : 0.f;
+  const double a0 = last >= 0 ? load_sum(p.c, last) : 0.0;
   float* cn = (float*)(ws + w.cn) + ((size_t)h * w.nblk + pl.bstart[b]) * MB;
   double carry = 0.0;
   for (int base = 0; base < sp.n; base += WT) {
@@ -659,7 +659,7 @@ __device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, 
       const double c = carry + before + x;
       cn[r] = (float)c;
       const long long at = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 + r);
-      if (at >= 0) p.c.a_pool[at] = (float)(a0 + c);
+      if (at >= 0) store_sum(p.c, at, a0 + c);
     }
     carry += all;
   }

@@ -435,8 +435,8 @@ __global__ void __launch_bounds__(CT) copy_kernel(path_paged_cache_t c, Lists w,
   const size_t abytes = c.a_pool ? (size_t)c.heads * c.page_size * 4 : 0;
   const long long pieces = (long long)((page_bytes + kPiece - 1) / kPiece);  // (a piece may be short)
   const long long apieces = (long long)((abytes + kPiece - 1) / kPiece);
-  const long long uk = nk * pieces, uv = nv * pieces, ua = nv * apieces;
-  for (long long u = blockIdx.x; u < uk + uv + ua; u += gridDim.x) {
+  const long long uk = nk * pieces, uv = nv * pieces, ua = nv * apieces, ur = c.a_rest ? ua : 0;
+  for (long long u = blockIdx.x; u < uk + uv + ua + ur; u += gridDim.x) {
     char* pool;
     const int *src, *dst;
     size_t size = page_bytes;
@@ -449,6 +449,10 @@ __global__ void __launch_bounds__(CT) copy_kernel(path_paged_cache_t c, Lists w,
     } else {
       x = u - uk - uv;
       pool = (char*)c.a_pool; src = w.vsrc; dst = w.vdst;
+      if (x >= ua) {
+        x -= ua;
+        pool = (char*)c.a_rest;
+      }
       size = abytes;
       per = apieces;
     }

@@ -62,6 +62,7 @@ struct __align__(1024) TcSmem {
   uint8_t z[ZT][X][TILE];
   uint8_t buf[NBUF][X][TILE];
   float aj[FOX ? NINFO : 1][FOX ? KT : 1];  // forget gate: running sums of the tile's rows
+  float ar[FOX ? NINFO : 1][FOX ? KT : 1];  // and what fp32 left of them (cached rows of a cache that keeps it)
   alignas(16) float kbias[FOX ? 2 : 1][FOX ? 2 : 1][FOX ? KT : 4];  // the softmax threads' key biases (log2 units)
   uint32_t okmask[NINFO];       // 16-row groups of the tile that are there
   uint64_t info[NINFO];
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(ATHREADS, 1)
         if (!ok) break;
         if (lane == 0) {
           s.okmask[ib] = groups;
-          if (FOX) mbar_arrive_expect_tx(&s.info[ib], loads * pr * 4);
+          if (FOX) mbar_arrive_expect_tx(&s.info[ib], loads * pr * (!g.own && p.c.a_rest ? 8 : 4));
           else mbar_arrive(&s.info[ib]);
           mbar_arrive_expect_tx(&s.full[kb], loads * pr * 128 * X);
         }
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(ATHREADS, 1)
             const float* a = g.own ? pl.cn + ((size_t)g.h * pl.blocks + pl.bstart[g.b]) * kTcBlockTokens + j0
                                    : p.c.a_pool + ((size_t)vp * p.c.heads + g.h) * P + in;
             bulk_load(s.aj[ib] + lane * pr, a, pr * 4, &s.info[ib]);
+            if (!g.own && p.c.a_rest) bulk_load(s.ar[ib] + lane * pr, p.c.a_rest + (a - p.c.a_pool), pr * 4, &s.info[ib]);
           }
         }
         if (n + 1 >= NBUF) ok = mbar_wait_lean(&s.empty[vb], ((n + 1) / NBUF - 1) & 1, err, 3);
@@ -383,10 +385,14 @@ __global__ void __launch_bounds__(ATHREADS, 1)
       const int pos = g.sp.t0 + R / p.G;
       // positions of this warp's tile: a tile of keys that all of them see needs no mask
       const int p_max = g.sp.t0 + (g.pair * 256 + 128 * t + 127) / p.G;
-      float a_last = 0.f;
+      float a_last = 0.f, a_more = 0.f;
+      const bool pairs = FOX && !g.own && p.c.a_rest;
       if (FOX && !g.own && g.sp.t0 > 0) {  // (own rows: the sums start at 0)
         const long long row = pool_row(p.c, p.c.v_table, p.c.v_pages, g.b, g.h, g.sp.t0 - 1);
-        if (row >= 0) a_last = p.c.a_pool[row];
+        if (row >= 0) {
+          a_last = p.c.a_pool[row];
+          a_more = sum_rest(p.c, row);
+        }
       }
       float m = -INFINITY, l = 0.f;
       for (int k = 0; (FOX || ok) && k < nk; ++k, ++kk, ++ns) {
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(ATHREADS, 1)
         // forget gate: the keys' biases, one per thread of the tile, doubly buffered by the barrier of the next step
         float* kb = s.kbias[FOX ? t : 0][FOX ? (ns & 1) : 0];
         if (FOX) {
-          kb[r] = (a_last - s.aj[kk % NINFO][r]) * kLog2e;
+          kb[r] = ((a_last - s.aj[kk % NINFO][r]) + (pairs ? a_more - s.ar[kk % NINFO][r] : 0.f)) * kLog2e;
           asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
         }
         // bits of the keys 32 q .. 32 q + 31 that the row sees: there, and a first token or in the window

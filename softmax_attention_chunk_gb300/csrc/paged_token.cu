@@ -203,23 +203,27 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
     uint32_t wf[KB][4];                          // ONE: the lane's pieces of w
     float beta = 0.f;
     const uint32_t* frag = nullptr;              // drafts: this item's fragments, lane-major words
-    // bias of a column's token since t0 (FOX) and its position
+    // bias of a column's token since t0 (FOX, drafts) and its position
     float cb[NQ8][2];
     int cp[NQ8][2];
 #pragma unroll
     for (int q = 0; q < NQ8; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int col = 8 * q + 2 * t + e, i = col < cols ? col / G : 0;
+        const int col = 8 * q + 2 * t + e, i = !ONE && col < cols ? col / G : 0;
         cp[q][e] = sp.t0 + i;
         cb[q][e] = 0.f;
-        if (FOX)
-          for (int x = 0; x <= i; ++x) cb[q][e] += p.log_f[((size_t)sp.q0 + x) * H + h];
+        if (FOX && !ONE)
+          for (int x = 0; x <= i; ++x) cb[q][e] += p.log_f[((size_t)sp.q0 + x) * H + h] * kLog2e;
       }
-    float a_last = 0.f;
-    if (FOX && sp.t0 > 0) {
+    // forget gate: lanes 0 and 1 of a row's four hold the sums of rows g and g + 8, lanes 2 and 3 what fp32 left of them;
+    // they arrive with the tile's keys (24 x 6000..16384 rows under a window of 4096, 16 heads, head dim 64: 117 us, with
+    // the values, waited for behind the next keys' loads, 133)
+    const float* sums = t < 2 ? p.c.a_pool : p.c.a_rest;
+    float last = 0.f;  // the last row's sum, or its rest
+    if (FOX && sp.t0 > 0 && sums) {
       const long long r = pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1);
-      if (r >= 0) a_last = p.c.a_pool[r];
+      if (r >= 0) last = sums[r];
     }
     const size_t tok = (size_t)sp.q0 * H + h;    // the first new token's row of k, v, w
     if constexpr (ONE) {
@@ -294,8 +298,12 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
           *reinterpret_cast<uint4*>((__nv_bfloat16*)p.c.k_pool + kr * D + lane * 8) = ld16((const __nv_bfloat16*)p.k + tok * D + lane * 8);
           *reinterpret_cast<uint4*>((__nv_bfloat16*)p.c.v_pool + vr * D + lane * 8) = ld16((const __nv_bfloat16*)p.v + tok * D + lane * 8);
         }
-        if (FOX && lane == 0) p.c.a_pool[vr] = a_last + p.log_f[tok];
+        if (FOX) {
+          const float rest = __shfl_sync(0xffffffffu, last, 2);
+          if (lane == 0) store_sum(p.c, vr, (double)last + rest + p.log_f[tok]);
+        }
       }
+      if (FOX && t >= 2) last += p.log_f[tok];  // the one token's bias
     } else {
       const size_t item = (size_t)b * H + h;
       frag = (const uint32_t*)(ws + w.frag) + item * 32 * frag_words<D, NQ8>();
@@ -322,7 +330,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
     // ---- the cached tiles ----
     const int i0 = u - s0, i1 = lt.count > 0 ? ue - s0 : i0;  // (no cached rows: nothing to stream)
     uint4 kr[2][KB], vr[4][CS];
-    float aj[2] = {0.f, 0.f};
+    float aj = 0.f;  // this lane's part of the tile's sums
     auto page = [&](const int* table, int i) { return table[(size_t)b * p.c.table_width + newest_tile(lt, i) * RT / P]; };
     int kp = -1, vp = -1, kpn = -1, vpn = -1;  // pages of the current and the next tile
     long long krow = 0, vrow = 0;
@@ -346,10 +354,9 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
       for (int y = 0; y < 4; ++y)
 #pragma unroll
         for (int x = 0; x < CS; ++x) vr[y][x] = ld16(at + (size_t)(2 * t + (y & 1) + 8 * (y >> 1)) * D + 64 * x);
-      if (FOX) {
-        aj[0] = p.c.a_pool[r + g];
-        aj[1] = p.c.a_pool[r + g + 8];
-      }
+    };
+    auto load_a = [&](long long r) {
+      if (FOX && sums) aj = sums[r + g + 8 * (t & 1)];
     };
     bool ok = false;
     if (i0 < i1) {
@@ -359,6 +366,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
       if (ok) {
         rows_of(i0, kp, vp, krow, vrow);
         load_k(krow);
+        load_a(vrow);
         load_v(vrow);
       }
       if (i0 + 1 < i1) {
@@ -483,12 +491,21 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
           }
         }
       }
-      // the next tile's keys set out as soon as this one's registers are free
+      float bias0 = 0.f, bias1 = 0.f;  // a_last - a_j of rows g and g + 8, log2 units
+      if (FOX && cur) {
+        float x = last - aj;
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        const float y = __shfl_xor_sync(0xffffffffu, x, 1);
+        bias0 = (t & 1 ? y : x) * kLog2e;
+        bias1 = (t & 1 ? x : y) * kLog2e;
+      }
+      // the next tile's keys (and sums) set out as soon as this one's registers are free
       long long kn = 0, vn = 0;
       ok = i + 1 < i1 && good(kpn, vpn);
       if (ok) {
         rows_of(i + 1, kpn, vpn, kn, vn);
         load_k(kn);
+        load_a(vn);
       }
       krow = kn;
       const long long vnext = vn;
@@ -497,14 +514,13 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
         vpn = page(p.c.v_table, i + 2);
       }
       if (cur) {
-        const float bias0 = FOX ? a_last - aj[0] : 0.f, bias1 = FOX ? a_last - aj[1] : 0.f;
         bool up = false;
 #pragma unroll
         for (int q = 0; q < NQ8; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float x = s[q][e] * p.scl;
-            if (FOX) x += ((e < 2 ? bias0 : bias1) + cb[q][e & 1]) * kLog2e;
+            if (FOX) x += (e < 2 ? bias0 : bias1) + (ONE ? 0.f : cb[q][e & 1]);
             if (!whole) {
               const int j = j0 + g + (e < 2 ? 0 : 8);
               if (j >= sp.t0 || !sees(p.window, p.sinks, cp[q][e & 1], j)) x = -INFINITY;
@@ -777,7 +793,7 @@ __global__ void __launch_bounds__(DT) draft_prep_kernel(PagedArgs p, TokenWs w, 
       ((__nv_bfloat16*)p.c.v_pool)[vr * D + x] = __float2bfloat16_rn(sm.v[r][x]);
       if (FOX && x == 0) {
         const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
-        p.c.a_pool[vr] = (last >= 0 ? p.c.a_pool[last] : 0.f) + sm.lf[r];
+        store_sum(p.c, vr, (last >= 0 ? load_sum(p.c, last) : 0.0) + sm.lf[r]);
       }
     }
   }
@@ -953,11 +969,14 @@ __global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs 
     const float beta = clamp_beta(p.beta[tok]);
     const float4 wv = ld4((const float*)p.w + tok * D + x4), kv = ld4((const float*)p.k + tok * D + x4);
     const float4 vv = ld4((const float*)p.v + tok * D + x4);
-    float a_last = 0.f, lf = 0.f;
+    float a_last = 0.f, a_more = 0.f, lf = 0.f;
     if (FOX) {
       lf = p.log_f[tok];
       const long long r = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
-      if (r >= 0) a_last = p.c.a_pool[r];
+      if (r >= 0) {
+        a_last = p.c.a_pool[r];
+        a_more = sum_rest(p.c, r);
+      }
     }
     float4 z[GP], acc[GP];
     float m[GP], l[GP];
@@ -978,7 +997,7 @@ __global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs 
         *reinterpret_cast<float4*>(kpool + kr * D + x4) = kv;
         *reinterpret_cast<float4*>(vpool + vr * D + x4) = vv;
       }
-      if (FOX && lane == 0) p.c.a_pool[vr] = a_last + lf;
+      if (FOX && lane == 0) store_sum(p.c, vr, (double)a_last + a_more + lf);
     }
     const int i0 = u - s0, i1 = lt.count > 0 ? ue - s0 : i0;
     for (int i = i0; i < i1; ++i) {
@@ -995,13 +1014,13 @@ __global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs 
 #pragma unroll 1
       for (int r0 = 0; r0 < RT; r0 += AHEAD * RW) {
         float4 kk[AHEAD], va[AHEAD];
-        float aj[AHEAD];
+        float bias[AHEAD];  // a_last - a_j
 #pragma unroll
         for (int e = 0; e < AHEAD; ++e) {
           const int r = r0 + e * RW + grp;
           kk[e] = ld4(krow + (size_t)r * D);
           va[e] = ld4(vrow + (size_t)r * D);
-          aj[e] = FOX ? p.c.a_pool[vr0 + r] : 0.f;
+          bias[e] = FOX ? (a_last - p.c.a_pool[vr0 + r]) + (a_more - sum_rest(p.c, vr0 + r)) : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < AHEAD; ++e) {
@@ -1014,10 +1033,9 @@ __global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs 
             *reinterpret_cast<float4*>(krow + (size_t)r * D) =
                 make_float4(kk[e].x - c * wv.x, kk[e].y - c * wv.y, kk[e].z - c * wv.z, kk[e].w - c * wv.w);
           if (j < sp.t0 && sees(p.window, p.sinks, sp.t0, j)) {  // (uniform in the row's lanes)
-            const float bias = FOX ? (a_last - aj[e] + lf) * kLog2e : 0.f;
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
-              const float v = s[g] + bias, mn = fmaxf(m[g], v);
+              const float v = FOX ? s[g] + (bias[e] + lf) * kLog2e : s[g], mn = fmaxf(m[g], v);
               const float f = fast_exp2(m[g] - mn), pr = fast_exp2(v - mn);
               m[g] = mn;
               l[g] = l[g] * f + pr;

@@ -55,14 +55,15 @@ class PagedCache:
                    torch.zeros(v_pages, heads, page_size, dtype=torch.float32, device=device) if fox else None)
 
     @classmethod
-    def from_tensors(cls, k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool=None, extended=None):
+    def from_tensors(cls, k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool=None, extended=None, a_rest=None):
         """A cache over tensors that exist already (kept, not copied).  extended (int32 [slots]; default: zeros) is
-        what extend leaves for advance: a second handle of one cache takes the first one's."""
+        what extend leaves for advance, a_rest (as a_pool; default: zeros) what rounding the gate's running sums to
+        float32 left of them: a second handle of one cache takes the first one's."""
         self = cls.__new__(cls)
-        self._bind(k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended)
+        self._bind(k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended, a_rest)
         return self
 
-    def _bind(self, k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended=None):
+    def _bind(self, k_pool, v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended=None, a_rest=None):
         if k_pool.dim() != 4 or v_pool.dim() != 4 or k_table.dim() != 2:
             raise ValueError("pools are [pages, heads, page_size, head_dim], tables [slots, table_width]")
         kp, H, P, d = k_pool.shape
@@ -81,18 +82,24 @@ class PagedCache:
         if extended is None:
             extended = torch.zeros(slots, dtype=torch.int32, device=self.device)
         pa._need(extended, torch.int32, (slots,), "extended")
-        for t in (v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended):
+        if a_pool is not None and a_rest is None:
+            a_rest = torch.zeros_like(a_pool)
+        if a_rest is not None:
+            pa._need(a_rest, torch.float32, (vp, H, P), "a_rest")
+            if a_pool is None:
+                raise ValueError("a_rest goes with a_pool")
+        for t in (v_pool, k_table, v_table, seq_len, k_ref, v_ref, a_pool, extended, a_rest):
             if t is not None and t.device != self.device:
                 raise ValueError("the tensors of a cache lie on one device")
         self.k_pool, self.v_pool, self.a_pool = k_pool, v_pool, a_pool
         self.k_table, self.v_table, self.seq_len, self.k_ref, self.v_ref = k_table, v_table, seq_len, k_ref, v_ref
-        self.extended = extended
+        self.extended, self.a_rest = extended, a_rest
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.slots, self.heads, self.head_dim, self.page_size, self.dtype = slots, H, d, P, k_pool.dtype
         p = pa._p
         self.c = pa.path_paged_cache_t(slots, H, d, P, width, kp, vp, pa._DT[k_pool.dtype], p(k_pool), p(v_pool),
                                        p(a_pool), p(k_table), p(v_table), p(seq_len), p(k_ref), p(v_ref),
-                                       p(self.status), p(extended))
+                                       p(self.status), p(extended), p(a_rest))
         self._index = self.device.index
         self._plans = {}
         self._pages_bytes = pa.path_pages_workspace_size(self.c)

@@ -42,7 +42,7 @@ class path_paged_cache_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("slots", "heads", "head_dim", "page_size", "table_width", "k_pages",
                                             "v_pages", "cache_dtype")] + \
                [(n, ctypes.c_void_p) for n in ("k_pool", "v_pool", "a_pool", "k_table", "v_table", "seq_len", "k_ref",
-                                               "v_ref", "status", "extended")]
+                                               "v_ref", "status", "extended", "a_rest")]
 
 
 class path_paged_desc_t(ctypes.Structure):
