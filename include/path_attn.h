@@ -419,6 +419,10 @@ typedef struct {
   float scale;       /* multiplies the logit; the forget bias is added unscaled */
   int window;        /* 0: every earlier token is seen; W > 0: the token at position p sees j > p - W ... */
   int sinks;         /* ... and the first `sinks` tokens of its sequence */
+  int max_multi;     /* at most so many slots have several new tokens (0: any number).  Others beyond them may
+                        be left out with PATH_PAGED_BAD_START.  What the workspace of a call with max_new > 1
+                        is for: unstated, it holds half as many slots as there are new tokens, in rounds of
+                        what about 4 GiB hold */
 } path_paged_desc_t;
 
 /* Bytes of workspace path_paged_extend needs; 0 if cache or desc is invalid.  Host only. */

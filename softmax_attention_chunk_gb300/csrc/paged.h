@@ -9,6 +9,14 @@ namespace pathattn {
 constexpr int kPagedMaxGroup = 16;   // query heads per key head
 constexpr int kPagedChunk = 32;      // new tokens per UT chunk of the CUDA-core kernels
 
+// Slots with several new tokens go through the chunk kernels in rounds of as many slots as this workspace holds (one at
+// least).  A call's host side knows neither which slots these are nor, unless it is told, how many: up to half as many as
+// there are new tokens, and each may end in a partly filled chunk, block and query pair.  So a workspace for all of them at
+// once grows with the slots of the cache (2 tokens of a slot, 8 key and 32 query heads of dim 128: 9 MB; 512 tokens beside 1023
+// single ones 9 GiB).  A round more costs its launches and a tail (1024 prompts of 30 tokens, those heads: 5.06 ms in one round,
+// 5.55 in three, 6.16 in five of 2 GiB).
+constexpr size_t kRoundBytes = size_t(4) << 30;
+
 // What a kernel of path_paged_extend needs of the call, by value.
 struct PagedArgs {
   path_paged_cache_t c;
@@ -21,6 +29,7 @@ struct PagedArgs {
   const float *beta, *log_f;
   void* o;
   int min_new;          // more tokens: slots with fewer new ones are left to the streaming kernels
+  int multi;            // slots with several new tokens that the caller allows, 0: any number
   int skip;             // prompt chunks: new tokens of each slot that earlier passes have done
 };
 
@@ -29,6 +38,27 @@ struct PagedArgs {
 #else
 #define PATH_HD inline
 #endif
+
+// The most slots with several new tokens that a call may have, and of these those that a round takes: bytes(n) is the
+// workspace for n of them.
+inline int most_multi(const PagedArgs& p) {
+  int n = p.total / 2 < p.c.slots ? p.total / 2 : p.c.slots;
+  if (p.multi > 0 && p.multi < n) n = p.multi;
+  return n < 1 ? 1 : n;
+}
+template <typename F>
+int round_slots(int most, F bytes) {
+  if (bytes(most) <= kRoundBytes) return most;
+  int lo = 1, hi = most;  // lo: fits, or is one
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (bytes(mid) <= kRoundBytes) lo = mid; else hi = mid;
+  }
+  const int rounds = (most + lo - 1) / lo;
+  return (most + rounds - 1) / rounds;  // (rounds of like size)
+}
+// Bytes asked for: those of a round, and with several rounds no less than smaller calls in one round ask for.
+inline size_t round_bytes(size_t bytes, bool rounds) { return rounds && bytes < kRoundBytes ? kRoundBytes : bytes; }
 
 // The new tokens of slot b: first packed token and count, and the cached length.  A bad row of q_start, a
 // negative or overlong length gives count 0 and its code.

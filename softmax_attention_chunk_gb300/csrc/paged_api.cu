@@ -38,7 +38,7 @@ int check_cache(const path_paged_cache_t* c) {
 }
 int check_paged_desc(const path_paged_cache_t* c, const path_paged_desc_t* d) {
   if (!d) return PATH_ERR_INVALID_ARG;
-  if (d->heads_q <= 0 || d->total_tokens < 0 || d->max_new < 0 || d->window < 0 || d->sinks < 0 || !isfinite(d->scale))
+  if (d->heads_q <= 0 || d->total_tokens < 0 || d->max_new < 0 || d->window < 0 || d->sinks < 0 || d->max_multi < 0 || !isfinite(d->scale))
     return PATH_ERR_INVALID_ARG;
   if (d->heads_q % c->heads != 0) return PATH_ERR_INVALID_ARG;
   if (d->heads_q / c->heads > kPagedMaxGroup) return PATH_ERR_UNSUPPORTED;
@@ -54,6 +54,7 @@ PagedArgs paged_args(const path_paged_cache_t* c, const path_paged_desc_t* d) {
   p.max_new = d->max_new < d->total_tokens ? d->max_new : d->total_tokens;
   p.window = d->window;
   p.sinks = d->sinks;
+  p.multi = d->max_multi;
   p.scl = d->scale * kLog2e;
   return p;
 }

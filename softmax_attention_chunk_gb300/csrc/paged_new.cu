@@ -116,12 +116,13 @@ __device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.commit_gro
 
 // ---- workspace ----
 struct NewWs {
-  int nch, nblk;           // chunks and blocks of any legal pass
-  size_t cstart, bstart, pstart, ustart, vstart, rstart;  // plan (TcPlan)
+  int most, group;         // slots with several new tokens: of any legal call, of a round
+  int nch, nblk;           // chunks and blocks of any legal pass of a round
+  size_t cstart, bstart, pstart, ustart, vstart, rstart, mstart;  // plan (TcPlan)
   size_t nx, nuw;          // -X [nch][H][64][64], -U W [2][nch][H][64][D] (high, rest)
   size_t kr, f;            // K-> [2][nch][H][64][D], F [2][nch][H][D][D] (high, rest)
   size_t ke, fb;           // keys at their block's end [2][nblk][H][256][D], block products [2][nblk][H][D][D]
-  size_t gb, mm;           // G_b [2][nblk][H][D][D], M [2][slots][H][D][D]
+  size_t gb, mm;           // G_b [2][nblk][H][D][D], M [2][group][H][D][D]
   size_t ver;              // versions: rows [D]
   size_t cn;               // forget gate: sums since the start of the call [H][nblk * 256]
   size_t zs, z;            // queries at the block's and at the call's start [2][H][pairs][256][D] (rest: TcPlan)
@@ -131,10 +132,10 @@ struct NewWs {
   long long ver_rows;
   int pairs;
 };
-NewWs new_ws(const PagedArgs& p) {
+NewWs new_ws(const PagedArgs& p, int group) {  // for rounds of `group` slots
   NewWs w{};
   const size_t D = p.c.head_dim, H = p.c.heads, hq = p.hq;
-  const long long live = p.c.slots < p.total ? p.c.slots : p.total;
+  const long long live = w.group = group;
   const long long most = p.max_new < kTcPassTokens ? p.max_new : kTcPassTokens;  // new tokens of a slot in a pass
   const long long tokens = p.total < most * live ? p.total : most * live;
   auto parts_of = [&](long long x) { const long long n = (tokens + (x - 1) * live) / x; return n < 1 ? 1LL : n; };
@@ -151,6 +152,7 @@ NewWs new_ws(const PagedArgs& p) {
   w.bstart = take(S1 * 4);
   w.pstart = take(S1 * 4);
   w.rstart = take(S1 * 4);
+  w.mstart = take(S1 * 4);
   w.vstart = take(S1 * 8);
   w.ustart = take(S1 * 8);
   w.nx = take((size_t)w.nch * H * C * C * 2);
@@ -160,7 +162,7 @@ NewWs new_ws(const PagedArgs& p) {
   w.ke = take((size_t)2 * w.nblk * H * MB * D * 2);
   w.fb = take((size_t)2 * w.nblk * H * D * D * 2);
   w.gb = take((size_t)2 * w.nblk * H * D * D * 2);
-  w.mm = take((size_t)2 * p.c.slots * H * D * D * 2);
+  w.mm = take((size_t)2 * group * H * D * D * 2);
   w.ver = take((size_t)w.ver_rows * D * 2);
   w.cn = take((size_t)H * w.nblk * MB * 4);
   w.zs = take((size_t)2 * H * w.pairs * kTcPair * D * 2);
@@ -177,12 +179,21 @@ NewWs new_ws(const PagedArgs& p) {
   return w;
 }
 
+NewWs new_ws(const PagedArgs& p) {
+  const int most = most_multi(p);
+  NewWs w = new_ws(p, round_slots(most, [&](int n) { return new_ws(p, n).total; }));
+  w.most = most;
+  return w;
+}
+
 // ---- plan ----
-// Exclusive prefix sums over the slots, all at once: chunks, blocks, query pairs, rewrite tiles, version rows, units.
-__global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool report) {
+// Exclusive prefix sums over the slots, all at once: chunks, blocks, query pairs, rewrite tiles, version rows, units, slots of
+// the round.  Slots with several new tokens are numbered in order; the round takes those from number `first` on, and those from number `most` on are left out.
+__global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, int first, int most, bool report) {
   chain();
-  constexpr int N = 6;
+  constexpr int N = 7;
   __shared__ long long wsum[N][32], carry[N];
+  __shared__ int multi[32];
   __shared__ unsigned long long tokens;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < N) carry[tid] = 0;
@@ -190,21 +201,39 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
     *pl.err = 0;
     tokens = 0;
   }
+  int numbered = 0;  // slots with several new tokens so far
   __syncthreads();
   for (int base = 0; base < p.c.slots; base += 1024) {
     const int b = base + tid;
-    long long v[N] = {0, 0, 0, 0, 0, 0}, x[N];
-    SlotSpan all{}, s{};
+    long long v[N] = {0, 0, 0, 0, 0, 0, 0}, x[N];
+    SlotSpan all{};
+    int n = 0;
     if (b < p.c.slots) {
       all = slot_span(p, b);
-      s = pass_part(p, all);
-      if (report && s.code) paged_error(p.c.status, s.code);
+      if (report && all.code) paged_error(p.c.status, all.code);
+      if (all.n < p.min_new) all.n = 0;
+      n = all.n;
     }
-    leave_out_pageless(p.c, b, all.t0, all.n, s, report);
-    if (b < p.c.slots) {
-      if (report && all.n >= p.min_new) note_extended(p.c, b, s.n > 0 ? all.n : -1);
-      if (s.n > 0) {
-        atomicAdd(&tokens, (unsigned long long)s.n);
+    leave_out_pageless(p.c, b, all.t0, n, all, report);
+    const unsigned have = __ballot_sync(0xffffffffu, all.n > 0);
+    if (lane == 0) multi[warp] = __popc(have);
+    __syncthreads();
+    int number = numbered + __popc(have & ((1u << lane) - 1));
+    for (int i = 0; i < 32; ++i) {
+      if (i < warp) number += multi[i];
+      numbered += multi[i];
+    }
+    if (all.n > 0) {
+      atomicAdd(&tokens, (unsigned long long)all.n);
+      if (number >= most) {
+        all.n = 0;
+        if (report) paged_error(p.c.status, PATH_PAGED_BAD_START);
+      }
+    }
+    if (report && n > 0) note_extended(p.c, b, all.n > 0 ? n : -1);
+    if (all.n > 0) {
+      const SlotSpan s = pass_part(p, all);
+      if (s.n > 0 && number >= first && number - first < pl.group) {
         const long long H = p.c.heads, np = ((long long)s.n * p.G + kTcPair - 1) / kTcPair, nb = (s.n + MB - 1) / MB;
         v[0] = (s.n + C - 1) / C;
         v[1] = nb;
@@ -212,6 +241,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
         v[3] = live_tiles(s.t0, p.window, p.sinks, kRewriteRows).count;
         v[4] = H * (MB / 2) * nb * (nb - 1);
         v[5] = H * (np * live_tiles(s.t0, p.window, p.sinks, kTcKeys).count + new_units(np, p.G));
+        v[6] = 1;
       }
     }
 #pragma unroll
@@ -248,6 +278,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
       pl.rstart[b] = (int)e[3];
       pl.vstart[b] = e[4];
       pl.ustart[b] = e[5];
+      pl.mstart[b] = (int)e[6];
     }
     __syncthreads();
   }
@@ -259,6 +290,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
     pl.rstart[S] = (int)carry[3];
     pl.vstart[S] = carry[4];
     pl.ustart[S] = carry[5];
+    pl.mstart[S] = (int)carry[6];
   }
   // rows of q_start that overlap: more tokens than the workspace is for
   if (tokens > (unsigned long long)p.total) {
@@ -266,7 +298,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, bool
     __syncthreads();
     for (int b = tid; b <= S; b += 1024) {
       if (report && b < S && slot_span(p, b).n >= p.min_new) note_extended(p.c, b, -1);
-      pl.cstart[b] = pl.bstart[b] = pl.pstart[b] = pl.rstart[b] = 0;
+      pl.cstart[b] = pl.bstart[b] = pl.pstart[b] = pl.rstart[b] = pl.mstart[b] = 0;
       pl.vstart[b] = pl.ustart[b] = 0;
     }
   }
@@ -606,8 +638,8 @@ __device__ void carry_on(const PagedArgs& p, const NewWs& w, const TcPlan& pl, c
     s.times(at, at + fstep, sm);
   }
   if (slab >= CPB) {
-    bf16* at = (bf16*)(ws + w.mm) + ((size_t)b * H + h) * D * D + (size_t)ir * D;
-    s.store(at, at + (size_t)p.c.slots * H * D * D);
+    bf16* at = (bf16*)(ws + w.mm) + ((size_t)pl.mstart[b] * H + h) * D * D + (size_t)ir * D;
+    s.store(at, at + (size_t)pl.group * H * D * D);
     return;
   }
   // the appended rows
@@ -627,12 +659,14 @@ __device__ void carry_on(const PagedArgs& p, const NewWs& w, const TcPlan& pl, c
   }
 }
 
-// Sums of log f since the start of the pass, and the running sums of the appended rows: one block per (slot, head).
-__device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, char* ws, int b, int h) {
+// Sums of log f since the start of the pass, and the running sums of the appended rows: one block per (slot of the round,
+// head).
+__device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, char* ws, int m, int h) {
   __shared__ float wsum[WT / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.c.heads;
+  if (m >= pl.mstart[p.c.slots]) return;
+  const int b = owner(pl.mstart, p.c.slots, m);
   const SlotSpan sp = pass_span(p, b);
-  if (pl.cstart[b + 1] == pl.cstart[b]) return;  // no new tokens, or left out
   const long long last = sp.t0 > 0 ? pool_row(p.c, p.c.v_table, p.c.v_pages, b, h, sp.t0 - 1) : -1;
   const double a0 = last >= 0 ? load_sum(p.c, last) : 0.0;
   float* cn = (float*)(ws + w.cn) + ((size_t)h * w.nblk + pl.bstart[b]) * MB;
@@ -665,7 +699,7 @@ __device__ void gate_sums(const PagedArgs& p, const NewWs& w, const TcPlan& pl, 
   }
 }
 
-// Blocks: (block, head, slab) of level 1, then (slot, head) of the gate's sums.
+// Blocks: (block, head, slab) of level 1, then (slot of the round, head) of the gate's sums.
 template <int D>
 __global__ void __launch_bounds__(WT) carry_in_block_kernel(PagedArgs p, NewWs w, TcPlan pl, char* ws) {
   chain();
@@ -1045,6 +1079,8 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
       (e = cudaFuncSetAttribute(sk, big, (int)s4)) != cudaSuccess)
     return e;
   TcPlan pl{};
+  pl.group = w.group;
+  pl.mstart = (int*)(ws + w.mstart);
   pl.pairs = w.pairs;
   pl.blocks = w.nblk;
   pl.cstart = (int*)(ws + w.cstart);
@@ -1064,25 +1100,29 @@ cudaError_t new_t(PagedArgs p, char* ws, cudaStream_t st) {
   pl.mm = ws + w.mm;
   pl.err = (int*)(ws + w.err);
   const bool many = p.max_new > MB;  // a slot may have a second block
-  for (p.skip = 0; p.skip < p.max_new; p.skip += kTcPassTokens) {
-    const unsigned carries = (unsigned)(w.nblk * H * (CPB + D / 64));
-    if ((e = launch_chained(plan_kernel, 1, 1024, 0, st, p, pl, p.skip == 0)) != cudaSuccess ||
-        (e = launch_chained(prep, dim3(w.nch, H), PT, s1, st, p, w, pl, ws)) != cudaSuccess ||
-        (e = launch_chained(c1, carries + (fox ? p.c.slots * H : 0), WT, s2, st, p, w, pl, ws)) != cudaSuccess ||
-        (e = launch_chained(qk, carries + w.nch * p.hq, WT, s3 > s2 ? s3 : s2, st, p, w, pl, ws)) != cudaSuccess)
-      return e;
-    if (many && (e = launch_chained(sk, dim3(w.pairs * 4, H), WT, s4, st, p, w, pl, ws)) != cudaSuccess) return e;
-    const int gr = (long long)w.nch * p.hq < 1024 ? 16 : C;
-    if ((e = launch_attend_tc(p, pl, st)) != cudaSuccess || (e = launch_rewrite_tc(p, pl, st)) != cudaSuccess ||
-        (e = launch_chained(merge_kernel<D>, dim3(w.nch * (C / gr), p.hq), GT, 0, st, p, w, pl, gr, ws)) != cudaSuccess)
-      return e;
-  }
+  const unsigned carries = (unsigned)(w.nblk * H * (CPB + D / 64));
+  const int gr = (long long)w.nch * p.hq < 1024 ? 16 : C;
+  for (int first = 0; first < w.most; first += w.group)
+    for (p.skip = 0; p.skip < p.max_new; p.skip += kTcPassTokens) {
+      if ((e = launch_chained(plan_kernel, 1, 1024, 0, st, p, pl, first, w.most, first == 0 && p.skip == 0)) != cudaSuccess ||
+          (e = launch_chained(prep, dim3(w.nch, H), PT, s1, st, p, w, pl, ws)) != cudaSuccess ||
+          (e = launch_chained(c1, carries + (fox ? w.group * H : 0), WT, s2, st, p, w, pl, ws)) != cudaSuccess ||
+          (e = launch_chained(qk, carries + w.nch * p.hq, WT, s3 > s2 ? s3 : s2, st, p, w, pl, ws)) != cudaSuccess)
+        return e;
+      if (many && (e = launch_chained(sk, dim3(w.pairs * 4, H), WT, s4, st, p, w, pl, ws)) != cudaSuccess) return e;
+      if ((e = launch_attend_tc(p, pl, st)) != cudaSuccess || (e = launch_rewrite_tc(p, pl, st)) != cudaSuccess ||
+          (e = launch_chained(merge_kernel<D>, dim3(w.nch * (C / gr), p.hq), GT, 0, st, p, w, pl, gr, ws)) != cudaSuccess)
+        return e;
+    }
   return cudaSuccess;
 }
 
 }  // namespace
 
-size_t paged_new_ws_bytes(const PagedArgs& p) { return new_ws(p).total; }
+size_t paged_new_ws_bytes(const PagedArgs& p) {
+  const NewWs w = new_ws(p);
+  return round_bytes(w.total, w.group < w.most);
+}
 cudaError_t launch_paged_new(const PagedArgs& p, char* ws, cudaStream_t st) {
   return p.c.head_dim == kHeadDim ? new_t<kHeadDim>(p, ws, st) : new_t<kHeadDimWide>(p, ws, st);
 }

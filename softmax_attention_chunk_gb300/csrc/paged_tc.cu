@@ -633,10 +633,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (seg > 0) ok = mbar_wait_lean(&s.m_empty, (seg - 1) & 1, err, 20);
       if (!ok) break;
       if (lane == 0) {
+        const int m = pl.mstart[g.b];
         mbar_arrive_expect_tx(&s.m_full, 2 * X * D * 128);
         for (int v = 0; v < 2; ++v)
           for (int x = 0; x < X; ++x)
-            tma_load_2d(s.m[v][x], &tm_m, 64 * x, ((v * p.c.slots + g.b) * p.c.heads + g.h) * D, &s.m_full);
+            tma_load_2d(s.m[v][x], &tm_m, 64 * x, ((v * pl.group + m) * p.c.heads + g.h) * D, &s.m_full);
       }
       for (int i = g.i0; i < g.i1; ++i, ++n) {
         const int j = live_tile(g.lt, i) * KT + lane * RB;
@@ -777,7 +778,7 @@ template <int D>
 cudaError_t rewrite_t(const PagedArgs& p, const TcPlan& pl, cudaStream_t st) {
   CUtensorMap mm, mk;
   const int P = p.c.page_size, RB = P < KT ? P : KT;
-  if (!make_map(&mm, pl.mm, D, (uint64_t)2 * p.c.slots * p.c.heads * D, D) ||
+  if (!make_map(&mm, pl.mm, D, (uint64_t)2 * pl.group * p.c.heads * D, D) ||
       !make_map(&mk, p.c.k_pool, D, (uint64_t)p.c.k_pages * p.c.heads * P, RB))
     return cudaErrorInvalidValue;
   auto kern = rewrite_tc_kernel<D>;

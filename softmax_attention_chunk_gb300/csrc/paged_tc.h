@@ -18,6 +18,8 @@ struct TcPlan {
   int pairs, blocks;        // query pairs of a head and blocks that the arrays hold
   int *cstart, *bstart;     // [slots + 1]: first chunk, first block of each slot
   int *pstart, *rstart;     // first query pair, first rewrite tile
+  int *mstart;              // slots of the round before this one: the number of its M
+  int group;                // slots that a round may have
   long long* vstart;        // first version row
   long long* ustart;        // first (head, pair, key tile) unit: a pair's cached tiles, then those of earlier blocks
   float *m, *l, *acc;       // parts [..][256](, [D]): thread block c's share of item i is part i + c; the items of
@@ -26,7 +28,7 @@ struct TcPlan {
   const void *z, *zs;       // queries at the start of the pass and of their block [rounded, rest][heads][pairs][256][D]; the
                             // rest at head dim 128 only of pairs with up to 128 rows
   const void* ver;          // version rows
-  const void* mm;           // M: [high, rest][slots][heads][D][D]
+  const void* mm;           // M: [high, rest][slots of the round][heads][D][D]
   long long ver_rows;
   int* err;                 // first wait that gave up
 };

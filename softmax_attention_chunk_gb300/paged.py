@@ -108,11 +108,12 @@ class PagedCache:
 
     # ---- attention ----
     def extend(self, q, k, v, w, beta, log_f=None, q_start=None, max_new=None, scale=1.0, window=0, sinks=0, ws=None,
-               out=None):
+               out=None, max_multi=0):
         """o [tokens, heads_q, head_dim] of the packed new tokens q [tokens, heads_q, head_dim], k, v, w [tokens,
         heads, head_dim], beta and log_f [tokens, heads] float32 (log_f exactly for a cache with fox).  q_start
         (int32 [slots + 1]): slot b's tokens are q_start[b] .. q_start[b + 1] - 1, at most max_new of them
-        (default: all); without it, token b is slot b's.  window > 0 hides all but the last `window` tokens and
+        (default: all); without it, token b is slot b's.  At most max_multi slots have several tokens (0: any number;
+        stated, a prompt among many single tokens needs the workspace of a prompt).  window > 0 hides all but the last `window` tokens and
         the first `sinks`.  The cache's keys are rewritten and the new rows appended; seq_len is not changed.  out
         must not overlap the other tensors."""
         if q.dim() != 3:
@@ -133,10 +134,10 @@ class PagedCache:
             raise ValueError(f"without q_start there is one token per slot: {N} tokens for {self.slots} slots")
         if max_new is None:
             max_new = 1 if q_start is None else N
-        key = (hq, N, max_new, scale, window, sinks)
+        key = (hq, N, max_new, scale, window, sinks, max_multi)
         plan = self._plans.get(key)
         if plan is None:  # descriptor and workspace size of calls of these sizes
-            desc = pa.path_paged_desc_t(hq, N, int(max_new), float(scale), int(window), int(sinks))
+            desc = pa.path_paged_desc_t(hq, N, int(max_new), float(scale), int(window), int(sinks), int(max_multi))
             n = pa.path_paged_workspace_size(self.c, desc)
             if n == 0:
                 raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens, window {window}, sinks {sinks}")

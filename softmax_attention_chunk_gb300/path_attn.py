@@ -47,7 +47,7 @@ class path_paged_cache_t(ctypes.Structure):
 
 class path_paged_desc_t(ctypes.Structure):
     _fields_ = [("heads_q", ctypes.c_int), ("total_tokens", ctypes.c_int), ("max_new", ctypes.c_int),
-                ("scale", ctypes.c_float), ("window", ctypes.c_int), ("sinks", ctypes.c_int)]
+                ("scale", ctypes.c_float), ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("max_multi", ctypes.c_int)]
 
 
 _vp, _sz, _i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
