@@ -154,6 +154,19 @@ __device__ __forceinline__ void store_sum(const path_paged_cache_t& c, long long
   if (c.a_rest) c.a_rest[at] = isfinite(hi) ? (float)(a - hi) : 0.f;
 }
 __device__ __forceinline__ float sum_rest(const path_paged_cache_t& c, long long at) { return c.a_rest ? c.a_rest[at] : 0.f; }
+// Numbers the slots with several new tokens in slot order, by a block of 32 warps, one slot per thread and step: this
+// slot's number; `numbered` (the same in all threads) counts on.  multi: 32 ints in shared memory, not written again before
+// the block's next barrier.
+__device__ __forceinline__ int number_multi(bool have, int* multi, int& numbered) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned some = __ballot_sync(0xffffffffu, have);
+  if (lane == 0) multi[warp] = __popc(some);
+  __syncthreads();
+  const int m = multi[lane];
+  const int number = numbered + (int)__reduce_add_sync(0xffffffffu, lane < warp ? m : 0) + __popc(some & ((1u << lane) - 1));
+  numbered += (int)__reduce_add_sync(0xffffffffu, m);
+  return number;
+}
 // What a call did with slot b, for path_paged_advance: its new tokens, or -1 where it was left out.
 __device__ __forceinline__ void note_extended(const path_paged_cache_t& c, int b, int n) {
   if (c.extended) c.extended[b] = n;

@@ -88,28 +88,31 @@ __device__ __forceinline__ void product(const float* A, int lda, const float* B,
 
 // Workspace (element offsets are computed on the host and the device from the same sizes).
 struct ChunkWs {
-  int nch;             // chunk slots: at least the chunks of any legal q_start
+  int most, group;     // slots with several new tokens: of any legal call, of a round
+  int nch;             // chunk slots: at least the chunks of any legal round
   int nsplit;          // key ranges of the cached attention (range 0 also carries the new tokens' state)
-  size_t plan;         // int: [slots + 1] first chunk of each slot, [slots + 1] first live cached tile
+  size_t plan;         // int [3][slots + 1]: first chunk of each slot, first live cached tile, slots of the round before it
   size_t kr, f;        // K-> [nch][H][B][D], F [nch][H][D][D]
   size_t fa, ft;       // forget gate: inclusive sums inside the chunk [nch][H][B], chunk totals [nch][H]
   size_t z, qb;        // Q<-, then z [nch][hq][B][D]; row biases sum of log f since t0 [nch][hq][B]
   size_t m, l, acc;    // softmax states [nsplit][nch][hq][B](, [D])
-  size_t mm;           // M [slots][H][D][D]
+  size_t mm;           // M [group][H][D][D]
   size_t total;
 };
-ChunkWs chunk_ws(const PagedArgs& p) {
+ChunkWs chunk_ws(const PagedArgs& p, int group) {  // for rounds of `group` slots
   ChunkWs w{};
+  w.group = group;
   const size_t D = p.c.head_dim, H = p.c.heads, hq = p.hq;
   // every slot may end in a partly filled chunk
-  const long long most = (p.total + (long long)(B - 1) * (p.c.slots < p.total ? p.c.slots : p.total)) / B;
+  const long long tokens = p.total < (long long)p.max_new * group ? p.total : (long long)p.max_new * group;
+  const long long most = (tokens + (long long)(B - 1) * group) / B;
   w.nch = (int)(most < 1 ? 1 : most);
   const long long ctas = (long long)w.nch * p.hq;
   w.nsplit = ctas >= 1216 ? 1 : (int)((1216 + ctas - 1) / ctas);
   if (w.nsplit > 64) w.nsplit = 64;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes, 256); return o; };
-  w.plan = take((size_t)2 * (p.c.slots + 1) * 4);
+  w.plan = take((size_t)3 * (p.c.slots + 1) * 4);
   w.kr = take((size_t)w.nch * H * B * D * 4);
   w.f = take((size_t)w.nch * H * D * D * 4);
   w.fa = take((size_t)w.nch * H * B * 4);
@@ -119,8 +122,14 @@ ChunkWs chunk_ws(const PagedArgs& p) {
   w.m = take((size_t)w.nsplit * w.nch * hq * B * 4);
   w.l = take((size_t)w.nsplit * w.nch * hq * B * 4);
   w.acc = take((size_t)w.nsplit * w.nch * hq * B * D * 4);
-  w.mm = take((size_t)p.c.slots * H * D * D * 4);
+  w.mm = take((size_t)group * H * D * D * 4);
   w.total = off;
+  return w;
+}
+ChunkWs chunk_ws(const PagedArgs& p) {
+  const int most = most_multi(p);
+  ChunkWs w = chunk_ws(p, round_slots(most, [&](int n) { return chunk_ws(p, n).total; }));
+  w.most = most;
   return w;
 }
 
@@ -130,17 +139,22 @@ __device__ __forceinline__ SlotSpan chunk_span(const PagedArgs& p, int b) {
   return s;
 }
 
-// First chunk and first live tile of every slot (exclusive prefix sums; entry `slots` holds the totals).
-__global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* plan) {
+// First chunk and first live tile of every slot, and the slots of the round before it (exclusive prefix sums; entry `slots`
+// holds the totals).  Slots with several new tokens are numbered in order: the round takes `group` of them from number
+// `first` on, and those from number `most` on are left out.
+__global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* plan, int first, int group, int most) {
   chain();
-  __shared__ int wsum[2][32];
+  __shared__ int wsum[2][32], multi[32];
   __shared__ int carry[2];
   __shared__ unsigned long long tokens;
+  const bool report = first == 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* cstart = plan;
   int* tstart = plan + p.c.slots + 1;
+  int* mstart = tstart + p.c.slots + 1;
   if (tid < 2) carry[tid] = 0;
   if (tid == 0) tokens = 0;
+  int numbered = 0;  // slots with several new tokens so far
   __syncthreads();
   for (int base = 0; base < p.c.slots; base += 1024) {
     const int b = base + tid;
@@ -148,16 +162,25 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* plan) {
     SlotSpan s{};
     if (b < p.c.slots) {
       s = chunk_span(p, b);
-      if (s.code) paged_error(p.c.status, s.code);
+      if (report && s.code) paged_error(p.c.status, s.code);
     }
     const int n = s.n;
-    leave_out_pageless(p.c, b, s.t0, n, s, true);
-    if (b < p.c.slots) {
-      if (n > 0) note_extended(p.c, b, s.n > 0 ? n : -1);
-      nc = (s.n + B - 1) / B;
-      if (s.n) atomicAdd(&tokens, (unsigned long long)s.n);
-      nt = s.n ? live_tiles(s.t0, p.window, p.sinks, KT).count : 0;
+    leave_out_pageless(p.c, b, s.t0, n, s, report);
+    const int number = number_multi(s.n > 0, multi, numbered);
+    if (s.n > 0) {
+      atomicAdd(&tokens, (unsigned long long)s.n);
+      if (number >= most) {
+        s.n = 0;
+        if (report) paged_error(p.c.status, PATH_PAGED_BAD_START);
+      }
     }
+    if (report && n > 0) note_extended(p.c, b, s.n > 0 ? n : -1);
+    const int before = number - first;
+    if (s.n > 0 && before >= 0 && before < group) {
+      nc = (s.n + B - 1) / B;
+      nt = live_tiles(s.t0, p.window, p.sinks, KT).count;
+    }
+    if (b < p.c.slots) mstart[b] = before < 0 ? 0 : before < group ? before : group;
     int ic = nc, it = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -173,14 +196,19 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, int* plan) {
     if (tid == 1023) { carry[0] = oc + ic; carry[1] = ot + it; }
     __syncthreads();
   }
-  if (tid == 0) { cstart[p.c.slots] = carry[0]; tstart[p.c.slots] = carry[1]; }
+  if (tid == 0) {
+    cstart[p.c.slots] = carry[0];
+    tstart[p.c.slots] = carry[1];
+    const int left = min(numbered, most) - first;
+    mstart[p.c.slots] = left < 0 ? 0 : left < group ? left : group;
+  }
   // rows of q_start that overlap: more tokens than the workspace is for
   if (tokens > (unsigned long long)p.total) {
     if (tid == 0) paged_error(p.c.status, PATH_PAGED_BAD_START);
     __syncthreads();
     for (int b = tid; b <= p.c.slots; b += 1024) {
-      if (b < p.c.slots && chunk_span(p, b).n > 0) note_extended(p.c, b, -1);
-      cstart[b] = tstart[b] = 0;
+      if (report && b < p.c.slots && chunk_span(p, b).n > 0) note_extended(p.c, b, -1);
+      cstart[b] = tstart[b] = mstart[b] = 0;
     }
   }
 }
@@ -444,16 +472,18 @@ __device__ void scan_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
   }
 }
 
-// Key walk of one (slot, key head): the new rows to the end of the call and into the pages, M.
+// Key walk of one (slot m of the round, key head): the new rows to the end of the call and into the pages, M.
 template <int D>
-__device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float* sm, int b, int h) {
+__device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float* sm, int m, int h) {
   constexpr int DS = D + 4;
   float *sR = sm, *sF = sR + D * DS, *sK = sF + D * DS;
   const int* cstart = (const int*)(ws + w.plan);
+  const int* mstart = cstart + 2 * (p.c.slots + 1);
   const int tid = threadIdx.x, H = p.c.heads;
+  if (m >= mstart[p.c.slots]) return;
+  const int b = owner(mstart, p.c.slots, m);
   const SlotSpan sp = chunk_span(p, b);
   const int nc = cstart[b + 1] - cstart[b];
-  if (nc == 0) return;  // no new tokens, or left out
   float* kp = (float*)p.c.k_pool;
   float* vp = (float*)p.c.v_pool;
   const float* v = (const float*)p.v;
@@ -493,7 +523,7 @@ __device__ void walk_block(const PagedArgs& p, const ChunkWs& w, char* ws, float
     }
   }
   for (int e = tid; e < D * D; e += NT) sR[(e / D) * DS + e % D] = (e / D == e % D) ? 1.f : 0.f;
-  float* mm = (float*)(ws + w.mm) + ((size_t)b * H + h) * D * D;
+  float* mm = (float*)(ws + w.mm) + ((size_t)m * H + h) * D * D;
   for (int lc = nc - 1; lc >= 0; --lc) {
     const size_t cc = (size_t)(cstart[b] + lc) * H + h;
     const float* kr = (const float*)(ws + w.kr) + cc * B * D;
@@ -524,12 +554,12 @@ constexpr size_t scan_walk_smem() {
   return scan > walk ? scan : walk;
 }
 
-// Blocks [0, slots * H) walk keys, the others scan queries.
+// Blocks [0, group * H) walk keys, the others scan queries.
 template <int D>
 __global__ void __launch_bounds__(NT) scan_walk_kernel(PagedArgs p, ChunkWs w, char* ws) {
   chain();
   extern __shared__ float sm[];
-  const int nw = p.c.slots * p.c.heads;
+  const int nw = w.group * p.c.heads;
   if ((int)blockIdx.x < nw) {
     walk_block<D>(p, w, ws, sm, blockIdx.x / p.c.heads, blockIdx.x % p.c.heads);
     return;
@@ -735,7 +765,8 @@ __global__ void __launch_bounds__(NT) rewrite_kernel(PagedArgs p, ChunkWs w, con
     const int j0 = live_tile(lt, i) * KT;
     __syncthreads();
     if (have != b * H + h) {
-      const float* mm = (const float*)(ws + w.mm) + ((size_t)b * H + h) * D * D;
+      const int m = tstart[p.c.slots + 1 + b];  // (mstart)
+      const float* mm = (const float*)(ws + w.mm) + ((size_t)m * H + h) * D * D;
       tile_in<D, D>(sMm, DS, mm, D);
       have = b * H + h;
     }
@@ -814,18 +845,23 @@ cudaError_t chunk_t(const PagedArgs& p, char* ws, cudaStream_t st) {
   if ((e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s2)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(att, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s3)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(rew, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s4)) != cudaSuccess) return e;
-  if ((e = launch_chained(plan_kernel, 1, 1024, 0, st, p, (int*)(ws + w.plan))) != cudaSuccess ||
-      (e = launch_chained(prep, dim3(w.nch, p.c.heads), NT, s1, st, p, w, ws)) != cudaSuccess ||
-      (e = launch_chained(scan, p.c.slots * p.c.heads + w.nch * p.hq, NT, s2, st, p, w, ws)) != cudaSuccess ||
-      (e = launch_chained(att, dim3(w.nch, p.hq, w.nsplit), AT, s3, st, p, w, ws)) != cudaSuccess ||
-      (e = launch_chained(rew, 608, NT, s4, st, p, w, ws)) != cudaSuccess)
-    return e;
-  return launch_chained(merge_kernel<D>, dim3(w.nch * (B / (NT / 32)), p.hq), NT, 0, st, p, w, ws);
+  for (int first = 0; first < w.most; first += w.group)
+    if ((e = launch_chained(plan_kernel, 1, 1024, 0, st, p, (int*)(ws + w.plan), first, w.group, w.most)) != cudaSuccess ||
+        (e = launch_chained(prep, dim3(w.nch, p.c.heads), NT, s1, st, p, w, ws)) != cudaSuccess ||
+        (e = launch_chained(scan, w.group * p.c.heads + w.nch * p.hq, NT, s2, st, p, w, ws)) != cudaSuccess ||
+        (e = launch_chained(att, dim3(w.nch, p.hq, w.nsplit), AT, s3, st, p, w, ws)) != cudaSuccess ||
+        (e = launch_chained(rew, 608, NT, s4, st, p, w, ws)) != cudaSuccess ||
+        (e = launch_chained(merge_kernel<D>, dim3(w.nch * (B / (NT / 32)), p.hq), NT, 0, st, p, w, ws)) != cudaSuccess)
+      return e;
+  return cudaSuccess;
 }
 
 }  // namespace
 
-size_t paged_chunk_ws_bytes(const PagedArgs& p) { return chunk_ws(p).total; }
+size_t paged_chunk_ws_bytes(const PagedArgs& p) {
+  const ChunkWs w = chunk_ws(p);
+  return round_bytes(w.total, w.group < w.most);
+}
 
 cudaError_t launch_paged_chunk(const PagedArgs& p, char* ws, cudaStream_t st) {
   return p.c.head_dim == kHeadDim ? chunk_t<kHeadDim>(p, ws, st) : chunk_t<kHeadDimWide>(p, ws, st);

@@ -215,14 +215,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedArgs p, TcPlan pl, int 
       n = all.n;
     }
     leave_out_pageless(p.c, b, all.t0, n, all, report);
-    const unsigned have = __ballot_sync(0xffffffffu, all.n > 0);
-    if (lane == 0) multi[warp] = __popc(have);
-    __syncthreads();
-    int number = numbered + __popc(have & ((1u << lane) - 1));
-    for (int i = 0; i < 32; ++i) {
-      if (i < warp) number += multi[i];
-      numbered += multi[i];
-    }
+    const int number = number_multi(all.n > 0, multi, numbered);
     if (all.n > 0) {
       atomicAdd(&tokens, (unsigned long long)all.n);
       if (number >= most) {

@@ -49,3 +49,27 @@ def test_stated_number_of_prompts(cuda_lib):
     R.check_extend(few, got, R.extend_ref(few, 0.125), 0.125, tokens=kept)
     assert (got["o"][[i for i in range(sum(n)) if i not in kept]] == 3).all()
     assert cache.seq_len.tolist() == [70, 6, 120, 0, 65, 33]
+
+
+def test_many_short_fp32_prompts(cuda_lib):
+    """1300 slots of up to 3 new tokens and 128 heads: several rounds of the fp32 kernels."""
+    t = [(7 * b) % 37 if b % 29 else -1 for b in range(1300)]
+    n = [0 if x < 0 else b % 4 for b, x in enumerate(t)]
+    c = R.make_case("fp32", 128, 128, 8, 16, t, n, seed=13)
+    got, cache = run(c, 0.1)
+    R.check_extend(c, got, R.extend_ref(c, 0.1), 0.1)
+    cache.check()
+
+
+def test_stated_number_of_fp32_prompts(cuda_lib):
+    t, n = [40, 5, 100, 0, 64], [30, 1, 20, 17, 1]
+    c = R.make_case("fp32", 64, 4, 2, 16, t, n, seed=14)
+    out = torch.full_like(c["q"], 3.0).to(DEV)
+    got, cache = run(c, 0.125, max_multi=2, out=out)
+    cache.advance(c["q_start"].to(DEV))
+    with pytest.raises(RuntimeError, match="q_start"):
+        cache.check()
+    few = dict(c, n=[30, 1, 20, 0, 1])
+    kept = [i for b in (0, 1, 2, 4) for i in range(int(c["q_start"][b]), int(c["q_start"][b + 1]))]
+    R.check_extend(few, got, R.extend_ref(few, 0.125), 0.125, tokens=kept)
+    assert cache.seq_len.tolist() == [70, 6, 120, 0, 65]

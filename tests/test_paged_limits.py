@@ -64,3 +64,12 @@ def test_workspace_grows_with_the_call(pa):
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
     sizes = [size(40000, most) for most in range(20, 20000, 517)]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("slots,total,max_new,heads_q", [(4096, 512 + 4095, 512, 32), (16384, 512 + 16383, 512, 32), (1024, 64 * 4096, 4096, 32)])
+def test_workspace_of_fp32_calls(pa, slots, total, max_new, heads_q):
+    c = big(pa, pa.PATH_FP32, slots=slots)
+    size = lambda **kw: pa.path_paged_workspace_size(c, desc(pa, heads_q=heads_q, **kw))  # noqa: E731
+    one, singles = size(total_tokens=max_new, max_new=max_new, max_multi=1), size(total_tokens=slots, max_new=1)
+    assert 0 < size(total_tokens=total, max_new=max_new) <= max(one, 4 * GB) + singles
+    assert size(total_tokens=total, max_new=max_new, max_multi=1) < 0.3 * GB
