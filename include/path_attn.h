@@ -415,7 +415,8 @@ typedef struct {
   int heads_q;       /* query heads, a multiple of cache.heads (at most 16 times): head hq reads key head
                         hq / (heads_q / heads) */
   int total_tokens;  /* new tokens of the call */
-  int max_new;       /* at least the most new tokens of one slot */
+  int max_new;       /* at least the most new tokens of one slot.  0 says that there are none: nothing is
+                        launched and q_start is not looked at */
   float scale;       /* multiplies the logit; the forget bias is added unscaled */
   int window;        /* 0: every earlier token is seen; W > 0: the token at position p sees j > p - W ... */
   int sinks;         /* ... and the first `sinks` tokens of its sequence */

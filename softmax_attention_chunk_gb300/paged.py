@@ -134,6 +134,8 @@ class PagedCache:
             raise ValueError(f"without q_start there is one token per slot: {N} tokens for {self.slots} slots")
         if max_new is None:
             max_new = 1 if q_start is None else N
+        if N > 0 and max_new < 1:
+            raise ValueError(f"max_new must be at least 1 for {N} tokens, got {max_new}")
         key = (hq, N, max_new, scale, window, sinks, max_multi)
         plan = self._plans.get(key)
         if plan is None:  # descriptor and workspace size of calls of these sizes
