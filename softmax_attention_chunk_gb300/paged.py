@@ -115,7 +115,8 @@ class PagedCache:
         (default: all); without it, token b is slot b's.  At most max_multi slots have several tokens (0: any number;
         stated, a prompt among many single tokens needs the workspace of a prompt).  window > 0 hides all but the last `window` tokens and
         the first `sinks`.  The cache's keys are rewritten and the new rows appended; seq_len is not changed.  out
-        must not overlap the other tensors."""
+        must not overlap the other tensors.  ws: uint8, at least path_paged_workspace_size bytes, for one call at a
+        time (default: a new one)."""
         if q.dim() != 3:
             raise ValueError(f"q: expected [tokens, heads_q, head_dim], got {tuple(q.shape)}")
         N, hq, d = q.shape
@@ -155,6 +156,9 @@ class PagedCache:
             return out
         if ws is None:
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        elif ws.dtype != torch.uint8 or ws.device != self.device or not ws.is_contiguous() or ws.numel() < n:
+            raise ValueError(f"ws: expected at least {n} contiguous uint8 on {self.device}, got {ws.numel()} {ws.dtype} on "
+                             f"{ws.device} contiguous={ws.is_contiguous()}")
         p = pa._p
         self._call(pa.path_paged_extend, desc, p(q_start), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
                    beta.data_ptr(), p(log_f), out.data_ptr(), ws.data_ptr(), ws.numel())

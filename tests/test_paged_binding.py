@@ -41,3 +41,18 @@ def test_max_new_below_one_is_refused(cache):
     assert cache.calls == []
     cache.extend(*tokens(0), q_start=torch.zeros(4, dtype=torch.int32))  # no tokens: nothing to do
     assert cache.calls == []
+
+
+@pytest.mark.parametrize("ws", [lambda n: torch.empty(n, dtype=torch.uint8, device="meta"), lambda n: torch.empty(2 * n, dtype=torch.uint8)[::2],
+                                lambda n: torch.empty(n, dtype=torch.float32), lambda n: torch.empty(n - 1, dtype=torch.uint8)])
+def test_workspaces_that_are_none(cache, ws):
+    """Another device, gaps, another type (whose elements are not bytes), too few bytes."""
+    start = torch.tensor([0, 4, 8, 9], dtype=torch.int32)
+    t = tokens(9)
+    cache.extend(*t, q_start=start)
+    n = cache.calls.pop()[1][-1]
+    with pytest.raises(ValueError, match="ws"):
+        cache.extend(*t, q_start=start, ws=ws(n))
+    assert cache.calls == []
+    cache.extend(*t, q_start=start, ws=torch.empty(n + 5, dtype=torch.uint8))
+    assert cache.calls.pop()[1][-1] == n + 5
