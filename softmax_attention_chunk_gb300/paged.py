@@ -159,6 +159,10 @@ class PagedCache:
         elif ws.dtype != torch.uint8 or ws.device != self.device or not ws.is_contiguous() or ws.numel() < n:
             raise ValueError(f"ws: expected at least {n} contiguous uint8 on {self.device}, got {ws.numel()} {ws.dtype} on "
                              f"{ws.device} contiguous={ws.is_contiguous()}")
+        if beta.data_ptr() % 16:  # (of a part of a packed batch; the library wants 16-byte boundaries)
+            beta = beta.clone()
+        if log_f is not None and log_f.data_ptr() % 16:
+            log_f = log_f.clone()
         p = pa._p
         self._call(pa.path_paged_extend, desc, p(q_start), q.data_ptr(), k.data_ptr(), v.data_ptr(), w.data_ptr(),
                    beta.data_ptr(), p(log_f), out.data_ptr(), ws.data_ptr(), ws.numel())

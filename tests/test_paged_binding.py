@@ -56,3 +56,20 @@ def test_workspaces_that_are_none(cache, ws):
     assert cache.calls == []
     cache.extend(*t, q_start=start, ws=torch.empty(n + 5, dtype=torch.uint8))
     assert cache.calls.pop()[1][-1] == n + 5
+
+
+def test_tensors_off_a_16_byte_boundary(cache):
+    """beta and log_f of a part of a packed batch may begin anywhere: the library gets aligned copies."""
+    import ctypes
+
+    cache.a_pool = torch.zeros(1)  # with a gate
+    q, k, v, w, _ = tokens(9)
+    start = torch.tensor([0, 4, 8, 9], dtype=torch.int32)
+    beta, log_f = torch.rand(20, 2), -torch.rand(20, 2)
+    kept = []
+    cache._call = lambda fn, *a: (kept.append([ctypes.string_at(x, 72) for x in a[6:8]]), cache.calls.append((fn.__name__, a)))
+    for s in (0, 1, 3, 11):
+        cache.extend(q, k, v, w, beta[s : s + 9], log_f=log_f[s : s + 9], q_start=start)
+        a = cache.calls.pop()[1]
+        assert a[6] % 16 == 0 and a[7] % 16 == 0
+        assert kept.pop() == [x[s : s + 9].contiguous().numpy().tobytes() for x in (beta, log_f)]
