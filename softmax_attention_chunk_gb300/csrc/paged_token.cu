@@ -90,7 +90,11 @@ TokenWs token_ws(const PagedArgs& p, int n) {
 // kSetup that stand for the time a warp needs to begin it (no work, so that runs over many
 // short sequences are not longer than others), then its live tiles, at least one (the new tokens themselves).
 constexpr int kSetup = 2;
-__device__ __forceinline__ int slot_units(const PagedArgs& p, int b, int mode, bool report) {
+// Units are numbered with 32 bits.  Slots whose visible rows all lie in key pages of their own have at most 2^31 / 16 (the rows
+// of a pool) and 3 * 2^26 for beginnings and new tokens; more than this means that lengths name rows without pages, and the
+// call leaves all its slots out.
+constexpr long long kMaxUnits = 1 << 30;
+__device__ __forceinline__ long long slot_units(const PagedArgs& p, int b, int mode, bool report) {
   const SlotSpan s = slot_span(p, b);
   const bool mine = s.n > 0 && (mode != kOnlyOne || s.n == 1);
   const bool there = !mine || rows_there(p.c, b, s.t0, s.n);
@@ -100,34 +104,43 @@ __device__ __forceinline__ int slot_units(const PagedArgs& p, int b, int mode, b
   }
   if (!mine || !there) return 0;
   const int nt = live_tiles(s.t0, p.window, p.sinks, RT).count;
-  return (kSetup + (nt > 0 ? nt : 1)) * p.c.heads;
+  return (long long)(kSetup + (nt > 0 ? nt : 1)) * p.c.heads;
 }
 // First unit of each slot, by the whole block; out may be shared memory.
 template <int THREADS>
 __device__ void unit_starts(const PagedArgs& p, int mode, bool report, int* out) {
-  __shared__ int wsum[THREADS / 32], carry;
+  __shared__ long long wsum[THREADS / 32], carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) carry = 0;
   __syncthreads();
   for (int base = 0; base < p.c.slots; base += THREADS) {
     const int b = base + tid;
-    const int n = b < p.c.slots ? slot_units(p, b, mode, report) : 0;
-    int x = n;
+    const long long n = b < p.c.slots ? slot_units(p, b, mode, report) : 0;
+    long long x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, x, o);
+      const long long a = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += a;
     }
     if (lane == 31) wsum[warp] = x;
     __syncthreads();
-    int before = carry;
+    long long before = carry;
     for (int w = 0; w < warp; ++w) before += wsum[w];
-    if (b < p.c.slots) out[b] = before + x - n;
+    if (b < p.c.slots) out[b] = (int)(before + x - n);
     __syncthreads();
     if (tid == THREADS - 1) carry = before + x;
     __syncthreads();
   }
-  if (tid == 0) out[p.c.slots] = carry;
+  if (carry > kMaxUnits) {
+    for (int b = tid; b < p.c.slots; b += THREADS) {
+      if (report && slot_units(p, b, mode, false) > 0) {
+        paged_error(p.c.status, PATH_PAGED_BAD_PAGE);
+        note_extended(p.c, b, -1);
+      }
+      out[b] = 0;
+    }
+  }
+  if (tid == 0) out[p.c.slots] = carry > kMaxUnits ? 0 : (int)carry;
   __syncthreads();
 }
 __global__ void __launch_bounds__(1024) unit_starts_kernel(PagedArgs p, int mode, int* out) {
