@@ -18,11 +18,12 @@
 //  * z, P and c are held as bf16 pairs (high + rest, about 16 bits), so that the only rounding to 8 bits is the
 //    one that the cache and the output need: the extra MMAs are free under the memory bound.
 // Measured: 4 x 32 heads x 32000 rows, head dim 64, 252 us (6.2 TB/s, 93 % of a copy's rate); 48 ragged sequences up
-// to 4096 x 8 key heads, head dim 128, 4 heads per key head, 111 us (5.5 TB/s, 82 %: 250 registers leave 8 warps
+// to 4096 x 8 key heads, head dim 128, 4 heads per key head, 112 us (5.4 TB/s, 80 %: 250 registers leave 8 warps
 // per SM, and a warp's loads wait on one another's tiles).  Value and key pieces through a ring in shared memory
-// (cp.async, 2 to 4 tiles ahead): 278 us in place of 244 for the former's kernel.  16 x 8 heads x 5000 rows, 8 draft
-// tokens of 2 heads, head dim 64: 90 us (floor 38: the two preparing and merging launches, and 12 warps per SM beside
-// 168 registers of operands and accumulators; DRAM 43 %).
+// (cp.async, 2 to 4 tiles ahead): 278 us in place of 244 for the former's kernel; not tried at head dim 128, where registers
+// are what is short.  16 x 8 heads x 5000 rows, 8 draft tokens of 2 heads, head dim 64: 90 us (floor 37: the preparing and
+// merging launches, 12 warps per SM beside 168 registers of operands and accumulators, and the fragments of z, W and Y, read
+// again for every tile: 9 KB beside 4 KB of keys and values; DRAM 42 %).
 #include "paged.h"
 #include "dev_common.cuh"
 #include "mma_common.cuh"
@@ -38,7 +39,7 @@ constexpr float kTau = 8.f;        // lazy rescale: the reference moves when a s
 struct TokenWs {
   int blocks;              // of the streaming kernel
   int nq;                  // query columns of a (slot, head): 8 NQ8
-  size_t ustart;           // int [slots + 1]: first unit of each slot (more than kSmemSlots slots)
+  size_t ustart;           // int [slots + 1]: first unit of each slot
   size_t m, l, acc;        // partial states [2 * warps][nq](, [D])
   size_t frag;             // draft tokens: per (slot, head) z and W, Y fragments
   size_t sm, sl, sacc;     // draft tokens: the new tokens' own state [slots][H][nq](, [D])
@@ -147,6 +148,11 @@ __global__ void __launch_bounds__(1024) unit_starts_kernel(PagedArgs p, int mode
   chain();
   unit_starts<1024>(p, mode, true, out);
 }
+// The first block's list for the merge.
+__device__ __forceinline__ void keep_starts(const int* start, int slots, int* out) {
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= slots; b += NT) out[b] = start[b];
+}
 __device__ __forceinline__ int find_slot(const int* start, int slots, int u) {
   int lo = 0, hi = slots;
   while (hi - lo > 1) {
@@ -192,11 +198,16 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
   const int units = start[p.c.slots];
   const int run = run_length(units, warps);
   const int u0 = warp * run, u1 = min(u0 + run, units);
-  if (u0 >= u1) return;
+  // the list for the merge: with drafts here, with one token at the end (each where the registers of the loop do not suffer:
+  // 4 x 32000 rows of 32 heads 253 us, with this here 270)
+  if (!ONE) {
+    if (p.c.slots <= kSmemSlots) keep_starts(start, p.c.slots, (int*)(ws + w.ustart));
+    if (u0 >= u1) return;
+  }
 
   const __nv_bfloat16* kpool = (const __nv_bfloat16*)p.c.k_pool;
   const __nv_bfloat16* vpool = (const __nv_bfloat16*)p.c.v_pool;
-  int b = find_slot(start, p.c.slots, u0);
+  int b = u0 < u1 ? find_slot(start, p.c.slots, u0) : 0;
   int u = u0;
   while (u < u1) {
     while (start[b + 1] <= u) ++b;  // slots without units are passed over
@@ -643,6 +654,7 @@ __global__ void __launch_bounds__(NT, blocks_per_sm(D, NQ8)) token_kernel(PagedA
       }
     u = ue;
   }
+  if (ONE && p.c.slots <= kSmemSlots) keep_starts(start, p.c.slots, (int*)(ws + w.ustart));
 }
 
 // ---- draft tokens: the n <= 16 new tokens of a (slot, head) among themselves ----
@@ -877,20 +889,13 @@ __global__ void __launch_bounds__(MT) token_merge_kernel(PagedArgs p, TokenWs w,
                                                          int cs) {
   chain();
   constexpr int L = D / 4, GR = MT / L;
-  __shared__ int s_start[kSmemSlots + 1];
   __shared__ float4 s_acc[GR][L];
   __shared__ float s_l[GR];
   const int b = blockIdx.x, h = blockIdx.y, gr = threadIdx.x / L, x = threadIdx.x % L;
   const SlotSpan sp = slot_span(p, b);
   const int cols = sp.n * p.G, c0 = blockIdx.z * cs;
   if (sp.n == 0 || (mode == kOnlyOne && sp.n != 1) || c0 >= cols) return;
-  const int* start;
-  if (p.c.slots <= kSmemSlots) {
-    unit_starts<MT>(p, mode, false, s_start);
-    start = s_start;
-  } else {
-    start = (const int*)(ws + w.ustart);
-  }
+  const int* start = (const int*)(ws + w.ustart);
   if (start[b + 1] == start[b]) return;  // left out
   const int run = run_length(start[p.c.slots], warps);
   const int kt = live_tiles(sp.t0, p.window, p.sinks, RT).count;
@@ -961,11 +966,10 @@ __global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs 
   }
   const int units = start[p.c.slots], run = run_length(units, warps);
   const int u0 = warp * run, u1 = min(u0 + run, units);
-  if (u0 >= u1) return;
   auto ld4 = [](const float* q) { return *reinterpret_cast<const float4*>(q); };
   auto dot4 = [](const float4& a, const float4& c) { return a.x * c.x + a.y * c.y + a.z * c.z + a.w * c.w; };
   float *kpool = (float*)p.c.k_pool, *vpool = (float*)p.c.v_pool;
-  int b = find_slot(start, p.c.slots, u0);
+  int b = u0 < u1 ? find_slot(start, p.c.slots, u0) : 0;
   int u = u0;
   while (u < u1) {
     while (start[b + 1] <= u) ++b;
@@ -1090,6 +1094,7 @@ __global__ void __launch_bounds__(NT, blocks32(D, GP)) token32_kernel(PagedArgs 
     }
     u = ue;
   }
+  if (p.c.slots <= kSmemSlots) keep_starts(start, p.c.slots, (int*)(ws + w.ustart));
 }
 template <int D, int GP, bool FOX>
 cudaError_t token32_t(const PagedArgs& p, const TokenWs& w, char* ws, cudaStream_t st) {
@@ -1147,7 +1152,8 @@ cudaError_t token_d(const PagedArgs& p, const TokenWs& w, bool drafts, char* ws,
 // Drafts go through the streaming pass while their columns' accumulators and fragments leave it fast enough: 16
 // columns (8 heads x 16 x 2000..8192 rows, 8 tokens, G = 2: head dim 64 102 us against 137 for the prompt chunk path, 128
 // 182 against 216), at head dim 64 up to 8 tokens also 32 (135 against 142).  Beyond that the chunk path's second
-// pass over the keys costs less (32 columns, head dim 128: 337 against 227; 16 tokens, head dim 64: 153 against 138).
+// pass over the keys costs less (32 columns, head dim 128: 337 against 227; 16 tokens, head dim 64: 153 against 138).  All of
+// these figures are of that one batch; where the two paths meet at other lengths was not measured.
 bool paged_drafts(const PagedArgs& p) {
   if (p.c.cache_dtype != PATH_BF16 || p.max_new <= 1 || p.max_new > DN) return false;
   const int cols = p.max_new * p.G;
