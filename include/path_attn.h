@@ -392,8 +392,9 @@ typedef struct {
   int* v_ref;       /* [v_pages]: sequences that hold the page, 0 free */
   int* status;      /* one int: the first PATH_PAGED_* code since it was last cleared (start it at 0) */
   int* extended;    /* [slots] or NULL: tokens that the last path_paged_extend of a slot gave it and no
-                       path_paged_advance has counted yet; -1: it left the slot out (start it at 0).
-                       NULL: advance cannot tell and counts what its q_start says */
+                       path_paged_advance has counted yet; -1: it left the slot out (start it at 0, and set
+                       it to 0 with a seq_len of your own).  NULL: advance cannot tell and counts what its
+                       q_start says, as far as there are pages */
   float* a_rest;    /* as a_pool, or NULL: what rounding the running sums to fp32 left of them (0 where the
                        caller fills a_pool itself).  NULL: every call rounds the sums it appends by up to
                        2^-24 of their size, which far into a sequence is more than a token adds */
@@ -495,7 +496,8 @@ size_t path_pages_workspace_size(const path_paged_cache_t* cache);
  * free: the slots become empty and their pages return (a shared value page with its last holder).
  * trim: returns the pages of every slot in use that hold only rows which a window of `window` tokens
  *   and `sinks` first tokens hides from every later token; their table entries become -1.  The page
- *   of the last row stays.
+ *   of the last row stays.  Positions go on: the columns are not given back, and a slot ends at table_width
+ *   * page_size tokens whatever the window.
  * compact: moves the pages in use to the front of each pool: with n pages in use, those numbered n and
  *   above go, in rising order, to the free numbers below n.  Tables and counts follow.
  */

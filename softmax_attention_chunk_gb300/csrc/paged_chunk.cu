@@ -13,9 +13,10 @@
 // Six launches: plan (lengths, chunk list), chunk preparation, then one of {query scan, key walk} per
 // block, cached attention split over key ranges, cached rewrite, and the merge of the splits.
 //
-// Bound: fp32 multiply-adds and shared-memory reads of the products (no fp32 tensor path keeps 24 bits); products keep
+// Bound: fp32 multiply-adds and shared-memory reads of the products on the CUDA cores (operands as three bf16 parts each
+// would keep 24 bits on the tensor cores too; not built); products keep
 // 2 x 4 results per thread, tiles move 16 bytes at a time, the merge takes a row's ranges side by side (262 -> 184 -> 140 ->
-// 116 -> 105 us for 3 slots of 5 to 97 tokens over up to 1500 rows x 8 heads, head dim 64: what is left is a chain of six
+// 116 -> 109 us for 3 slots of 5 to 97 tokens over up to 1500 rows x 8 heads, head dim 64: what is left is a chain of six
 // launches with few blocks each, every one a chain of products; attention 25, scan and walk 33, rewrite 17).
 #include "paged.h"
 #include "dev_common.cuh"

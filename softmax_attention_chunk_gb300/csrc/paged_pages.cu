@@ -5,7 +5,7 @@
 // goes into the workspace as a list of (source, destination) pages, which a second kernel copies with
 // the whole GPU.  A call first counts what it needs and looks at every entry of its lists, and only then
 // writes; a code in the status word means that nothing was written.
-// Bound: the copies (each byte read and written once): compaction that moves 423 MB 145 us, of which the copy 126 (6.7
+// Bound: the copies (each byte read and written once): compaction that moves 426 MB 148 us, of which the copy 127 (6.7
 // TB/s, a plain copy's rate) and the bookkeeping by one block the rest (pieces of 16 KB in place of 8: 147); a fork of
 // one short sequence is the latency of its launches.
 #include "paged.h"
