@@ -165,3 +165,86 @@ def test_drafts_are_checked_on_a_fork(cuda_lib, dtype, d):
     cache.check()
     R.check_extend(part, got, R.extend_ref(part, 0.125), 0.125)
     assert cache.seq_len.tolist() == [48, -1]
+
+
+def test_captured_steps_run_on_past_a_full_pool(cuda_lib):
+    """reserve, extend and advance as one captured step, replayed without a look at the status while the pool runs full:
+    sequences stand still at a page that is not there and go on when one is freed, with every counted token in place."""
+    from softmax_attention_chunk_gb300.paged import PagedCache
+
+    P, pages = 16, 7
+    cache = PagedCache(3, 2, 64, P, pages, table_width=12)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    bf = lambda *s: torch.randn(*s, device=DEV, generator=g).to(torch.bfloat16)  # noqa: E731
+    q, k, v, w, beta = bf(3, 4, 64), bf(3, 2, 64), bf(3, 2, 64), bf(3, 2, 64), torch.zeros(3, 2, device=DEV)
+    lens, own, free = [20, 28, 5], [2, 2, 1], pages - 5
+    cache.reserve(i32(lens))
+    cache.k_pool.copy_(bf(*cache.k_pool.shape))
+    cache.v_pool.copy_(bf(*cache.v_pool.shape))
+    cache.advance(i32([0, 20, 48, 53]))
+    cache.check()
+    first = [(cache.k_table[b].clone(), cache.v_table[b].clone()) for b in range(3)]
+    k0, v0 = cache.k_pool.clone(), cache.v_pool.clone()
+    out = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device=DEV)
+
+    def step():
+        cache.reserve()
+        cache.extend(q, k, v, w, beta, scale=0.125, out=out)
+        cache.advance()
+
+    step_graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(step_graph):
+        step()
+    live = [True] * 3
+    start = list(lens)
+    for i in range(60):
+        if i == 40:  # one sequence ends
+            cache.free(i32([2]))
+            free += own[2]
+            live[2] = False
+        step_graph.replay()
+        need = [b for b in range(3) if live[b] and lens[b] % P == 0 and own[b] * P == lens[b]]
+        if len(need) <= free:
+            free -= len(need)
+            for b in need:
+                own[b] += 1
+        for b in range(3):
+            if live[b] and lens[b] < own[b] * P:
+                lens[b] += 1
+    torch.cuda.synchronize()
+    assert cache.seq_len.tolist() == [lens[0], lens[1], -1]
+    assert any(x < s + 60 for x, s in zip(lens[:2], start))  # (some stood still)
+    with pytest.raises(RuntimeError, match="not enough free pages"):
+        cache.check()
+    for b in range(2):
+        pos = torch.arange(start[b], device=DEV)
+        table = [x[b].cpu().long() for x in (cache.k_table, cache.v_table)]
+        made = torch.arange(start[b], lens[b])
+        for pool, new, t, (old, was) in ((cache.k_pool, k, table[0], (k0, first[b][0])), (cache.v_pool, v, table[1], (v0, first[b][1]))):
+            x = pool.cpu()
+            assert torch.equal(x[t[made // P], :, made % P], new[b].cpu().expand(len(made), 2, 64))
+            assert torch.equal(x[t[pos.cpu() // P], :, pos.cpu() % P], old.cpu()[was.cpu().long()[pos.cpu() // P], :, pos.cpu() % P])
+
+
+@pytest.mark.parametrize("n", [[1, 1, 1, 1], [6, 3, 2, 8], [90, 40, 200, 1]])
+def test_two_calls_at_once_on_one_cache(cuda_lib, n):
+    """Calls on different slots of a cache, on two streams and with a workspace each."""
+    c = R.make_case("bf16", 64, 4, 2, 16, [3000, 64, 2000, 500], n, seed=sum(n))
+    cache = to_cache(c)
+    cut = int(c["q_start"][2])
+    parts = []
+    for sl, start in ((slice(0, cut), [0, n[0], cut, cut, cut]), (slice(cut, None), [0, 0, 0, n[2], n[2] + n[3]])):
+        parts.append(([c[x][sl].clone().to(DEV) for x in ("q", "k", "v", "w", "beta")], i32(start)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for s, (x, start) in zip(streams, parts):
+        with torch.cuda.stream(s):
+            outs.append(cache.extend(*x, q_start=start, max_new=max(n), scale=0.125))
+    torch.cuda.synchronize()
+    got = dict(o=torch.cat([o.cpu() for o in outs]), k=cache.k_pool.cpu(), v=cache.v_pool.cpu())
+    R.check_extend(c, got, R.extend_ref(c, 0.125), 0.125)
+    for _, start in parts:
+        cache.advance(start)
+    cache.check()
+    assert cache.seq_len.tolist() == [a + b for a, b in zip(c["t"], n)]
