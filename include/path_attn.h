@@ -409,6 +409,7 @@ enum {
   PATH_PAGED_NO_PAGES = 4,    /* not enough free pages */
   PATH_PAGED_BAD_START = 5,   /* q_start falls, leaves [0, total_tokens] or exceeds max_new; advance: it
                                  is not what extend was given */
+  PATH_PAGED_BAD_TOKEN = 6,   /* verify: a drafted token is not in the vocabulary */
   PATH_PAGED_WAIT = 64        /* and above: a bounded wait of a tensor-core kernel gave up */
 };
 
@@ -508,6 +509,107 @@ int path_pages_free(const path_paged_cache_t* cache, const int* slots, int count
                     void* stream);
 int path_pages_trim(const path_paged_cache_t* cache, int window, int sinks, void* ws, size_t ws_bytes, void* stream);
 int path_pages_compact(const path_paged_cache_t* cache, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A step's plan: path_pages_reserve(n_new), and where the new tokens go, for tokens packed in slot order.
+ * n_new [slots], negative values count as 0, or NULL: 1 for every slot in use.  All outputs are written whole:
+ *   q_start [slots + 1]: running sums of n_new;
+ *   slot, position [tokens]: each packed token's slot and position in its sequence (seq_len + its number);
+ *   k_row, v_row [tokens]: its row in each pool, page * page_size + place in the page (head h of it is row
+ *     place of [page][h]);
+ *   source [tokens] with from_start [slots + 1], or both NULL: from_start[slot] + its number, its row in an
+ *     earlier packing that began with the same tokens of each slot (draft tokens, say, of which n_new were kept).
+ * What stands behind the last token is -1.  tokens: what the arrays hold.  With more new tokens than that
+ * (PATH_PAGED_BAD_START), and where reserve records a code, no page is given out, q_start is 0 and the maps are -1.
+ * ws as for path_pages_reserve.
+ */
+int path_pages_plan(const path_paged_cache_t* cache, const int* n_new, const int* from_start, int tokens, int* q_start,
+                    int* slot, int* position, int* k_row, int* v_row, int* source, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/*
+ * Verification of drafted tokens: which of them a target model keeps, and the token after them, so that what is
+ * kept is distributed as if the target had drawn it.  A slot's packed tokens q_start[b] .. q_start[b + 1] - 1 (as
+ * given to path_paged_extend) are one that is known, then its drafts; row i of target holds the target's
+ * probabilities of the token after token i, row i of draft those that token i was drawn from (of a slot's first
+ * token: not read).  draft NULL: the drafts are certain, their probability is 1.
+ *   Draft i is kept if all before it are and uniform[i] * draft[i][x] < target[i - 1][x], x = tokens[i].
+ *   keep[b]: tokens kept, the known one among them (1 .. count; 0: the slot has none).
+ *   next[b]: drawn with uniform[q_start[b]] from max(0, target - draft) of the first draft not kept (where that
+ *     is 0 throughout: from target), or from target's last row where all are kept: the lowest x at which the
+ *     running sum exceeds uniform * the row's sum.  -1: the slot has no token, or the row no positive entry.
+ * Products, differences and sums are exact to 2^-40 and better.  Probabilities need not add up to 1; NaN and negative ones
+ * count as 0.  A draft outside [0, vocab) is not kept (PATH_PAGED_BAD_TOKEN; none is taken out of its row).  A slot
+ * whose row of q_start is bad gets 0 and -1 (PATH_PAGED_BAD_START).
+ */
+typedef struct {
+  int slots;          /* 1..65535 */
+  int total_tokens;   /* rows of target and draft, entries of tokens and uniform */
+  int max_new;        /* at least the most tokens of one slot */
+  int vocab;          /* entries of a row, 1..2^20 */
+  int dtype;          /* path_dtype_t of target and draft */
+  long long target_stride, draft_stride; /* entries from a row to the next, at least vocab */
+} path_verify_desc_t;
+int path_draft_verify(const path_verify_desc_t* desc, const int* q_start, const int* tokens, const float* uniform,
+                      const void* target, const void* draft, int* keep, int* next, int* status, void* stream);
+
+/*
+ * Linear attention
+ * ----------------
+ * With a decay g = exp(log_decay[h]) per key head and a state S (head_dim x head_dim, float32):
+ *   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
+ * log_decay [heads] float32, natural log, kept in [-10000, 0]; NaN makes its head's outputs NaN.
+ */
+typedef struct {
+  int batch, heads_q;  /* heads_q: a multiple of heads (at most 16 times); head hq reads key head hq / (heads_q / heads) */
+  int heads, seqlen;
+  int head_dim;        /* 64 or 128 */
+  int dtype;           /* path_dtype_t of q, k, v, o and the gradients */
+  float scale;
+} path_linear_desc_t;
+
+/* Bytes of workspace of path_linear_fwd (for_backward 0) or path_linear_bwd (1); 0 if desc is invalid.  Host only. */
+size_t path_linear_workspace_size(const path_linear_desc_t* desc, int for_backward);
+/* o from a zero state.  q, o [batch][heads_q][seqlen][head_dim], k, v [batch][heads][seqlen][head_dim]. */
+int path_linear_fwd(const path_linear_desc_t* desc, const void* q, const void* k, const void* v, const float* log_decay,
+                    void* o, void* ws, size_t ws_bytes, void* stream);
+/* Gradients of q, k and v (a key head's summed over its query heads); log_decay is a constant of the model.
+ * Those of dq, dk and dv that are NULL are not computed (one at least is not). */
+int path_linear_bwd(const path_linear_desc_t* desc, const void* q, const void* k, const void* v, const float* log_decay,
+                    const void* dO, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream);
+/* As path_attn_workspace_status, of the call that ran on ws last. */
+int path_linear_workspace_status(const path_linear_desc_t* desc, const void* ws, size_t ws_bytes, int* code, void* stream);
+
+/* States of many sequences, for serving: the slots' states in place of their tokens. */
+typedef struct {
+  int slots, heads;    /* slots 1..65535 */
+  int head_dim;        /* 64 or 128 */
+  int dtype;           /* path_dtype_t of q, k, v, o */
+  float* state;        /* [slots][heads][head_dim (of k)][head_dim (of v)] */
+  int* status;         /* one int, as in path_paged_cache_t */
+} path_linear_cache_t;
+typedef struct {
+  int heads_q, total_tokens, max_new;  /* as in path_paged_desc_t */
+  float scale;
+  int update;          /* 0: the states stay (draft tokens of which some may be rejected) */
+} path_linear_step_t;
+
+/* Bytes of workspace path_linear_extend needs; 0 if cache or step is invalid.  Host only. */
+size_t path_linear_extend_workspace_size(const path_linear_cache_t* cache, const path_linear_step_t* step);
+/*
+ * New tokens of many sequences, packed as for path_paged_extend: q, o [total_tokens][heads_q][head_dim], k, v
+ * [total_tokens][heads][head_dim], slot b's being q_start[b] .. q_start[b + 1] - 1 (NULL: token b is slot b's).
+ * A slot whose row of q_start is bad is left out (PATH_PAGED_BAD_START).  o must not overlap the inputs or the
+ * states.  An infinity or NaN in a slot's tokens or state may reach any output of that slot, never another's.
+ */
+int path_linear_extend(const path_linear_cache_t* cache, const path_linear_step_t* step, const int* q_start, const void* q,
+                       const void* k, const void* v, const float* log_decay, void* o, void* ws, size_t ws_bytes,
+                       void* stream);
+/* children[i] takes the state of parents[i] (NULL: zeros, a new sequence).  An entry that names no slot, or a child
+ * that is listed twice or is a parent too, is left out (PATH_PAGED_BAD_SLOT). */
+int path_linear_fork(const path_linear_cache_t* cache, const int* parents, const int* children, int count, void* stream);
+/* As path_paged_status. */
+int path_linear_status(const path_linear_cache_t* cache, int* code, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,120 @@
+// Linear attention with a decay per head: declarations shared by its translation units (not part of the ABI).
+//
+// All of it is one operation ("walk"), for a key head with decay g and its state S (D x D, float32):
+//   S <- g S + y_i z_i^T,   o_i = scale S^T x_i      for the tokens i of a sequence in walk order,
+//   o_i = scale sum_{j <= i} g^(i-j) (x_i . y_j) z_j + scale g^(i+1) S_0^T x_i.
+// The forward is (x, y, z) = (q, k, v), and because the weight of a pair of tokens depends on their distance alone, each
+// gradient is the same walk over other operands: dq = (do, v, k), and from the last token to the first
+// dk = (v, do, q), dv = (k, q, do).  With several query heads to a key head, either x has them (o too: they read one state)
+// or y and z do (their products add up in one state).
+#pragma once
+
+#include "../../include/path_attn.h"
+#include "internal.h"
+#include "paged.h"
+
+namespace pathattn {
+
+constexpr int kLinTokenMax = 16;  // slots with up to so many new tokens go through the recurrent kernel
+constexpr int kLinChunk = 128;    // segments are multiples of it
+
+struct LinOp {
+  const void *x, *y, *z;
+  void* o;
+  int gx, gy;                      // query heads of a key head in x and o, in y and z (one of them is 1)
+  int reverse;                     // from the last token to the first
+  long long xt, xh, xb;            // strides of x and o in elements: token, head, sequence
+  long long yt, yh, yb;            // of y and z
+};
+
+// What the kernels of a call need, by value.
+struct LinArgs {
+  LinOp op[3];
+  int ops;
+  int D, heads, G;                 // G: query heads per key head
+  int seqs, L;                     // dense: sequences of L tokens
+  const int* q_start;              // packed: slot b's tokens are q_start[b] .. q_start[b + 1] - 1; null: one each
+  int packed, total, max_new, min_new;  // packed: slots with fewer than min_new tokens are the recurrent kernel's
+  int seg, items;                  // tokens of a segment; (sequence, segment) pairs that the grid covers
+  float scale;
+  const float* log_decay;          // [heads]
+  float* state;                    // [seqs][heads][D][D] or null (zero): the state before, and after where update is set
+  int update;
+  float* parts;                    // [ops][items][heads][D][D]: states of single segments, then those at their starts
+  int* err;                        // tensor-core kernels: first wait that gave up
+};
+
+// log2 of the decay: log_decay is kept in [-10000, 0] (exp of the lower end is 0 for any distance but 0), NaN stays.
+PATH_HD float lin_log2(float ld) {
+  const float c = ld > 0.f ? 0.f : ld < -10000.f ? -10000.f : ld;
+  return c * kLog2e;
+}
+
+// New tokens of slot b of a packed call; code for a bad row of q_start.
+struct LinSpan {
+  int q0, n, code;
+};
+PATH_HD LinSpan lin_span(const int* q_start, int b, int total, int max_new) {
+  LinSpan s{b, 1, 0};
+  if (!q_start) return s;
+  s.q0 = q_start[b];
+  const long long n = (long long)q_start[b + 1] - s.q0;
+  if (s.q0 < 0 || n < 0 || (long long)s.q0 + n > total || n > max_new) {
+    s.q0 = s.n = 0;
+    s.code = PATH_PAGED_BAD_START;
+    return s;
+  }
+  s.n = (int)n;
+  return s;
+}
+
+#ifdef __CUDACC__
+struct LinItem {
+  int seq, q0, n, seg;  // seg < 0: none
+};
+// Item `item` of a call, by a whole warp: the segments of all sequences in order.
+__device__ __forceinline__ LinItem lin_item(const LinArgs& p, int item) {
+  if (!p.packed) {
+    const int per = p.items / p.seqs;
+    return {item / per, 0, p.L, item % per};
+  }
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int base = 0; base < p.seqs; base += 32) {
+    LinSpan s{0, 0, 0};
+    if (base + lane < p.seqs) s = lin_span(p.q_start, base + lane, p.total, p.max_new);
+    if (s.n < p.min_new) s.n = 0;
+    int upto = (s.n + p.seg - 1) / p.seg;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += a;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > item);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      const int prev = at ? __shfl_sync(0xffffffffu, upto, at - 1) : 0;
+      return {base + at, __shfl_sync(0xffffffffu, s.q0, at), __shfl_sync(0xffffffffu, s.n, at), item - before - prev};
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return {0, 0, 0, -1};
+}
+#endif
+
+// ---- launchers ----
+// Segments of a call: chosen on the host from sizes alone (ctas: blocks that run at once; per_head: blocks per key head).
+int lin_choose_seg(int seqs, int len, int units, int ctas);
+size_t lin_ws_bytes(const LinArgs& p);
+// Fills items and seg, then parts and err from ws.
+void lin_plan(LinArgs& p, bool bf16);
+cudaError_t launch_linear(LinArgs p, bool bf16, char* ws, cudaStream_t st);
+
+cudaError_t launch_linear_simt(const LinArgs& p, bool bf16, bool states, cudaStream_t st);
+cudaError_t launch_linear_scan(const LinArgs& p, cudaStream_t st);
+// Slots with up to kLinTokenMax new tokens; reports bad rows of q_start.
+cudaError_t launch_linear_token(const LinArgs& p, bool bf16, int* status, cudaStream_t st);
+cudaError_t launch_linear_copy(float* state, int* status, int slots, size_t elems, const int* parents, const int* children,
+                               int count, cudaStream_t st);
+
+}  // namespace pathattn

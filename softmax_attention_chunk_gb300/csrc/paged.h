@@ -240,6 +240,8 @@ cudaError_t launch_paged_new(const PagedArgs& p, char* ws, cudaStream_t st);
 
 size_t pages_ws_bytes(const path_paged_cache_t& c);
 cudaError_t launch_pages_reserve(const path_paged_cache_t& c, const int* n_new, char* ws, cudaStream_t st);
+cudaError_t launch_pages_plan(const path_paged_cache_t& c, const int* n_new, const int* from_start, int tokens, int* q_start,
+                              int* slot, int* position, int* k_row, int* v_row, int* source, char* ws, cudaStream_t st);
 cudaError_t launch_pages_fork(const path_paged_cache_t& c, const int* parents, const int* children, int count, char* ws,
                               cudaStream_t st);
 cudaError_t launch_pages_free(const path_paged_cache_t& c, const int* slots, int count, char* ws, cudaStream_t st);

@@ -48,26 +48,27 @@ Lists lists(const path_paged_cache_t& c, char* ws) {
   return {at(w.head), at(w.ksrc), at(w.kdst), at(w.vsrc), at(w.vdst), at(w.koff), at(w.voff), at(w.kmap), at(w.vmap)};
 }
 
-struct BlockScan {
-  int sum[NW];
+template <typename I> struct BlockScanOf {
+  I sum[NW];
 };
-// Exclusive prefix sum of one int per thread over the block; *total gets the sum.
-__device__ int block_scan(int x, BlockScan& s, int* total) {
+using BlockScan = BlockScanOf<int>;
+// Exclusive prefix sum of one number per thread over the block; *total gets the sum.
+template <typename I> __device__ I block_scan(I x, BlockScanOf<I>& s, I* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int v = x;
+  I v = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, v, o);
+    const I a = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += a;
   }
   __syncthreads();  // the previous use of s is over
   if (lane == 31) s.sum[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    int t = s.sum[lane];
+    I t = s.sum[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, t, o);
+      const I a = __shfl_up_sync(0xffffffffu, t, o);
       if (lane >= o) t += a;
     }
     s.sum[lane] = t;
@@ -121,10 +122,13 @@ __device__ bool bad_slots(const int* list, int count, const int* seq_len, int sl
   return __syncthreads_or(bad) != 0;
 }
 
-// ---------------- reserve ----------------
-__global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const int* n_new, Lists w) {
+// ---------------- reserve, plan ----------------
+// q_start (or null): gets the running sums of the slots' new tokens, zeros where the call records a code; more of them than
+// `tokens` are one.
+__global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const int* n_new, Lists w, int* q_start, int tokens) {
   chain();
   __shared__ BlockScan s;
+  __shared__ BlockScanOf<long long> wide;
   __shared__ int code;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = c.page_size;
   if (tid == 0) code = 0;
@@ -169,14 +173,33 @@ __global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const
     needk += t1;
     needv += t2;
   }
+  if (q_start) {
+    long long all = 0;
+    for (int base = 0; base < c.slots; base += NT) {
+      const int b = base + tid;
+      long long t;
+      const long long a = all + block_scan<long long>(b < c.slots ? asked(b) : 0, wide, &t);
+      if (b < c.slots) q_start[b] = (int)(a < tokens ? a : tokens);
+      all += t;
+    }
+    if (tid == 0) {
+      q_start[c.slots] = (int)(all < tokens ? all : tokens);
+      if (all > tokens) atomicCAS(&code, 0, PATH_PAGED_BAD_START);
+    }
+  }
+  auto refuse = [&](int why) {
+    if (tid == 0) paged_error(c.status, why);
+    if (q_start)
+      for (int b = tid; b <= c.slots; b += NT) q_start[b] = 0;
+  };
   __syncthreads();
   if (code) {
-    if (tid == 0) paged_error(c.status, code);
+    refuse(code);
     return;
   }
   if (needk > c.k_pages || needv > c.v_pages || lowest_free(c.k_ref, c.k_pages, needk, w.kdst, s) < needk ||
       lowest_free(c.v_ref, c.v_pages, needv, w.vdst, s) < needv) {
-    if (tid == 0) paged_error(c.status, PATH_PAGED_NO_PAGES);
+    refuse(PATH_PAGED_NO_PAGES);
     return;
   }
   __syncthreads();
@@ -210,6 +233,46 @@ __global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const
       note_extended(c, b, 0);
     }
   }
+}
+
+// Where the packed tokens of a plan go.
+struct PlanMaps {
+  const int *q_start, *from_start;
+  int *slot, *position, *k_row, *v_row, *source;
+  int tokens;
+};
+constexpr int kPlanStarts = 2048;  // q_start in shared memory, up to so many slots
+__global__ void __launch_bounds__(CT) plan_kernel(path_paged_cache_t c, PlanMaps m) {
+  chain();
+  __shared__ int starts[kPlanStarts + 1];
+  const int* at = m.q_start;
+  if (c.slots <= kPlanStarts) {
+    for (int b = threadIdx.x; b <= c.slots; b += CT) starts[b] = m.q_start[b];
+    __syncthreads();
+    at = starts;
+  }
+  const int i = blockIdx.x * CT + threadIdx.x;
+  if (i >= m.tokens) return;
+  int slot = -1, pos = -1, k = -1, v = -1, from = -1;
+  if (i < at[c.slots]) {
+    int lo = 0, hi = c.slots;  // the last slot that starts at i or before: slots without tokens start where the next one does
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (at[mid] <= i) lo = mid; else hi = mid;
+    }
+    slot = lo;
+    pos = c.seq_len[slot] + i - at[slot];
+    const size_t e = (size_t)slot * c.table_width + pos / c.page_size;
+    const int kp = c.k_table[e], vp = c.v_table[e], in = pos % c.page_size;
+    k = (unsigned)kp < (unsigned)c.k_pages ? kp * c.page_size + in : -1;
+    v = (unsigned)vp < (unsigned)c.v_pages ? vp * c.page_size + in : -1;
+    if (m.from_start) from = m.from_start[slot] + i - at[slot];
+  }
+  m.slot[i] = slot;
+  m.position[i] = pos;
+  m.k_row[i] = k;
+  m.v_row[i] = v;
+  if (m.source) m.source[i] = from;
 }
 
 // ---------------- fork ----------------
@@ -520,7 +583,14 @@ cudaError_t copy_pages(const path_paged_cache_t& c, const Lists& w, int map, cud
 size_t pages_ws_bytes(const path_paged_cache_t& c) { return pages_ws(c).total; }
 
 cudaError_t launch_pages_reserve(const path_paged_cache_t& c, const int* n_new, char* ws, cudaStream_t st) {
-  return launch_chained(reserve_kernel, 1, NT, 0, st, c, n_new, lists(c, ws));
+  return launch_chained(reserve_kernel, 1, NT, 0, st, c, n_new, lists(c, ws), nullptr, 0);
+}
+cudaError_t launch_pages_plan(const path_paged_cache_t& c, const int* n_new, const int* from_start, int tokens, int* q_start,
+                              int* slot, int* position, int* k_row, int* v_row, int* source, char* ws, cudaStream_t st) {
+  const cudaError_t e = launch_chained(reserve_kernel, 1, NT, 0, st, c, n_new, lists(c, ws), q_start, tokens);
+  if (e != cudaSuccess || tokens == 0) return e;
+  return launch_chained(plan_kernel, (unsigned)((tokens + CT - 1) / CT), CT, 0, st, c,
+                        PlanMaps{q_start, from_start, slot, position, k_row, v_row, source, tokens});
 }
 cudaError_t launch_pages_fork(const path_paged_cache_t& c, const int* parents, const int* children, int count, char* ws,
                               cudaStream_t st) {

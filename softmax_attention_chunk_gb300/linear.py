@@ -1,0 +1,208 @@
+"""Linear attention with a decay per head: S_t = g S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t, g = exp(log_decay[head]).
+
+linear_attention(q, k, v, log_decay, scale=1.0) is the layer over whole sequences, differentiable in q, k and v (log_decay
+is a constant of the model).  LinearCache holds the states of many sequences for serving, in the slots and the packing of
+a PagedCache beside it:
+
+    cache = LinearCache(slots=64, heads=8, head_dim=128)
+    o = cache.extend(q, k, v, log_decay, q_start=starts, max_new=512)   # packed new tokens, as PagedCache.extend
+    o = cache.extend(q, k, v, log_decay)                                # one token for every slot
+    o = cache.extend(..., update=False)                                 # drafts: the states stay as they were
+    cache.fork(parents, children); cache.reset(slots)
+    cache.check()                                                       # raises what the device found, if anything
+
+Argument marshalling only: every step runs in the CUDA library, on the current stream of the tensors' device, without
+synchronising (check() does).  Calls that change one cache must be ordered on one stream.  A call can be captured into a
+CUDA graph: q_start and lists are read on the device.
+"""
+from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import path_attn as pa
+
+
+def _same(like, **others):
+    for name, (t, dtype, shape) in others.items():
+        pa._need(t, dtype, shape, name)
+        if t.device != like.device:
+            raise ValueError(f"{name} lies on {t.device}, q on {like.device}")
+
+
+class LinearAttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, scale):
+        q, k, v, log_decay = (t.contiguous() for t in (q, k, v, log_decay))
+        if q.dtype not in pa._DT:
+            raise ValueError(f"unsupported dtype {q.dtype}")
+        if q.dim() != 4 or k.dim() != 4:
+            raise ValueError(f"q is [B, heads_q, L, d], k and v [B, heads, L, d], got {tuple(q.shape)} and {tuple(k.shape)}")
+        B, hq, L, d = q.shape
+        H = k.shape[1]
+        _same(q, q=(q, q.dtype, q.shape), k=(k, q.dtype, (B, H, L, d)), v=(v, q.dtype, (B, H, L, d)),
+              log_decay=(log_decay, torch.float32, (H,)))
+        o = torch.empty_like(q)
+        ctx.save_for_backward(q, k, v, log_decay)
+        ctx.desc = pa.path_linear_desc_t(B, hq, H, L, d, pa._DT[q.dtype], float(scale))
+        if q.numel():
+            _launch(pa.path_linear_fwd, ctx.desc, 0, q, q, k, v, log_decay, o)
+        return o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do):
+        q, k, v, log_decay = ctx.saved_tensors
+        grads = [torch.empty_like(t) if need else None for t, need in zip((q, k, v), ctx.needs_input_grad)]
+        if q.numel() and any(g is not None for g in grads):
+            _launch(pa.path_linear_bwd, ctx.desc, 1, q, q, k, v, log_decay, do.contiguous(), *grads)
+        return *grads, None, None
+
+
+def _launch(fn, desc, for_backward, like, *tensors):
+    with torch.cuda.device(like.device):
+        n = pa.path_linear_workspace_size(desc, for_backward)
+        if n == 0:
+            raise ValueError(f"linear_attention: {desc.heads_q} query heads over {desc.heads} (a multiple, at most 16 times), "
+                             f"head dim {desc.head_dim} (64 or 128), or sizes out of range")
+        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+        pa._check(fn(desc, *(pa._p(t) for t in tensors), ws.data_ptr(), n, pa._stream()), fn.__name__)
+
+
+def linear_attention(q, k, v, log_decay, scale=1.0):
+    """o [B, heads_q, L, d] of q [B, heads_q, L, d], k and v [B, heads, L, d] (bf16 or float32, one dtype; heads_q a
+    multiple of heads: query head hq reads key head hq // (heads_q // heads)) and log_decay [heads] float32, the natural
+    logarithm of the decay per token, kept in [-10000, 0].  Sequences begin with a zero state."""
+    if log_decay.requires_grad:
+        raise ValueError("log_decay is a constant: linear_attention has no gradient for it")
+    return LinearAttentionFunction.apply(q, k, v, log_decay, scale)
+
+
+class LinearCache:
+    """States [slots, heads, head_dim of k, head_dim of v] float32 of many sequences (path_linear_cache_t in
+    include/path_attn.h).  A new cache's states are zero: empty sequences."""
+
+    def __init__(self, slots, heads, head_dim, dtype=torch.bfloat16, device="cuda"):
+        for name, x in (("slots", slots), ("heads", heads)):
+            if int(x) <= 0:
+                raise ValueError(f"{name} must be positive, got {x}")
+        if head_dim not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+        if dtype not in pa._DT:
+            raise ValueError(f"unsupported dtype {dtype}")
+        self._bind(torch.zeros(slots, heads, head_dim, head_dim, dtype=torch.float32, device=device), dtype)
+
+    @classmethod
+    def from_tensors(cls, state, dtype=torch.bfloat16):
+        """A cache over states that exist already (kept, not copied), for tokens of the given dtype."""
+        self = cls.__new__(cls)
+        self._bind(state, dtype)
+        return self
+
+    def _bind(self, state, dtype):
+        if dtype not in pa._DT:
+            raise ValueError(f"unsupported dtype {dtype}")
+        if state.dim() != 4 or state.shape[2] != state.shape[3]:
+            raise ValueError(f"states are [slots, heads, head_dim, head_dim], got {tuple(state.shape)}")
+        pa._need(state, torch.float32, state.shape, "state")
+        self.state, self.dtype, self.device = state, dtype, state.device
+        self.slots, self.heads, self.head_dim = state.shape[:3]
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.c = pa.path_linear_cache_t(self.slots, self.heads, self.head_dim, pa._DT[dtype], pa._p(state), pa._p(self.status))
+        self._index = self.device.index
+        self._plans = {}
+        if pa.path_linear_extend_workspace_size(self.c, pa.path_linear_step_t(self.heads, 0, 0, 1.0, 1)) == 0:
+            raise ValueError("unsupported cache (head_dim 64 or 128, at most 65535 slots and 1024 heads)")
+
+    def extend(self, q, k, v, log_decay, q_start=None, max_new=None, scale=1.0, update=True, ws=None, out=None):
+        """o [tokens, heads_q, head_dim] of the packed new tokens q [tokens, heads_q, head_dim], k, v [tokens, heads,
+        head_dim]; log_decay [heads] float32.  q_start (int32 [slots + 1]): slot b's tokens are q_start[b] ..
+        q_start[b + 1] - 1, at most max_new of them (default: all); without it, token b is slot b's.  The states take the
+        tokens in; with update=False they stay.  out must not overlap the other tensors.  ws: uint8, at least
+        path_linear_extend_workspace_size bytes, for one call at a time (default: a new one)."""
+        if q.dim() != 3:
+            raise ValueError(f"q: expected [tokens, heads_q, head_dim], got {tuple(q.shape)}")
+        N, hq, _ = q.shape
+        self._need(q, self.dtype, (N, hq, self.head_dim), "q")
+        for name, t in (("k", k), ("v", v)):
+            self._need(t, self.dtype, (N, self.heads, self.head_dim), name)
+        self._need(log_decay, torch.float32, (self.heads,), "log_decay")
+        if q_start is not None:
+            self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
+        elif N != self.slots:
+            raise ValueError(f"without q_start there is one token per slot: {N} tokens for {self.slots} slots")
+        if max_new is None:
+            max_new = 1 if q_start is None else N
+        if N > 0 and max_new < 1:
+            raise ValueError(f"max_new must be at least 1 for {N} tokens, got {max_new}")
+        key = (hq, N, max_new, scale, bool(update))
+        plan = self._plans.get(key)
+        if plan is None:  # descriptor and workspace size of calls of these sizes
+            step = pa.path_linear_step_t(hq, N, int(max_new), float(scale), int(bool(update)))
+            n = pa.path_linear_extend_workspace_size(self.c, step)
+            if n == 0:
+                raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens")
+            if len(self._plans) >= 1024:
+                self._plans.clear()
+            plan = self._plans[key] = (step, n)
+        step, n = plan
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._need(out, self.dtype, tuple(q.shape), "out")
+        if N == 0:
+            return out
+        if ws is None:
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        elif ws.dtype != torch.uint8 or ws.device != self.device or not ws.is_contiguous() or ws.numel() < n:
+            raise ValueError(f"ws: expected at least {n} contiguous uint8 on {self.device}, got {ws.numel()} {ws.dtype} on "
+                             f"{ws.device} contiguous={ws.is_contiguous()}")
+        self._call(pa.path_linear_extend, step, pa._p(q_start), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                   out.data_ptr(), ws.data_ptr(), ws.numel())
+        return out
+
+    def fork(self, parents, children):
+        """children[i] takes the state of parents[i] (int32 lists on the device)."""
+        self._list(parents, "parents")
+        self._list(children, "children")
+        if parents.numel() != children.numel():
+            raise ValueError("parents and children have different lengths")
+        if parents.numel():
+            self._call(pa.path_linear_fork, pa._p(parents), pa._p(children), parents.numel())
+
+    def reset(self, slots):
+        """The listed slots begin new sequences: their states become zero."""
+        self._list(slots, "slots")
+        if slots.numel():
+            self._call(pa.path_linear_fork, None, pa._p(slots), slots.numel())
+
+    def check(self):
+        """Raises RuntimeError with what the device recorded since the last check; synchronises."""
+        from .paged import CODES
+
+        with torch.cuda.device(self.device):
+            rc, code = pa.path_linear_status(self.c, pa._stream())
+        if rc != pa.PATH_OK:
+            what = CODES.get(code, f"a kernel's bounded wait gave up (code {code})" if code else "")
+            raise RuntimeError(f"linear cache: {pa.path_status_string(rc)}: {what}")
+
+    # ---- helpers ----
+    def _call(self, fn, *args):
+        """fn(cache, *args, stream) on the current stream of the cache's device; raises on a status."""
+        if torch._C._cuda_getDevice() == self._index:  # (as torch.cuda.current_device, without its checks)
+            rc = fn(self.c, *args, torch._C._cuda_getCurrentRawStream(self._index))
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(self.c, *args, pa._stream())
+        if rc != pa.PATH_OK:
+            pa._check(rc, fn.__name__)
+
+    def _need(self, t, dtype, shape, name):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != self.device:
+            pa._need(t, dtype, shape, name)
+            raise ValueError(f"{name} lies on {t.device}, the cache on {self.device}")
+
+    def _list(self, t, name):
+        if t.dim() != 1 or t.numel() > self.slots:
+            raise ValueError(f"{name}: a list of at most {self.slots} slots")
+        self._need(t, torch.int32, tuple(t.shape), name)

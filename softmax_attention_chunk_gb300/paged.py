@@ -23,14 +23,27 @@ lengths, tables and lists on the device.
 """
 from __future__ import annotations
 
+from typing import NamedTuple, Optional
+
 import torch
 
 from . import path_attn as pa
 
 CODES = {1: "a needed page-table entry is not a page of the pool", 2: "a sequence would outgrow its table row",
          3: "slot out of range, listed twice, empty where it must not be, or in use", 4: "not enough free pages",
-         5: "q_start falls, leaves the packed tokens, exceeds max_new, or (advance) is not what extend was given"}
+         5: "q_start falls, leaves the packed tokens, exceeds max_new, or (advance) is not what extend was given",
+         6: "a drafted token is not in the vocabulary"}
 
+
+class StepPlan(NamedTuple):
+    """Where the packed new tokens of a step go (int32 on the device; -1 behind the last token)."""
+
+    q_start: torch.Tensor   # [slots + 1]: for extend and advance
+    slot: torch.Tensor      # [tokens]
+    position: torch.Tensor  # in the sequence
+    k_row: torch.Tensor     # row of the key pool: page * page_size + place in the page
+    v_row: torch.Tensor     # of the value pool
+    source: Optional[torch.Tensor]  # row of an earlier packing
 
 class PagedCache:
     """Pools, page tables and counts of a paged cache (see path_paged_cache_t in include/path_attn.h)."""
@@ -183,6 +196,58 @@ class PagedCache:
             what = CODES.get(code, f"a kernel's bounded wait gave up (code {code})" if code else "")
             raise RuntimeError(f"paged cache: {pa.path_status_string(rc)}: {what}")
 
+    # ---- a step's tokens ----
+    def plan(self, n_new, tokens, from_start=None):
+        """reserve(n_new), and the StepPlan of these new tokens, packed in slot order into arrays of `tokens` rows.
+        from_start (int32 [slots + 1]): the q_start of an earlier packing that began with the same tokens of each slot;
+        source then says which of its rows each token is (draft tokens of which n_new were kept).  With more than
+        `tokens` new tokens, or where reserve records an error, nothing is reserved and the plan is empty."""
+        if n_new is not None:
+            self._need(n_new, torch.int32, (self.slots,), "n_new")
+        if from_start is not None:
+            self._need(from_start, torch.int32, (self.slots + 1,), "from_start")
+        tokens = int(tokens)
+        if not 0 <= tokens <= 1 << 22:
+            raise ValueError(f"tokens must be in 0 .. {1 << 22}, got {tokens}")
+        # one allocation: q_start, then the maps
+        rows = torch.empty(self.slots + 1 + tokens * (4 if from_start is None else 5), dtype=torch.int32, device=self.device)
+        start, maps = rows[: self.slots + 1], rows[self.slots + 1 :].view(-1, tokens)
+        at = maps.data_ptr()
+        self._pages("plan", pa._p(n_new), pa._p(from_start), tokens, start.data_ptr(), at, at + 4 * tokens, at + 8 * tokens,
+                    at + 12 * tokens, None if from_start is None else at + 16 * tokens)
+        return StepPlan(start, maps[0], maps[1], maps[2], maps[3], None if from_start is None else maps[4])
+
+    def verify(self, target, tokens, uniform, draft=None, q_start=None, max_new=None):
+        """(keep, next), int32 [slots]: how many of each slot's packed tokens stay, the first (known) one among them, and
+        the token after those.  A slot's tokens (int32, packed as for extend with the same q_start) are a known one, then
+        its drafts; target [tokens, vocab] (bf16 or float32) holds the target's probabilities after each token, draft (the
+        same, or None: the drafts are certain) those that each was drawn from.  Draft i stays if those before it do and
+        uniform[i] * draft[i][x] < target[i - 1][x]; next is drawn with the uniform of the slot's first token from
+        max(0, target - draft) of the first draft that went, or from target behind the last token.  Slots without tokens
+        get 0 and -1.  Rows may be apart (a stride), their entries not."""
+        if target.dim() != 2 or target.dtype not in pa._DT:
+            raise ValueError(f"target: expected [tokens, vocab] bf16 or float32, got {target.dtype} {tuple(target.shape)}")
+        N, vocab = target.shape
+        for name, t in (("target", target), ("draft", draft)):
+            if t is not None and (t.shape != target.shape or t.dtype != target.dtype or t.device != self.device
+                                  or (vocab > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < vocab)):
+                raise ValueError(f"{name}: expected {target.dtype} {tuple(target.shape)} with contiguous rows on {self.device}, got "
+                                 f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+        self._need(tokens, torch.int32, (N,), "tokens")
+        self._need(uniform, torch.float32, (N,), "uniform")
+        if q_start is None:
+            raise ValueError("q_start is needed: it says which tokens are whose")
+        self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
+        max_new = N if max_new is None else int(max_new)
+        if max_new < 0 or not 0 < vocab <= 1 << 20:
+            raise ValueError(f"max_new must not be negative and vocab in 1 .. {1 << 20}, got {max_new} and {vocab}")
+        keep, after = torch.empty(2, self.slots, dtype=torch.int32, device=self.device)
+        stride = lambda t: vocab if t is None or N <= 1 else t.stride(0)  # noqa: E731
+        desc = pa.path_verify_desc_t(self.slots, N, max_new, vocab, pa._DT[target.dtype], stride(target), stride(draft))
+        self._call(lambda _, *a: pa.path_draft_verify(desc, *a), pa._p(q_start), pa._p(tokens), pa._p(uniform), pa._p(target),
+                   pa._p(draft), keep.data_ptr(), after.data_ptr(), pa._p(self.status), name="path_draft_verify")
+        return keep, after
+
     # ---- pages ----
     def reserve(self, n_new=None):
         """Pages for n_new[b] (int32 [slots]; None: 1 for every slot in use) more tokens per slot; an empty
@@ -219,7 +284,7 @@ class PagedCache:
         ws = torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
         self._call(getattr(pa, "path_pages_" + name), *args, ws.data_ptr(), ws.numel())
 
-    def _call(self, fn, *args):
+    def _call(self, fn, *args, name=None):
         """fn(cache, *args, stream) on the current stream of the cache's device; raises on a status."""
         if torch._C._cuda_getDevice() == self._index:  # (as torch.cuda.current_device, without its checks)
             rc = fn(self.c, *args, torch._C._cuda_getCurrentRawStream(self._index))
@@ -227,7 +292,7 @@ class PagedCache:
             with torch.cuda.device(self.device):
                 rc = fn(self.c, *args, pa._stream())
         if rc != pa.PATH_OK:
-            pa._check(rc, fn.__name__)
+            pa._check(rc, name or fn.__name__)
 
     def _need(self, t, dtype, shape, name):
         if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != self.device:

@@ -50,6 +50,26 @@ class path_paged_desc_t(ctypes.Structure):
                 ("scale", ctypes.c_float), ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("max_multi", ctypes.c_int)]
 
 
+class path_verify_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("slots", "total_tokens", "max_new", "vocab", "dtype")] + \
+               [("target_stride", ctypes.c_longlong), ("draft_stride", ctypes.c_longlong)]
+
+
+class path_linear_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads_q", "heads", "seqlen", "head_dim", "dtype")] + \
+               [("scale", ctypes.c_float)]
+
+
+class path_linear_cache_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("slots", "heads", "head_dim", "dtype")] + \
+               [("state", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class path_linear_step_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("heads_q", "total_tokens", "max_new")] + \
+               [("scale", ctypes.c_float), ("update", ctypes.c_int)]
+
+
 _vp, _sz, _i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _DP = ctypes.POINTER(path_attn_desc_t)
 _DDP = ctypes.POINTER(path_decode_desc_t)
@@ -114,6 +134,27 @@ _lib.path_pages_trim.restype = _i
 _lib.path_pages_trim.argtypes = [_CP, _i, _i, _vp, _sz, _vp]
 _lib.path_pages_compact.restype = _i
 _lib.path_pages_compact.argtypes = [_CP, _vp, _sz, _vp]
+_lib.path_pages_plan.restype = _i
+_lib.path_pages_plan.argtypes = [_CP, _vp, _vp, _i] + [_vp] * 7 + [_sz, _vp]
+_lib.path_draft_verify.restype = _i
+_lib.path_draft_verify.argtypes = [ctypes.POINTER(path_verify_desc_t)] + [_vp] * 9
+_LD, _LC, _LS = (ctypes.POINTER(t) for t in (path_linear_desc_t, path_linear_cache_t, path_linear_step_t))
+_lib.path_linear_workspace_size.restype = _sz
+_lib.path_linear_workspace_size.argtypes = [_LD, _i]
+_lib.path_linear_fwd.restype = _i
+_lib.path_linear_fwd.argtypes = [_LD] + [_vp] * 6 + [_sz, _vp]
+_lib.path_linear_bwd.restype = _i
+_lib.path_linear_bwd.argtypes = [_LD] + [_vp] * 9 + [_sz, _vp]
+_lib.path_linear_workspace_status.restype = _i
+_lib.path_linear_workspace_status.argtypes = [_LD, _vp, _sz, ctypes.POINTER(_i), _vp]
+_lib.path_linear_extend_workspace_size.restype = _sz
+_lib.path_linear_extend_workspace_size.argtypes = [_LC, _LS]
+_lib.path_linear_extend.restype = _i
+_lib.path_linear_extend.argtypes = [_LC, _LS] + [_vp] * 7 + [_sz, _vp]
+_lib.path_linear_fork.restype = _i
+_lib.path_linear_fork.argtypes = [_LC, _vp, _vp, _i, _vp]
+_lib.path_linear_status.restype = _i
+_lib.path_linear_status.argtypes = [_LC, ctypes.POINTER(_i), _vp]
 PATH_DECODE_NOALLOC_MAX_HEADS = 496
 PATH_ERR_INTERNAL = 6
 
@@ -131,7 +172,9 @@ EXPORTED = ("path_status_string", "path_attn_chunk", "path_attn_workspace_size",
             "path_cp_block_workspace_size", "path_cp_attend_block", "path_cp_pass_block",
             "path_paged_workspace_size", "path_paged_extend", "path_paged_advance", "path_paged_status",
             "path_pages_workspace_size", "path_pages_reserve", "path_pages_fork", "path_pages_free",
-            "path_pages_trim", "path_pages_compact")
+            "path_pages_trim", "path_pages_compact", "path_pages_plan", "path_draft_verify",
+            "path_linear_workspace_size", "path_linear_fwd", "path_linear_bwd", "path_linear_workspace_status",
+            "path_linear_extend_workspace_size", "path_linear_extend", "path_linear_fork", "path_linear_status")
 
 
 # ---------------- raw entry points (same names as the C ABI) ----------------
@@ -282,6 +325,56 @@ def path_pages_trim(cache, window, sinks, ws, ws_bytes, stream) -> int:
 
 def path_pages_compact(cache, ws, ws_bytes, stream) -> int:
     return _lib.path_pages_compact(ctypes.byref(cache), ws, ws_bytes, stream)
+
+
+def path_pages_plan(cache, n_new, from_start, tokens, q_start, slot, position, k_row, v_row, source, ws, ws_bytes,
+                    stream) -> int:
+    return _lib.path_pages_plan(ctypes.byref(cache), n_new, from_start, int(tokens), q_start, slot, position, k_row,
+                                v_row, source, ws, ws_bytes, stream)
+
+
+def path_draft_verify(desc, q_start, tokens, uniform, target, draft, keep, next_, status, stream) -> int:
+    return _lib.path_draft_verify(ctypes.byref(desc), q_start, tokens, uniform, target, draft, keep, next_, status,
+                                  stream)
+
+
+def path_linear_workspace_size(desc, for_backward) -> int:
+    return _lib.path_linear_workspace_size(ctypes.byref(desc), int(for_backward))
+
+
+def path_linear_fwd(desc, q, k, v, log_decay, o, ws, ws_bytes, stream) -> int:
+    return _lib.path_linear_fwd(ctypes.byref(desc), q, k, v, log_decay, o, ws, ws_bytes, stream)
+
+
+def path_linear_bwd(desc, q, k, v, log_decay, dO, dq, dk, dv, ws, ws_bytes, stream) -> int:
+    return _lib.path_linear_bwd(ctypes.byref(desc), q, k, v, log_decay, dO, dq, dk, dv, ws, ws_bytes, stream)
+
+
+def path_linear_workspace_status(desc, ws, ws_bytes, stream):
+    """(status, first recorded device code) of the call that ran on the workspace last; synchronises the stream."""
+    code = _i(0)
+    rc = _lib.path_linear_workspace_status(ctypes.byref(desc), ws, ws_bytes, ctypes.byref(code), stream)
+    return rc, code.value
+
+
+def path_linear_extend_workspace_size(cache, step) -> int:
+    return _lib.path_linear_extend_workspace_size(ctypes.byref(cache), ctypes.byref(step))
+
+
+def path_linear_extend(cache, step, q_start, q, k, v, log_decay, o, ws, ws_bytes, stream) -> int:
+    return _lib.path_linear_extend(ctypes.byref(cache), ctypes.byref(step), q_start, q, k, v, log_decay, o, ws, ws_bytes,
+                                   stream)
+
+
+def path_linear_fork(cache, parents, children, count, stream) -> int:
+    return _lib.path_linear_fork(ctypes.byref(cache), parents, children, int(count), stream)
+
+
+def path_linear_status(cache, stream):
+    """(status, code): reads and clears the cache's status word; synchronises the stream."""
+    code = _i(0)
+    rc = _lib.path_linear_status(ctypes.byref(cache), ctypes.byref(code), stream)
+    return rc, code.value
 
 
 # ---------------- torch-tensor wrappers ----------------
