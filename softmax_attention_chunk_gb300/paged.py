@@ -210,8 +210,9 @@ class PagedCache:
         if not 0 <= tokens <= 1 << 22:
             raise ValueError(f"tokens must be in 0 .. {1 << 22}, got {tokens}")
         # one allocation: q_start, then the maps
-        rows = torch.empty(self.slots + 1 + tokens * (4 if from_start is None else 5), dtype=torch.int32, device=self.device)
-        start, maps = rows[: self.slots + 1], rows[self.slots + 1 :].view(-1, tokens)
+        count = 4 if from_start is None else 5
+        rows = torch.empty(self.slots + 1 + count * tokens, dtype=torch.int32, device=self.device)
+        start, maps = rows[: self.slots + 1], rows[self.slots + 1 :].view(count, tokens)
         at = maps.data_ptr()
         self._pages("plan", pa._p(n_new), pa._p(from_start), tokens, start.data_ptr(), at, at + 4 * tokens, at + 8 * tokens,
                     at + 12 * tokens, None if from_start is None else at + 16 * tokens)
