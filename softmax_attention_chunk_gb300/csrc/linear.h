@@ -41,7 +41,8 @@ struct LinArgs {
   float* state;                    // [seqs][heads][D][D] or null (zero): the state before, and after where update is set
   int update;
   float* parts;                    // [ops][items][heads][D][D]: states of single segments, then those at their starts
-  int* err;                        // tensor-core kernels: first wait that gave up
+  int* err;                        // tensor-core kernels: first wait that gave up,
+  int* status;                     // and where a cache keeps it (or null)
 };
 
 // log2 of the decay: log_decay is kept in [-10000, 0] (exp of the lower end is 0 for any distance but 0), NaN stays.
@@ -103,17 +104,16 @@ __device__ __forceinline__ LinItem lin_item(const LinArgs& p, int item) {
 #endif
 
 // ---- launchers ----
-// Segments of a call: chosen on the host from sizes alone (ctas: blocks that run at once; per_head: blocks per key head).
-int lin_choose_seg(int seqs, int len, int units, int ctas);
+// Fills seg and items, chosen on the host from sizes alone.
+void lin_plan(LinArgs& p);
 size_t lin_ws_bytes(const LinArgs& p);
-// Fills items and seg, then parts and err from ws.
-void lin_plan(LinArgs& p, bool bf16);
 cudaError_t launch_linear(LinArgs p, bool bf16, char* ws, cudaStream_t st);
 
-cudaError_t launch_linear_simt(const LinArgs& p, bool bf16, bool states, cudaStream_t st);
+cudaError_t launch_linear_simt(const LinArgs& p, bool states, cudaStream_t st);  // float32
+cudaError_t launch_linear_tc(const LinArgs& p, bool states, cudaStream_t st);    // bf16
 cudaError_t launch_linear_scan(const LinArgs& p, cudaStream_t st);
-// Slots with up to kLinTokenMax new tokens; reports bad rows of q_start.
-cudaError_t launch_linear_token(const LinArgs& p, bool bf16, int* status, cudaStream_t st);
+// Slots with up to kLinTokenMax new tokens; reports bad rows of q_start and clears err.
+cudaError_t launch_linear_token(const LinArgs& p, bool bf16, cudaStream_t st);
 cudaError_t launch_linear_copy(float* state, int* status, int slots, size_t elems, const int* parents, const int* children,
                                int count, cudaStream_t st);
 

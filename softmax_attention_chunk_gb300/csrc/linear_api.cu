@@ -50,7 +50,7 @@ LinArgs dense_args(const path_linear_desc_t* d, int ops) {
   p.seqs = d->batch;
   p.L = d->seqlen;
   p.scale = d->scale;
-  lin_plan(p, d->dtype == PATH_BF16);
+  lin_plan(p);
   return p;
 }
 // o = walk of x over y and z; queries: x and o have the query heads (else y and z have them).
@@ -74,7 +74,7 @@ LinArgs packed_args(const path_linear_cache_t* c, const path_linear_step_t* s) {
   p.scale = s->scale;
   p.state = c->state;
   p.update = s->update != 0;
-  if (p.max_new > kLinTokenMax) lin_plan(p, c->dtype == PATH_BF16);
+  if (p.max_new > kLinTokenMax) lin_plan(p);
   return p;
 }
 size_t packed_ws(const LinArgs& p) { return p.max_new > kLinTokenMax ? lin_ws_bytes(p) : 256; }
@@ -97,6 +97,7 @@ PATH_API int path_linear_fwd(const path_linear_desc_t* desc, const void* q, cons
   LinArgs p = dense_args(desc, 1);
   if (ws_bytes < lin_ws_bytes(p)) return PATH_ERR_WORKSPACE;
   p.log_decay = log_decay;
+  p.err = (int*)ws;
   p.op[0] = dense_op(desc, q, k, v, o, true, false);
   return cuda_status(launch_linear(p, desc->dtype == PATH_BF16, (char*)ws, (cudaStream_t)stream));
 }
@@ -111,6 +112,7 @@ PATH_API int path_linear_bwd(const path_linear_desc_t* desc, const void* q, cons
   LinArgs p = dense_args(desc, 3);
   if (ws_bytes < lin_ws_bytes(p)) return PATH_ERR_WORKSPACE;
   p.log_decay = log_decay;
+  p.err = (int*)ws;
   p.ops = 0;
   if (dq) p.op[p.ops++] = dense_op(desc, dO, v, k, dq, true, false);
   if (dk) p.op[p.ops++] = dense_op(desc, v, dO, q, dk, false, true);
@@ -153,9 +155,11 @@ PATH_API int path_linear_extend(const path_linear_cache_t* cache, const path_lin
   const long long d = cache->head_dim, tq = d * step->heads_q, tk = d * cache->heads;
   p.q_start = q_start;
   p.log_decay = log_decay;
+  p.err = (int*)ws;
+  p.status = cache->status;
   p.op[0] = LinOp{q, k, v, o, p.G, 1, 0, tq, d, 0, tk, d, 0};
   const bool bf16 = cache->dtype == PATH_BF16;
-  cudaError_t e = launch_linear_token(p, bf16, cache->status, (cudaStream_t)stream);
+  cudaError_t e = launch_linear_token(p, bf16, (cudaStream_t)stream);
   if (e == cudaSuccess && p.max_new > kLinTokenMax && q_start) e = launch_linear(p, bf16, (char*)ws, (cudaStream_t)stream);
   return cuda_status(e);
 }

@@ -1,7 +1,6 @@
-// Linear attention on CUDA cores: the walk of linear.h in chunks of 32 tokens, one block per key head, segment and 64 columns
+// Linear attention in float32 on CUDA cores: the walk of linear.h in chunks of 32 tokens, one block per key head, segment and 64 columns
 // of the state.  Inside a chunk the products x_i . y_j are masked and weighted with g^(i-j); what lies before goes through the
 // state at the chunk's start.
-#include "dev_common.cuh"
 #include "linear.h"
 
 namespace pathattn {
@@ -13,29 +12,18 @@ template <int D> struct Smem {
   float x[C][D + 4], y[C][D + 4], z[C][V + 4], s[D][V + 4], p[C][C + 1], pw[C + 1];
 };
 
-template <typename T> __device__ __forceinline__ void load4(const T* g, float (&v)[4]);
-template <> __device__ __forceinline__ void load4<float>(const float* g, float (&v)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(g);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-}
-template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* g, float (&v)[4]) {
-  const uint2 a = *reinterpret_cast<const uint2*>(g);
-  v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xffff0000u);
-  v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xffff0000u);
-}
-
 // Rows pos .. pos + m - 1 (walk order) of W columns into shared memory, zeros behind them.
-template <typename T, int W, int LD>
-__device__ __forceinline__ void load_rows(float (&dst)[C][LD], const T* src, long long stride, int pos, int m, int n, bool reverse) {
+template <int W, int LD>
+__device__ __forceinline__ void load_rows(float (&dst)[C][LD], const float* src, long long stride, int pos, int m, int n, bool reverse) {
   for (int e = threadIdx.x; e < C * W / 4; e += NT) {
     const int r = e / (W / 4), c = e % (W / 4) * 4;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < m) load4<T>(src + (reverse ? n - 1 - (pos + r) : pos + r) * stride + c, v);
-    *reinterpret_cast<float4*>(&dst[r][c]) = make_float4(v[0], v[1], v[2], v[3]);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < m) v = *reinterpret_cast<const float4*>(src + (reverse ? n - 1 - (pos + r) : pos + r) * stride + c);
+    *reinterpret_cast<float4*>(&dst[r][c]) = v;
   }
 }
 
-template <typename T, int D, bool STATES>
+template <int D, bool STATES>
 __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
   chain();
   extern __shared__ uint8_t smem_raw[];
@@ -54,10 +42,10 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
   const bool split = p.max_new > p.seg;  // the segments' starting states are in parts
   const float* from = STATES ? nullptr : split ? part : own;
   for (int e = tid; e < D * V; e += NT) s.s[e / V][e % V] = from ? from[(size_t)(e / V) * D + e % V] : 0.f;
-  const T* x = (const T*)op.x + it.seq * op.xb + it.q0 * op.xt + (long long)h * op.gx * op.xh;
-  T* o = (T*)op.o + it.seq * op.xb + it.q0 * op.xt + (long long)h * op.gx * op.xh + v0;
-  const T* y = (const T*)op.y + it.seq * op.yb + it.q0 * op.yt + (long long)h * op.gy * op.yh;
-  const T* z = (const T*)op.z + it.seq * op.yb + it.q0 * op.yt + (long long)h * op.gy * op.yh + v0;
+  const float* x = (const float*)op.x + it.seq * op.xb + it.q0 * op.xt + (long long)h * op.gx * op.xh;
+  float* o = (float*)op.o + it.seq * op.xb + it.q0 * op.xt + (long long)h * op.gx * op.xh + v0;
+  const float* y = (const float*)op.y + it.seq * op.yb + it.q0 * op.yt + (long long)h * op.gy * op.yh;
+  const float* z = (const float*)op.z + it.seq * op.yb + it.q0 * op.yt + (long long)h * op.gy * op.yh + v0;
   const int end = min(it.n, (it.seg + 1) * p.seg);
   for (int pos = it.seg * p.seg; pos < end; pos += C) {
     const int m = min(C, end - pos);
@@ -111,21 +99,20 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (r + 16 * i >= m) continue;
-        T* to = o + (long long)g * op.xh + (rev ? it.n - 1 - (pos + r + 16 * i) : pos + r + 16 * i) * op.xt + c4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) to[j] = from_f<T>(acc[i][j] * p.scale);
+        float* to = o + (long long)g * op.xh + (rev ? it.n - 1 - (pos + r + 16 * i) : pos + r + 16 * i) * op.xt + c4;
+        *reinterpret_cast<float4*>(to) = make_float4(acc[i][0] * p.scale, acc[i][1] * p.scale, acc[i][2] * p.scale, acc[i][3] * p.scale);
       }
     };
     if (!STATES && op.gy > 1) {  // one x, its products with all heads of y
       __syncthreads();
-      load_rows<T, D>(s.x, x, op.xt, pos, m, it.n, rev);
+      load_rows<D>(s.x, x, op.xt, pos, m, it.n, rev);
       __syncthreads();
       inter();
     }
     for (int g = 0; g < op.gy; ++g) {
       __syncthreads();  // y, z of the round before have been read
-      load_rows<T, D>(s.y, y + (long long)g * op.yh, op.yt, pos, m, it.n, rev);
-      load_rows<T, V>(s.z, z + (long long)g * op.yh, op.yt, pos, m, it.n, rev);
+      load_rows<D>(s.y, y + (long long)g * op.yh, op.yt, pos, m, it.n, rev);
+      load_rows<V>(s.z, z + (long long)g * op.yh, op.yt, pos, m, it.n, rev);
       __syncthreads();
       if (!STATES) {
         if (op.gy > 1) {
@@ -133,7 +120,7 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
         } else {
           for (int k = 0; k < op.gx; ++k) {
             __syncthreads();
-            load_rows<T, D>(s.x, x + (long long)k * op.xh, op.xt, pos, m, it.n, rev);
+            load_rows<D>(s.x, x + (long long)k * op.xh, op.xt, pos, m, it.n, rev);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -168,22 +155,17 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
     for (int e = tid; e < D * V; e += NT) to[(size_t)(e / V) * D + e % V] = s.s[e / V][e % V];
 }
 
-template <typename T, int D, bool STATES> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(linear_simt_kernel<T, D, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(Smem<D>));
+template <int D, bool STATES> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(linear_simt_kernel<D, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
-  return launch_chained(linear_simt_kernel<T, D, STATES>, dim3(p.items, p.heads * (D / V), p.ops), NT, sizeof(Smem<D>), st, p);
+  return launch_chained(linear_simt_kernel<D, STATES>, dim3(p.items, p.heads * (D / V), p.ops), NT, sizeof(Smem<D>), st, p);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_simt(const LinArgs& p, bool bf16, bool states, cudaStream_t st) {
-  if (bf16) {
-    if (p.D == 64) return states ? launch<__nv_bfloat16, 64, true>(p, st) : launch<__nv_bfloat16, 64, false>(p, st);
-    return states ? launch<__nv_bfloat16, 128, true>(p, st) : launch<__nv_bfloat16, 128, false>(p, st);
-  }
-  if (p.D == 64) return states ? launch<float, 64, true>(p, st) : launch<float, 64, false>(p, st);
-  return states ? launch<float, 128, true>(p, st) : launch<float, 128, false>(p, st);
+cudaError_t launch_linear_simt(const LinArgs& p, bool states, cudaStream_t st) {
+  if (p.D == 64) return states ? launch<64, true>(p, st) : launch<64, false>(p, st);
+  return states ? launch<128, true>(p, st) : launch<128, false>(p, st);
 }
 
 }  // namespace pathattn

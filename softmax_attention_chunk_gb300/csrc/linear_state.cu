@@ -84,14 +84,17 @@ cudaError_t launch_linear_copy(float* state, int* status, int slots, size_t elem
   return launch_chained(linear_copy_kernel, dim3(x < 64 ? x : 64, count), NT, 0, st, state, status, slots, elems, parents, children, count);
 }
 
-int lin_choose_seg(int seqs, int len, int units, int ctas) {
+// Tokens per segment, a multiple of the chunk: as many segments as let the blocks' waves end evenly, where a call with
+// several pays for their states first (measured: about 0.6 of the walk itself, and the launches).
+static int choose_seg(int seqs, int len, int units) {
+  constexpr int kBlocks = 2 * 152;
   const int chunks = (len + kLinChunk - 1) / kLinChunk;
   int best = chunks;
   double least = 0;
   for (int c = chunks; c >= 1; --c) {  // chunks of a segment
     const int n = (chunks + c - 1) / c;
-    if (n > 1 && (chunks + n - 1) / n != c) continue;
-    const double waves = ((long long)seqs * n * units + ctas - 1) / ctas;
+    if (n > 1 && (chunks + n - 1) / n != c) continue;  // (fewer chunks make as many segments)
+    const double waves = (double)(((long long)seqs * n * units + kBlocks - 1) / kBlocks);
     const double cost = waves * c * (n > 1 ? 1.6 : 1.0) + (n > 1 ? 4.0 + 0.05 * n : 0.0);
     if (c == chunks || cost < least) {
       least = cost;
@@ -101,20 +104,17 @@ int lin_choose_seg(int seqs, int len, int units, int ctas) {
   return best * kLinChunk;
 }
 
-void lin_plan(LinArgs& p, bool bf16) {
-  const int V = 64;
-  const int ctas = 152 * 2;
+void lin_plan(LinArgs& p) {
   const int len = p.packed ? p.max_new : p.L;
   const int seqs = p.packed ? (p.total + p.max_new - 1) / p.max_new : p.seqs;
-  p.seg = lin_choose_seg(seqs, len, p.heads * (p.D / V) * p.ops, ctas);
+  p.seg = choose_seg(seqs, len, p.heads * (p.D / 64) * p.ops);
   if (!p.packed) {
     p.max_new = p.L;
     p.items = p.seqs * ((p.L + p.seg - 1) / p.seg);
   } else {  // every slot of several tokens may end in a partly filled segment
-    const long long multi = p.total / p.min_new;
-    p.items = p.total / p.seg + (int)(multi < p.seqs ? multi : p.seqs);
+    const int multi = p.total / p.min_new;
+    p.items = p.total / p.seg + (multi < p.seqs ? multi : p.seqs);
   }
-  (void)bf16;
 }
 
 size_t lin_ws_bytes(const LinArgs& p) {
@@ -122,15 +122,15 @@ size_t lin_ws_bytes(const LinArgs& p) {
 }
 
 cudaError_t launch_linear(LinArgs p, bool bf16, char* ws, cudaStream_t st) {
-  p.err = (int*)ws;
   p.parts = (float*)(ws + 256);
   cudaError_t e = cudaSuccess;
-  if (p.max_new > p.seg) {
-    e = launch_linear_simt(p, bf16, true, st);
+  if (bf16 && !p.packed) e = cudaMemsetAsync(p.err, 0, sizeof(int), st);  // (packed: the token kernel has)
+  auto pass = [&](bool states) { return bf16 ? launch_linear_tc(p, states, st) : launch_linear_simt(p, states, st); };
+  if (e == cudaSuccess && p.max_new > p.seg) {
+    e = pass(true);
     if (e == cudaSuccess) e = launch_linear_scan(p, st);
   }
-  if (e == cudaSuccess) e = launch_linear_simt(p, bf16, false, st);
-  return e;
+  return e == cudaSuccess ? pass(false) : e;
 }
 
 }  // namespace pathattn

@@ -22,8 +22,9 @@ template <> __device__ __forceinline__ void load4s<__nv_bfloat16>(const __nv_bfl
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p, int* status) {
+__global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
   chain();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.err = 0;
   constexpr int CG = D / 4;      // lanes of a row, four columns each
   constexpr int RG = NT / CG;    // row groups
   constexpr int RP = D / RG;     // rows of a thread, one behind the other
@@ -35,7 +36,7 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p, int* 
   const int c = tid % CG * 4, r0 = tid / CG * RP;
   const int h = blockIdx.x, b = blockIdx.y, G = p.G;
   const LinSpan sp = lin_span(p.q_start, b, p.total, p.max_new);
-  if (sp.code && h == 0 && tid == 0) paged_error(status, sp.code);
+  if (sp.code && h == 0 && tid == 0) paged_error(p.status, sp.code);
   const int n = sp.n;
   if (n == 0 || n > kLinTokenMax) return;
   float* own = p.state + (((size_t)b * p.heads + h) * D + r0) * D + c;
@@ -106,19 +107,19 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p, int* 
     for (int i = 0; i < RP; ++i) *reinterpret_cast<float4*>(own + i * D) = s[i];
 }
 
-template <typename T, int D> cudaError_t launch(const LinArgs& p, int* status, cudaStream_t st) {
+template <typename T, int D> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
   const int most = p.max_new < kLinTokenMax ? p.max_new : kLinTokenMax;
   const size_t smem = sizeof(float) * 2 * GB * (NT / 32) * D + sizeof(T) * most * (2 + p.G) * D;
   cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(linear_token_kernel<T, D>, dim3(p.heads, p.seqs), NT, smem, st, p, status);
+  return launch_chained(linear_token_kernel<T, D>, dim3(p.heads, p.seqs), NT, smem, st, p);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_token(const LinArgs& p, bool bf16, int* status, cudaStream_t st) {
-  if (bf16) return p.D == 64 ? launch<__nv_bfloat16, 64>(p, status, st) : launch<__nv_bfloat16, 128>(p, status, st);
-  return p.D == 64 ? launch<float, 64>(p, status, st) : launch<float, 128>(p, status, st);
+cudaError_t launch_linear_token(const LinArgs& p, bool bf16, cudaStream_t st) {
+  if (bf16) return p.D == 64 ? launch<__nv_bfloat16, 64>(p, st) : launch<__nv_bfloat16, 128>(p, st);
+  return p.D == 64 ? launch<float, 64>(p, st) : launch<float, 128>(p, st);
 }
 
 }  // namespace pathattn
