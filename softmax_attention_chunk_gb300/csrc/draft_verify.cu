@@ -18,8 +18,8 @@ namespace cg = cooperative_groups;
 namespace pathattn {
 namespace {
 
-constexpr int NT = 512, NW = NT / 32;
-constexpr int STEP = 512;        // entries whose sums a lane keeps apart
+constexpr int NT = 256, NW = NT / 32;
+constexpr int STEP = 512;        // entries whose sum a warp keeps apart
 constexpr int kMaxSteps = 32;    // steps of a warp: one lane each in the search
 constexpr int kMaxCluster = 8;
 
@@ -55,12 +55,7 @@ template <typename T, int N> __device__ __forceinline__ void load_n(const T* a, 
   }
 }
 
-// What the next token is drawn from: max(0, p - q), p without entry `out`, or p.
-struct Rows {
-  const void *p, *q;   // q null: none
-  int out;             // -1: none
-};
-// Residual as an exact pair (hi, lo).
+// Residual max(0, p - q) as an exact pair (hi, lo).
 __device__ __forceinline__ float2 residual(float p, float q) {
   if (!(p > q)) return make_float2(0.f, 0.f);
   const float s = p - q;
@@ -71,11 +66,6 @@ __device__ __forceinline__ void add_pair(float2& sum, float2 r) {
   const float t = sum.x + r.x, b = t - sum.x;
   sum.y += ((sum.x - (t - b)) + (r.x - b)) + r.y;
   sum.x = t;
-}
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
 }
 __device__ __forceinline__ double warp_scan(double x) {
   const int lane = threadIdx.x & 31;
@@ -93,11 +83,11 @@ __device__ __forceinline__ int first_past(double upto, double part, double goal)
 }
 
 template <typename T, int N>
-__global__ void __launch_bounds__(NT) draft_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(NT, 2) draft_verify_kernel(const VerifyArgs a) {
   chain();
   constexpr int LOADS = STEP / (32 * N);
-  extern __shared__ float2 step_sum[];  // [warp][step][lane]
-  __shared__ double tile_sum[NW], total;
+  constexpr int PER = kMaxCluster * NW / 32;  // warps' sums of the cluster to a lane
+  __shared__ double warp_sum[NW];
   __shared__ int first_bad;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -117,6 +107,7 @@ __global__ void __launch_bounds__(NT) draft_verify_kernel(const VerifyArgs a) {
   }
   const T* target = (const T*)a.target;
   const T* draft = (const T*)a.draft;
+  const double u = a.uniform[q0];
   if (warp == 0) {
     int bad = n;
     for (int i0 = 1; i0 < n && bad == n; i0 += 32) {
@@ -124,12 +115,13 @@ __global__ void __launch_bounds__(NT) draft_verify_kernel(const VerifyArgs a) {
       bool good = true;
       if (i < n) {
         const int x = a.tokens[q0 + i];
+        const float ui = a.uniform[q0 + i];
         good = (unsigned)x < (unsigned)a.d.vocab;
         if (!good && rank == 0) paged_error(a.status, PATH_PAGED_BAD_TOKEN);
         if (good) {
           const float p = positive(to_f<T>(target[(q0 + i - 1) * a.d.target_stride + x]));
           const float q = draft ? positive(to_f<T>(draft[(q0 + i) * a.d.draft_stride + x])) : 1.f;
-          good = (double)a.uniform[q0 + i] * q < (double)p;
+          good = (double)ui * q < (double)p;
         }
       }
       const unsigned no = __ballot_sync(0xffffffffu, !good);
@@ -144,117 +136,129 @@ __global__ void __launch_bounds__(NT) draft_verify_kernel(const VerifyArgs a) {
   const int bad = first_bad;
   const T* p = target + (q0 + bad - 1) * a.d.target_stride;
   const T* q = draft && bad < n ? draft + (q0 + bad) * a.d.draft_stride : nullptr;
-  int out = !draft && bad < n ? a.tokens[q0 + bad] : -1;
+  int out = !draft && bad < n ? a.tokens[q0 + bad] : -1;  // the entry that is left out of p
   const int vocab = a.d.vocab, steps = a.tile / STEP;
   const int v0 = (rank * NW + warp) * a.tile;
-  double before = 0, all = 0;
-  for (int round = 0; round < 2; ++round) {
-    double mine = 0;
-    for (int s = 0; s < steps; ++s) {
-      float2 sum = make_float2(0.f, 0.f);
-      float pv[LOADS][N], qv[LOADS][N];
+  float pv[LOADS][N], qv[LOADS][N];
+  auto load = [&](int at0) {
 #pragma unroll
-      for (int j = 0; j < LOADS; ++j) {
-        const int at = v0 + s * STEP + (j * 32 + lane) * N;
-        load_n<T, N>(p + at, vocab - at, pv[j]);
-        if (q) load_n<T, N>(q + at, vocab - at, qv[j]);
-      }
+    for (int j = 0; j < LOADS; ++j) {
+      const int at = at0 + (j * 32 + lane) * N;
+      load_n<T, N>(p + at, vocab - at, pv[j]);
+      if (q) load_n<T, N>(q + at, vocab - at, qv[j]);
+    }
+  };
+  auto entry = [&](int at0, int j, int i) {
+    return residual(at0 + (j * 32 + lane) * N + i == out ? 0.f : pv[j][i], q ? qv[j][i] : 0.f);
+  };
+  for (int round = 0; round < 2; ++round) {
+    double mine = 0;  // of step `lane`
+    for (int s = 0; s < steps; ++s) {
+      load(v0 + s * STEP);
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < LOADS; ++j)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int at = v0 + s * STEP + (j * 32 + lane) * N + i;
-          add_pair(sum, residual(at == out ? 0.f : pv[j][i], q ? qv[j][i] : 0.f));
-        }
-      step_sum[(warp * steps + s) * 32 + lane] = sum;
-      mine += (double)sum.x + (double)sum.y;
+        for (int i = 0; i < N; ++i) add_pair(sum, entry(v0 + s * STEP, j, i));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        add_pair(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
+      if (lane == s) mine = (double)sum.x + (double)sum.y;
     }
-    mine = warp_sum(mine);
-    if (lane == 0) tile_sum[warp] = mine;
-    __syncthreads();
-    if (tid == 0) {
-      double t = 0;
-      for (int w = 0; w < NW; ++w) t += tile_sum[w];
-      total = t;
-    }
+    const double upto = warp_scan(mine);
+    if (lane == 31) warp_sum[warp] = upto;
     cluster.sync();
-    // (the slices' sums, by lane)
-    const double part = lane < a.slots_cl ? *cluster.map_shared_rank(&total, lane) : 0.0;
-    const double upto = warp_scan(part);
-    all = __shfl_sync(0xffffffffu, upto, 31);
-    cluster.sync();  // no block leaves, or sums again, while others read its sum
-    if (all > 0.0 || round == 1 || (!q && out < 0)) {
-      const double goal = (double)a.uniform[q0] * all;
-      const int owner = first_past(upto, part, goal);
-      if (owner < 0 && rank == 0 && tid == 0) a.next[b] = -1;
-      if (owner != rank || warp != 0) return;
-      before = owner ? __shfl_sync(0xffffffffu, upto, owner - 1) : 0.0;
-      // the warp's share, then its step, then the entry
-      const double tp = lane < NW ? tile_sum[lane] : 0.0, tu = before + warp_scan(tp);
-      const int w = first_past(tu, tp, goal);
-      if (w < 0) {  // (an infinity in the row)
-        if (lane == 0) a.next[b] = -1;
-        return;
-      }
-      if (w) before = __shfl_sync(0xffffffffu, tu, w - 1);
-      double sp = 0;
-      if (lane < steps)
-        for (int l = 0; l < 32; ++l) {
-          const float2 x = step_sum[(w * steps + lane) * 32 + ((l + lane) & 31)];
-          sp += (double)x.x + (double)x.y;
-        }
-      const double su = before + warp_scan(sp);
-      const int s = first_past(su, sp, goal);
-      if (s < 0) {
-        if (lane == 0) a.next[b] = -1;
-        return;
-      }
-      if (s) before = __shfl_sync(0xffffffffu, su, s - 1);
-      int found = -1;
-      float pv[LOADS][N], qv[LOADS][N];
-      const int w0 = (rank * NW + w) * a.tile + s * STEP;
+    // every warp finds the cluster's sum, and whether the goal lies in its own share
+    double part[PER];
 #pragma unroll
-      for (int j = 0; j < LOADS; ++j) {
-        const int at = w0 + (j * 32 + lane) * N;
-        load_n<T, N>(p + at, vocab - at, pv[j]);
-        if (q) load_n<T, N>(q + at, vocab - at, qv[j]);
-      }
-      for (int j = 0; j < LOADS; ++j) {
-        double part_j = 0, r[N];
+    for (int i = 0; i < PER; ++i) {
+      const int w = lane * PER + i;
+      part[i] = w < a.slots_cl * NW ? *cluster.map_shared_rank(&warp_sum[w % NW], w / NW) : 0.0;
+    }
+    cluster.sync();  // no block leaves, or sums again, while others read its sums
+    double lane_sum = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int at = w0 + (j * 32 + lane) * N + i;
-          const float2 x = residual(at == out ? 0.f : pv[j][i], q ? qv[j][i] : 0.f);
-          r[i] = (double)x.x + (double)x.y;
-          part_j += r[i];
-        }
-        const double upto_j = before + warp_scan(part_j);
-        const unsigned past = __ballot_sync(0xffffffffu, upto_j > goal && part_j > 0.0);
-        const unsigned some = __ballot_sync(0xffffffffu, part_j > 0.0);
-        const int l = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : -1;  // (in case rounding lets none pass)
-        if (l >= 0) {
-          double run = __shfl_up_sync(0xffffffffu, upto_j, 1);
-          if (lane == 0) run = before;
-          int at = -1;
-          bool there = false;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            run += r[i];
-            if (r[i] > 0.0 && !there) {
-              at = w0 + (j * 32 + lane) * N + i;
-              there = run > goal;
-            }
-          }
-          found = __shfl_sync(0xffffffffu, at, l);
-          if (past) break;
-        }
-        before = __shfl_sync(0xffffffffu, upto_j, 31);
-      }
-      if (lane == 0) a.next[b] = found;
+    for (int i = 0; i < PER; ++i) lane_sum += part[i];
+    const double lane_upto = warp_scan(lane_sum);
+    const double all = __shfl_sync(0xffffffffu, lane_upto, 31);
+    if (!(all > 0.0) && round == 0 && (q || out >= 0)) {
+      q = nullptr;  // nothing is left of the target: its own row
+      out = -1;
+      continue;
+    }
+    const double goal = u * all;
+    const int l = first_past(lane_upto, lane_sum, goal);
+    if (l < 0) {
+      if (rank == 0 && tid == 0) a.next[b] = -1;
       return;
     }
-    q = nullptr;  // nothing is left of the target: its own row
-    out = -1;
+    const double before_lane = lane_upto - lane_sum;
+    // the first part at which the running sum passes
+    double run = before_lane, at_owner = before_lane;
+    bool there = false;
+    int owner = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (!there && part[i] > 0.0) {
+        owner = i;
+        at_owner = run;
+        there = run + part[i] > goal;
+      }
+      run += part[i];
+    }
+    owner = __shfl_sync(0xffffffffu, lane * PER + owner, l);
+    double before = __shfl_sync(0xffffffffu, at_owner, l);
+    if (owner != rank * NW + warp) return;
+    const int s = first_past(before + upto, mine, goal);
+    if (s < 0) {  // (an infinity in the row)
+      if (lane == 0) a.next[b] = -1;
+      return;
+    }
+    const double prev = __shfl_sync(0xffffffffu, upto, s > 0 ? s - 1 : 0);
+    if (s > 0) before += prev;
+    // the step's entries again, exactly
+    load(v0 + s * STEP);
+    double sum_j[LOADS], upto_j[LOADS];
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) add_pair(sum, entry(v0 + s * STEP, j, i));
+      upto_j[j] = sum_j[j] = (double)sum.x + (double)sum.y;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j) {
+        const double x = __shfl_up_sync(0xffffffffu, upto_j[j], o);
+        if (lane >= o) upto_j[j] += x;
+      }
+    int found = -1;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto_j[j] > goal && sum_j[j] > 0.0);
+      const unsigned some = __ballot_sync(0xffffffffu, sum_j[j] > 0.0);
+      if (some) {
+        const int w = past ? __ffs(past) - 1 : 31 - __clz(some);  // (in case rounding lets none pass: the last)
+        double at = before + (upto_j[j] - sum_j[j]);
+        int x = -1;
+        bool passed = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float2 r = entry(v0 + s * STEP, j, i);
+          at += (double)r.x + (double)r.y;
+          if (r.x > 0.f && !passed) {
+            x = v0 + s * STEP + (j * 32 + lane) * N + i;
+            passed = at > goal;
+          }
+        }
+        found = __shfl_sync(0xffffffffu, x, w);
+        if (past) break;
+      }
+      before += __shfl_sync(0xffffffffu, upto_j[j], 31);
+    }
+    if (lane == 0) a.next[b] = found;
+    return;
   }
 }
 
@@ -264,13 +268,9 @@ template <typename T, int N> cudaError_t launch(VerifyArgs& a, int slots, cudaSt
   while (cl < kMaxCluster && ((long long)slots * cl < 304 || a.d.vocab > cl * NW * STEP * kMaxSteps) && a.d.vocab > cl * 4096) cl *= 2;
   a.slots_cl = cl;
   a.tile = (a.d.vocab + cl * NW * STEP - 1) / (cl * NW * STEP) * STEP;
-  const size_t smem = sizeof(float2) * NW * 32 * (a.tile / STEP);
-  cudaError_t e = cudaFuncSetAttribute(draft_verify_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(slots * cl));
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -147,10 +147,12 @@ PATH_API int path_linear_extend(const path_linear_cache_t* cache, const path_lin
   if (rc == PATH_OK) rc = check_step(cache, step);
   if (rc != PATH_OK) return rc;
   if (q_start ? !aligned(q_start, 4) : step->total_tokens != cache->slots || step->max_new < 1) return PATH_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(log_decay, 4) || !aligned(o, 16) || !aligned(ws, 256))
-    return PATH_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(log_decay, 4) || !aligned(o, 16)) return PATH_ERR_INVALID_ARG;
   LinArgs p = packed_args(cache, step);
-  if (ws_bytes < packed_ws(p)) return PATH_ERR_WORKSPACE;
+  if (p.max_new > kLinTokenMax) {
+    if (!aligned(ws, 256)) return PATH_ERR_INVALID_ARG;
+    if (ws_bytes < packed_ws(p)) return PATH_ERR_WORKSPACE;
+  }
   if (step->total_tokens == 0 || step->max_new == 0) return PATH_OK;
   const long long d = cache->head_dim, tq = d * step->heads_q, tk = d * cache->heads;
   p.q_start = q_start;

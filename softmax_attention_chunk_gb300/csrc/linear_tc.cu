@@ -43,11 +43,6 @@ template <int D, int PARTS> struct Smem {
   uint32_t tmem_base;
 };
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t f2_bits(uint32_t a, uint32_t b) { return (uint64_t)b << 32 | a; }
 __device__ __forceinline__ uint32_t pack_pair(uint64_t v) { return pack_bf16(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))); }
 // 32 bytes of global memory, aligned to them or (wide false) to 16.

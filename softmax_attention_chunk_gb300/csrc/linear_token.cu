@@ -3,12 +3,15 @@
 // Bound: the state's bytes, 8 D^2 per slot and key head (4 D^2 where it is not written back).
 #include "dev_common.cuh"
 #include "linear.h"
+#include "tc_common.cuh"
 
 namespace pathattn {
 namespace {
 
-constexpr int NT = 256;
-constexpr int GB = 4;  // query heads whose sums are joined at once
+using namespace tc;
+
+constexpr int NT = 256, W = NT / 32;
+constexpr int OB = 8;  // rows of o (token, query head) whose sums the warps join at once
 
 template <typename T> __device__ __forceinline__ void load4s(const T* a, float (&v)[4]);
 template <> __device__ __forceinline__ void load4s<float>(const float* a, float (&v)[4]) {
@@ -24,14 +27,12 @@ template <> __device__ __forceinline__ void load4s<__nv_bfloat16>(const __nv_bfl
 template <typename T, int D>
 __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
   chain();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.err = 0;
+  if (p.max_new > kLinTokenMax && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.err = 0;  // (of the kernels that follow)
   constexpr int CG = D / 4;      // lanes of a row, four columns each
   constexpr int RG = NT / CG;    // row groups
   constexpr int RP = D / RG;     // rows of a thread, one behind the other
-  constexpr int W = NT / 32;
   extern __shared__ uint8_t smem_raw[];
-  float (*red)[GB][W][D] = reinterpret_cast<float (*)[GB][W][D]>(smem_raw);  // [2]: the warps' sums
-  T* tok = reinterpret_cast<T*>(smem_raw + sizeof(float) * 2 * GB * W * D);  // per token: k, v, q of the group
+  T* tok = reinterpret_cast<T*>(smem_raw);  // per token: k, v, q of the group
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = tid % CG * 4, r0 = tid / CG * RP;
   const int h = blockIdx.x, b = blockIdx.y, G = p.G;
@@ -40,11 +41,12 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
   const int n = sp.n;
   if (n == 0 || n > kLinTokenMax) return;
   float* own = p.state + (((size_t)b * p.heads + h) * D + r0) * D + c;
-  float4 s[RP];
+  ulonglong2 s[RP];  // pairs of floats
 #pragma unroll
-  for (int i = 0; i < RP; ++i) s[i] = *reinterpret_cast<const float4*>(own + i * D);
+  for (int i = 0; i < RP; ++i) s[i] = *reinterpret_cast<const ulonglong2*>(own + i * D);
   const LinOp& op = p.op[0];
   const int per = (2 + G) * D;
+  float* red = reinterpret_cast<float*>(tok + min(p.max_new, kLinTokenMax) * per);  // [2][OB][W][D]: the warps' sums
   for (int e = tid * 4; e < n * per; e += NT * 4) {
     const int t = e / per, x = e % per / D, col = e % D;
     const long long at = sp.q0 + t;
@@ -54,64 +56,78 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
     if (sizeof(T) == 4) *reinterpret_cast<float4*>(tok + e) = *reinterpret_cast<const float4*>(src + col);
     else *reinterpret_cast<uint2*>(tok + e) = *reinterpret_cast<const uint2*>(src + col);
   }
-  const float keep = exp2f(lin_log2(p.log_decay[h]));
+  const float g1 = exp2f(lin_log2(p.log_decay[h]));
+  const uint64_t keep = f2(g1, g1);
   __syncthreads();
-  int buf = 0;
-  for (int t = 0; t < n; ++t) {
-    const T* at = tok + t * per;
-    float v[4];
-    load4s<T>(at + D + c, v);
+  T* o = (T*)op.o + (long long)sp.q0 * op.xt + (long long)h * G * op.xh;
+  const T* at = tok;
+  int g = 0, t0 = 0, g0 = 0, buf = 0;  // head; token and head of the first row not joined yet
+  const int rows = n * G;
+  for (int i = 0; i < rows; ++i) {
+    if (g == 0) {
+      float v[4];
+      load4s<T>(at + D + c, v);
+      const uint64_t v0 = f2(v[0], v[1]), v1 = f2(v[2], v[3]);
 #pragma unroll
-    for (int i = 0; i < RP; i += 4) {
-      float k[4];
-      load4s<T>(at + r0 + i, k);
+      for (int j = 0; j < RP; j += 4) {
+        float k[4];
+        load4s<T>(at + r0 + j, k);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float4& a = s[i + j];
-        a.x = a.x * keep + k[j] * v[0], a.y = a.y * keep + k[j] * v[1];
-        a.z = a.z * keep + k[j] * v[2], a.w = a.w * keep + k[j] * v[3];
+        for (int x = 0; x < 4; ++x) {
+          const uint64_t kk = f2(k[x], k[x]);
+          s[j + x].x = f2_fma(s[j + x].x, keep, f2_mul(kk, v0));
+          s[j + x].y = f2_fma(s[j + x].y, keep, f2_mul(kk, v1));
+        }
       }
     }
-    for (int g0 = 0; g0 < G; g0 += GB, buf ^= 1) {
+    uint64_t o0 = 0, o1 = 0;
 #pragma unroll
-      for (int g = 0; g < GB; ++g) {
-        if (g0 + g >= G) break;
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < RP; j += 4) {
+      float q[4];
+      load4s<T>(at + (2 + g) * D + r0 + j, q);
 #pragma unroll
-        for (int i = 0; i < RP; i += 4) {
-          float q[4];
-          load4s<T>(at + (2 + g0 + g) * D + r0 + i, q);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4& a = s[i + j];
-            o[0] += a.x * q[j], o[1] += a.y * q[j], o[2] += a.z * q[j], o[3] += a.w * q[j];
-          }
-        }
-        if (CG < 32)  // two row groups to a warp
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] += __shfl_xor_sync(0xffffffffu, o[j], 16);
-        if (CG == 32 || lane < CG) *reinterpret_cast<float4*>(&red[buf][g][warp][c]) = make_float4(o[0], o[1], o[2], o[3]);
+      for (int x = 0; x < 4; ++x) {
+        const uint64_t qq = f2(q[x], q[x]);
+        o0 = f2_fma(s[j + x].x, qq, o0);
+        o1 = f2_fma(s[j + x].y, qq, o1);
       }
+    }
+    float a[4];
+    f2_split(o0, a[0], a[1]);
+    f2_split(o1, a[2], a[3]);
+    if (CG < 32)  // two row groups to a warp
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] += __shfl_xor_sync(0xffffffffu, a[j], 16);
+    if (CG == 32 || lane < CG)
+      *reinterpret_cast<float4*>(red + ((buf * OB + i % OB) * W + warp) * D + c) = make_float4(a[0], a[1], a[2], a[3]);
+    if (++g == G) g = 0, at += per;
+    const int done = i % OB + 1;
+    if (done == OB || i + 1 == rows) {
       __syncthreads();  // (the other half of red was read before the block came here)
-      for (int e = tid; e < min(GB, G - g0) * D; e += NT) {
-        const int g = e / D, col = e % D;
+      for (int e = tid; e < done * D; e += NT) {
+        const int row = g0 + e / D, col = e % D;
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) sum += red[buf][g][w][col];
-        ((T*)op.o)[(long long)(sp.q0 + t) * op.xt + (long long)(h * G + g0 + g) * op.xh + col] = from_f<T>(sum * p.scale);
+        for (int w = 0; w < W; ++w) sum += red[((buf * OB + e / D) * W + w) * D + col];
+        o[(t0 + row / G) * op.xt + (long long)(row % G) * op.xh + col] = from_f<T>(sum * p.scale);
       }
+      buf ^= 1;
+      t0 += (g0 + done) / G;
+      g0 = (g0 + done) % G;
     }
   }
   if (p.update)
 #pragma unroll
-    for (int i = 0; i < RP; ++i) *reinterpret_cast<float4*>(own + i * D) = s[i];
+    for (int i = 0; i < RP; ++i) *reinterpret_cast<ulonglong2*>(own + i * D) = s[i];
 }
 
 template <typename T, int D> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
-  const int most = p.max_new < kLinTokenMax ? p.max_new : kLinTokenMax;
-  const size_t smem = sizeof(float) * 2 * GB * (NT / 32) * D + sizeof(T) * most * (2 + p.G) * D;
-  cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  const int most = p.max_new < kLinTokenMax ? p.max_new : kLinTokenMax, rows = most * p.G;
+  const size_t smem = sizeof(T) * most * (2 + p.G) * D + sizeof(float) * W * D * (rows > OB ? 2 * OB : rows);
+  if (smem > 48 << 10) {
+    cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_chained(linear_token_kernel<T, D>, dim3(p.heads, p.seqs), NT, smem, st, p);
 }
 

@@ -8,7 +8,11 @@
 // Bound: the copies (each byte read and written once): compaction that moves 426 MB 148 us, of which the copy 127 (6.7
 // TB/s, a plain copy's rate) and the bookkeeping by one block the rest (pieces of 16 KB in place of 8: 147); a fork of
 // one short sequence is the latency of its launches.
+#include <cooperative_groups.h>
+
 #include "paged.h"
+
+namespace cg = cooperative_groups;
 
 namespace pathattn {
 namespace {
@@ -79,26 +83,37 @@ template <typename I> __device__ I block_scan(I x, BlockScanOf<I>& s, I* total) 
 }
 
 // The numbers of the first `need` pages with ref == 0, in rising order, into out; returns how many were
-// found (fewer: the pool has no more).
+// found (fewer: the pool has no more).  A warp looks at PER rows of 32 neighbouring pages, the next ones on their way.
 __device__ int lowest_free(const int* ref, int pages, int need, int* out, BlockScan& s) {
-  constexpr int PER = 8;
+  constexpr int PER = 16;
+  const int lane = threadIdx.x & 31, at0 = (threadIdx.x >> 5) * (32 * PER) + lane;
   int have = 0;
+  int r[PER], next[PER];
+  auto load = [&](int base, int (&x)[PER]) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) x[i] = base + at0 + 32 * i < pages ? ref[base + at0 + 32 * i] : 1;
+  };
+  if (need > 0) load(0, next);
   for (int base = 0; base < pages && have < need; base += NT * PER) {
-    unsigned bits = 0;
-    const int p0 = base + threadIdx.x * PER;
-    int r[PER];
+    unsigned free[PER];
+    int mine = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) r[i] = p0 + i < pages ? ref[p0 + i] : 1;
+    for (int i = 0; i < PER; ++i) r[i] = next[i];
+    if (base + NT * PER < pages) load(base + NT * PER, next);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) bits |= (r[i] <= 0 ? 1u : 0u) << i;
+    for (int i = 0; i < PER; ++i) {
+      free[i] = __ballot_sync(0xffffffffu, r[i] <= 0);
+      mine += __popc(free[i]);
+    }
     int tot;
-    int at = have + block_scan(__popc(bits), s, &tot);
+    int at = have + block_scan(lane == 0 ? mine : 0, s, &tot);
+    at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (bits >> i & 1) {
-        if (at < need) out[at] = p0 + i;
-        ++at;
-      }
+    for (int i = 0; i < PER; ++i) {
+      const int mineat = at + __popc(free[i] & ((1u << lane) - 1));
+      if ((free[i] >> lane & 1) && mineat < need) out[mineat] = base + at0 + 32 * i;
+      at += __popc(free[i]);
+    }
     have += tot;
   }
   return have < need ? have : need;
@@ -123,116 +138,105 @@ __device__ bool bad_slots(const int* list, int count, const int* seq_len, int sl
 }
 
 // ---------------- reserve, plan ----------------
+// One block for the keys' pool and one for the values' (a cluster): each counts what its table lacks and looks for as many
+// free pages; only when both know that nothing is refused do they write.  Slots are taken NT at a time, their columns
+// (those behind the last page, up to the page of the last new row) side by side in order.
 // q_start (or null): gets the running sums of the slots' new tokens, zeros where the call records a code; more of them than
 // `tokens` are one.
-__global__ void __launch_bounds__(NT) reserve_kernel(path_paged_cache_t c, const int* n_new, Lists w, int* q_start, int tokens) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT)
+    reserve_kernel(path_paged_cache_t c, const int* n_new, Lists w, int* q_start, int tokens) {
   chain();
   __shared__ BlockScan s;
   __shared__ BlockScanOf<long long> wide;
-  __shared__ int code;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = c.page_size;
+  __shared__ int code, first[NT + 1], column[NT];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, P = c.page_size;
+  const bool values = cluster.block_rank() == 1;
+  int* table = values ? c.v_table : c.k_table;
+  int* ref = values ? c.v_ref : c.k_ref;
+  int* list = values ? w.vdst : w.kdst;
+  const int pages = values ? c.v_pages : c.k_pages;
   if (tid == 0) code = 0;
   __syncthreads();
-  auto asked = [&](int b) {
-    const int n = n_new ? n_new[b] : (c.seq_len[b] >= 0 ? 1 : 0);
-    return n < 0 ? 0 : n;
-  };
-  // columns that slot b needs: those behind its last page, up to the page of its last new row
-  auto columns = [&](int b, int* c0, int* c1) {
-    const int len = c.seq_len[b] < 0 ? 0 : c.seq_len[b], n = asked(b);
-    *c0 = (int)(((long long)len + P - 1) / P);
-    *c1 = n ? (int)(((long long)len + n + P - 1) / P) : *c0;
-    if (n && (long long)len + n > (long long)c.table_width * P) {
-      atomicCAS(&code, 0, PATH_PAGED_CAPACITY);
-      *c1 = *c0;
-    }
-  };
-  for (int b = warp; b < c.slots; b += NW) {  // pages each slot lacks, one warp per slot
-    int c0, c1, nk = 0, nv = 0;
-    columns(b, &c0, &c1);
-    for (int x = c0 + lane; x < c1; x += 32) {
-      nk += c.k_table[(size_t)b * c.table_width + x] < 0;
-      nv += c.v_table[(size_t)b * c.table_width + x] < 0;
-    }
-    nk = __reduce_add_sync(0xffffffffu, nk);
-    nv = __reduce_add_sync(0xffffffffu, nv);
-    if (lane == 0) {
-      w.koff[b] = nk;
-      w.voff[b] = nv;
-    }
-  }
-  __syncthreads();
-  int needk = 0, needv = 0;
-  for (int base = 0; base < c.slots; base += NT) {
-    const int b = base + tid;
-    int t1, t2;
-    const int a = block_scan(b < c.slots ? w.koff[b] : 0, s, &t1);
-    if (b < c.slots) w.koff[b] = needk + a;
-    const int e = block_scan(b < c.slots ? w.voff[b] : 0, s, &t2);
-    if (b < c.slots) w.voff[b] = needv + e;
-    needk += t1;
-    needv += t2;
-  }
-  if (q_start) {
-    long long all = 0;
+  long long all = 0;
+  // visit(entry, lacks) for every column of every slot, by the whole block in step; count: the first time
+  auto walk = [&](bool count, auto visit) {
     for (int base = 0; base < c.slots; base += NT) {
       const int b = base + tid;
-      long long t;
-      const long long a = all + block_scan<long long>(b < c.slots ? asked(b) : 0, wide, &t);
-      if (b < c.slots) q_start[b] = (int)(a < tokens ? a : tokens);
-      all += t;
+      int cols = 0, n = 0;
+      if (b < c.slots) {
+        const int len = c.seq_len[b];
+        n = n_new ? n_new[b] : (len >= 0 ? 1 : 0);
+        n = n < 0 ? 0 : n;
+        const long long have = len < 0 ? 0 : len, to = have + n;
+        column[tid] = (int)((have + P - 1) / P);
+        if (n && to > (long long)c.table_width * P) atomicCAS(&code, 0, PATH_PAGED_CAPACITY);
+        else if (n) cols = (int)((to + P - 1) / P) - column[tid];
+      }
+      if (count && q_start) {
+        long long t;
+        const long long a = all + block_scan<long long>(n, wide, &t);
+        if (!values && b < c.slots) q_start[b] = (int)(a < tokens ? a : tokens);
+        all += t;
+      }
+      int total;
+      first[tid] = block_scan(cols, s, &total);
+      if (tid == 0) first[NT] = total;
+      __syncthreads();
+      for (int i0 = 0; i0 < total; i0 += NT) {
+        const int i = i0 + tid;
+        size_t e = 0;
+        bool lacks = false;
+        if (i < total) {
+          int lo = 0, hi = NT;
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= i) lo = mid; else hi = mid;
+          }
+          e = (size_t)(base + lo) * c.table_width + column[lo] + (i - first[lo]);
+          lacks = table[e] < 0;
+        }
+        visit(e, lacks);
+      }
+      __syncthreads();
     }
-    if (tid == 0) {
-      q_start[c.slots] = (int)(all < tokens ? all : tokens);
-      if (all > tokens) atomicCAS(&code, 0, PATH_PAGED_BAD_START);
-    }
-  }
-  auto refuse = [&](int why) {
-    if (tid == 0) paged_error(c.status, why);
-    if (q_start)
-      for (int b = tid; b <= c.slots; b += NT) q_start[b] = 0;
   };
-  __syncthreads();
-  if (code) {
-    refuse(code);
-    return;
-  }
-  if (needk > c.k_pages || needv > c.v_pages || lowest_free(c.k_ref, c.k_pages, needk, w.kdst, s) < needk ||
-      lowest_free(c.v_ref, c.v_pages, needv, w.vdst, s) < needv) {
-    refuse(PATH_PAGED_NO_PAGES);
-    return;
+  int need = 0;
+  walk(true, [&](size_t, bool lacks) { need += __syncthreads_count(lacks); });
+  if (q_start && tid == 0) {
+    if (!values) q_start[c.slots] = (int)(all < tokens ? all : tokens);
+    if (all > tokens) atomicCAS(&code, 0, PATH_PAGED_BAD_START);
   }
   __syncthreads();
-  for (int b = warp; b < c.slots; b += NW) {
-    int c0, c1;
-    columns(b, &c0, &c1);
-    int ak = w.koff[b], av = w.voff[b];
-    for (int x0 = c0; x0 < c1; x0 += 32) {
-      const int x = x0 + lane;
-      int* kt = c.k_table + (size_t)b * c.table_width + x;
-      int* vt = c.v_table + (size_t)b * c.table_width + x;
-      const bool fk = x < c1 && *kt < 0, fv = x < c1 && *vt < 0;
-      const unsigned mk = __ballot_sync(0xffffffffu, fk), mv = __ballot_sync(0xffffffffu, fv);
-      const unsigned below = (1u << lane) - 1;
-      if (fk) {
-        const int pg = w.kdst[ak + __popc(mk & below)];
-        *kt = pg;
-        c.k_ref[pg] = 1;
-      }
-      if (fv) {
-        const int pg = w.vdst[av + __popc(mv & below)];
-        *vt = pg;
-        c.v_ref[pg] = 1;
-      }
-      ak += __popc(mk);
-      av += __popc(mv);
+  if (code == 0 && (need > pages || lowest_free(ref, pages, need, list, s) < need) && tid == 0) code = PATH_PAGED_NO_PAGES;
+  cluster.sync();
+  const int mine = code, other = *cluster.map_shared_rank(&code, values ? 0 : 1);
+  cluster.sync();  // (neither block has gone while the other reads, nor writes before both know)
+  if (mine || other) {
+    if (!values) {
+      if (tid == 0) paged_error(c.status, mine ? mine : other);
+      if (q_start)
+        for (int b = tid; b <= c.slots; b += NT) q_start[b] = 0;
     }
-    __syncwarp();
-    if (lane == 0 && c.seq_len[b] < 0 && asked(b) > 0) {
-      c.seq_len[b] = 0;
-      note_extended(c, b, 0);
-    }
+    return;
   }
+  int given = 0;
+  walk(false, [&](size_t e, bool lacks) {
+    int t;
+    const int at = given + block_scan<int>(lacks, s, &t);
+    if (lacks) {
+      const int pg = list[at];
+      table[e] = pg;
+      ref[pg] = 1;
+    }
+    given += t;
+  });
+  if (!values)  // (empty slots count as length 0 above, so it does not matter when the other block sees this)
+    for (int b = tid; b < c.slots; b += NT)
+      if (n_new && n_new[b] > 0 && c.seq_len[b] < 0) {
+        c.seq_len[b] = 0;
+        note_extended(c, b, 0);
+      }
 }
 
 // Where the packed tokens of a plan go.
@@ -583,11 +587,11 @@ cudaError_t copy_pages(const path_paged_cache_t& c, const Lists& w, int map, cud
 size_t pages_ws_bytes(const path_paged_cache_t& c) { return pages_ws(c).total; }
 
 cudaError_t launch_pages_reserve(const path_paged_cache_t& c, const int* n_new, char* ws, cudaStream_t st) {
-  return launch_chained(reserve_kernel, 1, NT, 0, st, c, n_new, lists(c, ws), nullptr, 0);
+  return launch_chained(reserve_kernel, 2, NT, 0, st, c, n_new, lists(c, ws), nullptr, 0);
 }
 cudaError_t launch_pages_plan(const path_paged_cache_t& c, const int* n_new, const int* from_start, int tokens, int* q_start,
                               int* slot, int* position, int* k_row, int* v_row, int* source, char* ws, cudaStream_t st) {
-  const cudaError_t e = launch_chained(reserve_kernel, 1, NT, 0, st, c, n_new, lists(c, ws), q_start, tokens);
+  const cudaError_t e = launch_chained(reserve_kernel, 2, NT, 0, st, c, n_new, lists(c, ws), q_start, tokens);
   if (e != cudaSuccess || tokens == 0) return e;
   return launch_chained(plan_kernel, (unsigned)((tokens + CT - 1) / CT), CT, 0, st, c,
                         PlanMaps{q_start, from_start, slot, position, k_row, v_row, source, tokens});

@@ -22,31 +22,35 @@ from torch.autograd.function import once_differentiable
 
 from . import path_attn as pa
 
+TOKEN_MAX = 16  # new tokens of a slot up to which no workspace is used
 
-def _same(like, **others):
-    for name, (t, dtype, shape) in others.items():
-        pa._need(t, dtype, shape, name)
-        if t.device != like.device:
-            raise ValueError(f"{name} lies on {t.device}, q on {like.device}")
+
+_sizes = {}  # (descriptor's numbers, backward?) -> workspace bytes
 
 
 class LinearAttentionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, log_decay, scale):
-        q, k, v, log_decay = (t.contiguous() for t in (q, k, v, log_decay))
-        if q.dtype not in pa._DT:
-            raise ValueError(f"unsupported dtype {q.dtype}")
+        q, k, v, log_decay = q.contiguous(), k.contiguous(), v.contiguous(), log_decay.contiguous()
+        dt = q.dtype
+        if dt not in pa._DT:
+            raise ValueError(f"unsupported dtype {dt}")
         if q.dim() != 4 or k.dim() != 4:
             raise ValueError(f"q is [B, heads_q, L, d], k and v [B, heads, L, d], got {tuple(q.shape)} and {tuple(k.shape)}")
         B, hq, L, d = q.shape
         H = k.shape[1]
-        _same(q, q=(q, q.dtype, q.shape), k=(k, q.dtype, (B, H, L, d)), v=(v, q.dtype, (B, H, L, d)),
-              log_decay=(log_decay, torch.float32, (H,)))
+        for name, t, want, shape in (("q", q, dt, (B, hq, L, d)), ("k", k, dt, (B, H, L, d)), ("v", v, dt, (B, H, L, d)),
+                                     ("log_decay", log_decay, torch.float32, (H,))):
+            if t.dtype is not want or t.shape != shape or not t.is_cuda:
+                pa._need(t, want, shape, name)
+            if t.device != q.device:
+                raise ValueError(f"{name} lies on {t.device}, q on {q.device}")
         o = torch.empty_like(q)
         ctx.save_for_backward(q, k, v, log_decay)
-        ctx.desc = pa.path_linear_desc_t(B, hq, H, L, d, pa._DT[q.dtype], float(scale))
+        ctx.sizes = (B, hq, H, L, d, pa._DT[dt])
+        ctx.scale = float(scale)
         if q.numel():
-            _launch(pa.path_linear_fwd, ctx.desc, 0, q, q, k, v, log_decay, o)
+            _launch(pa.path_linear_fwd, 0, ctx, q, k, v, log_decay, o)
         return o
 
     @staticmethod
@@ -55,18 +59,32 @@ class LinearAttentionFunction(torch.autograd.Function):
         q, k, v, log_decay = ctx.saved_tensors
         grads = [torch.empty_like(t) if need else None for t, need in zip((q, k, v), ctx.needs_input_grad)]
         if q.numel() and any(g is not None for g in grads):
-            _launch(pa.path_linear_bwd, ctx.desc, 1, q, q, k, v, log_decay, do.contiguous(), *grads)
+            _launch(pa.path_linear_bwd, 1, ctx, q, k, v, log_decay, do.contiguous(), *grads)
         return *grads, None, None
 
 
-def _launch(fn, desc, for_backward, like, *tensors):
-    with torch.cuda.device(like.device):
+def _launch(fn, for_backward, ctx, q, *tensors):
+    desc = pa.path_linear_desc_t(*ctx.sizes, ctx.scale)
+    key = (ctx.sizes, for_backward)
+    n = _sizes.get(key)
+    if n is None:
         n = pa.path_linear_workspace_size(desc, for_backward)
         if n == 0:
             raise ValueError(f"linear_attention: {desc.heads_q} query heads over {desc.heads} (a multiple, at most 16 times), "
-                             f"head dim {desc.head_dim} (64 or 128), or sizes out of range")
-        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
-        pa._check(fn(desc, *(pa._p(t) for t in tensors), ws.data_ptr(), n, pa._stream()), fn.__name__)
+                             f"head dim {desc.head_dim} (64 or 128), scale {desc.scale}, or sizes out of range")
+        if len(_sizes) >= 1024:
+            _sizes.clear()
+        _sizes[key] = n
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    args = [None if t is None else t.data_ptr() for t in tensors]
+    index = q.device.index
+    if torch._C._cuda_getDevice() == index:  # (as torch.cuda.current_device, without its checks)
+        rc = fn(desc, q.data_ptr(), *args, ws.data_ptr(), n, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(desc, q.data_ptr(), *args, ws.data_ptr(), n, pa._stream())
+    if rc != pa.PATH_OK:
+        pa._check(rc, fn.__name__)
 
 
 def linear_attention(q, k, v, log_decay, scale=1.0):
@@ -120,46 +138,53 @@ class LinearCache:
         q_start[b + 1] - 1, at most max_new of them (default: all); without it, token b is slot b's.  The states take the
         tokens in; with update=False they stay.  out must not overlap the other tensors.  ws: uint8, at least
         path_linear_extend_workspace_size bytes, for one call at a time (default: a new one)."""
+        dt, at = self.dtype, self._index
+        key = (q.shape, k.shape, v.shape, q_start is None, max_new, scale, update)
+        plan = self._plans.get(key)
+        if plan is None or q.dtype is not dt or k.dtype is not dt or v.dtype is not dt or not (
+                q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and q.get_device() == k.get_device() == v.get_device() == at):
+            plan = self._plans[key] = self._plan(q, k, v, q_start, max_new, scale, update)
+        step, n, chunks = plan
+        self._need(log_decay, torch.float32, (self.heads,), "log_decay")
+        if q_start is not None:
+            self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._need(out, dt, tuple(q.shape), "out")
+        if out.shape[0] == 0:
+            return out
+        if ws is not None:
+            if ws.dtype != torch.uint8 or ws.device != self.device or not ws.is_contiguous() or ws.numel() < n:
+                raise ValueError(f"ws: expected at least {n} contiguous uint8 on {self.device}, got {ws.numel()} {ws.dtype} on "
+                                 f"{ws.device} contiguous={ws.is_contiguous()}")
+        elif chunks:
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self._call(pa.path_linear_extend, step, None if q_start is None else q_start.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                   log_decay.data_ptr(), out.data_ptr(), None if ws is None else ws.data_ptr(), n)
+        return out
+
+    def _plan(self, q, k, v, q_start, max_new, scale, update):
+        """(descriptor, workspace bytes, whether they are used) of calls of these sizes, once their tensors are right."""
         if q.dim() != 3:
             raise ValueError(f"q: expected [tokens, heads_q, head_dim], got {tuple(q.shape)}")
         N, hq, _ = q.shape
         self._need(q, self.dtype, (N, hq, self.head_dim), "q")
         for name, t in (("k", k), ("v", v)):
             self._need(t, self.dtype, (N, self.heads, self.head_dim), name)
-        self._need(log_decay, torch.float32, (self.heads,), "log_decay")
-        if q_start is not None:
-            self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
-        elif N != self.slots:
+        if q_start is None and N != self.slots:
             raise ValueError(f"without q_start there is one token per slot: {N} tokens for {self.slots} slots")
         if max_new is None:
             max_new = 1 if q_start is None else N
         if N > 0 and max_new < 1:
             raise ValueError(f"max_new must be at least 1 for {N} tokens, got {max_new}")
-        key = (hq, N, max_new, scale, bool(update))
-        plan = self._plans.get(key)
-        if plan is None:  # descriptor and workspace size of calls of these sizes
-            step = pa.path_linear_step_t(hq, N, int(max_new), float(scale), int(bool(update)))
-            n = pa.path_linear_extend_workspace_size(self.c, step)
-            if n == 0:
-                raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens")
-            if len(self._plans) >= 1024:
-                self._plans.clear()
-            plan = self._plans[key] = (step, n)
-        step, n = plan
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            self._need(out, self.dtype, tuple(q.shape), "out")
-        if N == 0:
-            return out
-        if ws is None:
-            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        elif ws.dtype != torch.uint8 or ws.device != self.device or not ws.is_contiguous() or ws.numel() < n:
-            raise ValueError(f"ws: expected at least {n} contiguous uint8 on {self.device}, got {ws.numel()} {ws.dtype} on "
-                             f"{ws.device} contiguous={ws.is_contiguous()}")
-        self._call(pa.path_linear_extend, step, pa._p(q_start), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                   out.data_ptr(), ws.data_ptr(), ws.numel())
-        return out
+        step = pa.path_linear_step_t(hq, N, int(max_new), float(scale), int(bool(update)))
+        n = pa.path_linear_extend_workspace_size(self.c, step)
+        if n == 0:
+            raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens, scale {scale}")
+        if len(self._plans) >= 1024:
+            self._plans.clear()
+        return step, n, min(int(max_new), N) > TOKEN_MAX
 
     def fork(self, parents, children):
         """children[i] takes the state of parents[i] (int32 lists on the device)."""

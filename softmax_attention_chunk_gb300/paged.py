@@ -45,6 +45,10 @@ class StepPlan(NamedTuple):
     v_row: torch.Tensor     # of the value pool
     source: Optional[torch.Tensor]  # row of an earlier packing
 
+def _verify(cache, *args):
+    return pa.path_draft_verify(*args)
+
+
 class PagedCache:
     """Pools, page tables and counts of a paged cache (see path_paged_cache_t in include/path_attn.h)."""
 
@@ -114,7 +118,7 @@ class PagedCache:
                                        p(a_pool), p(k_table), p(v_table), p(seq_len), p(k_ref), p(v_ref),
                                        p(self.status), p(extended), p(a_rest))
         self._index = self.device.index
-        self._plans = {}
+        self._plans, self._verifications = {}, {}
         self._pages_bytes = pa.path_pages_workspace_size(self.c)
         if self._pages_bytes == 0:
             raise ValueError("unsupported cache (head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; sizes in range)")
@@ -209,14 +213,13 @@ class PagedCache:
         tokens = int(tokens)
         if not 0 <= tokens <= 1 << 22:
             raise ValueError(f"tokens must be in 0 .. {1 << 22}, got {tokens}")
-        # one allocation: q_start, then the maps
         count = 4 if from_start is None else 5
         rows = torch.empty(self.slots + 1 + count * tokens, dtype=torch.int32, device=self.device)
-        start, maps = rows[: self.slots + 1], rows[self.slots + 1 :].view(count, tokens)
-        at = maps.data_ptr()
-        self._pages("plan", pa._p(n_new), pa._p(from_start), tokens, start.data_ptr(), at, at + 4 * tokens, at + 8 * tokens,
-                    at + 12 * tokens, None if from_start is None else at + 16 * tokens)
-        return StepPlan(start, maps[0], maps[1], maps[2], maps[3], None if from_start is None else maps[4])
+        parts = rows.split([self.slots + 1] + [tokens] * count)  # q_start, then the maps
+        start = rows.data_ptr()
+        at = [start + 4 * (self.slots + 1 + i * tokens) for i in range(count)]
+        self._pages("plan", pa._p(n_new), pa._p(from_start), tokens, start, *at, *([None] if from_start is None else []))
+        return StepPlan(*parts, *([None] if from_start is None else []))
 
     def verify(self, target, tokens, uniform, draft=None, q_start=None, max_new=None):
         """(keep, next), int32 [slots]: how many of each slot's packed tokens stay, the first (known) one among them, and
@@ -226,28 +229,43 @@ class PagedCache:
         uniform[i] * draft[i][x] < target[i - 1][x]; next is drawn with the uniform of the slot's first token from
         max(0, target - draft) of the first draft that went, or from target behind the last token.  Slots without tokens
         get 0 and -1.  Rows may be apart (a stride), their entries not."""
-        if target.dim() != 2 or target.dtype not in pa._DT:
-            raise ValueError(f"target: expected [tokens, vocab] bf16 or float32, got {target.dtype} {tuple(target.shape)}")
-        N, vocab = target.shape
-        for name, t in (("target", target), ("draft", draft)):
-            if t is not None and (t.shape != target.shape or t.dtype != target.dtype or t.device != self.device
-                                  or (vocab > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < vocab)):
-                raise ValueError(f"{name}: expected {target.dtype} {tuple(target.shape)} with contiguous rows on {self.device}, got "
-                                 f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+        key = (target.shape, target.dtype, target.stride(), None if draft is None else draft.stride(), max_new)
+        desc = self._verifications.get(key)
+        if desc is None:
+            desc = self._verification(target, draft, max_new)
+            if len(self._verifications) >= 1024:
+                self._verifications.clear()
+            self._verifications[key] = desc
+        N = desc.total_tokens
+        if target.device != self.device or (draft is not None and (draft.dtype != target.dtype or draft.shape != target.shape
+                                                                   or draft.device != self.device)):
+            raise ValueError(f"target and draft: expected one type and shape on {self.device}, got {target.dtype} {tuple(target.shape)} on "
+                             f"{target.device}" + ("" if draft is None else f" and {draft.dtype} {tuple(draft.shape)} on {draft.device}"))
         self._need(tokens, torch.int32, (N,), "tokens")
         self._need(uniform, torch.float32, (N,), "uniform")
         if q_start is None:
             raise ValueError("q_start is needed: it says which tokens are whose")
         self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
+        keep = torch.empty(self.slots, dtype=torch.int32, device=self.device)
+        after = torch.empty(self.slots, dtype=torch.int32, device=self.device)
+        self._call(_verify, desc, q_start.data_ptr(), tokens.data_ptr(), uniform.data_ptr(), target.data_ptr(), pa._p(draft),
+                   keep.data_ptr(), after.data_ptr(), self.status.data_ptr())
+        return keep, after
+
+    def _verification(self, target, draft, max_new):
+        """The descriptor of calls with rows like these."""
+        if target.dim() != 2 or target.dtype not in pa._DT:
+            raise ValueError(f"target: expected [tokens, vocab] bf16 or float32, got {target.dtype} {tuple(target.shape)}")
+        N, vocab = target.shape
+        strides = []
+        for name, t in (("target", target), ("draft", draft)):
+            if t is not None and (t.shape != target.shape or (vocab > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < vocab)):
+                raise ValueError(f"{name}: expected {tuple(target.shape)} with contiguous rows, got {tuple(t.shape)} strides {t.stride()}")
+            strides.append(vocab if t is None or N <= 1 else t.stride(0))
         max_new = N if max_new is None else int(max_new)
         if max_new < 0 or not 0 < vocab <= 1 << 20:
             raise ValueError(f"max_new must not be negative and vocab in 1 .. {1 << 20}, got {max_new} and {vocab}")
-        keep, after = torch.empty(2, self.slots, dtype=torch.int32, device=self.device)
-        stride = lambda t: vocab if t is None or N <= 1 else t.stride(0)  # noqa: E731
-        desc = pa.path_verify_desc_t(self.slots, N, max_new, vocab, pa._DT[target.dtype], stride(target), stride(draft))
-        self._call(lambda _, *a: pa.path_draft_verify(desc, *a), pa._p(q_start), pa._p(tokens), pa._p(uniform), pa._p(target),
-                   pa._p(draft), keep.data_ptr(), after.data_ptr(), pa._p(self.status), name="path_draft_verify")
-        return keep, after
+        return pa.path_verify_desc_t(self.slots, N, max_new, vocab, pa._DT[target.dtype], *strides)
 
     # ---- pages ----
     def reserve(self, n_new=None):
@@ -285,7 +303,7 @@ class PagedCache:
         ws = torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
         self._call(getattr(pa, "path_pages_" + name), *args, ws.data_ptr(), ws.numel())
 
-    def _call(self, fn, *args, name=None):
+    def _call(self, fn, *args):
         """fn(cache, *args, stream) on the current stream of the cache's device; raises on a status."""
         if torch._C._cuda_getDevice() == self._index:  # (as torch.cuda.current_device, without its checks)
             rc = fn(self.c, *args, torch._C._cuda_getCurrentRawStream(self._index))
@@ -293,7 +311,7 @@ class PagedCache:
             with torch.cuda.device(self.device):
                 rc = fn(self.c, *args, pa._stream())
         if rc != pa.PATH_OK:
-            pa._check(rc, name or fn.__name__)
+            pa._check(rc, fn.__name__)
 
     def _need(self, t, dtype, shape, name):
         if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != self.device:

@@ -90,15 +90,18 @@ def test_steps(pa, field, value, want):
 
 
 def test_extend_pointers(pa):
+    many = lstep(pa, total_tokens=90, max_new=50)
     for name in ("q", "k", "v", "ld", "o", "ws"):
         for bad in (None, FAKE + 2):
-            assert extend(pa, lcache(pa), lstep(pa), **{name: bad}) == 1, name
+            assert extend(pa, lcache(pa), many, **{name: bad}) == 1, name
+            if name != "ws":
+                assert extend(pa, lcache(pa), lstep(pa), **{name: bad}) == 1, name
     for name in ("state", "status"):
         for bad in (None, FAKE + 2):
             c = lcache(pa, **{name: bad})
             assert extend(pa, c, lstep(pa)) == 1 and pa.path_linear_status(c, None)[0] == 1
             assert pa.path_linear_fork(c, None, FAKE, 1, None) == 1
-    assert extend(pa, lcache(pa), lstep(pa), nbytes=8) == 3
+    assert extend(pa, lcache(pa), many, nbytes=8) == 3
     assert extend(pa, lcache(pa), lstep(pa), q_start=FAKE + 1) == 1
     assert extend(pa, lcache(pa), lstep(pa), q_start=None) == 1  # nine tokens for three slots
     assert extend(pa, lcache(pa), lstep(pa, total_tokens=3, max_new=0), q_start=None) == 1
