@@ -16,7 +16,8 @@
 namespace pathattn {
 
 constexpr int kLinTokenMax = 16;  // slots with up to so many new tokens go through the recurrent kernel
-constexpr int kLinChunk = 128;    // segments are multiples of it
+constexpr int kLinChunk = 128;    // tokens of a chunk; segments are multiples of it
+constexpr int kLinChunkF32 = 64;  // in float32
 
 struct LinOp {
   const void *x, *y, *z;
@@ -105,7 +106,7 @@ __device__ __forceinline__ LinItem lin_item(const LinArgs& p, int item) {
 
 // ---- launchers ----
 // Fills seg and items, chosen on the host from sizes alone.
-void lin_plan(LinArgs& p);
+void lin_plan(LinArgs& p, bool bf16);
 size_t lin_ws_bytes(const LinArgs& p);
 cudaError_t launch_linear(LinArgs p, bool bf16, char* ws, cudaStream_t st);
 

@@ -50,7 +50,7 @@ LinArgs dense_args(const path_linear_desc_t* d, int ops) {
   p.seqs = d->batch;
   p.L = d->seqlen;
   p.scale = d->scale;
-  lin_plan(p);
+  lin_plan(p, d->dtype == PATH_BF16);
   return p;
 }
 // o = walk of x over y and z; queries: x and o have the query heads (else y and z have them).
@@ -74,7 +74,7 @@ LinArgs packed_args(const path_linear_cache_t* c, const path_linear_step_t* s) {
   p.scale = s->scale;
   p.state = c->state;
   p.update = s->update != 0;
-  if (p.max_new > kLinTokenMax) lin_plan(p);
+  if (p.max_new > kLinTokenMax) lin_plan(p, c->dtype == PATH_BF16);
   return p;
 }
 size_t packed_ws(const LinArgs& p) { return p.max_new > kLinTokenMax ? lin_ws_bytes(p) : 256; }

@@ -1,34 +1,62 @@
-// Linear attention in float32 on CUDA cores: the walk of linear.h in chunks of 32 tokens, one block per key head, segment and 64 columns
-// of the state.  Inside a chunk the products x_i . y_j are masked and weighted with g^(i-j); what lies before goes through the
-// state at the chunk's start.
+// Linear attention in float32 on CUDA cores: the walk of linear.h in chunks of 64 tokens, one block per key head, segment and
+// 64 columns of the state.  Inside a chunk the products x_i . y_j are masked and weighted with g^(i-j); what lies before goes
+// through the state at the chunk's start.
+// Bound: FP32 multiply-adds and the shared-memory reads that feed them; a thread holds 4 x 4 of every product, so a 16-byte
+// read feeds 8 of them.
 #include "linear.h"
+#include "tc_common.cuh"
 
 namespace pathattn {
 namespace {
 
-constexpr int NT = 256, C = 32, V = 64;
+using namespace tc;
+
+constexpr int NT = 256, C = kLinChunkF32, V = 64;
 
 template <int D> struct Smem {
-  float x[C][D + 4], y[C][D + 4], z[C][V + 4], s[D][V + 4], p[C][C + 1], pw[C + 1];
+  float x[C][D + 4], y[C][D + 4], z[C][V + 4], s[D][V + 4], p[C][C + 4], pw[C + 1];
 };
 
 // Rows pos .. pos + m - 1 (walk order) of W columns into shared memory, zeros behind them.
 template <int W, int LD>
 __device__ __forceinline__ void load_rows(float (&dst)[C][LD], const float* src, long long stride, int pos, int m, int n, bool reverse) {
-  for (int e = threadIdx.x; e < C * W / 4; e += NT) {
-    const int r = e / (W / 4), c = e % (W / 4) * 4;
+#pragma unroll
+  for (int i = 0; i < C * W / 4 / NT; ++i) {
+    const int e = threadIdx.x + i * NT, r = e / (W / 4), c = e % (W / 4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < m) v = *reinterpret_cast<const float4*>(src + (reverse ? n - 1 - (pos + r) : pos + r) * stride + c);
     *reinterpret_cast<float4*>(&dst[r][c]) = v;
+  }
+}
+__device__ __forceinline__ void get4(const float* a, float (&v)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(a);
+  v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+}
+// acc[4][4] += rows r0 .. r0 + 3 of a (K columns) times rows 0 .. K - 1 of b, columns c0 .. c0 + 3.
+template <int K, int LA, int LB>
+__device__ __forceinline__ void product(float (&acc)[4][4], const float (&a)[C][LA], const float (*b)[LB], int r0, int c0) {
+#pragma unroll 4
+  for (int e = 0; e < K; e += 4) {
+    float x[4][4], y[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) get4(&a[r0 + i][e], x[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) get4(&b[e + i][c0], y[i]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] += x[i][k] * y[k][j];
   }
 }
 
 template <int D, bool STATES>
 __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
   chain();
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<D>& s = *reinterpret_cast<Smem<D>*>(smem_raw);
-  const int tid = threadIdx.x, r = tid / 16, c4 = tid % 16 * 4;  // owns o rows r, r + 16 and state rows r + 16 k, columns c4 ..
+  const int tid = threadIdx.x, r0 = tid / 16 * 4, j0 = tid % 16, c0 = j0 * 4;  // owns o rows r0 .. r0 + 3, columns c0 .. c0 + 3
   constexpr int NV = D / V;
   const int h = blockIdx.y / NV, v0 = blockIdx.y % NV * V, item = blockIdx.x;
   const LinOp& op = p.op[blockIdx.z];
@@ -41,7 +69,9 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
   float* own = p.state ? p.state + ((size_t)it.seq * p.heads + h) * D * D + v0 : nullptr;
   const bool split = p.max_new > p.seg;  // the segments' starting states are in parts
   const float* from = STATES ? nullptr : split ? part : own;
-  for (int e = tid; e < D * V; e += NT) s.s[e / V][e % V] = from ? from[(size_t)(e / V) * D + e % V] : 0.f;
+  for (int e = tid * 4; e < D * V; e += NT * 4)
+    *reinterpret_cast<float4*>(&s.s[e / V][e % V]) =
+        from ? *reinterpret_cast<const float4*>(from + (size_t)(e / V) * D + e % V) : make_float4(0.f, 0.f, 0.f, 0.f);
   const float* x = (const float*)op.x + it.seq * op.xb + it.q0 * op.xt + (long long)h * op.gx * op.xh;
   float* o = (float*)op.o + it.seq * op.xb + it.q0 * op.xt + (long long)h * op.gx * op.xh + v0;
   const float* y = (const float*)op.y + it.seq * op.yb + it.q0 * op.yt + (long long)h * op.gy * op.yh;
@@ -49,57 +79,50 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
   const int end = min(it.n, (it.seg + 1) * p.seg);
   for (int pos = it.seg * p.seg; pos < end; pos += C) {
     const int m = min(C, end - pos);
-    float acc[2][4] = {};
+    float acc[4][4] = {};
     auto inter = [&]() {
-#pragma unroll 4
-      for (int e = 0; e < D; ++e) {
-        const float4 b = *reinterpret_cast<const float4*>(&s.s[e][c4]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float a = s.x[r + 16 * i][e];
-          acc[i][0] += a * b.x, acc[i][1] += a * b.y, acc[i][2] += a * b.z, acc[i][3] += a * b.w;
-        }
-      }
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] *= s.pw[r + 16 * i + 1];
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+      product<D>(acc, s.x, s.s, r0, c0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] *= s.pw[r0 + i + 1];
     };
     auto intra = [&]() {
-      float d[2][2] = {};
-      const int j0 = tid % 16;
+      uint64_t d[4][4] = {};  // rows r0 .. r0 + 3, columns j0 + 16 j: sums over even and odd places
 #pragma unroll 4
       for (int e = 0; e < D; e += 4) {
-        const float4 x0 = *reinterpret_cast<const float4*>(&s.x[r][e]), x1 = *reinterpret_cast<const float4*>(&s.x[r + 16][e]);
-        const float4 y0 = *reinterpret_cast<const float4*>(&s.y[j0][e]), y1 = *reinterpret_cast<const float4*>(&s.y[j0 + 16][e]);
-        d[0][0] += x0.x * y0.x + x0.y * y0.y + x0.z * y0.z + x0.w * y0.w;
-        d[0][1] += x0.x * y1.x + x0.y * y1.y + x0.z * y1.z + x0.w * y1.w;
-        d[1][0] += x1.x * y0.x + x1.y * y0.y + x1.z * y0.z + x1.w * y0.w;
-        d[1][1] += x1.x * y1.x + x1.y * y1.y + x1.z * y1.z + x1.w * y1.w;
+        ulonglong2 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(&s.x[r0 + i][e]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const ulonglong2*>(&s.y[j0 + 16 * j][e]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[i][j] = f2_fma(a[i].y, b[j].y, f2_fma(a[i].x, b[j].x, d[i][j]));
       }
       __syncthreads();  // the previous products' p has been read
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int gap = r + 16 * i - (j0 + 16 * j);
-          s.p[r + 16 * i][j0 + 16 * j] = gap >= 0 ? d[i][j] * s.pw[gap] : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          const int gap = r0 + i - (j0 + 16 * j);
+          float even, odd;
+          f2_split(d[i][j], even, odd);
+          s.p[r0 + i][j0 + 16 * j] = gap >= 0 ? (even + odd) * s.pw[gap] : 0.f;
         }
       __syncthreads();
-#pragma unroll 4
-      for (int j = 0; j < C; ++j) {
-        const float4 b = *reinterpret_cast<const float4*>(&s.z[j][c4]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float a = s.p[r + 16 * i][j];
-          acc[i][0] += a * b.x, acc[i][1] += a * b.y, acc[i][2] += a * b.z, acc[i][3] += a * b.w;
-        }
-      }
+      product<C>(acc, s.p, s.z, r0, c0);
     };
     auto store = [&](int g) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (r + 16 * i >= m) continue;
-        float* to = o + (long long)g * op.xh + (rev ? it.n - 1 - (pos + r + 16 * i) : pos + r + 16 * i) * op.xt + c4;
+      for (int i = 0; i < 4; ++i) {
+        if (r0 + i >= m) continue;
+        float* to = o + (long long)g * op.xh + (rev ? it.n - 1 - (pos + r0 + i) : pos + r0 + i) * op.xt + c0;
         *reinterpret_cast<float4*>(to) = make_float4(acc[i][0] * p.scale, acc[i][1] * p.scale, acc[i][2] * p.scale, acc[i][3] * p.scale);
       }
     };
@@ -113,46 +136,67 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
       __syncthreads();  // y, z of the round before have been read
       load_rows<D>(s.y, y + (long long)g * op.yh, op.yt, pos, m, it.n, rev);
       load_rows<V>(s.z, z + (long long)g * op.yh, op.yt, pos, m, it.n, rev);
+      if (!STATES && op.gy == 1) load_rows<D>(s.x, x, op.xt, pos, m, it.n, rev);
       __syncthreads();
       if (!STATES) {
         if (op.gy > 1) {
           intra();
         } else {
           for (int k = 0; k < op.gx; ++k) {
-            __syncthreads();
-            load_rows<D>(s.x, x + (long long)k * op.xh, op.xt, pos, m, it.n, rev);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+            if (k > 0) {
+              __syncthreads();
+              load_rows<D>(s.x, x + (long long)k * op.xh, op.xt, pos, m, it.n, rev);
+              __syncthreads();
+            }
             inter();
             intra();
             store(k);
           }
         }
-        __syncthreads();  // the state has been read
+        __syncthreads();  // the state and z have been read
       }
+      for (int e = tid * 4; e < m * V; e += NT * 4) {  // z weighted with its distance to the chunk's end
+        float4& v = *reinterpret_cast<float4*>(&s.z[e / V][e % V]);
+        const float w = s.pw[m - 1 - e / V];
+        v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+      }
+      __syncthreads();
+      const float keep = g == 0 ? s.pw[m] : 1.f;
+      float a[D / 64][4][4];  // state rows r0 + 64 k ..
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        float a[4];
-        const float keep = g == 0 ? s.pw[m] : 1.f;
+      for (int k = 0; k < D / 64; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = s.s[r + 16 * k][c4 + j] * keep;
-        for (int j = 0; j < m; ++j) {
-          const float w = s.y[j][r + 16 * k] * s.pw[m - 1 - j];
-          const float4 b = *reinterpret_cast<const float4*>(&s.z[j][c4]);
-          a[0] += w * b.x, a[1] += w * b.y, a[2] += w * b.z, a[3] += w * b.w;
+        for (int i = 0; i < 4; ++i) {
+          get4(&s.s[64 * k + r0 + i][c0], a[k][i]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[k][i][j] *= keep;
         }
+#pragma unroll 4
+      for (int t = 0; t < C; ++t) {  // (rows behind m are zeros)
+        float b[4];
+        get4(&s.z[t][c0], b);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s.s[r + 16 * k][c4 + j] = a[j];
+        for (int k = 0; k < D / 64; ++k) {
+          float w[4];
+          get4(&s.y[t][64 * k + r0], w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[k][i][j] += w[i] * b[j];
+        }
       }
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(&s.s[64 * k + r0 + i][c0]) = make_float4(a[k][i][0], a[k][i][1], a[k][i][2], a[k][i][3]);
     }
     if (!STATES && op.gy > 1) store(0);
   }
   __syncthreads();
   float* to = STATES ? part : !split && p.update ? own : nullptr;
   if (to)
-    for (int e = tid; e < D * V; e += NT) to[(size_t)(e / V) * D + e % V] = s.s[e / V][e % V];
+    for (int e = tid * 4; e < D * V; e += NT * 4)
+      *reinterpret_cast<float4*>(to + (size_t)(e / V) * D + e % V) = *reinterpret_cast<const float4*>(&s.s[e / V][e % V]);
 }
 
 template <int D, bool STATES> cudaError_t launch(const LinArgs& p, cudaStream_t st) {

@@ -85,29 +85,30 @@ cudaError_t launch_linear_copy(float* state, int* status, int slots, size_t elem
 }
 
 // Tokens per segment, a multiple of the chunk: as many segments as let the blocks' waves end evenly, where a call with
-// several pays for their states first (measured: about 0.6 of the walk itself, and the launches).
-static int choose_seg(int seqs, int len, int units) {
-  constexpr int kBlocks = 2 * 152;
-  const int chunks = (len + kLinChunk - 1) / kLinChunk;
+// several pays for their states first (`again` of the walk itself, and the launches and the joining, in chunks).
+static int choose_seg(int seqs, int len, int units, int chunk, int blocks, double again, double launches) {
+  const int chunks = (len + chunk - 1) / chunk;
   int best = chunks;
   double least = 0;
   for (int c = chunks; c >= 1; --c) {  // chunks of a segment
     const int n = (chunks + c - 1) / c;
     if (n > 1 && (chunks + n - 1) / n != c) continue;  // (fewer chunks make as many segments)
-    const double waves = (double)(((long long)seqs * n * units + kBlocks - 1) / kBlocks);
-    const double cost = waves * c * (n > 1 ? 1.6 : 1.0) + (n > 1 ? 4.0 + 0.05 * n : 0.0);
+    const double waves = (double)(((long long)seqs * n * units + blocks - 1) / blocks);
+    const double cost = waves * c * (n > 1 ? 1 + again : 1.0) + (n > 1 ? launches + 0.05 * n : 0.0);
     if (c == chunks || cost < least) {
       least = cost;
       best = c;
     }
   }
-  return best * kLinChunk;
+  return best * chunk;
 }
 
-void lin_plan(LinArgs& p) {
+void lin_plan(LinArgs& p, bool bf16) {
   const int len = p.packed ? p.max_new : p.L;
   const int seqs = p.packed ? (p.total + p.max_new - 1) / p.max_new : p.seqs;
-  p.seg = choose_seg(seqs, len, p.heads * (p.D / 64) * p.ops);
+  const int units = p.heads * (p.D / 64) * p.ops;
+  p.seg = bf16 ? choose_seg(seqs, len, units, kLinChunk, 2 * 152, 0.6, 4.0)
+               : choose_seg(seqs, len, units, kLinChunkF32, (p.D == 64 ? 2 : 1) * 152, 0.35, 1.5);
   if (!p.packed) {
     p.max_new = p.L;
     p.items = p.seqs * ((p.L + p.seg - 1) / p.seg);

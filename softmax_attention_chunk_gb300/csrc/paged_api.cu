@@ -145,8 +145,8 @@ PATH_API int path_pages_plan(const path_paged_cache_t* cache, const int* n_new, 
   const int rc = check_pages_call(cache, ws, ws_bytes);
   if (rc != PATH_OK) return rc;
   if (tokens < 0 || (n_new && !aligned(n_new, 4)) || !aligned(q_start, 4)) return PATH_ERR_INVALID_ARG;
-  if ((from_start == nullptr) != (source == nullptr) || (from_start && !aligned(from_start, 4))) return PATH_ERR_INVALID_ARG;
-  if (tokens > 0 && (!aligned(slot, 4) || !aligned(position, 4) || !aligned(k_row, 4) || !aligned(v_row, 4) || (source && !aligned(source, 4))))
+  if (from_start && !aligned(from_start, 4)) return PATH_ERR_INVALID_ARG;
+  if (tokens > 0 && ((from_start == nullptr) != (source == nullptr) || !aligned(slot, 4) || !aligned(position, 4) || !aligned(k_row, 4) || !aligned(v_row, 4) || (source && !aligned(source, 4))))
     return PATH_ERR_INVALID_ARG;
   if (tokens > (1 << 22)) return PATH_ERR_UNSUPPORTED;
   return cuda_status(launch_pages_plan(*cache, n_new, from_start, tokens, q_start, slot, position, k_row, v_row, source, (char*)ws,

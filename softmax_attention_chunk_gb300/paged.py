@@ -122,6 +122,8 @@ class PagedCache:
         self._pages_bytes = pa.path_pages_workspace_size(self.c)
         if self._pages_bytes == 0:
             raise ValueError("unsupported cache (head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; sizes in range)")
+        # (one for all page calls: calls that change a cache are ordered)
+        self._pages_ws = torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
 
     # ---- attention ----
     def extend(self, q, k, v, w, beta, log_f=None, q_start=None, max_new=None, scale=1.0, window=0, sinks=0, ws=None,
@@ -214,12 +216,12 @@ class PagedCache:
         if not 0 <= tokens <= 1 << 22:
             raise ValueError(f"tokens must be in 0 .. {1 << 22}, got {tokens}")
         count = 4 if from_start is None else 5
-        rows = torch.empty(self.slots + 1 + count * tokens, dtype=torch.int32, device=self.device)
-        parts = rows.split([self.slots + 1] + [tokens] * count)  # q_start, then the maps
-        start = rows.data_ptr()
-        at = [start + 4 * (self.slots + 1 + i * tokens) for i in range(count)]
-        self._pages("plan", pa._p(n_new), pa._p(from_start), tokens, start, *at, *([None] if from_start is None else []))
-        return StepPlan(*parts, *([None] if from_start is None else []))
+        start = torch.empty(self.slots + 1, dtype=torch.int32, device=self.device)
+        maps = torch.empty((count, tokens), dtype=torch.int32, device=self.device)
+        at, row = maps.data_ptr(), 4 * tokens
+        self._pages("plan", pa._p(n_new), pa._p(from_start), tokens, start.data_ptr(), at, at + row, at + 2 * row, at + 3 * row,
+                    None if from_start is None else at + 4 * row)
+        return StepPlan(start, *maps.unbind(0)) if count == 5 else StepPlan(start, *maps.unbind(0), None)
 
     def verify(self, target, tokens, uniform, draft=None, q_start=None, max_new=None):
         """(keep, next), int32 [slots]: how many of each slot's packed tokens stay, the first (known) one among them, and
@@ -300,8 +302,7 @@ class PagedCache:
 
     # ---- helpers ----
     def _pages(self, name, *args):
-        ws = torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
-        self._call(getattr(pa, "path_pages_" + name), *args, ws.data_ptr(), ws.numel())
+        self._call(getattr(pa, "path_pages_" + name), *args, self._pages_ws.data_ptr(), self._pages_bytes)
 
     def _call(self, fn, *args):
         """fn(cache, *args, stream) on the current stream of the cache's device; raises on a status."""
