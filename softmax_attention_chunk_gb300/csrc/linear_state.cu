@@ -106,9 +106,9 @@ static int choose_seg(int seqs, int len, int units, int chunk, int blocks, doubl
 void lin_plan(LinArgs& p, bool bf16) {
   const int len = p.packed ? p.max_new : p.L;
   const int seqs = p.packed ? (p.total + p.max_new - 1) / p.max_new : p.seqs;
-  const int units = p.heads * (p.D / 64) * p.ops;
-  p.seg = bf16 ? choose_seg(seqs, len, units, kLinChunk, 2 * 152, 0.6, 4.0)
-               : choose_seg(seqs, len, units, kLinChunkF32, (p.D == 64 ? 2 : 1) * 152, 0.35, 1.5);
+  const int units = p.heads * p.ops, blocks = (p.D == 64 ? 2 : 1) * 152;
+  p.seg = bf16 ? choose_seg(seqs, len, units, kLinChunk, blocks, 0.6, 4.0)
+               : choose_seg(seqs, len, units * (p.D / 64), kLinChunkF32, blocks, 0.35, 1.5);
   if (!p.packed) {
     p.max_new = p.L;
     p.items = p.seqs * ((p.L + p.seg - 1) / p.seg);
