@@ -1,16 +1,16 @@
 // Linear attention on the tensor cores (bf16): the walk of linear.h in chunks of 128 tokens, one block per key head and segment.
 // Of a chunk, with r the row and m the rows that are tokens,
 //   S = X Y^T,  O = X State (tcgen05),  P = S masked and weighted with g^(distance), O scaled by g^(distance to the state),
-//   O += P Z,  Delta^T = Z'^T Y, Z' = Z weighted with g^(distance to the chunk's end),  State = g^m State + Delta.
-// State is float32 in registers, transposed (a thread holds a column of it); the operand of the next chunk is its copy as two
-// bf16 numbers.  P goes back to tensor memory over S.
+//   O += P Z,  Delta^T = Z^T Y', Y' = Y weighted with g^(distance to the chunk's end),  State = g^m State + Delta.
+// State is float32 in registers, transposed (a thread holds a part of a column); the operand of the next chunk is its copy as
+// two bf16 numbers.  P goes back to tensor memory over S, Y' to shared memory over Y.
 //
 // One warp loads (TMA) and issues every product, the others (a row and 32 columns of O per thread) do the rest; they meet at
-// mbarriers only.  Of the chain from chunk to chunk (O needs State, State needs the chunk before it) only the products with
-// State, O's scaling and P Z stay on it: S of the next chunk is issued as soon as P has been read, Delta beside S.
+// mbarriers only.  S of the next chunk is issued as soon as P has been read, so that the chain from chunk to chunk is P, Y',
+// Delta, State and the product with it.
 //
-// Roundings beside the output's: P and Z' to bf16, the operands' type (relative 2^-8; what reaches an output is the sum of
-// independent ones).  Where the state is an output itself (serving) Z' is the sum of three bf16 numbers, as exact as float32.
+// Roundings beside the output's: P and Y' to bf16, the operands' type (relative 2^-8; what reaches an output is the sum of
+// independent ones).  Where the state is an output itself (serving) Y' is the sum of three bf16 numbers, as exact as float32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -43,22 +43,21 @@ template <int D> struct Shape {
   static constexpr int COL_D = COL_O + D, COLS = D == 64 ? 256 : 512;
 };
 template <int D, int PARTS> struct Smem {
-  // Buffers of y and of z: what the block's share of 227 KB leaves.  The second part of Z' takes x's place once x has been
-  // read, the third has its own.
-  static constexpr int X = D / 64, NY = D == 64 && PARTS == 1 ? 2 : 1, NZ = D == 64 || PARTS == 1 ? 2 : 1;
-  uint8_t x[X][TILE], y[NY][X][TILE], z[NZ][X][TILE];
-  uint8_t zs[PARTS == 3 ? 2 : 1][X][TILE];  // Z'
+  // Buffers: what the block's share of 227 KB holds.  The second part of Y' takes x's place once x has been read, the third has
+  // its own.
+  static constexpr int X = D / 64, NX = PARTS == 1 ? 2 : 1, NY = 2, NZ = D == 64 ? 2 : 1, NE = PARTS == 3 ? 1 : 0;
+  uint8_t x[NX][X][TILE], y[NY][X][TILE], z[NZ + NE][X][TILE];
   uint8_t sb[2][X][D * 128];                // the state, rows of D columns: rounded, and what that leaves
   float pw[Z0 + C + 8];                     // 0 .., then g^n
   alignas(16) float colw[32];               // g^n of a 32-column block's columns
-  uint64_t full_x, full_y[NY], full_z[NZ], clean, s_full, o_full, d_full, c_full, zs_full, p_full, done;
+  uint64_t full_x[NX], full_y[NY], full_z[NZ], clean, s_full, o_full, d_full, c_full, w_full, p_full, done;
   uint32_t tmem_base;
 };
 
 __device__ __forceinline__ uint64_t f2_bits(uint32_t a, uint32_t b) { return (uint64_t)b << 32 | a; }
 __device__ __forceinline__ uint32_t pack_pair(uint64_t v) { return pack_bf16(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))); }
 // 32 bytes of global memory, aligned to them or (wide false) to 16.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wide) {
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
                  "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -69,23 +68,37 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8], bool wi
   }
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-// Issued by one elected lane of a converged warp.
-__device__ __forceinline__ void mma_ss_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Four products in a row, of operands AS and BS (16-byte units) apart, issued by one elected lane of a converged warp; the
+// first adds to D where accumulate is set.
+template <int AS, int BS> __device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, %5;\n\tadd.s64 b1, %2, %6;\n\t"
+      "add.s64 a2, %1, 2 * %5;\n\tadd.s64 b2, %2, 2 * %6;\n\t"
+      "add.s64 a3, %1, 3 * %5;\n\tadd.s64 b3, %2, 3 * %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(AS), "n"(BS)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts_elect(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The same with A in tensor memory, at a0 .. a3.
+template <int BS> __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 b1, b2, b3;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 b1, %5, %8;\n\tadd.s64 b2, %5, 2 * %8;\n\tadd.s64 b3, %5, 3 * %8;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %6, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], b1, %6, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], b2, %6, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], b3, %6, t;\n\t}" ::"r"(d),
+      "r"(a0), "r"(a1), "r"(a2), "r"(a3), "l"(b), "r"(idesc), "r"(accumulate), "n"(BS)
       : "memory");
 }
 __device__ __forceinline__ void commit_elect(uint64_t* bar) {
@@ -98,9 +111,9 @@ __device__ __forceinline__ void commit_elect(uint64_t* bar) {
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 16 bytes of Z (8 columns of a row), weighted, as a sum of PARTS bf16 numbers.
-template <int PARTS> __device__ __forceinline__ void weighted(uint4 z, float w, uint4 (&out)[PARTS]) {
-  const uint32_t in[4] = {z.x, z.y, z.z, z.w};
+// 16 bytes of Y (8 columns of a row), weighted, as a sum of PARTS bf16 numbers.
+template <int PARTS> __device__ __forceinline__ void weighted(uint4 y, float w, uint4 (&out)[PARTS]) {
+  const uint32_t in[4] = {y.x, y.y, y.z, y.w};
   uint32_t o[PARTS][4];
   const uint64_t ww = f2(w, w), minus = f2(-1.f, -1.f);
 #pragma unroll
@@ -123,7 +136,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   using Sh = Shape<D>;
   using Sm = Smem<D, PARTS>;
-  constexpr int X = Sh::X, NY = Sm::NY, NZ = Sm::NZ, NCT = 32 * Sh::WARPS, COL_D = Sh::COL_D;
+  constexpr int X = Sh::X, NX = Sm::NX, NY = Sm::NY, NZ = Sm::NZ, NCT = 32 * Sh::WARPS, COL_D = Sh::COL_D;
   constexpr int NS = D == 64 ? 16 : 32;       // state elements of a thread
   constexpr int SW = C / Sh::CG, SQ = SW / 32;  // columns of S of a warp
   Sm& s = *reinterpret_cast<Sm*>(smem_raw);
@@ -152,7 +165,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   auto ragged = [&](int k) { return p.packed && rows_of(k) < C; };  // (the last chunk of a walk onwards)
 
   if (tid == 0) {
-    mbar_init(&s.full_x, 1);
+    for (int i = 0; i < NX; ++i) mbar_init(&s.full_x[i], 1);
     for (int i = 0; i < NY; ++i) mbar_init(&s.full_y[i], 1);
     for (int i = 0; i < NZ; ++i) mbar_init(&s.full_z[i], 1);
     mbar_init(&s.s_full, 1);
@@ -160,7 +173,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     mbar_init(&s.d_full, 1);
     mbar_init(&s.c_full, 1);
     mbar_init(&s.clean, Sh::WARPS);
-    mbar_init(&s.zs_full, Sh::WARPS);
+    mbar_init(&s.w_full, Sh::WARPS);
     mbar_init(&s.p_full, Sh::WARPS);
     mbar_init(&s.done, Sh::WARPS);
     fence_barrier_init();
@@ -223,7 +236,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     int kx = 0, hx = 0, nx = 0, ky = 0, hy = 0, ny = 0, kz = 0, hz = 0, nz = 0;  // (chunk, head, number) of the next load
     auto next_x = [&]() {
       if (kx >= count) return;
-      load(s.x, &maps.x[oi], &s.full_x, kx, px + hx);
+      load(s.x[nx % NX], &maps.x[oi], &s.full_x[nx % NX], kx, px + hx);
       ++nx;
       if (++hx >= gx) hx = 0, ++kx;
     };
@@ -242,107 +255,90 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     next_y();
     if (!STATES) next_x();
     next_z();
-    if (NY > 1) next_y();
+    next_y();
+    if (!STATES && NX > 1) next_x();
     if (NZ > 1) next_z();
     const uint32_t id_s = idesc_bf16(C, C, 0, 0), id_x = idesc_bf16(C, D, 0, 0), id_o = idesc_bf16(C, D, 0, 1), id_d = idesc_bf16(D, D, 1, 1);
     const uint64_t kd = sdesc_sw128(0, 1024, 16), md = sdesc_sw128(0, 1024, TILE);
     const uint32_t tbu = uniform(tb), base = uniform(smem_u32(smem_raw) >> 4);
     auto at16 = [&](const void* a) { return base + (uint32_t)(((const uint8_t*)a - smem_raw) >> 4); };
     auto buffer = [&](const void* first, int i) { return at16(first) + uniform(i * (X * TILE / 16)); };
-    // S of the step with y number yn: over P of the step before, which has been read
-    auto issue_s = [&](int yn) {
-      const uint32_t a_x = at16(s.x), a_y = buffer(s.y, yn % NY);
-#pragma unroll
-      for (int j = 0; j < X; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_ss_elect(tbu + COL_S, kd + (a_x + j * (TILE / 16) + 2u * e), kd + (a_y + j * (TILE / 16) + 2u * e), id_s, (j | e) ? 1u : 0u);
-      commit_elect(&s.s_full);
-    };
-    auto issue_delta = [&](int yn, uint32_t accumulate) {
-      const uint32_t a_y = buffer(s.y, yn % NY);
-#pragma unroll
-      for (int t = 0; t < PARTS; ++t) {
-        const uint32_t a_w = at16(t == 0 ? s.zs[0] : t == 1 ? s.x : s.zs[PARTS == 3 ? 1 : 0]);
-#pragma unroll
-        for (int k = 0; k < C / 16; ++k)
-          mma_ss_elect(tbu + COL_D, md + (a_w + 128u * k), md + (a_y + 128u * k), id_d, (t | k) ? 1u : accumulate);
-      }
-      commit_elect(&s.d_full);
-    };
-    int g = 0, k = 0, yn = 0, xn = 0, un = 0, in = 0;  // head, chunk; numbers of y (and z) and x; of deltas; of products with the state
-    auto operands = [&](int k, int xn, int yn) {       // of a step's S
+    int g = 0, k = 0, yn = 0, xn = 0, un = 0;  // head, chunk; numbers of y (and z) and x; of deltas
+    auto operands = [&]() {
       wait(&s.full_y[yn % NY], yn / NY, 17);
-      if (!STATES) wait(&s.full_x, xn, 18);
+      if (STATES) wait(&s.full_z[yn % NZ], yn / NZ, 25);
+      else wait(&s.full_x[xn % NX], xn / NX, 18);
       if (ragged(k)) wait(&s.clean, 0, 19);
       tc_fence_after();
     };
-    operands(0, 0, 0);
-    if (!STATES && ok) issue_s(0);
+    auto issue_s = [&]() {  // over P of the step before, which has been read
+      const uint32_t a_x = buffer(s.x, xn % NX), a_y = buffer(s.y, yn % NY);
+#pragma unroll
+      for (int j = 0; j < X; ++j) mma4_ss<2, 2>(tbu + COL_S, kd + (a_x + j * (TILE / 16)), kd + (a_y + j * (TILE / 16)), id_s, j ? 1u : 0u);
+      commit_elect(&s.s_full);
+    };
+    auto issue_delta = [&](uint32_t accumulate) {
+      const uint32_t a_z = buffer(s.z, yn % NZ);
+#pragma unroll
+      for (int t = 0; t < PARTS; ++t) {
+        const uint32_t a_w = t == 0 ? buffer(s.y, yn % NY) : at16(t == 1 ? s.x[0] : s.z[NZ]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) mma4_ss<128, 128>(tbu + COL_D, md + (a_z + 512u * k), md + (a_w + 512u * k), id_d, (t | k) ? 1u : accumulate);
+      }
+      commit_elect(&s.d_full);
+    };
+    operands();
+    if (!STATES && ok) issue_s();
     for (int i = 0; i < steps && ok; ++i) {
-      const bool fresh = gy > 1 || g == 0, last = g == G - 1;
+      const bool last = g == G - 1, update = gy > 1 || last;
       const bool old = from || k > 0;  // there is a state before the chunk
-      const bool inter = old && (gx > 1 || g == 0);
-      if constexpr (STATES) {
-        if (i > 0) operands(k, 0, yn);
-        if (!wait(&s.zs_full, un, 20)) break;
-        tc_fence_after();
-        issue_delta(yn, uniform(g > 0 ? 1u : 0u));
-        next_z();
-        if (!wait(&s.d_full, un, 21)) break;
-        ++un;
-        next_y();
-      } else {
-        if (inter) {
-          if (i > 0 && !wait(&s.done, i - 1, 22)) break;
+      const uint32_t more = uniform(gy > 1 && g > 0 ? 1u : 0u);
+      if constexpr (!STATES) {
+        if (old && (gx > 1 || g == 0)) {
+          if (i > 0 && !wait(&s.done, i - 1, 20)) break;
           tc_fence_after();
-          const uint32_t a_x = at16(s.x);
+          const uint32_t a_x = buffer(s.x, xn % NX);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int j = 0; j < X; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                mma_ss_elect(tbu + COL_O, kd + (a_x + j * (TILE / 16) + 2u * e), kd + (at16(s.sb[t][j]) + 2u * e), id_x, (t | j | e) ? 1u : 0u);
+            for (int j = 0; j < X; ++j) mma4_ss<2, 2>(tbu + COL_O, kd + (a_x + j * (TILE / 16)), kd + at16(s.sb[t][j]), id_x, (t | j) ? 1u : 0u);
           commit_elect(&s.o_full);
         }
-        if (fresh) {
-          if (!wait(&s.zs_full, un, 23)) break;
-          tc_fence_after();
-          issue_delta(yn, uniform(gy > 1 && g > 0 ? 1u : 0u));
-        }
-        if (inter) {
-          if (!wait(&s.o_full, in, 24)) break;
-          ++in;
-        } else if (!wait(&s.s_full, i, 25)) {
-          break;
-        }
-        const bool spent = gx > 1 || last;  // x has been read
-        if (spent && !(PARTS > 1 && fresh)) next_x();
-        if (!wait(&s.p_full, i, 26)) break;
+        if (!wait(&s.full_z[yn % NZ], yn / NZ, 25) || !wait(&s.p_full, i, 21)) break;
         tc_fence_after();
-        const uint32_t a_z = buffer(s.z, yn % NZ), first = uniform(old || (gy > 1 && g > 0) ? 1u : 0u);
+        const uint32_t a_z = buffer(s.z, yn % NZ), first = uniform(old ? 1u : 0u) | more;
+        auto at_p = [&](int e) { return tbu + COL_S + 16 * e / SW * SW + 16 * e % SW / 2; };  // of 16 tokens
 #pragma unroll
-        for (int e = 0; e < C / 16; ++e)
-          mma_ts_elect(tbu + COL_O, tbu + COL_S + 16 * e / SW * SW + 16 * e % SW / 2, md + (a_z + 128u * e), id_o, e ? 1u : first);
+        for (int e = 0; e < 8; e += 4)
+          mma4_ts<128>(tbu + COL_O, at_p(e), at_p(e + 1), at_p(e + 2), at_p(e + 3), md + (a_z + 128u * e), id_o, e ? 1u : first);
         commit_elect(&s.c_full);
-        if (fresh) {
-          if (!wait(&s.d_full, un, 27)) break;
-          ++un;
-          if (PARTS > 1 && spent) next_x();
-        }
-        if (gy > 1 || last) next_y();
-        if (!wait(&s.c_full, i, 28)) break;
-        if (gy > 1 || last) next_z();
+        if ((gx > 1 || last) && !(PARTS > 1 && update)) next_x();  // (P waits for the products with x)
       }
+      if (update) {
+        if (!wait(&s.w_full, un, 22)) break;
+        tc_fence_after();
+        issue_delta(more);
+      }
+      auto spent = [&]() {  // y and z have been read
+        if (!update) return;
+        if (!wait(&s.d_full, un, 23)) return;
+        ++un;
+        if (!STATES && PARTS > 1) next_x();
+        next_y();
+        next_z();
+      };
+      // (a cache's tokens: the rows behind a sequence's last are cleared first, which takes all of the next step's operands)
+      if (PARTS > 1 || STATES) spent();
       if (gy > 1 || last) ++yn;
       if (gx > 1 || last) ++xn;
       if (last) g = 0, ++k;
       else ++g;
-      if (!STATES && i + 1 < steps) {
-        operands(k, xn, yn);
-        if (ok) issue_s(yn);
+      if (ok && i + 1 < steps) {
+        if (!STATES) wait(&s.c_full, i, 24);
+        operands();
+        if (!STATES && ok) issue_s();
       }
+      if (!(PARTS > 1 || STATES)) spent();
     }
   } else {
     // ---------------- weights, state, output ----------------
@@ -352,53 +348,27 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    int g = 0, k = 0, yn = 0, un = 0, in = 0;
+    int g = 0, k = 0, yn = 0, un = 0, dn = 0, in = 0;  // deltas begun, and those waited for; products with the state
     for (int i = 0; i < steps && ok; ++i) {
-      const int m = rows_of(k), zb = yn % NZ;
-      const bool fresh = gy > 1 || g == 0, last = g == G - 1;
-      const bool old = from || k > 0, inter = old && (gx > 1 || g == 0);
+      const int m = rows_of(k), yb = yn % NY;
+      const bool fresh = gy > 1 || g == 0, last = g == G - 1, update = gy > 1 || last;
+      const bool inter = (from || k > 0) && (gx > 1 || g == 0);
       if (fresh && ragged(k)) {  // rows of the next sequence: they may hold anything
-        wait(&s.full_y[yn % NY], yn / NY, 32);
-        if (!wait(&s.full_z[zb], yn / NZ, 33)) break;
+        wait(&s.full_y[yb], yn / NY, 32);
+        if (!wait(&s.full_z[yn % NZ], yn / NZ, 33)) break;
         for (int e = tid; e < (C - m) * 8 * X; e += NCT) {
           const uint32_t at = e / ((C - m) * 8) * TILE + (m * 8 + e % ((C - m) * 8)) * 16;
-          *reinterpret_cast<uint4*>(&s.y[yn % NY][0][0] + at) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(&s.z[zb][0][0] + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(&s.y[yb][0][0] + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(&s.z[yn % NZ][0][0] + at) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         arrive(&s.clean);
       }
-      auto weigh = [&]() {  // Z' (weights of rows behind m: of zeros)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int e = j * NCT + tid, row = e / 8 % C;
-          const uint32_t at = e / (8 * C) * TILE + (e % (8 * C)) * 16;
-          uint4 out[PARTS], z = *reinterpret_cast<const uint4*>(&s.z[zb][0][0] + at);
-          if (row >= m) z = make_uint4(0, 0, 0, 0);  // (another warp may be clearing it)
-          weighted<PARTS>(z, s.pw[Z0 + (rev ? row : max(m - 1 - row, 0))], out);
-          *reinterpret_cast<uint4*>(&s.zs[0][0][0] + at) = out[0];
-          if constexpr (PARTS > 1) {
-            *reinterpret_cast<uint4*>(&s.x[0][0] + at) = out[1];
-            *reinterpret_cast<uint4*>(&s.zs[1][0][0] + at) = out[2];
-          }
-        }
-        fence_proxy_async_smem();
-        arrive(&s.zs_full);
-      };
-      if ((STATES || PARTS == 1) && fresh) {
-        if (!wait(&s.full_z[zb], yn / NZ, 34)) break;
-        weigh();
-      }
+      uint32_t a[32];
       if constexpr (!STATES) {
-        if (!wait(&s.s_full, i, 35)) break;
-        if (PARTS > 1 && fresh) {  // (into x's place)
-          if (inter && !wait(&s.o_full, in, 36)) break;
-          if (!wait(&s.full_z[zb], yn / NZ, 37)) break;
-          weigh();
-        }
+        if (!wait(&s.s_full, i, 34)) break;
         tc_fence_after();
         // P over S: a warp's columns become half as many of packed pairs, in the place of their first half
-        uint32_t a[32];
 #pragma unroll
         for (int q = 0; q < SQ; ++q) {
           const int jb = SQ * cg + q;
@@ -433,7 +403,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
           tmem_st16(tb + lane_off + COL_S + SW * cg + 16 * q, b);
         }
         if (inter) {  // what lies before the chunk, weighted
-          if (!wait(&s.o_full, in, 38)) break;
+          if (!wait(&s.o_full, in, 35)) break;
           ++in;
           tc_fence_after();
           tmem_ld32(tb + lane_off + COL_O + 32 * cg, a);
@@ -451,49 +421,61 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
         tc_fence_before();
         arrive(&s.p_full);
       }
-      if (fresh || last) {
-        if (!wait(&s.d_full, fresh ? un : un - 1, 39)) break;
-        if (fresh) ++un;
+      if (update) {  // Y' over Y, whose products have been made; rows behind m become 0
+        if (STATES && !wait(&s.full_y[yb], yn / NY, 36)) break;
+        if (dn < un && !wait(&s.d_full, dn++, 37)) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = j * NCT + tid, row = e / 8 % C;
+          const uint32_t at = e / (8 * C) * TILE + (e % (8 * C)) * 16;
+          uint8_t* y = &s.y[yb][0][0] + at;
+          uint4 out[PARTS], in = *reinterpret_cast<const uint4*>(y);
+          if (row >= m) in = make_uint4(0, 0, 0, 0);
+          weighted<PARTS>(in, s.pw[Z0 + (rev ? row : max(m - 1 - row, 0))], out);
+          *reinterpret_cast<uint4*>(y) = out[0];
+          if constexpr (PARTS > 1) {
+            *reinterpret_cast<uint4*>(&s.x[0][0][0] + at) = out[1];
+            *reinterpret_cast<uint4*>(&s.z[NZ][0][0] + at) = out[2];
+          }
+        }
+        fence_proxy_async_smem();
+        arrive(&s.w_full);
+        ++un;
       }
-      if (last) {
+      const bool emit = !STATES && (gx > 1 || last);
+      uint32_t out[16];
+      if (emit) {
+        if (!wait(&s.c_full, i, 38)) break;
         tc_fence_after();
-        const float keep = s.pw[Z0 + m];
-        uint32_t a[NS];
-        if constexpr (D == 64) tmem_ld16x2_16(tb + lane_off + COL_D + 16 * cg, a);
-        else tmem_ld32(tb + lane_off + COL_D + 32 * cg, a);
+        tmem_ld32(tb + lane_off + COL_O + 32 * cg, a);
+        const uint64_t scale = f2(p.scale, p.scale);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < NS; ++e) st[e] = st[e] * keep + __uint_as_float(a[e]);
+        for (int j = 0; j < 16; ++j) out[j] = pack_pair(f2_mul(f2_bits(a[2 * j], a[2 * j + 1]), scale));
+      }
+      if (last) {
+        while (dn < un && wait(&s.d_full, dn, 39)) ++dn;
+        if (!ok) break;
+        tc_fence_after();
+        const float keep = s.pw[Z0 + m];
+        uint32_t b[NS];
+        if constexpr (D == 64) tmem_ld16x2_16(tb + lane_off + COL_D + 16 * cg, b);
+        else tmem_ld32(tb + lane_off + COL_D + 32 * cg, b);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < NS; ++e) st[e] = st[e] * keep + __uint_as_float(b[e]);
         if (!STATES && k + 1 < count) {  // (the last product with the old one is over: P waited for it)
           put_state();
           fence_proxy_async_smem();
         }
-        tc_fence_before();
       }
-      if constexpr (!STATES) {
-        if (gx > 1 || last) {
-          if (!wait(&s.c_full, i, 40)) break;
-          tc_fence_after();
-          uint32_t a[32];
-          tmem_ld32(tb + lane_off + COL_O + 32 * cg, a);
-          __nv_bfloat16* o = (__nv_bfloat16*)op.o + (p.packed ? 0 : it.seq * op.xb) + ((long long)(p.packed ? it.q0 : 0) + chunk_of(k) * C + r) * op.xt +
-                             (long long)(h * gx + (gx > 1 ? g : 0)) * op.xh + 32 * cg;
-          const bool wide = (reinterpret_cast<uintptr_t>(op.o) & 31) == 0;
-          const uint64_t scale = f2(p.scale, p.scale);
-          tmem_ld_wait();
-          tc_fence_before();
-          arrive(&s.done);
-          if (r < m)
-#pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              uint32_t w[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) w[j] = pack_pair(f2_mul(f2_bits(a[e + 2 * j], a[e + 2 * j + 1]), scale));
-              store32(o + e, w, wide);
-            }
-        } else {
-          arrive(&s.done);
-        }
+      tc_fence_before();
+      if (!STATES) arrive(&s.done);
+      if (emit && r < m) {
+        __nv_bfloat16* o = (__nv_bfloat16*)op.o + (p.packed ? 0 : it.seq * op.xb) + ((long long)(p.packed ? it.q0 : 0) + chunk_of(k) * C + r) * op.xt +
+                           (long long)(h * gx + (gx > 1 ? g : 0)) * op.xh + 32 * cg;
+        store32(o, out, (reinterpret_cast<uintptr_t>(op.o) & 31) == 0);
+        store32(o + 16, out + 8, (reinterpret_cast<uintptr_t>(op.o) & 31) == 0);
       }
       if (gy > 1 || last) ++yn;
       if (last) g = 0, ++k;
@@ -508,7 +490,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     if (p.status) paged_error(p.status, *reinterpret_cast<volatile int*>(err));
     // after a failure: no copy may land in shared memory once the block has gone (bounded waits on whatever is in flight)
     for (int b = 0; b < 2; ++b) {
-      mbar_wait_ns(&s.full_x, b, nullptr, 0, 1000000ull);
+      for (int j = 0; j < NX; ++j) mbar_wait_ns(&s.full_x[j], b, nullptr, 0, 1000000ull);
       for (int j = 0; j < NY; ++j) mbar_wait_ns(&s.full_y[j], b, nullptr, 0, 1000000ull);
       for (int j = 0; j < NZ; ++j) mbar_wait_ns(&s.full_z[j], b, nullptr, 0, 1000000ull);
     }
