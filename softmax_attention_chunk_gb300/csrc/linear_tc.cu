@@ -5,9 +5,9 @@
 // State is float32 in registers, transposed (a thread holds a part of a column); the operand of the next chunk is its copy as
 // two bf16 numbers.  P goes back to tensor memory over S, Y' to shared memory over Y.
 //
-// One warp loads (TMA) and issues every product, the others (a row and 32 columns of O per thread) do the rest; they meet at
-// mbarriers only.  S of the next chunk is issued as soon as P has been read, so that the chain from chunk to chunk is P, Y',
-// Delta, State and the product with it.
+// One warp moves tiles (TMA), one issues every product, the others (a row and 32 columns of O per thread) do the rest; they meet
+// at mbarriers only.  S of the next chunk is issued as soon as P has been read; the warps whose part of P is all masked weigh Y
+// meanwhile.  The chain from chunk to chunk is P, P Z and Delta, State and the product with it.
 //
 // Roundings beside the output's: P and Y' to bf16, the operands' type (relative 2^-8; what reaches an output is the sum of
 // independent ones).  Where the state is an output itself (serving) Y' is the sum of three bf16 numbers, as exact as float32.
@@ -31,20 +31,21 @@ constexpr int COL_S = 0, COL_O = 128;   // tensor memory: S and P, O, then Delta
 constexpr int Z0 = 32;                  // zeros before g^0 in the table
 
 struct LinMaps {
-  CUtensorMap x[3], y[3], z[3];
+  CUtensorMap x[3], y[3], z[3], o[3];
 };
 
 template <int D> struct Shape {
   static constexpr int X = D / 64;          // 64-column tiles of a row block
   static constexpr int CG = D / 32;         // column groups: a warp of each to every 32 rows
-  static constexpr int WARPS = 4 * CG;      // computing warps; one more loads and issues
-  static constexpr int NT = 32 * (WARPS + 1);
+  static constexpr int WARPS = 4 * CG;      // computing warps; one more issues, one moves tiles
+  static constexpr int LIGHT = D == 64 ? 2 : 6;  // warps whose part of P is all masked
+  static constexpr int NT = 32 * (WARPS + 2);
   static constexpr int BLOCKS = D == 64 ? 2 : 1;  // to an SM
   static constexpr int COL_D = COL_O + D, COLS = D == 64 ? 256 : 512;
 };
 template <int D, int PARTS> struct Smem {
-  // Buffers: what the block's share of 227 KB holds.  The second part of Y' takes x's place once x has been read, the third has
-  // its own.
+  // Buffers: what the block's share of 227 KB holds.  O leaves through x's place once x has been read; before that the second
+  // part of Y' lies there, the third has a place of its own.
   static constexpr int X = D / 64, NX = PARTS == 1 ? 2 : 1, NY = 2, NZ = D == 64 ? 2 : 1, NE = PARTS == 3 ? 1 : 0;
   uint8_t x[NX][X][TILE], y[NY][X][TILE], z[NZ + NE][X][TILE];
   uint8_t sb[2][X][D * 128];                // the state, rows of D columns: rounded, and what that leaves
@@ -56,17 +57,6 @@ template <int D, int PARTS> struct Smem {
 
 __device__ __forceinline__ uint64_t f2_bits(uint32_t a, uint32_t b) { return (uint64_t)b << 32 | a; }
 __device__ __forceinline__ uint32_t pack_pair(uint64_t v) { return pack_bf16(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))); }
-// 32 bytes of global memory, aligned to them or (wide false) to 16.
-__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-                 "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
 // Four products in a row, of operands AS and BS (16-byte units) apart, issued by one elected lane of a converged warp; the
 // first adds to D where accumulate is set.
@@ -141,7 +131,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   constexpr int SW = C / Sh::CG, SQ = SW / 32;  // columns of S of a warp
   Sm& s = *reinterpret_cast<Sm*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, cg = warp >> 2;
-  const bool lead = warp == Sh::WARPS;
+  const bool lead = warp == Sh::WARPS, mover = warp == Sh::WARPS + 1;
+  constexpr bool ALL = STATES || PARTS > 1;  // every computing warp weighs Y
   int blk = blockIdx.x;  // (neighbouring blocks, the gradients of one head, share operands)
   const int oi = blk % p.ops;
   blk /= p.ops;
@@ -173,7 +164,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     mbar_init(&s.d_full, 1);
     mbar_init(&s.c_full, 1);
     mbar_init(&s.clean, Sh::WARPS);
-    mbar_init(&s.w_full, Sh::WARPS);
+    mbar_init(&s.w_full, ALL ? Sh::WARPS : Sh::LIGHT);
     mbar_init(&s.p_full, Sh::WARPS);
     mbar_init(&s.done, Sh::WARPS);
     fence_barrier_init();
@@ -206,7 +197,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       *reinterpret_cast<uint4*>(&s.sb[1][0][0] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   };
-  if (!lead) {
+  if (warp < Sh::WARPS) {
 #pragma unroll
     for (int e = 0; e < NS; ++e) st[e] = from ? from[(size_t)(sk + e) * D + sv] : 0.f;
     if (!STATES && from) put_state();
@@ -223,8 +214,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     return ok;
   };
 
-  if (lead) {
-    // ---------------- loads and products ----------------
+  if (mover) {
+    // ---------------- tiles in and out ----------------
     const int row0 = p.packed ? it.q0 : 0;
     const int px = (p.packed ? 0 : it.seq * p.heads * gx) + h * gx, py = (p.packed ? 0 : it.seq * p.heads * gy) + h * gy;
     auto load = [&](uint8_t (*to)[TILE], const CUtensorMap* map, uint64_t* bar, int k, int plane) {
@@ -258,6 +249,32 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     next_y();
     if (!STATES && NX > 1) next_x();
     if (NZ > 1) next_z();
+    int g = 0, k = 0, un = 0, xn = 0;
+    for (int i = 0; i < steps && ok; ++i) {
+      const bool last = g == G - 1;
+      if (gy > 1 || last) {  // y and z have been read
+        if (!wait(&s.d_full, un++, 10)) break;
+        next_y();
+        next_z();
+      }
+      if (!STATES && (gx > 1 || last)) {  // o lies in x's place
+        if (!wait(&s.done, i, 11)) break;
+        if (!ragged(k) && lane == 0)
+#pragma unroll
+          for (int j = 0; j < X; ++j) tma_store_3d(&maps.o[oi], s.x[xn % NX][j], 64 * j, row0 + chunk_of(k) * C, px + (gx > 1 ? g : 0));
+        if (lane == 0) {
+          bulk_commit();
+          bulk_wait_read0();
+        }
+        __syncwarp();
+        next_x();
+        ++xn;
+      }
+      if (last) g = 0, ++k;
+      else ++g;
+    }
+  } else if (lead) {
+    // ---------------- products ----------------
     const uint32_t id_s = idesc_bf16(C, C, 0, 0), id_x = idesc_bf16(C, D, 0, 0), id_o = idesc_bf16(C, D, 0, 1), id_d = idesc_bf16(D, D, 1, 1);
     const uint64_t kd = sdesc_sw128(0, 1024, 16), md = sdesc_sw128(0, 1024, TILE);
     const uint32_t tbu = uniform(tb), base = uniform(smem_u32(smem_raw) >> 4);
@@ -312,33 +329,23 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
         for (int e = 0; e < 8; e += 4)
           mma4_ts<128>(tbu + COL_O, at_p(e), at_p(e + 1), at_p(e + 2), at_p(e + 3), md + (a_z + 128u * e), id_o, e ? 1u : first);
         commit_elect(&s.c_full);
-        if ((gx > 1 || last) && !(PARTS > 1 && update)) next_x();  // (P waits for the products with x)
       }
       if (update) {
-        if (!wait(&s.w_full, un, 22)) break;
+        if (!wait(&s.w_full, un++, 22)) break;
         tc_fence_after();
         issue_delta(more);
       }
-      auto spent = [&]() {  // y and z have been read
-        if (!update) return;
-        if (!wait(&s.d_full, un, 23)) return;
-        ++un;
-        if (!STATES && PARTS > 1) next_x();
-        next_y();
-        next_z();
-      };
-      // (a cache's tokens: the rows behind a sequence's last are cleared first, which takes all of the next step's operands)
-      if (PARTS > 1 || STATES) spent();
       if (gy > 1 || last) ++yn;
       if (gx > 1 || last) ++xn;
       if (last) g = 0, ++k;
       else ++g;
-      if (ok && i + 1 < steps) {
-        if (!STATES) wait(&s.c_full, i, 24);
+      if (i + 1 < steps) {
         operands();
-        if (!STATES && ok) issue_s();
+        if (!STATES && wait(&s.c_full, i, 24)) {
+          tc_fence_after();
+          issue_s();
+        }
       }
-      if (!(PARTS > 1 || STATES)) spent();
     }
   } else {
     // ---------------- weights, state, output ----------------
@@ -348,11 +355,15 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    int g = 0, k = 0, yn = 0, un = 0, dn = 0, in = 0;  // deltas begun, and those waited for; products with the state
+    // number among the warps whose part of P is all masked, or -1
+    const int far = rev ? quad - cg * SQ - SQ + 1 : cg * SQ - quad;  // (> 0)
+    const int light = far <= 0 ? -1 : D == 64 ? (rev ? quad - 2 : quad) : rev ? (cg == 0 ? quad - 1 : cg == 1 ? quad + 1 : 5) : (quad == 0 ? cg - 1 : quad == 1 ? cg + 1 : 5);
+    int g = 0, k = 0, yn = 0, xn = 0, un = 0, dn = 0, in = 0;  // deltas begun, and those waited for; products with the state
     for (int i = 0; i < steps && ok; ++i) {
       const int m = rows_of(k), yb = yn % NY;
       const bool fresh = gy > 1 || g == 0, last = g == G - 1, update = gy > 1 || last;
       const bool inter = (from || k > 0) && (gx > 1 || g == 0);
+      if (dn < un && !wait(&s.d_full, dn++, 31)) break;  // (its phases one by one)
       if (fresh && ragged(k)) {  // rows of the next sequence: they may hold anything
         wait(&s.full_y[yb], yn / NY, 32);
         if (!wait(&s.full_z[yn % NZ], yn / NZ, 33)) break;
@@ -423,23 +434,25 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       }
       if (update) {  // Y' over Y, whose products have been made; rows behind m become 0
         if (STATES && !wait(&s.full_y[yb], yn / NY, 36)) break;
-        if (dn < un && !wait(&s.d_full, dn++, 37)) break;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int e = j * NCT + tid, row = e / 8 % C;
-          const uint32_t at = e / (8 * C) * TILE + (e % (8 * C)) * 16;
-          uint8_t* y = &s.y[yb][0][0] + at;
-          uint4 out[PARTS], in = *reinterpret_cast<const uint4*>(y);
-          if (row >= m) in = make_uint4(0, 0, 0, 0);
-          weighted<PARTS>(in, s.pw[Z0 + (rev ? row : max(m - 1 - row, 0))], out);
-          *reinterpret_cast<uint4*>(y) = out[0];
-          if constexpr (PARTS > 1) {
-            *reinterpret_cast<uint4*>(&s.x[0][0][0] + at) = out[1];
-            *reinterpret_cast<uint4*>(&s.z[NZ][0][0] + at) = out[2];
+        if (ALL || light >= 0) {
+          constexpr int STEP = 32 * (ALL ? Sh::WARPS : Sh::LIGHT);
+#pragma unroll 4
+          for (int e = ALL ? tid : 32 * light + lane; e < C * 8 * X; e += STEP) {
+            const int row = e / 8 % C;
+            const uint32_t at = e / (8 * C) * TILE + (e % (8 * C)) * 16;
+            uint8_t* y = &s.y[yb][0][0] + at;
+            uint4 w[PARTS], in = *reinterpret_cast<const uint4*>(y);
+            if (row >= m) in = make_uint4(0, 0, 0, 0);
+            weighted<PARTS>(in, s.pw[Z0 + (rev ? row : max(m - 1 - row, 0))], w);
+            *reinterpret_cast<uint4*>(y) = w[0];
+            if constexpr (PARTS > 1) {
+              *reinterpret_cast<uint4*>(&s.x[0][0][0] + at) = w[1];
+              *reinterpret_cast<uint4*>(&s.z[NZ][0][0] + at) = w[2];
+            }
           }
+          fence_proxy_async_smem();
+          arrive(&s.w_full);
         }
-        fence_proxy_async_smem();
-        arrive(&s.w_full);
         ++un;
       }
       const bool emit = !STATES && (gx > 1 || last);
@@ -454,8 +467,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
         for (int j = 0; j < 16; ++j) out[j] = pack_pair(f2_mul(f2_bits(a[2 * j], a[2 * j + 1]), scale));
       }
       if (last) {
-        while (dn < un && wait(&s.d_full, dn, 39)) ++dn;
-        if (!ok) break;
+        if (!wait(&s.d_full, dn++, 39)) break;
         tc_fence_after();
         const float keep = s.pw[Z0 + m];
         uint32_t b[NS];
@@ -469,14 +481,21 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
           fence_proxy_async_smem();
         }
       }
+      if (emit) {
+        if (!ragged(k)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(s.x[xn % NX][cg / 2] + sw128_offset(r, cg % 2 * 32 + 8 * j)) = make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
+          fence_proxy_async_smem();
+        } else if (r < m) {  // a box would reach into the next sequence
+          __nv_bfloat16* o = (__nv_bfloat16*)op.o + ((long long)it.q0 + chunk_of(k) * C + r) * op.xt + (long long)(h * gx + (gx > 1 ? g : 0)) * op.xh + 32 * cg;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(o + 8 * j) = make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
+        }
+      }
       tc_fence_before();
       if (!STATES) arrive(&s.done);
-      if (emit && r < m) {
-        __nv_bfloat16* o = (__nv_bfloat16*)op.o + (p.packed ? 0 : it.seq * op.xb) + ((long long)(p.packed ? it.q0 : 0) + chunk_of(k) * C + r) * op.xt +
-                           (long long)(h * gx + (gx > 1 ? g : 0)) * op.xh + 32 * cg;
-        store32(o, out, (reinterpret_cast<uintptr_t>(op.o) & 31) == 0);
-        store32(o + 16, out + 8, (reinterpret_cast<uintptr_t>(op.o) & 31) == 0);
-      }
+      if (gx > 1 || last) ++xn;
       if (gy > 1 || last) ++yn;
       if (last) g = 0, ++k;
       else ++g;
@@ -486,7 +505,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
 #pragma unroll
       for (int e = 0; e < NS; ++e) to[(size_t)(sk + e) * D + sv] = st[e];
   }
-  if (!ok && lead && lane == 0) {
+  if (!ok && mover && lane == 0) {
     if (p.status) paged_error(p.status, *reinterpret_cast<volatile int*>(err));
     // after a failure: no copy may land in shared memory once the block has gone (bounded waits on whatever is in flight)
     for (int b = 0; b < 2; ++b) {
@@ -504,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
 }
 
 // [planes][rows][D] bf16, `row` and `plane` elements apart, in boxes of 128 rows x 64 columns; rows behind the last read as
-// zero.
+// zero and are not written.
 bool make_map(CUtensorMap* m, const void* base, int D, long long rows, long long planes, long long row, long long plane) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
@@ -533,7 +552,7 @@ cudaError_t launch_linear_tc(const LinArgs& p, bool states, cudaStream_t st) {
     const long long rows = p.packed ? p.total : p.L, seqs = p.packed ? 1 : p.seqs;
     const long long nx = seqs * p.heads * op.gx, ny = seqs * p.heads * op.gy;
     // (planes of one sequence follow one another at the heads' distance, and so do sequences)
-    if (!make_map(&maps.x[i], op.x, p.D, rows, nx, op.xt, op.xh) ||
+    if (!make_map(&maps.x[i], op.x, p.D, rows, nx, op.xt, op.xh) || !make_map(&maps.o[i], op.o, p.D, rows, nx, op.xt, op.xh) ||
         !make_map(&maps.y[i], op.y, p.D, rows, ny, op.yt, op.yh) || !make_map(&maps.z[i], op.z, p.D, rows, ny, op.yt, op.yh))
       return cudaErrorInvalidValue;
   }
