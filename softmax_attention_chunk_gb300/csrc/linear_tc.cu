@@ -38,7 +38,7 @@ template <int D> struct Shape {
   static constexpr int X = D / 64;          // 64-column tiles of a row block
   static constexpr int CG = D / 32;         // column groups: a warp of each to every 32 rows
   static constexpr int WARPS = 4 * CG;      // computing warps; one more issues, one moves tiles
-  static constexpr int LIGHT = D == 64 ? 2 : 6;  // warps whose part of P is all masked
+  static constexpr int LIGHT = 2;           // (head dim 64) warps whose part of P is all masked
   static constexpr int NT = 32 * (WARPS + 2);
   static constexpr int BLOCKS = D == 64 ? 2 : 1;  // to an SM
   static constexpr int COL_D = COL_O + D, COLS = D == 64 ? 256 : 512;
@@ -98,9 +98,6 @@ __device__ __forceinline__ void commit_elect(uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
 // 16 bytes of Y (8 columns of a row), weighted, as a sum of PARTS bf16 numbers.
 template <int PARTS> __device__ __forceinline__ void weighted(uint4 y, float w, uint4 (&out)[PARTS]) {
   const uint32_t in[4] = {y.x, y.y, y.z, y.w};
@@ -132,7 +129,9 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   Sm& s = *reinterpret_cast<Sm*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3, cg = warp >> 2;
   const bool lead = warp == Sh::WARPS, mover = warp == Sh::WARPS + 1;
-  constexpr bool ALL = STATES || PARTS > 1;  // every computing warp weighs Y
+  // At head dim 64 the warps whose part of P is all masked weigh Y while the others make P; else every computing warp does,
+  // after P (head dim 128, 4 x 16 x 2048: forward 59 us in place of 70 with six of sixteen warps).
+  constexpr bool ALL = STATES || PARTS > 1 || D == 128;
   int blk = blockIdx.x;  // (neighbouring blocks, the gradients of one head, share operands)
   const int oi = blk % p.ops;
   blk /= p.ops;
@@ -180,16 +179,17 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   // this thread's part of the state: column sv, rows sk ..
   const int sv = D == 64 ? 16 * quad + (lane & 15) : 32 * quad + lane;
   const int sk = D == 64 ? 32 * (lane >> 4) + 16 * cg : 32 * cg;
-  float st[NS];
+  uint64_t st[NS / 2];  // pairs of floats
   auto put_state = [&]() {
+    const uint64_t minus = f2(-1.f, -1.f);
 #pragma unroll
     for (int e = 0; e < NS; e += 8) {
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = st[e + 2 * j], b = st[e + 2 * j + 1];
-        hi[j] = pack_bf16(a, b);
-        lo[j] = pack_bf16(a - lo_of(hi[j]), b - hi_of(hi[j]));
+        const uint64_t v = st[e / 2 + j];
+        hi[j] = pack_pair(v);
+        lo[j] = pack_pair(f2_fma(f2_bits(hi[j] << 16, hi[j] & 0xffff0000u), minus, v));
       }
       const int k = sk + e;
       const uint32_t at = k / 64 * (D * 128) + sw128_offset(sv, k % 64);
@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   };
   if (warp < Sh::WARPS) {
 #pragma unroll
-    for (int e = 0; e < NS; ++e) st[e] = from ? from[(size_t)(sk + e) * D + sv] : 0.f;
+    for (int e = 0; e < NS; e += 2)
+      st[e / 2] = from ? f2(from[(size_t)(sk + e) * D + sv], from[(size_t)(sk + e + 1) * D + sv]) : 0;
     if (!STATES && from) put_state();
   }
   fence_proxy_async_smem();
@@ -355,9 +356,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // number among the warps whose part of P is all masked, or -1
-    const int far = rev ? quad - cg * SQ - SQ + 1 : cg * SQ - quad;  // (> 0)
-    const int light = far <= 0 ? -1 : D == 64 ? (rev ? quad - 2 : quad) : rev ? (cg == 0 ? quad - 1 : cg == 1 ? quad + 1 : 5) : (quad == 0 ? cg - 1 : quad == 1 ? cg + 1 : 5);
+    const int light = rev ? (cg == 0 ? quad - 2 : -1) : (cg == 1 && quad < 2 ? quad : -1);  // number among them, or below 0
     int g = 0, k = 0, yn = 0, xn = 0, un = 0, dn = 0, in = 0;  // deltas begun, and those waited for; products with the state
     for (int i = 0; i < steps && ok; ++i) {
       const int m = rows_of(k), yb = yn % NY;
@@ -457,31 +456,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       }
       const bool emit = !STATES && (gx > 1 || last);
       uint32_t out[16];
-      if (emit) {
-        if (!wait(&s.c_full, i, 38)) break;
-        tc_fence_after();
-        tmem_ld32(tb + lane_off + COL_O + 32 * cg, a);
-        const uint64_t scale = f2(p.scale, p.scale);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) out[j] = pack_pair(f2_mul(f2_bits(a[2 * j], a[2 * j + 1]), scale));
-      }
-      if (last) {
-        if (!wait(&s.d_full, dn++, 39)) break;
-        tc_fence_after();
-        const float keep = s.pw[Z0 + m];
-        uint32_t b[NS];
-        if constexpr (D == 64) tmem_ld16x2_16(tb + lane_off + COL_D + 16 * cg, b);
-        else tmem_ld32(tb + lane_off + COL_D + 32 * cg, b);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < NS; ++e) st[e] = st[e] * keep + __uint_as_float(b[e]);
-        if (!STATES && k + 1 < count) {  // (the last product with the old one is over: P waited for it)
-          put_state();
-          fence_proxy_async_smem();
-        }
-      }
-      if (emit) {
+      auto put_out = [&]() {
         if (!ragged(k)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -492,7 +467,33 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
 #pragma unroll
           for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(o + 8 * j) = make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
         }
+      };
+      if (emit) {
+        if (!wait(&s.c_full, i, 38)) break;
+        tc_fence_after();
+        tmem_ld32(tb + lane_off + COL_O + 32 * cg, a);
+        const uint64_t scale = f2(p.scale, p.scale);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) out[j] = pack_pair(f2_mul(f2_bits(a[2 * j], a[2 * j + 1]), scale));
+        if (PARTS == 1) put_out();
       }
+      if (last) {
+        if (!wait(&s.d_full, dn++, 39)) break;
+        tc_fence_after();
+        const uint64_t keep = f2(s.pw[Z0 + m], s.pw[Z0 + m]);
+        uint32_t b[NS];
+        if constexpr (D == 64) tmem_ld16x2_16(tb + lane_off + COL_D + 16 * cg, b);
+        else tmem_ld32(tb + lane_off + COL_D + 32 * cg, b);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < NS; e += 2) st[e / 2] = f2_fma(st[e / 2], keep, f2_bits(b[e], b[e + 1]));
+        if (!STATES && k + 1 < count) {  // (the last product with the old one is over: P waited for it)
+          put_state();
+          fence_proxy_async_smem();
+        }
+      }
+      if (emit && PARTS > 1) put_out();  // (x's place holds a part of Y' until now)
       tc_fence_before();
       if (!STATES) arrive(&s.done);
       if (gx > 1 || last) ++xn;
@@ -503,7 +504,12 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     float* to = STATES ? part : !split && p.update ? own : nullptr;
     if (ok && to)
 #pragma unroll
-      for (int e = 0; e < NS; ++e) to[(size_t)(sk + e) * D + sv] = st[e];
+      for (int e = 0; e < NS; e += 2) {
+        float a, b;
+        f2_split(st[e / 2], a, b);
+        to[(size_t)(sk + e) * D + sv] = a;
+        to[(size_t)(sk + e + 1) * D + sv] = b;
+      }
   }
   if (!ok && mover && lane == 0) {
     if (p.status) paged_error(p.status, *reinterpret_cast<volatile int*>(err));
