@@ -26,12 +26,14 @@ struct LinOp {
   int reverse;                     // from the last token to the first
   long long xt, xh, xb;            // strides of x and o in elements: token, head, sequence
   long long yt, yh, yb;            // of y and z
+  int slot, turned;                // its states in parts, and whether they lie there transposed
 };
 
 // What the kernels of a call need, by value.
 struct LinArgs {
   LinOp op[3];
   int ops;
+  int slots, maker[3];             // states in parts: dk's are dv's transposed; the operation that makes each slot's
   int D, heads, G;                 // G: query heads per key head
   int seqs, L;                     // dense: sequences of L tokens
   const int* q_start;              // packed: slot b's tokens are q_start[b] .. q_start[b + 1] - 1; null: one each
@@ -41,7 +43,7 @@ struct LinArgs {
   const float* log_decay;          // [heads]
   float* state;                    // [seqs][heads][D][D] or null (zero): the state before, and after where update is set
   int update;
-  float* parts;                    // [ops][items][heads][D][D]: states of single segments, then those at their starts
+  float* parts;                    // [slots][items][heads][D][D]: states of single segments, then those at their starts
   int* err;                        // tensor-core kernels: first wait that gave up,
   int* status;                     // and where a cache keeps it (or null)
 };

@@ -44,6 +44,7 @@ int check_step(const path_linear_cache_t* c, const path_linear_step_t* s) {
 LinArgs dense_args(const path_linear_desc_t* d, int ops) {
   LinArgs p{};
   p.ops = ops;
+  p.slots = ops == 1 ? 1 : 2;
   p.D = d->head_dim;
   p.heads = d->heads;
   p.G = d->heads_q / d->heads;
@@ -62,7 +63,7 @@ LinOp dense_op(const path_linear_desc_t* d, const void* x, const void* y, const 
 }
 LinArgs packed_args(const path_linear_cache_t* c, const path_linear_step_t* s) {
   LinArgs p{};
-  p.ops = 1;
+  p.ops = p.slots = 1;
   p.D = c->head_dim;
   p.heads = c->heads;
   p.G = s->heads_q / c->heads;
@@ -113,10 +114,21 @@ PATH_API int path_linear_bwd(const path_linear_desc_t* desc, const void* q, cons
   if (ws_bytes < lin_ws_bytes(p)) return PATH_ERR_WORKSPACE;
   p.log_decay = log_decay;
   p.err = (int*)ws;
-  p.ops = 0;
-  if (dq) p.op[p.ops++] = dense_op(desc, dO, v, k, dq, true, false);
-  if (dk) p.op[p.ops++] = dense_op(desc, v, dO, q, dk, false, true);
-  if (dv) p.op[p.ops++] = dense_op(desc, k, q, dO, dv, false, true);
+  p.ops = p.slots = 0;
+  if (dq) {
+    p.maker[p.slots++] = p.ops;
+    p.op[p.ops++] = dense_op(desc, dO, v, k, dq, true, false);
+  }
+  if (dk || dv) {  // sums of q dO^T over later tokens are dv's states, their transposes dk's
+    const int slot = p.slots++;
+    p.maker[slot] = p.ops;
+    if (dv) p.op[p.ops++] = dense_op(desc, k, q, dO, dv, false, true);
+    if (dk) p.op[p.ops++] = dense_op(desc, v, dO, q, dk, false, true);
+    for (int i = p.maker[slot]; i < p.ops; ++i) {
+      p.op[i].slot = slot;
+      p.op[i].turned = i > p.maker[slot];
+    }
+  }
   return cuda_status(launch_linear(p, desc->dtype == PATH_BF16, (char*)ws, (cudaStream_t)stream));
 }
 

@@ -59,19 +59,22 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
   const int tid = threadIdx.x, r0 = tid / 16 * 4, j0 = tid % 16, c0 = j0 * 4;  // owns o rows r0 .. r0 + 3, columns c0 .. c0 + 3
   constexpr int NV = D / V;
   const int h = blockIdx.y / NV, v0 = blockIdx.y % NV * V, item = blockIdx.x;
-  const LinOp& op = p.op[blockIdx.z];
+  const LinOp& op = p.op[STATES ? p.maker[blockIdx.z] : blockIdx.z];
   const LinItem it = lin_item(p, item);
   if (it.seg < 0) return;
   const bool rev = op.reverse;
   const float l2 = lin_log2(p.log_decay[h]);
   if (tid <= C) s.pw[tid] = exp2f(l2 * tid);
-  float* part = p.parts + (((size_t)blockIdx.z * p.items + item) * p.heads + h) * D * D + v0;
-  float* own = p.state ? p.state + ((size_t)it.seq * p.heads + h) * D * D + v0 : nullptr;
+  float* part = p.parts + (((size_t)op.slot * p.items + item) * p.heads + h) * D * D;
+  float* own = p.state ? p.state + ((size_t)it.seq * p.heads + h) * D * D : nullptr;
   const bool split = p.max_new > p.seg;  // the segments' starting states are in parts
   const float* from = STATES ? nullptr : split ? part : own;
-  for (int e = tid * 4; e < D * V; e += NT * 4)
-    *reinterpret_cast<float4*>(&s.s[e / V][e % V]) =
-        from ? *reinterpret_cast<const float4*>(from + (size_t)(e / V) * D + e % V) : make_float4(0.f, 0.f, 0.f, 0.f);
+  if (from && op.turned)
+    for (int e = tid; e < D * V; e += NT) s.s[e % D][e / D] = from[(size_t)(v0 + e / D) * D + e % D];
+  else
+    for (int e = tid * 4; e < D * V; e += NT * 4)
+      *reinterpret_cast<float4*>(&s.s[e / V][e % V]) =
+          from ? *reinterpret_cast<const float4*>(from + (size_t)(e / V) * D + v0 + e % V) : make_float4(0.f, 0.f, 0.f, 0.f);
   const float* x = (const float*)op.x + it.seq * op.xb + it.q0 * op.xt + (long long)h * op.gx * op.xh;
   float* o = (float*)op.o + it.seq * op.xb + it.q0 * op.xt + (long long)h * op.gx * op.xh + v0;
   const float* y = (const float*)op.y + it.seq * op.yb + it.q0 * op.yt + (long long)h * op.gy * op.yh;
@@ -196,13 +199,13 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
   float* to = STATES ? part : !split && p.update ? own : nullptr;
   if (to)
     for (int e = tid * 4; e < D * V; e += NT * 4)
-      *reinterpret_cast<float4*>(to + (size_t)(e / V) * D + e % V) = *reinterpret_cast<const float4*>(&s.s[e / V][e % V]);
+      *reinterpret_cast<float4*>(to + (size_t)(e / V) * D + v0 + e % V) = *reinterpret_cast<const float4*>(&s.s[e / V][e % V]);
 }
 
 template <int D, bool STATES> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(linear_simt_kernel<D, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
   if (e != cudaSuccess) return e;
-  return launch_chained(linear_simt_kernel<D, STATES>, dim3(p.items, p.heads * (D / V), p.ops), NT, sizeof(Smem<D>), st, p);
+  return launch_chained(linear_simt_kernel<D, STATES>, dim3(p.items, p.heads * (D / V), STATES ? p.slots : p.ops), NT, sizeof(Smem<D>), st, p);
 }
 
 }  // namespace

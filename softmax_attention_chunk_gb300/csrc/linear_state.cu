@@ -11,7 +11,7 @@ constexpr int NT = 256;
 // four elements per thread; the state after the last segment goes back to the sequence's own.
 __global__ void __launch_bounds__(NT) linear_scan_kernel(const LinArgs p) {
   chain();
-  const int lane = threadIdx.x & 31, b = blockIdx.y, h = blockIdx.z % p.heads, op = blockIdx.z / p.heads;
+  const int lane = threadIdx.x & 31, b = blockIdx.y, h = blockIdx.z % p.heads, slot = blockIdx.z / p.heads;
   int first = 0, n = p.L;
   if (!p.packed) {
     first = b * (p.items / p.seqs);
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(NT) linear_scan_kernel(const LinArgs p) {
   const float l2 = lin_log2(p.log_decay[h]);
   const float whole = exp2f(l2 * p.seg), tail = exp2f(l2 * (n - (count - 1) * p.seg));
   const size_t dd = (size_t)p.D * p.D, step = (size_t)p.heads * dd, e = ((size_t)blockIdx.x * NT + threadIdx.x) * 4;
-  float* part = p.parts + (((size_t)op * p.items + first) * p.heads + h) * dd + e;
+  float* part = p.parts + (((size_t)slot * p.items + first) * p.heads + h) * dd + e;
   float* own = p.state ? p.state + ((size_t)b * p.heads + h) * dd + e : nullptr;
   float4 s = own ? *reinterpret_cast<const float4*>(own) : make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int AHEAD = 8;  // loads in flight
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(NT) linear_copy_kernel(float* state, int* stat
 }  // namespace
 
 cudaError_t launch_linear_scan(const LinArgs& p, cudaStream_t st) {
-  return launch_chained(linear_scan_kernel, dim3(p.D * p.D / (4 * NT), p.seqs, p.heads * p.ops), NT, 0, st, p);
+  return launch_chained(linear_scan_kernel, dim3(p.D * p.D / (4 * NT), p.seqs, p.heads * p.slots), NT, 0, st, p);
 }
 
 cudaError_t launch_linear_copy(float* state, int* status, int slots, size_t elems, const int* parents, const int* children,
@@ -107,8 +107,11 @@ void lin_plan(LinArgs& p, bool bf16) {
   const int len = p.packed ? p.max_new : p.L;
   const int seqs = p.packed ? (p.total + p.max_new - 1) / p.max_new : p.seqs;
   const int units = p.heads * p.ops, blocks = (p.D == 64 ? 2 : 1) * 152;
-  p.seg = bf16 ? choose_seg(seqs, len, units, kLinChunk, blocks, 0.6, 4.0)
-               : choose_seg(seqs, len, units * (p.D / 64), kLinChunkF32, blocks, 0.35, 1.5);
+  // A state takes about half as long as a walk; of several query heads, each is a walk of its own (the launches then are less
+  // beside a chunk) but dq's and the forward's states are made once.
+  const double again = bf16 ? 0.5 * (p.ops == 1 ? 1.0 / p.G : (1.0 + p.G) / (3.0 * p.G)) : 0.35;
+  p.seg = bf16 ? choose_seg(seqs, len, units, kLinChunk, blocks, again, 2.5 / p.G)
+               : choose_seg(seqs, len, units * (p.D / 64), kLinChunkF32, blocks, again, 1.5);
   if (!p.packed) {
     p.max_new = p.L;
     p.items = p.seqs * ((p.L + p.seg - 1) / p.seg);
@@ -119,7 +122,7 @@ void lin_plan(LinArgs& p, bool bf16) {
 }
 
 size_t lin_ws_bytes(const LinArgs& p) {
-  return 256 + (p.max_new > p.seg ? (size_t)p.ops * p.items * p.heads * p.D * p.D * 4 : 0);
+  return 256 + (p.max_new > p.seg ? (size_t)p.slots * p.items * p.heads * p.D * p.D * 4 : 0);
 }
 
 cudaError_t launch_linear(LinArgs p, bool bf16, char* ws, cudaStream_t st) {

@@ -41,7 +41,8 @@ template <int D> struct Shape {
   static constexpr int LIGHT = 2;           // (head dim 64) warps whose part of P is all masked
   static constexpr int NT = 32 * (WARPS + 2);
   static constexpr int BLOCKS = D == 64 ? 2 : 1;  // to an SM
-  static constexpr int COL_D = COL_O + D, COLS = D == 64 ? 256 : 512;
+  static constexpr int NO = D == 64 ? 1 : 2;      // buffers of O
+  static constexpr int COL_D = COL_O + NO * D, COLS = D == 64 ? 256 : 512;
 };
 template <int D, int PARTS> struct Smem {
   // Buffers: what the block's share of 227 KB holds.  O leaves through x's place once x has been read; before that the second
@@ -51,7 +52,7 @@ template <int D, int PARTS> struct Smem {
   uint8_t sb[2][X][D * 128];                // the state, rows of D columns: rounded, and what that leaves
   float pw[Z0 + C + 8];                     // 0 .., then g^n
   alignas(16) float colw[32];               // g^n of a 32-column block's columns
-  uint64_t full_x[NX], full_y[NY], full_z[NZ], clean, s_full, o_full, d_full, c_full, w_full, p_full, done;
+  uint64_t full_x[NX], full_y[NY], full_z[2], clean, s_full, o_full, d_full, t_full, c_full, w_full, p_full, done;
   uint32_t tmem_base;
 };
 
@@ -123,7 +124,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   using Sh = Shape<D>;
   using Sm = Smem<D, PARTS>;
-  constexpr int X = Sh::X, NX = Sm::NX, NY = Sm::NY, NZ = Sm::NZ, NCT = 32 * Sh::WARPS, COL_D = Sh::COL_D;
+  constexpr int X = Sh::X, NX = Sm::NX, NY = Sm::NY, NCT = 32 * Sh::WARPS, COL_D = Sh::COL_D;
+  constexpr int NZ = STATES && PARTS == 1 ? 2 : Sm::NZ;  // (states alone: x's place is z's second buffer)
   constexpr int NS = D == 64 ? 16 : 32;       // state elements of a thread
   constexpr int SW = C / Sh::CG, SQ = SW / 32;  // columns of S of a warp
   Sm& s = *reinterpret_cast<Sm*>(smem_raw);
@@ -133,8 +135,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   // after P (head dim 128, 4 x 16 x 2048: forward 59 us in place of 70 with six of sixteen warps).
   constexpr bool ALL = STATES || PARTS > 1 || D == 128;
   int blk = blockIdx.x;  // (neighbouring blocks, the gradients of one head, share operands)
-  const int oi = blk % p.ops;
-  blk /= p.ops;
+  const int kinds = STATES ? p.slots : p.ops, oi = STATES ? p.maker[blk % kinds] : blk % kinds;
+  blk /= kinds;
   const int h = blk % p.heads, item = blk / p.heads;
   const LinOp& op = p.op[oi];
   const LinItem it = lin_item(p, item);
@@ -157,10 +159,11 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   if (tid == 0) {
     for (int i = 0; i < NX; ++i) mbar_init(&s.full_x[i], 1);
     for (int i = 0; i < NY; ++i) mbar_init(&s.full_y[i], 1);
-    for (int i = 0; i < NZ; ++i) mbar_init(&s.full_z[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.full_z[i], 1);
     mbar_init(&s.s_full, 1);
     mbar_init(&s.o_full, 1);
     mbar_init(&s.d_full, 1);
+    mbar_init(&s.t_full, 1);
     mbar_init(&s.c_full, 1);
     mbar_init(&s.clean, Sh::WARPS);
     mbar_init(&s.w_full, ALL ? Sh::WARPS : Sh::LIGHT);
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   if (tid < Z0 + C + 1) s.pw[tid] = tid < Z0 ? 0.f : exp2f(l2 * (tid - Z0));
   if (tid < 32) s.colw[tid] = exp2f(l2 * (rev ? tid : 31 - tid));
   const size_t dd = (size_t)D * D;
-  float* part = p.parts + (((size_t)oi * p.items + item) * p.heads + h) * dd;
+  float* part = p.parts + (((size_t)op.slot * p.items + item) * p.heads + h) * dd;
   float* own = p.state ? p.state + ((size_t)it.seq * p.heads + h) * dd : nullptr;
   const bool split = p.max_new > p.seg;  // the segments' starting states are in parts
   const float* from = STATES ? nullptr : split ? part : own;
@@ -199,8 +202,10 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   };
   if (warp < Sh::WARPS) {
 #pragma unroll
-    for (int e = 0; e < NS; e += 2)
-      st[e / 2] = from ? f2(from[(size_t)(sk + e) * D + sv], from[(size_t)(sk + e + 1) * D + sv]) : 0;
+    for (int e = 0; e < NS; e += 2) {
+      const size_t at = op.turned ? (size_t)sv * D + sk + e : (size_t)(sk + e) * D + sv;
+      st[e / 2] = from ? f2(from[at], from[at + (op.turned ? 1 : D)]) : 0;
+    }
     if (!STATES && from) put_state();
   }
   fence_proxy_async_smem();
@@ -215,6 +220,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     return ok;
   };
 
+  auto z_buffer = [&](int n) -> uint8_t (*)[TILE] { return STATES && PARTS == 1 && n % NZ ? s.x[0] : s.z[n % Sm::NZ]; };
   if (mover) {
     // ---------------- tiles in and out ----------------
     const int row0 = p.packed ? it.q0 : 0;
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     };
     auto next_z = [&]() {
       if (kz >= count) return;
-      load(s.z[nz % NZ], &maps.z[oi], &s.full_z[nz % NZ], kz, py + hz);
+      load(z_buffer(nz), &maps.z[oi], &s.full_z[nz % NZ], kz, py + hz);
       ++nz;
       if (++hz >= gy) hz = 0, ++kz;
     };
@@ -295,16 +301,30 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       for (int j = 0; j < X; ++j) mma4_ss<2, 2>(tbu + COL_S, kd + (a_x + j * (TILE / 16)), kd + (a_y + j * (TILE / 16)), id_s, j ? 1u : 0u);
       commit_elect(&s.s_full);
     };
-    auto issue_delta = [&](uint32_t accumulate) {
-      const uint32_t a_z = buffer(s.z, yn % NZ);
+    auto z_at = [&](int n) { return base + uniform((uint32_t)(&z_buffer(n)[0][0] - smem_raw) >> 4); };
+    auto issue_delta = [&](int yn, uint32_t accumulate, bool total) {
+      const uint32_t a_z = z_at(yn);
 #pragma unroll
       for (int t = 0; t < PARTS; ++t) {
-        const uint32_t a_w = t == 0 ? buffer(s.y, yn % NY) : at16(t == 1 ? s.x[0] : s.z[NZ]);
+        const uint32_t a_w = t == 0 ? buffer(s.y, yn % NY) : at16(t == 1 ? s.x[0] : s.z[Sm::NZ]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) mma4_ss<128, 128>(tbu + COL_D, md + (a_z + 512u * k), md + (a_w + 512u * k), id_d, (t | k) ? 1u : accumulate);
       }
       commit_elect(&s.d_full);
+      if (total) commit_elect(&s.t_full);
     };
+    // O's part from the state, of the x at hand: into the O buffer whose last output has been taken
+    int on = 0;
+    auto o_at = [&](int n) { return tbu + COL_O + uniform(n % Sh::NO * D); };
+    auto issue_inter = [&]() {
+      const uint32_t a_x = buffer(s.x, xn % NX), d_o = o_at(on);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < X; ++j) mma4_ss<2, 2>(d_o, kd + (a_x + j * (TILE / 16)), kd + at16(s.sb[t][j]), id_x, (t | j) ? 1u : 0u);
+      commit_elect(&s.o_full);
+    };
+    bool early = false;  // this step's has been issued
     operands();
     if (!STATES && ok) issue_s();
     for (int i = 0; i < steps && ok; ++i) {
@@ -312,41 +332,46 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       const bool old = from || k > 0;  // there is a state before the chunk
       const uint32_t more = uniform(gy > 1 && g > 0 ? 1u : 0u);
       if constexpr (!STATES) {
-        if (old && (gx > 1 || g == 0)) {
+        if (old && (gx > 1 || g == 0) && !early) {
           if (i > 0 && !wait(&s.done, i - 1, 20)) break;
           tc_fence_after();
-          const uint32_t a_x = buffer(s.x, xn % NX);
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < X; ++j) mma4_ss<2, 2>(tbu + COL_O, kd + (a_x + j * (TILE / 16)), kd + at16(s.sb[t][j]), id_x, (t | j) ? 1u : 0u);
-          commit_elect(&s.o_full);
+          issue_inter();
         }
+        early = false;
         if (!wait(&s.full_z[yn % NZ], yn / NZ, 25) || !wait(&s.p_full, i, 21)) break;
         tc_fence_after();
-        const uint32_t a_z = buffer(s.z, yn % NZ), first = uniform(old ? 1u : 0u) | more;
+        const uint32_t a_z = z_at(yn), first = uniform(old ? 1u : 0u) | more;
         auto at_p = [&](int e) { return tbu + COL_S + 16 * e / SW * SW + 16 * e % SW / 2; };  // of 16 tokens
 #pragma unroll
         for (int e = 0; e < 8; e += 4)
-          mma4_ts<128>(tbu + COL_O, at_p(e), at_p(e + 1), at_p(e + 2), at_p(e + 3), md + (a_z + 128u * e), id_o, e ? 1u : first);
+          mma4_ts<128>(o_at(on), at_p(e), at_p(e + 1), at_p(e + 2), at_p(e + 3), md + (a_z + 128u * e), id_o, e ? 1u : first);
         commit_elect(&s.c_full);
       }
-      if (update) {
-        if (!wait(&s.w_full, un++, 22)) break;
+      // Delta, and S of the next step; S first where no state waits for Delta
+      const int y0 = yn;
+      const bool s_first = !STATES && gy > 1 && !last;
+      auto delta = [&]() {
+        if (!update || !wait(&s.w_full, un++, 22)) return;
         tc_fence_after();
-        issue_delta(more);
-      }
+        issue_delta(y0, more, last);
+      };
+      if (!s_first) delta();
       if (gy > 1 || last) ++yn;
-      if (gx > 1 || last) ++xn;
+      if (gx > 1 || last) ++xn, ++on;
       if (last) g = 0, ++k;
       else ++g;
-      if (i + 1 < steps) {
+      if (ok && i + 1 < steps) {
         operands();
         if (!STATES && wait(&s.c_full, i, 24)) {
           tc_fence_after();
           issue_s();
+          if (Sh::NO > 1 && gx > 1 && g > 0 && old) {  // (the state is the same, and P of this step was made after the last output)
+            issue_inter();
+            early = true;
+          }
         }
       }
+      if (s_first && ok) delta();
     }
   } else {
     // ---------------- weights, state, output ----------------
@@ -357,19 +382,19 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       if (lane == 0) mbar_arrive(bar);
     };
     const int light = rev ? (cg == 0 ? quad - 2 : -1) : (cg == 1 && quad < 2 ? quad : -1);  // number among them, or below 0
-    int g = 0, k = 0, yn = 0, xn = 0, un = 0, dn = 0, in = 0;  // deltas begun, and those waited for; products with the state
+    int g = 0, k = 0, yn = 0, xn = 0, in = 0;  // in: products with the state
     for (int i = 0; i < steps && ok; ++i) {
       const int m = rows_of(k), yb = yn % NY;
       const bool fresh = gy > 1 || g == 0, last = g == G - 1, update = gy > 1 || last;
       const bool inter = (from || k > 0) && (gx > 1 || g == 0);
-      if (dn < un && !wait(&s.d_full, dn++, 31)) break;  // (its phases one by one)
       if (fresh && ragged(k)) {  // rows of the next sequence: they may hold anything
         wait(&s.full_y[yb], yn / NY, 32);
         if (!wait(&s.full_z[yn % NZ], yn / NZ, 33)) break;
+        uint8_t* z = &z_buffer(yn)[0][0];
         for (int e = tid; e < (C - m) * 8 * X; e += NCT) {
           const uint32_t at = e / ((C - m) * 8) * TILE + (m * 8 + e % ((C - m) * 8)) * 16;
           *reinterpret_cast<uint4*>(&s.y[yb][0][0] + at) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(&s.z[yn % NZ][0][0] + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(z + at) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         arrive(&s.clean);
@@ -416,7 +441,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
           if (!wait(&s.o_full, in, 35)) break;
           ++in;
           tc_fence_after();
-          tmem_ld32(tb + lane_off + COL_O + 32 * cg, a);
+          tmem_ld32(tb + lane_off + COL_O + xn % Sh::NO * D + 32 * cg, a);
           const float w = s.pw[Z0 + (rev ? max(m - r, 0) : r + 1)];
           const uint64_t ww = f2(w, w);
           tmem_ld_wait();
@@ -425,7 +450,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
             const uint64_t v = f2_mul(f2_bits(a[e], a[e + 1]), ww);
             a[e] = (uint32_t)v, a[e + 1] = (uint32_t)(v >> 32);
           }
-          tmem_st32(tb + lane_off + COL_O + 32 * cg, a);
+          tmem_st32(tb + lane_off + COL_O + xn % Sh::NO * D + 32 * cg, a);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -446,13 +471,14 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
             *reinterpret_cast<uint4*>(y) = w[0];
             if constexpr (PARTS > 1) {
               *reinterpret_cast<uint4*>(&s.x[0][0][0] + at) = w[1];
-              *reinterpret_cast<uint4*>(&s.z[NZ][0][0] + at) = w[2];
+              *reinterpret_cast<uint4*>(&s.z[Sm::NZ][0][0] + at) = w[2];
             }
           }
           fence_proxy_async_smem();
+          // (one phase ahead at most: with one y to a chunk t_full sees to it)
+          if (gy > 1 && i > 0 && !wait(&s.d_full, i - 1, 37)) break;
           arrive(&s.w_full);
         }
-        ++un;
       }
       const bool emit = !STATES && (gx > 1 || last);
       uint32_t out[16];
@@ -471,7 +497,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       if (emit) {
         if (!wait(&s.c_full, i, 38)) break;
         tc_fence_after();
-        tmem_ld32(tb + lane_off + COL_O + 32 * cg, a);
+        tmem_ld32(tb + lane_off + COL_O + xn % Sh::NO * D + 32 * cg, a);
         const uint64_t scale = f2(p.scale, p.scale);
         tmem_ld_wait();
 #pragma unroll
@@ -479,7 +505,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
         if (PARTS == 1) put_out();
       }
       if (last) {
-        if (!wait(&s.d_full, dn++, 39)) break;
+        if (!wait(&s.t_full, k, 39)) break;
         tc_fence_after();
         const uint64_t keep = f2(s.pw[Z0 + m], s.pw[Z0 + m]);
         uint32_t b[NS];
@@ -546,7 +572,7 @@ template <int D, bool STATES, int PARTS> cudaError_t launch(const LinMaps& maps,
   auto kern = linear_tc_kernel<D, STATES, PARTS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D, PARTS>));
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, dim3((unsigned)((long long)p.items * p.heads * p.ops)), Shape<D>::NT, sizeof(Smem<D, PARTS>), st, maps, p);
+  return launch_chained(kern, dim3((unsigned)((long long)p.items * p.heads * (STATES ? p.slots : p.ops))), Shape<D>::NT, sizeof(Smem<D, PARTS>), st, maps, p);
 }
 
 }  // namespace
