@@ -84,17 +84,37 @@ cudaError_t launch_linear_copy(float* state, int* status, int slots, size_t elem
   return launch_chained(linear_copy_kernel, dim3(x < 64 ? x : 64, count), NT, 0, st, state, status, slots, elems, parents, children, count);
 }
 
-// Tokens per segment, a multiple of the chunk: as many segments as let the blocks' waves end evenly, where a call with
-// several pays for their states first (`again` of the walk itself, and the launches and the joining, in chunks).
-static int choose_seg(int seqs, int len, int units, int chunk, int blocks, double again, double launches) {
+// Microseconds of a step (a chunk of one query head) of a walk and of a state, with a block to an SM and with all the blocks an
+// SM holds, as measured (bf16: the walks of several query heads overlap more than chunks of one do).
+struct Steps {
+  double walk, walk_full, state, state_full;
+};
+static Steps step_times(const LinArgs& p, bool bf16) {
+  if (!bf16) return p.D == 64 ? Steps{10.4, 17.0, 3.2, 5.0} : Steps{15.5, 15.5, 4.6, 4.6};
+  if (p.D == 64) return p.G == 1 ? Steps{2.4, 2.85, 1.0, 2.0} : Steps{1.65, 2.3, 1.0, 2.0};
+  return p.G == 1 ? Steps{3.1, 3.1, 1.45, 1.45} : Steps{2.3, 2.3, 1.45, 1.45};
+}
+// Tokens per segment, a multiple of the chunk.  One segment to a sequence needs nothing but the walk; several run side by
+// side, and cost the states at their starts: the states' own pass, two more launches and 16 D^2 bytes of traffic each (1 x 8 x
+// 4096 d 64, forward: 78 us in one segment, 25 in sixteen; 8 x 32 x 4096: 103 in one, 174 in two).
+static int choose_seg(const LinArgs& p, bool bf16, int seqs, int len, int chunk) {
+  const Steps t = step_times(p, bf16);
+  const int per_head = bf16 ? 1 : p.D / 64, full = 152 * (p.D == 64 ? 2 : 1);
   const int chunks = (len + chunk - 1) / chunk;
   int best = chunks;
   double least = 0;
   for (int c = chunks; c >= 1; --c) {  // chunks of a segment
     const int n = (chunks + c - 1) / c;
     if (n > 1 && (chunks + n - 1) / n != c) continue;  // (fewer chunks make as many segments)
-    const double waves = (double)(((long long)seqs * n * units + blocks - 1) / blocks);
-    const double cost = waves * c * (n > 1 ? 1 + again : 1.0) + (n > 1 ? launches + 0.05 * n : 0.0);
+    auto waves = [&](double blocks, double one, double all) { return blocks <= 152 ? one : all * (double)(long long)((blocks + full - 1) / full); };
+    const double heads = (double)seqs * p.heads * n;
+    double cost = c * p.G * waves(heads * p.ops * per_head, t.walk, t.walk_full);
+    if (n > 1) {
+      // (of a backward pass's two states one has all query heads to add up)
+      const double most = p.slots == 1 ? 1 : p.G, mean = p.slots == 1 ? 1 : (1 + p.G) / 2.0;
+      const double states = c * mean * waves(heads * p.slots * per_head, t.state, t.state_full);
+      cost += (states > c * most * t.state ? states : c * most * t.state) + 7 + p.D / 64 * 0.45 * n + heads * p.slots * p.D * p.D * 16 / 5e6;
+    }
     if (c == chunks || cost < least) {
       least = cost;
       best = c;
@@ -106,12 +126,7 @@ static int choose_seg(int seqs, int len, int units, int chunk, int blocks, doubl
 void lin_plan(LinArgs& p, bool bf16) {
   const int len = p.packed ? p.max_new : p.L;
   const int seqs = p.packed ? (p.total + p.max_new - 1) / p.max_new : p.seqs;
-  const int units = p.heads * p.ops, blocks = (p.D == 64 ? 2 : 1) * 152;
-  // A state takes about half as long as a walk; of several query heads, each is a walk of its own (the launches then are less
-  // beside a chunk) but dq's and the forward's states are made once.
-  const double again = bf16 ? 0.5 * (p.ops == 1 ? 1.0 / p.G : (1.0 + p.G) / (3.0 * p.G)) : 0.35;
-  p.seg = bf16 ? choose_seg(seqs, len, units, kLinChunk, blocks, again, 2.5 / p.G)
-               : choose_seg(seqs, len, units * (p.D / 64), kLinChunkF32, blocks, again, 1.5);
+  p.seg = choose_seg(p, bf16, seqs, len, bf16 ? kLinChunk : kLinChunkF32);
   if (!p.packed) {
     p.max_new = p.L;
     p.items = p.seqs * ((p.L + p.seg - 1) / p.seg);

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     for (int i = 0; i < steps && ok; ++i) {
       const bool last = g == G - 1, update = gy > 1 || last;
       const bool old = from || k > 0;  // there is a state before the chunk
-      const uint32_t more = uniform(gy > 1 && g > 0 ? 1u : 0u);
+      const uint32_t more = uniform(STATES ? i > 0 : gy > 1 && g > 0);
       if constexpr (!STATES) {
         if (old && (gx > 1 || g == 0) && !early) {
           if (i > 0 && !wait(&s.done, i - 1, 20)) break;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       auto delta = [&]() {
         if (!update || !wait(&s.w_full, un++, 22)) return;
         tc_fence_after();
-        issue_delta(y0, more, last);
+        issue_delta(y0, more, STATES ? i + 1 == steps : last);
       };
       if (!s_first) delta();
       if (gy > 1 || last) ++yn;
@@ -458,6 +458,10 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       }
       if (update) {  // Y' over Y, whose products have been made; rows behind m become 0
         if (STATES && !wait(&s.full_y[yb], yn / NY, 36)) break;
+        // (PARTS > 1: the further parts' places have been read)
+        if (STATES && PARTS > 1 && i > 0 && !wait(&s.d_full, i - 1, 36)) break;
+        // states alone: weighed to the segment's end, so that all deltas add up where they are
+        const float ahead = STATES ? exp2f(l2 * (rev ? (chunk_of(k) - c0) * C : min(it.n, (c0 + count) * C) - chunk_of(k) * C - m)) : 1.f;
         if (ALL || light >= 0) {
           constexpr int STEP = 32 * (ALL ? Sh::WARPS : Sh::LIGHT);
 #pragma unroll 4
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
             uint8_t* y = &s.y[yb][0][0] + at;
             uint4 w[PARTS], in = *reinterpret_cast<const uint4*>(y);
             if (row >= m) in = make_uint4(0, 0, 0, 0);
-            weighted<PARTS>(in, s.pw[Z0 + (rev ? row : max(m - 1 - row, 0))], w);
+            weighted<PARTS>(in, s.pw[Z0 + (rev ? row : max(m - 1 - row, 0))] * ahead, w);
             *reinterpret_cast<uint4*>(y) = w[0];
             if constexpr (PARTS > 1) {
               *reinterpret_cast<uint4*>(&s.x[0][0][0] + at) = w[1];
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
           }
           fence_proxy_async_smem();
           // (one phase ahead at most: with one y to a chunk t_full sees to it)
-          if (gy > 1 && i > 0 && !wait(&s.d_full, i - 1, 37)) break;
+          if ((gy > 1 || (STATES && PARTS == 1)) && i > 0 && !wait(&s.d_full, i - 1, 37)) break;
           arrive(&s.w_full);
         }
       }
@@ -504,8 +508,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
         for (int j = 0; j < 16; ++j) out[j] = pack_pair(f2_mul(f2_bits(a[2 * j], a[2 * j + 1]), scale));
         if (PARTS == 1) put_out();
       }
-      if (last) {
-        if (!wait(&s.t_full, k, 39)) break;
+      if (STATES ? i + 1 == steps : last) {
+        if (!wait(&s.t_full, STATES ? 0 : k, 39)) break;
         tc_fence_after();
         const uint64_t keep = f2(s.pw[Z0 + m], s.pw[Z0 + m]);
         uint32_t b[NS];
