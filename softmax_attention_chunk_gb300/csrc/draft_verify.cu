@@ -83,7 +83,7 @@ __device__ __forceinline__ int first_past(double upto, double part, double goal)
 }
 
 template <typename T, int N>
-__global__ void __launch_bounds__(NT, 2) draft_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a) {
   chain();
   constexpr int LOADS = STEP / (32 * N);
   constexpr int PER = kMaxCluster * NW / 32;  // warps' sums of the cluster to a lane
@@ -154,12 +154,22 @@ __global__ void __launch_bounds__(NT, 2) draft_verify_kernel(const VerifyArgs a)
   for (int round = 0; round < 2; ++round) {
     double mine = 0;  // of step `lane`
     for (int s = 0; s < steps; ++s) {
-      load(v0 + s * STEP);
       float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {  // (in halves: registers for four blocks to an SM, which keep more loads on their way)
+        constexpr int H = LOADS / 2;
+        float ph[H][N], qh[H][N];
+        const int at0 = v0 + s * STEP + half * (STEP / 2) + lane * N;
 #pragma unroll
-      for (int j = 0; j < LOADS; ++j)
+        for (int j = 0; j < H; ++j) {
+          load_n<T, N>(p + at0 + j * 32 * N, vocab - at0 - j * 32 * N, ph[j]);
+          if (q) load_n<T, N>(q + at0 + j * 32 * N, vocab - at0 - j * 32 * N, qh[j]);
+        }
 #pragma unroll
-        for (int i = 0; i < N; ++i) add_pair(sum, entry(v0 + s * STEP, j, i));
+        for (int j = 0; j < H; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i) add_pair(sum, residual(at0 + j * 32 * N + i == out ? 0.f : ph[j][i], q ? qh[j][i] : 0.f));
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         add_pair(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));

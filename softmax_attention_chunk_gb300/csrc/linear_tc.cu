@@ -52,7 +52,10 @@ template <int D, int PARTS> struct Smem {
   uint8_t sb[2][X][D * 128];                // the state, rows of D columns: rounded, and what that leaves
   float pw[Z0 + C + 8];                     // 0 .., then g^n
   alignas(16) float colw[32];               // g^n of a 32-column block's columns
-  uint64_t full_x[NX], full_y[NY], full_z[2], clean, s_full, o_full, d_full, t_full, c_full, w_full, p_full, done;
+  // A wait looks at the parity of a phase: none of these may complete two phases while someone still waits for the first.  So
+  // what frees or fills one of several buffers has a barrier for each.
+  uint64_t full_x[NX], full_y[NY], full_z[2], yz_free[2], out_full[NX];
+  uint64_t clean, s_full, o_full, d_full, t_full, c_full, w_full, p_full, done;
   uint32_t tmem_base;
 };
 
@@ -126,6 +129,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   using Sm = Smem<D, PARTS>;
   constexpr int X = Sh::X, NX = Sm::NX, NY = Sm::NY, NCT = 32 * Sh::WARPS, COL_D = Sh::COL_D;
   constexpr int NZ = STATES && PARTS == 1 ? 2 : Sm::NZ;  // (states alone: x's place is z's second buffer)
+  constexpr int NF = NZ < NY ? NZ : NY;       // of y and z together: the next of the same number waits for the one before
   constexpr int NS = D == 64 ? 16 : 32;       // state elements of a thread
   constexpr int SW = C / Sh::CG, SQ = SW / 32;  // columns of S of a warp
   Sm& s = *reinterpret_cast<Sm*>(smem_raw);
@@ -160,6 +164,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     for (int i = 0; i < NX; ++i) mbar_init(&s.full_x[i], 1);
     for (int i = 0; i < NY; ++i) mbar_init(&s.full_y[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&s.full_z[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.yz_free[i], 1);
+    for (int i = 0; i < NX; ++i) mbar_init(&s.out_full[i], Sh::WARPS);
     mbar_init(&s.s_full, 1);
     mbar_init(&s.o_full, 1);
     mbar_init(&s.d_full, 1);
@@ -260,12 +266,13 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     for (int i = 0; i < steps && ok; ++i) {
       const bool last = g == G - 1;
       if (gy > 1 || last) {  // y and z have been read
-        if (!wait(&s.d_full, un++, 10)) break;
+        if (!wait(&s.yz_free[un % NF], un / NF, 10)) break;
+        ++un;
         next_y();
         next_z();
       }
       if (!STATES && (gx > 1 || last)) {  // o lies in x's place
-        if (!wait(&s.done, i, 11)) break;
+        if (!wait(&s.out_full[xn % NX], xn / NX, 11)) break;
         if (!ragged(k) && lane == 0)
 #pragma unroll
           for (int j = 0; j < X; ++j) tma_store_3d(&maps.o[oi], s.x[xn % NX][j], 64 * j, row0 + chunk_of(k) * C, px + (gx > 1 ? g : 0));
@@ -310,7 +317,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
 #pragma unroll
         for (int k = 0; k < 2; ++k) mma4_ss<128, 128>(tbu + COL_D, md + (a_z + 512u * k), md + (a_w + 512u * k), id_d, (t | k) ? 1u : accumulate);
       }
-      commit_elect(&s.d_full);
+      commit_elect(&s.yz_free[yn % NF]);
+      if (STATES || gy > 1) commit_elect(&s.d_full);
       if (total) commit_elect(&s.t_full);
     };
     // O's part from the state, of the x at hand: into the O buffer whose last output has been taken
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
             }
           }
           fence_proxy_async_smem();
-          // (one phase ahead at most: with one y to a chunk t_full sees to it)
+          // (w_full is one phase ahead at most; with one y to a chunk t_full sees to it)
           if ((gy > 1 || (STATES && PARTS == 1)) && i > 0 && !wait(&s.d_full, i - 1, 37)) break;
           arrive(&s.w_full);
         }
@@ -497,6 +505,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
 #pragma unroll
           for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(o + 8 * j) = make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
         }
+        arrive(&s.out_full[xn % NX]);
       };
       if (emit) {
         if (!wait(&s.c_full, i, 38)) break;
@@ -592,13 +601,15 @@ cudaError_t launch_linear_tc(const LinArgs& p, bool states, cudaStream_t st) {
         !make_map(&maps.y[i], op.y, p.D, rows, ny, op.yt, op.yh) || !make_map(&maps.z[i], op.z, p.D, rows, ny, op.yt, op.yh))
       return cudaErrorInvalidValue;
   }
-  // (a cache's states: whether or not they are written, for the same outputs)
+  // A cache's states (whether or not they are written, for the same outputs) come from the states' pass where there are
+  // several segments, else from the walk.
+  const bool exact = p.state && (states || p.max_new <= p.seg);
   if (p.D == 64) {
-    if (states) return p.state ? launch<64, true, 3>(maps, p, st) : launch<64, true, 1>(maps, p, st);
-    return p.state ? launch<64, false, 3>(maps, p, st) : launch<64, false, 1>(maps, p, st);
+    if (states) return exact ? launch<64, true, 3>(maps, p, st) : launch<64, true, 1>(maps, p, st);
+    return exact ? launch<64, false, 3>(maps, p, st) : launch<64, false, 1>(maps, p, st);
   }
-  if (states) return p.state ? launch<128, true, 3>(maps, p, st) : launch<128, true, 1>(maps, p, st);
-  return p.state ? launch<128, false, 3>(maps, p, st) : launch<128, false, 1>(maps, p, st);
+  if (states) return exact ? launch<128, true, 3>(maps, p, st) : launch<128, true, 1>(maps, p, st);
+  return exact ? launch<128, false, 3>(maps, p, st) : launch<128, false, 1>(maps, p, st);
 }
 
 }  // namespace pathattn

@@ -24,29 +24,30 @@ template <> __device__ __forceinline__ void load4s<__nv_bfloat16>(const __nv_bfl
   v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
 }
 
-template <typename T, int D>
+// A block holds V columns of a state.
+template <typename T, int D, int V>
 __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
   chain();
   if (p.max_new > kLinTokenMax && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.err = 0;  // (of the kernels that follow)
-  constexpr int CG = D / 4;      // lanes of a row, four columns each
+  constexpr int CG = V / 4;      // lanes of a row, four columns each
   constexpr int RG = NT / CG;    // row groups
   constexpr int RP = D / RG;     // rows of a thread, one behind the other
   extern __shared__ uint8_t smem_raw[];
   T* tok = reinterpret_cast<T*>(smem_raw);  // per token: k, v, q of the group
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = tid % CG * 4, r0 = tid / CG * RP;
-  const int h = blockIdx.x, b = blockIdx.y, G = p.G;
+  const int h = blockIdx.x / (D / V), v0 = blockIdx.x % (D / V) * V, b = blockIdx.y, G = p.G;
   const LinSpan sp = lin_span(p.q_start, b, p.total, p.max_new);
-  if (sp.code && h == 0 && tid == 0) paged_error(p.status, sp.code);
+  if (sp.code && blockIdx.x == 0 && tid == 0) paged_error(p.status, sp.code);
   const int n = sp.n;
   if (n == 0 || n > kLinTokenMax) return;
-  float* own = p.state + (((size_t)b * p.heads + h) * D + r0) * D + c;
+  float* own = p.state + (((size_t)b * p.heads + h) * D + r0) * D + v0 + c;
   ulonglong2 s[RP];  // pairs of floats
 #pragma unroll
   for (int i = 0; i < RP; ++i) s[i] = *reinterpret_cast<const ulonglong2*>(own + i * D);
   const LinOp& op = p.op[0];
   const int per = (2 + G) * D;
-  float* red = reinterpret_cast<float*>(tok + min(p.max_new, kLinTokenMax) * per);  // [2][OB][W][D]: the warps' sums
+  float* red = reinterpret_cast<float*>(tok + min(p.max_new, kLinTokenMax) * per);  // [2][OB][W][V]: the warps' sums
   for (int e = tid * 4; e < n * per; e += NT * 4) {
     const int t = e / per, x = e % per / D, col = e % D;
     const long long at = sp.q0 + t;
@@ -59,14 +60,14 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
   const float g1 = exp2f(lin_log2(p.log_decay[h]));
   const uint64_t keep = f2(g1, g1);
   __syncthreads();
-  T* o = (T*)op.o + (long long)sp.q0 * op.xt + (long long)h * G * op.xh;
+  T* o = (T*)op.o + (long long)sp.q0 * op.xt + (long long)h * G * op.xh + v0;
   const T* at = tok;
   int g = 0, t0 = 0, g0 = 0, buf = 0;  // head; token and head of the first row not joined yet
   const int rows = n * G;
   for (int i = 0; i < rows; ++i) {
     if (g == 0) {
       float v[4];
-      load4s<T>(at + D + c, v);
+      load4s<T>(at + D + v0 + c, v);
       const uint64_t v0 = f2(v[0], v[1]), v1 = f2(v[2], v[3]);
 #pragma unroll
       for (int j = 0; j < RP; j += 4) {
@@ -99,16 +100,16 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) a[j] += __shfl_xor_sync(0xffffffffu, a[j], 16);
     if (CG == 32 || lane < CG)
-      *reinterpret_cast<float4*>(red + ((buf * OB + i % OB) * W + warp) * D + c) = make_float4(a[0], a[1], a[2], a[3]);
+      *reinterpret_cast<float4*>(red + ((buf * OB + i % OB) * W + warp) * V + c) = make_float4(a[0], a[1], a[2], a[3]);
     if (++g == G) g = 0, at += per;
     const int done = i % OB + 1;
     if (done == OB || i + 1 == rows) {
       __syncthreads();  // (the other half of red was read before the block came here)
-      for (int e = tid; e < done * D; e += NT) {
-        const int row = g0 + e / D, col = e % D;
+      for (int e = tid; e < done * V; e += NT) {
+        const int row = g0 + e / V, col = e % V;
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) sum += red[((buf * OB + e / D) * W + w) * D + col];
+        for (int w = 0; w < W; ++w) sum += red[((buf * OB + e / V) * W + w) * V + col];
         o[(t0 + row / G) * op.xt + (long long)(row % G) * op.xh + col] = from_f<T>(sum * p.scale);
       }
       buf ^= 1;
@@ -121,21 +122,26 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
     for (int i = 0; i < RP; ++i) *reinterpret_cast<ulonglong2*>(own + i * D) = s[i];
 }
 
-template <typename T, int D> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
+template <typename T, int D, int V> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
   const int most = p.max_new < kLinTokenMax ? p.max_new : kLinTokenMax, rows = most * p.G;
-  const size_t smem = sizeof(T) * most * (2 + p.G) * D + sizeof(float) * W * D * (rows > OB ? 2 * OB : rows);
+  const size_t smem = sizeof(T) * most * (2 + p.G) * D + sizeof(float) * W * V * (rows > OB ? 2 * OB : rows);
   if (smem > 48 << 10) {
-    cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<T, D, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_chained(linear_token_kernel<T, D>, dim3(p.heads, p.seqs), NT, smem, st, p);
+  return launch_chained(linear_token_kernel<T, D, V>, dim3(p.heads * (D / V), p.seqs), NT, smem, st, p);
+}
+// Single tokens are bound by the states' bytes, whole rows to a block; with several tokens a block works between its loads, and
+// half a state's columns make room for twice the blocks (48 slots x 8 heads of dim 128 with 2 .. 9 tokens: YY us in place of 16.7).
+template <typename T> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
+  if (p.D == 64) return launch<T, 64, 64>(p, st);
+  return p.max_new > 1 ? launch<T, 128, 64>(p, st) : launch<T, 128, 128>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_token(const LinArgs& p, bool bf16, cudaStream_t st) {
-  if (bf16) return p.D == 64 ? launch<__nv_bfloat16, 64>(p, st) : launch<__nv_bfloat16, 128>(p, st);
-  return p.D == 64 ? launch<float, 64>(p, st) : launch<float, 128>(p, st);
+  return bf16 ? launch<__nv_bfloat16>(p, st) : launch<float>(p, st);
 }
 
 }  // namespace pathattn

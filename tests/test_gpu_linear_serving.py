@@ -213,3 +213,16 @@ def test_many_slots(cuda_lib):
     for b, rows, (want, A), (state, SA) in list(expect(before, q, k, v, ld, n, 1.0))[::97]:
         check("o", o[rows], want, A, "bf16", terms=n[b] + 200)
         check_state(cache.state[b], state, SA, "bf16", terms=n[b] + 64)
+
+
+@pytest.mark.parametrize("d,hq,hkv,n", [(64, 2, 2, [3000]), (128, 4, 1, [700, 1, 30])])
+def test_many_calls_in_a_row(cuda_lib, d, hq, hkv, n):
+    """Thousands of calls behind one another: the kernels' warps meet in every order, and no bounded wait gives up."""
+    cache, q, k, v, ld = make("bf16", d, hq, hkv, n, seed=9)
+    s = starts(n)
+    want = cache.extend(q, k, v, ld, q_start=s, max_new=max(n), update=False).clone()
+    out = torch.empty_like(q)
+    for _ in range(3000):
+        cache.extend(q, k, v, ld, q_start=s, max_new=max(n), update=False, out=out)
+    cache.check()
+    assert torch.equal(out, want)
