@@ -16,12 +16,13 @@ __global__ void __launch_bounds__(NT) linear_scan_kernel(const LinArgs p) {
   if (!p.packed) {
     first = b * (p.items / p.seqs);
   } else {
+    n = lin_span(p.q_start, b, p.total, p.max_new).n;
+    if (n < p.min_new) return;
     for (int base = 0; base <= b; base += 32) {  // items of the slots before this one
       LinSpan s{0, 0, 0};
       if (base + lane <= b) s = lin_span(p.q_start, base + lane, p.total, p.max_new);
       if (s.n < p.min_new) s.n = 0;
       first += (int)__reduce_add_sync(0xffffffffu, base + lane < b ? (s.n + p.seg - 1) / p.seg : 0);
-      n = __shfl_sync(0xffffffffu, s.n, b & 31);
     }
   }
   const int count = min((n + p.seg - 1) / p.seg, p.items - first);

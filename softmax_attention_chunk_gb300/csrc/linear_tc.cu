@@ -156,6 +156,9 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   const int nch = (it.n + C - 1) / C, per = p.seg / C, nseg = (nch + per - 1) / per;
   const int c0 = (rev ? nseg - 1 - it.seg : it.seg) * per, count = min(per, nch - c0);
   const int steps = count * G;
+  // S of step i: with several y to an x, O's second buffer is S's, and the next S does not wait for P to be read
+  const bool two_s = Sh::NO > 1 && gy > 1;
+  auto s_col = [&](int i) { return two_s && i % 2 ? COL_O + D : COL_S; };
   auto chunk_of = [&](int k) { return rev ? c0 + count - 1 - k : c0 + k; };
   auto rows_of = [&](int k) { return min(C, it.n - chunk_of(k) * C); };
   auto ragged = [&](int k) { return p.packed && rows_of(k) < C; };  // (the last chunk of a walk onwards)
@@ -237,24 +240,33 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
 #pragma unroll
       for (int j = 0; j < X; ++j) tma_load_3d(to[j], map, 64 * j, row0 + chunk_of(k) * C, plane, bar);
     };
+    // the tile after that, into L2: by the time its buffer is free it is near
+    auto ahead = [&](const CUtensorMap* map, int k, int plane) {
+      if (lane != 0 || k >= count) return;
+#pragma unroll
+      for (int j = 0; j < X; ++j) tma_prefetch_3d(map, 64 * j, row0 + chunk_of(k) * C, plane);
+    };
     int kx = 0, hx = 0, nx = 0, ky = 0, hy = 0, ny = 0, kz = 0, hz = 0, nz = 0;  // (chunk, head, number) of the next load
     auto next_x = [&]() {
       if (kx >= count) return;
       load(s.x[nx % NX], &maps.x[oi], &s.full_x[nx % NX], kx, px + hx);
       ++nx;
       if (++hx >= gx) hx = 0, ++kx;
+      ahead(&maps.x[oi], kx, px + hx);
     };
     auto next_y = [&]() {
       if (ky >= count) return;
       load(s.y[ny % NY], &maps.y[oi], &s.full_y[ny % NY], ky, py + hy);
       ++ny;
       if (++hy >= gy) hy = 0, ++ky;
+      ahead(&maps.y[oi], ky, py + hy);
     };
     auto next_z = [&]() {
       if (kz >= count) return;
       load(z_buffer(nz), &maps.z[oi], &s.full_z[nz % NZ], kz, py + hz);
       ++nz;
       if (++hz >= gy) hz = 0, ++kz;
+      ahead(&maps.z[oi], kz, py + hz);
     };
     next_y();
     if (!STATES) next_x();
@@ -302,10 +314,11 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       if (ragged(k)) wait(&s.clean, 0, 19);
       tc_fence_after();
     };
-    auto issue_s = [&]() {  // over P of the step before, which has been read
+    auto issue_s = [&](int i) {  // over P of the step before (two_s: before that one), which has been read
+      const uint32_t d_s = tbu + uniform(s_col(i));
       const uint32_t a_x = buffer(s.x, xn % NX), a_y = buffer(s.y, yn % NY);
 #pragma unroll
-      for (int j = 0; j < X; ++j) mma4_ss<2, 2>(tbu + COL_S, kd + (a_x + j * (TILE / 16)), kd + (a_y + j * (TILE / 16)), id_s, j ? 1u : 0u);
+      for (int j = 0; j < X; ++j) mma4_ss<2, 2>(d_s, kd + (a_x + j * (TILE / 16)), kd + (a_y + j * (TILE / 16)), id_s, j ? 1u : 0u);
       commit_elect(&s.s_full);
     };
     auto z_at = [&](int n) { return base + uniform((uint32_t)(&z_buffer(n)[0][0] - smem_raw) >> 4); };
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     };
     // O's part from the state, of the x at hand: into the O buffer whose last output has been taken
     int on = 0;
-    auto o_at = [&](int n) { return tbu + COL_O + uniform(n % Sh::NO * D); };
+    auto o_at = [&](int n) { return tbu + COL_O + uniform(two_s ? 0 : n % Sh::NO * D); };
     auto issue_inter = [&]() {
       const uint32_t a_x = buffer(s.x, xn % NX), d_o = o_at(on);
 #pragma unroll
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     };
     bool early = false;  // this step's has been issued
     operands();
-    if (!STATES && ok) issue_s();
+    if (!STATES && ok) issue_s(0);
     for (int i = 0; i < steps && ok; ++i) {
       const bool last = g == G - 1, update = gy > 1 || last;
       const bool old = from || k > 0;  // there is a state before the chunk
@@ -349,7 +362,8 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
         if (!wait(&s.full_z[yn % NZ], yn / NZ, 25) || !wait(&s.p_full, i, 21)) break;
         tc_fence_after();
         const uint32_t a_z = z_at(yn), first = uniform(old ? 1u : 0u) | more;
-        auto at_p = [&](int e) { return tbu + COL_S + 16 * e / SW * SW + 16 * e % SW / 2; };  // of 16 tokens
+        const uint32_t d_s = tbu + uniform(s_col(i));
+        auto at_p = [&](int e) { return d_s + 16 * e / SW * SW + 16 * e % SW / 2; };  // of 16 tokens
 #pragma unroll
         for (int e = 0; e < 8; e += 4)
           mma4_ts<128>(o_at(on), at_p(e), at_p(e + 1), at_p(e + 2), at_p(e + 3), md + (a_z + 128u * e), id_o, e ? 1u : first);
@@ -357,7 +371,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       }
       // Delta, and S of the next step; S first where no state waits for Delta
       const int y0 = yn;
-      const bool s_first = !STATES && gy > 1 && !last;
+      const bool s_first = !STATES && D == 64 && gy > 1 && !last;  // (with one buffer of z its next tile waits for Delta)
       auto delta = [&]() {
         if (!update || !wait(&s.w_full, un++, 22)) return;
         tc_fence_after();
@@ -370,9 +384,9 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       else ++g;
       if (ok && i + 1 < steps) {
         operands();
-        if (!STATES && wait(&s.c_full, i, 24)) {
+        if (!STATES && (two_s ? ok : wait(&s.c_full, i, 24))) {
           tc_fence_after();
-          issue_s();
+          issue_s(i + 1);
           if (Sh::NO > 1 && gx > 1 && g > 0 && old) {  // (the state is the same, and P of this step was made after the last output)
             issue_inter();
             early = true;
@@ -390,6 +404,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       if (lane == 0) mbar_arrive(bar);
     };
     const int light = rev ? (cg == 0 ? quad - 2 : -1) : (cg == 1 && quad < 2 ? quad : -1);  // number among them, or below 0
+    auto o_col = [&](int n) { return COL_O + (two_s ? 0 : n % Sh::NO * D); };
     int g = 0, k = 0, yn = 0, xn = 0, in = 0;  // in: products with the state
     for (int i = 0; i < steps && ok; ++i) {
       const int m = rows_of(k), yb = yn % NY;
@@ -409,6 +424,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       }
       uint32_t a[32];
       if constexpr (!STATES) {
+        if (two_s && g > 0 && !wait(&s.c_full, i - 1, 33)) break;  // (its phases one by one)
         if (!wait(&s.s_full, i, 34)) break;
         tc_fence_after();
         // P over S: a warp's columns become half as many of packed pairs, in the place of their first half
@@ -417,7 +433,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
           const int jb = SQ * cg + q;
           uint32_t b[16];
           if (jb == quad || (jb < quad) != rev) {
-            tmem_ld32(tb + lane_off + COL_S + 32 * jb, a);
+            tmem_ld32(tb + lane_off + s_col(i) + 32 * jb, a);
             if (jb == quad) {
               const float* w = &s.pw[Z0 + (rev ? -lane : lane)];
               tmem_ld_wait();
@@ -443,13 +459,13 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
 #pragma unroll
             for (int e = 0; e < 16; ++e) b[e] = 0;
           }
-          tmem_st16(tb + lane_off + COL_S + SW * cg + 16 * q, b);
+          tmem_st16(tb + lane_off + s_col(i) + SW * cg + 16 * q, b);
         }
         if (inter) {  // what lies before the chunk, weighted
           if (!wait(&s.o_full, in, 35)) break;
           ++in;
           tc_fence_after();
-          tmem_ld32(tb + lane_off + COL_O + xn % Sh::NO * D + 32 * cg, a);
+          tmem_ld32(tb + lane_off + o_col(xn) + 32 * cg, a);
           const float w = s.pw[Z0 + (rev ? max(m - r, 0) : r + 1)];
           const uint64_t ww = f2(w, w);
           tmem_ld_wait();
@@ -458,7 +474,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
             const uint64_t v = f2_mul(f2_bits(a[e], a[e + 1]), ww);
             a[e] = (uint32_t)v, a[e + 1] = (uint32_t)(v >> 32);
           }
-          tmem_st32(tb + lane_off + COL_O + xn % Sh::NO * D + 32 * cg, a);
+          tmem_st32(tb + lane_off + o_col(xn) + 32 * cg, a);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -510,7 +526,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       if (emit) {
         if (!wait(&s.c_full, i, 38)) break;
         tc_fence_after();
-        tmem_ld32(tb + lane_off + COL_O + xn % Sh::NO * D + 32 * cg, a);
+        tmem_ld32(tb + lane_off + o_col(xn) + 32 * cg, a);
         const uint64_t scale = f2(p.scale, p.scale);
         tmem_ld_wait();
 #pragma unroll
