@@ -558,7 +558,8 @@ int path_draft_verify(const path_verify_desc_t* desc, const int* q_start, const 
  * ----------------
  * With a decay g = exp(log_decay[h]) per key head and a state S (head_dim x head_dim, float32):
  *   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
- * log_decay [heads] float32, natural log, kept in [-10000, 0]; NaN makes its head's outputs NaN.
+ * log_decay [heads] float32, natural log, kept in [-10000, 0]; NaN makes its head's outputs NaN.  An infinity or NaN in
+ * a sequence may reach any output of that sequence and head, of earlier tokens too.
  */
 typedef struct {
   int batch, heads_q;  /* heads_q: a multiple of heads (at most 16 times); head hq reads key head hq / (heads_q / heads) */

@@ -104,9 +104,9 @@ static int choose_seg(const LinArgs& p, bool bf16, int seqs, int len, int chunk)
   const int chunks = (len + chunk - 1) / chunk;
   int best = chunks;
   double least = 0;
-  for (int c = chunks; c >= 1; --c) {  // chunks of a segment
-    const int n = (chunks + c - 1) / c;
-    if (n > 1 && (chunks + n - 1) / n != c) continue;  // (fewer chunks make as many segments)
+  for (int s = 1; s <= chunks && s <= full; ++s) {  // segments
+    const int c = (chunks + s - 1) / s, n = (chunks + c - 1) / c;  // chunks of one; as many of those as there then are
+    if (n != s) continue;
     auto waves = [&](double blocks, double one, double all) { return blocks <= 152 ? one : all * (double)(long long)((blocks + full - 1) / full); };
     const double heads = (double)seqs * p.heads * n;
     double cost = c * p.G * waves(heads * p.ops * per_head, t.walk, t.walk_full);
@@ -116,7 +116,7 @@ static int choose_seg(const LinArgs& p, bool bf16, int seqs, int len, int chunk)
       const double states = c * mean * waves(heads * p.slots * per_head, t.state, t.state_full);
       cost += (states > c * most * t.state ? states : c * most * t.state) + 7 + p.D / 64 * 0.45 * n + heads * p.slots * p.D * p.D * 16 / 5e6;
     }
-    if (c == chunks || cost < least) {
+    if (n == 1 || cost < least) {
       least = cost;
       best = c;
     }

@@ -1,7 +1,8 @@
 // Linear attention of single and draft tokens: the recurrence itself, S <- g S + k v^T, o = scale S^T q, token by token, with
 // the state of a slot and key head in one block's registers (float32, read and written once per call).
 // Bound: the state's bytes, 8 D^2 per slot and key head (4 D^2 where it is not written back); with several tokens the paired
-// multiply-adds, 32 and 16 per query head and row of four columns, which shared memory feeds with k and q in float32, twice each.
+// multiply-adds (for a row of four columns four to take a token in, two for each query head), which shared memory feeds with k
+// and q in float32, each number twice.
 #include "dev_common.cuh"
 #include "linear.h"
 #include "tc_common.cuh"

@@ -13,7 +13,8 @@ a PagedCache beside it:
 
 Argument marshalling only: every step runs in the CUDA library, on the current stream of the tensors' device, without
 synchronising (check() does).  Calls that change one cache must be ordered on one stream.  A call can be captured into a
-CUDA graph: q_start and lists are read on the device.
+CUDA graph: q_start and lists are read on the device.  (A training step is captured as torch asks for it: with leaves of
+which no eager graph is alive.)
 """
 from __future__ import annotations
 
@@ -57,7 +58,8 @@ class LinearAttentionFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, do):
         q, k, v, log_decay = ctx.saved_tensors
-        grads = [torch.empty_like(t) if need else None for t, need in zip((q, k, v), ctx.needs_input_grad)]
+        new = torch.empty_like if q.numel() else torch.zeros_like
+        grads = [new(t) if need else None for t, need in zip((q, k, v), ctx.needs_input_grad)]
         if q.numel() and any(g is not None for g in grads):
             _launch(pa.path_linear_bwd, 1, ctx, q, k, v, log_decay, do.contiguous(), *grads)
         return *grads, None, None
@@ -91,7 +93,7 @@ def linear_attention(q, k, v, log_decay, scale=1.0):
     """o [B, heads_q, L, d] of q [B, heads_q, L, d], k and v [B, heads, L, d] (bf16 or float32, one dtype; heads_q a
     multiple of heads: query head hq reads key head hq // (heads_q // heads)) and log_decay [heads] float32, the natural
     logarithm of the decay per token, kept in [-10000, 0].  Sequences begin with a zero state."""
-    if log_decay.requires_grad:
+    if log_decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("log_decay is a constant: linear_attention has no gradient for it")
     return LinearAttentionFunction.apply(q, k, v, log_decay, scale)
 

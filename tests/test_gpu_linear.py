@@ -177,3 +177,53 @@ def test_two_calls_at_once(cuda_lib):
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert all(torch.equal(g[n], w[n]) for n in w)
+
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,L", [("bf16", 64, 2, 1, 3000), ("bf16", 128, 2, 2, 900), ("fp32", 64, 2, 1, 900)])
+@pytest.mark.parametrize("wanted", ["q", "k", "v", "qk", "qv", "kv"])
+def test_some_of_the_gradients(cuda_lib, dtype, d, hq, hkv, L, wanted):
+    """Those that are wanted alone: dk and dv share their segments' states where both are."""
+    from softmax_attention_chunk_gb300.linear import linear_attention
+
+    q, k, v, do = inputs(dtype, d, 1, hq, hkv, L, seed=8)
+    ld = torch.tensor([-0.01, -0.2][:hkv], device=DEV)
+    want = reference(q, k, v, do, ld, 0.2)
+    t = {n: x.clone().requires_grad_(n in wanted) for n, x in zip("qkv", (q, k, v))}
+    o = linear_attention(t["q"], t["k"], t["v"], ld, scale=0.2)
+    for n, g in zip(wanted, torch.autograd.grad(o, [t[n] for n in wanted], do)):
+        check("d" + n, g, *want["d" + n], dtype, terms=L * (hq // hkv) + 2 * d + 64)
+
+
+def test_status_of_a_workspace(cuda_lib):
+    pa = cuda_lib
+    q, k, v, _ = inputs("bf16", 64, 2, 4, 4, 500, seed=9)
+    ld, o = torch.tensor([-0.1] * 4, device=DEV), torch.empty_like(q)
+    desc = pa.path_linear_desc_t(2, 4, 4, 500, 64, pa.PATH_BF16, 1.0)
+    n = pa.path_linear_workspace_size(desc, 0)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)  # (whatever lay there)
+    assert pa.path_linear_fwd(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), ld.data_ptr(), o.data_ptr(), ws.data_ptr(), n, pa._stream()) == 0
+    assert pa.path_linear_workspace_status(desc, ws.data_ptr(), n, pa._stream()) == (0, 0)
+
+
+def test_a_parameter_as_decay_without_gradients(cuda_lib):
+    from softmax_attention_chunk_gb300.linear import linear_attention
+
+    q, k, v, _ = inputs("bf16", 64, 1, 2, 2, 50, seed=10)
+    ld = torch.nn.Parameter(torch.tensor([-0.1, -0.2], device=DEV))
+    with torch.no_grad():
+        assert torch.equal(linear_attention(q, k, v, ld), linear_attention(q, k, v, ld.detach()))
+
+
+def test_outputs_beside_others_in_memory(cuda_lib):
+    """Nothing is written outside o: its neighbours in one allocation stay."""
+    pa = cuda_lib
+    for L, d in ((1, 64), (129, 64), (300, 128)):
+        q, k, v, _ = inputs("bf16", d, 1, 3, 3, L, seed=11)
+        ld = torch.tensor([-0.1, -0.01, -1.0], device=DEV)
+        room = torch.full((q.numel() + 4096,), 5.0, dtype=torch.bfloat16, device=DEV)
+        desc = pa.path_linear_desc_t(1, 3, 3, L, d, pa.PATH_BF16, 1.0)
+        n = pa.path_linear_workspace_size(desc, 0)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        o = room[2048 : 2048 + q.numel()]
+        assert pa.path_linear_fwd(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), ld.data_ptr(), o.data_ptr(), ws.data_ptr(), n, pa._stream()) == 0
+        assert bool((room[:2048] == 5.0).all()) and bool((room[2048 + q.numel() :] == 5.0).all())
