@@ -18,6 +18,8 @@ which no eager graph is alive.)
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 from torch.autograd.function import once_differentiable
 
@@ -129,7 +131,7 @@ class LinearCache:
         self.slots, self.heads, self.head_dim = state.shape[:3]
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.c = pa.path_linear_cache_t(self.slots, self.heads, self.head_dim, pa._DT[dtype], pa._p(state), pa._p(self.status))
-        self._index = self.device.index
+        self._ref, self._index = ctypes.byref(self.c), self.device.index
         self._plans = {}
         if pa.path_linear_extend_workspace_size(self.c, pa.path_linear_step_t(self.heads, 0, 0, 1.0, 1)) == 0:
             raise ValueError("unsupported cache (head_dim 64 or 128, at most 65535 slots and 1024 heads)")
@@ -162,8 +164,8 @@ class LinearCache:
                                  f"{ws.device} contiguous={ws.is_contiguous()}")
         elif chunks:
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        self._call(pa.path_linear_extend, step, None if q_start is None else q_start.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                   log_decay.data_ptr(), out.data_ptr(), None if ws is None else ws.data_ptr(), n)
+        self._call(pa._lib.path_linear_extend, step, None if q_start is None else q_start.data_ptr(), q.data_ptr(), k.data_ptr(),
+                   v.data_ptr(), log_decay.data_ptr(), out.data_ptr(), None if ws is None else ws.data_ptr(), n)
         return out
 
     def _plan(self, q, k, v, q_start, max_new, scale, update):
@@ -186,7 +188,7 @@ class LinearCache:
             raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens, scale {scale}")
         if len(self._plans) >= 1024:
             self._plans.clear()
-        return step, n, min(int(max_new), N) > TOKEN_MAX
+        return ctypes.byref(step), n, min(int(max_new), N) > TOKEN_MAX
 
     def fork(self, parents, children):
         """children[i] takes the state of parents[i] (int32 lists on the device)."""
@@ -195,13 +197,13 @@ class LinearCache:
         if parents.numel() != children.numel():
             raise ValueError("parents and children have different lengths")
         if parents.numel():
-            self._call(pa.path_linear_fork, pa._p(parents), pa._p(children), parents.numel())
+            self._call(pa._lib.path_linear_fork, pa._p(parents), pa._p(children), parents.numel())
 
     def reset(self, slots):
         """The listed slots begin new sequences: their states become zero."""
         self._list(slots, "slots")
         if slots.numel():
-            self._call(pa.path_linear_fork, None, pa._p(slots), slots.numel())
+            self._call(pa._lib.path_linear_fork, None, pa._p(slots), slots.numel())
 
     def check(self):
         """Raises RuntimeError with what the device recorded since the last check; synchronises."""
@@ -215,12 +217,12 @@ class LinearCache:
 
     # ---- helpers ----
     def _call(self, fn, *args):
-        """fn(cache, *args, stream) on the current stream of the cache's device; raises on a status."""
+        """The library's fn(cache, *args, stream) on the current stream of the cache's device; raises on a status."""
         if torch._C._cuda_getDevice() == self._index:  # (as torch.cuda.current_device, without its checks)
-            rc = fn(self.c, *args, torch._C._cuda_getCurrentRawStream(self._index))
+            rc = fn(self._ref, *args, torch._C._cuda_getCurrentRawStream(self._index))
         else:
             with torch.cuda.device(self.device):
-                rc = fn(self.c, *args, pa._stream())
+                rc = fn(self._ref, *args, pa._stream())
         if rc != pa.PATH_OK:
             pa._check(rc, fn.__name__)
 

@@ -23,6 +23,7 @@ lengths, tables and lists on the device.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -44,9 +45,6 @@ class StepPlan(NamedTuple):
     k_row: torch.Tensor     # row of the key pool: page * page_size + place in the page
     v_row: torch.Tensor     # of the value pool
     source: Optional[torch.Tensor]  # row of an earlier packing
-
-def _verify(cache, *args):
-    return pa.path_draft_verify(*args)
 
 
 class PagedCache:
@@ -117,7 +115,7 @@ class PagedCache:
         self.c = pa.path_paged_cache_t(slots, H, d, P, width, kp, vp, pa._DT[k_pool.dtype], p(k_pool), p(v_pool),
                                        p(a_pool), p(k_table), p(v_table), p(seq_len), p(k_ref), p(v_ref),
                                        p(self.status), p(extended), p(a_rest))
-        self._index = self.device.index
+        self._ref, self._index = ctypes.byref(self.c), self.device.index
         self._plans, self._verifications = {}, {}
         self._pages_bytes = pa.path_pages_workspace_size(self.c)
         if self._pages_bytes == 0:
@@ -219,8 +217,9 @@ class PagedCache:
         start = torch.empty(self.slots + 1, dtype=torch.int32, device=self.device)
         maps = torch.empty((count, tokens), dtype=torch.int32, device=self.device)
         at, row = maps.data_ptr(), 4 * tokens
-        self._pages("plan", pa._p(n_new), pa._p(from_start), tokens, start.data_ptr(), at, at + row, at + 2 * row, at + 3 * row,
-                    None if from_start is None else at + 4 * row)
+        self._library(pa._lib.path_pages_plan, self._ref, None if n_new is None else n_new.data_ptr(),
+                      None if from_start is None else from_start.data_ptr(), tokens, start.data_ptr(), at, at + row, at + 2 * row,
+                      at + 3 * row, None if from_start is None else at + 4 * row, self._pages_ws.data_ptr(), self._pages_bytes)
         return StepPlan(start, *maps.unbind(0)) if count == 5 else StepPlan(start, *maps.unbind(0), None)
 
     def verify(self, target, tokens, uniform, draft=None, q_start=None, max_new=None):
@@ -234,11 +233,11 @@ class PagedCache:
         key = (target.shape, target.dtype, target.stride(), None if draft is None else draft.stride(), max_new)
         desc = self._verifications.get(key)
         if desc is None:
-            desc = self._verification(target, draft, max_new)
+            desc = ctypes.byref(self._verification(target, draft, max_new))
             if len(self._verifications) >= 1024:
                 self._verifications.clear()
             self._verifications[key] = desc
-        N = desc.total_tokens
+        N = target.shape[0]
         if target.device != self.device or (draft is not None and (draft.dtype != target.dtype or draft.shape != target.shape
                                                                    or draft.device != self.device)):
             raise ValueError(f"target and draft: expected one type and shape on {self.device}, got {target.dtype} {tuple(target.shape)} on "
@@ -250,8 +249,8 @@ class PagedCache:
         self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
         keep = torch.empty(self.slots, dtype=torch.int32, device=self.device)
         after = torch.empty(self.slots, dtype=torch.int32, device=self.device)
-        self._call(_verify, desc, q_start.data_ptr(), tokens.data_ptr(), uniform.data_ptr(), target.data_ptr(), pa._p(draft),
-                   keep.data_ptr(), after.data_ptr(), self.status.data_ptr())
+        self._library(pa._lib.path_draft_verify, desc, q_start.data_ptr(), tokens.data_ptr(), uniform.data_ptr(), target.data_ptr(),
+                      None if draft is None else draft.data_ptr(), keep.data_ptr(), after.data_ptr(), self.status.data_ptr())
         return keep, after
 
     def _verification(self, target, draft, max_new):
@@ -311,6 +310,16 @@ class PagedCache:
         else:
             with torch.cuda.device(self.device):
                 rc = fn(self.c, *args, pa._stream())
+        if rc != pa.PATH_OK:
+            pa._check(rc, fn.__name__)
+
+    def _library(self, fn, *args):
+        """The library's fn(*args, stream), as _call."""
+        if torch._C._cuda_getDevice() == self._index:
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(self._index))
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, pa._stream())
         if rc != pa.PATH_OK:
             pa._check(rc, fn.__name__)
 
