@@ -214,13 +214,13 @@ class PagedCache:
         if not 0 <= tokens <= 1 << 22:
             raise ValueError(f"tokens must be in 0 .. {1 << 22}, got {tokens}")
         count = 4 if from_start is None else 5
-        start = torch.empty(self.slots + 1, dtype=torch.int32, device=self.device)
-        maps = torch.empty((count, tokens), dtype=torch.int32, device=self.device)
-        at, row = maps.data_ptr(), 4 * tokens
+        flat = torch.empty(count * tokens + self.slots + 1, dtype=torch.int32, device=self.device)
+        *maps, start = flat.split_with_sizes([tokens] * count + [self.slots + 1])
+        at, row = flat.data_ptr(), 4 * tokens
         self._library(pa._lib.path_pages_plan, self._ref, None if n_new is None else n_new.data_ptr(),
-                      None if from_start is None else from_start.data_ptr(), tokens, start.data_ptr(), at, at + row, at + 2 * row,
+                      None if from_start is None else from_start.data_ptr(), tokens, at + count * row, at, at + row, at + 2 * row,
                       at + 3 * row, None if from_start is None else at + 4 * row, self._pages_ws.data_ptr(), self._pages_bytes)
-        return StepPlan(start, *maps.unbind(0)) if count == 5 else StepPlan(start, *maps.unbind(0), None)
+        return StepPlan(start, *maps) if count == 5 else StepPlan(start, *maps, None)
 
     def verify(self, target, tokens, uniform, draft=None, q_start=None, max_new=None):
         """(keep, next), int32 [slots]: how many of each slot's packed tokens stay, the first (known) one among them, and
