@@ -5,9 +5,9 @@
 // (target, draft) that decide the next token, and sums r = max(0, p - q) over it; the slices' sums go round through
 // distributed shared memory, and the block in whose slice the running sum passes uniform * total finds the entry.
 // Sums: the result is an index, so sums that are only nearly right give wrong answers: the running sum passes its goal at
-// another entry with probability (entries) * (error).  double sums would be exact enough and cost 13 us of the GPU's few FP64
-// units for 64 rows of 131072; a lane instead adds pairs of floats (p - q and the sum with their rounding errors, exactly),
-// about 2^-44 of the sum, and only lanes' totals become doubles.
+// another entry with probability (entries) * (error).  Sums are pairs of floats instead, the second what rounding took from the
+// first: about 2^-44 of the sum.  double would be as exact and costs 13 us of the GPU's few FP64 units for 64 rows of 131072
+// (with double for the warps' totals and the search alone: 25 us a call there, 19 without; of 5 tokens 12 and 8).
 #include <cooperative_groups.h>
 
 #include "dev_common.cuh"
@@ -67,19 +67,42 @@ __device__ __forceinline__ void add_pair(float2& sum, float2 r) {
   sum.y += ((sum.x - (t - b)) + (r.x - b)) + r.y;
   sum.x = t;
 }
-__device__ __forceinline__ double warp_scan(double x) {
+__device__ __forceinline__ float2 shfl_up_pair(float2 x, int o) {
+  return make_float2(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o));
+}
+__device__ __forceinline__ float2 shfl_pair(float2 x, int l) {
+  return make_float2(__shfl_sync(0xffffffffu, x.x, l), __shfl_sync(0xffffffffu, x.y, l));
+}
+// The lanes' running sums, N of them at once.
+template <int N> __device__ __forceinline__ void warp_scan(float2 (&x)[N]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double a = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += a;
-  }
-  return x;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float2 a = shfl_up_pair(x[j], o);
+      if (lane >= o) add_pair(x[j], a);
+    }
 }
-// The first lane whose running sum passes goal, or (rounding) the last with a positive part; -1: none is.
-__device__ __forceinline__ int first_past(double upto, double part, double goal) {
-  const unsigned past = __ballot_sync(0xffffffffu, upto > goal && part > 0.0), some = __ballot_sync(0xffffffffu, part > 0.0);
-  return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : -1;
+__device__ __forceinline__ bool some(float2 x) { return x.x + x.y > 0.f; }
+// Whether a sum passes the goal u * all.
+struct Goal {
+  float up;    // of a total so small that products would lose bits (under 2^-60): 2^60
+  float2 goal;
+  __device__ __forceinline__ Goal(float u, float2 all) : up(all.x < 0x1p-60f ? 0x1p60f : 1.f) {
+    goal.x = u * (all.x * up);
+    goal.y = __fmaf_rn(u, all.x * up, -goal.x) + u * (all.y * up);
+  }
+  __device__ __forceinline__ bool passed(float2 sum) const {
+    float2 d = make_float2(sum.x * up, sum.y * up);
+    add_pair(d, make_float2(-goal.x, -goal.y));
+    return some(d);
+  }
+};
+// The first lane whose running sum passes the goal, or (rounding) the last with a positive part; -1: none is.
+__device__ __forceinline__ int first_past(const Goal& goal, float2 upto, float2 part) {
+  const unsigned past = __ballot_sync(0xffffffffu, goal.passed(upto) && some(part)), any = __ballot_sync(0xffffffffu, some(part));
+  return past ? __ffs(past) - 1 : any ? 31 - __clz(any) : -1;
 }
 
 template <typename T, int N>
@@ -87,7 +110,7 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
   chain();
   constexpr int LOADS = STEP / (32 * N);
   constexpr int PER = kMaxCluster * NW / 32;  // warps' sums of the cluster to a lane
-  __shared__ double warp_sum[NW];
+  __shared__ float2 warp_sum[NW];
   __shared__ int first_bad;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -107,7 +130,7 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
   }
   const T* target = (const T*)a.target;
   const T* draft = (const T*)a.draft;
-  const double u = a.uniform[q0];
+  const float u = a.uniform[q0];
   if (warp == 0) {
     int bad = n;
     for (int i0 = 1; i0 < n && bad == n; i0 += 32) {
@@ -152,7 +175,7 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
     return residual(at0 + (j * 32 + lane) * N + i == out ? 0.f : pv[j][i], q ? qv[j][i] : 0.f);
   };
   for (int round = 0; round < 2; ++round) {
-    double mine = 0;  // of step `lane`
+    float2 mine = make_float2(0.f, 0.f);  // of step `lane`
     for (int s = 0; s < steps; ++s) {
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -173,99 +196,102 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         add_pair(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
-      if (lane == s) mine = (double)sum.x + (double)sum.y;
+      if (lane == s) mine = sum;
     }
-    const double upto = warp_scan(mine);
-    if (lane == 31) warp_sum[warp] = upto;
+    float2 upto[1] = {mine};
+    warp_scan(upto);
+    if (lane == 31) warp_sum[warp] = upto[0];
     cluster.sync();
     // every warp finds the cluster's sum, and whether the goal lies in its own share
-    double part[PER];
+    float2 part[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int w = lane * PER + i;
-      part[i] = w < a.slots_cl * NW ? *cluster.map_shared_rank(&warp_sum[w % NW], w / NW) : 0.0;
+      part[i] = w < a.slots_cl * NW ? *cluster.map_shared_rank(&warp_sum[w % NW], w / NW) : make_float2(0.f, 0.f);
     }
     cluster.sync();  // no block leaves, or sums again, while others read its sums
-    double lane_sum = 0;
+    float2 lane_sum = part[0];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) lane_sum += part[i];
-    const double lane_upto = warp_scan(lane_sum);
-    const double all = __shfl_sync(0xffffffffu, lane_upto, 31);
-    if (!(all > 0.0) && round == 0 && (q || out >= 0)) {
+    for (int i = 1; i < PER; ++i) add_pair(lane_sum, part[i]);
+    float2 lane_upto[1] = {lane_sum};
+    warp_scan(lane_upto);
+    const float2 all = shfl_pair(lane_upto[0], 31);
+    if (!some(all) && round == 0 && (q || out >= 0)) {
       q = nullptr;  // nothing is left of the target: its own row
       out = -1;
       continue;
     }
-    const double goal = u * all;
-    const int l = first_past(lane_upto, lane_sum, goal);
+    const Goal goal(u, all);
+    const int l = first_past(goal, lane_upto[0], lane_sum);
     if (l < 0) {
       if (rank == 0 && tid == 0) a.next[b] = -1;
       return;
     }
-    const double before_lane = lane_upto - lane_sum;
     // the first part at which the running sum passes
-    double run = before_lane, at_owner = before_lane;
+    float2 run = shfl_up_pair(lane_upto[0], 1);
+    if (lane == 0) run = make_float2(0.f, 0.f);
+    float2 at_owner = run;
     bool there = false;
     int owner = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      if (!there && part[i] > 0.0) {
+      const float2 old = run;
+      add_pair(run, part[i]);
+      if (!there && some(part[i])) {
         owner = i;
-        at_owner = run;
-        there = run + part[i] > goal;
+        at_owner = old;
+        there = goal.passed(run);
       }
-      run += part[i];
     }
     owner = __shfl_sync(0xffffffffu, lane * PER + owner, l);
-    double before = __shfl_sync(0xffffffffu, at_owner, l);
+    float2 before = shfl_pair(at_owner, l);
     if (owner != rank * NW + warp) return;
-    const int s = first_past(before + upto, mine, goal);
+    float2 past = before;
+    add_pair(past, upto[0]);
+    const int s = first_past(goal, past, mine);
     if (s < 0) {  // (an infinity in the row)
       if (lane == 0) a.next[b] = -1;
       return;
     }
-    const double prev = __shfl_sync(0xffffffffu, upto, s > 0 ? s - 1 : 0);
-    if (s > 0) before += prev;
+    const float2 prev = shfl_pair(upto[0], s > 0 ? s - 1 : 0);
+    if (s > 0) add_pair(before, prev);
     // the step's entries again, exactly
     load(v0 + s * STEP);
-    double sum_j[LOADS], upto_j[LOADS];
+    float2 sum_j[LOADS], upto_j[LOADS];
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < N; ++i) add_pair(sum, entry(v0 + s * STEP, j, i));
-      upto_j[j] = sum_j[j] = (double)sum.x + (double)sum.y;
+      upto_j[j] = sum_j[j] = sum;
     }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j) {
-        const double x = __shfl_up_sync(0xffffffffu, upto_j[j], o);
-        if (lane >= o) upto_j[j] += x;
-      }
+    warp_scan(upto_j);
     int found = -1;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      const unsigned past = __ballot_sync(0xffffffffu, before + upto_j[j] > goal && sum_j[j] > 0.0);
-      const unsigned some = __ballot_sync(0xffffffffu, sum_j[j] > 0.0);
-      if (some) {
-        const int w = past ? __ffs(past) - 1 : 31 - __clz(some);  // (in case rounding lets none pass: the last)
-        double at = before + (upto_j[j] - sum_j[j]);
+      float2 upto = before;
+      add_pair(upto, upto_j[j]);
+      const unsigned past = __ballot_sync(0xffffffffu, goal.passed(upto) && some(sum_j[j]));
+      const unsigned any = __ballot_sync(0xffffffffu, some(sum_j[j]));
+      if (any) {
+        const int w = past ? __ffs(past) - 1 : 31 - __clz(any);  // (in case rounding lets none pass: the last)
+        float2 at = shfl_up_pair(upto, 1);
+        if (lane == 0) at = before;
         int x = -1;
         bool passed = false;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float2 r = entry(v0 + s * STEP, j, i);
-          at += (double)r.x + (double)r.y;
+          add_pair(at, r);
           if (r.x > 0.f && !passed) {
             x = v0 + s * STEP + (j * 32 + lane) * N + i;
-            passed = at > goal;
+            passed = goal.passed(at);
           }
         }
         found = __shfl_sync(0xffffffffu, x, w);
         if (past) break;
       }
-      before += __shfl_sync(0xffffffffu, upto_j[j], 31);
+      before = shfl_pair(upto, 31);
     }
     if (lane == 0) a.next[b] = found;
     return;
