@@ -2,8 +2,8 @@
 // and the draw of the token after them, one cluster of blocks per slot.
 //
 // Every block of the cluster finds the first draft not kept (a few loads), takes a slice of the one row (target) or two
-// (target, draft) that decide the next token, and sums r = max(0, p - q) over it; the slices' sums go round through
-// distributed shared memory, and the block in whose slice the running sum passes uniform * total finds the entry.
+// (target, draft) that decide the next token, and sums r = max(0, p - q) over it; every warp writes its sum to every block of the
+// cluster, and the warp in whose share the running sum passes uniform * total finds the entry.
 // Sums: the result is an index, so sums that are only nearly right give wrong answers: the running sum passes its goal at
 // another entry with probability (entries) * (error).  Sums are pairs of floats instead, the second what rounding took from the
 // first: about 2^-44 of the sum.  double would be as exact and costs 13 us of the GPU's few FP64 units for 64 rows of 131072
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
   chain();
   constexpr int LOADS = STEP / (32 * N);
   constexpr int PER = kMaxCluster * NW / 32;  // warps' sums of the cluster to a lane
-  __shared__ float2 warp_sum[NW];
+  __shared__ float2 warp_sum[2][kMaxCluster * NW];  // of every warp of the cluster; one for each round
   __shared__ int first_bad;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
     if (rank == 0 && tid == 0) a.keep[b] = 0, a.next[b] = -1;
     return;
   }
+  auto started = cluster.barrier_arrive();  // (waited for before the others' shared memory is written)
   const T* target = (const T*)a.target;
   const T* draft = (const T*)a.draft;
   const float u = a.uniform[q0];
@@ -200,16 +201,17 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
     }
     float2 upto[1] = {mine};
     warp_scan(upto);
-    if (lane == 31) warp_sum[warp] = upto[0];
-    cluster.sync();
+    const float2 total = shfl_pair(upto[0], 31);
+    if (round == 0) cluster.barrier_wait(std::move(started));
+    if (lane < a.slots_cl) *cluster.map_shared_rank(&warp_sum[round][rank * NW + warp], lane) = total;
+    cluster.sync();  // (the only one of a round: a block that leaves after it has written and been written to)
     // every warp finds the cluster's sum, and whether the goal lies in its own share
     float2 part[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int w = lane * PER + i;
-      part[i] = w < a.slots_cl * NW ? *cluster.map_shared_rank(&warp_sum[w % NW], w / NW) : make_float2(0.f, 0.f);
+      part[i] = w < a.slots_cl * NW ? warp_sum[round][w] : make_float2(0.f, 0.f);
     }
-    cluster.sync();  // no block leaves, or sums again, while others read its sums
     float2 lane_sum = part[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) add_pair(lane_sum, part[i]);
