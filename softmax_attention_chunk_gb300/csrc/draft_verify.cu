@@ -7,21 +7,29 @@
 // Sums: the result is an index, so sums that are only nearly right give wrong answers: the running sum passes its goal at
 // another entry with probability (entries) * (error).  Sums are pairs of floats instead, the second what rounding took from the
 // first: about 2^-44 of the sum.  double would be as exact and costs 13 us of the GPU's few FP64 units for 64 rows of 131072
-// (with double for the warps' totals and the search alone: 25 us a call there, 19 without; of 5 tokens 12 and 8).
+// (with double for the warps' totals and the search alone: 25 us a call there, 19 without; of 5 tokens 12 and 8).  The sums of
+// two entries at a time by paired arithmetic: 19 -> 16.5 us with the rows in L2.
+// Bound: the rows' bytes, behind a chain of dependent loads (q_start, tokens, their probabilities) and before the search.  A
+// warp keeps four loads of each row on their way through shared memory (64 rows of 131072 from HBM: 21 -> 17 us; asked for in
+// L2 ahead of loads to registers instead: 24).
 #include <cooperative_groups.h>
 
 #include "dev_common.cuh"
 #include "paged.h"
+#include "tc_common.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace pathattn {
 namespace {
 
+using namespace tc;
+
 constexpr int NT = 256, NW = NT / 32;
 constexpr int STEP = 512;        // entries whose sum a warp keeps apart
 constexpr int kMaxSteps = 32;    // steps of a warp: one lane each in the search
 constexpr int kMaxCluster = 8;
+constexpr int RING = 5;          // loads of a warp in shared memory, all but one on their way
 
 struct VerifyArgs {
   path_verify_desc_t d;
@@ -55,9 +63,16 @@ template <typename T, int N> __device__ __forceinline__ void load_n(const T* a, 
   }
 }
 
+// 16 bytes to shared memory, zeros where there are none.
+__device__ __forceinline__ void cp_16(void* to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Residual max(0, p - q) as an exact pair (hi, lo).
 __device__ __forceinline__ float2 residual(float p, float q) {
-  if (!(p > q)) return make_float2(0.f, 0.f);
+  q = fminf(p, q);
   const float s = p - q;
   return make_float2(s, (p - s) - q);  // exact: p >= q >= 0
 }
@@ -67,6 +82,24 @@ __device__ __forceinline__ void add_pair(float2& sum, float2 r) {
   sum.y += ((sum.x - (t - b)) + (r.x - b)) + r.y;
   sum.x = t;
 }
+// The residuals of two entries to two sums, by paired arithmetic.
+struct TwoSums {
+  uint64_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(uint64_t p, uint64_t q) {  // p >= q
+    const uint64_t minus = f2(-1.f, -1.f), s = f2_fma(q, minus, p), rest = f2_fma(q, minus, f2_fma(s, minus, p));
+    const uint64_t t = f2_add(hi, s), b = f2_fma(hi, minus, t);
+    lo = f2_add(lo, f2_add(f2_add(f2_fma(f2_fma(b, minus, t), minus, hi), f2_fma(b, minus, s)), rest));
+    hi = t;
+  }
+  __device__ __forceinline__ float2 sum() const {
+    float a, b, c, d;
+    f2_split(hi, a, b);
+    f2_split(lo, c, d);
+    float2 x = make_float2(a, c);
+    add_pair(x, make_float2(b, d));
+    return x;
+  }
+};
 __device__ __forceinline__ float2 shfl_up_pair(float2 x, int o) {
   return make_float2(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o));
 }
@@ -109,9 +142,11 @@ template <typename T, int N>
 __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a) {
   chain();
   constexpr int LOADS = STEP / (32 * N);
+  constexpr int PAIR = N > 1 ? 1 : 2;          // loads whose entries are taken in pairs
   constexpr int PER = kMaxCluster * NW / 32;  // warps' sums of the cluster to a lane
   __shared__ float2 warp_sum[2][kMaxCluster * NW];  // of every warp of the cluster; one for each round
   __shared__ int first_bad;
+  __shared__ __align__(16) uint8_t ring[N > 1 ? NW : 1][RING][2][32][16];
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster.block_rank(), b = blockIdx.x / a.slots_cl;
@@ -163,37 +198,47 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
   int out = !draft && bad < n ? a.tokens[q0 + bad] : -1;  // the entry that is left out of p
   const int vocab = a.d.vocab, steps = a.tile / STEP;
   const int v0 = (rank * NW + warp) * a.tile;
-  float pv[LOADS][N], qv[LOADS][N];
-  auto load = [&](int at0) {
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const int at = at0 + (j * 32 + lane) * N;
-      load_n<T, N>(p + at, vocab - at, pv[j]);
-      if (q) load_n<T, N>(q + at, vocab - at, qv[j]);
+  // The warp's i-th 512 bytes of each row on their way to shared memory: a lane's 16 bytes are its own, nobody else waits.
+  auto fetch = [&](int i) {
+    const int at = v0 + (i * 32 + lane) * N;
+    if (i < steps * LOADS) {
+      cp_16(ring[warp][i % RING][0][lane], at < vocab ? p + at : p, at < vocab);
+      if (q) cp_16(ring[warp][i % RING][1][lane], at < vocab ? q + at : q, at < vocab);
     }
-  };
-  auto entry = [&](int at0, int j, int i) {
-    return residual(at0 + (j * 32 + lane) * N + i == out ? 0.f : pv[j][i], q ? qv[j][i] : 0.f);
+    cp_commit();
   };
   for (int round = 0; round < 2; ++round) {
     float2 mine = make_float2(0.f, 0.f);  // of step `lane`
+    if constexpr (N > 1)
+      for (int i = 0; i < RING - 1; ++i) fetch(i);
     for (int s = 0; s < steps; ++s) {
-      float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {  // (in halves: registers for four blocks to an SM, which keep more loads on their way)
-        constexpr int H = LOADS / 2;
-        float ph[H][N], qh[H][N];
-        const int at0 = v0 + s * STEP + half * (STEP / 2) + lane * N;
-#pragma unroll
-        for (int j = 0; j < H; ++j) {
-          load_n<T, N>(p + at0 + j * 32 * N, vocab - at0 - j * 32 * N, ph[j]);
-          if (q) load_n<T, N>(q + at0 + j * 32 * N, vocab - at0 - j * 32 * N, qh[j]);
+      TwoSums sums;
+#pragma unroll(N > 1 ? LOADS : 2)
+      for (int j = 0; j < LOADS; j += PAIR) {
+        float pv[PAIR * N], qv[PAIR * N];
+        const int from = v0 + s * STEP + j * 32 * N;
+        if constexpr (N > 1) {
+          const int i = s * LOADS + j;
+          cp_wait<RING - 2>();
+          load_n<T, N>((const T*)ring[warp][i % RING][0][lane], 1, pv);
+          if (q) load_n<T, N>((const T*)ring[warp][i % RING][1][lane], 1, qv);
+          fetch(i + RING - 1);
+        } else {
+          for (int i = 0; i < PAIR; ++i) {
+            const int at = from + 32 * i + lane;
+            load_n<T, N>(p + at, vocab - at, *reinterpret_cast<float(*)[N]>(pv + i));
+            if (q) load_n<T, N>(q + at, vocab - at, *reinterpret_cast<float(*)[N]>(qv + i));
+          }
         }
+        if (out >= from && out < from + PAIR * 32 * N)
 #pragma unroll
-        for (int j = 0; j < H; ++j)
+          for (int i = 0; i < PAIR * N; ++i)
+            if (from + i / N * 32 * N + lane * N + i % N == out) pv[i] = 0.f;
 #pragma unroll
-          for (int i = 0; i < N; ++i) add_pair(sum, residual(at0 + j * 32 * N + i == out ? 0.f : ph[j][i], q ? qh[j][i] : 0.f));
+        for (int i = 0; i < PAIR * N; i += 2)
+          sums.add(f2(pv[i], pv[i + 1]), q ? f2(fminf(pv[i], qv[i]), fminf(pv[i + 1], qv[i + 1])) : 0);
       }
+      float2 sum = sums.sum();
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         add_pair(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
@@ -257,43 +302,44 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
     }
     const float2 prev = shfl_pair(upto[0], s > 0 ? s - 1 : 0);
     if (s > 0) add_pair(before, prev);
-    // the step's entries again, exactly
-    load(v0 + s * STEP);
-    float2 sum_j[LOADS], upto_j[LOADS];
+    // the step's entries again: 16 to a lane, then those of the lane at which the sum passes, one to a lane
+    const int e0 = v0 + s * STEP + lane * (STEP / 32);
+    TwoSums sums;
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      float2 sum = make_float2(0.f, 0.f);
+    for (int j = 0; j < STEP / 32; j += N < 2 ? 2 : N) {
+      float pv[N < 2 ? 2 : N], qv[N < 2 ? 2 : N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) add_pair(sum, entry(v0 + s * STEP, j, i));
-      upto_j[j] = sum_j[j] = sum;
-    }
-    warp_scan(upto_j);
-    int found = -1;
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      float2 upto = before;
-      add_pair(upto, upto_j[j]);
-      const unsigned past = __ballot_sync(0xffffffffu, goal.passed(upto) && some(sum_j[j]));
-      const unsigned any = __ballot_sync(0xffffffffu, some(sum_j[j]));
-      if (any) {
-        const int w = past ? __ffs(past) - 1 : 31 - __clz(any);  // (in case rounding lets none pass: the last)
-        float2 at = shfl_up_pair(upto, 1);
-        if (lane == 0) at = before;
-        int x = -1;
-        bool passed = false;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float2 r = entry(v0 + s * STEP, j, i);
-          add_pair(at, r);
-          if (r.x > 0.f && !passed) {
-            x = v0 + s * STEP + (j * 32 + lane) * N + i;
-            passed = goal.passed(at);
-          }
-        }
-        found = __shfl_sync(0xffffffffu, x, w);
-        if (past) break;
+      for (int i = 0; i < (N < 2 ? 2 : 1); ++i) {
+        load_n<T, N>(p + e0 + j + i, vocab - e0 - j - i, *reinterpret_cast<float(*)[N]>(pv + i));
+        if (q) load_n<T, N>(q + e0 + j + i, vocab - e0 - j - i, *reinterpret_cast<float(*)[N]>(qv + i));
       }
-      before = shfl_pair(upto, 31);
+#pragma unroll
+      for (int i = 0; i < (N < 2 ? 2 : N); i += 2) {
+        const float p0 = e0 + j + i == out ? 0.f : pv[i], p1 = e0 + j + i + 1 == out ? 0.f : pv[i + 1];
+        sums.add(f2(p0, p1), q ? f2(fminf(p0, qv[i]), fminf(p1, qv[i + 1])) : 0);
+      }
+    }
+    const float2 own = sums.sum();
+    float2 own_upto[1] = {own};
+    warp_scan(own_upto);
+    past = before;
+    add_pair(past, own_upto[0]);
+    const int w = first_past(goal, past, own);
+    int found = -1;
+    if (w >= 0) {
+      const float2 less = shfl_pair(own_upto[0], w > 0 ? w - 1 : 0);
+      if (w > 0) add_pair(before, less);
+      const int x = v0 + s * STEP + w * (STEP / 32) + lane, left = lane < STEP / 32 && x != out ? vocab - x : 0;
+      float px[1], qx[1] = {0.f};
+      load_n<T, 1>(p + x, left, px);
+      if (q) load_n<T, 1>(q + x, left, qx);
+      const float2 r = residual(px[0], qx[0]);
+      float2 r_upto[1] = {r};
+      warp_scan(r_upto);
+      past = before;
+      add_pair(past, r_upto[0]);
+      const int i = first_past(goal, past, r);
+      if (i >= 0) found = x - lane + i;
     }
     if (lane == 0) a.next[b] = found;
     return;
