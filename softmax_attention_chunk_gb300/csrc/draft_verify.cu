@@ -10,7 +10,7 @@
 // (with double for the warps' totals and the search alone: 25 us a call there, 19 without; of 5 tokens 12 and 8).  The sums of
 // two entries at a time by paired arithmetic: 19 -> 16.5 us with the rows in L2.
 // Bound: the rows' bytes, behind a chain of dependent loads (q_start, tokens, their probabilities) and before the search.  A
-// warp keeps four loads of each row on their way through shared memory (64 rows of 131072 from HBM: 21 -> 17 us; asked for in
+// warp keeps three loads of each row on their way through shared memory (64 rows of 131072 from HBM: 21 -> 17 us; asked for in
 // L2 ahead of loads to registers instead: 24).
 #include <cooperative_groups.h>
 
@@ -29,7 +29,7 @@ constexpr int NT = 256, NW = NT / 32;
 constexpr int STEP = 512;        // entries whose sum a warp keeps apart
 constexpr int kMaxSteps = 32;    // steps of a warp: one lane each in the search
 constexpr int kMaxCluster = 8;
-constexpr int RING = 5;          // loads of a warp in shared memory, all but one on their way
+constexpr int RING = 4;          // loads of a warp in shared memory, all but one on their way
 
 struct VerifyArgs {
   path_verify_desc_t d;
@@ -198,19 +198,23 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
   int out = !draft && bad < n ? a.tokens[q0 + bad] : -1;  // the entry that is left out of p
   const int vocab = a.d.vocab, steps = a.tile / STEP;
   const int v0 = (rank * NW + warp) * a.tile;
-  // The warp's i-th 512 bytes of each row on their way to shared memory: a lane's 16 bytes are its own, nobody else waits.
-  auto fetch = [&](int i) {
-    const int at = v0 + (i * 32 + lane) * N;
-    if (i < steps * LOADS) {
-      cp_16(ring[warp][i % RING][0][lane], at < vocab ? p + at : p, at < vocab);
-      if (q) cp_16(ring[warp][i % RING][1][lane], at < vocab ? q + at : q, at < vocab);
-    }
+  // The warp's next 512 bytes of each row on their way to shared memory: a lane's 16 bytes are its own, nobody else waits.
+  int coming = 0;
+  const int stop = min(vocab, v0 + a.tile);
+  auto fetch = [&](int slot) {
+    const int at = min(coming, vocab - N);
+    cp_16(ring[warp][slot][0][lane], p + at, coming < stop);
+    if (q) cp_16(ring[warp][slot][1][lane], q + at, coming < stop);
     cp_commit();
+    coming += 32 * N;
   };
   for (int round = 0; round < 2; ++round) {
     float2 mine = make_float2(0.f, 0.f);  // of step `lane`
-    if constexpr (N > 1)
+    if constexpr (N > 1) {
+      coming = v0 + lane * N;
+#pragma unroll
       for (int i = 0; i < RING - 1; ++i) fetch(i);
+    }
     for (int s = 0; s < steps; ++s) {
       TwoSums sums;
 #pragma unroll(N > 1 ? LOADS : 2)
@@ -218,11 +222,11 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
         float pv[PAIR * N], qv[PAIR * N];
         const int from = v0 + s * STEP + j * 32 * N;
         if constexpr (N > 1) {
-          const int i = s * LOADS + j;
+          const int i = LOADS % RING ? s * LOADS + j : j;
           cp_wait<RING - 2>();
           load_n<T, N>((const T*)ring[warp][i % RING][0][lane], 1, pv);
           if (q) load_n<T, N>((const T*)ring[warp][i % RING][1][lane], 1, qv);
-          fetch(i + RING - 1);
+          fetch((i + RING - 1) % RING);
         } else {
           for (int i = 0; i < PAIR; ++i) {
             const int at = from + 32 * i + lane;
