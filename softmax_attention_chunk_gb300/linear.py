@@ -28,7 +28,7 @@ from . import path_attn as pa
 TOKEN_MAX = 16  # new tokens of a slot up to which no workspace is used
 
 
-_sizes = {}  # (descriptor's numbers, backward?) -> workspace bytes
+_descs = {}  # (descriptor's numbers, backward?) -> reference to the descriptor, workspace bytes
 
 
 class LinearAttentionFunction(torch.autograd.Function):
@@ -42,46 +42,56 @@ class LinearAttentionFunction(torch.autograd.Function):
             raise ValueError(f"q is [B, heads_q, L, d], k and v [B, heads, L, d], got {tuple(q.shape)} and {tuple(k.shape)}")
         B, hq, L, d = q.shape
         H = k.shape[1]
-        for name, t, want, shape in (("q", q, dt, (B, hq, L, d)), ("k", k, dt, (B, H, L, d)), ("v", v, dt, (B, H, L, d)),
-                                     ("log_decay", log_decay, torch.float32, (H,))):
-            if t.dtype is not want or t.shape != shape or not t.is_cuda:
+        at = q.get_device()  # (below 0: host memory)
+        if not (at >= 0 and k.dtype is dt and v.dtype is dt and log_decay.dtype is torch.float32 and k.shape == (B, H, L, d)
+                and v.shape == k.shape and log_decay.shape == (H,) and k.get_device() == at and v.get_device() == at
+                and log_decay.get_device() == at):
+            for name, t, want, shape in (("q", q, dt, (B, hq, L, d)), ("k", k, dt, (B, H, L, d)), ("v", v, dt, (B, H, L, d)),
+                                         ("log_decay", log_decay, torch.float32, (H,))):
                 pa._need(t, want, shape, name)
-            if t.device != q.device:
-                raise ValueError(f"{name} lies on {t.device}, q on {q.device}")
+                if t.device != q.device:
+                    raise ValueError(f"{name} lies on {t.device}, q on {q.device}")
         o = torch.empty_like(q)
         ctx.save_for_backward(q, k, v, log_decay)
-        ctx.sizes = (B, hq, H, L, d, pa._DT[dt])
-        ctx.scale = float(scale)
+        ctx.desc = (B, hq, H, L, d, pa._DT[dt], float(scale))
         if q.numel():
-            _launch(pa.path_linear_fwd, 0, ctx, q, k, v, log_decay, o)
+            _launch(pa._lib.path_linear_fwd, 0, ctx.desc, q, k, v, log_decay, o)
         return o
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, do):
-        q, k, v, log_decay = ctx.saved_tensors
-        new = torch.empty_like if q.numel() else torch.zeros_like
-        grads = [new(t) if need else None for t, need in zip((q, k, v), ctx.needs_input_grad)]
-        if q.numel() and any(g is not None for g in grads):
-            _launch(pa.path_linear_bwd, 1, ctx, q, k, v, log_decay, do.contiguous(), *grads)
-        return *grads, None, None
+        # (only a graph of the gradients themselves needs to know that there is none)
+        return _backward_once(ctx, do) if torch.is_grad_enabled() else _backward(ctx, do)
 
 
-def _launch(fn, for_backward, ctx, q, *tensors):
-    desc = pa.path_linear_desc_t(*ctx.sizes, ctx.scale)
-    key = (ctx.sizes, for_backward)
-    n = _sizes.get(key)
-    if n is None:
+def _backward(ctx, do):
+    q, k, v, log_decay = ctx.saved_tensors
+    new = torch.empty_like if q.numel() else torch.zeros_like
+    dq, dk, dv = [new(t) if need else None for t, need in zip((q, k, v), ctx.needs_input_grad)]
+    if q.numel() and not (dq is dk is dv is None):
+        _launch(pa._lib.path_linear_bwd, 1, ctx.desc, q, k, v, log_decay, do.contiguous(), dq, dk, dv)
+    return dq, dk, dv, None, None
+
+
+_backward_once = once_differentiable(_backward)
+
+
+def _launch(fn, for_backward, numbers, q, *tensors):
+    key = (numbers, for_backward)
+    made = _descs.get(key)
+    if made is None:
+        desc = pa.path_linear_desc_t(*numbers)
         n = pa.path_linear_workspace_size(desc, for_backward)
         if n == 0:
             raise ValueError(f"linear_attention: {desc.heads_q} query heads over {desc.heads} (a multiple, at most 16 times), "
                              f"head dim {desc.head_dim} (64 or 128), scale {desc.scale}, or sizes out of range")
-        if len(_sizes) >= 1024:
-            _sizes.clear()
-        _sizes[key] = n
+        if len(_descs) >= 1024:
+            _descs.clear()
+        _descs[key] = made = (ctypes.byref(desc), n)
+    desc, n = made
     ws = torch.empty(n, dtype=torch.uint8, device=q.device)
     args = [None if t is None else t.data_ptr() for t in tensors]
-    index = q.device.index
+    index = q.get_device()
     if torch._C._cuda_getDevice() == index:  # (as torch.cuda.current_device, without its checks)
         rc = fn(desc, q.data_ptr(), *args, ws.data_ptr(), n, torch._C._cuda_getCurrentRawStream(index))
     else:
