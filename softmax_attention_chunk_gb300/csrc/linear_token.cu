@@ -26,20 +26,28 @@ template <> __device__ __forceinline__ void load4s<__nv_bfloat16>(const __nv_bfl
   v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
 }
 
+template <typename T> __device__ __forceinline__ void store4(T* a, const float (&v)[4], float scale);
+template <> __device__ __forceinline__ void store4<float>(float* a, const float (&v)[4], float scale) {
+  *reinterpret_cast<float4*>(a) = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+}
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* a, const float (&v)[4], float scale) {
+  *reinterpret_cast<uint2*>(a) = make_uint2(pack_bf16(v[0] * scale, v[1] * scale), pack_bf16(v[2] * scale, v[3] * scale));
+}
+
 // Rows of o (token, query head) whose sums the warps join at once; floats of a token in shared memory: k twice, v, q twice;
 // tokens there at once.
-template <int D> constexpr int kJoin = D == 64 ? 8 : 4;
+constexpr int kJoin = 8;
 PATH_HD int token_floats(int D, int G) { return (3 + 2 * G) * D; }
 PATH_HD int token_batch(int D, int G) { return kTokenBytes / (4 * token_floats(D, G)); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
+__global__ void __launch_bounds__(NT, D == 64 ? 4 : 2) linear_token_kernel(const LinArgs p) {
   chain();
   if (p.max_new > kLinTokenMax && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.err = 0;  // (of the kernels that follow)
   constexpr int CG = D / 4;      // lanes of a row, four columns each
   constexpr int RG = NT / CG;    // row groups
   constexpr int RP = D / RG;     // rows of a thread, one behind the other
-  constexpr int OB = kJoin<D>;
+  constexpr int OB = kJoin;
   extern __shared__ __align__(16) float smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = tid % CG * 4, r0 = tid / CG * RP;
@@ -61,15 +69,17 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
   for (int t0 = 0; t0 < n; t0 += batch) {
     const int m = min(batch, n - t0);
     __syncthreads();  // the batch before has been read
-    for (int e = tid * 4; e < m * (2 + G) * D; e += NT * 4) {
-      const int t = e / ((2 + G) * D), x = e / D % (2 + G), col = e % D;
+    // a row (k, v or a head's q of a token) to D / 4 threads
+    for (int t = 0, x = tid / CG;; x += RG) {
+      while (x >= 2 + G) x -= 2 + G, ++t;
+      if (t >= m) break;
       const long long at = sp.q0 + t0 + t;
       float a[4];
-      load4s<T>(x == 0 ? (const T*)op.y + at * op.yt + h * op.yh + col
-                : x == 1 ? (const T*)op.z + at * op.yt + h * op.yh + col
-                         : (const T*)op.x + at * op.xt + (long long)(h * G + x - 2) * op.xh + col,
+      load4s<T>(x == 0 ? (const T*)op.y + at * op.yt + h * op.yh + c
+                : x == 1 ? (const T*)op.z + at * op.yt + h * op.yh + c
+                         : (const T*)op.x + at * op.xt + (long long)(h * G + x - 2) * op.xh + c,
                 a);
-      float* to = smem + t * per + (x == 0 ? 2 * col : x == 1 ? 2 * D + col : (2 * x - 1) * D + 2 * col);
+      float* to = smem + t * per + (x == 0 ? 2 * c : x == 1 ? 2 * D + c : (2 * x - 1) * D + 2 * c);
       if (x == 1) {
         *reinterpret_cast<float4*>(to) = make_float4(a[0], a[1], a[2], a[3]);
       } else {
@@ -80,7 +90,7 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
     __syncthreads();
     T* o = (T*)op.o + (long long)(sp.q0 + t0) * op.xt + (long long)h * G * op.xh;
     const float* at = smem;
-    int g = 0, tj = 0, gj = 0;  // head; token and head of the first row not joined yet
+    int g = 0;  // head
     const int rows = m * G;
     for (int i = 0; i < rows; ++i) {
       if (g == 0) {
@@ -116,16 +126,19 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
       const int done = i % OB + 1;
       if (done == OB || i + 1 == rows) {
         __syncthreads();  // (the other half of red was read before the block came here)
-        for (int e = tid; e < done * D; e += NT) {
-          const int row = gj + e / D, col = e % D;
-          float sum = 0.f;
+        const int j = tid / CG;
+        if (j < done) {
+          const float* from = red + ((buf * OB + j) * W) * D + c;
+          float sum[4] = {};
 #pragma unroll
-          for (int w = 0; w < W; ++w) sum += red[((buf * OB + e / D) * W + w) * D + col];
-          o[(tj + row / G) * op.xt + (long long)(row % G) * op.xh + col] = from_f<T>(sum * p.scale);
+          for (int w = 0; w < W; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(from + w * D);
+            sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+          }
+          const unsigned row = i + 1 - done + j, t = row / (unsigned)G, gr = row % (unsigned)G;
+          store4<T>(o + t * op.xt + gr * op.xh + c, sum, p.scale);
         }
         buf ^= 1;
-        tj += (gj + done) / G;
-        gj = (gj + done) % G;
       }
     }
   }
@@ -136,7 +149,7 @@ __global__ void __launch_bounds__(NT) linear_token_kernel(const LinArgs p) {
 
 template <typename T, int D> cudaError_t launch(const LinArgs& p, cudaStream_t st) {
   const int most = p.max_new < kLinTokenMax ? p.max_new : kLinTokenMax, fits = token_batch(D, p.G), batch = most < fits ? most : fits;
-  const int rows = most * p.G <= kJoin<D> ? most * p.G : 2 * kJoin<D>;
+  const int rows = most * p.G <= kJoin ? most * p.G : 2 * kJoin;
   const size_t smem = sizeof(float) * (batch * token_floats(D, p.G) + W * D * rows);
   if (smem > 48 << 10) {
     cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
