@@ -10,7 +10,8 @@
 // meanwhile.  The chain from chunk to chunk is P, P Z and Delta, State and the product with it.
 //
 // Roundings beside the output's: P and Y' to bf16, the operands' type (relative 2^-8; what reaches an output is the sum of
-// independent ones).  Where the state is an output itself (serving) Y' is the sum of three bf16 numbers, as exact as float32.
+// independent ones; of few sequences of one chunk P is two bf16 numbers).  Where the state is an output itself (serving) Y' is
+// the sum of three bf16 numbers, as exact as float32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -120,7 +121,8 @@ template <int PARTS> __device__ __forceinline__ void weighted(uint4 y, float w, 
   for (int t = 0; t < PARTS; ++t) out[t] = make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
 }
 
-template <int D, bool STATES, int PARTS>
+// FINE: P as two bf16 numbers.
+template <int D, bool STATES, int PARTS, bool FINE>
 __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
     linear_tc_kernel(const __grid_constant__ LinMaps maps, const LinArgs p) {
   chain();
@@ -365,8 +367,11 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
         const uint32_t d_s = tbu + uniform(s_col(i));
         auto at_p = [&](int e) { return d_s + 16 * e / SW * SW + 16 * e % SW / 2; };  // of 16 tokens
 #pragma unroll
-        for (int e = 0; e < 8; e += 4)
+        for (int e = 0; e < 8; e += 4) {
           mma4_ts<128>(o_at(on), at_p(e), at_p(e + 1), at_p(e + 2), at_p(e + 3), md + (a_z + 128u * e), id_o, e ? 1u : first);
+          constexpr int R = SW / 2;  // what rounding left of P, behind it
+          if (FINE) mma4_ts<128>(o_at(on), at_p(e) + R, at_p(e + 1) + R, at_p(e + 2) + R, at_p(e + 3) + R, md + (a_z + 128u * e), id_o, 1u);
+        }
         commit_elect(&s.c_full);
       }
       // Delta, and S of the next step; S first where no state waits for Delta
@@ -427,11 +432,17 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
         if (two_s && g > 0 && !wait(&s.c_full, i - 1, 33)) break;  // (its phases one by one)
         if (!wait(&s.s_full, i, 34)) break;
         tc_fence_after();
-        // P over S: a warp's columns become half as many of packed pairs, in the place of their first half
+        // P over S: a warp's columns become half as many of packed pairs, in the place of their first half; FINE: the rest of
+        // each in that of the second, once all of S has been read
+        uint32_t rest[FINE ? SQ : 1][16];
 #pragma unroll
         for (int q = 0; q < SQ; ++q) {
           const int jb = SQ * cg + q;
           uint32_t b[16];
+          auto pair = [&](int e, uint64_t v) {
+            b[e] = pack_pair(v);
+            if (FINE) rest[q][e] = pack_pair(f2_fma(f2_bits(b[e] << 16, b[e] & 0xffff0000u), f2(-1.f, -1.f), v));
+          };
           if (jb == quad || (jb < quad) != rev) {
             tmem_ld32(tb + lane_off + s_col(i) + 32 * jb, a);
             if (jb == quad) {
@@ -439,10 +450,10 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
               tmem_ld_wait();
               if (rev) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) b[e / 2] = pack_pair(f2_mul(f2_bits(a[e], a[e + 1]), f2(w[e], w[e + 1])));
+                for (int e = 0; e < 32; e += 2) pair(e / 2, f2_mul(f2_bits(a[e], a[e + 1]), f2(w[e], w[e + 1])));
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) b[e / 2] = pack_pair(f2_mul(f2_bits(a[e], a[e + 1]), f2(w[-e], w[-e - 1])));
+                for (int e = 0; e < 32; e += 2) pair(e / 2, f2_mul(f2_bits(a[e], a[e + 1]), f2(w[-e], w[-e - 1])));
               }
             } else {
               const float w = s.pw[Z0 + (rev ? 32 * jb - r : r - 32 * jb - 31)];
@@ -451,16 +462,19 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
                 const ulonglong2 cw = *reinterpret_cast<const ulonglong2*>(&s.colw[e]);
-                b[e / 2] = pack_pair(f2_mul(f2_mul(f2_bits(a[e], a[e + 1]), cw.x), ww));
-                b[e / 2 + 1] = pack_pair(f2_mul(f2_mul(f2_bits(a[e + 2], a[e + 3]), cw.y), ww));
+                pair(e / 2, f2_mul(f2_mul(f2_bits(a[e], a[e + 1]), cw.x), ww));
+                pair(e / 2 + 1, f2_mul(f2_mul(f2_bits(a[e + 2], a[e + 3]), cw.y), ww));
               }
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) b[e] = 0;
+            for (int e = 0; e < 16; ++e) pair(e, 0);
           }
           tmem_st16(tb + lane_off + s_col(i) + SW * cg + 16 * q, b);
         }
+        if constexpr (FINE)
+#pragma unroll
+          for (int q = 0; q < SQ; ++q) tmem_st16(tb + lane_off + s_col(i) + SW * cg + SW / 2 + 16 * q, rest[q]);
         if (inter) {  // what lies before the chunk, weighted
           if (!wait(&s.o_full, in, 35)) break;
           ++in;
@@ -596,9 +610,9 @@ bool make_map(CUtensorMap* m, const void* base, int D, long long rows, long long
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool STATES, int PARTS> cudaError_t launch(const LinMaps& maps, const LinArgs& p, cudaStream_t st) {
+template <int D, bool STATES, int PARTS, bool FINE = false> cudaError_t launch(const LinMaps& maps, const LinArgs& p, cudaStream_t st) {
   static_assert(Shape<D>::BLOCKS * (sizeof(Smem<D, PARTS>) + 1024) <= 233472, "shared memory of an SM");
-  auto kern = linear_tc_kernel<D, STATES, PARTS>;
+  auto kern = linear_tc_kernel<D, STATES, PARTS, FINE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D, PARTS>));
   if (e != cudaSuccess) return e;
   return launch_chained(kern, dim3((unsigned)((long long)p.items * p.heads * (STATES ? p.slots : p.ops))), Shape<D>::NT, sizeof(Smem<D, PARTS>), st, maps, p);
@@ -620,11 +634,17 @@ cudaError_t launch_linear_tc(const LinArgs& p, bool states, cudaStream_t st) {
   // A cache's states (whether or not they are written, for the same outputs) come from the states' pass where there are
   // several segments, else from the walk.
   const bool exact = p.state && (states || p.max_new <= p.seg);
+  // Few sequences of one chunk: P's rounding is one of an output's two, and of so few numbers that it need not average out to the
+  // other's size (a token alone: up to 2^-8 of its output, beside the output's own).  Free where the blocks are one wave (8 heads x
+  // 128: 11.9 us with and without); 64 x 32 x 128 would take 56 us in place of 50.
+  const bool fine = p.max_new <= C && (long long)p.items * p.heads * p.ops <= 152 * (p.D == 64 ? Shape<64>::BLOCKS : Shape<128>::BLOCKS);
   if (p.D == 64) {
     if (states) return exact ? launch<64, true, 3>(maps, p, st) : launch<64, true, 1>(maps, p, st);
+    if (fine) return exact ? launch<64, false, 3, true>(maps, p, st) : launch<64, false, 1, true>(maps, p, st);
     return exact ? launch<64, false, 3>(maps, p, st) : launch<64, false, 1>(maps, p, st);
   }
   if (states) return exact ? launch<128, true, 3>(maps, p, st) : launch<128, true, 1>(maps, p, st);
+  if (fine) return exact ? launch<128, false, 3, true>(maps, p, st) : launch<128, false, 1, true>(maps, p, st);
   return exact ? launch<128, false, 3>(maps, p, st) : launch<128, false, 1>(maps, p, st);
 }
 

@@ -43,6 +43,27 @@ def test_outputs_and_gradients(cuda_lib, dtype, d, batch, hq, hkv, L):
         check(n, got[n], *want[n], dtype, terms=L * (hq // hkv) + 2 * d + 64)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch,hq,hkv,L", [(1, 1, 1, 1), (1, 2, 1, 3), (2, 2, 2, 17), (1, 3, 1, 64), (1, 4, 4, 128)])
+def test_few_short_sequences_are_as_exact_as_their_outputs_type(cuda_lib, d, batch, hq, hkv, L):
+    """Weights of two bf16 numbers: 2^-16 of each, beside the output's 2^-8 and float32 sums (of d products in a weight, L of them
+    in an output; 64 for the decay and what is multiplied)."""
+    q, k, v, do = inputs("bf16", d, batch, hq, hkv, L, seed=11)
+    ld, G = torch.full((hkv,), -0.02, device=DEV), hq // hkv
+    got = run(q, k, v, do, ld, 0.3)
+    gap = torch.arange(L, device=DEV)[:, None] - torch.arange(L, device=DEV)[None, :]
+    w = torch.where(gap >= 0, 0.3 * torch.exp(ld[0].double() * gap.clamp(min=0)), 0.0)
+    x, y, z, g = (t.double().repeat_interleave(1 if t.shape[1] == hq else G, 1) for t in (q, k, v, do))
+    heads = lambda t: t.view(batch, hkv, G, L, d).sum(2)  # noqa: E731
+    same = lambda t: t  # noqa: E731
+    for name, a, b, c, m, add in (("o", x, y, z, w, same), ("dq", g, z, y, w, same), ("dk", z, g, x, w.mT, heads), ("dv", y, x, g, w.mT, heads)):
+        p = a @ b.mT
+        want, size = add((p * m) @ c), add((p.abs() * m) @ c.abs())
+        sums = add(((a.abs() @ b.abs().mT) * m) @ c.abs()) * (2 * d + 2 * L * G + 64) * 2.0 ** -24
+        far = (got[name].double() - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -16 * size + sums) * (1 + 2.0 ** -7)
+        assert far.max() <= 0, (name, float(far.max()))
+
+
 @pytest.mark.parametrize("dtype,d,hq,hkv,L", [("fp32", 64, 1, 1, 3001), ("bf16", 64, 2, 1, 5000), ("bf16", 128, 1, 1, 4097), ("bf16", 128, 8, 2, 2300)])
 def test_long_sequences_of_few_heads(cuda_lib, dtype, d, hq, hkv, L):
     """Cut into segments that run side by side."""
