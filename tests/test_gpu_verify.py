@@ -154,6 +154,28 @@ def test_equal_probabilities(cuda_lib):
     assert after.tolist() == (u.double() * V).long().tolist() and keep.tolist() == [1] * 32
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("power", [-100, -70, -62, 100])
+@pytest.mark.parametrize("V", [1000, 1001, 32768])
+def test_rows_of_tiny_and_huge_numbers(cuda_lib, dtype, power, V):
+    """Probabilities need not add up to 1 (at 2^-100 some are denormal: the reference gets the same)."""
+    n = [4, 1, 3, 6, 2, 5]
+    target, draft, tokens, uniform = case(dtype, V, n, seed=V + power + 200)
+    target, draft = target * 2.0 ** power, draft * 2.0 ** power
+    keep, after = make_cache(len(n)).verify(target, tokens, uniform, draft=draft, q_start=i32(starts(n)))
+    assert (keep.tolist(), after.tolist()) == reference(target, draft, tokens, uniform, starts(n))
+
+
+def test_infinity_in_both_rows(cuda_lib):
+    n = [3, 3, 1]
+    target, draft, tokens, uniform = case("fp32", 6000, n, seed=5)
+    want = reference(target, draft, tokens, uniform, starts(n))
+    target[4, 9], draft[5, 9] = float("inf"), float("inf")
+    keep, after = make_cache(3).verify(target, tokens, uniform, draft=draft, q_start=i32(starts(n)))
+    assert [keep.tolist()[b] for b in (0, 2)] == [want[0][b] for b in (0, 2)] and [after.tolist()[b] for b in (0, 2)] == [want[1][b] for b in (0, 2)]
+    assert 1 <= int(keep[1]) <= 3 and -1 <= int(after[1]) < 6000
+
+
 def test_nan_and_infinity(cuda_lib):
     n = [3, 3, 1]
     target, draft, tokens, uniform = case("fp32", 6000, n, seed=5)
