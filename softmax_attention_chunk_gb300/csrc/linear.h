@@ -54,6 +54,19 @@ PATH_HD float lin_log2(float ld) {
   return c * kLog2e;
 }
 
+#ifdef __CUDACC__
+// g^n as the sum of two floats (x: rounded, y: what that leaves).  A state is multiplied by it over and over: one float, off by
+// up to 2^-24 near 1 and the same way every time, would let it forget at another rate (single tokens at log_decay -1e-5: 7e-4 of the
+// state after 20000; with the rest under 1.1e-5, the sums' own rounding).  1 + expm1(x) is a float and a rest exactly for x > -1/2; states that
+// lose more at a time remember nothing for long enough.
+__device__ __forceinline__ float2 lin_decay(float ld, int n) {
+  const float x = (ld > 0.f ? 0.f : ld < -10000.f ? -10000.f : ld) * n;
+  if (!(x > -0.5f)) return make_float2(expf(x), 0.f);  // (NaN too)
+  const float e = expm1f(x), hi = 1.f + e;
+  return make_float2(hi, (1.f - hi) + e);
+}
+#endif
+
 // New tokens of slot b of a packed call; code for a bad row of q_start.
 struct LinSpan {
   int q0, n, code;

@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
   const bool rev = op.reverse;
   const float l2 = lin_log2(p.log_decay[h]);
   if (tid <= C) s.pw[tid] = exp2f(l2 * tid);
+  const float2 whole = lin_decay(p.log_decay[h], C);
   float* part = p.parts + (((size_t)op.slot * p.items + item) * p.heads + h) * D * D;
   float* own = p.state ? p.state + ((size_t)it.seq * p.heads + h) * D * D : nullptr;
   const bool split = p.max_new > p.seg;  // the segments' starting states are in parts
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
         v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
       }
       __syncthreads();
-      const float keep = g == 0 ? s.pw[m] : 1.f;
+      const float2 keep = g > 0 ? make_float2(1.f, 0.f) : m == C ? whole : lin_decay(p.log_decay[h], m);
       float a[D / 64][4][4];  // state rows r0 + 64 k ..
 #pragma unroll
       for (int k = 0; k < D / 64; ++k)
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(NT) linear_simt_kernel(const LinArgs p) {
         for (int i = 0; i < 4; ++i) {
           get4(&s.s[64 * k + r0 + i][c0], a[k][i]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) a[k][i][j] *= keep;
+          for (int j = 0; j < 4; ++j) a[k][i][j] = __fmaf_rn(a[k][i][j], keep.x, a[k][i][j] * keep.y);
         }
 #pragma unroll 4
       for (int t = 0; t < C; ++t) {  // (rows behind m are zeros)

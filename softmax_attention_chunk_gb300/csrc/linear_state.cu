@@ -30,8 +30,7 @@ __global__ void __launch_bounds__(NT) linear_scan_kernel(const LinArgs p) {
   }
   const int count = min((n + p.seg - 1) / p.seg, p.items - first);
   if (n == 0 || count <= 0) return;
-  const float l2 = lin_log2(p.log_decay[h]);
-  const float whole = exp2f(l2 * p.seg), tail = exp2f(l2 * (n - (count - 1) * p.seg));
+  const float2 whole = lin_decay(p.log_decay[h], p.seg), tail = lin_decay(p.log_decay[h], n - (count - 1) * p.seg);
   const size_t dd = (size_t)p.D * p.D, step = (size_t)p.heads * dd, e = ((size_t)blockIdx.x * NT + threadIdx.x) * 4;
   float* part = p.parts + (((size_t)slot * p.items + first) * p.heads + h) * dd + e;
   float* own = p.state ? p.state + ((size_t)b * p.heads + h) * dd + e : nullptr;
@@ -45,8 +44,9 @@ __global__ void __launch_bounds__(NT) linear_scan_kernel(const LinArgs p) {
     for (int i = 0; i < AHEAD; ++i)
       if (i0 + i < count) {
         *reinterpret_cast<float4*>(part + (i0 + i) * step) = s;
-        const float w = i0 + i + 1 < count ? whole : tail;
-        s.x = s.x * w + add[i].x, s.y = s.y * w + add[i].y, s.z = s.z * w + add[i].z, s.w = s.w * w + add[i].w;
+        const float2 w = i0 + i + 1 < count ? whole : tail;
+        s.x = s.x * w.x + (s.x * w.y + add[i].x), s.y = s.y * w.x + (s.y * w.y + add[i].y);
+        s.z = s.z * w.x + (s.z * w.y + add[i].z), s.w = s.w * w.x + (s.w * w.y + add[i].w);
       }
   }
   if (own && p.update) *reinterpret_cast<float4*>(own) = s;

@@ -51,7 +51,8 @@ template <int D, int PARTS> struct Smem {
   static constexpr int X = D / 64, NX = PARTS == 1 ? 2 : 1, NY = 2, NZ = D == 64 ? 2 : 1, NE = PARTS == 3 ? 1 : 0;
   uint8_t x[NX][X][TILE], y[NY][X][TILE], z[NZ + NE][X][TILE];
   uint8_t sb[2][X][D * 128];                // the state, rows of D columns: rounded, and what that leaves
-  float pw[Z0 + C + 8];                     // 0 .., then g^n
+  float pw[Z0 + C + 4];                     // 0 .., then g^n
+  float2 keep[2];                           // g^n of a whole chunk and of the last one
   alignas(16) float colw[32];               // g^n of a 32-column block's columns
   // A wait looks at the parity of a phase: none of these may complete two phases while someone still waits for the first.  So
   // what frees or fills one of several buffers has a barrier for each.
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   if (lead) tmem_alloc(&s.tmem_base, Sh::COLS);
   if (tid < Z0 + C + 1) s.pw[tid] = tid < Z0 ? 0.f : exp2f(l2 * (tid - Z0));
   if (tid < 32) s.colw[tid] = exp2f(l2 * (rev ? tid : 31 - tid));
+  if (tid < 2) s.keep[tid] = lin_decay(p.log_decay[h], tid == 0 ? C : it.n - (nch - 1) * C);
   const size_t dd = (size_t)D * D;
   float* part = p.parts + (((size_t)op.slot * p.items + item) * p.heads + h) * dd;
   float* own = p.state ? p.state + ((size_t)it.seq * p.heads + h) * dd : nullptr;
@@ -550,13 +552,14 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
       if (STATES ? i + 1 == steps : last) {
         if (!wait(&s.t_full, STATES ? 0 : k, 39)) break;
         tc_fence_after();
-        const uint64_t keep = f2(s.pw[Z0 + m], s.pw[Z0 + m]);
+        const float2 kept = s.keep[m < C];
+        const uint64_t keep = f2(kept.x, kept.x), rest = f2(kept.y, kept.y);
         uint32_t b[NS];
         if constexpr (D == 64) tmem_ld16x2_16(tb + lane_off + COL_D + 16 * cg, b);
         else tmem_ld32(tb + lane_off + COL_D + 32 * cg, b);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < NS; e += 2) st[e / 2] = f2_fma(st[e / 2], keep, f2_bits(b[e], b[e + 1]));
+        for (int e = 0; e < NS; e += 2) st[e / 2] = f2_fma(st[e / 2], keep, f2_fma(st[e / 2], rest, f2_bits(b[e], b[e + 1])));
         if (!STATES && k + 1 < count) {  // (the last product with the old one is over: P waited for it)
           put_state();
           fence_proxy_async_smem();
