@@ -600,8 +600,10 @@ size_t path_linear_extend_workspace_size(const path_linear_cache_t* cache, const
 /*
  * New tokens of many sequences, packed as for path_paged_extend: q, o [total_tokens][heads_q][head_dim], k, v
  * [total_tokens][heads][head_dim], slot b's being q_start[b] .. q_start[b + 1] - 1 (NULL: token b is slot b's).
- * A slot whose row of q_start is bad is left out (PATH_PAGED_BAD_START).  o must not overlap the inputs or the
- * states.  ws: for one call at a time; not used, and may be NULL, with a max_new of at most 16.  An infinity or NaN in a slot's tokens or state may reach any output of that slot, never another's.
+ * A slot whose row of q_start is bad, or begins before an earlier good row's tokens end, is left out whole
+ * (PATH_PAGED_BAD_START).  o must not overlap the inputs or the states.  ws: for one call at a time; not used, and may
+ * be NULL, with a max_new of at most 16.  An infinity or NaN in a slot's tokens or state may reach any output of that
+ * slot, never another's.
  */
 int path_linear_extend(const path_linear_cache_t* cache, const path_linear_step_t* step, const int* q_start, const void* q,
                        const void* k, const void* v, const float* log_decay, void* o, void* ws, size_t ws_bytes,

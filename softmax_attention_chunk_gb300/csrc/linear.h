@@ -67,7 +67,9 @@ __device__ __forceinline__ float2 lin_decay(float ld, int n) {
 }
 #endif
 
-// New tokens of slot b of a packed call; code for a bad row of q_start.
+// New tokens of slot b of a packed call; code for a bad row of q_start.  A row by itself: a good one that begins before an earlier good
+// one's tokens end (which takes a row between them that falls) is as bad, and every kernel leaves its slot out.  So no token is two
+// slots', and the slots' segments are no more than the tokens allow.
 struct LinSpan {
   int q0, n, code;
 };
@@ -86,6 +88,29 @@ PATH_HD LinSpan lin_span(const int* q_start, int b, int total, int max_new) {
 }
 
 #ifdef __CUDACC__
+// The spans of slots base .. base + 31, one to a lane, by a whole warp that takes the slots in order.
+struct LinOrder {
+  int end = 0;        // of the tokens so far
+  bool fell = false;  // a bad row was among the slots
+};
+__device__ __forceinline__ LinSpan lin_spans(const LinArgs& p, int base, LinOrder& o) {
+  const int lane = threadIdx.x & 31;
+  LinSpan s{0, 0, 0};
+  if (base + lane < p.seqs) s = lin_span(p.q_start, base + lane, p.total, p.max_new);
+  int upto = s.n ? s.q0 + s.n : 0;
+  o.fell |= __any_sync(0xffffffffu, s.code != 0) != 0;
+  if (o.fell) {  // (else the ends rise)
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto = max(upto, a);
+    }
+    const int before = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (s.q0 < max(o.end, lane ? before : 0)) s.n = 0;
+  }
+  o.end = max(o.end, __reduce_max_sync(0xffffffffu, upto));
+  return s;
+}
 struct LinItem {
   int seq, q0, n, seg;  // seg < 0: none
 };
@@ -97,9 +122,9 @@ __device__ __forceinline__ LinItem lin_item(const LinArgs& p, int item) {
   }
   const int lane = threadIdx.x & 31;
   int before = 0;
+  LinOrder order;
   for (int base = 0; base < p.seqs; base += 32) {
-    LinSpan s{0, 0, 0};
-    if (base + lane < p.seqs) s = lin_span(p.q_start, base + lane, p.total, p.max_new);
+    LinSpan s = lin_spans(p, base, order);
     if (s.n < p.min_new) s.n = 0;
     int upto = (s.n + p.seg - 1) / p.seg;
 #pragma unroll

@@ -19,17 +19,17 @@ __global__ void __launch_bounds__(NT) linear_scan_kernel(const LinArgs p) {
   if (!p.packed) {
     first = b * (p.items / p.seqs);
   } else {
-    n = lin_span(p.q_start, b, p.total, p.max_new).n;
-    if (n < p.min_new) return;
+    if (lin_span(p.q_start, b, p.total, p.max_new).n < p.min_new) return;
+    LinOrder order;
     for (int base = 0; base <= b; base += 32) {  // items of the slots before this one
-      LinSpan s{0, 0, 0};
-      if (base + lane <= b) s = lin_span(p.q_start, base + lane, p.total, p.max_new);
+      LinSpan s = lin_spans(p, base, order);
       if (s.n < p.min_new) s.n = 0;
       first += (int)__reduce_add_sync(0xffffffffu, base + lane < b ? (s.n + p.seg - 1) / p.seg : 0);
+      n = __shfl_sync(0xffffffffu, s.n, b & 31);  // (the last time: this slot's)
     }
   }
-  const int count = min((n + p.seg - 1) / p.seg, p.items - first);
-  if (n == 0 || count <= 0) return;
+  const int count = (n + p.seg - 1) / p.seg;
+  if (n == 0 || first + count > p.items) return;  // (the tokens are no two slots', so there are items for all)
   const float2 whole = lin_decay(p.log_decay[h], p.seg), tail = lin_decay(p.log_decay[h], n - (count - 1) * p.seg);
   const size_t dd = (size_t)p.D * p.D, step = (size_t)p.heads * dd, e = ((size_t)blockIdx.x * NT + threadIdx.x) * 4;
   float* part = p.parts + (((size_t)slot * p.items + first) * p.heads + h) * dd + e;

@@ -55,7 +55,22 @@ __global__ void __launch_bounds__(NT, D == 64 ? 4 : 2) linear_token_kernel(const
   const LinSpan sp = lin_span(p.q_start, b, p.total, p.max_new);
   if (sp.code && h == 0 && tid == 0) paged_error(p.status, sp.code);
   const int n = sp.n;
-  if (n == 0 || n > kLinTokenMax) return;
+  if (n == 0 || (n > kLinTokenMax && h > 0)) return;
+  int before = 0;  // where earlier slots' tokens end
+  if (p.q_start)
+    for (int i = tid; i < b; i += NT) {
+      const LinSpan e = lin_span(p.q_start, i, p.total, p.max_new);
+      if (e.n) before = max(before, e.q0 + e.n);
+    }
+  auto late = [&]() {  // met by the whole block
+    const bool is = __syncthreads_or(sp.q0 < before);
+    if (is && h == 0 && tid == 0) paged_error(p.status, PATH_PAGED_BAD_START);
+    return is;
+  };
+  if (n > kLinTokenMax) {  // (reported here, left out by the kernels that follow)
+    late();
+    return;
+  }
   float* own = p.state + (((size_t)b * p.heads + h) * D + r0) * D + c;
   ulonglong2 s[RP];  // pairs of floats
 #pragma unroll
@@ -87,7 +102,7 @@ __global__ void __launch_bounds__(NT, D == 64 ? 4 : 2) linear_token_kernel(const
         reinterpret_cast<float4*>(to)[1] = make_float4(a[2], a[2], a[3], a[3]);
       }
     }
-    __syncthreads();
+    if (late()) return;  // (at the barrier that the tokens need anyway: one of its own took 64 slots 47 us in place of 43)
     T* o = (T*)op.o + (long long)(sp.q0 + t0) * op.xt + (long long)h * G * op.xh;
     const float* at = smem;
     int g = 0;  // head
