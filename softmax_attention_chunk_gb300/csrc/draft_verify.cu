@@ -248,6 +248,8 @@ __global__ void __launch_bounds__(NT, 4) draft_verify_kernel(const VerifyArgs a)
         add_pair(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o)));
       if (lane == s) mine = sum;
     }
+    // The last copies (zeros) too: nothing orders two copies to one place, and the second round's first ones go to theirs.
+    if constexpr (N > 1) cp_wait<0>();
     float2 upto[1] = {mine};
     warp_scan(upto);
     const float2 total = shfl_pair(upto[0], 31);
