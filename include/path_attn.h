@@ -275,7 +275,8 @@ int path_decode_step_noalloc(const path_decode_desc_t* desc, void* k_cache, void
  * with PATH_BWD_REUSE_FWD or PATH_BWD_Z_FROM_FWD, where it keeps the forward's code), so it covers
  * every tensor-core kernel since the last clearing.
  * Test hook: with the environment variable PATH_ATTN_DEBUG_STALL_NS set to n > 0 at the time of
- * a call, the forward's PREPARE phase on the tensor-core path makes every CTA wait on a barrier
+ * a call, the forward's PREPARE phase on the tensor-core path (and, with code 99 as well, every tensor-core
+ * kernel of linear attention; their statuses are below) makes every CTA wait on a barrier
  * that nothing arrives at, give up after n ns (at most 1 s), record code 99 and end without
  * writing anything; the workspace status then reads PATH_ERR_INTERNAL with code 99.  The context
  * stays usable: a later call without the variable runs normally.
@@ -578,7 +579,8 @@ int path_linear_fwd(const path_linear_desc_t* desc, const void* q, const void* k
  * Those of dq, dk and dv that are NULL are not computed (one at least is not). */
 int path_linear_bwd(const path_linear_desc_t* desc, const void* q, const void* k, const void* v, const float* log_decay,
                     const void* dO, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream);
-/* As path_attn_workspace_status, of the call that ran on ws last. */
+/* As path_attn_workspace_status, of the call that ran on ws last: with a code (PATH_PAGED_WAIT and above), what it wrote is
+ * incomplete. */
 int path_linear_workspace_status(const path_linear_desc_t* desc, const void* ws, size_t ws_bytes, int* code, void* stream);
 
 /* States of many sequences, for serving: the slots' states in place of their tokens. */
@@ -611,7 +613,8 @@ int path_linear_extend(const path_linear_cache_t* cache, const path_linear_step_
 /* children[i] takes the state of parents[i] (NULL: zeros, a new sequence).  An entry that names no slot, or a child
  * that is listed twice or is a parent too, is left out (PATH_PAGED_BAD_SLOT). */
 int path_linear_fork(const path_linear_cache_t* cache, const int* parents, const int* children, int count, void* stream);
-/* As path_paged_status. */
+/* As path_paged_status.  After a code of PATH_PAGED_WAIT and above the outputs and the states of that call's slots are not
+ * to be used. */
 int path_linear_status(const path_linear_cache_t* cache, int* code, void* stream);
 
 #ifdef __cplusplus

@@ -74,16 +74,6 @@ size_t fwd_ws_total(const path_attn_desc_t* d, const Geom& g) {
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? PATH_OK : PATH_ERR_CUDA; }
 
-// Test hook of the failure path: PATH_ATTN_DEBUG_STALL_NS=<n> (n > 0) in the environment makes
-// the forward's PREPARE phase on the tensor-core path give up a wait after n ns in every CTA (see
-// launch_ut_prep64).  Read at every call; unset (the normal case) it is 0.
-uint32_t debug_stall_ns() {
-  const char* v = getenv("PATH_ATTN_DEBUG_STALL_NS");
-  if (!v || !*v) return 0;
-  const long long n = atoll(v);
-  return n <= 0 ? 0u : (n > 1000000000LL ? 1000000000u : (uint32_t)n);
-}
-
 // Reads the int error word at dev_word after the work queued on st; PATH_ERR_INTERNAL if it is set.
 int read_error_word(const void* dev_word, int* code, cudaStream_t st) {
   int h = 0;
@@ -95,6 +85,13 @@ int read_error_word(const void* dev_word, int* code, cudaStream_t st) {
 }
 
 }  // namespace
+
+uint32_t pathattn::debug_stall_ns() {
+  const char* v = getenv("PATH_ATTN_DEBUG_STALL_NS");
+  if (!v || !*v) return 0;
+  const long long n = atoll(v);
+  return n <= 0 ? 0u : (n > 1000000000LL ? 1000000000u : (uint32_t)n);
+}
 
 #define PATH_API __attribute__((visibility("default")))
 extern "C" {

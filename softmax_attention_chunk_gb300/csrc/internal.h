@@ -21,6 +21,11 @@ constexpr int kDecodeMaxSplits = 128;
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Test hook of the failure path: PATH_ATTN_DEBUG_STALL_NS=<n> (n > 0) in the environment makes the forward's PREPARE
+// phase on the tensor-core path (launch_ut_prep64) and the tensor-core kernels of linear attention give up a wait after n ns
+// in every CTA.  Read at every call; unset (the normal case) it is 0.
+uint32_t debug_stall_ns();
+
 // Problem geometry derived from a descriptor.
 struct Geom {
   int BH;       // batch * heads

@@ -46,6 +46,7 @@ struct LinArgs {
   float* parts;                    // [slots][items][heads][D][D]: states of single segments, then those at their starts
   int* err;                        // tensor-core kernels: first wait that gave up,
   int* status;                     // and where a cache keeps it (or null)
+  unsigned stall_ns;               // test hook: nonzero makes every block give up a wait (debug_stall_ns)
 };
 
 // log2 of the decay: log_decay is kept in [-10000, 0] (exp of the lower end is 0 for any distance but 0), NaN stays.

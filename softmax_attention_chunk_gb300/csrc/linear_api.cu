@@ -99,6 +99,7 @@ PATH_API int path_linear_fwd(const path_linear_desc_t* desc, const void* q, cons
   if (ws_bytes < lin_ws_bytes(p)) return PATH_ERR_WORKSPACE;
   p.log_decay = log_decay;
   p.err = (int*)ws;
+  p.stall_ns = debug_stall_ns();
   p.op[0] = dense_op(desc, q, k, v, o, true, false);
   return cuda_status(launch_linear(p, desc->dtype == PATH_BF16, (char*)ws, (cudaStream_t)stream));
 }
@@ -114,6 +115,7 @@ PATH_API int path_linear_bwd(const path_linear_desc_t* desc, const void* q, cons
   if (ws_bytes < lin_ws_bytes(p)) return PATH_ERR_WORKSPACE;
   p.log_decay = log_decay;
   p.err = (int*)ws;
+  p.stall_ns = debug_stall_ns();
   p.ops = p.slots = 0;
   if (dq) {
     p.maker[p.slots++] = p.ops;
@@ -170,6 +172,7 @@ PATH_API int path_linear_extend(const path_linear_cache_t* cache, const path_lin
   p.q_start = q_start;
   p.log_decay = log_decay;
   p.err = (int*)ws;
+  p.stall_ns = debug_stall_ns();
   p.status = cache->status;
   p.op[0] = LinOp{q, k, v, o, p.G, 1, 0, tq, d, 0, tk, d, 0};
   const bool bf16 = cache->dtype == PATH_BF16;

@@ -149,7 +149,10 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   const LinItem it = lin_item(p, item);
   if (it.seg < 0) return;
   if (smem_u32(smem_raw) & 1023) {  // (swizzled tiles begin on 1024 bytes)
-    if (tid == 0) atomicCAS(p.err, 0, PATH_PAGED_WAIT + 16);
+    if (tid == 0) {
+      atomicCAS(p.err, 0, PATH_PAGED_WAIT + 16);
+      if (p.status) paged_error(p.status, PATH_PAGED_WAIT + 16);
+    }
     return;
   }
   const bool rev = op.reverse != 0;
@@ -228,6 +231,13 @@ __global__ void __launch_bounds__(Shape<D>::NT, Shape<D>::BLOCKS)
   const uint32_t tb = s.tmem_base;
   int* err = p.err;
   bool ok = true;
+  if (p.stall_ns) {  // before any copy or product: a wait that nothing arrives at, and the block's end after it
+    if (mover && lane == 0) ok = mbar_wait_ns(&s.done, 0, err, PATH_PAGED_WAIT + 35, p.stall_ns);
+    if (!ok && p.status) paged_error(p.status, PATH_PAGED_WAIT + 35);
+    __syncthreads();
+    if (lead) tmem_dealloc(tb, Sh::COLS);
+    return;
+  }
   auto wait = [&](uint64_t* bar, uint32_t n, int code) {  // for the n-th completion; the whole warp agrees
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_lean(bar, n & 1, err, PATH_PAGED_WAIT + code));
     return ok;

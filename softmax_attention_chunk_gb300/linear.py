@@ -33,7 +33,7 @@ _descs = {}  # (descriptor's numbers, backward?) -> reference to the descriptor,
 
 class LinearAttentionFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, log_decay, scale):
+    def forward(ctx, q, k, v, log_decay, scale, check):
         q, k, v, log_decay = q.contiguous(), k.contiguous(), v.contiguous(), log_decay.contiguous()
         dt = q.dtype
         if dt not in pa._DT:
@@ -53,9 +53,9 @@ class LinearAttentionFunction(torch.autograd.Function):
                     raise ValueError(f"{name} lies on {t.device}, q on {q.device}")
         o = torch.empty_like(q)
         ctx.save_for_backward(q, k, v, log_decay)
-        ctx.desc = (B, hq, H, L, d, pa._DT[dt], float(scale))
+        ctx.desc, ctx.check = (B, hq, H, L, d, pa._DT[dt], float(scale)), check
         if q.numel():
-            _launch(pa._lib.path_linear_fwd, 0, ctx.desc, q, k, v, log_decay, o)
+            _launch(pa._lib.path_linear_fwd, 0, ctx.desc, check, q, k, v, log_decay, o)
         return o
 
     @staticmethod
@@ -69,14 +69,16 @@ def _backward(ctx, do):
     new = torch.empty_like if q.numel() else torch.zeros_like
     dq, dk, dv = [new(t) if need else None for t, need in zip((q, k, v), ctx.needs_input_grad)]
     if q.numel() and not (dq is dk is dv is None):
-        _launch(pa._lib.path_linear_bwd, 1, ctx.desc, q, k, v, log_decay, do.contiguous(), dq, dk, dv)
-    return dq, dk, dv, None, None
+        _launch(pa._lib.path_linear_bwd, 1, ctx.desc, ctx.check, q, k, v, log_decay, do.contiguous(), dq, dk, dv)
+    return dq, dk, dv, None, None, None
 
 
 _backward_once = once_differentiable(_backward)
 
 
-def _launch(fn, for_backward, numbers, q, *tensors):
+def _launch(fn, for_backward, numbers, check, q, *tensors):
+    if check and torch.cuda.is_current_stream_capturing():
+        raise ValueError("check=True waits for the device: not while its stream is captured into a graph")
     key = (numbers, for_backward)
     made = _descs.get(key)
     if made is None:
@@ -99,15 +101,22 @@ def _launch(fn, for_backward, numbers, q, *tensors):
             rc = fn(desc, q.data_ptr(), *args, ws.data_ptr(), n, pa._stream())
     if rc != pa.PATH_OK:
         pa._check(rc, fn.__name__)
+    if check:
+        with torch.cuda.device(index):
+            rc, code = pa.path_linear_workspace_status(desc._obj, ws.data_ptr(), n, pa._stream())
+        if rc != pa.PATH_OK:
+            raise RuntimeError(f"{fn.__name__}: device status of the workspace: {pa.path_status_string(rc)} (code {code})")
 
 
-def linear_attention(q, k, v, log_decay, scale=1.0):
+def linear_attention(q, k, v, log_decay, scale=1.0, check=False):
     """o [B, heads_q, L, d] of q [B, heads_q, L, d], k and v [B, heads, L, d] (bf16 or float32, one dtype; heads_q a
     multiple of heads: query head hq reads key head hq // (heads_q // heads)) and log_decay [heads] float32, the natural
-    logarithm of the decay per token, kept in [-10000, 0].  Sequences begin with a zero state."""
+    logarithm of the decay per token, kept in [-10000, 0].  Sequences begin with a zero state.  check=True: this call and its
+    backward synchronise and raise if a kernel gave up a bounded wait (what it wrote is then incomplete; without check nobody is
+    told)."""
     if log_decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("log_decay is a constant: linear_attention has no gradient for it")
-    return LinearAttentionFunction.apply(q, k, v, log_decay, scale)
+    return LinearAttentionFunction.apply(q, k, v, log_decay, scale, check)
 
 
 class LinearCache:
