@@ -162,6 +162,8 @@ class LinearCache:
         tokens in; with update=False they stay.  out must not overlap the other tensors.  ws: uint8, at least
         path_linear_extend_workspace_size bytes, for one call at a time (default: a new one)."""
         dt, at = self.dtype, self._index
+        # (numbers, whatever holds them: a tensor would be found by its identity, not by what it holds now)
+        max_new, scale, update = None if max_new is None else int(max_new), float(scale), bool(update)
         key = (q.shape, k.shape, v.shape, q_start is None, max_new, scale, update)
         plan = self._plans.get(key)
         if plan is None or q.dtype is not dt or k.dtype is not dt or v.dtype is not dt or not (
@@ -201,13 +203,13 @@ class LinearCache:
             max_new = 1 if q_start is None else N
         if N > 0 and max_new < 1:
             raise ValueError(f"max_new must be at least 1 for {N} tokens, got {max_new}")
-        step = pa.path_linear_step_t(hq, N, int(max_new), float(scale), int(bool(update)))
+        step = pa.path_linear_step_t(hq, N, max_new, scale, int(update))
         n = pa.path_linear_extend_workspace_size(self.c, step)
         if n == 0:
             raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens, scale {scale}")
         if len(self._plans) >= 1024:
             self._plans.clear()
-        return ctypes.byref(step), n, min(int(max_new), N) > TOKEN_MAX
+        return ctypes.byref(step), n, min(max_new, N) > TOKEN_MAX
 
     def fork(self, parents, children):
         """children[i] takes the state of parents[i] (int32 lists on the device)."""

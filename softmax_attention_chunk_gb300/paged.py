@@ -150,14 +150,15 @@ class PagedCache:
             self._need(q_start, torch.int32, (self.slots + 1,), "q_start")
         elif N != self.slots:
             raise ValueError(f"without q_start there is one token per slot: {N} tokens for {self.slots} slots")
-        if max_new is None:
-            max_new = 1 if q_start is None else N
+        # (numbers, whatever holds them: a tensor would be found by its identity below, not by what it holds now)
+        max_new = (1 if q_start is None else N) if max_new is None else int(max_new)
+        scale, window, sinks, max_multi = float(scale), int(window), int(sinks), int(max_multi)
         if N > 0 and max_new < 1:
             raise ValueError(f"max_new must be at least 1 for {N} tokens, got {max_new}")
         key = (hq, N, max_new, scale, window, sinks, max_multi)
         plan = self._plans.get(key)
         if plan is None:  # descriptor and workspace size of calls of these sizes
-            desc = pa.path_paged_desc_t(hq, N, int(max_new), float(scale), int(window), int(sinks), int(max_multi))
+            desc = pa.path_paged_desc_t(hq, N, max_new, scale, window, sinks, max_multi)
             n = pa.path_paged_workspace_size(self.c, desc)
             if n == 0:
                 raise ValueError(f"invalid sizes: {hq} query heads over {self.heads}, {N} tokens, window {window}, sinks {sinks}")
@@ -230,6 +231,7 @@ class PagedCache:
         uniform[i] * draft[i][x] < target[i - 1][x]; next is drawn with the uniform of the slot's first token from
         max(0, target - draft) of the first draft that went, or from target behind the last token.  Slots without tokens
         get 0 and -1.  Rows may be apart (a stride), their entries not."""
+        max_new = None if max_new is None else int(max_new)
         key = (target.shape, target.dtype, target.stride(), None if draft is None else draft.stride(), max_new)
         desc = self._verifications.get(key)
         if desc is None:
@@ -263,7 +265,7 @@ class PagedCache:
             if t is not None and (t.shape != target.shape or (vocab > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < vocab)):
                 raise ValueError(f"{name}: expected {tuple(target.shape)} with contiguous rows, got {tuple(t.shape)} strides {t.stride()}")
             strides.append(vocab if t is None or N <= 1 else t.stride(0))
-        max_new = N if max_new is None else int(max_new)
+        max_new = N if max_new is None else max_new
         if max_new < 0 or not 0 < vocab <= 1 << 20:
             raise ValueError(f"max_new must not be negative and vocab in 1 .. {1 << 20}, got {max_new} and {vocab}")
         return pa.path_verify_desc_t(self.slots, N, max_new, vocab, pa._DT[target.dtype], *strides)
