@@ -19,7 +19,8 @@ and advance() takes the tokens of an extend whole or not at all.  A slot that ex
 pages are missing after a refused reserve, say) is passed over by advance().  Argument marshalling only: every step runs in the CUDA
 library, on the current stream of the cache's device, without synchronising (check() does).  Calls that
 change one cache must be ordered on one stream.  A call can be captured into a CUDA graph: it reads
-lengths, tables and lists on the device.
+lengths, tables and lists on the device.  Graphs and work still queued use the handle's tensors (its status word too; with
+from_tensors those that it was not given): the handle outlives both.
 """
 from __future__ import annotations
 
@@ -120,8 +121,6 @@ class PagedCache:
         self._pages_bytes = pa.path_pages_workspace_size(self.c)
         if self._pages_bytes == 0:
             raise ValueError("unsupported cache (head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; sizes in range)")
-        # (one for all page calls: calls that change a cache are ordered)
-        self._pages_ws = torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
 
     # ---- attention ----
     def extend(self, q, k, v, w, beta, log_f=None, q_start=None, max_new=None, scale=1.0, window=0, sinks=0, ws=None,
@@ -217,10 +216,10 @@ class PagedCache:
         count = 4 if from_start is None else 5
         flat = torch.empty(count * tokens + self.slots + 1, dtype=torch.int32, device=self.device)
         *maps, start = flat.split_with_sizes([tokens] * count + [self.slots + 1])
-        at, row = flat.data_ptr(), 4 * tokens
+        at, row, ws = flat.data_ptr(), 4 * tokens, self._pages_workspace()
         self._library(pa._lib.path_pages_plan, self._ref, None if n_new is None else n_new.data_ptr(),
                       None if from_start is None else from_start.data_ptr(), tokens, at + count * row, at, at + row, at + 2 * row,
-                      at + 3 * row, None if from_start is None else at + 4 * row, self._pages_ws.data_ptr(), self._pages_bytes)
+                      at + 3 * row, None if from_start is None else at + 4 * row, ws.data_ptr(), self._pages_bytes)
         return StepPlan(start, *maps) if count == 5 else StepPlan(start, *maps, None)
 
     def verify(self, target, tokens, uniform, draft=None, q_start=None, max_new=None):
@@ -302,8 +301,13 @@ class PagedCache:
         self._pages("compact")
 
     # ---- helpers ----
+    def _pages_workspace(self):
+        # (for one call, on its stream: a captured call's lies in the graph's memory and stays when the handle goes)
+        return torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
+
     def _pages(self, name, *args):
-        self._call(getattr(pa, "path_pages_" + name), *args, self._pages_ws.data_ptr(), self._pages_bytes)
+        ws = self._pages_workspace()
+        self._call(getattr(pa, "path_pages_" + name), *args, ws.data_ptr(), self._pages_bytes)
 
     def _call(self, fn, *args):
         """fn(cache, *args, stream) on the current stream of the cache's device; raises on a status."""
