@@ -58,12 +58,12 @@ PATH_HD float lin_log2(float ld) {
 #ifdef __CUDACC__
 // g^n as the sum of two floats (x: rounded, y: what that leaves).  A state is multiplied by it over and over: one float, off by
 // up to 2^-24 near 1 and the same way every time, would let it forget at another rate (single tokens at log_decay -1e-5: 7e-4 of the
-// state after 20000; with the rest under 1.1e-5, the sums' own rounding).  1 + expm1(x) is a float and a rest exactly for x > -1/2; states that
-// lose more at a time remember nothing for long enough.
+// state after 20000; with the rest under 1.1e-5, the sums' own rounding).  For x > -1/8, expm1(x) by five terms of its series (the sixth
+// is 2^-24 of it at most), 1 + that as a float and a rest exactly; states that lose more at a time remember eight times at most.
 __device__ __forceinline__ float2 lin_decay(float ld, int n) {
   const float x = (ld > 0.f ? 0.f : ld < -10000.f ? -10000.f : ld) * n;
-  if (!(x > -0.5f)) return make_float2(expf(x), 0.f);  // (NaN too)
-  const float e = expm1f(x), hi = 1.f + e;
+  if (!(x > -0.125f)) return make_float2(exp2f(x * kLog2e), 0.f);  // (NaN too)
+  const float e = x * (1.f + x * (0.5f + x * (1.f / 6 + x * (1.f / 24 + x * (1.f / 120))))), hi = 1.f + e;
   return make_float2(hi, (1.f - hi) + e);
 }
 #endif
