@@ -542,6 +542,8 @@ int path_pages_plan(const path_paged_cache_t* cache, const int* n_new, const int
  * Products, differences and sums are exact to 2^-40 and better.  Probabilities need not add up to 1; NaN and negative ones
  * count as 0.  A draft outside [0, vocab) is not kept (PATH_PAGED_BAD_TOKEN; none is taken out of its row).  A slot
  * whose row of q_start is bad gets 0 and -1 (PATH_PAGED_BAD_START).
+ * The rows are probabilities: of logits, a softmax comes before this call and moves every row twice, where this call
+ * reads the one or two rows of a slot that decide.
  */
 typedef struct {
   int slots;          /* 1..65535 */
@@ -561,6 +563,8 @@ int path_draft_verify(const path_verify_desc_t* desc, const int* q_start, const 
  *   S_t = g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
  * log_decay [heads] float32, natural log, kept in [-10000, 0]; NaN makes its head's outputs NaN.  An infinity or NaN in
  * a sequence may reach any output of that sequence and head, of earlier tokens too.
+ * Results are the same from call to call.  How a sequence is cut and, in bf16, how often a weight is rounded goes by the
+ * sizes of the whole call: beside others a sequence may get other last bits than alone, within the same bounds.
  */
 typedef struct {
   int batch, heads_q;  /* heads_q: a multiple of heads (at most 16 times); head hq reads key head hq / (heads_q / heads) */

@@ -8,6 +8,8 @@ a PagedCache beside it:
     o = cache.extend(q, k, v, log_decay, q_start=starts, max_new=512)   # packed new tokens, as PagedCache.extend
     o = cache.extend(q, k, v, log_decay)                                # one token for every slot
     o = cache.extend(..., update=False)                                 # drafts: the states stay as they were
+    # (drafts that a PagedCache holds under forks need none here: with a q_start that gives their rows to the parents,
+    #  in the children's order, the parents' states are read)
     cache.fork(parents, children); cache.reset(slots)
     cache.check()                                                       # raises what the device found, if anything
 
@@ -113,7 +115,8 @@ def linear_attention(q, k, v, log_decay, scale=1.0, check=False):
     multiple of heads: query head hq reads key head hq // (heads_q // heads)) and log_decay [heads] float32, the natural
     logarithm of the decay per token, kept in [-10000, 0].  Sequences begin with a zero state.  check=True: this call and its
     backward synchronise and raise if a kernel gave up a bounded wait (what it wrote is then incomplete; without check nobody is
-    told)."""
+    told).  An infinity or NaN in a sequence may reach any output and gradient of that sequence and head, those of earlier
+    tokens too: padding has to be clean.  The same call gives the same bits; a sequence in another batch may get other last ones."""
     if log_decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("log_decay is a constant: linear_attention has no gradient for it")
     return LinearAttentionFunction.apply(q, k, v, log_decay, scale, check)
@@ -158,7 +161,8 @@ class LinearCache:
     def extend(self, q, k, v, log_decay, q_start=None, max_new=None, scale=1.0, update=True, ws=None, out=None):
         """o [tokens, heads_q, head_dim] of the packed new tokens q [tokens, heads_q, head_dim], k, v [tokens, heads,
         head_dim]; log_decay [heads] float32.  q_start (int32 [slots + 1]): slot b's tokens are q_start[b] ..
-        q_start[b + 1] - 1, at most max_new of them (default: all); without it, token b is slot b's.  The states take the
+        q_start[b + 1] - 1, at most max_new of them (default: all); without it, token b is slot b's.  A slot whose row of
+        q_start is bad, or begins inside an earlier slot's tokens, is left out (check() tells).  The states take the
         tokens in; with update=False they stay.  out must not overlap the other tensors.  ws: uint8, at least
         path_linear_extend_workspace_size bytes, for one call at a time (default: a new one)."""
         dt, at = self.dtype, self._index

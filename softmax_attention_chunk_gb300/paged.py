@@ -229,7 +229,8 @@ class PagedCache:
         same, or None: the drafts are certain) those that each was drawn from.  Draft i stays if those before it do and
         uniform[i] * draft[i][x] < target[i - 1][x]; next is drawn with the uniform of the slot's first token from
         max(0, target - draft) of the first draft that went, or from target behind the last token.  Slots without tokens
-        get 0 and -1.  Rows may be apart (a stride), their entries not."""
+        get 0 and -1.  Rows may be apart (a stride), their entries not.  Of drafts on forks keep and next stand at the children:
+        the parents' new tokens are those counts, moved to the parents' slots."""
         max_new = None if max_new is None else int(max_new)
         key = (target.shape, target.dtype, target.stride(), None if draft is None else draft.stride(), max_new)
         desc = self._verifications.get(key)
