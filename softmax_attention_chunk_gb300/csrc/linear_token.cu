@@ -40,6 +40,16 @@ constexpr int kJoin = 8;
 PATH_HD int token_floats(int D, int G) { return (3 + 2 * G) * D; }
 PATH_HD int token_batch(int D, int G) { return kTokenBytes / (4 * token_floats(D, G)); }
 
+// Of many slots: whether there is a bad row among all.  (Every block reading all rows before its own: 60000 slots of one head 582 us a
+// call, with this pass 341.)
+__global__ void __launch_bounds__(NT) linear_rows_kernel(const LinArgs p) {
+  chain();
+  const int b = blockIdx.x * NT + threadIdx.x;
+  if (b >= p.seqs) return;
+  const LinSpan s = lin_span(p.q_start, b, p.total, p.max_new);
+  if (s.code) paged_error(p.status, s.code);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(NT, D == 64 ? 4 : 2) linear_token_kernel(const LinArgs p) {
   chain();
@@ -52,18 +62,24 @@ __global__ void __launch_bounds__(NT, D == 64 ? 4 : 2) linear_token_kernel(const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = tid % CG * 4, r0 = tid / CG * RP;
   const int h = blockIdx.x, b = blockIdx.y, G = p.G;
+  // Whether the slot may begin before an earlier one's tokens end: only where a row before it ends above its start (a thread each) or,
+  // with more slots than threads, where a row is bad, for which linear_rows_kernel has looked at all.  Asked for beside the slot's own
+  // row and compared with it: waited for later, or earlier than the state's loads, 4096 slots of 4 heads at d 64 take 110 and 97 us, 95 so.
+  const bool here = p.q_start && p.seqs <= NT;
+  const int above = here ? p.q_start[min(tid + 1, b)] : tid == 0 ? __ldcg(p.status) : 0;
   const LinSpan sp = lin_span(p.q_start, b, p.total, p.max_new);
+  const bool may = here ? above > sp.q0 : p.q_start && above != 0;
   if (sp.code && h == 0 && tid == 0) paged_error(p.status, sp.code);
   const int n = sp.n;
   if (n == 0 || (n > kLinTokenMax && h > 0)) return;
-  int before = 0;  // where earlier slots' tokens end
-  if (p.q_start)
+  auto late = [&]() {  // met by the whole block
+    if (!__syncthreads_or(may)) return false;
+    bool is = false;
     for (int i = tid; i < b; i += NT) {
       const LinSpan e = lin_span(p.q_start, i, p.total, p.max_new);
-      if (e.n) before = max(before, e.q0 + e.n);
+      is |= e.n > 0 && e.q0 + e.n > sp.q0;
     }
-  auto late = [&]() {  // met by the whole block
-    const bool is = __syncthreads_or(sp.q0 < before);
+    is = __syncthreads_or(is);
     if (is && h == 0 && tid == 0) paged_error(p.status, PATH_PAGED_BAD_START);
     return is;
   };
@@ -174,6 +190,10 @@ template <typename T, int D> cudaError_t launch(const LinArgs& p, cudaStream_t s
   const size_t smem = sizeof(float) * (batch * token_floats(D, p.G) + W * D * rows);
   if (smem > 48 << 10) {
     cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  if (p.q_start && p.seqs > NT) {
+    cudaError_t e = launch_chained(linear_rows_kernel, (unsigned)((p.seqs + NT - 1) / NT), NT, 0, st, p);
     if (e != cudaSuccess) return e;
   }
   return launch_chained(linear_token_kernel<T, D>, dim3(p.heads, p.seqs), NT, smem, st, p);

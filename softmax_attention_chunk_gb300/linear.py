@@ -15,8 +15,8 @@ a PagedCache beside it:
 
 Argument marshalling only: every step runs in the CUDA library, on the current stream of the tensors' device, without
 synchronising (check() does).  Calls that change one cache must be ordered on one stream.  A call can be captured into a
-CUDA graph: q_start and lists are read on the device; the cache's handle, whose status word it uses, outlives the graph.  (A training step is captured as torch asks for it: with leaves of
-which no eager graph is alive.)
+CUDA graph: q_start and lists are read on the device; the cache's handle, whose status word it uses, outlives the graph.
+(A training step is captured as torch asks for it: with leaves of which no eager graph is alive.)
 """
 from __future__ import annotations
 

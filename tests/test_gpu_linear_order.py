@@ -61,3 +61,30 @@ def test_slots_that_begin_before_an_earlier_one_ends(cuda_lib, dtype, d, hq, hkv
             check("o", out[rows], want, A, dtype, terms=n + 2 * d + 64)
             check_state(cache.state[b], state, SA, dtype, terms=n + 64)
     assert bool((out[~written.to(DEV)] == 7.0).all()), "rows of no slot"
+
+
+@pytest.mark.parametrize("slots", [257, 5000])
+def test_many_slots_after_an_error_that_nobody_has_read(cuda_lib, slots):
+    """More slots than a block has threads: a code that still stands makes blocks look closer, good rows stay good."""
+    n = [1 + b % 3 for b in range(slots)]
+    cache, q, k, v, ld = make("bf16", 64, 1, 1, n, seed=22)
+    before = cache.state.clone()
+    good = torch.tensor([0] + torch.tensor(n).cumsum(0).tolist(), dtype=torch.int32, device=DEV)
+    want = cache.extend(q, k, v, ld, q_start=good, max_new=3).clone()
+    cache.check()
+    state = cache.state.clone()
+    cache.state.copy_(before)
+    bad = good.clone()
+    bad[slots - 3] = 0  # the slot before it falls, the one after it begins in the first one's tokens and has too many
+    bad[slots - 2] = 2  # now it has two, which are others' tokens
+    cache.extend(q, k, v, ld, q_start=bad, max_new=3, update=False)
+    got = cache.extend(q, k, v, ld, q_start=good, max_new=3)
+    assert torch.equal(got, want) and torch.equal(cache.state, state)
+    with pytest.raises(RuntimeError, match="q_start"):
+        cache.check()
+    cache.extend(q, k, v, ld, q_start=bad, max_new=3)
+    with pytest.raises(RuntimeError, match="q_start"):
+        cache.check()
+    left_out = [b for b in range(slots) if b not in taken(bad.tolist(), len(q), 3)]
+    assert left_out == [slots - 4, slots - 3, slots - 2]
+    assert torch.equal(cache.state[left_out], state[left_out])
